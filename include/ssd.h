@@ -70,7 +70,9 @@ typedef enum {
     SSD_ERR_WORKSPACE = 6
 } ssd_status;
 
-typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype;
+/* SSD_F16 is a type of the paged-cache calls only; logits are SSD_F32 or
+ * SSD_BF16. */
+typedef enum { SSD_F32 = 0, SSD_BF16 = 1, SSD_F16 = 2 } ssd_dtype;
 
 /* Bits of the device error word (ssd_get_device_error). */
 #define SSD_DEVERR_BAD_TEMPERATURE 0x1 /* T < 0 or NaN: row sentinel -1   */
@@ -80,6 +82,11 @@ typedef enum { SSD_F32 = 0, SSD_BF16 = 1 } ssd_dtype;
 #define SSD_DEVERR_TIMEOUT 0x10        /* a bounded device wait ran out   */
 #define SSD_DEVERR_FILTER_BAND 0x20    /* a filtered row's cut fell outside its collected
                                           bins; it was cut by bisection (results exact) */
+#define SSD_DEVERR_BAD_TREE 0x40       /* a node whose way to the root is broken, or an
+                                          accepted path that is none: left out */
+#define SSD_DEVERR_BAD_LENGTH 0x80     /* a length, node count or position out of range:
+                                          the sequence (or node) is left out */
+#define SSD_DEVERR_BAD_PAGE 0x100      /* a page id outside [0, num_pages)  */
 
 /* Sentinels written to accept_len. */
 #define SSD_ROW_INVALID (-1)
@@ -502,6 +509,166 @@ SSD_API ssd_status ssd_spec_cache_get_error(ssd_spec_cache *cache, ssd_stream_t 
 
 SSD_API int ssd_spec_cache_capacity(const ssd_spec_cache *cache);
 SSD_API int ssd_spec_cache_depth(const ssd_spec_cache *cache);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The target pass around a verification: a paged cache of keys and values,
+ * filled with a batch of drafted nodes (ssd_kv_append), attended by them
+ * (ssd_tree_attention), and cut down to the accepted path afterwards
+ * (ssd_kv_commit).  The nodes of a sequence are those of ssd_verify_tree:
+ * node 0 is the last committed token, whose key and value are not cached
+ * yet; a chain of k drafted tokens (ssd_verify) is the tree parent[j] = j-1
+ * with N = k + 1; plain decoding is N = 1.
+ *   - Slots 0 .. ctx_len[b]-1 of sequence b hold its committed context.  Node
+ *     j is stored in slot ctx_len[b] + j; its position (for the rotation) is
+ *     ctx_len[b] + depth(j).
+ *   - Slot s of sequence b is entry s % page_size of page
+ *     page_table[b*table_stride + s / page_size].
+ * ---------------------------------------------------------------------------
+ */
+
+/* A paged cache of one layer: a HOST struct of device pointers and sizes,
+ * read during the call only.  Entry d of head h of slot `off` of page `p`
+ * is k[p*k_page + off*k_slot + h*k_head + d] (all strides in elements, so
+ * token-major and head-major pages are both served).  k and v need 16-byte
+ * alignment and strides that are positive multiples of 8 elements, below
+ * 2^38 elements, and rows must not overlap. */
+typedef struct {
+    void *k, *v;
+    int64_t k_page, k_slot, k_head;
+    int64_t v_page, v_slot, v_head;
+    ssd_dtype dtype;        /* SSD_BF16 or SSD_F16 */
+    int num_pages, page_size;
+    int Hkv, D;             /* key/value heads; head size 64 or 128 */
+    const int32_t *page_table; /* device, [B, max_pages] */
+    int64_t table_stride;
+    int max_pages;          /* a sequence holds at most max_pages*page_size slots */
+} ssd_paged_kv;
+
+/* The drafted nodes of a batch (HOST struct).  Every node's way to the root
+ * has to satisfy parent[b, 0] == -1 and 0 <= parent[b, j] < j; a node whose
+ * way does not (SSD_DEVERR_BAD_TREE) or with j >= n_nodes[b] is absent: it is
+ * not stored, sees nothing and is seen by none.  A sequence with
+ * ctx_len < 0, n_nodes outside [0, N] or ctx_len + n_nodes beyond its table
+ * (SSD_DEVERR_BAD_LENGTH) has no nodes. */
+typedef struct {
+    int B, N;               /* 1 <= N <= SSD_MAX_TREE_NODES */
+    const int32_t *ctx_len; /* device, [B] */
+    const int32_t *parent;  /* device, [B, N]; NULL: a chain */
+    const int32_t *n_nodes; /* device, [B]; NULL: N everywhere */
+} ssd_draft_nodes;
+
+/* Bytes of the workspace of ssd_kv_append, ssd_kv_commit and ssd_logprobs
+ * (its first word is the device error word). */
+#define SSD_ERRWORD_BYTES 256
+
+/*
+ * ssd_kv_append -- the queries, keys and values of the drafted nodes on their
+ * way from the projections to the attention: per head x (q and k alike, each
+ * with its own weights)
+ *     y = x / sqrt(mean(x^2) + eps) * w        (q_norm / k_norm given)
+ *     z = y with its first rot entries rotated by the node's position
+ * computed in fp32 and rounded once; z_q goes to q_out, z_k and v to the
+ * node's slot of the cache.
+ *   q        : [B, N, Hq, D], element strides q_b, q_n, q_h (D contiguous);
+ *              k, v: [B, N, Hkv, D] with one set of strides kv_b, kv_n, kv_h
+ *              (views into a packed projection).  Type kv->dtype, 2-byte
+ *              alignment; 16-byte aligned rows are read with vector loads.
+ *   q_out    : [B, N, Hq, D] contiguous, 16-byte aligned; may be q itself when
+ *              that is contiguous.  Absent nodes get zeros.
+ *   cos_sin  : [max_pos, rot] fp32, 16-byte aligned: rot/2 cosines, then rot/2
+ *              sines, of each position; NULL (rot = 0): no rotation.
+ *              rot % 16 == 0, rot <= D.  A position >= max_pos makes its node
+ *              absent (SSD_DEVERR_BAD_LENGTH).
+ *   interleaved : 0 rotates pairs (i, i + rot/2), else pairs (2i, 2i+1).
+ *   q_norm, k_norm : [D] weights of kv->dtype, both or neither.
+ * A node whose page id is out of range is not stored (SSD_DEVERR_BAD_PAGE).
+ */
+SSD_API ssd_status ssd_kv_append(const ssd_paged_kv *kv, const ssd_draft_nodes *nodes, int Hq,
+                         const void *q, int64_t q_b, int64_t q_n, int64_t q_h, const void *k,
+                         const void *v, int64_t kv_b, int64_t kv_n, int64_t kv_h, void *q_out,
+                         const float *cos_sin, int max_pos, int rot, int interleaved,
+                         const void *q_norm, const void *k_norm, float eps, void *ws,
+                         size_t ws_bytes, ssd_stream_t stream);
+
+/*
+ * ssd_tree_attention -- attention of the drafted nodes over the cache: query
+ * head h of node i sees the context slots and the slots of node i and its
+ * ancestors, of key/value head h / (Hq / Hkv);
+ *     out = sum_s p_s v_s,  p = softmax over the seen slots of scale * q.k_s.
+ *   q        : [B, N, Hq, D] with element strides q_b, q_n, q_h, type
+ *              kv->dtype, 16-byte aligned rows; Hq a multiple of Hkv, at most
+ *              64 heads a group.
+ *   out      : [B, N, Hq, D] contiguous, kv->dtype, 16-byte aligned.
+ *   lse      : [B, N, Hq] fp32 or NULL: log sum exp(scale * q.k) of the seen
+ *              slots.
+ *   scale    : finite.
+ *   ws       : ssd_tree_attention_workspace_bytes(B, N, Hq, Hkv, D) bytes.
+ * An absent node, or one whose seen slots all score -inf, gets out 0 and
+ * lse -inf.  Slots that a node does not see never reach its output, whatever
+ * they hold (NaN and infinities included).  A page id out of range reads as a
+ * page of zeros (SSD_DEVERR_BAD_PAGE).
+ */
+SSD_API size_t ssd_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
+SSD_API ssd_status ssd_tree_attention(const ssd_paged_kv *kv, const ssd_draft_nodes *nodes, int Hq,
+                              const void *q, int64_t q_b, int64_t q_n, int64_t q_h, float scale,
+                              void *out, float *lse, void *ws, size_t ws_bytes,
+                              ssd_stream_t stream);
+
+/*
+ * ssd_kv_commit -- after a verification: the keys and values of the accepted
+ * path move to the slots right behind the context, in `layers` caches that
+ * share one page table (layer l starts at k + l*k_layer, v + l*v_layer).
+ *   accept_len, out_node : ssd_verify_tree's outputs ([B], and [B, N] with row
+ *              stride N): slot ctx + out_node[b, i] moves to slot ctx + 1 + i
+ *              for i < accept_len[b].  out_node NULL: a chain, whose nodes
+ *              already lie there.
+ *   new_len  : [B] int32: ctx_len + 1 + accept_len.  Must not be ctx_len.
+ * A negative accept_len commits nothing (new_len = ctx_len), and so does a
+ * path that is not increasing within 1 .. N-1 (SSD_DEVERR_BAD_TREE) or a
+ * length out of range (SSD_DEVERR_BAD_LENGTH).  A move from or to a page id
+ * out of range is left out (SSD_DEVERR_BAD_PAGE).
+ */
+SSD_API ssd_status ssd_kv_commit(const ssd_paged_kv *kv, int layers, int64_t k_layer, int64_t v_layer,
+                         int B, int N, const int32_t *ctx_len, const int32_t *accept_len,
+                         const int32_t *out_node, int32_t *new_len, void *ws, size_t ws_bytes,
+                         ssd_stream_t stream);
+
+/*
+ * ssd_logprobs -- what a server answers about emitted tokens, in one pass over
+ * their rows: log p(tok), the entropy of p in nats, the token's rank and the
+ * K best tokens with their log probabilities; p = softmax(z / T).
+ *   logits   : rows of V logits, row_stride elements apart (>= V).
+ *   rows     : [R] int32 or NULL: answer r is about row rows[r] of n_rows
+ *              (a row id < 0: no answer, NaN and -1); NULL: row r, R <= n_rows.
+ *   tok      : [R] int32; a token outside [0, V) gets logprob NaN, rank -1
+ *              (SSD_DEVERR_BAD_TOKEN unless it is -1).
+ *   T        : [R] fp32 or NULL (1).  T == 0: the one-hot at the lowest
+ *              argmax (logprob 0 or -inf, entropy 0); T < 0 or NaN:
+ *              SSD_DEVERR_BAD_TEMPERATURE, an answer of NaN and -1.
+ *   logprob, entropy : [R] fp32; rank: [R] int32, 1 for the best token (larger
+ *              logit first, then lower index).  entropy, rank may be NULL.
+ *   K, top_tok, top_logprob : 0 <= K <= SSD_MAX_TOP; [R, K], best first.
+ * A row with a NaN or +inf logit, or only -inf, sets SSD_DEVERR_BAD_LOGITS and
+ * gives NaN and -1.  A row id >= n_rows sets SSD_DEVERR_BAD_LENGTH.
+ */
+#define SSD_MAX_TOP 32
+SSD_API size_t ssd_logprobs_workspace_bytes(int R, int V, int K);
+SSD_API ssd_status ssd_logprobs(const void *logits, ssd_dtype dtype, int64_t row_stride, int n_rows,
+                        int V, const int32_t *rows, int R, const int32_t *tok, const float *T,
+                        int K, float *logprob, float *entropy, int32_t *rank, int32_t *top_tok,
+                        float *top_logprob, void *ws, size_t ws_bytes, ssd_stream_t stream);
+
+/*
+ * Self-test hooks (HOST pointers, no GPU): the page lookup and the node walk
+ * that the kernels above use.  ssd_selftest_kv_slot returns 1 and the page
+ * and the entry within it, or 0 for a slot that the table does not hold.
+ * ssd_selftest_node returns 1 and the node's ancestors-or-self as a bit mask
+ * and its depth, or 0 for an absent node; parent NULL: a chain.
+ */
+SSD_API int ssd_selftest_kv_slot(const int32_t *table_row, int max_pages, int num_pages, int page_size,
+                         int64_t slot, int32_t *page, int32_t *off);
+SSD_API int ssd_selftest_node(const int32_t *parent, int n, int j, uint64_t *mask, int32_t *depth);
 
 /*
  * Launch profiler (observability, not part of the method).  Between

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libssd_gb300.so")
 
 SSD_F32 = 0
 SSD_BF16 = 1
+SSD_F16 = 2
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_INVALID_ARG", 2: "SSD_ERR_UNSUPPORTED_DTYPE",
           3: "SSD_ERR_CUDA", 4: "SSD_ERR_CACHE_FULL", 5: "SSD_ERR_TIMEOUT",
           6: "SSD_ERR_WORKSPACE"}
@@ -27,12 +28,19 @@ DEVERR_BAD_TOKEN = 0x4
 DEVERR_CACHE_FULL = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_FILTER_BAND = 0x20
+DEVERR_BAD_TREE = 0x40
+DEVERR_BAD_LENGTH = 0x80
+DEVERR_BAD_PAGE = 0x100
+MAX_TREE_NODES = 64
+MAX_TOP = 32
+_ERRWORD_BYTES = 256
 
 # (name, restype, argtypes)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
 _Z = ctypes.c_size_t
+_F = ctypes.c_float
 SIGNATURES = [
     ("ssd_status_string", ctypes.c_char_p, [_I]),
     ("ssd_version", _I, []),
@@ -80,6 +88,16 @@ SIGNATURES = [
     ("ssd_set_split", _I, [_I, _I]),
     ("ssd_set_chain_batch", _I, [_I]),
     ("ssd_set_step_schedule", _I, [_I, _I]),
+    ("ssd_kv_append", _I, [_P, _P, _I, _P, _L, _L, _L, _P, _P, _L, _L, _L, _P, _P, _I, _I, _I,
+                           _P, _P, _F, _P, _Z, _P]),
+    ("ssd_tree_attention_workspace_bytes", _Z, [_I, _I, _I, _I, _I]),
+    ("ssd_tree_attention", _I, [_P, _P, _I, _P, _L, _L, _L, _F, _P, _P, _P, _Z, _P]),
+    ("ssd_kv_commit", _I, [_P, _I, _L, _L, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
+    ("ssd_logprobs_workspace_bytes", _Z, [_I, _I, _I]),
+    ("ssd_logprobs", _I, [_P, _I, _L, _I, _I, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _P, _Z,
+                          _P]),
+    ("ssd_selftest_kv_slot", _I, [_P, _I, _I, _I, _L, _P, _P]),
+    ("ssd_selftest_node", _I, [_P, _I, _I, _P, _P]),
     ("ssd_profile_begin", _I, [_I]),
     ("ssd_profile_end", _I, [_P, _I, _P]),
 ]
@@ -88,6 +106,19 @@ SIGNATURES = [
 class ProfileEntry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 40), ("launches", ctypes.c_int),
                 ("timed", ctypes.c_int), ("total_ms", ctypes.c_double)]
+
+
+class PagedKV(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P),
+                ("k_page", _L), ("k_slot", _L), ("k_head", _L),
+                ("v_page", _L), ("v_slot", _L), ("v_head", _L),
+                ("dtype", _I), ("num_pages", _I), ("page_size", _I), ("Hkv", _I), ("D", _I),
+                ("page_table", _P), ("table_stride", _L), ("max_pages", _I)]
+
+
+class DraftNodes(ctypes.Structure):
+    _fields_ = [("B", _I), ("N", _I), ("ctx_len", _P), ("parent", _P), ("n_nodes", _P)]
+
 
 _lib = None
 
@@ -508,6 +539,257 @@ def ssd_verify_tree(Z: torch.Tensor, D: torch.Tensor, parent: torch.Tensor,
         _dev(u_smp, "u_smp"), _dev(o["accept_len"], "accept_len"),
         _dev(o["out_tok"], "out_tok"), _dev(o["out_node"], "out_node"), wp, wn,
         _stream(stream)))
+    o["ws"] = ws
+    return o
+
+
+# ---------------------------------------------------------------------------
+# the target pass around a verification: paged cache, tree attention, answers
+# ---------------------------------------------------------------------------
+_KV_DTYPE = {torch.bfloat16: SSD_BF16, torch.float16: SSD_F16}
+
+
+def _strides(t: torch.Tensor, one: int):
+    """Element strides, `one` in place of those of dimensions of one entry
+    (which torch leaves arbitrary)."""
+    st = t.stride()
+    return st if 1 not in t.shape else [one if n == 1 else s for n, s in zip(t.shape, st)]
+
+
+def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor) -> PagedKV:
+    """k_cache, v_cache: [pages, page_size, Hkv, D] views (any order of the
+    first three dimensions in memory); page_table [B, max_pages] int32."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be [pages, page_size, Hkv, D] of one dtype")
+    code = _KV_DTYPE.get(k_cache.dtype)
+    if code is None:
+        raise TypeError("the cache must be bfloat16 or float16, got %s" % k_cache.dtype)
+    if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
+        raise ValueError("the cache and its page table must be CUDA tensors")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
+        raise ValueError("page_table must be int32 [B, max_pages] with contiguous rows")
+    pages, ps, H, D = k_cache.shape
+    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
+        raise ValueError("head entries must be contiguous")
+    ks, vs = _strides(k_cache, D), _strides(v_cache, D)
+    width = page_table.shape[1]
+    return PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                   code, pages, ps, H, D, page_table.data_ptr(), max(page_table.stride(0), width),
+                   width)
+
+
+def _i32(t: Optional[torch.Tensor], shape, name: str):
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError("%s must be int32, got %s" % (name, t.dtype))
+    if t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError("%s must be a contiguous CUDA tensor of shape %s" % (name, tuple(shape)))
+    return t.data_ptr()
+
+
+def _draft_nodes(B: int, N: int, page_table, ctx_len, parent, n_nodes) -> DraftNodes:
+    if ctx_len is None or page_table.shape[0] != B:
+        raise ValueError("ctx_len and page_table must have one entry (row) per sequence")
+    return DraftNodes(B, N, _i32(ctx_len, (B,), "ctx_len"), _i32(parent, (B, N), "parent"),
+                      _i32(n_nodes, (B,), "n_nodes"))
+
+
+def _heads(t: torch.Tensor, like: torch.Tensor, name: str):
+    """[B, N, heads, D] view with contiguous head entries."""
+    if t.dim() != 4 or not t.is_cuda or t.dtype != like.dtype or t.shape[3] != like.shape[3]:
+        raise ValueError("%s must be a CUDA tensor [B, N, heads, %d] of type %s"
+                         % (name, like.shape[3], like.dtype))
+    if t.stride(3) != 1:
+        raise ValueError("%s: head entries must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _error_ws(ws, dev):
+    if ws is None:
+        ws = new_workspace(_ERRWORD_BYTES, dev)
+    return ws
+
+
+def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda",
+               inv_freq: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """[max_pos, rot] float32 for ssd_kv_append: rot/2 cosines, then rot/2
+    sines, of position * base^(-2i/rot) (or of position * inv_freq, for scaled
+    rotations), the angles in float64: in float32 a position of 10^5 leaves
+    0.01 of a radian unknown."""
+    if inv_freq is None:
+        inv_freq = float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    if inv_freq.numel() * 2 != rot:
+        raise ValueError("inv_freq must hold rot / 2 values")
+    ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv_freq.double()
+    return torch.cat([ang.cos(), ang.sin()], 1).float()
+
+
+def ssd_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                  v_cache: torch.Tensor, page_table: torch.Tensor, ctx_len: torch.Tensor, *,
+                  parent: Optional[torch.Tensor] = None, n_nodes: Optional[torch.Tensor] = None,
+                  cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+                  q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, ws: Optional[torch.Tensor] = None,
+                  out: Optional[dict] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Norms and position rotation of the drafted nodes' q [B,N,Hq,D] and
+    k [B,N,Hkv,D] (views of a packed projection will do), and k, v stored in
+    the nodes' slots of the paged cache [pages,page_size,Hkv,D].  Node j of
+    sequence b goes to slot ctx_len[b] + j and has position ctx_len[b] +
+    depth(j); parent [B,N] int32 is the tree of ssd_verify_tree, None a chain;
+    n_nodes [B] the nodes of each sequence.  cos_sin: rope_table(...) or None;
+    q_norm, k_norm: [D] weights or None.  Returns {"q": [B,N,Hq,D], "ws"}."""
+    kv = _paged_kv(k_cache, v_cache, page_table)
+    qp, kp, vp = _heads(q, k_cache, "q"), _heads(k, k_cache, "k"), _heads(v, k_cache, "v")
+    B, N, Hq, D = q.shape
+    if k.shape != (B, N, kv.Hkv, D) or v.shape != k.shape or _strides(v, 0) != _strides(k, 0):
+        raise ValueError("k and v must be [B, N, Hkv, D] with the same strides")
+    nodes = _draft_nodes(B, N, page_table, ctx_len, parent, n_nodes)
+    max_pos = rot = 0
+    if cos_sin is not None:
+        _want(cos_sin, torch.float32, "cos_sin")
+        max_pos, rot = cos_sin.shape
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None and (w.dtype != q.dtype or w.numel() != D):
+            raise ValueError("%s must be [D] of q's type" % name)
+    ws = _error_ws(ws, q.device)
+    wp, wn = _ws_ptr(ws)
+    out = {} if out is None else out
+    qo = out.get("q")
+    if qo is None:
+        qo = out["q"] = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+    elif qo.shape != q.shape or qo.dtype != q.dtype:
+        raise ValueError("out['q'] must be like q")
+    qs, ks = _strides(q, 0), _strides(k, 0)
+    _check("ssd_kv_append", load_library().ssd_kv_append(
+        ctypes.byref(kv), ctypes.byref(nodes), Hq, qp, qs[0], qs[1], qs[2], kp, vp, ks[0], ks[1],
+        ks[2], _dev(qo, "out['q']"), _opt(cos_sin, "cos_sin"), max_pos, rot, int(interleaved),
+        _opt(q_norm, "q_norm"), _opt(k_norm, "k_norm"), eps, wp, wn, _stream(stream)))
+    out["ws"] = ws
+    return out
+
+
+def tree_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load_library().ssd_tree_attention_workspace_bytes(B, N, Hq, Hkv, D))
+
+
+def ssd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       page_table: torch.Tensor, ctx_len: torch.Tensor, *,
+                       parent: Optional[torch.Tensor] = None,
+                       n_nodes: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                       ws: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                       stream=None) -> Dict[str, torch.Tensor]:
+    """Attention of the drafted nodes q [B,N,Hq,D] over the paged cache: node i
+    sees the context (slots below ctx_len[b]) and the slots of its ancestors
+    and itself.  scale defaults to D ** -0.5.  Returns {"out": [B,N,Hq,D],
+    "lse": [B,N,Hq] float32, "ws"}; nodes that are absent get 0 and -inf."""
+    lib = load_library()
+    kv = _paged_kv(k_cache, v_cache, page_table)
+    qp = _heads(q, k_cache, "q")
+    B, N, Hq, D = q.shape
+    nodes = _draft_nodes(B, N, page_table, ctx_len, parent, n_nodes)
+    if ws is None:
+        n = lib.ssd_tree_attention_workspace_bytes(B, N, Hq, kv.Hkv, D)
+        if n == 0:
+            raise SSDError("ssd_tree_attention_workspace_bytes", 1)
+        ws = new_workspace(n, q.device)
+    wp, wn = _ws_ptr(ws)
+    o = {} if out is None else out
+    if "out" not in o:
+        o["out"] = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
+        o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    elif o["out"].shape != q.shape or o["out"].dtype != q.dtype or o["lse"].shape != q.shape[:3]:
+        raise ValueError("out must hold out like q and lse [B, N, Hq]")
+    qs = _strides(q, 0)
+    _check("ssd_tree_attention", lib.ssd_tree_attention(
+        ctypes.byref(kv), ctypes.byref(nodes), Hq, qp, qs[0], qs[1], qs[2],
+        D ** -0.5 if scale is None else scale, _dev(o["out"], "out"), _dev(o["lse"], "lse"), wp,
+        wn, _stream(stream)))
+    o["ws"] = ws
+    return o
+
+
+def ssd_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                  ctx_len: torch.Tensor, accept_len: torch.Tensor,
+                  out_node: Optional[torch.Tensor] = None, *, ws: Optional[torch.Tensor] = None,
+                  out: Optional[dict] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """After a verification: the accepted path's keys and values move to the
+    slots right behind the context.  The caches are [pages,page_size,Hkv,D], or
+    [layers,pages,page_size,Hkv,D] for every layer in one call; accept_len [B]
+    and out_node [B,N] come from ssd_verify_tree (out_node None: a chain
+    verified by ssd_verify, which needs no moves).  Returns {"ctx_len": [B],
+    "ws"}: the lengths after the commit."""
+    layers, kl, vl = 1, 0, 0
+    if k_cache.dim() == 5:
+        if v_cache.shape != k_cache.shape:
+            raise ValueError("k_cache and v_cache must have one shape")
+        layers, kl, vl = k_cache.shape[0], k_cache.stride(0), v_cache.stride(0)
+        k_cache, v_cache = k_cache[0], v_cache[0]
+    kv = _paged_kv(k_cache, v_cache, page_table)
+    B = page_table.shape[0]
+    N = MAX_TREE_NODES
+    if out_node is not None:
+        if out_node.dim() != 2:
+            raise ValueError("out_node must be [B, N]")
+        N = out_node.shape[1]
+    ws = _error_ws(ws, k_cache.device)
+    wp, wn = _ws_ptr(ws)
+    o = {} if out is None else out
+    if "ctx_len" not in o:
+        o["ctx_len"] = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+    _check("ssd_kv_commit", load_library().ssd_kv_commit(
+        ctypes.byref(kv), layers, kl, vl, B, N, _i32(ctx_len, (B,), "ctx_len"),
+        _i32(accept_len, (B,), "accept_len"), _i32(out_node, (B, N), "out_node"),
+        _i32(o["ctx_len"], (B,), "out['ctx_len']"), wp, wn, _stream(stream)))
+    o["ws"] = ws
+    return o
+
+
+def ssd_logprobs(logits: torch.Tensor, tok: torch.Tensor, K: int = 0,
+                 T: Optional[torch.Tensor] = None, *, rows: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                 stream=None) -> Dict[str, torch.Tensor]:
+    """log p(tok), entropy (nats), rank and the K best tokens with their log
+    probabilities under softmax(z / T), one pass over the rows.  logits
+    [n,V] (rows may be strided), tok [R] int32; rows [R] int32 picks the
+    logits row of each answer (e.g. the rows of accepted nodes; < 0: no
+    answer); T [R] float32 or None.  Returns {"logprob", "entropy", "rank",
+    "top_tok" [R,K], "top_logprob" [R,K], "ws"} (the last two for K > 0)."""
+    lib = load_library()
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [n, V]")
+    n, V = logits.shape
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("a row of logits must be contiguous")
+    R = tok.numel()
+    _want(tok, torch.int32, "tok")
+    if T is not None:
+        _want(T, torch.float32, "T")
+        if T.numel() != R:
+            raise ValueError("T must hold one temperature per token")
+    dev = logits.device
+    if ws is None:
+        nb = lib.ssd_logprobs_workspace_bytes(R, V, K)
+        if nb == 0:
+            raise SSDError("ssd_logprobs_workspace_bytes", 1)
+        ws = new_workspace(nb, dev)
+    wp, wn = _ws_ptr(ws)
+    o = {} if out is None else out
+    if "logprob" not in o:
+        o["logprob"] = torch.empty(R, dtype=torch.float32, device=dev)
+        o["entropy"] = torch.empty(R, dtype=torch.float32, device=dev)
+        o["rank"] = torch.empty(R, dtype=torch.int32, device=dev)
+    if K > 0 and "top_tok" not in o:
+        o["top_tok"] = torch.empty((R, K), dtype=torch.int32, device=dev)
+        o["top_logprob"] = torch.empty((R, K), dtype=torch.float32, device=dev)
+    if o["logprob"].numel() != R or (K > 0 and o["top_tok"].shape != (R, K)):
+        raise ValueError("out is of another call's sizes")
+    _check("ssd_logprobs", lib.ssd_logprobs(
+        logits.data_ptr(), _dtype_code(logits), max(logits.stride(0), V), n, V,
+        _i32(rows, (R,), "rows"), R, _dev(tok, "tok"), _opt(T, "T"), K,
+        _dev(o["logprob"], "logprob"), _dev(o["entropy"], "entropy"), _dev(o["rank"], "rank"),
+        _dev(o["top_tok"], "top_tok") if K > 0 else None,
+        _dev(o["top_logprob"], "top_logprob") if K > 0 else None, wp, wn, _stream(stream)))
     o["ws"] = ws
     return o
 
