@@ -1,9 +1,42 @@
 // ssd_attn.cu -- attention of the drafted nodes over the paged cache.
 //
-// A warp per (node, query head): 32 slots at a time, one slot's score per
-// lane, an online softmax (running maximum m, sum l, output o):
-//     m' = max(m, max_s x_s),  o' = o 2^(m - m') + sum_s 2^(x_s - m') v_s.
-// Slots a node does not see are skipped, so what they hold cannot matter.
+// For one key/value head the query rows are the R = N * G (node, query head of
+// the group) pairs.  Over tiles of 128 cache slots,
+//     S^T = K Q^T          [128 slots, R]    (scores, slots on the M axis)
+//     P^T = 2^(c S^T - m)  masked            (c = scale log2 e, m per row)
+//     O^T += V^T P^T       [D, R],  l += column sums of P^T
+// and at the end O / l.  Slots lie on the tensor cores' M axis and rows on
+// their N axis, so that few rows cost few columns (16 at least) instead of
+// most of a 128-row tile, and one kernel serves one token, chains and wide
+// trees.
+//
+// One persistent CTA per SM.  The batch's tiles (every sequence's, for every
+// key/value head) are numbered and cut into equal ranges, one per CTA, by the
+// lengths on the device: ragged batches and long single sequences are
+// balanced alike.  A (sequence, head) whose tiles lie in one range is
+// finished there; one that is cut leaves its parts (m, l, O in 32 bits) in
+// the workspace, and attn_combine_kernel joins them in range order.
+//
+// Warps of a CTA:
+//   0      copies K and V tiles, page by page, by TMA into a ring of slots
+//          (128-byte swizzle; a page id out of range is a coordinate out of
+//          bounds, which TMA fills with zeros)
+//   1      issues tcgen05.mma: S^T (K, Q from shared memory) two jobs ahead
+//          of O^T (V^T read transposed from the same row-major tile, P^T from
+//          shared memory)
+//   2, 3   gather the next rows of Q, the rows' ancestor masks, and clear what
+//          must not be multiplied in tiles that hold drafted nodes: V rows
+//          behind the sequence's end, and NaN or infinite entries of nodes
+//          (added at the end for the rows that see them)
+//   4..11  two warpgroups for the softmax, a slot per thread.  Up to 128 rows:
+//          the warpgroups take alternate tiles and keep their own m, l, O;
+//          more: the same tiles, half of the rows each.
+//
+// m follows the running maximum lazily: as long as no score exceeds it by
+// more than 2^8, the tile is used as it is (P keeps its relative precision,
+// l and O their range).  Otherwise the warpgroup finds the tile's row maxima
+// and rescales l and O.
+#include <cuda.h>
 #include <math.h>
 
 #include "ssd_device.cuh"
@@ -12,114 +45,1324 @@
 namespace ssd {
 namespace {
 
-constexpr int kRows = 4;  // warps per CTA
+constexpr int kAttnThreads = 384;
+constexpr int kTile = 128;           // slots of a tile (rows of the ring's tiles)
+constexpr int kHalf = kTile * 128;   // bytes of a tile's 64-column half
+constexpr int kMaxRing = 8;
+constexpr int kMaxRows = 256;        // rows of a row block
+constexpr int kMaxJob = 128;         // rows of a job (one warpgroup's columns)
+constexpr int kMaxCtas = 160;
+constexpr float kNoScore = -1e30f;   // m of a row that has seen nothing
+constexpr float kSlack = 8.f;
+constexpr int kSmemMax = 227 * 1024;
 
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kRows) attn_kernel(const AttnParams p) {
-  constexpr int E = D / 32;  // output columns per lane
-  __shared__ float qs[kRows][D];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = p.nodes.N;
-  const long long row = static_cast<long long>(blockIdx.x) * kRows + w;
-  if (row >= static_cast<long long>(p.nodes.B) * N * p.Hq) return;
-  const int h = static_cast<int>(row % p.Hq);
-  const long long bj = row / p.Hq;
-  const int j = static_cast<int>(bj % N), b = static_cast<int>(bj / N);
-  const int hk = h / p.G;
-  const int ctx = p.nodes.ctx_len[b];
-  bool bad_len, broken;
-  const int n = seq_nodes(ctx, p.nodes.n_nodes ? p.nodes.n_nodes[b] : N, N, p.kv.width, p.kv.ps, bad_len);
-  uint64_t mask;
-  int depth;
-  const bool there = node_way(p.nodes.parent ? p.nodes.parent + static_cast<long long>(b) * N : nullptr,
-                              n, j, mask, depth, broken);
-  int bits = (bad_len ? kErrBadLength : 0) | (broken ? kErrBadTree : 0);
-  const char* q = p.q + 2 * (b * p.q_b + j * p.q_n + h * p.q_h);
-  for (int e = lane * 2; e < D; e += 64) {
-    const uint32_t x = *reinterpret_cast<const uint32_t*>(q + 2 * e);
-    qs[w][e] = T::lo(x);
-    qs[w][e + 1] = T::hi(x);
-  }
-  __syncwarp();
-  const float c = p.scale * 1.4426950408889634f;
-  float m = -INFINITY, l = 0.f, o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  const int tot = there ? ctx + n : 0;
-  for (int s0 = 0; s0 < tot; s0 += 32) {
-    const int s = s0 + lane;
-    const bool seen = s < tot && (s < ctx || ((mask >> (s - ctx)) & 1));
-    float x = -INFINITY;
-    const char* vrow = nullptr;
-    if (seen) {
-      int page, off;
-      float acc = 0.f;
-      if (kv_slot(p.kv.table + b * p.kv.table_stride, p.kv.width, p.kv.pages, p.kv.ps, s, page, off)) {
-        const char* k = p.kv.k + 2 * (page * p.kv.k_page + off * p.kv.k_slot + hk * p.kv.k_head);
-        vrow = p.kv.v + 2 * (page * p.kv.v_page + off * p.kv.v_slot + hk * p.kv.v_head);
-        for (int e = 0; e < D; e += 8) {
-          float f[8];
-          unpack8<T>(*reinterpret_cast<const uint4*>(k + 2 * e), f);
-#pragma unroll
-          for (int t = 0; t < 8; ++t) acc = fmaf(f[t], qs[w][e + t], acc);
-        }
-      } else {
-        bits |= kErrBadPage;
-      }
-      x = acc * c;
-    }
-    float mx = x;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const float mn = fmaxf(m, mx);
-    const float ref = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - ref);
-    const float pr = seen ? exp2f(x - ref) : 0.f;
-    m = mn;
-    l = l * f + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= f;
-    for (int t = 0; t < 32; ++t) {
-      const float pt = __shfl_sync(0xffffffffu, pr, t);
-      const char* vt = reinterpret_cast<const char*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(vrow), t));
-      if (!vt || pt == 0.f) continue;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const uint32_t x2 = *reinterpret_cast<const uint32_t*>(vt + 2 * (lane * E + e));
-        o[e] = fmaf(pt, T::lo(x2), o[e]);
-        o[e + 1] = fmaf(pt, T::hi(x2), o[e + 1]);
-      }
-    }
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  const bool any = !(l <= 0.f);
-  const float inv = any ? 1.f / l : 0.f;
-  char* out = p.out + 2 * (row * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(out + 2 * e) =
-        any ? T::pack(o[e] * inv, o[e + 1] * inv) : 0u;
-  if (p.lse && lane == 0)
-    p.lse[row] = any ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
-  bits = __reduce_or_sync(0xffffffffu, bits);
-  if (bits && lane == 0) atomicOr(p.err, bits);
+struct Args {
+  NodesView nodes;
+  const int* table;
+  long long table_stride;
+  int width, pages, ps;
+  int Hq, Hkv, G, R;
+  int RB, rows_per_block;   // row blocks of a key/value head
+  int two;                  // the warpgroups split the rows
+  int ncj, cols;            // columns of a job; of Q (ncj or 2 ncj)
+  int qbufs, ring;
+  int box, ppt, tk, tpp;    // rows of a TMA box, pages a tile, slots a tile, tiles a page
+  int ragged;               // tiles have rows that are no slot
+  int cover;                // rows of a tile that TMA writes
+  const char* q;
+  long long q_b, q_n, q_h;
+  float c;                  // scale * log2(e)
+  char* out;
+  float* lse;
+  const char* vcache;       // for the rows that see a node with NaN or infinities
+  long long v_page, v_slot, v_head;
+  float* part_o;            // [2 ctas][cols][D]
+  float2* part_ml;          // [2 ctas][cols]
+  long long* sched;         // [B + 1] tiles before each sequence
+  int* err;
+};
+
+// Shared memory behind the ring, Q and P (256 rows leave 3 KB for it).
+struct alignas(16) Misc {
+  uint64_t full[kMaxRing], empty[kMaxRing];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2], vready, vclean, done;
+  uint64_t anc[2][kMaxNodes + 1];   // nodes' ancestors (0: absent); the last: no row
+  long long lo, hi, off0;
+  alignas(16) float nm[2][kMaxJob]; // -m
+  uint8_t node[kMaxRows];           // rows' nodes; two buffers of 64 or one of 256
+  unsigned nf[2][2];                // nodes with NaN or infinite values
+  int b0;
+  unsigned tmem;
+  int abort;
+};
+static_assert(sizeof(Misc) <= 3072, "shared memory of 256 rows");
+
+// What a warpgroup keeps in its P buffer while that holds no P: between the
+// product of one tile and the P of the next, and at the end of a piece.
+struct Scratch {
+  float red[4][kMaxJob];
+  float fac[kMaxJob];
+};
+
+// ---------------------------------------------------------------------------
+// mbarriers, TMA, tcgen05
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t sptr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void bar_init(uint64_t* b, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sptr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sptr(b)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(sptr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
 }
 
+// Bounded wait: after a second (or once another wait of the CTA gave up) the
+// CTA runs on without waiting, to its end; the error word says so.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Misc& sm, int* err) {
+  if (bar_try(b, parity)) return true;
+  const unsigned long long t0 = now_ns();
+  while (!bar_try(b, parity)) {
+    if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+    if (now_ns() - t0 > 1000000000ull) {
+      *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+__device__ __forceinline__ void named_sync(int id, int n) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+__device__ __forceinline__ bool named_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred p, %1, %2, q;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"(static_cast<uint32_t>(v))
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int d, int slot, int head,
+                                         int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(map), "r"(sptr(bar)), "r"(d), "r"(slot), "r"(head), "r"(page)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ void tc_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   sptr(b))
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+
+// Shared-memory operand descriptor: 128-byte swizzle, strides in bytes.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: 32-bit accumulator, 128 x n, 16-bit operands.
 template <class T>
-cudaError_t attn_t(const AttnParams& p, int D, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.nodes.B) * p.nodes.N * p.Hq;
-  const unsigned grid = static_cast<unsigned>((rows + kRows - 1) / kRows);
-  if (D == 128) attn_kernel<T, 128><<<grid, 32 * kRows, 0, s>>>(p);
-  else attn_kernel<T, 64><<<grid, 32 * kRows, 0, s>>>(p);
-  return cudaGetLastError();
+__device__ __forceinline__ uint32_t instr(int n, bool a_mn, bool b_mn) {
+  const uint32_t f = T::kId == Bf16::kId ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+         (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+#define SSD_TM16(r)                                                                              \
+  "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), \
+      "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),   \
+      "=r"(r[15])
+
+__device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : SSD_TM16(r)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr));
+}
+// Waits for this thread's tcgen05.ld; the registers are tied to the wait so
+// that no use moves before it.
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tm_wait_ld8(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7])::"memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Largest value of the warp (NaN ignored).
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// ---------------------------------------------------------------------------
+// the tiles of the batch
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int tiles_of(const Args& a, int tot) {
+  if (a.ps <= kTile) return (tot + a.tk - 1) / a.tk;
+  return (tot / a.ps) * a.tpp + (tot % a.ps + kTile - 1) / kTile;
+}
+// First slot of tile t, and how many it holds.
+__device__ __forceinline__ void tile_slots(const Args& a, int t, int& first, int& count) {
+  if (a.ps <= kTile) {
+    first = t * a.tk;
+    count = a.tk;
+  } else {
+    const int r = (t % a.tpp) * kTile;
+    first = (t / a.tpp) * a.ps + r;
+    count = min(kTile, a.ps - r);
+  }
+}
+// Offset of a tile's row from its first slot, -1 for a row that is no slot.
+__device__ __forceinline__ int row_slot(const Args& a, int row, int count) {
+  if (a.ps > kTile) return row < count ? row : -1;
+  const int p = row / a.box, r = row - p * a.box;
+  return p < a.ppt && r < a.ps ? p * a.ps + r : -1;
+}
+
+__device__ __forceinline__ int seq_len(const Args& a, int b, int& ctx, bool& bad) {
+  ctx = __ldg(a.nodes.ctx_len + b);
+  const int nn = a.nodes.n_nodes ? __ldg(a.nodes.n_nodes + b) : a.nodes.N;
+  const int n = seq_nodes(ctx, nn, a.nodes.N, a.width, a.ps, bad);
+  return n == 0 ? 0 : ctx + n;  // a sequence without nodes has no tiles
+}
+
+// First tile of CTA c's range.
+__device__ __forceinline__ long long range_start(long long W, int c, int C) { return W * c / C; }
+
+// The pieces of a CTA's range, one (sequence, head, row block) after another.
+struct Pieces {
+  const Args& a;
+  long long off, left;
+  int b, T, ctx, tot;
+  int item, t0, count;  // item = head * RB + row block; tiles t0 .. t0 + count
+  bool loaded;
+  __device__ Pieces(const Args& a_, const Misc& sm)
+      : a(a_), off(sm.off0), left(sm.hi - sm.lo), b(sm.b0), T(0), ctx(0), tot(0), item(0), t0(0), count(0),
+        loaded(false) {}
+  __device__ void load() {
+    bool bad;
+    tot = seq_len(a, b, ctx, bad);
+    T = tiles_of(a, tot);
+  }
+  __device__ bool next() {
+    if (left <= 0) return false;
+    if (!loaded) {
+      loaded = true;
+      load();
+    }
+    const int per = a.Hkv * a.RB;
+    while (off >= static_cast<long long>(T) * per) {
+      off = 0;
+      if (++b >= a.nodes.B) {
+        left = 0;
+        return false;
+      }
+      load();
+    }
+    item = static_cast<int>(off / T);
+    t0 = static_cast<int>(off - static_cast<long long>(item) * T);
+    count = static_cast<int>(min(static_cast<long long>(T - t0), left));
+    off += count;
+    left -= count;
+    return true;
+  }
+  // Whether tile t holds slots behind the context.
+  __device__ bool tail(int t) const {
+    int first, n;
+    tile_slots(a, t, first, n);
+    return first + n > ctx;
+  }
+};
+
+// Jobs of a CTA in order: a tile for one warpgroup's columns.
+struct Jobs {
+  Pieces pc;
+  int t, half, in_item, item_no, gj;
+  bool two, started;
+  __device__ Jobs(const Args& a, const Misc& sm)
+      : pc(a, sm), t(0), half(0), in_item(0), item_no(-1), gj(-1), two(a.two != 0), started(false) {}
+  // Advances; new_tile: whether the job is the first of its tile.
+  __device__ bool next(bool& new_tile) {
+    new_tile = true;
+    if (started) {
+      if (two && half == 0) {
+        half = 1;
+        ++in_item;
+        ++gj;
+        new_tile = false;
+        return true;
+      }
+      half = 0;
+      ++t;
+      ++in_item;
+    }
+    ++gj;
+    if (!started || t == pc.t0 + pc.count) {
+      started = true;
+      if (!pc.next()) return false;
+      t = pc.t0;
+      in_item = 0;
+      ++item_no;
+    }
+    return true;
+  }
+  __device__ int wg() const { return two ? half : gj & 1; }
+  __device__ bool last_of_tile() const { return !two || half == 1; }
+};
+
+// ---------------------------------------------------------------------------
+// softmax: one tile for one warpgroup
+// ---------------------------------------------------------------------------
+// What a thread's slot means for the rows: seen by all, by none, or by those
+// whose mask holds node j.
+struct SlotSeen {
+  uint64_t all;  // ~0: every row
+  int j;
+  unsigned any;  // 0: no row
+};
+
+// Rows' masks: the ancestors of their nodes.
+struct RowMasks {
+  const uint64_t* anc;
+  const uint8_t* node;
+  __device__ __forceinline__ uint64_t operator[](int r) const { return anc[node[r]]; }
+};
+
+template <bool MASKED>
+__device__ __forceinline__ void masked16(float (&t)[16], const SlotSeen& s, const RowMasks& mask, int r0) {
+  if (!MASKED) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const unsigned bit = static_cast<unsigned>((mask[r0 + i] | s.all) >> s.j) & s.any;
+    t[i] = bit ? t[i] : -INFINITY;
+  }
+}
+
+// t = c s - m of 16 rows.
+__device__ __forceinline__ void scaled16(const uint32_t (&s)[16], f32x2 c2, const float* nm, float (&t)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nm + i);
+    const f32x2 a = fma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, m.x);
+    const f32x2 b = fma2(pk2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2, m.y);
+    up2(a, t[i], t[i + 1]);
+    up2(b, t[i + 2], t[i + 3]);
+  }
+}
+
+template <int NC, bool MASKED>
+__device__ __forceinline__ float tile_excess(uint32_t tS, int nch, f32x2 c2, const float* nm,
+                                             const SlotSeen& seen, const RowMasks& mask) {
+  float ex = -INFINITY;
+  uint32_t s[2][16];
+  tm_ld16(tS, s[0]);
+#pragma unroll
+  for (int k = 0; k < NC / 16; ++k) {
+    if (k < nch) {
+      tm_wait_ld(s[k & 1]);
+      if (k + 1 < nch) tm_ld16(tS + (k + 1) * 16, s[(k + 1) & 1]);
+      float t[16];
+      scaled16(s[k & 1], c2, nm + k * 16, t);
+      masked16<MASKED>(t, seen, mask, k * 16);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) ex = max3(ex, t[i], t[i + 1]);
+    }
+  }
+  return ex;
+}
+
+// P^T of the tile into shared memory (rows contiguous, 64 of them and 128
+// slots a block, 128-byte swizzle), l += P.
+template <class T, int NC, bool MASKED>
+__device__ __forceinline__ void tile_probs(uint32_t tS, int nch, f32x2 c2, const float* nm,
+                                           const SlotSeen& seen, const RowMasks& mask, char* P, int slot,
+                                           f32x2 (&l)[NC / 2]) {
+  uint32_t s[2][16];
+  tm_ld16(tS, s[0]);
+#pragma unroll
+  for (int k = 0; k < NC / 16; ++k) {
+    if (k < nch) {
+      tm_wait_ld(s[k & 1]);
+      if (k + 1 < nch) tm_ld16(tS + (k + 1) * 16, s[(k + 1) & 1]);
+      float t[16];
+      scaled16(s[k & 1], c2, nm + k * 16, t);
+      masked16<MASKED>(t, seen, mask, k * 16);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float e0 = ex2_fast(t[i]), e1 = ex2_fast(t[i + 1]);
+        l[k * 8 + i / 2] = add2(l[k * 8 + i / 2], pk2(e0, e1));
+        w[i / 2] = T::pack(e0, e1);
+      }
+      char* row = P + (k / 4) * kHalf + slot * 128;
+      const int ch = (k & 3) * 2;
+      *reinterpret_cast<uint4*>(row + (((ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+// Row maxima of the tile over the warp's 32 slots, into red[warp][row].
+template <int NC, bool MASKED>
+__device__ __forceinline__ void tile_maxima(uint32_t tS, int nch, float c, const SlotSeen& seen,
+                                            const RowMasks& mask, float* red, int lane) {
+#pragma unroll 1
+  for (int k = 0; k < nch; ++k) {
+    uint32_t s[16];
+    tm_ld16(tS + k * 16, s);
+    tm_wait_ld(s);
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = __uint_as_float(s[i]) * c;
+    masked16<MASKED>(t, seen, mask, k * 16);
+    float keep = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float m = warp_max(t[i]);
+      keep = lane == i ? m : keep;
+    }
+    if (lane < 16) red[k * 16 + lane] = keep;
+  }
+}
+
+template <class T, int D, int NC>
+__device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* P0, int pbytes,
+                                             int wg) {
+  char* P = P0 + wg * pbytes;
+  Scratch& sc0 = *reinterpret_cast<Scratch*>(P0);
+  Scratch& sc1 = *reinterpret_cast<Scratch*>(P0 + pbytes);
+  Scratch& sc = wg == 0 ? sc0 : sc1;
+  constexpr int LANES = D;  // lanes of O^T that hold an output column (64: the rest repeat them)
+  const int wt = threadIdx.x - 128 - wg * 128;  // thread of the warpgroup = slot row = TMEM lane
+  const int warp = wt >> 5, lane = wt & 31;
+  const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t tS = tmem + lane_base + wg * kMaxJob;
+  const uint32_t tO0 = tmem + lane_base + 2 * kMaxJob;
+  const uint32_t tO = tO0 + wg * kMaxJob;
+  const int ncj = a.ncj, nch = ncj / 16;
+  const f32x2 c2 = pk2(a.c, a.c);
+  float* nm = sm.nm[wg];
+  float* fac = sc.fac;
+  const int bar = 1 + wg;
+  const int colbase = a.two ? wg * ncj : 0;
+  uint32_t ps = 0, ppv = 0;  // phases of sfull, pvdone
+  int gj = 0, item_no = 0;
+  Pieces pc(a, sm);
+  const long long left0 = pc.left;
+  while (pc.next()) {
+    const int qb = item_no % a.qbufs;
+    bar_wait(&sm.qfull[qb], (item_no / a.qbufs) & 1, sm, a.err);
+    const RowMasks mask{sm.anc[qb], sm.node + qb * 64 + colbase};
+    if (wt < ncj) nm[wt] = -kNoScore;
+    f32x2 l[NC / 2];
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) l[i] = 0ull;
+    named_sync(bar, 128);
+    int jobs = 0;
+    for (int t = pc.t0; t < pc.t0 + pc.count; ++t) {
+      if (!a.two && ((gj + (t - pc.t0)) & 1) != wg) continue;
+      int first, count;
+      tile_slots(a, t, first, count);
+      const bool masked = a.ragged || first + count > pc.ctx;
+      SlotSeen seen;
+      seen.all = ~0ull;
+      seen.j = 0;
+      seen.any = 1;
+      if (masked) {
+        const int r = row_slot(a, wt, count);
+        const int slot = first + r;
+        if (r < 0 || slot >= pc.tot) {
+          seen.any = 0;
+        } else if (slot >= pc.ctx) {
+          seen.all = 0;
+          seen.j = slot - pc.ctx;
+        }
+      }
+      bar_wait(&sm.sfull[wg], ps, sm, a.err);
+      ps ^= 1;
+      tc_after();
+      const float ex = masked ? tile_excess<NC, true>(tS, nch, c2, nm, seen, mask)
+                              : tile_excess<NC, false>(tS, nch, c2, nm, seen, mask);
+      if (jobs > 0) {  // the last tile's product: P may be written, O rescaled
+        bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
+        ppv ^= 1;
+        tc_after();
+      }
+      if (named_or(bar, 128, ex > kSlack)) {
+        if (masked) tile_maxima<NC, true>(tS, nch, a.c, seen, mask, sc.red[warp], lane);
+        else tile_maxima<NC, false>(tS, nch, a.c, seen, mask, sc.red[warp], lane);
+        named_sync(bar, 128);
+        if (wt < ncj) {
+          const float mx = fmaxf(fmaxf(sc.red[0][wt], sc.red[1][wt]),
+                                 fmaxf(sc.red[2][wt], sc.red[3][wt]));
+          const float mo = -nm[wt];
+          const float mn = fmaxf(mo, mx);
+          fac[wt] = mn == mo ? 1.f : exp2f(mo - mn);
+          nm[wt] = -mn;
+        }
+        named_sync(bar, 128);
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i)
+          if (2 * i < ncj) l[i] = mul2(l[i], *reinterpret_cast<const f32x2*>(fac + 2 * i));
+        if (jobs > 0) {
+#pragma unroll 1
+          for (int k = 0; k < nch; ++k) {
+            uint32_t o[16];
+            tm_ld16(tO + k * 16, o);
+            tm_wait_ld(o);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[k * 16 + i]);
+            tm_st16(tO + k * 16, o);
+          }
+          tm_wait_st();
+        }
+        named_sync(bar, 128);  // the factors lie where P goes
+      }
+      if (masked) tile_probs<T, NC, true>(tS, nch, c2, nm, seen, mask, P, wt, l);
+      else tile_probs<T, NC, false>(tS, nch, c2, nm, seen, mask, P, wt, l);
+      tc_before();
+      fence_async();
+      bar_arrive(&sm.pfull[wg]);
+      ++jobs;
+    }
+
+    // ---- end of the piece: l over the slots, then O ----
+    if (jobs > 0) {
+      bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
+      ppv ^= 1;
+      tc_after();
+    }
+    // each lane ends with the sum of one column of every 32 (halving exchange)
+#pragma unroll
+    for (int k = 0; k < NC / 32; ++k) {
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) up2(l[k * 16 + i], v[2 * i], v[2 * i + 1]);
+#pragma unroll
+      for (int h = 16; h > 0; h >>= 1) {
+        const bool up = lane & h;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+          const float send = up ? v[i] : v[i + h];
+          const float mine = up ? v[i + h] : v[i];
+          v[i] = mine + __shfl_xor_sync(0xffffffffu, send, h);
+        }
+      }
+      if (k * 32 + lane < ncj) sc.red[warp][k * 32 + lane] = v[0];
+    }
+    if (a.two) named_sync(bar, 128);
+    else named_sync(3, 256);
+    const int h = pc.item / a.RB, r0 = pc.item % a.RB * a.rows_per_block + colbase;
+    const int rows = min(a.rows_per_block, a.R - r0 + colbase) - colbase;  // of this job's columns
+    const bool direct = pc.t0 == 0 && pc.count == pc.T;
+    const bool first_piece = left0 == pc.left + pc.count;
+    const long long pslot = (2ll * blockIdx.x + (first_piece ? 0 : 1)) * a.cols;
+    // alternate tiles: which warpgroups took part
+    const bool used0 = a.two ? wg == 0 : pc.count > 1 || (gj & 1) == 0;
+    const bool used1 = a.two ? wg == 1 : pc.count > 1 || (gj & 1) == 1;
+    {
+      // weights of the warpgroups' O, into fac
+      const int cc = wt;  // column
+      if (cc < rows && cc < ncj && (a.two || wg == 0)) {
+        const float m0 = used0 ? -sm.nm[0][cc] : kNoScore, m1 = used1 ? -sm.nm[1][cc] : kNoScore;
+        const float M = fmaxf(m0, m1);
+        const float w0 = used0 ? (m0 == M ? 1.f : exp2f(m0 - M)) : 0.f;
+        const float w1 = used1 ? (m1 == M ? 1.f : exp2f(m1 - M)) : 0.f;
+        float L = 0.f;
+        if (used0)
+          L += w0 * ((sc0.red[0][cc] + sc0.red[1][cc]) + (sc0.red[2][cc] + sc0.red[3][cc]));
+        if (used1)
+          L += w1 * ((sc1.red[0][cc] + sc1.red[1][cc]) + (sc1.red[2][cc] + sc1.red[3][cc]));
+        {
+          const bool empty = mask[cc] == 0 || L == 0.f;
+          if (direct) {
+            const float inv = empty ? 0.f : 1.f / L;
+            (a.two ? sc : sc0).fac[cc] = w0 * inv + (a.two ? w1 * inv : 0.f);
+            if (!a.two) sc1.fac[cc] = w1 * inv;
+            if (a.lse)
+              a.lse[(static_cast<long long>(pc.b) * a.nodes.N + (r0 + cc) / a.G) * a.Hq + h * a.G +
+                    (r0 + cc) % a.G] =
+                  empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          } else {
+            (a.two ? sc : sc0).fac[cc] = a.two ? w0 + w1 : w0;
+            if (!a.two) sc1.fac[cc] = w1;
+            a.part_ml[pslot + colbase + cc] = make_float2(M, L);
+          }
+        }
+      }
+    }
+    if (a.two) named_sync(bar, 128);
+    else named_sync(3, 256);
+    {
+      // columns by eights: shared out over the warpgroups (alternate tiles)
+      // and, where O^T repeats itself, over the two copies
+      const int d = wt & (LANES - 1);
+      const int groups = (a.two ? 1 : 2) * (128 / LANES);
+      const int me = (a.two ? 0 : wg) * (128 / LANES) + wt / LANES;
+      const unsigned long long nf =
+          sm.nf[qb][0] | (static_cast<unsigned long long>(sm.nf[qb][1]) << 32);
+      char* obase = a.out + 2 * ((static_cast<long long>(pc.b) * a.nodes.N * a.Hq + h * a.G) * D);
+      for (int k = me; k < ncj / 8; k += groups) {
+        uint32_t v0[8], v1[8];
+        if (used0) tm_ld8(tO0 + k * 8, v0);
+        if (used1) tm_ld8(tO0 + kMaxJob + k * 8, v1);
+        if (used0) tm_wait_ld8(v0);
+        if (used1) tm_wait_ld8(v1);
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x = 0.f;
+          if (a.two) {
+            x = fac[k * 8 + i] * __uint_as_float(wg == 0 ? v0[i] : v1[i]);
+          } else {
+            if (used0) x = sc0.fac[k * 8 + i] * __uint_as_float(v0[i]);
+            if (used1) x = fmaf(sc1.fac[k * 8 + i], __uint_as_float(v1[i]), x);
+          }
+          o[i] = x;
+        }
+        if (nf) {  // nodes with NaN or infinite values, for the rows that see them
+          for (int j = 0; j < a.nodes.N; ++j) {
+            if (!((nf >> j) & 1)) continue;
+            int page, off;
+            if (!kv_slot(a.table + pc.b * a.table_stride, a.width, a.pages, a.ps,
+                         static_cast<long long>(pc.ctx) + j, page, off))
+              continue;
+            const unsigned short raw = *reinterpret_cast<const unsigned short*>(
+                a.vcache + 2 * (page * a.v_page + off * a.v_slot + h * a.v_head + d));
+            const float v = T::lo(raw);
+            if (fabsf(v) < INFINITY) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if ((mask[k * 8 + i] >> j) & 1) o[i] += v;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const int c0 = k * 8 + i;
+          if (direct) {
+            // neighbouring lanes trade so that each stores two entries of one row
+            const bool z0 = mask[k * 8 + i] == 0, z1 = mask[k * 8 + i + 1] == 0;
+            const float x0 = z0 ? 0.f : o[i], x1 = z1 ? 0.f : o[i + 1];
+            const bool odd = d & 1;
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
+            const uint32_t w = odd ? T::pack(other, x1) : T::pack(x0, other);
+            const int cr = c0 + (d & 1), r = r0 + cr;
+            if (cr < rows)
+              *reinterpret_cast<uint32_t*>(
+                  obase + 2 * (static_cast<long long>(r / a.G * a.Hq + r % a.G) * D + (d & ~1))) = w;
+          } else {
+            if (c0 < rows) a.part_o[(pslot + colbase + c0) * D + d] = o[i];
+            if (c0 + 1 < rows) a.part_o[(pslot + colbase + c0 + 1) * D + d] = o[i + 1];
+          }
+        }
+      }
+    }
+    bar_arrive(&sm.qempty[qb]);
+    tc_before();
+    if (a.two) named_sync(bar, 128);
+    else named_sync(3, 256);
+    gj += pc.count;
+    ++item_no;
+  }
+}
+
+// Q rows of a piece into shared memory, their masks and places.
+template <class T, int D>
+__device__ __forceinline__ void gather_rows(const Args& a, Misc& sm, const Pieces& pc, char* Q, int qb,
+                                            int at) {
+  const int h = pc.item / a.RB, rb = pc.item % a.RB;
+  const int r0 = rb * a.rows_per_block;
+  const int rows = min(a.rows_per_block, a.R - r0);
+  const int n = pc.tot - pc.ctx;
+  const int* parent = a.nodes.parent ? a.nodes.parent + static_cast<long long>(pc.b) * a.nodes.N : nullptr;
+  if (at < 2) sm.nf[qb][at] = 0;
+  bool any_broken = false;
+  for (int i = at; i <= kMaxNodes; i += 64) {
+    uint64_t m = 0;
+    int depth;
+    bool broken = false;
+    if (i < n) node_way(parent, n, i, m, depth, broken);
+    any_broken |= broken;
+    sm.anc[qb][i] = m;
+  }
+  for (int r = at; r < a.cols; r += 64)
+    sm.node[qb * 64 + r] = static_cast<uint8_t>(r < rows ? (r0 + r) / a.G : kMaxNodes);
+  if (any_broken) atomicOr(a.err, kErrBadTree);
+  named_sync(4, 64);
+  constexpr int PER = D / 8;
+  const int tasks = a.cols * PER;
+  const char* qb_ = a.q + 2 * (pc.b * a.q_b + static_cast<long long>(h) * a.G * a.q_h);
+  for (int k0 = at; k0 < tasks; k0 += 64 * 8) {
+    uint4 x[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = k0 + u * 64;
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (k < tasks) {
+        const int r = k / PER, v = k % PER;
+        const int i = sm.node[qb * 64 + r];
+        if (sm.anc[qb][i]) {
+          const int g = r0 + r - i * a.G;
+          x[u] = *reinterpret_cast<const uint4*>(qb_ + 2 * (i * a.q_n + g * a.q_h + v * 8));
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int k = k0 + u * 64;
+      if (k < tasks) {
+        const int r = k / PER, v = k % PER;
+        *reinterpret_cast<uint4*>(Q + (v / 8) * (a.cols * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4)) = x[u];
+      }
+    }
+  }
+  fence_async();
+}
+
+// Clears V rows that are no slot of the sequence and the NaN or infinite
+// entries of its nodes (whose bits go to nf).
+template <class T, int D>
+__device__ __forceinline__ void clean_tile(const Args& a, Misc& sm, const Pieces& pc, int t, char* V, int qb,
+                                           int at) {
+  int first, count;
+  tile_slots(a, t, first, count);
+  constexpr int PER = D / 8;
+  for (int k = at; k < kTile * PER; k += 64) {
+    const int r = k / PER, v = k % PER;
+    const int rs = row_slot(a, r, count);
+    const int slot = rs < 0 ? 0x7fffffff : first + rs;
+    if (slot < pc.ctx) continue;
+    uint4* p = reinterpret_cast<uint4*>(V + (v / 8) * kHalf + r * 128 + (((v & 7) ^ (r & 7)) << 4));
+    if (slot >= pc.tot) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 x = *p;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!(fabsf(T::lo(w[i])) < INFINITY)) { w[i] &= 0xffff0000u; bad = true; }
+      if (!(fabsf(T::hi(w[i])) < INFINITY)) { w[i] &= 0x0000ffffu; bad = true; }
+    }
+    if (bad) {
+      *p = make_uint4(w[0], w[1], w[2], w[3]);
+      const int j = slot - pc.ctx;
+      atomicOr(&sm.nf[qb][j >> 5], 1u << (j & 31));
+    }
+  }
+  fence_async();
+}
+
+template <class T, int D, int NC>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap mapk, const __grid_constant__ CUtensorMap mapv,
+                const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) char base[];
+  constexpr int HALVES = D / 64;
+  constexpr int kSlotBytes = HALVES * kHalf;
+  char* ring = base;
+  char* Q = ring + a.ring * kSlotBytes;
+  const int qbytes = a.cols * D * 2;
+  char* P = Q + a.qbufs * qbytes;
+  const int pbytes = ((a.ncj + 63) / 64) * kHalf;
+  Misc& sm = *reinterpret_cast<Misc*>(P + 2 * pbytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = gridDim.x, B = a.nodes.B;
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxRing; ++i) {
+      bar_init(&sm.full[i], 1);
+      bar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sm.qfull[i], 64);
+      bar_init(&sm.qempty[i], 256);
+      bar_init(&sm.sfull[i], 1);
+      bar_init(&sm.pfull[i], 128);
+      bar_init(&sm.pvdone[i], 1);
+    }
+    bar_init(&sm.vready, 1);
+    bar_init(&sm.vclean, 64);
+    bar_init(&sm.done, 1);
+    sm.abort = 0;
+    sm.b0 = 0;
+    sm.off0 = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sptr(&sm.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapk));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapv));
+  }
+  // rows of the ring that no copy writes are zeros (they meet P = 0, and
+  // must not be NaN)
+  if (a.cover < kTile) {
+    for (int i = tid; i < a.ring * kSlotBytes / 16; i += kAttnThreads)
+      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+    fence_async();
+  }
+
+  // ---- this CTA's range: tiles before each sequence (a block scan over the
+  // batch), and where the range starts ----
+  {
+    const int per = (B + kAttnThreads - 1) / kAttnThreads;
+    const int f = tid * per, e = min(B, f + per);
+    const int items = a.Hkv * a.RB;
+    long long mine = 0;
+    bool any_bad = false;
+    for (int b = f; b < e; ++b) {
+      int ctx;
+      bool bad;
+      mine += static_cast<long long>(tiles_of(a, seq_len(a, b, ctx, bad))) * items;
+      any_bad |= bad;
+    }
+    if (any_bad && blockIdx.x == 0) atomicOr(a.err, kErrBadLength);
+    long long inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += o;
+    }
+    long long* pre = reinterpret_cast<long long*>(Q);  // not in use yet
+    if (lane == 31) pre[warp] = inc;
+    __syncthreads();
+    long long before = 0, W = 0;
+    for (int i = 0; i < kAttnThreads / 32; ++i) {
+      if (i < warp) before += pre[i];
+      W += pre[i];
+    }
+    before += inc - mine;
+    const long long lo = range_start(W, blockIdx.x, C), hi = range_start(W, blockIdx.x + 1, C);
+    if (tid == 0) {
+      sm.lo = lo;
+      sm.hi = hi;
+    }
+    if (lo < hi && lo >= before && lo < before + mine) {
+      long long p = before;
+      for (int b = f; b < e; ++b) {
+        int ctx;
+        bool bad;
+        const long long w = static_cast<long long>(tiles_of(a, seq_len(a, b, ctx, bad))) * items;
+        if (lo < p + w) {
+          sm.b0 = b;
+          sm.off0 = lo - p;
+          break;
+        }
+        p += w;
+      }
+    }
+    if (blockIdx.x == 0) {  // for the joining kernel
+      long long p = before;
+      for (int b = f; b < e; ++b) {
+        int ctx;
+        bool bad;
+        a.sched[b] = p;
+        p += static_cast<long long>(tiles_of(a, seq_len(a, b, ctx, bad))) * items;
+      }
+      if (tid == 0) a.sched[B] = W;
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  pdl_trigger();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp == 0) {
+    // ---- K and V tiles ----
+    Pieces pc(a, sm);
+    int slot = 0;
+    uint32_t phase = 0;
+    bool bad_page = false;
+    while (pc.next()) {
+      const int h = pc.item / a.RB;
+      const int* trow = a.table + pc.b * a.table_stride;
+      const int npages = (pc.tot + a.ps - 1) / a.ps;
+      auto lookup = [&](int t) {
+        const int p = a.ps <= kTile ? t * a.ppt + lane : t / a.tpp;
+        int id = 0;
+        if ((a.ps > kTile || lane < a.ppt) && p < npages) {
+          id = __ldg(trow + p);
+          if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.pages)) {
+            bad_page = true;
+            id = a.pages;  // out of bounds: zeros
+          }
+        }
+        return id;
+      };
+      int id = lookup(pc.t0);
+      for (int t = pc.t0; t < pc.t0 + pc.count; ++t) {
+        const int cur = id;
+        if (t + 1 < pc.t0 + pc.count) id = lookup(t + 1);
+        const int boxes = a.ps <= kTile ? min(a.ppt, npages - t * a.ppt) : 1;
+        const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const bool ok = bar_wait(&sm.empty[slot], phase ^ 1, sm, a.err) &&
+                          !*reinterpret_cast<volatile int*>(&sm.abort);
+          if (__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) bar_expect(&sm.full[slot], boxes * a.box * 128 * HALVES);
+            __syncwarp();
+            if (lane < boxes) {
+              const uint32_t dst = sptr(ring + slot * kSlotBytes) + lane * a.box * 128;
+#pragma unroll
+              for (int d = 0; d < HALVES; ++d)
+                tma_rows(dst + d * kHalf, kv ? &mapv : &mapk, d * 64, s0, h, cur, &sm.full[slot]);
+            }
+          }
+          __syncwarp();
+          if (++slot == a.ring) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+    }
+    if (bad_page) atomicOr(a.err, kErrBadPage);
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---- tensor cores ----
+      const uint32_t iqk = instr<T>(a.ncj, false, false), ipv = instr<T>(a.ncj, true, true);
+      const uint32_t ring_s = sptr(ring), q_s = sptr(Q), p_s = sptr(P);
+      Jobs jq(a, sm), jp(a, sm);
+      int kslot = -2, vslot = -1;        // ring slots of the current tiles
+      uint32_t kph = 0, vph = 0, ppf = 0, vcl = 0;
+      bool more_q = true, tail = false;
+      auto scores = [&]() {
+        bool nt;
+        if (!more_q || !jq.next(nt)) {
+          more_q = false;
+          return;
+        }
+        if (nt) {
+          kslot += 2;
+          if (kslot >= a.ring) { kslot -= a.ring; kph ^= 1; }
+        }
+        const int qb = jq.item_no % a.qbufs;
+        if (jq.in_item == 0) bar_wait(&sm.qfull[qb], (jq.item_no / a.qbufs) & 1, sm, a.err);
+        if (nt) bar_wait(&sm.full[kslot], kph, sm, a.err);
+        tc_after();
+        const int w = jq.wg();
+        const uint32_t ka = ring_s + kslot * kSlotBytes;
+        const uint32_t qa = q_s + qb * qbytes + (a.two ? w * a.ncj * 128 : 0);
+        const uint32_t d = tmem + w * kMaxJob;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (k & 3) * 32;
+          tc_mma(d, operand(ka + (k / 4) * kHalf + o, 16, 1024),
+                 operand(qa + (k / 4) * a.cols * 128 + o, 16, 1024), iqk, k > 0);
+        }
+        if (jq.last_of_tile()) tc_commit(&sm.empty[kslot]);
+        tc_commit(&sm.sfull[w]);
+      };
+      scores();
+      scores();
+      bool nt;
+      while (jp.next(nt)) {
+        const int w = jp.wg();
+        if (nt) {
+          vslot += 2;
+          if (vslot >= a.ring) { vslot -= a.ring; vph ^= 1; }
+          bar_wait(&sm.full[vslot], vph, sm, a.err);
+          tail = jp.pc.tail(jp.t);
+          if (tail) bar_arrive(&sm.vready);
+        }
+        bar_wait(&sm.pfull[w], (ppf >> w) & 1, sm, a.err);
+        if (nt && tail) {
+          bar_wait(&sm.vclean, vcl, sm, a.err);
+          vcl ^= 1;
+        }
+        ppf ^= 1u << w;
+        tc_after();
+        const uint32_t va = ring_s + vslot * kSlotBytes;
+        const uint32_t pa = p_s + w * pbytes;
+        const uint32_t d = tmem + 2 * kMaxJob + w * kMaxJob;
+        const bool fresh = jp.in_item < 2;  // the warpgroup's first tile of the piece
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          tc_mma(d, operand(va + k * 2048, D == 128 ? kHalf : 0, 1024), operand(pa + k * 2048, kHalf, 1024), ipv,
+                 !(fresh && k == 0));
+        if (jp.last_of_tile()) tc_commit(&sm.empty[vslot]);
+        tc_commit(&sm.pvdone[w]);
+        scores();
+      }
+      tc_commit(&sm.done);
+      bar_wait(&sm.done, 0, sm, a.err);
+    }
+    __syncwarp();
+  } else if (warp < 4) {
+    // ---- rows of Q; tiles with drafted nodes ----
+    const int at = tid - 64;
+    Pieces pq(a, sm), pv(a, sm);
+    int qi = 0, vi = 0, tiles = 0;
+    uint32_t vrd = 0;
+    auto rows = [&]() {
+      if (!pq.next()) return;
+      const int qb = qi % a.qbufs;
+      if (qi >= a.qbufs) bar_wait(&sm.qempty[qb], ((qi / a.qbufs) & 1) ^ 1, sm, a.err);
+      gather_rows<T, D>(a, sm, pq, Q + qb * qbytes, qb, at);
+      bar_arrive(&sm.qfull[qb]);
+      ++qi;
+    };
+    rows();
+    while (pv.next()) {
+      if (a.qbufs == 2) rows();
+      for (int t = pv.t0; t < pv.t0 + pv.count; ++t) {
+        if (!pv.tail(t)) continue;
+        const int s = (2 * (tiles + t - pv.t0) + 1) % a.ring;  // the V tile's slot
+        bar_wait(&sm.vready, vrd, sm, a.err);
+        vrd ^= 1;
+        clean_tile<T, D>(a, sm, pv, t, ring + s * kSlotBytes, vi % a.qbufs, at);
+        bar_arrive(&sm.vclean);
+      }
+      tiles += pv.count;
+      ++vi;
+      if (a.qbufs == 1) rows();
+    }
+    // sequences without tiles: their rows are empty
+    for (int b = blockIdx.x; b < B; b += C) {
+      int ctx;
+      bool bad;
+      if (seq_len(a, b, ctx, bad) != 0) continue;
+      const long long n = static_cast<long long>(a.nodes.N) * a.Hq;
+      uint4* o = reinterpret_cast<uint4*>(a.out + 2 * (b * n * D));
+      for (long long i = at; i < n * D / 8; i += 64) o[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (long long i = at; i < n; i += 64) a.lse[b * n + i] = -INFINITY;
+    }
+  } else {
+    const int wg = (warp - 4) >> 2;
+    softmax_role<T, D, NC>(a, sm, tmem, P, pbytes, wg);
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 0 && *reinterpret_cast<volatile int*>(&sm.abort)) {
+    // given up: let copies in flight land before the shared memory is freed
+    const unsigned long long t0 = now_ns();
+    while (now_ns() - t0 < 20000000ull) __nanosleep(100000);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the parts of the (sequence, head, row block)s that range borders cut:
+//     M = max m_i,  w_i = 2^(m_i - M),  o = sum w_i O_i / sum w_i l_i
+// in range order.  blockIdx.x: a border between two ranges; the first border
+// inside a cut item does its work, a warp per row.
+// ---------------------------------------------------------------------------
+constexpr int kJoinWarps = 8;
+
+template <class T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __grid_constant__ Args a, int C) {
+  constexpr int E = D / 32;
+  pdl_wait();
+  const int B = a.nodes.B;
+  const long long W = a.sched[B];
+  const int c = blockIdx.x + 1;
+  const long long x = range_start(W, c, C);
+  if (x >= W) return;
+  int lo = 0, hi = B;  // last b with sched[b] <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.sched[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  const int b = lo;
+  const int items = a.Hkv * a.RB;
+  const int Tn = static_cast<int>((a.sched[b + 1] - a.sched[b]) / items);
+  const long long first = a.sched[b];
+  const int item = static_cast<int>((x - first) / Tn);
+  const long long s = first + static_cast<long long>(item) * Tn, e = s + Tn;
+  if (x == s || range_start(W, c - 1, C) > s) return;  // not cut here, or an earlier border's item
+  const int h = item / a.RB, rb = item % a.RB;
+  const int r0 = rb * a.rows_per_block, rows = min(a.rows_per_block, a.R - r0);
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= rows) return;
+  const int i = (r0 + r) / a.G, g = (r0 + r) % a.G;
+  int ctx;
+  bool bad, broken;
+  const int tot = seq_len(a, b, ctx, bad);
+  uint64_t mask;
+  int depth;
+  const bool there = node_way(a.nodes.parent ? a.nodes.parent + static_cast<long long>(b) * a.nodes.N : nullptr,
+                              tot - ctx, i, mask, depth, broken);
+  auto part = [&](int k) { return (2ll * k + (k == c - 1 && range_start(W, k, C) < s ? 1 : 0)) * a.cols + r; };
+  float M = kNoScore;
+  int last = c - 1;
+  for (int k = c - 1; k < C && range_start(W, k, C) < e; ++k) {
+    last = k;
+    if (range_start(W, k + 1, C) == range_start(W, k, C)) continue;
+    M = fmaxf(M, a.part_ml[part(k)].x);
+  }
+  float L = 0.f, o[E];
+#pragma unroll
+  for (int q = 0; q < E; ++q) o[q] = 0.f;
+#pragma unroll 2
+  for (int k = c - 1; k <= last; ++k) {
+    if (range_start(W, k + 1, C) == range_start(W, k, C)) continue;
+    const long long p = part(k);
+    const float2 ml = a.part_ml[p];
+    const float w = ml.x == M ? 1.f : exp2f(ml.x - M);
+    L = fmaf(w, ml.y, L);
+    const float* src = a.part_o + p * D + lane * E;
+#pragma unroll
+    for (int q = 0; q < E; q += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + q);
+      o[q] = fmaf(w, v.x, o[q]);
+      o[q + 1] = fmaf(w, v.y, o[q + 1]);
+    }
+  }
+  const bool empty = !there || L == 0.f;
+  const float inv = empty ? 0.f : 1.f / L;
+  const long long row = (static_cast<long long>(b) * a.nodes.N + i) * a.Hq + h * a.G + g;
+  char* out = a.out + 2 * (row * D + lane * E);
+#pragma unroll
+  for (int q = 0; q < E; q += 2)
+    *reinterpret_cast<uint32_t*>(out + 2 * q) = empty ? 0u : T::pack(o[q] * inv, o[q + 1] * inv);
+  if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) !=
+            cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// {D, page_size, Hkv, pages}; boxes of 64 columns and `box` slots of one head
+// of one page.
+bool encode(CUtensorMap* m, void* base, int dtype, int D, int ps, int H, int pages, long long slot,
+            long long head, long long page, int box) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(ps),
+                              static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot) * 2, static_cast<cuuint64_t>(head) * 2,
+                                 static_cast<cuuint64_t>(page) * 2};
+  const cuuint32_t bx[4] = {64, static_cast<cuuint32_t>(box), 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(m, dtype == Bf16::kId ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
+            dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Shape {
+  int RB, rows, two, ncj, cols;
+};
+Shape shape_of(int R) {
+  Shape s;
+  s.RB = (R + kMaxRows - 1) / kMaxRows;
+  s.rows = (R + s.RB - 1) / s.RB;
+  s.two = s.rows > kMaxJob;
+  const int per = s.two ? (s.rows + 1) / 2 : s.rows;
+  s.ncj = (per + 15) / 16 * 16;
+  s.cols = s.two ? 2 * s.ncj : s.ncj;
+  return s;
+}
+
+struct Layout {
+  size_t sched, ml, o, total;
+};
+Layout layout_of(int B, int R, int D) {
+  const Shape s = shape_of(R);
+  Layout L;
+  L.sched = 256;
+  L.ml = (L.sched + 8 * (static_cast<size_t>(B) + 1) + 255) / 256 * 256;
+  L.o = (L.ml + 8ull * 2 * kMaxCtas * s.cols + 255) / 256 * 256;
+  L.total = L.o + 4ull * 2 * kMaxCtas * s.cols * D;
+  return L;
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
+}
+
+template <class T, int D, int NC>
+cudaError_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C, size_t smem,
+                     cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  if (e != cudaSuccess) return e;
+  attn_kernel<T, D, NC><<<C, kAttnThreads, smem, s>>>(mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || C < 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C - 1, (a.rows_per_block + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_combine_kernel<T, D>, a, C);
+}
+
+template <class T, int D>
+cudaError_t launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C, size_t smem,
+                     cudaStream_t s) {
+  if (a.ncj <= 32) return launch_t<T, D, 32>(mk, mv, a, C, smem, s);
+  if (a.ncj <= 64) return launch_t<T, D, 64>(mk, mv, a, C, smem, s);
+  return launch_t<T, D, 128>(mk, mv, a, C, smem, s);
 }
 
 }  // namespace
 
+size_t tree_attention_bytes(int B, int N, int G, int D) { return layout_of(B, N * G, D).total; }
+
 cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStream_t s) {
-  return dtype == Bf16::kId ? attn_t<Bf16>(p, D, s) : attn_t<F16>(p, D, s);
+  Args a;
+  a.nodes = p.nodes;
+  a.table = p.kv.table;
+  a.table_stride = p.kv.table_stride;
+  a.width = p.kv.width; a.pages = p.kv.pages; a.ps = p.kv.ps;
+  a.Hq = p.Hq; a.Hkv = p.kv.Hkv; a.G = p.G; a.R = p.nodes.N * p.G;
+  const Shape sh = shape_of(a.R);
+  a.RB = sh.RB; a.rows_per_block = sh.rows; a.two = sh.two; a.ncj = sh.ncj; a.cols = sh.cols;
+  a.q = p.q; a.q_b = p.q_b; a.q_n = p.q_n; a.q_h = p.q_h;
+  a.c = p.scale * 1.4426950408889634f;
+  a.out = p.out; a.lse = p.lse;
+  a.vcache = p.kv.v; a.v_page = p.kv.v_page; a.v_slot = p.kv.v_slot; a.v_head = p.kv.v_head;
+  a.err = p.err;
+  const Layout L = layout_of(p.nodes.B, a.R, D);
+  char* ws = reinterpret_cast<char*>(p.err);
+  a.sched = reinterpret_cast<long long*>(ws + L.sched);
+  a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+  a.part_o = reinterpret_cast<float*>(ws + L.o);
+  // tiles: whole pages up to 128 slots; boxes of a multiple of 8 rows (the
+  // swizzle's period), what exceeds the page filled with zeros
+  if (a.ps <= kTile) {
+    a.box = (a.ps + 7) / 8 * 8;
+    a.ppt = kTile / a.box;
+    if (a.ppt > 32) a.ppt = 32;
+    a.tk = a.ppt * a.ps;
+    a.tpp = 1;
+    a.cover = a.ppt * a.box;
+    a.ragged = a.tk != kTile;
+  } else {
+    a.box = kTile;
+    a.ppt = 1;
+    a.tk = kTile;
+    a.tpp = (a.ps + kTile - 1) / kTile;
+    a.cover = kTile;
+    a.ragged = a.ps % kTile != 0;
+  }
+  const int slot = D * 2 * kTile;
+  const size_t qb = static_cast<size_t>(a.cols) * D * 2, pb = ((a.ncj + 63) / 64) * static_cast<size_t>(kHalf);
+  a.qbufs = a.cols <= 64 ? 2 : 1;
+  const size_t fixed = a.qbufs * qb + 2 * pb + sizeof(Misc);
+  int ring = static_cast<int>((kSmemMax - fixed) / slot);
+  a.ring = ring < kMaxRing ? ring : kMaxRing;
+  if (a.ring < 3) return cudaErrorInvalidConfiguration;
+  const size_t smem = fixed + static_cast<size_t>(a.ring) * slot;
+  CUtensorMap mk, mv;
+  if (!encode(&mk, p.kv.k, dtype, D, a.ps, a.Hkv, a.pages, p.kv.k_slot, p.kv.k_head, p.kv.k_page, a.box) ||
+      !encode(&mv, p.kv.v, dtype, D, a.ps, a.Hkv, a.pages, p.kv.v_slot, p.kv.v_head, p.kv.v_page, a.box))
+    return cudaErrorInvalidValue;
+  int C = sm_count();
+  if (C < 1) return cudaErrorInvalidDevice;
+  C = C < kMaxCtas ? C : kMaxCtas;
+  if (dtype == Bf16::kId)
+    return D == 128 ? launch_d<Bf16, 128>(mk, mv, a, C, smem, s) : launch_d<Bf16, 64>(mk, mv, a, C, smem, s);
+  return D == 128 ? launch_d<F16, 128>(mk, mv, a, C, smem, s) : launch_d<F16, 64>(mk, mv, a, C, smem, s);
 }
 
 }  // namespace ssd
