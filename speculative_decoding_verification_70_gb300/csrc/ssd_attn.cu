@@ -18,24 +18,25 @@
 // the workspace, and attn_combine_kernel joins them in range order.
 //
 // Warps of a CTA:
-//   0      copies K and V tiles, page by page, by TMA into a ring of slots
+//   0, 2   copy K and V tiles, page by page, by TMA into a ring of slots
 //          (128-byte swizzle; a page id out of range is a coordinate out of
 //          bounds, which TMA fills with zeros)
 //   1      issues tcgen05.mma: S^T (K, Q from shared memory) two jobs ahead
 //          of O^T (V^T read transposed from the same row-major tile, P^T from
 //          shared memory)
-//   2, 3   gather the next rows of Q, the rows' ancestor masks, and clear what
-//          must not be multiplied in tiles that hold drafted nodes: V rows
-//          behind the sequence's end, and NaN or infinite entries of nodes
-//          (added at the end for the rows that see them)
-//   4..11  two warpgroups for the softmax, a slot per thread.  Up to 128 rows:
-//          the warpgroups take alternate tiles and keep their own m, l, O;
-//          more: the same tiles, half of the rows each.
+//   3      clears, in tiles that hold drafted nodes, what must not be
+//          multiplied: V rows behind the sequence's end, and NaN or infinite
+//          entries of nodes (added at the end for the rows that see them)
+//   4..11  two warpgroups for the softmax, which also fetch the rows of Q and
+//          write the results.  Up to 128 rows: the warpgroups take alternate
+//          tiles and keep their own m, l, O; more: the same tiles, half of
+//          the rows each.
 //
-// m follows the running maximum lazily: as long as no score exceeds it by
-// more than 2^8, the tile is used as it is (P keeps its relative precision,
-// l and O their range).  Otherwise the warpgroup finds the tile's row maxima
-// and rescales l and O.
+// m follows the running maximum lazily: P, l and the largest excess over m come
+// out of one pass over the scores, and only where that exceeds 2^30 (2^8 for
+// fp16, whose range is short) the warpgroup finds the tile's row maxima,
+// rescales l and O and repeats the pass.  P keeps its relative precision at
+// any excess, l and O their 32-bit range.
 #include <cuda.h>
 #include <math.h>
 
@@ -52,8 +53,8 @@ constexpr int kMaxRing = 8;
 constexpr int kMaxRows = 256;        // rows of a row block
 constexpr int kMaxJob = 128;         // rows of a job (one warpgroup's columns)
 constexpr int kMaxCtas = 160;
+constexpr int kNoRow = 0x7fffffff;   // a column without a row (rows of zeros: ~row)
 constexpr float kNoScore = -1e30f;   // m of a row that has seen nothing
-constexpr float kSlack = 8.f;
 constexpr int kSmemMax = 227 * 1024;
 
 struct Args {
@@ -72,6 +73,7 @@ struct Args {
   const char* q;
   long long q_b, q_n, q_h;
   float c;                  // scale * log2(e)
+  int zero;                 // scale 0: Q counts as zeros (and c as 1)
   char* out;
   float* lse;
   const char* vcache;       // for the rows that see a node with NaN or infinities
@@ -85,13 +87,13 @@ struct Args {
 // Shared memory behind the ring, Q and P (256 rows leave 3 KB for it).
 struct alignas(16) Misc {
   uint64_t full[kMaxRing], empty[kMaxRing];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], pvdone[2], vready, vclean, done;
+  uint64_t qfull[2], sfull[2], pfull[2], pvdone[2], vready, vclean, done;
   uint64_t anc[2][kMaxNodes + 1];   // nodes' ancestors (0: absent); the last: no row
-  long long lo, hi, off0;
+  long long left;
   alignas(16) float nm[2][kMaxJob]; // -m
   uint8_t node[kMaxRows];           // rows' nodes; two buffers of 64 or one of 256
   unsigned nf[2][2];                // nodes with NaN or infinite values
-  int b0;
+  int b0, h0, rb0, t0;              // first piece
   unsigned tmem;
   int abort;
 };
@@ -102,6 +104,7 @@ static_assert(sizeof(Misc) <= 3072, "shared memory of 256 rows");
 struct Scratch {
   float red[4][kMaxJob];
   float fac[kMaxJob];
+  int row[kMaxJob];  // node * Hq + head of the group, its complement, or kNoRow
 };
 
 // ---------------------------------------------------------------------------
@@ -124,10 +127,10 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.b32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(sptr(b)), "r"(parity)
+      : "r"(sptr(b)), "r"(parity), "r"(20000)  // sleeps up to 20 us a try
       : "memory");
   return ok != 0;
 }
@@ -140,17 +143,20 @@ __device__ __forceinline__ unsigned long long now_ns() {
 // Bounded wait: after a second (or once another wait of the CTA gave up) the
 // CTA runs on without waiting, to its end; the error word says so.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Misc& sm, int* err) {
-  if (bar_try(b, parity)) return true;
-  const unsigned long long t0 = now_ns();
-  while (!bar_try(b, parity)) {
-    if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
-    if (now_ns() - t0 > 1000000000ull) {
-      *reinterpret_cast<volatile int*>(&sm.abort) = 1;
-      atomicOr(err, kErrTimeout);
-      return false;
+  unsigned long long t0 = 0;
+  for (unsigned i = 1;; ++i) {
+    if (bar_try(b, parity)) return true;
+    if ((i & 31) == 0) {  // the global timer is slow to read
+      if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
+      const unsigned long long t = now_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > 1000000000ull) {
+        *reinterpret_cast<volatile int*>(&sm.abort) = 1;
+        atomicOr(err, kErrTimeout);
+        return false;
+      }
     }
   }
-  return true;
 }
 
 __device__ __forceinline__ void named_sync(int id, int n) {
@@ -186,6 +192,11 @@ __device__ __forceinline__ void tc_before() {
 }
 __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void tc_commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -252,6 +263,25 @@ __device__ __forceinline__ void tm_wait_ld8(uint32_t (&r)[8]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7])::"memory");
 }
+// 32 lanes x 16 columns as fragments: register [half][4 g + 2 r + i] of lane
+// 4 y + x is lane 16 half + 8 r + y, column 8 g + 2 x + i.
+__device__ __forceinline__ void tm_ld_frag(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(addr));
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15])
+      : "r"(addr + (16u << 16)));
+}
+__device__ __forceinline__ void tm_st_frag(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(addr));
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[8]), "r"(r[9]),
+               "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr + (16u << 16)));
+}
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -259,13 +289,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Largest value of the warp (NaN ignored).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // ---------------------------------------------------------------------------
 // the tiles of the batch
 // ---------------------------------------------------------------------------
@@ -298,51 +321,74 @@ __device__ __forceinline__ int seq_len(const Args& a, int b, int& ctx, bool& bad
   return n == 0 ? 0 : ctx + n;  // a sequence without nodes has no tiles
 }
 
+struct SeqTiles {
+  int T, ctx, tot, tail;  // tiles; lengths; the first tile with slots behind the context
+};
+__device__ __noinline__ SeqTiles seq_tiles(const Args& a, int b) {
+  SeqTiles q;
+  bool bad;
+  q.tot = seq_len(a, b, q.ctx, bad);
+  q.T = tiles_of(a, q.tot);
+  q.tail = a.ps <= kTile ? q.ctx / a.tk : (q.ctx / a.ps) * a.tpp + (q.ctx % a.ps) / kTile;
+  return q;
+}
+
 // First tile of CTA c's range.
 __device__ __forceinline__ long long range_start(long long W, int c, int C) { return W * c / C; }
 
 // The pieces of a CTA's range, one (sequence, head, row block) after another.
+// Only the first may start behind tile 0.
 struct Pieces {
-  const Args& a;
-  long long off, left;
-  int b, T, ctx, tot;
-  int item, t0, count;  // item = head * RB + row block; tiles t0 .. t0 + count
-  bool loaded;
-  __device__ Pieces(const Args& a_, const Misc& sm)
-      : a(a_), off(sm.off0), left(sm.hi - sm.lo), b(sm.b0), T(0), ctx(0), tot(0), item(0), t0(0), count(0),
-        loaded(false) {}
-  __device__ void load() {
-    bool bad;
-    tot = seq_len(a, b, ctx, bad);
-    T = tiles_of(a, tot);
+  long long left;     // tiles from t0 to the range's end
+  int b, h, rb;
+  int T, ctx, tot;    // of sequence b
+  int t0, end, tail;  // tiles t0 .. end - 1; the first with slots behind the context
+  bool fresh;
+  __device__ __forceinline__ void start(const Misc& sm) {
+    left = sm.left;
+    b = sm.b0;
+    h = sm.h0;
+    rb = sm.rb0;
+    t0 = sm.t0;
+    fresh = true;
   }
-  __device__ bool next() {
-    if (left <= 0) return false;
-    if (!loaded) {
-      loaded = true;
-      load();
-    }
-    const int per = a.Hkv * a.RB;
-    while (off >= static_cast<long long>(T) * per) {
-      off = 0;
-      if (++b >= a.nodes.B) {
-        left = 0;
-        return false;
+  __device__ __forceinline__ bool direct() const { return t0 == 0 && end == T; }
+  __device__ __forceinline__ void load(const Args& a) {
+    const SeqTiles q = seq_tiles(a, b);
+    T = q.T;
+    ctx = q.ctx;
+    tot = q.tot;
+    tail = q.tail;
+  }
+  __device__ __forceinline__ bool next(const Args& a) {
+    bool reload = fresh;
+    if (!fresh) {
+      left -= end - t0;
+      t0 = 0;
+      if (++rb == a.RB) {
+        rb = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          ++b;
+          reload = true;
+        }
       }
-      load();
     }
-    item = static_cast<int>(off / T);
-    t0 = static_cast<int>(off - static_cast<long long>(item) * T);
-    count = static_cast<int>(min(static_cast<long long>(T - t0), left));
-    off += count;
-    left -= count;
+    fresh = false;
+    if (left <= 0) return false;
+    if (reload) {
+#pragma unroll 1
+      for (;; ++b) {
+        if (b >= a.nodes.B) {
+          left = 0;
+          return false;
+        }
+        load(a);
+        if (T > 0) break;
+      }
+    }
+    end = static_cast<int>(min(static_cast<long long>(T), t0 + left));
     return true;
-  }
-  // Whether tile t holds slots behind the context.
-  __device__ bool tail(int t) const {
-    int first, n;
-    tile_slots(a, t, first, n);
-    return first + n > ctx;
   }
 };
 
@@ -350,47 +396,49 @@ struct Pieces {
 struct Jobs {
   Pieces pc;
   int t, half, in_item, item_no, gj;
-  bool two, started;
-  __device__ Jobs(const Args& a, const Misc& sm)
-      : pc(a, sm), t(0), half(0), in_item(0), item_no(-1), gj(-1), two(a.two != 0), started(false) {}
-  // Advances; new_tile: whether the job is the first of its tile.
-  __device__ bool next(bool& new_tile) {
-    new_tile = true;
-    if (started) {
-      if (two && half == 0) {
-        half = 1;
-        ++in_item;
-        ++gj;
-        new_tile = false;
-        return true;
-      }
-      half = 0;
-      ++t;
-      ++in_item;
-    }
-    ++gj;
-    if (!started || t == pc.t0 + pc.count) {
-      started = true;
-      if (!pc.next()) return false;
-      t = pc.t0;
-      in_item = 0;
-      ++item_no;
-    }
-    return true;
+  bool started;
+  __device__ void start(const Misc& sm) {
+    pc.start(sm);
+    half = in_item = 0;
+    item_no = gj = -1;
+    started = false;
   }
-  __device__ int wg() const { return two ? half : gj & 1; }
-  __device__ bool last_of_tile() const { return !two || half == 1; }
+  __device__ int wg(bool two) const { return two ? half : gj & 1; }
 };
+// Advances; new_tile: whether the job is the first of its tile.
+__device__ __forceinline__ bool next_job(const Args& a, Jobs& j, bool& new_tile) {
+  new_tile = true;
+  ++j.gj;
+  if (j.started) {
+    ++j.in_item;
+    if (a.two && j.half == 0) {
+      j.half = 1;
+      new_tile = false;
+      return true;
+    }
+    j.half = 0;
+    if (++j.t < j.pc.end) return true;
+  }
+  j.started = true;
+  if (!j.pc.next(a)) return false;
+  j.t = j.pc.t0;
+  j.in_item = 0;
+  ++j.item_no;
+  return true;
+}
 
 // ---------------------------------------------------------------------------
 // softmax: one tile for one warpgroup
 // ---------------------------------------------------------------------------
-// What a thread's slot means for the rows: seen by all, by none, or by those
-// whose mask holds node j.
+// A thread works on fragments: of every 16 rows (columns of S^T) it holds the
+// four 2 x + {0, 1}, 8 + 2 x + {0, 1} for the four slots y + {0, 8, 16, 24} of
+// its warp's 32 (lane 4 y + x), so a row's sum needs one register of four
+// threads' columns and m one load per two rows.
+
+// What each of the four slots means: < 0: seen by every row, kMaxNodes: by
+// none, else by the rows whose node has that ancestor.
 struct SlotSeen {
-  uint64_t all;  // ~0: every row
-  int j;
-  unsigned any;  // 0: no row
+  int j[4];
 };
 
 // Rows' masks: the ancestors of their nodes.
@@ -400,427 +448,474 @@ struct RowMasks {
   __device__ __forceinline__ uint64_t operator[](int r) const { return anc[node[r]]; }
 };
 
-template <bool MASKED>
-__device__ __forceinline__ void masked16(float (&t)[16], const SlotSeen& s, const RowMasks& mask, int r0) {
-  if (!MASKED) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const unsigned bit = static_cast<unsigned>((mask[r0 + i] | s.all) >> s.j) & s.any;
-    t[i] = bit ? t[i] : -INFINITY;
-  }
+__device__ __forceinline__ bool sees(int j, uint64_t m) {
+  return j < 0 || (j < kMaxNodes && ((m >> (j & 63)) & 1));
 }
 
-// t = c s - m of 16 rows.
-__device__ __forceinline__ void scaled16(const uint32_t (&s)[16], f32x2 c2, const float* nm, float (&t)[16]) {
+// t = c s - m of a fragment of 16 rows; t[8 g + 2 q + i]: row 8 g + x2 + i,
+// slot y + 8 q.
+__device__ __forceinline__ void frag_scores(const uint32_t (&s)[16], f32x2 c2, const float* nm, float (&t)[16]) {
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(nm + i);
-    const f32x2 a = fma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, m.x);
-    const f32x2 b = fma2(pk2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c2, m.y);
-    up2(a, t[i], t[i + 1]);
-    up2(b, t[i + 2], t[i + 3]);
-  }
-}
-
-template <int NC, bool MASKED>
-__device__ __forceinline__ float tile_excess(uint32_t tS, int nch, f32x2 c2, const float* nm,
-                                             const SlotSeen& seen, const RowMasks& mask) {
-  float ex = -INFINITY;
-  uint32_t s[2][16];
-  tm_ld16(tS, s[0]);
+  for (int g = 0; g < 2; ++g) {
+    const f32x2 m = *reinterpret_cast<const f32x2*>(nm + g * 8);
 #pragma unroll
-  for (int k = 0; k < NC / 16; ++k) {
-    if (k < nch) {
-      tm_wait_ld(s[k & 1]);
-      if (k + 1 < nch) tm_ld16(tS + (k + 1) * 16, s[(k + 1) & 1]);
-      float t[16];
-      scaled16(s[k & 1], c2, nm + k * 16, t);
-      masked16<MASKED>(t, seen, mask, k * 16);
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) ex = max3(ex, t[i], t[i + 1]);
-    }
-  }
-  return ex;
-}
-
-// P^T of the tile into shared memory (rows contiguous, 64 of them and 128
-// slots a block, 128-byte swizzle), l += P.
-template <class T, int NC, bool MASKED>
-__device__ __forceinline__ void tile_probs(uint32_t tS, int nch, f32x2 c2, const float* nm,
-                                           const SlotSeen& seen, const RowMasks& mask, char* P, int slot,
-                                           f32x2 (&l)[NC / 2]) {
-  uint32_t s[2][16];
-  tm_ld16(tS, s[0]);
-#pragma unroll
-  for (int k = 0; k < NC / 16; ++k) {
-    if (k < nch) {
-      tm_wait_ld(s[k & 1]);
-      if (k + 1 < nch) tm_ld16(tS + (k + 1) * 16, s[(k + 1) & 1]);
-      float t[16];
-      scaled16(s[k & 1], c2, nm + k * 16, t);
-      masked16<MASKED>(t, seen, mask, k * 16);
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float e0 = ex2_fast(t[i]), e1 = ex2_fast(t[i + 1]);
-        l[k * 8 + i / 2] = add2(l[k * 8 + i / 2], pk2(e0, e1));
-        w[i / 2] = T::pack(e0, e1);
-      }
-      char* row = P + (k / 4) * kHalf + slot * 128;
-      const int ch = (k & 3) * 2;
-      *reinterpret_cast<uint4*>(row + (((ch) ^ (slot & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (slot & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int q = 0; q < 4; ++q) {
+      const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
+      up2(fma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, m), t[g * 8 + q * 2],
+          t[g * 8 + q * 2 + 1]);
     }
   }
 }
 
-// Row maxima of the tile over the warp's 32 slots, into red[warp][row].
-template <int NC, bool MASKED>
-__device__ __forceinline__ void tile_maxima(uint32_t tS, int nch, float c, const SlotSeen& seen,
-                                            const RowMasks& mask, float* red, int lane) {
+// Scores that are not seen become `none` (-inf once scaled), in place.
+__device__ __noinline__ void mask_tile(const Args& a, int t, int ctx, int tot, uint32_t tS, int nch,
+                                       const uint64_t* anc, const uint8_t* node, float none) {
+  const RowMasks mask{anc, node};
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  int first, count;
+  tile_slots(a, t, first, count);
+  SlotSeen seen;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int r = row_slot(a, warp * 32 + (lane >> 2) + 8 * q, count);
+    const int slot = first + r;
+    seen.j[q] = r < 0 || slot >= tot ? kMaxNodes : slot < ctx ? -1 : slot - ctx;
+  }
 #pragma unroll 1
   for (int k = 0; k < nch; ++k) {
     uint32_t s[16];
-    tm_ld16(tS + k * 16, s);
+    tm_ld_frag(tS + k * 16, s);
     tm_wait_ld(s);
-    float t[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t[i] = __uint_as_float(s[i]) * c;
-    masked16<MASKED>(t, seen, mask, k * 16);
-    float keep = 0.f;
+    for (int g = 0; g < 2; ++g) {
+      const uint64_t m0 = mask[k * 16 + g * 8], m1 = mask[k * 16 + g * 8 + 1];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float m = warp_max(t[i]);
-      keep = lane == i ? m : keep;
+      for (int q = 0; q < 4; ++q) {
+        const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
+        if (!sees(seen.j[q], m0)) s[i] = __float_as_uint(none);
+        if (!sees(seen.j[q], m1)) s[i + 1] = __float_as_uint(none);
+      }
     }
-    if (lane < 16) red[k * 16 + lane] = keep;
+    tm_st_frag(tS + k * 16, s);
+  }
+  tm_wait_st();
+}
+
+// P^T of the tile into shared memory (rows contiguous, 64 of them and 128
+// slots a block, 128-byte swizzle), l += P; returns the largest excess over m.
+// prow: this lane's slot's line of the first block, which stmatrix takes as a
+// row of its 8 x 8 matrices.
+template <class T, int NC>
+__device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const float* nm, int x2, uint32_t prow,
+                                           int slot, f32x2 (&l)[NC / 8]) {
+  float ex[2] = {-INFINITY, -INFINITY};
+  uint32_t s[2][16];
+  tm_ld_frag(tS, s[0]);
+#pragma unroll
+  for (int k = 0; k < NC / 16; ++k) {
+    if (k < nch) {
+      tm_wait_ld(s[k & 1]);
+      if (k + 1 < nch) tm_ld_frag(tS + (k + 1) * 16, s[(k + 1) & 1]);
+      float t[16];
+      frag_scores(s[k & 1], c2, nm + k * 16 + x2, t);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float t0 = t[g * 8 + q * 2], t1 = t[g * 8 + q * 2 + 1];
+          ex[q & 1] = max3(ex[q & 1], t0, t1);
+          const float e0 = ex2_fast(t0), e1 = ex2_fast(t1);
+          l[k * 2 + g] = add2(l[k * 2 + g], pk2(e0, e1));
+          w[q] = T::pack(e0, e1);
+        }
+        const uint32_t at = prow + (k / 4) * kHalf + ((((k & 3) * 2 + g) ^ (slot & 7)) << 4);
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3])
+                     : "memory");
+      }
+    }
+  }
+  return fmaxf(ex[0], ex[1]);
+}
+
+// Over the eight lanes that hold the same rows.
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+
+// Row maxima of c s over the warp's 32 slots, into red.
+__device__ __noinline__ void tile_maxima(uint32_t tS, int nch, float c, float* red) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int k = 0; k < nch; ++k) {
+    uint32_t s[16];
+    tm_ld_frag(tS + k * 16, s);
+    tm_wait_ld(s);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float m[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = __uint_as_float(s[g * 4 + i]) * c, b = __uint_as_float(s[g * 4 + 2 + i]) * c;
+        const float d = __uint_as_float(s[8 + g * 4 + i]) * c, e = __uint_as_float(s[8 + g * 4 + 2 + i]) * c;
+        m[i] = lanes_max(fmaxf(fmaxf(a, b), fmaxf(d, e)));
+      }
+      if (lane < 4) *reinterpret_cast<float2*>(red + k * 16 + g * 8 + lane * 2) = make_float2(m[0], m[1]);
+    }
   }
 }
 
+// O of the warpgroup times the factors of its rows.
+__device__ __noinline__ void rescale(uint32_t tO, int nch, const float* fac) {
+#pragma unroll 1
+  for (int k = 0; k < nch; ++k) {
+    uint32_t o[16];
+    tm_ld16(tO + k * 16, o);
+    tm_wait_ld(o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[k * 16 + i]);
+    tm_st16(tO + k * 16, o);
+  }
+  tm_wait_st();
+}
+
+// Adds the NaN or infinite values that column d of node j holds, if any, to
+// the rows that see it (nf: the nodes that hold some).
+template <class T>
+__device__ __noinline__ void add_nonfinite(const Args& a, int b, int h, int ctx, unsigned long long nf, int d,
+                                           const uint64_t* anc, const uint8_t* node, float (&o)[8]) {
+  const RowMasks mask{anc, node};
+#pragma unroll 1
+  for (int j = 0; j < a.nodes.N; ++j) {
+    if (!((nf >> j) & 1)) continue;
+    int page, off;
+    if (!kv_slot(a.table + b * a.table_stride, a.width, a.pages, a.ps, static_cast<long long>(ctx) + j, page, off))
+      continue;
+    const unsigned short raw = *reinterpret_cast<const unsigned short*>(
+        a.vcache + 2 * (page * a.v_page + off * a.v_slot + h * a.v_head + d));
+    const float v = T::lo(raw);
+    if (fabsf(v) < INFINITY) continue;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if ((mask[i] >> j) & 1) o[i] += v;
+  }
+}
+
+// Rows of Q of a piece on their way into shared memory (by all 256 threads of
+// the warpgroups), their nodes and the nodes' masks.
+template <class T, int D>
+__device__ __noinline__ void gather_rows(const Args& a, Misc& sm, int b, int h, int rb, int n, char* Q, int qb) {
+  const int at = threadIdx.x - 128;
+  const int r0 = rb * a.rows_per_block;
+  const int rows = min(a.rows_per_block, a.R - r0);
+  constexpr int PER = D / 8;         // 16-byte vectors of a row
+  constexpr int STEP = 256 / PER;    // rows side by side
+  const int v = at % PER;
+  const char* base = a.q + 2 * (b * a.q_b + static_cast<long long>(h) * a.G * a.q_h + v * 8);
+  const uint32_t dst = sptr(Q) + (v / 8) * (a.cols * 128);
+#pragma unroll 1
+  for (int r = at / PER; r < a.cols; r += STEP) {
+    const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
+    const bool real = r < rows && i < n && !a.zero;
+    const char* src = real ? base + 2 * (i * a.q_n + g * a.q_h) : a.q;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((v ^ r) & 7) << 4)), "l"(src),
+                 "r"(real ? 16 : 0)
+                 : "memory");
+  }
+  if (at < 64) {
+    const int* parent = a.nodes.parent ? a.nodes.parent + static_cast<long long>(b) * a.nodes.N : nullptr;
+    uint64_t m = 0;
+    int depth;
+    bool broken = false;
+    if (at < n) node_way(parent, n, at, m, depth, broken);
+    if (broken) atomicOr(a.err, kErrBadTree);
+    sm.anc[qb][at] = m;
+    if (at < 2) sm.nf[qb][at] = 0;
+    if (at == 0) sm.anc[qb][kMaxNodes] = 0;
+  } else {
+#pragma unroll 1
+    for (int r = at - 64; r < a.cols; r += 192)
+      sm.node[qb * 64 + r] = static_cast<uint8_t>(r < rows ? (r0 + r) / a.G : kMaxNodes);
+  }
+}
+__device__ __forceinline__ void rows_ready(Misc& sm, int qb) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  fence_async();
+  bar_arrive(&sm.qfull[qb]);
+}
+
 template <class T, int D, int NC>
-__device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* P0, int pbytes,
-                                             int wg) {
+__device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* Q, int qbytes, char* P0,
+                                             int pbytes, int wg) {
+  constexpr float kSlack = T::kId == Bf16::kId ? 30.f : 8.f;
   char* P = P0 + wg * pbytes;
   Scratch& sc0 = *reinterpret_cast<Scratch*>(P0);
   Scratch& sc1 = *reinterpret_cast<Scratch*>(P0 + pbytes);
   Scratch& sc = wg == 0 ? sc0 : sc1;
-  constexpr int LANES = D;  // lanes of O^T that hold an output column (64: the rest repeat them)
-  const int wt = threadIdx.x - 128 - wg * 128;  // thread of the warpgroup = slot row = TMEM lane
+  const int wt = threadIdx.x - 128 - wg * 128;  // thread of the warpgroup = TMEM lane
   const int warp = wt >> 5, lane = wt & 31;
+  const int x2 = (lane & 3) * 2;  // first of the thread's rows in a group of 8
   const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t tS = tmem + lane_base + wg * kMaxJob;
   const uint32_t tO0 = tmem + lane_base + 2 * kMaxJob;
   const uint32_t tO = tO0 + wg * kMaxJob;
+  const uint32_t prow = sptr(P) + wt * 128;
   const int ncj = a.ncj, nch = ncj / 16;
   const f32x2 c2 = pk2(a.c, a.c);
   float* nm = sm.nm[wg];
-  float* fac = sc.fac;
   const int bar = 1 + wg;
-  const int colbase = a.two ? wg * ncj : 0;
+  const bool two = a.two;
+  const int colbase = two ? wg * ncj : 0;
+  const float none = a.c < 0.f ? INFINITY : -INFINITY;
   uint32_t ps = 0, ppv = 0;  // phases of sfull, pvdone
   int gj = 0, item_no = 0;
-  Pieces pc(a, sm);
-  const long long left0 = pc.left;
-  while (pc.next()) {
-    const int qb = item_no % a.qbufs;
-    bar_wait(&sm.qfull[qb], (item_no / a.qbufs) & 1, sm, a.err);
-    const RowMasks mask{sm.anc[qb], sm.node + qb * 64 + colbase};
+  Pieces pn;  // one piece ahead
+  pn.start(sm);
+  bool more = pn.next(a);
+  if (more) {
+    gather_rows<T, D>(a, sm, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, 0);
+    rows_ready(sm, 0);
+  }
+  while (more) {
+    const int b = pn.b, h = pn.h, t0 = pn.t0, end = pn.end, ctx = pn.ctx, tot = pn.tot;
+    const int tail = a.ragged ? 0 : pn.tail;
+    const bool direct = pn.direct();
+    const int r0 = pn.rb * a.rows_per_block + colbase;
+    const int rows = min(a.rows_per_block - colbase, a.R - r0);  // of this job's columns
+    const int qb = a.qbufs == 2 ? item_no & 1 : 0;
+    more = pn.next(a);
+    bool pending = false;
+    if (a.qbufs == 2 && more) {
+      gather_rows<T, D>(a, sm, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q + (qb ^ 1) * qbytes, qb ^ 1);
+      pending = true;
+    }
+    const uint64_t* anc = sm.anc[qb];
+    const uint8_t* node = sm.node + qb * 64 + colbase;
     if (wt < ncj) nm[wt] = -kNoScore;
-    f32x2 l[NC / 2];
+    f32x2 l[NC / 8];
 #pragma unroll
-    for (int i = 0; i < NC / 2; ++i) l[i] = 0ull;
-    named_sync(bar, 128);
+    for (int i = 0; i < NC / 8; ++i) l[i] = 0ull;
+    named_sync(3, 256);
     int jobs = 0;
-    for (int t = pc.t0; t < pc.t0 + pc.count; ++t) {
-      if (!a.two && ((gj + (t - pc.t0)) & 1) != wg) continue;
-      int first, count;
-      tile_slots(a, t, first, count);
-      const bool masked = a.ragged || first + count > pc.ctx;
-      SlotSeen seen;
-      seen.all = ~0ull;
-      seen.j = 0;
-      seen.any = 1;
-      if (masked) {
-        const int r = row_slot(a, wt, count);
-        const int slot = first + r;
-        if (r < 0 || slot >= pc.tot) {
-          seen.any = 0;
-        } else if (slot >= pc.ctx) {
-          seen.all = 0;
-          seen.j = slot - pc.ctx;
-        }
-      }
+    const int step = two ? 1 : 2;
+#pragma unroll 1
+    for (int t = t0 + (two ? 0 : (gj + wg) & 1); t < end; t += step) {
       bar_wait(&sm.sfull[wg], ps, sm, a.err);
       ps ^= 1;
-      tc_after();
-      const float ex = masked ? tile_excess<NC, true>(tS, nch, c2, nm, seen, mask)
-                              : tile_excess<NC, false>(tS, nch, c2, nm, seen, mask);
       if (jobs > 0) {  // the last tile's product: P may be written, O rescaled
         bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
         ppv ^= 1;
-        tc_after();
       }
-      if (named_or(bar, 128, ex > kSlack)) {
-        if (masked) tile_maxima<NC, true>(tS, nch, a.c, seen, mask, sc.red[warp], lane);
-        else tile_maxima<NC, false>(tS, nch, a.c, seen, mask, sc.red[warp], lane);
-        named_sync(bar, 128);
-        if (wt < ncj) {
-          const float mx = fmaxf(fmaxf(sc.red[0][wt], sc.red[1][wt]),
-                                 fmaxf(sc.red[2][wt], sc.red[3][wt]));
-          const float mo = -nm[wt];
-          const float mn = fmaxf(mo, mx);
-          fac[wt] = mn == mo ? 1.f : exp2f(mo - mn);
-          nm[wt] = -mn;
-        }
-        named_sync(bar, 128);
-#pragma unroll
-        for (int i = 0; i < NC / 2; ++i)
-          if (2 * i < ncj) l[i] = mul2(l[i], *reinterpret_cast<const f32x2*>(fac + 2 * i));
-        if (jobs > 0) {
+      tc_after();
+      if (t >= tail) mask_tile(a, t, ctx, tot, tS, nch, anc, node + x2, none);
+      bool raise = jobs == 0;
 #pragma unroll 1
-          for (int k = 0; k < nch; ++k) {
-            uint32_t o[16];
-            tm_ld16(tO + k * 16, o);
-            tm_wait_ld(o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[k * 16 + i]);
-            tm_st16(tO + k * 16, o);
+      while (true) {
+        if (raise) {
+          tile_maxima(tS, nch, a.c, sc.red[warp]);
+          named_sync(bar, 128);
+          if (wt < ncj) {
+            const float mx = fmaxf(fmaxf(sc.red[0][wt], sc.red[1][wt]), fmaxf(sc.red[2][wt], sc.red[3][wt]));
+            const float mo = -nm[wt];
+            const float mn = fmaxf(mo, mx);
+            sc.fac[wt] = mn == mo ? 1.f : exp2f(mo - mn);
+            nm[wt] = -mn;
           }
-          tm_wait_st();
+          named_sync(bar, 128);
+          if (jobs > 0) {
+#pragma unroll
+            for (int i = 0; i < NC / 8; ++i)
+              if (8 * i < ncj) l[i] = mul2(l[i], *reinterpret_cast<const f32x2*>(sc.fac + 8 * i + x2));
+            rescale(tO, nch, sc.fac);
+            named_sync(bar, 128);  // the factors lie where P goes
+          }
         }
-        named_sync(bar, 128);  // the factors lie where P goes
+        f32x2 old[NC / 8];
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) old[i] = l[i];
+        const float ex = tile_pass<T, NC>(tS, nch, c2, nm, x2, prow, wt, l);
+        if (!named_or(bar, 128, ex > kSlack)) break;
+        raise = true;
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i) l[i] = old[i];
       }
-      if (masked) tile_probs<T, NC, true>(tS, nch, c2, nm, seen, mask, P, wt, l);
-      else tile_probs<T, NC, false>(tS, nch, c2, nm, seen, mask, P, wt, l);
       tc_before();
       fence_async();
       bar_arrive(&sm.pfull[wg]);
       ++jobs;
+      if (pending) {
+        rows_ready(sm, qb ^ 1);
+        pending = false;
+      }
     }
 
     // ---- end of the piece: l over the slots, then O ----
+    if (pending) rows_ready(sm, qb ^ 1);
     if (jobs > 0) {
       bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
       ppv ^= 1;
       tc_after();
     }
-    // each lane ends with the sum of one column of every 32 (halving exchange)
 #pragma unroll
-    for (int k = 0; k < NC / 32; ++k) {
-      float v[32];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) up2(l[k * 16 + i], v[2 * i], v[2 * i + 1]);
-#pragma unroll
-      for (int h = 16; h > 0; h >>= 1) {
-        const bool up = lane & h;
-#pragma unroll
-        for (int i = 0; i < h; ++i) {
-          const float send = up ? v[i] : v[i + h];
-          const float mine = up ? v[i + h] : v[i];
-          v[i] = mine + __shfl_xor_sync(0xffffffffu, send, h);
-        }
+    for (int i = 0; i < NC / 8; ++i) {
+      if (8 * i < ncj) {
+        float u, v;
+        up2(l[i], u, v);
+        u = lanes_sum(u);
+        v = lanes_sum(v);
+        if (lane < 4) *reinterpret_cast<float2*>(sc.red[warp] + 8 * i + x2) = make_float2(u, v);
       }
-      if (k * 32 + lane < ncj) sc.red[warp][k * 32 + lane] = v[0];
     }
-    if (a.two) named_sync(bar, 128);
+    if (two) named_sync(bar, 128);
     else named_sync(3, 256);
-    const int h = pc.item / a.RB, r0 = pc.item % a.RB * a.rows_per_block + colbase;
-    const int rows = min(a.rows_per_block, a.R - r0 + colbase) - colbase;  // of this job's columns
-    const bool direct = pc.t0 == 0 && pc.count == pc.T;
-    const bool first_piece = left0 == pc.left + pc.count;
-    const long long pslot = (2ll * blockIdx.x + (first_piece ? 0 : 1)) * a.cols;
+    const int tiles = end - t0;
     // alternate tiles: which warpgroups took part
-    const bool used0 = a.two ? wg == 0 : pc.count > 1 || (gj & 1) == 0;
-    const bool used1 = a.two ? wg == 1 : pc.count > 1 || (gj & 1) == 1;
-    {
-      // weights of the warpgroups' O, into fac
-      const int cc = wt;  // column
-      if (cc < rows && cc < ncj && (a.two || wg == 0)) {
-        const float m0 = used0 ? -sm.nm[0][cc] : kNoScore, m1 = used1 ? -sm.nm[1][cc] : kNoScore;
-        const float M = fmaxf(m0, m1);
-        const float w0 = used0 ? (m0 == M ? 1.f : exp2f(m0 - M)) : 0.f;
-        const float w1 = used1 ? (m1 == M ? 1.f : exp2f(m1 - M)) : 0.f;
-        float L = 0.f;
-        if (used0)
-          L += w0 * ((sc0.red[0][cc] + sc0.red[1][cc]) + (sc0.red[2][cc] + sc0.red[3][cc]));
-        if (used1)
-          L += w1 * ((sc1.red[0][cc] + sc1.red[1][cc]) + (sc1.red[2][cc] + sc1.red[3][cc]));
-        {
-          const bool empty = mask[cc] == 0 || L == 0.f;
-          if (direct) {
-            const float inv = empty ? 0.f : 1.f / L;
-            (a.two ? sc : sc0).fac[cc] = w0 * inv + (a.two ? w1 * inv : 0.f);
-            if (!a.two) sc1.fac[cc] = w1 * inv;
-            if (a.lse)
-              a.lse[(static_cast<long long>(pc.b) * a.nodes.N + (r0 + cc) / a.G) * a.Hq + h * a.G +
-                    (r0 + cc) % a.G] =
-                  empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-          } else {
-            (a.two ? sc : sc0).fac[cc] = a.two ? w0 + w1 : w0;
-            if (!a.two) sc1.fac[cc] = w1;
-            a.part_ml[pslot + colbase + cc] = make_float2(M, L);
-          }
+    const bool used0 = two ? wg == 0 : tiles > 1 || (gj & 1) == 0;
+    const bool used1 = two ? wg == 1 : tiles > 1 || (gj & 1) == 1;
+    const long long pslot = (2ll * blockIdx.x + (item_no == 0 ? 0 : 1)) * a.cols + colbase;
+    const long long orow = static_cast<long long>(b) * a.nodes.N * a.Hq + h * a.G;
+    Scratch& so = two ? sc : sc0;
+    if (wt < ncj && (two || wg == 0)) {
+      // factors of the warpgroups' O, and where the rows go
+      const int cc = wt;
+      const float m0 = used0 ? -sm.nm[0][cc] : kNoScore, m1 = used1 ? -sm.nm[1][cc] : kNoScore;
+      const float M = fmaxf(m0, m1);
+      float w0 = used0 ? (m0 == M ? 1.f : exp2f(m0 - M)) : 0.f;
+      float w1 = used1 ? (m1 == M ? 1.f : exp2f(m1 - M)) : 0.f;
+      float L = 0.f;
+      if (used0) L += w0 * ((sc0.red[0][cc] + sc0.red[1][cc]) + (sc0.red[2][cc] + sc0.red[3][cc]));
+      if (used1) L += w1 * ((sc1.red[0][cc] + sc1.red[1][cc]) + (sc1.red[2][cc] + sc1.red[3][cc]));
+      int row = kNoRow;
+      if (cc < rows) {
+        const int i = (r0 + cc) / a.G;
+        row = i * a.Hq + (r0 + cc - i * a.G);
+        const bool absent = anc[node[cc]] == 0, empty = absent || L == 0.f;
+        if (direct) {
+          const float inv = empty ? 0.f : 1.f / L;
+          w0 *= inv;
+          w1 *= inv;
+          if (a.lse) a.lse[orow + row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          if (empty) row = ~row;
+        } else {
+          a.part_ml[pslot + cc] = make_float2(M, L);
         }
       }
+      so.row[cc] = row;
+      if (two) {
+        so.fac[cc] = w0 + w1;
+      } else {
+        sc0.fac[cc] = w0;
+        sc1.fac[cc] = w1;
+      }
     }
-    if (a.two) named_sync(bar, 128);
+    if (two) named_sync(bar, 128);
     else named_sync(3, 256);
     {
       // columns by eights: shared out over the warpgroups (alternate tiles)
-      // and, where O^T repeats itself, over the two copies
-      const int d = wt & (LANES - 1);
-      const int groups = (a.two ? 1 : 2) * (128 / LANES);
-      const int me = (a.two ? 0 : wg) * (128 / LANES) + wt / LANES;
-      const unsigned long long nf =
-          sm.nf[qb][0] | (static_cast<unsigned long long>(sm.nf[qb][1]) << 32);
-      char* obase = a.out + 2 * ((static_cast<long long>(pc.b) * a.nodes.N * a.Hq + h * a.G) * D);
-      for (int k = me; k < ncj / 8; k += groups) {
-        uint32_t v0[8], v1[8];
-        if (used0) tm_ld8(tO0 + k * 8, v0);
-        if (used1) tm_ld8(tO0 + kMaxJob + k * 8, v1);
-        if (used0) tm_wait_ld8(v0);
-        if (used1) tm_wait_ld8(v1);
-        float o[8];
+      // and, where O^T repeats itself (D = 64), over the two copies
+      const int d = wt & (D - 1);
+      const int groups = (two ? 1 : 2) * (128 / D);
+      const int me = (two ? 0 : wg) * (128 / D) + wt / D;
+      const unsigned long long nf = sm.nf[qb][0] | (static_cast<unsigned long long>(sm.nf[qb][1]) << 32);
+      char* obase = a.out + 2 * (orow * D + (d & ~1));
+      float* pbase = a.part_o + pslot * D + d;
+      const uint32_t src0 = two ? tO : tO0, src1 = tO0 + kMaxJob;
+      const bool use_a = two || used0, use_b = !two && used1;
+#pragma unroll 1
+      for (int k = me * 8; k < ncj; k += groups * 8) {
+        uint32_t u[8], v[8];
+        if (use_a) tm_ld8(src0 + k, u);
+        if (use_b) tm_ld8(src1 + k, v);
+        int row[8];
+        float f0[8], f1[8], o[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          *reinterpret_cast<int4*>(row + i) = *reinterpret_cast<const int4*>(so.row + k + i);
+          *reinterpret_cast<float4*>(f0 + i) = *reinterpret_cast<const float4*>(so.fac + k + i);
+          if (use_b) *reinterpret_cast<float4*>(f1 + i) = *reinterpret_cast<const float4*>(sc1.fac + k + i);
+        }
+        if (use_a) tm_wait_ld8(u);
+        if (use_b) tm_wait_ld8(v);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float x = 0.f;
-          if (a.two) {
-            x = fac[k * 8 + i] * __uint_as_float(wg == 0 ? v0[i] : v1[i]);
-          } else {
-            if (used0) x = sc0.fac[k * 8 + i] * __uint_as_float(v0[i]);
-            if (used1) x = fmaf(sc1.fac[k * 8 + i], __uint_as_float(v1[i]), x);
-          }
-          o[i] = x;
+          o[i] = use_a ? f0[i] * __uint_as_float(u[i]) : 0.f;
+          if (use_b) o[i] = fmaf(f1[i], __uint_as_float(v[i]), o[i]);
         }
-        if (nf) {  // nodes with NaN or infinite values, for the rows that see them
-          for (int j = 0; j < a.nodes.N; ++j) {
-            if (!((nf >> j) & 1)) continue;
-            int page, off;
-            if (!kv_slot(a.table + pc.b * a.table_stride, a.width, a.pages, a.ps,
-                         static_cast<long long>(pc.ctx) + j, page, off))
-              continue;
-            const unsigned short raw = *reinterpret_cast<const unsigned short*>(
-                a.vcache + 2 * (page * a.v_page + off * a.v_slot + h * a.v_head + d));
-            const float v = T::lo(raw);
-            if (fabsf(v) < INFINITY) continue;
+        if (nf) add_nonfinite<T>(a, b, h, ctx, nf, d, anc, node + k, o);
+        if (direct) {
+          // neighbouring lanes trade, so that each stores two entries of one row
+          const bool odd = d & 1;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if ((mask[k * 8 + i] >> j) & 1) o[i] += v;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const int c0 = k * 8 + i;
-          if (direct) {
-            // neighbouring lanes trade so that each stores two entries of one row
-            const bool z0 = mask[k * 8 + i] == 0, z1 = mask[k * 8 + i + 1] == 0;
-            const float x0 = z0 ? 0.f : o[i], x1 = z1 ? 0.f : o[i + 1];
-            const bool odd = d & 1;
+          for (int i = 0; i < 8; i += 2) {
+            const float x0 = row[i] >= 0 ? o[i] : 0.f, x1 = row[i + 1] >= 0 ? o[i + 1] : 0.f;
             const float other = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
             const uint32_t w = odd ? T::pack(other, x1) : T::pack(x0, other);
-            const int cr = c0 + (d & 1), r = r0 + cr;
-            if (cr < rows)
-              *reinterpret_cast<uint32_t*>(
-                  obase + 2 * (static_cast<long long>(r / a.G * a.Hq + r % a.G) * D + (d & ~1))) = w;
-          } else {
-            if (c0 < rows) a.part_o[(pslot + colbase + c0) * D + d] = o[i];
-            if (c0 + 1 < rows) a.part_o[(pslot + colbase + c0 + 1) * D + d] = o[i + 1];
+            int r = odd ? row[i + 1] : row[i];
+            if (r != kNoRow) {
+              r = r < 0 ? ~r : r;
+              *reinterpret_cast<uint32_t*>(obase + static_cast<long long>(r) * (2 * D)) = w;
+            }
           }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (row[i] != kNoRow) pbase[(k + i) * D] = o[i];
         }
       }
     }
-    bar_arrive(&sm.qempty[qb]);
     tc_before();
-    if (a.two) named_sync(bar, 128);
-    else named_sync(3, 256);
-    gj += pc.count;
+    named_sync(3, 256);  // Q, P and the masks may be written again
+    if (a.qbufs == 1 && more) {
+      gather_rows<T, D>(a, sm, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, 0);
+      rows_ready(sm, 0);
+    }
+    gj += tiles;
     ++item_no;
   }
 }
 
-// Q rows of a piece into shared memory, their masks and places.
-template <class T, int D>
-__device__ __forceinline__ void gather_rows(const Args& a, Misc& sm, const Pieces& pc, char* Q, int qb,
-                                            int at) {
-  const int h = pc.item / a.RB, rb = pc.item % a.RB;
-  const int r0 = rb * a.rows_per_block;
-  const int rows = min(a.rows_per_block, a.R - r0);
-  const int n = pc.tot - pc.ctx;
-  const int* parent = a.nodes.parent ? a.nodes.parent + static_cast<long long>(pc.b) * a.nodes.N : nullptr;
-  if (at < 2) sm.nf[qb][at] = 0;
-  bool any_broken = false;
-  for (int i = at; i <= kMaxNodes; i += 64) {
-    uint64_t m = 0;
-    int depth;
-    bool broken = false;
-    if (i < n) node_way(parent, n, i, m, depth, broken);
-    any_broken |= broken;
-    sm.anc[qb][i] = m;
-  }
-  for (int r = at; r < a.cols; r += 64)
-    sm.node[qb * 64 + r] = static_cast<uint8_t>(r < rows ? (r0 + r) / a.G : kMaxNodes);
-  if (any_broken) atomicOr(a.err, kErrBadTree);
-  named_sync(4, 64);
-  constexpr int PER = D / 8;
-  const int tasks = a.cols * PER;
-  const char* qb_ = a.q + 2 * (pc.b * a.q_b + static_cast<long long>(h) * a.G * a.q_h);
-  for (int k0 = at; k0 < tasks; k0 += 64 * 8) {
-    uint4 x[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int k = k0 + u * 64;
-      x[u] = make_uint4(0, 0, 0, 0);
-      if (k < tasks) {
-        const int r = k / PER, v = k % PER;
-        const int i = sm.node[qb * 64 + r];
-        if (sm.anc[qb][i]) {
-          const int g = r0 + r - i * a.G;
-          x[u] = *reinterpret_cast<const uint4*>(qb_ + 2 * (i * a.q_n + g * a.q_h + v * 8));
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int k = k0 + u * 64;
-      if (k < tasks) {
-        const int r = k / PER, v = k % PER;
-        *reinterpret_cast<uint4*>(Q + (v / 8) * (a.cols * 128) + r * 128 + (((v & 7) ^ (r & 7)) << 4)) = x[u];
-      }
-    }
-  }
-  fence_async();
-}
-
 // Clears V rows that are no slot of the sequence and the NaN or infinite
-// entries of its nodes (whose bits go to nf).
+// entries of its nodes (whose bits go to nf).  One warp.
 template <class T, int D>
-__device__ __forceinline__ void clean_tile(const Args& a, Misc& sm, const Pieces& pc, int t, char* V, int qb,
-                                           int at) {
+__device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx, int tot, char* V, int qb) {
   int first, count;
   tile_slots(a, t, first, count);
-  constexpr int PER = D / 8;
-  for (int k = at; k < kTile * PER; k += 64) {
-    const int r = k / PER, v = k % PER;
+#pragma unroll 1
+  for (int r = threadIdx.x & 31; r < kTile; r += 32) {
     const int rs = row_slot(a, r, count);
     const int slot = rs < 0 ? 0x7fffffff : first + rs;
-    if (slot < pc.ctx) continue;
-    uint4* p = reinterpret_cast<uint4*>(V + (v / 8) * kHalf + r * 128 + (((v & 7) ^ (r & 7)) << 4));
-    if (slot >= pc.tot) {
-      *p = make_uint4(0, 0, 0, 0);
+    if (slot < ctx) continue;
+    uint4* line = reinterpret_cast<uint4*>(V + r * 128);
+    if (slot >= tot) {
+#pragma unroll
+      for (int v = 0; v < D / 8; ++v) line[(v / 8) * (kHalf / 16) + ((v ^ r) & 7)] = make_uint4(0, 0, 0, 0);
       continue;
     }
-    uint4 x = *p;
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
     bool bad = false;
+#pragma unroll 4
+    for (int v = 0; v < D / 8; ++v) {
+      uint4* p = line + (v / 8) * (kHalf / 16) + ((v ^ r) & 7);
+      const uint4 x = *p;
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      bool here = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!(fabsf(T::lo(w[i])) < INFINITY)) { w[i] &= 0xffff0000u; bad = true; }
-      if (!(fabsf(T::hi(w[i])) < INFINITY)) { w[i] &= 0x0000ffffu; bad = true; }
+      for (int i = 0; i < 4; ++i) {
+        if (!(fabsf(T::lo(w[i])) < INFINITY)) { w[i] &= 0xffff0000u; here = true; }
+        if (!(fabsf(T::hi(w[i])) < INFINITY)) { w[i] &= 0x0000ffffu; here = true; }
+      }
+      if (here) *p = make_uint4(w[0], w[1], w[2], w[3]);
+      bad |= here;
     }
     if (bad) {
-      *p = make_uint4(w[0], w[1], w[2], w[3]);
-      const int j = slot - pc.ctx;
+      const int j = slot - ctx;
       atomicOr(&sm.nf[qb][j >> 5], 1u << (j & 31));
     }
   }
@@ -849,18 +944,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&sm.qfull[i], 64);
-      bar_init(&sm.qempty[i], 256);
+      bar_init(&sm.qfull[i], 256);
       bar_init(&sm.sfull[i], 1);
       bar_init(&sm.pfull[i], 128);
       bar_init(&sm.pvdone[i], 1);
     }
     bar_init(&sm.vready, 1);
-    bar_init(&sm.vclean, 64);
+    bar_init(&sm.vclean, 32);
     bar_init(&sm.done, 1);
     sm.abort = 0;
-    sm.b0 = 0;
-    sm.off0 = 0;
+    sm.b0 = sm.h0 = sm.rb0 = sm.t0 = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -888,6 +981,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int items = a.Hkv * a.RB;
     long long mine = 0;
     bool any_bad = false;
+#pragma unroll 1
     for (int b = f; b < e; ++b) {
       int ctx;
       bool bad;
@@ -905,25 +999,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (lane == 31) pre[warp] = inc;
     __syncthreads();
     long long before = 0, W = 0;
+#pragma unroll 1
     for (int i = 0; i < kAttnThreads / 32; ++i) {
       if (i < warp) before += pre[i];
       W += pre[i];
     }
     before += inc - mine;
     const long long lo = range_start(W, blockIdx.x, C), hi = range_start(W, blockIdx.x + 1, C);
-    if (tid == 0) {
-      sm.lo = lo;
-      sm.hi = hi;
-    }
+    if (tid == 0) sm.left = hi - lo;
     if (lo < hi && lo >= before && lo < before + mine) {
       long long p = before;
+#pragma unroll 1
       for (int b = f; b < e; ++b) {
         int ctx;
         bool bad;
-        const long long w = static_cast<long long>(tiles_of(a, seq_len(a, b, ctx, bad))) * items;
+        const int Tb = tiles_of(a, seq_len(a, b, ctx, bad));
+        const long long w = static_cast<long long>(Tb) * items;
         if (lo < p + w) {
+          const int item = static_cast<int>((lo - p) / Tb);
           sm.b0 = b;
-          sm.off0 = lo - p;
+          sm.h0 = item / a.RB;
+          sm.rb0 = item % a.RB;
+          sm.t0 = static_cast<int>(lo - p - static_cast<long long>(item) * Tb);
           break;
         }
         p += w;
@@ -931,6 +1028,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (blockIdx.x == 0) {  // for the joining kernel
       long long p = before;
+#pragma unroll 1
       for (int b = f; b < e; ++b) {
         int ctx;
         bool bad;
@@ -946,14 +1044,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   pdl_trigger();
   const uint32_t tmem = sm.tmem;
 
-  if (warp == 0) {
-    // ---- K and V tiles ----
-    Pieces pc(a, sm);
-    int slot = 0;
+  if (warp == 0 || warp == 2) {
+    // ---- K (warp 0) or V (warp 2) tiles ----
+    const CUtensorMap* map = warp == 0 ? &mapk : &mapv;
+    Pieces pc;
+    pc.start(sm);
+    int slot = warp == 0 ? -2 : -1;
     uint32_t phase = 0;
     bool bad_page = false;
-    while (pc.next()) {
-      const int h = pc.item / a.RB;
+#pragma unroll 1
+    while (pc.next(a)) {
       const int* trow = a.table + pc.b * a.table_stride;
       const int npages = (pc.tot + a.ps - 1) / a.ps;
       auto lookup = [&](int t) {
@@ -969,148 +1069,149 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         return id;
       };
       int id = lookup(pc.t0);
-      for (int t = pc.t0; t < pc.t0 + pc.count; ++t) {
+#pragma unroll 1
+      for (int t = pc.t0; t < pc.end; ++t) {
         const int cur = id;
-        if (t + 1 < pc.t0 + pc.count) id = lookup(t + 1);
+        if (t + 1 < pc.end) id = lookup(t + 1);
         const int boxes = a.ps <= kTile ? min(a.ppt, npages - t * a.ppt) : 1;
         const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
+        slot += 2;
+        if (slot >= a.ring) {
+          slot -= a.ring;
+          phase ^= 1;
+        }
+        const bool ok = bar_wait(&sm.empty[slot], phase ^ 1, sm, a.err) &&
+                        !*reinterpret_cast<volatile int*>(&sm.abort);
+        if (__all_sync(0xffffffffu, ok)) {
+          if (lane == 0) bar_expect(&sm.full[slot], boxes * a.box * 128 * HALVES);
+          __syncwarp();
+          if (lane < boxes) {
+            const uint32_t dst = sptr(ring) + slot * kSlotBytes + lane * a.box * 128;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const bool ok = bar_wait(&sm.empty[slot], phase ^ 1, sm, a.err) &&
-                          !*reinterpret_cast<volatile int*>(&sm.abort);
-          if (__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) bar_expect(&sm.full[slot], boxes * a.box * 128 * HALVES);
-            __syncwarp();
-            if (lane < boxes) {
-              const uint32_t dst = sptr(ring + slot * kSlotBytes) + lane * a.box * 128;
-#pragma unroll
-              for (int d = 0; d < HALVES; ++d)
-                tma_rows(dst + d * kHalf, kv ? &mapv : &mapk, d * 64, s0, h, cur, &sm.full[slot]);
-            }
+            for (int d = 0; d < HALVES; ++d) tma_rows(dst + d * kHalf, map, d * 64, s0, pc.h, cur, &sm.full[slot]);
           }
           __syncwarp();
-          if (++slot == a.ring) {
-            slot = 0;
-            phase ^= 1;
-          }
         }
       }
     }
     if (bad_page) atomicOr(a.err, kErrBadPage);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---- tensor cores ----
-      const uint32_t iqk = instr<T>(a.ncj, false, false), ipv = instr<T>(a.ncj, true, true);
-      const uint32_t ring_s = sptr(ring), q_s = sptr(Q), p_s = sptr(P);
-      Jobs jq(a, sm), jp(a, sm);
-      int kslot = -2, vslot = -1;        // ring slots of the current tiles
-      uint32_t kph = 0, vph = 0, ppf = 0, vcl = 0;
-      bool more_q = true, tail = false;
-      auto scores = [&]() {
-        bool nt;
-        if (!more_q || !jq.next(nt)) {
-          more_q = false;
-          return;
+    // ---- tensor cores (the warp runs as one; one lane issues) ----
+    const uint32_t iqk = instr<T>(a.ncj, false, false), ipv = instr<T>(a.ncj, true, true);
+    const uint64_t kd0 = operand(sptr(ring), 16, 1024), qd0 = operand(sptr(Q), 16, 1024);
+    const uint64_t vd0 = operand(sptr(ring), D == 128 ? kHalf : 0, 1024), pd0 = operand(sptr(P), kHalf, 1024);
+    Jobs jq, jp;
+    jq.start(sm);
+    jp.start(sm);
+    int kslot = -2, vslot = -1;  // ring slots of the current tiles
+    uint32_t kph = 0, vph = 0, ppf = 0, vcl = 0;
+    bool more_q = true, tail = false, held = false, nt = false;
+    int ahead = 0;  // scores issued beyond the products
+#pragma unroll 1
+    while (true) {
+#pragma unroll 1
+      while (ahead < 2) {
+        if (!held) {
+          if (!more_q || !next_job(a, jq, nt)) {
+            more_q = false;
+            break;
+          }
         }
+        // With one Q buffer the next piece's rows come after this piece's
+        // end, so its scores wait until no product of this piece is left.
+        held = a.qbufs == 1 && jq.in_item == 0 && ahead > 0;
+        if (held) break;
         if (nt) {
           kslot += 2;
           if (kslot >= a.ring) { kslot -= a.ring; kph ^= 1; }
         }
-        const int qb = jq.item_no % a.qbufs;
-        if (jq.in_item == 0) bar_wait(&sm.qfull[qb], (jq.item_no / a.qbufs) & 1, sm, a.err);
+        const int qb = a.qbufs == 2 ? jq.item_no & 1 : 0;
+        if (jq.in_item == 0)
+          bar_wait(&sm.qfull[qb], (a.qbufs == 2 ? jq.item_no >> 1 : jq.item_no) & 1, sm, a.err);
         if (nt) bar_wait(&sm.full[kslot], kph, sm, a.err);
         tc_after();
-        const int w = jq.wg();
-        const uint32_t ka = ring_s + kslot * kSlotBytes;
-        const uint32_t qa = q_s + qb * qbytes + (a.two ? w * a.ncj * 128 : 0);
+        const int w = jq.wg(a.two);
+        const uint64_t kd = kd0 + kslot * (kSlotBytes / 16);
+        const uint64_t qd = qd0 + (qb * qbytes + (a.two ? w * a.ncj * 128 : 0)) / 16;
+        const uint32_t qhalf = a.cols * 8;
         const uint32_t d = tmem + w * kMaxJob;
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (k & 3) * 32;
-          tc_mma(d, operand(ka + (k / 4) * kHalf + o, 16, 1024),
-                 operand(qa + (k / 4) * a.cols * 128 + o, 16, 1024), iqk, k > 0);
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma(d, kd + (k / 4) * (kHalf / 16) + (k & 3) * 2, qd + (k / 4) * qhalf + (k & 3) * 2, iqk, k > 0);
+          if (!a.two || w == 1) tc_commit(&sm.empty[kslot]);
+          tc_commit(&sm.sfull[w]);
         }
-        if (jq.last_of_tile()) tc_commit(&sm.empty[kslot]);
-        tc_commit(&sm.sfull[w]);
-      };
-      scores();
-      scores();
-      bool nt;
-      while (jp.next(nt)) {
-        const int w = jp.wg();
-        if (nt) {
-          vslot += 2;
-          if (vslot >= a.ring) { vslot -= a.ring; vph ^= 1; }
-          bar_wait(&sm.full[vslot], vph, sm, a.err);
-          tail = jp.pc.tail(jp.t);
-          if (tail) bar_arrive(&sm.vready);
-        }
-        bar_wait(&sm.pfull[w], (ppf >> w) & 1, sm, a.err);
-        if (nt && tail) {
-          bar_wait(&sm.vclean, vcl, sm, a.err);
-          vcl ^= 1;
-        }
-        ppf ^= 1u << w;
-        tc_after();
-        const uint32_t va = ring_s + vslot * kSlotBytes;
-        const uint32_t pa = p_s + w * pbytes;
-        const uint32_t d = tmem + 2 * kMaxJob + w * kMaxJob;
-        const bool fresh = jp.in_item < 2;  // the warpgroup's first tile of the piece
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k)
-          tc_mma(d, operand(va + k * 2048, D == 128 ? kHalf : 0, 1024), operand(pa + k * 2048, kHalf, 1024), ipv,
-                 !(fresh && k == 0));
-        if (jp.last_of_tile()) tc_commit(&sm.empty[vslot]);
-        tc_commit(&sm.pvdone[w]);
-        scores();
+        __syncwarp();
+        ++ahead;
       }
-      tc_commit(&sm.done);
-      bar_wait(&sm.done, 0, sm, a.err);
+      bool ntv;
+      if (!next_job(a, jp, ntv)) break;
+      const int w = jp.wg(a.two);
+      if (ntv) {
+        vslot += 2;
+        if (vslot >= a.ring) { vslot -= a.ring; vph ^= 1; }
+        bar_wait(&sm.full[vslot], vph, sm, a.err);
+        tail = jp.t >= jp.pc.tail;
+        if (tail && lane == 0) bar_arrive(&sm.vready);
+      }
+      bar_wait(&sm.pfull[w], (ppf >> w) & 1, sm, a.err);
+      ppf ^= 1u << w;
+      if (ntv && tail) {
+        bar_wait(&sm.vclean, vcl, sm, a.err);
+        vcl ^= 1;
+      }
+      tc_after();
+      const uint64_t vd = vd0 + vslot * (kSlotBytes / 16);
+      const uint64_t pd = pd0 + w * (pbytes / 16);
+      const uint32_t d = tmem + 2 * kMaxJob + w * kMaxJob;
+      const bool fresh = jp.in_item < 2;  // the warpgroup's first tile of the piece
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * 128, pd + k * 128, ipv, !(fresh && k == 0));
+        if (!a.two || w == 1) tc_commit(&sm.empty[vslot]);
+        tc_commit(&sm.pvdone[w]);
+      }
+      __syncwarp();
+      --ahead;
     }
+    if (elect_one()) tc_commit(&sm.done);
     __syncwarp();
-  } else if (warp < 4) {
-    // ---- rows of Q; tiles with drafted nodes ----
-    const int at = tid - 64;
-    Pieces pq(a, sm), pv(a, sm);
-    int qi = 0, vi = 0, tiles = 0;
+    bar_wait(&sm.done, 0, sm, a.err);
+  } else if (warp == 3) {
+    // ---- tiles with drafted nodes ----
+    Pieces pv;
+    pv.start(sm);
+    int vi = 0, tiles = 0;
     uint32_t vrd = 0;
-    auto rows = [&]() {
-      if (!pq.next()) return;
-      const int qb = qi % a.qbufs;
-      if (qi >= a.qbufs) bar_wait(&sm.qempty[qb], ((qi / a.qbufs) & 1) ^ 1, sm, a.err);
-      gather_rows<T, D>(a, sm, pq, Q + qb * qbytes, qb, at);
-      bar_arrive(&sm.qfull[qb]);
-      ++qi;
-    };
-    rows();
-    while (pv.next()) {
-      if (a.qbufs == 2) rows();
-      for (int t = pv.t0; t < pv.t0 + pv.count; ++t) {
-        if (!pv.tail(t)) continue;
+#pragma unroll 1
+    while (pv.next(a)) {
+#pragma unroll 1
+      for (int t = max(pv.t0, pv.tail); t < pv.end; ++t) {
         const int s = (2 * (tiles + t - pv.t0) + 1) % a.ring;  // the V tile's slot
         bar_wait(&sm.vready, vrd, sm, a.err);
         vrd ^= 1;
-        clean_tile<T, D>(a, sm, pv, t, ring + s * kSlotBytes, vi % a.qbufs, at);
+        clean_tile<T, D>(a, sm, t, pv.ctx, pv.tot, ring + s * kSlotBytes, a.qbufs == 2 ? vi & 1 : 0);
         bar_arrive(&sm.vclean);
       }
-      tiles += pv.count;
+      tiles += pv.end - pv.t0;
       ++vi;
-      if (a.qbufs == 1) rows();
     }
     // sequences without tiles: their rows are empty
+#pragma unroll 1
     for (int b = blockIdx.x; b < B; b += C) {
       int ctx;
       bool bad;
       if (seq_len(a, b, ctx, bad) != 0) continue;
       const long long n = static_cast<long long>(a.nodes.N) * a.Hq;
       uint4* o = reinterpret_cast<uint4*>(a.out + 2 * (b * n * D));
-      for (long long i = at; i < n * D / 8; i += 64) o[i] = make_uint4(0, 0, 0, 0);
+      for (long long i = lane; i < n * D / 8; i += 32) o[i] = make_uint4(0, 0, 0, 0);
       if (a.lse)
-        for (long long i = at; i < n; i += 64) a.lse[b * n + i] = -INFINITY;
+        for (long long i = lane; i < n; i += 32) a.lse[b * n + i] = -INFINITY;
     }
   } else {
     const int wg = (warp - 4) >> 2;
-    softmax_role<T, D, NC>(a, sm, tmem, P, pbytes, wg);
+    softmax_role<T, D, NC>(a, sm, tmem, Q, qbytes, P, pbytes, wg);
   }
   tc_before();
   __syncthreads();
@@ -1318,7 +1419,8 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   const Shape sh = shape_of(a.R);
   a.RB = sh.RB; a.rows_per_block = sh.rows; a.two = sh.two; a.ncj = sh.ncj; a.cols = sh.cols;
   a.q = p.q; a.q_b = p.q_b; a.q_n = p.q_n; a.q_h = p.q_h;
-  a.c = p.scale * 1.4426950408889634f;
+  a.zero = p.scale == 0.f;
+  a.c = a.zero ? 1.f : p.scale * 1.4426950408889634f;
   a.out = p.out; a.lse = p.lse;
   a.vcache = p.kv.v; a.v_page = p.kv.v_page; a.v_slot = p.kv.v_slot; a.v_head = p.kv.v_head;
   a.err = p.err;

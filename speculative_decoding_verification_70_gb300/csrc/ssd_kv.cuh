@@ -65,6 +65,9 @@ __host__ __device__ inline bool node_way(const int* parent, int n, int j, uint64
   }
   uint64_t m = 1ull << j;
   int i = j, d = 0;
+#ifdef __CUDA_ARCH__
+#pragma unroll 1
+#endif
   while (i > 0) {
     const int p = parent[i];
     if (p < 0 || p >= i) {

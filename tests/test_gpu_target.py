@@ -64,6 +64,12 @@ ATTN = [
     (1, 8, 8, 1, 128, 16, 6000, BF, "random", False, "slot"),
     (1, 64, 5, 1, 128, 16, 1500, BF, "random", False, "slot"),
     (1, 64, 64, 1, 64, 16, 130, BF, "random", False, "slot"),
+    # several (sequence, head)s and tiles a CTA: 32, 64, 104, 168 and 256 rows
+    (60, 2, 64, 4, 64, 16, tuple(100 + (i * 131) % 1500 for i in range(60)), FP, "chain", False, "slot"),
+    (40, 8, 32, 4, 128, 16, tuple((i * 131) % 1500 for i in range(40)), BF, "random", True, "slot"),
+    (40, 13, 32, 4, 128, 32, tuple((i * 131) % 1500 for i in range(40)), BF, "random", False, "head"),
+    (24, 21, 32, 4, 128, 16, tuple((i * 231) % 2500 for i in range(24)), BF, "random", False, "slot"),
+    (10, 64, 16, 4, 64, 16, tuple((i * 431) % 3500 for i in range(10)), FP, "random", True, "slot"),
 ]
 
 
