@@ -18,17 +18,16 @@
 // the workspace, and attn_combine_kernel joins them in range order.
 //
 // Warps of a CTA:
-//   0, 2   copy K and V tiles, page by page, by TMA into a ring of slots
+//   0, 2   copy K and V tiles, page by page, by TMA into rings of slots
 //          (128-byte swizzle; a page id out of range is a coordinate out of
 //          bounds, which TMA fills with zeros)
-//   1      issues tcgen05.mma: S^T (K, Q from shared memory) two jobs ahead
-//          of O^T (V^T read transposed from the same row-major tile, P^T from
-//          shared memory)
-//   3      clears, in tiles that hold drafted nodes, what must not be
-//          multiplied: V rows behind the sequence's end, and NaN or infinite
-//          entries of nodes (added at the end for the rows that see them)
-//   4..11  two warpgroups for the softmax, which also fetch the rows of Q and
-//          write the results.  Up to 128 rows: the warpgroups take alternate
+//   1, 3   issue tcgen05.mma: S^T (K, Q from shared memory), and O^T (V^T read
+//          transposed from the same row-major tile, P^T from shared memory)
+//   4..11  two warpgroups for the softmax, which also fetch the rows of Q,
+//          clear what must not be multiplied in tiles that hold drafted nodes
+//          (V rows behind the sequence's end; NaN or infinite entries of
+//          nodes, which are added at the end for the rows that see them) and
+//          write the results.  Up to 64 rows: the warpgroups take alternate
 //          tiles and keep their own m, l, O; more: the same tiles, half of
 //          the rows each.
 //
@@ -49,13 +48,21 @@ namespace {
 constexpr int kAttnThreads = 384;
 constexpr int kTile = 128;           // slots of a tile (rows of the ring's tiles)
 constexpr int kHalf = kTile * 128;   // bytes of a tile's 64-column half
-constexpr int kMaxRing = 8;
+constexpr int kMaxRing = 4;           // slots of each ring
 constexpr int kMaxRows = 256;        // rows of a row block
+constexpr int kAlternate = 64;       // most rows whose tiles the warpgroups take in turn
 constexpr int kMaxJob = 128;         // rows of a job (one warpgroup's columns)
 constexpr int kMaxCtas = 160;
 constexpr int kNoRow = 0x7fffffff;   // a column without a row (rows of zeros: ~row)
 constexpr float kNoScore = -1e30f;   // m of a row that has seen nothing
 constexpr int kSmemMax = 227 * 1024;
+
+// A CTA's range of tiles, for the joining kernel.
+struct Range {
+  long long lo;          // first tile
+  int b, h, rb, t0, T;   // its item, its place there, the item's tiles
+  int used;              // 0: an empty range
+};
 
 struct Args {
   NodesView nodes;
@@ -66,7 +73,7 @@ struct Args {
   int RB, rows_per_block;   // row blocks of a key/value head
   int two;                  // the warpgroups split the rows
   int ncj, cols;            // columns of a job; of Q (ncj or 2 ncj)
-  int qbufs, ring;
+  int nk, nv;               // slots of the K and V rings
   int box, ppt, tk, tpp;    // rows of a TMA box, pages a tile, slots a tile, tiles a page
   int ragged;               // tiles have rows that are no slot
   int cover;                // rows of a tile that TMA writes
@@ -80,18 +87,18 @@ struct Args {
   long long v_page, v_slot, v_head;
   float* part_o;            // [2 ctas][cols][D]
   float2* part_ml;          // [2 ctas][cols]
-  long long* sched;         // [B + 1] tiles before each sequence
+  struct Range* ranges;     // [ctas]
   int* err;
 };
 
 // Shared memory behind the ring, Q and P (256 rows leave 3 KB for it).
 struct alignas(16) Misc {
-  uint64_t full[kMaxRing], empty[kMaxRing];
-  uint64_t qfull[2], sfull[2], pfull[2], pvdone[2], vready, vclean, done;
+  uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
+  uint64_t qfull[2], sfull[2], pfull[2], pvdone[2], done;
   uint64_t anc[2][kMaxNodes + 1];   // nodes' ancestors (0: absent); the last: no row
   long long left;
   alignas(16) float nm[2][kMaxJob]; // -m
-  uint8_t node[kMaxRows];           // rows' nodes; two buffers of 64 or one of 256
+  uint8_t node[2][kMaxRows];        // rows' nodes
   unsigned nf[2][2];                // nodes with NaN or infinite values
   int b0, h0, rb0, t0;              // first piece
   unsigned tmem;
@@ -333,9 +340,6 @@ __device__ __noinline__ SeqTiles seq_tiles(const Args& a, int b) {
   return q;
 }
 
-// First tile of CTA c's range.
-__device__ __forceinline__ long long range_start(long long W, int c, int C) { return W * c / C; }
-
 // The pieces of a CTA's range, one (sequence, head, row block) after another.
 // Only the first may start behind tile 0.
 struct Pieces {
@@ -391,41 +395,6 @@ struct Pieces {
     return true;
   }
 };
-
-// Jobs of a CTA in order: a tile for one warpgroup's columns.
-struct Jobs {
-  Pieces pc;
-  int t, half, in_item, item_no, gj;
-  bool started;
-  __device__ void start(const Misc& sm) {
-    pc.start(sm);
-    half = in_item = 0;
-    item_no = gj = -1;
-    started = false;
-  }
-  __device__ int wg(bool two) const { return two ? half : gj & 1; }
-};
-// Advances; new_tile: whether the job is the first of its tile.
-__device__ __forceinline__ bool next_job(const Args& a, Jobs& j, bool& new_tile) {
-  new_tile = true;
-  ++j.gj;
-  if (j.started) {
-    ++j.in_item;
-    if (a.two && j.half == 0) {
-      j.half = 1;
-      new_tile = false;
-      return true;
-    }
-    j.half = 0;
-    if (++j.t < j.pc.end) return true;
-  }
-  j.started = true;
-  if (!j.pc.next(a)) return false;
-  j.t = j.pc.t0;
-  j.in_item = 0;
-  ++j.item_no;
-  return true;
-}
 
 // ---------------------------------------------------------------------------
 // softmax: one tile for one warpgroup
@@ -609,41 +578,53 @@ __device__ __noinline__ void add_nonfinite(const Args& a, int b, int h, int ctx,
   }
 }
 
-// Rows of Q of a piece on their way into shared memory (by all 256 threads of
-// the warpgroups), their nodes and the nodes' masks.
-template <class T, int D>
-__device__ __noinline__ void gather_rows(const Args& a, Misc& sm, int b, int h, int rb, int n, char* Q, int qb) {
+// The nodes of a piece's rows and the nodes' masks (by all 256 threads of the
+// warpgroups).
+__device__ __noinline__ void row_tables(const Args& a, Misc& sm, int b, int rb, int n, int tb) {
   const int at = threadIdx.x - 128;
   const int r0 = rb * a.rows_per_block;
   const int rows = min(a.rows_per_block, a.R - r0);
+  if (at < a.cols) sm.node[tb][at] = static_cast<uint8_t>(at < rows ? (r0 + at) / a.G : kMaxNodes);
+  if (at >= 192) {
+    const int j = at - 192;
+    const int* parent = a.nodes.parent ? a.nodes.parent + static_cast<long long>(b) * a.nodes.N : nullptr;
+    uint64_t m = 0;
+    int depth;
+    bool broken = false;
+    if (j < n) node_way(parent, n, j, m, depth, broken);
+    if (broken) atomicOr(a.err, kErrBadTree);
+    sm.anc[tb][j] = m;
+    if (j < 2) sm.nf[tb][j] = 0;
+    if (j == 0) sm.anc[tb][kMaxNodes] = 0;
+  }
+}
+
+// Columns c0 .. c1 - 1 of Q of a piece on their way into shared memory, by
+// `threads` threads, of which this is number `at`.
+template <int D>
+__device__ __noinline__ void fetch_rows(const Args& a, int b, int h, int rb, int n, char* Q, int c0, int c1, int at,
+                                        int threads) {
+  const int r0 = rb * a.rows_per_block;
+  const int rows = min(a.rows_per_block, a.R - r0);
   constexpr int PER = D / 8;         // 16-byte vectors of a row
-  constexpr int STEP = 256 / PER;    // rows side by side
+  const int step = threads / PER;    // rows side by side
   const int v = at % PER;
   const char* base = a.q + 2 * (b * a.q_b + static_cast<long long>(h) * a.G * a.q_h + v * 8);
   const uint32_t dst = sptr(Q) + (v / 8) * (a.cols * 128);
+  int r = c0 + at / PER;
+  int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
 #pragma unroll 1
-  for (int r = at / PER; r < a.cols; r += STEP) {
-    const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
+  for (; r < c1; r += step) {
     const bool real = r < rows && i < n && !a.zero;
     const char* src = real ? base + 2 * (i * a.q_n + g * a.q_h) : a.q;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + r * 128 + (((v ^ r) & 7) << 4)), "l"(src),
                  "r"(real ? 16 : 0)
                  : "memory");
-  }
-  if (at < 64) {
-    const int* parent = a.nodes.parent ? a.nodes.parent + static_cast<long long>(b) * a.nodes.N : nullptr;
-    uint64_t m = 0;
-    int depth;
-    bool broken = false;
-    if (at < n) node_way(parent, n, at, m, depth, broken);
-    if (broken) atomicOr(a.err, kErrBadTree);
-    sm.anc[qb][at] = m;
-    if (at < 2) sm.nf[qb][at] = 0;
-    if (at == 0) sm.anc[qb][kMaxNodes] = 0;
-  } else {
-#pragma unroll 1
-    for (int r = at - 64; r < a.cols; r += 192)
-      sm.node[qb * 64 + r] = static_cast<uint8_t>(r < rows ? (r0 + r) / a.G : kMaxNodes);
+    g += step;
+    while (g >= a.G) {
+      g -= a.G;
+      ++i;
+    }
   }
 }
 __device__ __forceinline__ void rows_ready(Misc& sm, int qb) {
@@ -652,9 +633,45 @@ __device__ __forceinline__ void rows_ready(Misc& sm, int qb) {
   bar_arrive(&sm.qfull[qb]);
 }
 
+// Clears V rows that are no slot of the sequence and the NaN or infinite
+// entries of its nodes (whose bits go to nf).  One warpgroup, a row a thread.
+template <class T, int D>
+__device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx, int tot, char* V, int tb, int r) {
+  int first, count;
+  tile_slots(a, t, first, count);
+  const int rs = row_slot(a, r, count);
+  const int slot = rs < 0 ? 0x7fffffff : first + rs;
+  if (slot < ctx) return;
+  uint4* line = reinterpret_cast<uint4*>(V + r * 128);
+  if (slot >= tot) {
+#pragma unroll
+    for (int v = 0; v < D / 8; ++v) line[(v / 8) * (kHalf / 16) + ((v ^ r) & 7)] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  bool bad = false;
+#pragma unroll 4
+  for (int v = 0; v < D / 8; ++v) {
+    uint4* p = line + (v / 8) * (kHalf / 16) + ((v ^ r) & 7);
+    const uint4 x = *p;
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    bool here = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!(fabsf(T::lo(w[i])) < INFINITY)) { w[i] &= 0xffff0000u; here = true; }
+      if (!(fabsf(T::hi(w[i])) < INFINITY)) { w[i] &= 0x0000ffffu; here = true; }
+    }
+    if (here) *p = make_uint4(w[0], w[1], w[2], w[3]);
+    bad |= here;
+  }
+  if (bad) {
+    const int j = slot - ctx;
+    atomicOr(&sm.nf[tb][j >> 5], 1u << (j & 31));
+  }
+}
+
 template <class T, int D, int NC>
-__device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* Q, int qbytes, char* P0,
-                                             int pbytes, int wg) {
+__device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* Q, int qbytes, char* V,
+                                             char* P0, int pbytes, int wg) {
   constexpr float kSlack = T::kId == Bf16::kId ? 30.f : 8.f;
   char* P = P0 + wg * pbytes;
   Scratch& sc0 = *reinterpret_cast<Scratch*>(P0);
@@ -676,12 +693,15 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
   const int colbase = two ? wg * ncj : 0;
   const float none = a.c < 0.f ? INFINITY : -INFINITY;
   uint32_t ps = 0, ppv = 0;  // phases of sfull, pvdone
-  int gj = 0, item_no = 0;
-  Pieces pn;  // one piece ahead
+  int item_no = 0;
+  const int at = threadIdx.x - 128;
+  int g0 = 0;  // tiles before this piece
+  Pieces pn;   // one piece ahead
   pn.start(sm);
   bool more = pn.next(a);
   if (more) {
-    gather_rows<T, D>(a, sm, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, 0);
+    fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, 0, a.cols, at, 256);
+    row_tables(a, sm, pn.b, pn.rb, pn.tot - pn.ctx, 0);
     rows_ready(sm, 0);
   }
   while (more) {
@@ -690,15 +710,15 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     const bool direct = pn.direct();
     const int r0 = pn.rb * a.rows_per_block + colbase;
     const int rows = min(a.rows_per_block - colbase, a.R - r0);  // of this job's columns
-    const int qb = a.qbufs == 2 ? item_no & 1 : 0;
+    const int tb = item_no & 1;                                  // tables
     more = pn.next(a);
-    bool pending = false;
-    if (a.qbufs == 2 && more) {
-      gather_rows<T, D>(a, sm, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q + (qb ^ 1) * qbytes, qb ^ 1);
-      pending = true;
-    }
-    const uint64_t* anc = sm.anc[qb];
-    const uint8_t* node = sm.node + qb * 64 + colbase;
+    if (more) row_tables(a, sm, pn.b, pn.rb, pn.tot - pn.ctx, tb ^ 1);
+    // the next rows of Q: into the other buffer now, or (one buffer) into
+    // this warpgroup's half once its last scores are there
+    bool pending = more && !two;
+    if (pending) fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q + (tb ^ 1) * qbytes, 0, a.cols, at, 256);
+    const uint64_t* anc = sm.anc[tb];
+    const uint8_t* node = sm.node[tb] + colbase;
     if (wt < ncj) nm[wt] = -kNoScore;
     f32x2 l[NC / 8];
 #pragma unroll
@@ -707,7 +727,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     int jobs = 0;
     const int step = two ? 1 : 2;
 #pragma unroll 1
-    for (int t = t0 + (two ? 0 : (gj + wg) & 1); t < end; t += step) {
+    for (int t = t0 + (two ? 0 : (g0 + wg) & 1); t < end; t += step) {
       bar_wait(&sm.sfull[wg], ps, sm, a.err);
       ps ^= 1;
       if (jobs > 0) {  // the last tile's product: P may be written, O rescaled
@@ -747,18 +767,24 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 #pragma unroll
         for (int i = 0; i < NC / 8; ++i) l[i] = old[i];
       }
+      if (t >= tail && (!two || wg == 0)) {
+        const int g = g0 + t - t0;
+        bar_wait(&sm.vfull[g % a.nv], (g / a.nv) & 1, sm, a.err);
+        clean_tile<T, D>(a, sm, t, ctx, tot, V + (g % a.nv) * (kTile * D * 2), tb, wt);
+      }
       tc_before();
       fence_async();
       bar_arrive(&sm.pfull[wg]);
       ++jobs;
       if (pending) {
-        rows_ready(sm, qb ^ 1);
+        rows_ready(sm, tb ^ 1);
         pending = false;
       }
     }
 
     // ---- end of the piece: l over the slots, then O ----
-    if (pending) rows_ready(sm, qb ^ 1);
+    if (pending) rows_ready(sm, tb ^ 1);
+    if (two && more) fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, colbase, colbase + ncj, wt, 128);
     if (jobs > 0) {
       bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
       ppv ^= 1;
@@ -778,8 +804,8 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     else named_sync(3, 256);
     const int tiles = end - t0;
     // alternate tiles: which warpgroups took part
-    const bool used0 = two ? wg == 0 : tiles > 1 || (gj & 1) == 0;
-    const bool used1 = two ? wg == 1 : tiles > 1 || (gj & 1) == 1;
+    const bool used0 = two ? wg == 0 : tiles > 1 || (g0 & 1) == 0;
+    const bool used1 = two ? wg == 1 : tiles > 1 || (g0 & 1) == 1;
     const long long pslot = (2ll * blockIdx.x + (item_no == 0 ? 0 : 1)) * a.cols + colbase;
     const long long orow = static_cast<long long>(b) * a.nodes.N * a.Hq + h * a.G;
     Scratch& so = two ? sc : sc0;
@@ -824,7 +850,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       const int d = wt & (D - 1);
       const int groups = (two ? 1 : 2) * (128 / D);
       const int me = (two ? 0 : wg) * (128 / D) + wt / D;
-      const unsigned long long nf = sm.nf[qb][0] | (static_cast<unsigned long long>(sm.nf[qb][1]) << 32);
+      const unsigned long long nf = sm.nf[tb][0] | (static_cast<unsigned long long>(sm.nf[tb][1]) << 32);
       char* obase = a.out + 2 * (orow * D + (d & ~1));
       float* pbase = a.part_o + pslot * D + d;
       const uint32_t src0 = two ? tO : tO0, src1 = tO0 + kMaxJob;
@@ -872,54 +898,11 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       }
     }
     tc_before();
-    named_sync(3, 256);  // Q, P and the masks may be written again
-    if (a.qbufs == 1 && more) {
-      gather_rows<T, D>(a, sm, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, 0);
-      rows_ready(sm, 0);
-    }
-    gj += tiles;
+    named_sync(3, 256);  // P and the tables may be written again
+    if (two && more) rows_ready(sm, 0);
+    g0 += tiles;
     ++item_no;
   }
-}
-
-// Clears V rows that are no slot of the sequence and the NaN or infinite
-// entries of its nodes (whose bits go to nf).  One warp.
-template <class T, int D>
-__device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx, int tot, char* V, int qb) {
-  int first, count;
-  tile_slots(a, t, first, count);
-#pragma unroll 1
-  for (int r = threadIdx.x & 31; r < kTile; r += 32) {
-    const int rs = row_slot(a, r, count);
-    const int slot = rs < 0 ? 0x7fffffff : first + rs;
-    if (slot < ctx) continue;
-    uint4* line = reinterpret_cast<uint4*>(V + r * 128);
-    if (slot >= tot) {
-#pragma unroll
-      for (int v = 0; v < D / 8; ++v) line[(v / 8) * (kHalf / 16) + ((v ^ r) & 7)] = make_uint4(0, 0, 0, 0);
-      continue;
-    }
-    bool bad = false;
-#pragma unroll 4
-    for (int v = 0; v < D / 8; ++v) {
-      uint4* p = line + (v / 8) * (kHalf / 16) + ((v ^ r) & 7);
-      const uint4 x = *p;
-      uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      bool here = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!(fabsf(T::lo(w[i])) < INFINITY)) { w[i] &= 0xffff0000u; here = true; }
-        if (!(fabsf(T::hi(w[i])) < INFINITY)) { w[i] &= 0x0000ffffu; here = true; }
-      }
-      if (here) *p = make_uint4(w[0], w[1], w[2], w[3]);
-      bad |= here;
-    }
-    if (bad) {
-      const int j = slot - ctx;
-      atomicOr(&sm.nf[qb][j >> 5], 1u << (j & 31));
-    }
-  }
-  fence_async();
 }
 
 template <class T, int D, int NC>
@@ -930,9 +913,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr int HALVES = D / 64;
   constexpr int kSlotBytes = HALVES * kHalf;
   char* ring = base;
-  char* Q = ring + a.ring * kSlotBytes;
+  char* ringv = ring + a.nk * kSlotBytes;
+  char* Q = ringv + a.nv * kSlotBytes;
   const int qbytes = a.cols * D * 2;
-  char* P = Q + a.qbufs * qbytes;
+  char* P = Q + (a.two ? 1 : 2) * qbytes;
   const int pbytes = ((a.ncj + 63) / 64) * kHalf;
   Misc& sm = *reinterpret_cast<Misc*>(P + 2 * pbytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -940,8 +924,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
-      bar_init(&sm.full[i], 1);
-      bar_init(&sm.empty[i], 1);
+      bar_init(&sm.kfull[i], 1);
+      bar_init(&sm.kempty[i], 1);
+      bar_init(&sm.vfull[i], 1);
+      bar_init(&sm.vempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.qfull[i], 256);
@@ -949,9 +935,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bar_init(&sm.pfull[i], 128);
       bar_init(&sm.pvdone[i], 1);
     }
-    bar_init(&sm.vready, 1);
-    bar_init(&sm.vclean, 32);
-    bar_init(&sm.done, 1);
+    bar_init(&sm.done, 2);
     sm.abort = 0;
     sm.b0 = sm.h0 = sm.rb0 = sm.t0 = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -968,7 +952,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // rows of the ring that no copy writes are zeros (they meet P = 0, and
   // must not be NaN)
   if (a.cover < kTile) {
-    for (int i = tid; i < a.ring * kSlotBytes / 16; i += kAttnThreads)
+    for (int i = tid; i < (a.nk + a.nv) * kSlotBytes / 16; i += kAttnThreads)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
     fence_async();
   }
@@ -1005,37 +989,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       W += pre[i];
     }
     before += inc - mine;
-    const long long lo = range_start(W, blockIdx.x, C), hi = range_start(W, blockIdx.x + 1, C);
-    if (tid == 0) sm.left = hi - lo;
-    if (lo < hi && lo >= before && lo < before + mine) {
+    // (at most W ranges, so that none of those is empty)
+    const long long Cr = min(static_cast<long long>(C), W), me = blockIdx.x;
+    const bool used = me < Cr;
+    const long long lo = used ? W * me / Cr : 0, hi = used ? W * (me + 1) / Cr : 0;
+    if (tid == 0) {
+      sm.left = hi - lo;
+      if (!used) a.ranges[me].used = 0;
+    }
+    if (used && lo >= before && lo < before + mine) {
       long long p = before;
 #pragma unroll 1
       for (int b = f; b < e; ++b) {
-        int ctx;
-        bool bad;
-        const int Tb = tiles_of(a, seq_len(a, b, ctx, bad));
+        const int Tb = seq_tiles(a, b).T;
         const long long w = static_cast<long long>(Tb) * items;
         if (lo < p + w) {
+          Range r;
           const int item = static_cast<int>((lo - p) / Tb);
-          sm.b0 = b;
-          sm.h0 = item / a.RB;
-          sm.rb0 = item % a.RB;
-          sm.t0 = static_cast<int>(lo - p - static_cast<long long>(item) * Tb);
+          r.lo = lo;
+          r.b = sm.b0 = b;
+          r.h = sm.h0 = item / a.RB;
+          r.rb = sm.rb0 = item - r.h * a.RB;
+          r.t0 = sm.t0 = static_cast<int>(lo - p - static_cast<long long>(item) * Tb);
+          r.T = Tb;
+          r.used = 1;
+          a.ranges[me] = r;
           break;
         }
         p += w;
       }
-    }
-    if (blockIdx.x == 0) {  // for the joining kernel
-      long long p = before;
-#pragma unroll 1
-      for (int b = f; b < e; ++b) {
-        int ctx;
-        bool bad;
-        a.sched[b] = p;
-        p += static_cast<long long>(tiles_of(a, seq_len(a, b, ctx, bad))) * items;
-      }
-      if (tid == 0) a.sched[B] = W;
     }
   }
   tc_before();
@@ -1049,7 +1031,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const CUtensorMap* map = warp == 0 ? &mapk : &mapv;
     Pieces pc;
     pc.start(sm);
-    int slot = warp == 0 ? -2 : -1;
+    uint64_t* full = warp == 0 ? sm.kfull : sm.vfull;
+    uint64_t* empty = warp == 0 ? sm.kempty : sm.vempty;
+    const uint32_t ring0 = sptr(warp == 0 ? ring : ringv);
+    const int slots = warp == 0 ? a.nk : a.nv;
+    int slot = -1;
     uint32_t phase = 0;
     bool bad_page = false;
 #pragma unroll 1
@@ -1075,20 +1061,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (t + 1 < pc.end) id = lookup(t + 1);
         const int boxes = a.ps <= kTile ? min(a.ppt, npages - t * a.ppt) : 1;
         const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
-        slot += 2;
-        if (slot >= a.ring) {
-          slot -= a.ring;
+        if (++slot == slots) {
+          slot = 0;
           phase ^= 1;
         }
-        const bool ok = bar_wait(&sm.empty[slot], phase ^ 1, sm, a.err) &&
+        const bool ok = bar_wait(&empty[slot], phase ^ 1, sm, a.err) &&
                         !*reinterpret_cast<volatile int*>(&sm.abort);
         if (__all_sync(0xffffffffu, ok)) {
-          if (lane == 0) bar_expect(&sm.full[slot], boxes * a.box * 128 * HALVES);
+          if (lane == 0) bar_expect(&full[slot], boxes * a.box * 128 * HALVES);
           __syncwarp();
           if (lane < boxes) {
-            const uint32_t dst = sptr(ring) + slot * kSlotBytes + lane * a.box * 128;
+            const uint32_t dst = ring0 + slot * kSlotBytes + lane * a.box * 128;
 #pragma unroll
-            for (int d = 0; d < HALVES; ++d) tma_rows(dst + d * kHalf, map, d * 64, s0, pc.h, cur, &sm.full[slot]);
+            for (int d = 0; d < HALVES; ++d) tma_rows(dst + d * kHalf, map, d * 64, s0, pc.h, cur, &full[slot]);
           }
           __syncwarp();
         }
@@ -1096,107 +1081,91 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (bad_page) atomicOr(a.err, kErrBadPage);
   } else if (warp == 1) {
-    // ---- tensor cores (the warp runs as one; one lane issues) ----
-    const uint32_t iqk = instr<T>(a.ncj, false, false), ipv = instr<T>(a.ncj, true, true);
+    // ---- scores (the warp runs as one; one lane issues) ----
+    const uint32_t iqk = instr<T>(a.ncj, false, false);
     const uint64_t kd0 = operand(sptr(ring), 16, 1024), qd0 = operand(sptr(Q), 16, 1024);
-    const uint64_t vd0 = operand(sptr(ring), D == 128 ? kHalf : 0, 1024), pd0 = operand(sptr(P), kHalf, 1024);
-    Jobs jq, jp;
-    jq.start(sm);
-    jp.start(sm);
-    int kslot = -2, vslot = -1;  // ring slots of the current tiles
-    uint32_t kph = 0, vph = 0, ppf = 0, vcl = 0;
-    bool more_q = true, tail = false, held = false, nt = false;
-    int ahead = 0;  // scores issued beyond the products
+    const uint32_t qhalf = a.cols * 8;
+    const int halves = a.two ? 2 : 1;
+    Pieces pc;
+    pc.start(sm);
+    int slot = -1, item = 0, g = 0;
+    uint32_t phase = 0;
 #pragma unroll 1
-    while (true) {
+    while (pc.next(a)) {
+      const int qb = a.two ? 0 : item & 1;
+      bar_wait(&sm.qfull[qb], (a.two ? item : item >> 1) & 1, sm, a.err);
+      const uint64_t qd = qd0 + qb * (qbytes / 16);
+      ++item;
 #pragma unroll 1
-      while (ahead < 2) {
-        if (!held) {
-          if (!more_q || !next_job(a, jq, nt)) {
-            more_q = false;
-            break;
+      for (int t = pc.t0; t < pc.end; ++t, ++g) {
+        if (++slot == a.nk) {
+          slot = 0;
+          phase ^= 1;
+        }
+        bar_wait(&sm.kfull[slot], phase, sm, a.err);
+        const uint64_t kd = kd0 + slot * (kSlotBytes / 16);
+#pragma unroll 1
+        for (int hf = 0; hf < halves; ++hf) {
+          // S of this warpgroup is free once it has made its P of the last one
+          const int w = a.two ? hf : g & 1, n = a.two ? g : g >> 1;
+          if (n > 0) bar_wait(&sm.pfull[w], (n - 1) & 1, sm, a.err);
+          tc_after();
+          const uint64_t q = qd + hf * a.ncj * 8;
+          const uint32_t d = tmem + w * kMaxJob;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc_mma(d, kd + (k / 4) * (kHalf / 16) + (k & 3) * 2, q + (k / 4) * qhalf + (k & 3) * 2, iqk, k > 0);
+            tc_commit(&sm.sfull[w]);
+            if (hf == halves - 1) tc_commit(&sm.kempty[slot]);
           }
+          __syncwarp();
         }
-        // With one Q buffer the next piece's rows come after this piece's
-        // end, so its scores wait until no product of this piece is left.
-        held = a.qbufs == 1 && jq.in_item == 0 && ahead > 0;
-        if (held) break;
-        if (nt) {
-          kslot += 2;
-          if (kslot >= a.ring) { kslot -= a.ring; kph ^= 1; }
-        }
-        const int qb = a.qbufs == 2 ? jq.item_no & 1 : 0;
-        if (jq.in_item == 0)
-          bar_wait(&sm.qfull[qb], (a.qbufs == 2 ? jq.item_no >> 1 : jq.item_no) & 1, sm, a.err);
-        if (nt) bar_wait(&sm.full[kslot], kph, sm, a.err);
-        tc_after();
-        const int w = jq.wg(a.two);
-        const uint64_t kd = kd0 + kslot * (kSlotBytes / 16);
-        const uint64_t qd = qd0 + (qb * qbytes + (a.two ? w * a.ncj * 128 : 0)) / 16;
-        const uint32_t qhalf = a.cols * 8;
-        const uint32_t d = tmem + w * kMaxJob;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma(d, kd + (k / 4) * (kHalf / 16) + (k & 3) * 2, qd + (k / 4) * qhalf + (k & 3) * 2, iqk, k > 0);
-          if (!a.two || w == 1) tc_commit(&sm.empty[kslot]);
-          tc_commit(&sm.sfull[w]);
-        }
-        __syncwarp();
-        ++ahead;
       }
-      bool ntv;
-      if (!next_job(a, jp, ntv)) break;
-      const int w = jp.wg(a.two);
-      if (ntv) {
-        vslot += 2;
-        if (vslot >= a.ring) { vslot -= a.ring; vph ^= 1; }
-        bar_wait(&sm.full[vslot], vph, sm, a.err);
-        tail = jp.t >= jp.pc.tail;
-        if (tail && lane == 0) bar_arrive(&sm.vready);
-      }
-      bar_wait(&sm.pfull[w], (ppf >> w) & 1, sm, a.err);
-      ppf ^= 1u << w;
-      if (ntv && tail) {
-        bar_wait(&sm.vclean, vcl, sm, a.err);
-        vcl ^= 1;
-      }
-      tc_after();
-      const uint64_t vd = vd0 + vslot * (kSlotBytes / 16);
-      const uint64_t pd = pd0 + w * (pbytes / 16);
-      const uint32_t d = tmem + 2 * kMaxJob + w * kMaxJob;
-      const bool fresh = jp.in_item < 2;  // the warpgroup's first tile of the piece
-      if (elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * 128, pd + k * 128, ipv, !(fresh && k == 0));
-        if (!a.two || w == 1) tc_commit(&sm.empty[vslot]);
-        tc_commit(&sm.pvdone[w]);
-      }
-      __syncwarp();
-      --ahead;
     }
     if (elect_one()) tc_commit(&sm.done);
     __syncwarp();
     bar_wait(&sm.done, 0, sm, a.err);
   } else if (warp == 3) {
-    // ---- tiles with drafted nodes ----
-    Pieces pv;
-    pv.start(sm);
-    int vi = 0, tiles = 0;
-    uint32_t vrd = 0;
+    // ---- values ----
+    const uint32_t ipv = instr<T>(a.ncj, true, true);
+    const uint64_t vd0 = operand(sptr(ringv), D == 128 ? kHalf : 0, 1024), pd0 = operand(sptr(P), kHalf, 1024);
+    const int halves = a.two ? 2 : 1;
+    Pieces pc;
+    pc.start(sm);
+    int slot = -1, g = 0;
+    uint32_t phase = 0;
 #pragma unroll 1
-    while (pv.next(a)) {
+    while (pc.next(a)) {
 #pragma unroll 1
-      for (int t = max(pv.t0, pv.tail); t < pv.end; ++t) {
-        const int s = (2 * (tiles + t - pv.t0) + 1) % a.ring;  // the V tile's slot
-        bar_wait(&sm.vready, vrd, sm, a.err);
-        vrd ^= 1;
-        clean_tile<T, D>(a, sm, t, pv.ctx, pv.tot, ring + s * kSlotBytes, a.qbufs == 2 ? vi & 1 : 0);
-        bar_arrive(&sm.vclean);
+      for (int t = pc.t0; t < pc.end; ++t, ++g) {
+        if (++slot == a.nv) {
+          slot = 0;
+          phase ^= 1;
+        }
+        bar_wait(&sm.vfull[slot], phase, sm, a.err);
+        const uint64_t vd = vd0 + slot * (kSlotBytes / 16);
+        const bool add = t - pc.t0 >= (a.two ? 1 : 2);  // not the warpgroup's first tile of the piece
+#pragma unroll 1
+        for (int hf = 0; hf < halves; ++hf) {
+          const int w = a.two ? hf : g & 1, n = a.two ? g : g >> 1;
+          bar_wait(&sm.pfull[w], n & 1, sm, a.err);
+          tc_after();
+          const uint64_t pd = pd0 + w * (pbytes / 16);
+          const uint32_t d = tmem + 2 * kMaxJob + w * kMaxJob;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * 128, pd + k * 128, ipv, add || k > 0);
+            tc_commit(&sm.pvdone[w]);
+            if (hf == halves - 1) tc_commit(&sm.vempty[slot]);
+          }
+          __syncwarp();
+        }
       }
-      tiles += pv.end - pv.t0;
-      ++vi;
     }
+    if (elect_one()) tc_commit(&sm.done);
+    __syncwarp();
+    bar_wait(&sm.done, 0, sm, a.err);
     // sequences without tiles: their rows are empty
 #pragma unroll 1
     for (int b = blockIdx.x; b < B; b += C) {
@@ -1211,7 +1180,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else {
     const int wg = (warp - 4) >> 2;
-    softmax_role<T, D, NC>(a, sm, tmem, Q, qbytes, P, pbytes, wg);
+    softmax_role<T, D, NC>(a, sm, tmem, Q, qbytes, ringv, P, pbytes, wg);
   }
   tc_before();
   __syncthreads();
@@ -1230,74 +1199,76 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---------------------------------------------------------------------------
 // Joins the parts of the (sequence, head, row block)s that range borders cut:
 //     M = max m_i,  w_i = 2^(m_i - M),  o = sum w_i O_i / sum w_i l_i
-// in range order.  blockIdx.x: a border between two ranges; the first border
-// inside a cut item does its work, a warp per row.
+// in range order.  blockIdx.x: a range that starts inside an item; the first
+// such range of an item does its work, a warp per row.  The loads of all parts
+// are independent: two round trips and the parts' own.
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
 
 template <class T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __grid_constant__ Args a, int C) {
   constexpr int E = D / 32;
-  pdl_wait();
-  const int B = a.nodes.B;
-  const long long W = a.sched[B];
+  const int lane = threadIdx.x & 31;
   const int c = blockIdx.x + 1;
-  const long long x = range_start(W, c, C);
-  if (x >= W) return;
-  int lo = 0, hi = B;  // last b with sched[b] <= x
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.sched[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  const int b = lo;
-  const int items = a.Hkv * a.RB;
-  const int Tn = static_cast<int>((a.sched[b + 1] - a.sched[b]) / items);
-  const long long first = a.sched[b];
-  const int item = static_cast<int>((x - first) / Tn);
-  const long long s = first + static_cast<long long>(item) * Tn, e = s + Tn;
-  if (x == s || range_start(W, c - 1, C) > s) return;  // not cut here, or an earlier border's item
-  const int h = item / a.RB, rb = item % a.RB;
-  const int r0 = rb * a.rows_per_block, rows = min(a.rows_per_block, a.R - r0);
-  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  pdl_wait();
+  const Range me = a.ranges[c], before = a.ranges[c - 1];
+  if (!me.used || me.t0 == 0) return;
+  const long long s = me.lo - me.t0, e = s + me.T;
+  if (before.lo > s) return;  // an earlier range's item
+  const int r0 = me.rb * a.rows_per_block, rows = min(a.rows_per_block, a.R - r0);
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   if (r >= rows) return;
-  const int i = (r0 + r) / a.G, g = (r0 + r) % a.G;
+  const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
   int ctx;
   bool bad, broken;
-  const int tot = seq_len(a, b, ctx, bad);
+  const int tot = seq_len(a, me.b, ctx, bad);
   uint64_t mask;
   int depth;
-  const bool there = node_way(a.nodes.parent ? a.nodes.parent + static_cast<long long>(b) * a.nodes.N : nullptr,
-                              tot - ctx, i, mask, depth, broken);
-  auto part = [&](int k) { return (2ll * k + (k == c - 1 && range_start(W, k, C) < s ? 1 : 0)) * a.cols + r; };
-  float M = kNoScore;
-  int last = c - 1;
-  for (int k = c - 1; k < C && range_start(W, k, C) < e; ++k) {
-    last = k;
-    if (range_start(W, k + 1, C) == range_start(W, k, C)) continue;
-    M = fmaxf(M, a.part_ml[part(k)].x);
-  }
-  float L = 0.f, o[E];
+  const bool there =
+      node_way(a.nodes.parent ? a.nodes.parent + static_cast<long long>(me.b) * a.nodes.N : nullptr, tot - ctx, i,
+               mask, depth, broken);
+  // part k is that of range c - 1 + k; only the first can be its CTA's last
+  const long long first = (2ll * (c - 1) + (before.lo < s ? 1 : 0)) * a.cols + r;
+  const long long others = 2ll * (c - 1) * a.cols + r;
+  float M = kNoScore, L = 0.f, o[E];
 #pragma unroll
   for (int q = 0; q < E; ++q) o[q] = 0.f;
-#pragma unroll 2
-  for (int k = c - 1; k <= last; ++k) {
-    if (range_start(W, k + 1, C) == range_start(W, k, C)) continue;
-    const long long p = part(k);
-    const float2 ml = a.part_ml[p];
-    const float w = ml.x == M ? 1.f : exp2f(ml.x - M);
-    L = fmaf(w, ml.y, L);
-    const float* src = a.part_o + p * D + lane * E;
+#pragma unroll 1
+  for (int k0 = 0;; k0 += 32) {
+    const int k = k0 + lane, at = c - 1 + k;
+    const bool in = at < C && (k == 0 || (a.ranges[at].used && a.ranges[at].lo < e));
+    const int n = __popc(__ballot_sync(0xffffffffu, in));
+    if (n == 0) break;
+    const float2 ml = in ? a.part_ml[k == 0 ? first : others + 2ll * k * a.cols] : make_float2(kNoScore, 0.f);
+    float m = ml.x;
 #pragma unroll
-    for (int q = 0; q < E; q += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(src + q);
-      o[q] = fmaf(w, v.x, o[q]);
-      o[q + 1] = fmaf(w, v.y, o[q + 1]);
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float Mn = fmaxf(M, m);
+    const float w = in ? (ml.x == Mn ? 1.f : exp2f(ml.x - Mn)) : 0.f;
+    float l = w * ml.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+    const float old = M == Mn ? 1.f : exp2f(M - Mn);
+    L = L * old + l;
+    M = Mn;
+#pragma unroll
+    for (int q = 0; q < E; ++q) o[q] *= old;
+#pragma unroll 4
+    for (int t = 0; t < n; ++t) {
+      const float wt = __shfl_sync(0xffffffffu, w, t);
+      const float* src = a.part_o + (k0 + t == 0 ? first : others + 2ll * (k0 + t) * a.cols) * D + lane * E;
+#pragma unroll
+      for (int q = 0; q < E; q += 2) {
+        const float2 v = *reinterpret_cast<const float2*>(src + q);
+        o[q] = fmaf(wt, v.x, o[q]);
+        o[q + 1] = fmaf(wt, v.y, o[q + 1]);
+      }
     }
+    if (n < 32) break;
   }
   const bool empty = !there || L == 0.f;
   const float inv = empty ? 0.f : 1.f / L;
-  const long long row = (static_cast<long long>(b) * a.nodes.N + i) * a.Hq + h * a.G + g;
+  const long long row = (static_cast<long long>(me.b) * a.nodes.N + i) * a.Hq + me.h * a.G + g;
   char* out = a.out + 2 * (row * D + lane * E);
 #pragma unroll
   for (int q = 0; q < E; q += 2)
@@ -1349,7 +1320,7 @@ Shape shape_of(int R) {
   Shape s;
   s.RB = (R + kMaxRows - 1) / kMaxRows;
   s.rows = (R + s.RB - 1) / s.RB;
-  s.two = s.rows > kMaxJob;
+  s.two = s.rows > kAlternate;
   const int per = s.two ? (s.rows + 1) / 2 : s.rows;
   s.ncj = (per + 15) / 16 * 16;
   s.cols = s.two ? 2 * s.ncj : s.ncj;
@@ -1357,13 +1328,13 @@ Shape shape_of(int R) {
 }
 
 struct Layout {
-  size_t sched, ml, o, total;
+  size_t ranges, ml, o, total;
 };
-Layout layout_of(int B, int R, int D) {
+Layout layout_of(int R, int D) {
   const Shape s = shape_of(R);
   Layout L;
-  L.sched = 256;
-  L.ml = (L.sched + 8 * (static_cast<size_t>(B) + 1) + 255) / 256 * 256;
+  L.ranges = 256;
+  L.ml = (L.ranges + sizeof(Range) * kMaxCtas + 255) / 256 * 256;
   L.o = (L.ml + 8ull * 2 * kMaxCtas * s.cols + 255) / 256 * 256;
   L.total = L.o + 4ull * 2 * kMaxCtas * s.cols * D;
   return L;
@@ -1407,7 +1378,7 @@ cudaError_t launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a
 
 }  // namespace
 
-size_t tree_attention_bytes(int B, int N, int G, int D) { return layout_of(B, N * G, D).total; }
+size_t tree_attention_bytes(int N, int G, int D) { return layout_of(N * G, D).total; }
 
 cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStream_t s) {
   Args a;
@@ -1424,9 +1395,9 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   a.out = p.out; a.lse = p.lse;
   a.vcache = p.kv.v; a.v_page = p.kv.v_page; a.v_slot = p.kv.v_slot; a.v_head = p.kv.v_head;
   a.err = p.err;
-  const Layout L = layout_of(p.nodes.B, a.R, D);
+  const Layout L = layout_of(a.R, D);
   char* ws = reinterpret_cast<char*>(p.err);
-  a.sched = reinterpret_cast<long long*>(ws + L.sched);
+  a.ranges = reinterpret_cast<Range*>(ws + L.ranges);
   a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
   a.part_o = reinterpret_cast<float*>(ws + L.o);
   // tiles: whole pages up to 128 slots; boxes of a multiple of 8 rows (the
@@ -1449,12 +1420,13 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   }
   const int slot = D * 2 * kTile;
   const size_t qb = static_cast<size_t>(a.cols) * D * 2, pb = ((a.ncj + 63) / 64) * static_cast<size_t>(kHalf);
-  a.qbufs = a.cols <= 64 ? 2 : 1;
-  const size_t fixed = a.qbufs * qb + 2 * pb + sizeof(Misc);
-  int ring = static_cast<int>((kSmemMax - fixed) / slot);
-  a.ring = ring < kMaxRing ? ring : kMaxRing;
-  if (a.ring < 3) return cudaErrorInvalidConfiguration;
-  const size_t smem = fixed + static_cast<size_t>(a.ring) * slot;
+  const size_t fixed = (a.two ? 1 : 2) * qb + 2 * pb + sizeof(Misc);
+  int slots = static_cast<int>((kSmemMax - fixed) / slot);
+  if (slots > 2 * kMaxRing) slots = 2 * kMaxRing;
+  if (slots < 3) return cudaErrorInvalidConfiguration;
+  a.nk = slots / 2;
+  a.nv = slots - a.nk;
+  const size_t smem = fixed + static_cast<size_t>(slots) * slot;
   CUtensorMap mk, mv;
   if (!encode(&mk, p.kv.k, dtype, D, a.ps, a.Hkv, a.pages, p.kv.k_slot, p.kv.k_head, p.kv.k_page, a.box) ||
       !encode(&mv, p.kv.v, dtype, D, a.ps, a.Hkv, a.pages, p.kv.v_slot, p.kv.v_head, p.kv.v_page, a.box))

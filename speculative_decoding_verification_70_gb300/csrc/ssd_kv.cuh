@@ -196,7 +196,7 @@ constexpr int kErrBadTemperature = 0x1, kErrBadLogits = 0x2, kErrBadToken = 0x4,
 cudaError_t launch_kv_append(const AppendParams& p, int dtype, int D, bool vec, cudaStream_t s);
 cudaError_t launch_kv_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStream_t s);
-size_t tree_attention_bytes(int B, int N, int G, int D);
+size_t tree_attention_bytes(int N, int G, int D);
 cudaError_t launch_logprobs(const LogprobParams& p, int dtype, bool vec, cudaStream_t s);
 
 }  // namespace ssd

@@ -123,7 +123,7 @@ size_t ssd_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) 
   if (B < 1 || N < 1 || N > SSD_MAX_TREE_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 ||
       Hq / Hkv > 64 || (D != 64 && D != 128))
     return 0;
-  return tree_attention_bytes(B, N, Hq / Hkv, D);
+  return tree_attention_bytes(N, Hq / Hkv, D);
 }
 
 ssd_status ssd_tree_attention(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, int Hq,
