@@ -100,7 +100,8 @@ struct alignas(16) Misc {
   alignas(16) float nm[2][kMaxJob]; // -m
   uint8_t node[2][kMaxRows];        // rows' nodes
   unsigned nf[2][2];                // nodes with NaN or infinite values
-  int b0, h0, rb0, t0;              // first piece
+  int b0, h0, rb0, t0;              // first piece, its sequence's
+  int T0, ctx0, tot0, tail0;        // tiles and lengths
   unsigned tmem;
   int abort;
 };
@@ -244,12 +245,6 @@ __device__ __forceinline__ void tm_ld16(uint32_t addr, uint32_t (&r)[16]) {
       : SSD_TM16(r)
       : "r"(addr));
 }
-__device__ __forceinline__ void tm_ld8(uint32_t addr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(addr));
-}
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -263,12 +258,7 @@ __device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-__device__ __forceinline__ void tm_wait_ld8(uint32_t (&r)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7])::"memory");
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 // 32 lanes x 16 columns as fragments: register [half][4 g + 2 r + i] of lane
 // 4 y + x is lane 16 half + 8 r + y, column 8 g + 2 x + i.
@@ -354,6 +344,10 @@ struct Pieces {
     h = sm.h0;
     rb = sm.rb0;
     t0 = sm.t0;
+    T = sm.T0;
+    ctx = sm.ctx0;
+    tot = sm.tot0;
+    tail = sm.tail0;
     fresh = true;
   }
   __device__ __forceinline__ bool direct() const { return t0 == 0 && end == T; }
@@ -365,7 +359,7 @@ struct Pieces {
     tail = q.tail;
   }
   __device__ __forceinline__ bool next(const Args& a) {
-    bool reload = fresh;
+    bool reload = false;
     if (!fresh) {
       left -= end - t0;
       t0 = 0;
@@ -404,12 +398,6 @@ struct Pieces {
 // its warp's 32 (lane 4 y + x), so a row's sum needs one register of four
 // threads' columns and m one load per two rows.
 
-// What each of the four slots means: < 0: seen by every row, kMaxNodes: by
-// none, else by the rows whose node has that ancestor.
-struct SlotSeen {
-  int j[4];
-};
-
 // Rows' masks: the ancestors of their nodes.
 struct RowMasks {
   const uint64_t* anc;
@@ -417,52 +405,56 @@ struct RowMasks {
   __device__ __forceinline__ uint64_t operator[](int r) const { return anc[node[r]]; }
 };
 
-__device__ __forceinline__ bool sees(int j, uint64_t m) {
-  return j < 0 || (j < kMaxNodes && ((m >> (j & 63)) & 1));
-}
-
-// t = c s - m of a fragment of 16 rows; t[8 g + 2 q + i]: row 8 g + x2 + i,
-// slot y + 8 q.
-__device__ __forceinline__ void frag_scores(const uint32_t (&s)[16], f32x2 c2, const float* nm, float (&t)[16]) {
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const f32x2 m = *reinterpret_cast<const f32x2*>(nm + g * 8);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
-      up2(fma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, m), t[g * 8 + q * 2],
-          t[g * 8 + q * 2 + 1]);
-    }
-  }
+// Bit 8 q: whether a row with ancestors m sees slot j + 8 q (j < 0: context).
+__device__ __forceinline__ uint32_t sees4(uint64_t m, int j) {
+  if (j >= kMaxNodes) return 0;
+  if (j >= 0) return static_cast<uint32_t>(m >> j);
+  if (j <= -32) return ~0u;
+  return (static_cast<uint32_t>(m) << -j) | ((1u << -j) - 1);
 }
 
 // Scores that are not seen become `none` (-inf once scaled), in place.
 __device__ __noinline__ void mask_tile(const Args& a, int t, int ctx, int tot, uint32_t tS, int nch,
                                        const uint64_t* anc, const uint8_t* node, float none) {
   const RowMasks mask{anc, node};
-  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const int row0 = ((threadIdx.x >> 5) & 3) * 32, y = (threadIdx.x & 31) >> 2;
   int first, count;
   tile_slots(a, t, first, count);
-  SlotSeen seen;
+  const bool plain = count == kTile;  // row r of the tile is slot first + r
+  if (plain && first + row0 + 32 <= ctx) return;
+  int j[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const int r = row_slot(a, warp * 32 + (lane >> 2) + 8 * q, count);
-    const int slot = first + r;
-    seen.j[q] = r < 0 || slot >= tot ? kMaxNodes : slot < ctx ? -1 : slot - ctx;
+    if (plain) {
+      j[q] = first + row0 + y + 8 * q - ctx;
+    } else {
+      const int r = row_slot(a, row0 + y + 8 * q, count);
+      j[q] = r < 0 || first + r >= tot ? kMaxNodes : max(first + r - ctx, -32);
+    }
   }
 #pragma unroll 1
   for (int k = 0; k < nch; ++k) {
-    uint32_t s[16];
+    uint32_t s[16], w[4];
     tm_ld_frag(tS + k * 16, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t m = mask[k * 16 + (i >> 1) * 8 + (i & 1)];
+      if (plain) {
+        w[i] = sees4(m, j[0]);
+      } else {
+        w[i] = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[i] |= (sees4(m, j[q]) & 1) << (8 * q);
+      }
+    }
     tm_wait_ld(s);
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const uint64_t m0 = mask[k * 16 + g * 8], m1 = mask[k * 16 + g * 8 + 1];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
-        if (!sees(seen.j[q], m0)) s[i] = __float_as_uint(none);
-        if (!sees(seen.j[q], m1)) s[i + 1] = __float_as_uint(none);
+        if (!(w[g * 2] & (1u << (8 * q)))) s[i] = __float_as_uint(none);
+        if (!(w[g * 2 + 1] & (1u << (8 * q)))) s[i + 1] = __float_as_uint(none);
       }
     }
     tm_st_frag(tS + k * 16, s);
@@ -470,41 +462,75 @@ __device__ __noinline__ void mask_tile(const Args& a, int t, int ctx, int tot, u
   tm_wait_st();
 }
 
+// Four 8 x 8 matrices of 16-bit entries from fragments into shared memory;
+// lane 8 i + j gives the address of row j of matrix i.  (Ordered among the
+// volatile statements; the fence before the consumers orders the memory.)
+__device__ __forceinline__ void st_matrices(uint32_t at, const uint32_t (&w)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]));
+}
+// The same with each matrix transposed.
+__device__ __forceinline__ void st_matrices_t(uint32_t at, const uint32_t (&w)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]));
+}
+
 // P^T of the tile into shared memory (rows contiguous, 64 of them and 128
 // slots a block, 128-byte swizzle), l += P; returns the largest excess over m.
-// prow: this lane's slot's line of the first block, which stmatrix takes as a
-// row of its 8 x 8 matrices.
+// prow: this lane's slot's line of the first block.  The matrices of 16 rows
+// are stored while the next rows' exponentials are on their way.
 template <class T, int NC>
 __device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const float* nm, int x2, uint32_t prow,
                                            int slot, f32x2 (&l)[NC / 8]) {
   float ex[2] = {-INFINITY, -INFINITY};
-  uint32_t s[2][16];
+  uint32_t s[2][16], w[2][4];
+  const uint32_t sw = slot & 7;
   tm_ld_frag(tS, s[0]);
+  const float* m = nm + x2;
+  f32x2 m0 = *reinterpret_cast<const f32x2*>(m), m1 = *reinterpret_cast<const f32x2*>(m + 8);
 #pragma unroll
   for (int k = 0; k < NC / 16; ++k) {
     if (k < nch) {
       tm_wait_ld(s[k & 1]);
-      if (k + 1 < nch) tm_ld_frag(tS + (k + 1) * 16, s[(k + 1) & 1]);
-      float t[16];
-      frag_scores(s[k & 1], c2, nm + k * 16 + x2, t);
+      f32x2 n0 = 0ull, n1 = 0ull;
+      if (k + 1 < nch) {
+        tm_ld_frag(tS + (k + 1) * 16, s[(k + 1) & 1]);
+        n0 = *reinterpret_cast<const f32x2*>(m + (k + 1) * 16);
+        n1 = *reinterpret_cast<const f32x2*>(m + (k + 1) * 16 + 8);
+      }
+      const uint32_t(&x)[16] = s[k & 1];
+      uint32_t v[2][4];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float t0 = t[g * 8 + q * 2], t1 = t[g * 8 + q * 2 + 1];
+          const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
+          float t0, t1;
+          up2(fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, g ? m1 : m0), t0, t1);
           ex[q & 1] = max3(ex[q & 1], t0, t1);
           const float e0 = ex2_fast(t0), e1 = ex2_fast(t1);
           l[k * 2 + g] = add2(l[k * 2 + g], pk2(e0, e1));
-          w[q] = T::pack(e0, e1);
+          v[g][q] = T::pack(e0, e1);
         }
-        const uint32_t at = prow + (k / 4) * kHalf + ((((k & 3) * 2 + g) ^ (slot & 7)) << 4);
-        asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]),
-                     "r"(w[1]), "r"(w[2]), "r"(w[3])
-                     : "memory");
       }
+      if (k > 0) {
+        const uint32_t line = prow + ((k - 1) / 4) * kHalf;
+        st_matrices(line + (((((k - 1) & 3) * 2) ^ sw) << 4), w[0]);
+        st_matrices(line + (((((k - 1) & 3) * 2 + 1) ^ sw) << 4), w[1]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        w[0][q] = v[0][q];
+        w[1][q] = v[1][q];
+      }
+      m0 = n0;
+      m1 = n1;
     }
   }
+  const int k = nch - 1;
+  const uint32_t line = prow + (k / 4) * kHalf;
+  st_matrices(line + ((((k & 3) * 2) ^ sw) << 4), w[0]);
+  st_matrices(line + ((((k & 3) * 2 + 1) ^ sw) << 4), w[1]);
   return fmaxf(ex[0], ex[1]);
 }
 
@@ -556,12 +582,13 @@ __device__ __noinline__ void rescale(uint32_t tO, int nch, const float* fac) {
   tm_wait_st();
 }
 
-// Adds the NaN or infinite values that column d of node j holds, if any, to
-// the rows that see it (nf: the nodes that hold some).
-template <class T>
+// Adds the NaN or infinite values of nodes (nf: the nodes that hold some) to
+// the written rows that see them: column d of the job's rows, in `out`
+// (row numbers in `row`) or in the parts.
+template <class T, int D>
 __device__ __noinline__ void add_nonfinite(const Args& a, int b, int h, int ctx, unsigned long long nf, int d,
-                                           const uint64_t* anc, const uint8_t* node, float (&o)[8]) {
-  const RowMasks mask{anc, node};
+                                           const uint64_t* anc, const uint8_t* node, const int* row, int c0, int c1,
+                                           char* out, float* part) {
 #pragma unroll 1
   for (int j = 0; j < a.nodes.N; ++j) {
     if (!((nf >> j) & 1)) continue;
@@ -572,9 +599,16 @@ __device__ __noinline__ void add_nonfinite(const Args& a, int b, int h, int ctx,
         a.vcache + 2 * (page * a.v_page + off * a.v_slot + h * a.v_head + d));
     const float v = T::lo(raw);
     if (fabsf(v) < INFINITY) continue;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if ((mask[i] >> j) & 1) o[i] += v;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+      if (row[c] < 0 || row[c] == kNoRow || !((anc[node[c]] >> j) & 1)) continue;
+      if (part) {
+        part[static_cast<long long>(c) * D + d] += v;
+      } else {
+        unsigned short* o = reinterpret_cast<unsigned short*>(out) + static_cast<long long>(row[c]) * D + d;
+        *o = static_cast<unsigned short>(T::pack(T::lo(*o) + v, 0.f));
+      }
+    }
   }
 }
 
@@ -648,20 +682,26 @@ __device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx,
     for (int v = 0; v < D / 8; ++v) line[(v / 8) * (kHalf / 16) + ((v ^ r) & 7)] = make_uint4(0, 0, 0, 0);
     return;
   }
-  bool bad = false;
-#pragma unroll 4
-  for (int v = 0; v < D / 8; ++v) {
-    uint4* p = line + (v / 8) * (kHalf / 16) + ((v ^ r) & 7);
-    const uint4 x = *p;
-    uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    bool here = false;
+  // an exponent of all ones carries into the sign's place
+  constexpr uint32_t kExp = T::kId == Bf16::kId ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kOne = T::kId == Bf16::kId ? 0x00800080u : 0x04000400u;
+  uint32_t carry = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!(fabsf(T::lo(w[i])) < INFINITY)) { w[i] &= 0xffff0000u; here = true; }
-      if (!(fabsf(T::hi(w[i])) < INFINITY)) { w[i] &= 0x0000ffffu; here = true; }
+  for (int v = 0; v < D / 8; ++v) {
+    const uint4 x = line[(v / 8) * (kHalf / 16) + ((v ^ r) & 7)];
+    carry |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
+  }
+  const bool bad = carry & 0x80008000u;
+  if (bad) {
+#pragma unroll 1
+    for (int v = 0; v < D / 8; ++v) {
+      uint32_t* p = reinterpret_cast<uint32_t*>(line + (v / 8) * (kHalf / 16) + ((v ^ r) & 7));
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c = ((p[i] & kExp) + kOne) & 0x80008000u;
+        if (c) p[i] &= (c & 0x8000u ? 0u : 0xffffu) | (c >> 31 ? 0u : 0xffff0000u);
+      }
     }
-    if (here) *p = make_uint4(w[0], w[1], w[2], w[3]);
-    bad |= here;
   }
   if (bad) {
     const int j = slot - ctx;
@@ -845,56 +885,92 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     if (two) named_sync(bar, 128);
     else named_sync(3, 256);
     {
-      // columns by eights: shared out over the warpgroups (alternate tiles)
-      // and, where O^T repeats itself (D = 64), over the two copies
-      const int d = wt & (D - 1);
-      const int groups = (two ? 1 : 2) * (128 / D);
-      const int me = (two ? 0 : wg) * (128 / D) + wt / D;
-      const unsigned long long nf = sm.nf[tb][0] | (static_cast<unsigned long long>(sm.nf[tb][1]) << 32);
-      char* obase = a.out + 2 * (orow * D + (d & ~1));
-      float* pbase = a.part_o + pslot * D + d;
+      // 16 rows (columns of O^T) at a time, a warp per 32 output columns;
+      // shared out over the warpgroups (alternate tiles) and, where O^T
+      // repeats itself (D = 64), over the two copies.  Finished rows go
+      // through shared memory, transposed, to 64-byte stores.
+      constexpr int WD = D / 32;
+      const int groups = (two ? 1 : 2) * (4 / WD), me = (two ? 0 : wg) * (4 / WD) + warp / WD;
+      const int d0 = (warp % WD) * 32;
+      char* obase = a.out + 2 * orow * D + 2 * (d0 + (lane & 3) * 8);
+      float* pbase = a.part_o + pslot * D + d0 + (lane >> 2);
       const uint32_t src0 = two ? tO : tO0, src1 = tO0 + kMaxJob;
       const bool use_a = two || used0, use_b = !two && used1;
+      char* stage = P + sizeof(Scratch) + warp * 1024;
+      const uint32_t st_at = sptr(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
+      const char* ld_at = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
 #pragma unroll 1
-      for (int k = me * 8; k < ncj; k += groups * 8) {
-        uint32_t u[8], v[8];
-        if (use_a) tm_ld8(src0 + k, u);
-        if (use_b) tm_ld8(src1 + k, v);
-        int row[8];
-        float f0[8], f1[8], o[8];
+      for (int k = me * 16; k < ncj; k += groups * 16) {
+        uint32_t u[16], v[16];
+        if (use_a) tm_ld_frag(src0 + k, u);
+        if (use_b) tm_ld_frag(src1 + k, v);
+        f32x2 f[2], e[2];
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          *reinterpret_cast<int4*>(row + i) = *reinterpret_cast<const int4*>(so.row + k + i);
-          *reinterpret_cast<float4*>(f0 + i) = *reinterpret_cast<const float4*>(so.fac + k + i);
-          if (use_b) *reinterpret_cast<float4*>(f1 + i) = *reinterpret_cast<const float4*>(sc1.fac + k + i);
+        for (int g = 0; g < 2; ++g) {
+          f[g] = *reinterpret_cast<const f32x2*>(so.fac + k + g * 8 + x2);
+          e[g] = use_b ? *reinterpret_cast<const f32x2*>(sc1.fac + k + g * 8 + x2) : 0ull;
         }
-        if (use_a) tm_wait_ld8(u);
-        if (use_b) tm_wait_ld8(v);
+        if (use_a) tm_wait_ld(u);
+        if (use_b) tm_wait_ld(v);
+        f32x2 o[2][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = use_a ? f0[i] * __uint_as_float(u[i]) : 0.f;
-          if (use_b) o[i] = fmaf(f1[i], __uint_as_float(v[i]), o[i]);
-        }
-        if (nf) add_nonfinite<T>(a, b, h, ctx, nf, d, anc, node + k, o);
-        if (direct) {
-          // neighbouring lanes trade, so that each stores two entries of one row
-          const bool odd = d & 1;
+        for (int g = 0; g < 2; ++g) {
 #pragma unroll
-          for (int i = 0; i < 8; i += 2) {
-            const float x0 = row[i] >= 0 ? o[i] : 0.f, x1 = row[i + 1] >= 0 ? o[i + 1] : 0.f;
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? x0 : x1, 1);
-            const uint32_t w = odd ? T::pack(other, x1) : T::pack(x0, other);
-            int r = odd ? row[i + 1] : row[i];
-            if (r != kNoRow) {
-              r = r < 0 ? ~r : r;
-              *reinterpret_cast<uint32_t*>(obase + static_cast<long long>(r) * (2 * D)) = w;
-            }
+          for (int q = 0; q < 4; ++q) {
+            const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
+            f32x2 x = use_a ? mul2(pk2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f[g]) : 0ull;
+            if (use_b) x = fma2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), e[g], x);
+            o[g][q] = x;
           }
+        }
+        if (direct) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float x, y;
+              up2(o[g][q], x, y);
+              w[q] = T::pack(x, y);
+            }
+            st_matrices_t(st_at + g * 512, w);
+          }
+          asm volatile("" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            int r = so.row[k + g * 8 + (lane >> 2)];
+            uint4 w = *reinterpret_cast<const uint4*>(ld_at + g * 512);
+            if (r < 0) {  // a row of zeros
+              r = ~r;
+              w = make_uint4(0, 0, 0, 0);
+            }
+            if (r != kNoRow) *reinterpret_cast<uint4*>(obase + static_cast<long long>(r) * (2 * D)) = w;
+          }
+          __syncwarp();
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (row[i] != kNoRow) pbase[(k + i) * D] = o[i];
+          for (int g = 0; g < 2; ++g) {
+            const int c = k + g * 8 + x2;
+            float* at0 = pbase + c * D;
+            const bool ok0 = so.row[c] != kNoRow, ok1 = so.row[c + 1] != kNoRow;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float x, y;
+              up2(o[g][q], x, y);
+              if (ok0) at0[8 * q] = x;
+              if (ok1) at0[D + 8 * q] = y;
+            }
+          }
         }
+      }
+      const unsigned long long nf = sm.nf[tb][0] | (static_cast<unsigned long long>(sm.nf[tb][1]) << 32);
+      if (nf) {
+        if (two) named_sync(bar, 128);
+        else named_sync(3, 256);
+        if (wt < D && (two || wg == 0))
+          add_nonfinite<T, D>(a, b, h, ctx, nf, wt, anc, node, so.row, 0, ncj, a.out + 2 * orow * D,
+                              direct ? nullptr : a.part_o + pslot * D);
       }
     }
     tc_before();
@@ -1001,7 +1077,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       long long p = before;
 #pragma unroll 1
       for (int b = f; b < e; ++b) {
-        const int Tb = seq_tiles(a, b).T;
+        const SeqTiles q = seq_tiles(a, b);
+        const int Tb = q.T;
         const long long w = static_cast<long long>(Tb) * items;
         if (lo < p + w) {
           Range r;
@@ -1011,7 +1088,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           r.h = sm.h0 = item / a.RB;
           r.rb = sm.rb0 = item - r.h * a.RB;
           r.t0 = sm.t0 = static_cast<int>(lo - p - static_cast<long long>(item) * Tb);
-          r.T = Tb;
+          r.T = sm.T0 = Tb;
+          sm.ctx0 = q.ctx;
+          sm.tot0 = q.tot;
+          sm.tail0 = q.tail;
           r.used = 1;
           a.ranges[me] = r;
           break;
@@ -1070,10 +1150,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (__all_sync(0xffffffffu, ok)) {
           if (lane == 0) bar_expect(&full[slot], boxes * a.box * 128 * HALVES);
           __syncwarp();
-          if (lane < boxes) {
-            const uint32_t dst = ring0 + slot * kSlotBytes + lane * a.box * 128;
+          const uint32_t dst = ring0 + slot * kSlotBytes;
+#pragma unroll 1
+          for (int p0 = 0; p0 < boxes; p0 += 8) {
+            int pg[8];
 #pragma unroll
-            for (int d = 0; d < HALVES; ++d) tma_rows(dst + d * kHalf, map, d * 64, s0, pc.h, cur, &full[slot]);
+            for (int p = 0; p < 8; ++p) pg[p] = __shfl_sync(0xffffffffu, cur, p0 + p);
+            if (elect_one()) {
+#pragma unroll
+              for (int p = 0; p < 8; ++p) {
+                if (p0 + p < boxes) {
+#pragma unroll
+                  for (int d = 0; d < HALVES; ++d)
+                    tma_rows(dst + (p0 + p) * a.box * 128 + d * kHalf, map, d * 64, s0, pc.h, pg[p], &full[slot]);
+                }
+              }
+            }
+            __syncwarp();
           }
           __syncwarp();
         }
@@ -1094,7 +1187,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     while (pc.next(a)) {
       const int qb = a.two ? 0 : item & 1;
       bar_wait(&sm.qfull[qb], (a.two ? item : item >> 1) & 1, sm, a.err);
-      const uint64_t qd = qd0 + qb * (qbytes / 16);
+      const uint64_t qd = qd0 + __shfl_sync(0xffffffffu, qb, 0) * (qbytes / 16);
       ++item;
 #pragma unroll 1
       for (int t = pc.t0; t < pc.end; ++t, ++g) {
@@ -1103,7 +1196,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           phase ^= 1;
         }
         bar_wait(&sm.kfull[slot], phase, sm, a.err);
-        const uint64_t kd = kd0 + slot * (kSlotBytes / 16);
+        const uint64_t kd = kd0 + __shfl_sync(0xffffffffu, slot, 0) * (kSlotBytes / 16);
 #pragma unroll 1
         for (int hf = 0; hf < halves; ++hf) {
           // S of this warpgroup is free once it has made its P of the last one
@@ -1111,7 +1204,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (n > 0) bar_wait(&sm.pfull[w], (n - 1) & 1, sm, a.err);
           tc_after();
           const uint64_t q = qd + hf * a.ncj * 8;
-          const uint32_t d = tmem + w * kMaxJob;
+          const uint32_t d = __shfl_sync(0xffffffffu, tmem + w * kMaxJob, 0);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
@@ -1144,15 +1237,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           phase ^= 1;
         }
         bar_wait(&sm.vfull[slot], phase, sm, a.err);
-        const uint64_t vd = vd0 + slot * (kSlotBytes / 16);
+        const uint64_t vd = vd0 + __shfl_sync(0xffffffffu, slot, 0) * (kSlotBytes / 16);
         const bool add = t - pc.t0 >= (a.two ? 1 : 2);  // not the warpgroup's first tile of the piece
 #pragma unroll 1
         for (int hf = 0; hf < halves; ++hf) {
           const int w = a.two ? hf : g & 1, n = a.two ? g : g >> 1;
           bar_wait(&sm.pfull[w], n & 1, sm, a.err);
           tc_after();
-          const uint64_t pd = pd0 + w * (pbytes / 16);
-          const uint32_t d = tmem + 2 * kMaxJob + w * kMaxJob;
+          const int wu = __shfl_sync(0xffffffffu, w, 0);
+          const uint64_t pd = pd0 + wu * (pbytes / 16);
+          const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + 2 * kMaxJob + wu * kMaxJob;
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * 128, pd + k * 128, ipv, add || k > 0);
