@@ -48,20 +48,22 @@ namespace {
 constexpr int kAttnThreads = 384;
 constexpr int kTile = 128;           // slots of a tile (rows of the ring's tiles)
 constexpr int kHalf = kTile * 128;   // bytes of a tile's 64-column half
+constexpr int kPBlock = kTile * 64;  // bytes of P of 32 rows
 constexpr int kMaxRing = 4;           // slots of each ring
 constexpr int kMaxRows = 256;        // rows of a row block
 constexpr int kAlternate = 64;       // most rows whose tiles the warpgroups take in turn
 constexpr int kMaxJob = 128;         // rows of a job (one warpgroup's columns)
 constexpr int kMaxCtas = 160;
 constexpr int kNoRow = 0x7fffffff;   // a column without a row (rows of zeros: ~row)
+constexpr int kItemCost = 4;         // what an item's start and end cost, in tiles
 constexpr float kNoScore = -1e30f;   // m of a row that has seen nothing
 constexpr int kSmemMax = 227 * 1024;
 
 // A CTA's range of tiles, for the joining kernel.
 struct Range {
-  long long lo;          // first tile
+  long long lo;          // first tile (its position in cost)
   int b, h, rb, t0, T;   // its item, its place there, the item's tiles
-  int used;              // 0: an empty range
+  int used;              // 0: a range without tiles
 };
 
 struct Args {
@@ -76,6 +78,8 @@ struct Args {
   int nk, nv;               // slots of the K and V rings
   int box, ppt, tk, tpp;    // rows of a TMA box, pages a tile, slots a tile, tiles a page
   int ragged;               // tiles have rows that are no slot
+  int fold;                 // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
+  int group, half;          // bytes from 8 slots of a tile to the next, from half to half
   int cover;                // rows of a tile that TMA writes
   const char* q;
   long long q_b, q_n, q_h;
@@ -102,6 +106,7 @@ struct alignas(16) Misc {
   unsigned nf[2][2];                // nodes with NaN or infinite values
   int b0, h0, rb0, t0;              // first piece, its sequence's
   int T0, ctx0, tot0, tail0;        // tiles and lengths
+  int cost;                         // of an item beside its tiles
   unsigned tmem;
   int abort;
 };
@@ -110,10 +115,17 @@ static_assert(sizeof(Misc) <= 3072, "shared memory of 256 rows");
 // What a warpgroup keeps in its P buffer while that holds no P: between the
 // product of one tile and the P of the next, and at the end of a piece.
 struct Scratch {
-  float red[4][kMaxJob];
   float fac[kMaxJob];
   int row[kMaxJob];  // node * Hq + head of the group, its complement, or kNoRow
+  union {
+    struct {
+      float red[4][kMaxJob];
+      uint4 seen[kMaxJob];  // rows' masks, for a tile with drafted nodes
+    };
+    char stage[4][1024];    // results on their way out, a part per warp
+  };
 };
+static_assert(sizeof(Scratch) <= kPBlock, "the smallest P buffer");
 
 // ---------------------------------------------------------------------------
 // mbarriers, TMA, tcgen05
@@ -192,6 +204,16 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// As tma_rows for whole groups of 8 slots, both 64-column halves in one copy.
+__device__ __forceinline__ void tma_groups(uint32_t dst, const CUtensorMap* map, int group, int head,
+                                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(sptr(bar)), "r"(0), "r"(group), "r"(head)
+      : "memory");
+}
+
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -220,10 +242,11 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
       : "memory");
 }
 
-// Shared-memory operand descriptor: 128-byte swizzle, strides in bytes.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+// Shared-memory operand descriptor: strides in bytes; swizzle 2: 128 bytes,
+// 4: 64 bytes.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle = 2) {
   return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
-         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (swizzle << 61);
 }
 // Instruction descriptor: 32-bit accumulator, 128 x n, 16-bit operands.
 template <class T>
@@ -333,13 +356,15 @@ __device__ __noinline__ SeqTiles seq_tiles(const Args& a, int b) {
 // The pieces of a CTA's range, one (sequence, head, row block) after another.
 // Only the first may start behind tile 0.
 struct Pieces {
-  long long left;     // tiles from t0 to the range's end
+  long long left;     // cost from t0 to the range's end: a tile 1, an item's end w
+  int w;
   int b, h, rb;
   int T, ctx, tot;    // of sequence b
   int t0, end, tail;  // tiles t0 .. end - 1; the first with slots behind the context
   bool fresh;
   __device__ __forceinline__ void start(const Misc& sm) {
     left = sm.left;
+    w = sm.cost;
     b = sm.b0;
     h = sm.h0;
     rb = sm.rb0;
@@ -361,7 +386,7 @@ struct Pieces {
   __device__ __forceinline__ bool next(const Args& a) {
     bool reload = false;
     if (!fresh) {
-      left -= end - t0;
+      left -= end - t0 + (end == T ? w : 0);
       t0 = 0;
       if (++rb == a.RB) {
         rb = 0;
@@ -398,39 +423,34 @@ struct Pieces {
 // its warp's 32 (lane 4 y + x), so a row's sum needs one register of four
 // threads' columns and m one load per two rows.
 
-// Rows' masks: the ancestors of their nodes.
-struct RowMasks {
-  const uint64_t* anc;
-  const uint8_t* node;
-  __device__ __forceinline__ uint64_t operator[](int r) const { return anc[node[r]]; }
-};
-
-// Bit 8 q: whether a row with ancestors m sees slot j + 8 q (j < 0: context).
-__device__ __forceinline__ uint32_t sees4(uint64_t m, int j) {
-  if (j >= kMaxNodes) return 0;
-  if (j >= 0) return static_cast<uint32_t>(m >> j);
-  if (j <= -32) return ~0u;
-  return (static_cast<uint32_t>(m) << -j) | ((1u << -j) - 1);
+// A row's mask as four words: ~0 for the 32 slots before the first node, the
+// 64 nodes, 0 behind them.  32 bits of it from slot j (relative to the first
+// node) on, j >= -32:
+__device__ __forceinline__ uint32_t seen_from(const uint4* row, int word, int shift) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
+  return __funnelshift_r(w[word], word < 3 ? w[word + 1] : 0u, shift);
 }
 
-// Scores that are not seen become `none` (-inf once scaled), in place.
+// Scores that are not seen become `none` (-inf once scaled), in place.  mask:
+// the rows' masks, from the thread's first row.
+template <bool PLAIN>
 __device__ __noinline__ void mask_tile(const Args& a, int t, int ctx, int tot, uint32_t tS, int nch,
-                                       const uint64_t* anc, const uint8_t* node, float none) {
-  const RowMasks mask{anc, node};
+                                       const uint4* mask, float none) {
   const int row0 = ((threadIdx.x >> 5) & 3) * 32, y = (threadIdx.x & 31) >> 2;
   int first, count;
   tile_slots(a, t, first, count);
-  const bool plain = count == kTile;  // row r of the tile is slot first + r
-  if (plain && first + row0 + 32 <= ctx) return;
-  int j[4];
+  if (PLAIN && first + row0 + 32 <= ctx) return;
+  int word[4], shift[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (plain) {
-      j[q] = first + row0 + y + 8 * q - ctx;
-    } else {
-      const int r = row_slot(a, row0 + y + 8 * q, count);
-      j[q] = r < 0 || first + r >= tot ? kMaxNodes : max(first + r - ctx, -32);
-    }
+  for (int q = 0; q < (PLAIN ? 1 : 4); ++q) {
+    // plain: row r of the tile is slot first + r, and bits 8 q of a word from
+    // the first of the thread's slots on are the four
+    const int r = PLAIN ? row0 + y : row_slot(a, row0 + y + 8 * q, count);
+    int j = first + r - ctx;
+    if (r < 0 || first + r >= tot) j = kMaxNodes;
+    j = min(max(j, -32), kMaxNodes) + 32;
+    word[q] = j >> 5;
+    shift[q] = j & 31;
   }
 #pragma unroll 1
   for (int k = 0; k < nch; ++k) {
@@ -438,13 +458,12 @@ __device__ __noinline__ void mask_tile(const Args& a, int t, int ctx, int tot, u
     tm_ld_frag(tS + k * 16, s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint64_t m = mask[k * 16 + (i >> 1) * 8 + (i & 1)];
-      if (plain) {
-        w[i] = sees4(m, j[0]);
-      } else {
-        w[i] = 0;
+      const uint4* m = mask + k * 16 + (i >> 1) * 8 + (i & 1);
+      w[i] = seen_from(m, word[0], shift[0]);
+      if (!PLAIN) {
+        w[i] &= 1;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) w[i] |= (sees4(m, j[q]) & 1) << (8 * q);
+        for (int q = 1; q < 4; ++q) w[i] |= (seen_from(m, word[q], shift[q]) & 1) << (8 * q);
       }
     }
     tm_wait_ld(s);
@@ -475,8 +494,8 @@ __device__ __forceinline__ void st_matrices_t(uint32_t at, const uint32_t (&w)[4
                "r"(w[1]), "r"(w[2]), "r"(w[3]));
 }
 
-// P^T of the tile into shared memory (rows contiguous, 64 of them and 128
-// slots a block, 128-byte swizzle), l += P; returns the largest excess over m.
+// P^T of the tile into shared memory (rows contiguous, 32 of them and 128
+// slots a block, 64-byte swizzle), l += P; returns the largest excess over m.
 // prow: this lane's slot's line of the first block.  The matrices of 16 rows
 // are stored while the next rows' exponentials are on their way.
 template <class T, int NC>
@@ -484,7 +503,7 @@ __device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const
                                            int slot, f32x2 (&l)[NC / 8]) {
   float ex[2] = {-INFINITY, -INFINITY};
   uint32_t s[2][16], w[2][4];
-  const uint32_t sw = slot & 7;
+  const uint32_t sw = (slot >> 1) & 3;
   tm_ld_frag(tS, s[0]);
   const float* m = nm + x2;
   f32x2 m0 = *reinterpret_cast<const f32x2*>(m), m1 = *reinterpret_cast<const f32x2*>(m + 8);
@@ -514,9 +533,9 @@ __device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const
         }
       }
       if (k > 0) {
-        const uint32_t line = prow + ((k - 1) / 4) * kHalf;
-        st_matrices(line + (((((k - 1) & 3) * 2) ^ sw) << 4), w[0]);
-        st_matrices(line + (((((k - 1) & 3) * 2 + 1) ^ sw) << 4), w[1]);
+        const uint32_t line = prow + ((k - 1) / 2) * kPBlock;
+        st_matrices(line + (((((k - 1) & 1) * 2) ^ sw) << 4), w[0]);
+        st_matrices(line + (((((k - 1) & 1) * 2 + 1) ^ sw) << 4), w[1]);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -528,44 +547,74 @@ __device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const
     }
   }
   const int k = nch - 1;
-  const uint32_t line = prow + (k / 4) * kHalf;
-  st_matrices(line + ((((k & 3) * 2) ^ sw) << 4), w[0]);
-  st_matrices(line + ((((k & 3) * 2 + 1) ^ sw) << 4), w[1]);
+  const uint32_t line = prow + (k / 2) * kPBlock;
+  st_matrices(line + ((((k & 1) * 2) ^ sw) << 4), w[0]);
+  st_matrices(line + ((((k & 1) * 2 + 1) ^ sw) << 4), w[1]);
   return fmaxf(ex[0], ex[1]);
 }
 
-// Over the eight lanes that hold the same rows.
-__device__ __forceinline__ float lanes_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-}
-__device__ __forceinline__ float lanes_sum(float v) {
-  v += __shfl_xor_sync(0xffffffffu, v, 4);
-  v += __shfl_xor_sync(0xffffffffu, v, 8);
-  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+// Joins v over the eight lanes that hold the same rows, each lane giving half
+// of its rows away at a step, and stores the results: v[2 i + h] belongs to
+// row 8 i + x2 + h.
+template <int NC, bool MAX>
+__device__ __forceinline__ void join_rows(float (&v)[NC / 4], float* red, int lane, int ncj) {
+  int base = 0, n = NC / 8;  // groups of 8 rows: base .. base + n - 1 are in v
+#pragma unroll
+  for (int d = 16; d >= 4; d >>= 1) {
+    const bool up = lane & d;
+    if (n > 1) {
+      n >>= 1;
+      if (up) base += n;
+#pragma unroll
+      for (int i = 0; i < NC / 8; ++i) {
+        if (i < 2 * n) {
+          const float give = up ? v[i] : v[i + 2 * n];
+          const float mine = up ? v[i + 2 * n] : v[i];
+          const float got = __shfl_xor_sync(0xffffffffu, give, d);
+          v[i] = MAX ? fmaxf(mine, got) : mine + got;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float got = __shfl_xor_sync(0xffffffffu, v[i], d);
+        v[i] = MAX ? fmaxf(v[i], got) : v[i] + got;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NC / 8; ++i) {
+    if (i < n && (base + i) * 8 < ncj)
+      *reinterpret_cast<float2*>(red + (base + i) * 8 + (lane & 3) * 2) = make_float2(v[2 * i], v[2 * i + 1]);
+  }
 }
 
 // Row maxima of c s over the warp's 32 slots, into red.
-__device__ __noinline__ void tile_maxima(uint32_t tS, int nch, float c, float* red) {
+template <int NC>
+__device__ __noinline__ void tile_maxima(uint32_t tS, int ncj, float c, float* red) {
   const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int k = 0; k < nch; ++k) {
-    uint32_t s[16];
-    tm_ld_frag(tS + k * 16, s);
-    tm_wait_ld(s);
+  float v[NC / 4];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      float m[2];
+  for (int k = 0; k < NC / 16; ++k) {
+    if (k * 16 < ncj) {
+      uint32_t s[16];
+      tm_ld_frag(tS + k * 16, s);
+      tm_wait_ld(s);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float a = __uint_as_float(s[g * 4 + i]) * c, b = __uint_as_float(s[g * 4 + 2 + i]) * c;
-        const float d = __uint_as_float(s[8 + g * 4 + i]) * c, e = __uint_as_float(s[8 + g * 4 + 2 + i]) * c;
-        m[i] = lanes_max(fmaxf(fmaxf(a, b), fmaxf(d, e)));
+      for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float a = __uint_as_float(s[g * 4 + i]) * c, b = __uint_as_float(s[g * 4 + 2 + i]) * c;
+          const float d = __uint_as_float(s[8 + g * 4 + i]) * c, e = __uint_as_float(s[8 + g * 4 + 2 + i]) * c;
+          v[k * 4 + g * 2 + i] = fmaxf(fmaxf(a, b), fmaxf(d, e));
+        }
       }
-      if (lane < 4) *reinterpret_cast<float2*>(red + k * 16 + g * 8 + lane * 2) = make_float2(m[0], m[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[k * 4 + i] = 0.f;
     }
   }
+  join_rows<NC, true>(v, red, lane, ncj);
 }
 
 // O of the warpgroup times the factors of its rows.
@@ -676,10 +725,11 @@ __device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx,
   const int rs = row_slot(a, r, count);
   const int slot = rs < 0 ? 0x7fffffff : first + rs;
   if (slot < ctx) return;
-  uint4* line = reinterpret_cast<uint4*>(V + r * 128);
+  uint4* line = reinterpret_cast<uint4*>(V + (r >> 3) * a.group + (r & 7) * 128);
+  const int half = a.half / 16;
   if (slot >= tot) {
 #pragma unroll
-    for (int v = 0; v < D / 8; ++v) line[(v / 8) * (kHalf / 16) + ((v ^ r) & 7)] = make_uint4(0, 0, 0, 0);
+    for (int v = 0; v < D / 8; ++v) line[(v / 8) * half + ((v ^ r) & 7)] = make_uint4(0, 0, 0, 0);
     return;
   }
   // an exponent of all ones carries into the sign's place
@@ -688,14 +738,14 @@ __device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx,
   uint32_t carry = 0;
 #pragma unroll
   for (int v = 0; v < D / 8; ++v) {
-    const uint4 x = line[(v / 8) * (kHalf / 16) + ((v ^ r) & 7)];
+    const uint4 x = line[(v / 8) * half + ((v ^ r) & 7)];
     carry |= ((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne);
   }
   const bool bad = carry & 0x80008000u;
   if (bad) {
 #pragma unroll 1
     for (int v = 0; v < D / 8; ++v) {
-      uint32_t* p = reinterpret_cast<uint32_t*>(line + (v / 8) * (kHalf / 16) + ((v ^ r) & 7));
+      uint32_t* p = reinterpret_cast<uint32_t*>(line + (v / 8) * half + ((v ^ r) & 7));
 #pragma unroll 1
       for (int i = 0; i < 4; ++i) {
         const uint32_t c = ((p[i] & kExp) + kOne) & 0x80008000u;
@@ -724,7 +774,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
   const uint32_t tS = tmem + lane_base + wg * kMaxJob;
   const uint32_t tO0 = tmem + lane_base + 2 * kMaxJob;
   const uint32_t tO = tO0 + wg * kMaxJob;
-  const uint32_t prow = sptr(P) + wt * 128;
+  const uint32_t prow = sptr(P) + wt * 64;
   const int ncj = a.ncj, nch = ncj / 16;
   const f32x2 c2 = pk2(a.c, a.c);
   float* nm = sm.nm[wg];
@@ -752,11 +802,18 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     const int rows = min(a.rows_per_block - colbase, a.R - r0);  // of this job's columns
     const int tb = item_no & 1;                                  // tables
     more = pn.next(a);
-    if (more) row_tables(a, sm, pn.b, pn.rb, pn.tot - pn.ctx, tb ^ 1);
-    // the next rows of Q: into the other buffer now, or (one buffer) into
-    // this warpgroup's half once its last scores are there
-    bool pending = more && !two;
-    if (pending) fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q + (tb ^ 1) * qbytes, 0, a.cols, at, 256);
+    // The next piece's tables and rows, while this piece's first product
+    // runs: the rows go into the other buffer, or (one buffer) later into
+    // this warpgroup's half, once its last scores are there.
+    bool todo = more, pending = false;
+    auto prefetch = [&]() {
+      row_tables(a, sm, pn.b, pn.rb, pn.tot - pn.ctx, tb ^ 1);
+      if (!two) {
+        fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q + (tb ^ 1) * qbytes, 0, a.cols, at, 256);
+        pending = true;
+      }
+      todo = false;
+    };
     const uint64_t* anc = sm.anc[tb];
     const uint8_t* node = sm.node[tb] + colbase;
     if (wt < ncj) nm[wt] = -kNoScore;
@@ -775,12 +832,21 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         ppv ^= 1;
       }
       tc_after();
-      if (t >= tail) mask_tile(a, t, ctx, tot, tS, nch, anc, node + x2, none);
+      if (t >= tail) {
+        if (wt < ncj) {
+          const uint64_t m = anc[node[wt]];
+          sc.seen[wt] = make_uint4(~0u, static_cast<uint32_t>(m), static_cast<uint32_t>(m >> 32), 0u);
+        }
+        named_sync(bar, 128);
+        if (a.ragged) mask_tile<false>(a, t, ctx, tot, tS, nch, sc.seen + x2, none);
+        else mask_tile<true>(a, t, ctx, tot, tS, nch, sc.seen + x2, none);
+        named_sync(bar, 128);  // the masks lie where P goes
+      }
       bool raise = jobs == 0;
 #pragma unroll 1
       while (true) {
         if (raise) {
-          tile_maxima(tS, nch, a.c, sc.red[warp]);
+          tile_maxima<NC>(tS, ncj, a.c, sc.red[warp]);
           named_sync(bar, 128);
           if (wt < ncj) {
             const float mx = fmaxf(fmaxf(sc.red[0][wt], sc.red[1][wt]), fmaxf(sc.red[2][wt], sc.red[3][wt]));
@@ -820,9 +886,11 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         rows_ready(sm, tb ^ 1);
         pending = false;
       }
+      if (todo) prefetch();
     }
 
     // ---- end of the piece: l over the slots, then O ----
+    if (todo) prefetch();
     if (pending) rows_ready(sm, tb ^ 1);
     if (two && more) fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, colbase, colbase + ncj, wt, 128);
     if (jobs > 0) {
@@ -830,15 +898,11 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       ppv ^= 1;
       tc_after();
     }
+    {
+      float v[NC / 4];
 #pragma unroll
-    for (int i = 0; i < NC / 8; ++i) {
-      if (8 * i < ncj) {
-        float u, v;
-        up2(l[i], u, v);
-        u = lanes_sum(u);
-        v = lanes_sum(v);
-        if (lane < 4) *reinterpret_cast<float2*>(sc.red[warp] + 8 * i + x2) = make_float2(u, v);
-      }
+      for (int i = 0; i < NC / 8; ++i) up2(l[i], v[2 * i], v[2 * i + 1]);
+      join_rows<NC, false>(v, sc.red[warp], lane, ncj);
     }
     if (two) named_sync(bar, 128);
     else named_sync(3, 256);
@@ -896,7 +960,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       float* pbase = a.part_o + pslot * D + d0 + (lane >> 2);
       const uint32_t src0 = two ? tO : tO0, src1 = tO0 + kMaxJob;
       const bool use_a = two || used0, use_b = !two && used1;
-      char* stage = P + sizeof(Scratch) + warp * 1024;
+      char* stage = sc.stage[warp];
       const uint32_t st_at = sptr(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
       const char* ld_at = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
 #pragma unroll 1
@@ -993,7 +1057,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   char* Q = ringv + a.nv * kSlotBytes;
   const int qbytes = a.cols * D * 2;
   char* P = Q + (a.two ? 1 : 2) * qbytes;
-  const int pbytes = ((a.ncj + 63) / 64) * kHalf;
+  const int pbytes = ((a.ncj + 31) / 32) * kPBlock;
   Misc& sm = *reinterpret_cast<Misc*>(P + 2 * pbytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = gridDim.x, B = a.nodes.B;
@@ -1039,17 +1103,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int per = (B + kAttnThreads - 1) / kAttnThreads;
     const int f = tid * per, e = min(B, f + per);
     const int items = a.Hkv * a.RB;
-    long long mine = 0;
+    long long mine = 0, seqs = 0;  // tiles; sequences with tiles
     bool any_bad = false;
 #pragma unroll 1
     for (int b = f; b < e; ++b) {
       int ctx;
       bool bad;
-      mine += static_cast<long long>(tiles_of(a, seq_len(a, b, ctx, bad))) * items;
+      const int Tb = tiles_of(a, seq_len(a, b, ctx, bad));
+      mine += Tb;
+      seqs += Tb > 0;
       any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) atomicOr(a.err, kErrBadLength);
-    long long inc = mine;
+    long long inc = mine + (seqs << 40);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, inc, d);
@@ -1058,47 +1124,65 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     long long* pre = reinterpret_cast<long long*>(Q);  // not in use yet
     if (lane == 31) pre[warp] = inc;
     __syncthreads();
-    long long before = 0, W = 0;
+    long long before = inc - mine - (seqs << 40), all = 0;
 #pragma unroll 1
     for (int i = 0; i < kAttnThreads / 32; ++i) {
       if (i < warp) before += pre[i];
-      W += pre[i];
+      all += pre[i];
     }
-    before += inc - mine;
-    // (at most W ranges, so that none of those is empty)
-    const long long Cr = min(static_cast<long long>(C), W), me = blockIdx.x;
-    const bool used = me < Cr;
-    const long long lo = used ? W * me / Cr : 0, hi = used ? W * (me + 1) / Cr : 0;
+    const long long tiles = (all & ((1ll << 40) - 1)) * items, n_items = (all >> 40) * items;
+    // What an item costs beside its tiles (first and last tile, results), in
+    // tiles: kItemCost, less where a range is of a few tiles only.
+    const long long w = min(static_cast<long long>(kItemCost), tiles / (8ll * C));
+    const long long W = tiles + w * n_items;
+    // The range's ends in cost: [lo, hi); an item's tiles come first in its
+    // T + w.  A range may hold no tile.
+    const long long me = blockIdx.x, lo = W * me / C, hi = W * (me + 1) / C;
+    long long p = ((before & ((1ll << 40) - 1)) + w * (before >> 40)) * items;
+    const long long mine_cost = (mine + w * seqs) * items;
     if (tid == 0) {
-      sm.left = hi - lo;
-      if (!used) a.ranges[me].used = 0;
+      sm.left = 0;
+      a.ranges[me].used = 0;
     }
-    if (used && lo >= before && lo < before + mine) {
-      long long p = before;
+    __syncthreads();
+    // the thread whose sequences hold the range's first tile (lo may lie behind
+    // the tiles of the last item before them)
+    const bool mine_here = lo < p + mine_cost && hi > p && p - lo <= w;
 #pragma unroll 1
-      for (int b = f; b < e; ++b) {
-        const SeqTiles q = seq_tiles(a, b);
-        const int Tb = q.T;
-        const long long w = static_cast<long long>(Tb) * items;
-        if (lo < p + w) {
-          Range r;
-          const int item = static_cast<int>((lo - p) / Tb);
-          r.lo = lo;
-          r.b = sm.b0 = b;
-          r.h = sm.h0 = item / a.RB;
-          r.rb = sm.rb0 = item - r.h * a.RB;
-          r.t0 = sm.t0 = static_cast<int>(lo - p - static_cast<long long>(item) * Tb);
-          r.T = sm.T0 = Tb;
-          sm.ctx0 = q.ctx;
-          sm.tot0 = q.tot;
-          sm.tail0 = q.tail;
-          r.used = 1;
-          a.ranges[me] = r;
+    for (int b = f; b < e && mine_here; ++b) {
+      const SeqTiles q = seq_tiles(a, b);
+      if (q.T == 0) continue;
+      const long long one = q.T + w, end = p + one * items;
+      if (lo < end) {
+        int item = lo > p ? static_cast<int>((lo - p) / one) : 0;
+        int t0 = lo > p ? static_cast<int>(lo - p - item * one) : 0;
+        if (t0 >= q.T) {  // behind the item's tiles: the next item
+          ++item;
+          t0 = 0;
+        }
+        const long long from = p + item * one + t0;  // cost position of the first tile
+        if (item < items) {
+          if (from < hi) {
+            Range r;
+            r.lo = from;
+            r.b = sm.b0 = b;
+            r.h = sm.h0 = item / a.RB;
+            r.rb = sm.rb0 = item - r.h * a.RB;
+            r.t0 = sm.t0 = t0;
+            r.T = sm.T0 = q.T;
+            sm.ctx0 = q.ctx;
+            sm.tot0 = q.tot;
+            sm.tail0 = q.tail;
+            r.used = 1;
+            a.ranges[me] = r;
+            sm.left = hi - from;
+          }
           break;
         }
-        p += w;
       }
+      p = end;
     }
+    if (tid == 0) sm.cost = static_cast<int>(w);
   }
   tc_before();
   __syncthreads();
@@ -1141,6 +1225,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (t + 1 < pc.end) id = lookup(t + 1);
         const int boxes = a.ps <= kTile ? min(a.ppt, npages - t * a.ppt) : 1;
         const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
+        // (a page id out of range: a coordinate behind the last)
+        const int unit = a.fold ? cur * a.fold + s0 / 8 : cur;
         if (++slot == slots) {
           slot = 0;
           phase ^= 1;
@@ -1155,14 +1241,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int p0 = 0; p0 < boxes; p0 += 8) {
             int pg[8];
 #pragma unroll
-            for (int p = 0; p < 8; ++p) pg[p] = __shfl_sync(0xffffffffu, cur, p0 + p);
+            for (int p = 0; p < 8; ++p) pg[p] = __shfl_sync(0xffffffffu, unit, p0 + p);
             if (elect_one()) {
+              if (D == 128 && a.fold) {
 #pragma unroll
-              for (int p = 0; p < 8; ++p) {
-                if (p0 + p < boxes) {
+                for (int p = 0; p < 8; ++p)
+                  if (p0 + p < boxes) tma_groups(dst + (p0 + p) * a.box * 256, map, pg[p], pc.h, &full[slot]);
+              } else {
 #pragma unroll
-                  for (int d = 0; d < HALVES; ++d)
-                    tma_rows(dst + (p0 + p) * a.box * 128 + d * kHalf, map, d * 64, s0, pc.h, pg[p], &full[slot]);
+                for (int p = 0; p < 8; ++p) {
+                  if (p0 + p < boxes) {
+#pragma unroll
+                    for (int d = 0; d < HALVES; ++d)
+                      tma_rows(dst + (p0 + p) * a.box * 128 + d * kHalf, map, d * 64, s0, pc.h, pg[p], &full[slot]);
+                  }
                 }
               }
             }
@@ -1176,7 +1268,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else if (warp == 1) {
     // ---- scores (the warp runs as one; one lane issues) ----
     const uint32_t iqk = instr<T>(a.ncj, false, false);
-    const uint64_t kd0 = operand(sptr(ring), 16, 1024), qd0 = operand(sptr(Q), 16, 1024);
+    const uint32_t khalf = a.half / 16;
+    const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
     const uint32_t qhalf = a.cols * 8;
     const int halves = a.two ? 2 : 1;
     Pieces pc;
@@ -1208,7 +1301,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              tc_mma(d, kd + (k / 4) * (kHalf / 16) + (k & 3) * 2, q + (k / 4) * qhalf + (k & 3) * 2, iqk, k > 0);
+              tc_mma(d, kd + (k / 4) * khalf + (k & 3) * 2, q + (k / 4) * qhalf + (k & 3) * 2, iqk, k > 0);
             tc_commit(&sm.sfull[w]);
             if (hf == halves - 1) tc_commit(&sm.kempty[slot]);
           }
@@ -1222,7 +1315,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else if (warp == 3) {
     // ---- values ----
     const uint32_t ipv = instr<T>(a.ncj, true, true);
-    const uint64_t vd0 = operand(sptr(ringv), D == 128 ? kHalf : 0, 1024), pd0 = operand(sptr(P), kHalf, 1024);
+    const uint32_t vstep = a.group / 8;  // 16 slots
+    const uint64_t vd0 = operand(sptr(ringv), D == 128 ? a.half : 0, a.group), pd0 = operand(sptr(P), kPBlock, 512, 4);
     const int halves = a.two ? 2 : 1;
     Pieces pc;
     pc.start(sm);
@@ -1249,7 +1343,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + 2 * kMaxJob + wu * kMaxJob;
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * 128, pd + k * 128, ipv, add || k > 0);
+            for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * vstep, pd + k * 64, ipv, add || k > 0);
             tc_commit(&sm.pvdone[w]);
             if (hf == halves - 1) tc_commit(&sm.vempty[slot]);
           }
@@ -1305,10 +1399,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x + 1;
   pdl_wait();
-  const Range me = a.ranges[c], before = a.ranges[c - 1];
+  const Range me = a.ranges[c];
   if (!me.used || me.t0 == 0) return;
   const long long s = me.lo - me.t0, e = s + me.T;
-  if (before.lo > s) return;  // an earlier range's item
+  int pk = c - 1;  // the range before, which holds the item's tile t0 - 1
+  while (pk > 0 && !a.ranges[pk].used) --pk;
+  const long long before = a.ranges[pk].lo;
+  if (before > s) return;  // an earlier range's item
   const int r0 = me.rb * a.rows_per_block, rows = min(a.rows_per_block, a.R - r0);
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   if (r >= rows) return;
@@ -1321,19 +1418,20 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
   const bool there =
       node_way(a.nodes.parent ? a.nodes.parent + static_cast<long long>(me.b) * a.nodes.N : nullptr, tot - ctx, i,
                mask, depth, broken);
-  // part k is that of range c - 1 + k; only the first can be its CTA's last
-  const long long first = (2ll * (c - 1) + (before.lo < s ? 1 : 0)) * a.cols + r;
-  const long long others = 2ll * (c - 1) * a.cols + r;
+  // the part of range pk + k; only the first can be its CTA's last
+  auto part = [&](int k) { return (2ll * (pk + k) + (k == 0 && before < s ? 1 : 0)) * a.cols + r; };
   float M = kNoScore, L = 0.f, o[E];
 #pragma unroll
   for (int q = 0; q < E; ++q) o[q] = 0.f;
 #pragma unroll 1
   for (int k0 = 0;; k0 += 32) {
-    const int k = k0 + lane, at = c - 1 + k;
-    const bool in = at < C && (k == 0 || (a.ranges[at].used && a.ranges[at].lo < e));
-    const int n = __popc(__ballot_sync(0xffffffffu, in));
-    if (n == 0) break;
-    const float2 ml = in ? a.part_ml[k == 0 ? first : others + 2ll * k * a.cols] : make_float2(kNoScore, 0.f);
+    const int k = k0 + lane, at = pk + k;
+    bool in = k == 0, past = at >= C;
+    if (!in && !past && a.ranges[at].used) {
+      in = a.ranges[at].lo < e;
+      past = !in;
+    }
+    const float2 ml = in ? a.part_ml[part(k)] : make_float2(kNoScore, 0.f);
     float m = ml.x;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -1347,10 +1445,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
     M = Mn;
 #pragma unroll
     for (int q = 0; q < E; ++q) o[q] *= old;
+    const unsigned parts = __ballot_sync(0xffffffffu, in);
+    const int n = parts ? 32 - __clz(parts) : 0;
 #pragma unroll 4
     for (int t = 0; t < n; ++t) {
       const float wt = __shfl_sync(0xffffffffu, w, t);
-      const float* src = a.part_o + (k0 + t == 0 ? first : others + 2ll * (k0 + t) * a.cols) * D + lane * E;
+      if (!((parts >> t) & 1)) continue;
+      const float* src = a.part_o + part(k0 + t) * D + lane * E;
 #pragma unroll
       for (int q = 0; q < E; q += 2) {
         const float2 v = *reinterpret_cast<const float2*>(src + q);
@@ -1358,7 +1459,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
         o[q + 1] = fmaf(wt, v.y, o[q + 1]);
       }
     }
-    if (n < 32) break;
+    if (__any_sync(0xffffffffu, past)) break;
   }
   const bool empty = !there || L == 0.f;
   const float inv = empty ? 0.f : 1.f / L;
@@ -1390,10 +1491,14 @@ EncodeFn encode_fn() {
   return fn;
 }
 
+CUtensorMapDataType map_type(int dtype) {
+  return dtype == Bf16::kId ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+}
+
 // {D, page_size, Hkv, pages}; boxes of 64 columns and `box` slots of one head
 // of one page.
-bool encode(CUtensorMap* m, void* base, int dtype, int D, int ps, int H, int pages, long long slot,
-            long long head, long long page, int box) {
+bool encode_rows(CUtensorMap* m, void* base, int dtype, int D, int ps, int H, int pages, long long slot,
+                 long long head, long long page, int box) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(ps),
@@ -1402,9 +1507,35 @@ bool encode(CUtensorMap* m, void* base, int dtype, int D, int ps, int H, int pag
                                  static_cast<cuuint64_t>(page) * 2};
   const cuuint32_t bx[4] = {64, static_cast<cuuint32_t>(box), 1, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn(m, dtype == Bf16::kId ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
-            dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(m, map_type(dtype), 4, base, dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Groups of 8 slots a page apart, where the cache's strides make the slots of
+// all pages one sequence of such groups; 0 where they don't, or where a tile
+// could run over a page's end.
+long long page_groups(int ps, int pages, long long slot, long long page) {
+  if (ps % 8 != 0 || (ps > kTile && ps % kTile != 0) || (ps < kTile && kTile % ps != 0)) return 0;
+  if (page % (8 * slot) != 0) return 0;
+  const long long g = page / (8 * slot);
+  return g >= ps / 8 && g * (pages + 1ll) < (1ll << 31) ? g : 0;
+}
+
+// {64, 8 slots, 2 halves, groups, Hkv}; boxes of `box` slots.
+bool encode_groups(CUtensorMap* m, void* base, int dtype, int ps, int H, int pages, long long slot, long long head,
+                   long long groups, int box) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[5] = {64, 8, 2, static_cast<cuuint64_t>(groups * (pages - 1) + ps / 8),
+                              static_cast<cuuint64_t>(H)};
+  const cuuint64_t strides[4] = {static_cast<cuuint64_t>(slot) * 2, 128, static_cast<cuuint64_t>(slot) * 16,
+                                 static_cast<cuuint64_t>(head) * 2};
+  const cuuint32_t bx[5] = {64, 8, 2, static_cast<cuuint32_t>(box / 8), 1};
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return fn(m, map_type(dtype), 5, base, dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 struct Shape {
@@ -1513,7 +1644,7 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
     a.ragged = a.ps % kTile != 0;
   }
   const int slot = D * 2 * kTile;
-  const size_t qb = static_cast<size_t>(a.cols) * D * 2, pb = ((a.ncj + 63) / 64) * static_cast<size_t>(kHalf);
+  const size_t qb = static_cast<size_t>(a.cols) * D * 2, pb = ((a.ncj + 31) / 32) * static_cast<size_t>(kPBlock);
   const size_t fixed = (a.two ? 1 : 2) * qb + 2 * pb + sizeof(Misc);
   int slots = static_cast<int>((kSmemMax - fixed) / slot);
   if (slots > 2 * kMaxRing) slots = 2 * kMaxRing;
@@ -1522,9 +1653,21 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   a.nv = slots - a.nk;
   const size_t smem = fixed + static_cast<size_t>(slots) * slot;
   CUtensorMap mk, mv;
-  if (!encode(&mk, p.kv.k, dtype, D, a.ps, a.Hkv, a.pages, p.kv.k_slot, p.kv.k_head, p.kv.k_page, a.box) ||
-      !encode(&mv, p.kv.v, dtype, D, a.ps, a.Hkv, a.pages, p.kv.v_slot, p.kv.v_head, p.kv.v_page, a.box))
-    return cudaErrorInvalidValue;
+  const KvView& kv = p.kv;
+  const long long gk = page_groups(a.ps, a.pages, kv.k_slot, kv.k_page);
+  const long long gv = page_groups(a.ps, a.pages, kv.v_slot, kv.v_page);
+  // One copy per page brings both halves of D = 128 (two copies of 2 KB of a
+  // page of 16 took the loader 80 cycles each, more than the copies' share of
+  // the memory's time).
+  a.fold = D == 128 && gk == gv ? static_cast<int>(gk) : 0;
+  a.group = a.fold ? 2048 : 1024;
+  a.half = a.fold ? 1024 : kHalf;
+  const bool ok =
+      a.fold ? encode_groups(&mk, kv.k, dtype, a.ps, a.Hkv, a.pages, kv.k_slot, kv.k_head, gk, a.box) &&
+                   encode_groups(&mv, kv.v, dtype, a.ps, a.Hkv, a.pages, kv.v_slot, kv.v_head, gv, a.box)
+             : encode_rows(&mk, kv.k, dtype, D, a.ps, a.Hkv, a.pages, kv.k_slot, kv.k_head, kv.k_page, a.box) &&
+                   encode_rows(&mv, kv.v, dtype, D, a.ps, a.Hkv, a.pages, kv.v_slot, kv.v_head, kv.v_page, a.box);
+  if (!ok) return cudaErrorInvalidValue;
   int C = sm_count();
   if (C < 1) return cudaErrorInvalidDevice;
   C = C < kMaxCtas ? C : kMaxCtas;
