@@ -23,18 +23,20 @@
 //          bounds, which TMA fills with zeros)
 //   1, 3   issue tcgen05.mma: S^T (K, Q from shared memory), and O^T (V^T read
 //          transposed from the same row-major tile, P^T from shared memory)
-//   4..11  two warpgroups for the softmax, which also fetch the rows of Q,
+//   4..15  three warpgroups for the softmax, which also fetch the rows of Q,
 //          clear what must not be multiplied in tiles that hold drafted nodes
 //          (V rows behind the sequence's end; NaN or infinite entries of
 //          nodes, which are added at the end for the rows that see them) and
-//          write the results.  Up to 64 rows: the warpgroups take alternate
-//          tiles and keep their own m, l, O; more: the same tiles, half of
-//          the rows each.
+//          write the results.  Up to 64 rows: the warpgroups take tiles in
+//          turn and keep their own m, l, O; more: the same tiles, a third of
+//          the rows each.  (Two warpgroups with half of the rows each left
+//          the pass over the scores waiting for its own latencies: 96 rows a
+//          tile took 1680 cycles, three times 64 take 1200.)
 //
-// m follows the running maximum lazily: P, l and the largest excess over m come
-// out of one pass over the scores, and only where that exceeds 2^30 (2^8 for
-// fp16, whose range is short) the warpgroup finds the tile's row maxima,
-// rescales l and O and repeats the pass.  P keeps its relative precision at
+// m follows the running maximum lazily: P and l come out of one pass over the
+// scores, and only where a row's l grew by more than 2^30 (2^8 for fp16, whose
+// range is short) the warpgroup finds the tile's row maxima, rescales l and O
+// and repeats the pass.  P keeps its relative precision at
 // any excess, l and O their 32-bit range.
 #include <cuda.h>
 #include <math.h>
@@ -45,14 +47,18 @@
 namespace ssd {
 namespace {
 
-constexpr int kAttnThreads = 384;
+constexpr int kGroups = 3;           // warpgroups of the softmax
+constexpr int kSoft = 128 * kGroups; // their threads
+constexpr int kAttnThreads = 128 + kSoft;
 constexpr int kTile = 128;           // slots of a tile (rows of the ring's tiles)
 constexpr int kHalf = kTile * 128;   // bytes of a tile's 64-column half
-constexpr int kPBlock = kTile * 64;  // bytes of P of 32 rows
+constexpr int kPBlock = kTile * 32;  // bytes of P of 16 rows
+constexpr int kPMin = 8192;          // least bytes of a warpgroup's P buffer
 constexpr int kMaxRing = 4;           // slots of each ring
 constexpr int kMaxRows = 256;        // rows of a row block
 constexpr int kAlternate = 64;       // most rows whose tiles the warpgroups take in turn
-constexpr int kMaxJob = 128;         // rows of a job (one warpgroup's columns)
+constexpr int kMaxJob = 96;          // most rows of a warpgroup
+constexpr int kTailBars = 8;
 constexpr int kMaxCtas = 160;
 constexpr int kNoRow = 0x7fffffff;   // a column without a row (rows of zeros: ~row)
 constexpr int kItemCost = 4;         // what an item's start and end cost, in tiles
@@ -73,8 +79,10 @@ struct Args {
   int width, pages, ps;
   int Hq, Hkv, G, R;
   int RB, rows_per_block;   // row blocks of a key/value head
-  int two;                  // the warpgroups split the rows
-  int ncj, cols;            // columns of a job; of Q (ncj or 2 ncj)
+  int split;                // the warpgroups split the rows
+  int cols;                 // columns of S^T: the rows, rounded up to 16
+  int wcols[kGroups], off[kGroups];  // a warpgroup's columns
+  int poff[kGroups], pbytes;         // its P buffer; all of them
   int nk, nv;               // slots of the K and V rings
   int box, ppt, tk, tpp;    // rows of a TMA box, pages a tile, slots a tile, tiles a page
   int ragged;               // tiles have rows that are no slot
@@ -98,10 +106,10 @@ struct Args {
 // Shared memory behind the ring, Q and P (256 rows leave 3 KB for it).
 struct alignas(16) Misc {
   uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
-  uint64_t qfull[2], sfull[2], pfull[2], pvdone[2], done;
+  uint64_t qfull[2], sfull[kGroups], pfull[kGroups], pvdone[kGroups], vready[kTailBars], done;
   uint64_t anc[2][kMaxNodes + 1];   // nodes' ancestors (0: absent); the last: no row
   long long left;
-  alignas(16) float nm[2][kMaxJob]; // -m
+  alignas(16) float nm[kMaxRows];   // -m, of each warpgroup's columns
   uint8_t node[2][kMaxRows];        // rows' nodes
   unsigned nf[2][2];                // nodes with NaN or infinite values
   int b0, h0, rb0, t0;              // first piece, its sequence's
@@ -125,7 +133,7 @@ struct Scratch {
     char stage[4][1024];    // results on their way out, a part per warp
   };
 };
-static_assert(sizeof(Scratch) <= kPBlock, "the smallest P buffer");
+static_assert(sizeof(Scratch) <= kPMin, "the smallest P buffer");
 
 // ---------------------------------------------------------------------------
 // mbarriers, TMA, tcgen05
@@ -243,7 +251,7 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 
 // Shared-memory operand descriptor: strides in bytes; swizzle 2: 128 bytes,
-// 4: 64 bytes.
+// 6: 32 bytes.
 __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride, uint64_t swizzle = 2) {
   return static_cast<uint64_t>((addr >> 4) & 0x3fff) | (static_cast<uint64_t>(lead >> 4) << 16) |
          (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (swizzle << 61);
@@ -494,16 +502,15 @@ __device__ __forceinline__ void st_matrices_t(uint32_t at, const uint32_t (&w)[4
                "r"(w[1]), "r"(w[2]), "r"(w[3]));
 }
 
-// P^T of the tile into shared memory (rows contiguous, 32 of them and 128
-// slots a block, 64-byte swizzle), l += P; returns the largest excess over m.
-// prow: this lane's slot's line of the first block.  The matrices of 16 rows
-// are stored while the next rows' exponentials are on their way.
-template <class T, int NC>
-__device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const float* nm, int x2, uint32_t prow,
-                                           int slot, f32x2 (&l)[NC / 8]) {
-  float ex[2] = {-INFINITY, -INFINITY};
+// P^T of the tile into shared memory (rows contiguous, 16 of them and 128
+// slots a block, 32-byte swizzle), l += P.  prow: this lane's slot's line of
+// the first block.  The matrices of 16 rows are stored while the next rows'
+// exponentials are on their way; `ready` is called before the first store.
+template <class T, int NC, class Ready>
+__device__ __forceinline__ void tile_pass(uint32_t tS, int nch, f32x2 c2, const float* nm, int x2, uint32_t prow,
+                                          int slot, f32x2 (&l)[NC / 8], Ready&& ready) {
   uint32_t s[2][16], w[2][4];
-  const uint32_t sw = (slot >> 1) & 3;
+  const uint32_t a0 = prow + (((slot >> 2) & 1) << 4), a1 = a0 ^ 16;
   tm_ld_frag(tS, s[0]);
   const float* m = nm + x2;
   f32x2 m0 = *reinterpret_cast<const f32x2*>(m), m1 = *reinterpret_cast<const f32x2*>(m + 8);
@@ -526,16 +533,16 @@ __device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const
           const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
           float t0, t1;
           up2(fma2(pk2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, g ? m1 : m0), t0, t1);
-          ex[q & 1] = max3(ex[q & 1], t0, t1);
           const float e0 = ex2_fast(t0), e1 = ex2_fast(t1);
           l[k * 2 + g] = add2(l[k * 2 + g], pk2(e0, e1));
           v[g][q] = T::pack(e0, e1);
         }
       }
       if (k > 0) {
-        const uint32_t line = prow + ((k - 1) / 2) * kPBlock;
-        st_matrices(line + (((((k - 1) & 1) * 2) ^ sw) << 4), w[0]);
-        st_matrices(line + (((((k - 1) & 1) * 2 + 1) ^ sw) << 4), w[1]);
+        st_matrices(a0 + (k - 1) * kPBlock, w[0]);
+        st_matrices(a1 + (k - 1) * kPBlock, w[1]);
+      } else {
+        ready();
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -546,11 +553,21 @@ __device__ __forceinline__ float tile_pass(uint32_t tS, int nch, f32x2 c2, const
       m1 = n1;
     }
   }
-  const int k = nch - 1;
-  const uint32_t line = prow + (k / 2) * kPBlock;
-  st_matrices(line + ((((k & 1) * 2) ^ sw) << 4), w[0]);
-  st_matrices(line + ((((k & 1) * 2 + 1) ^ sw) << 4), w[1]);
-  return fmaxf(ex[0], ex[1]);
+  st_matrices(a0 + (nch - 1) * kPBlock, w[0]);
+  st_matrices(a1 + (nch - 1) * kPBlock, w[1]);
+}
+
+// The largest growth of a row sum.
+template <int N>
+__device__ __forceinline__ float growth(const f32x2 (&l)[N], const f32x2 (&old)[N]) {
+  float ex = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float a, b;
+    up2(sub2(l[i], old[i]), a, b);
+    ex = max3(ex, a, b);
+  }
+  return ex;
 }
 
 // Joins v over the eight lanes that hold the same rows, each lane giving half
@@ -562,12 +579,12 @@ __device__ __forceinline__ void join_rows(float (&v)[NC / 4], float* red, int la
 #pragma unroll
   for (int d = 16; d >= 4; d >>= 1) {
     const bool up = lane & d;
-    if (n > 1) {
+    if (n % 2 == 0) {
       n >>= 1;
       if (up) base += n;
 #pragma unroll
       for (int i = 0; i < NC / 8; ++i) {
-        if (i < 2 * n) {
+        if (i < 2 * n && i + 2 * n < NC / 4) {
           const float give = up ? v[i] : v[i + 2 * n];
           const float mine = up ? v[i + 2 * n] : v[i];
           const float got = __shfl_xor_sync(0xffffffffu, give, d);
@@ -576,9 +593,11 @@ __device__ __forceinline__ void join_rows(float (&v)[NC / 4], float* red, int la
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float got = __shfl_xor_sync(0xffffffffu, v[i], d);
-        v[i] = MAX ? fmaxf(v[i], got) : v[i] + got;
+      for (int i = 0; i < NC / 4; ++i) {
+        if (i < 2 * n) {
+          const float got = __shfl_xor_sync(0xffffffffu, v[i], d);
+          v[i] = MAX ? fmaxf(v[i], got) : v[i] + got;
+        }
       }
     }
   }
@@ -661,15 +680,15 @@ __device__ __noinline__ void add_nonfinite(const Args& a, int b, int h, int ctx,
   }
 }
 
-// The nodes of a piece's rows and the nodes' masks (by all 256 threads of the
+// The nodes of a piece's rows and the nodes' masks (by all threads of the
 // warpgroups).
 __device__ __noinline__ void row_tables(const Args& a, Misc& sm, int b, int rb, int n, int tb) {
   const int at = threadIdx.x - 128;
   const int r0 = rb * a.rows_per_block;
   const int rows = min(a.rows_per_block, a.R - r0);
   if (at < a.cols) sm.node[tb][at] = static_cast<uint8_t>(at < rows ? (r0 + at) / a.G : kMaxNodes);
-  if (at >= 192) {
-    const int j = at - 192;
+  if (at >= kMaxRows && at < kMaxRows + kMaxNodes) {
+    const int j = at - kMaxRows;
     const int* parent = a.nodes.parent ? a.nodes.parent + static_cast<long long>(b) * a.nodes.N : nullptr;
     uint64_t m = 0;
     int depth;
@@ -761,42 +780,40 @@ __device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx,
 
 template <class T, int D, int NC>
 __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* Q, int qbytes, char* V,
-                                             char* P0, int pbytes, int wg) {
-  constexpr float kSlack = T::kId == Bf16::kId ? 30.f : 8.f;
-  char* P = P0 + wg * pbytes;
-  Scratch& sc0 = *reinterpret_cast<Scratch*>(P0);
-  Scratch& sc1 = *reinterpret_cast<Scratch*>(P0 + pbytes);
-  Scratch& sc = wg == 0 ? sc0 : sc1;
+                                             char* P0, int wg) {
+  constexpr float kGrow = T::kId == Bf16::kId ? 1073741824.f : 256.f;
+  const bool split = a.split;
+  char* P = P0 + a.poff[wg];
+  Scratch& sc = *reinterpret_cast<Scratch*>(P);
   const int wt = threadIdx.x - 128 - wg * 128;  // thread of the warpgroup = TMEM lane
   const int warp = wt >> 5, lane = wt & 31;
   const int x2 = (lane & 3) * 2;  // first of the thread's rows in a group of 8
+  const int ncj = a.wcols[wg], nch = ncj / 16, colbase = a.off[wg];
+  const int tcol = split ? colbase : wg * kAlternate;  // its columns of TMEM and of nm
   const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t tS = tmem + lane_base + wg * kMaxJob;
-  const uint32_t tO0 = tmem + lane_base + 2 * kMaxJob;
-  const uint32_t tO = tO0 + wg * kMaxJob;
-  const uint32_t prow = sptr(P) + wt * 64;
-  const int ncj = a.ncj, nch = ncj / 16;
+  const uint32_t tS = tmem + lane_base + tcol;
+  const uint32_t tO0 = tmem + lane_base + kMaxRows;
+  const uint32_t tO = tO0 + tcol;
+  const uint32_t prow = sptr(P) + wt * 32;
   const f32x2 c2 = pk2(a.c, a.c);
-  float* nm = sm.nm[wg];
+  float* nm = sm.nm + tcol;
   const int bar = 1 + wg;
-  const bool two = a.two;
-  const int colbase = two ? wg * ncj : 0;
   const float none = a.c < 0.f ? INFINITY : -INFINITY;
   uint32_t ps = 0, ppv = 0;  // phases of sfull, pvdone
   int item_no = 0;
   const int at = threadIdx.x - 128;
-  int g0 = 0;  // tiles before this piece
-  Pieces pn;   // one piece ahead
+  int g0 = 0, tails0 = 0;  // tiles (with drafted nodes) before this piece
+  Pieces pn;               // one piece ahead
   pn.start(sm);
   bool more = pn.next(a);
   if (more) {
-    fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, 0, a.cols, at, 256);
+    fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, 0, a.cols, at, kSoft);
     row_tables(a, sm, pn.b, pn.rb, pn.tot - pn.ctx, 0);
     rows_ready(sm, 0);
   }
   while (more) {
     const int b = pn.b, h = pn.h, t0 = pn.t0, end = pn.end, ctx = pn.ctx, tot = pn.tot;
-    const int tail = a.ragged ? 0 : pn.tail;
+    const int tail = max(pn.tail, t0), mask_from = a.ragged ? 0 : tail;
     const bool direct = pn.direct();
     const int r0 = pn.rb * a.rows_per_block + colbase;
     const int rows = min(a.rows_per_block - colbase, a.R - r0);  // of this job's columns
@@ -804,12 +821,12 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     more = pn.next(a);
     // The next piece's tables and rows, while this piece's first product
     // runs: the rows go into the other buffer, or (one buffer) later into
-    // this warpgroup's half, once its last scores are there.
+    // this warpgroup's part, once its last scores are there.
     bool todo = more, pending = false;
     auto prefetch = [&]() {
       row_tables(a, sm, pn.b, pn.rb, pn.tot - pn.ctx, tb ^ 1);
-      if (!two) {
-        fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q + (tb ^ 1) * qbytes, 0, a.cols, at, 256);
+      if (!split) {
+        fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q + (tb ^ 1) * qbytes, 0, a.cols, at, kSoft);
         pending = true;
       }
       todo = false;
@@ -820,19 +837,25 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     f32x2 l[NC / 8];
 #pragma unroll
     for (int i = 0; i < NC / 8; ++i) l[i] = 0ull;
-    named_sync(3, 256);
+    named_sync(kGroups + 1, kSoft);
     int jobs = 0;
-    const int step = two ? 1 : 2;
+    const int turn = split ? 0 : (wg + kGroups - g0 % kGroups) % kGroups, step = split ? 1 : kGroups;
 #pragma unroll 1
-    for (int t = t0 + (two ? 0 : (g0 + wg) & 1); t < end; t += step) {
+    for (int t = t0 + turn; t < end; t += step) {
       bar_wait(&sm.sfull[wg], ps, sm, a.err);
       ps ^= 1;
-      if (jobs > 0) {  // the last tile's product: P may be written, O rescaled
-        bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
-        ppv ^= 1;
-      }
+      bool fresh = jobs > 0;  // the last tile's product is to be waited for
+      auto ready = [&]() {
+        if (fresh) {
+          bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
+          ppv ^= 1;
+          fresh = false;
+          tc_after();
+        }
+      };
       tc_after();
-      if (t >= tail) {
+      if (t >= mask_from) {
+        ready();
         if (wt < ncj) {
           const uint64_t m = anc[node[wt]];
           sc.seen[wt] = make_uint4(~0u, static_cast<uint32_t>(m), static_cast<uint32_t>(m >> 32), 0u);
@@ -846,6 +869,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 #pragma unroll 1
       while (true) {
         if (raise) {
+          ready();
           tile_maxima<NC>(tS, ncj, a.c, sc.red[warp]);
           named_sync(bar, 128);
           if (wt < ncj) {
@@ -867,16 +891,16 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         f32x2 old[NC / 8];
 #pragma unroll
         for (int i = 0; i < NC / 8; ++i) old[i] = l[i];
-        const float ex = tile_pass<T, NC>(tS, nch, c2, nm, x2, prow, wt, l);
-        if (!named_or(bar, 128, ex > kSlack)) break;
+        tile_pass<T, NC>(tS, nch, c2, nm, x2, prow, wt, l, ready);
+        if (!named_or(bar, 128, growth(l, old) > kGrow)) break;
         raise = true;
 #pragma unroll
         for (int i = 0; i < NC / 8; ++i) l[i] = old[i];
       }
-      if (t >= tail && (!two || wg == 0)) {
-        const int g = g0 + t - t0;
-        bar_wait(&sm.vfull[g % a.nv], (g / a.nv) & 1, sm, a.err);
-        clean_tile<T, D>(a, sm, t, ctx, tot, V + (g % a.nv) * (kTile * D * 2), tb, wt);
+      if (t >= tail && (!split || wg == 0)) {
+        const int n = tails0 + t - tail, slot = (g0 + t - t0) % a.nv;
+        bar_wait(&sm.vready[n % kTailBars], (n / kTailBars) & 1, sm, a.err);
+        clean_tile<T, D>(a, sm, t, ctx, tot, V + slot * (kTile * D * 2), tb, wt);
       }
       tc_before();
       fence_async();
@@ -892,7 +916,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     // ---- end of the piece: l over the slots, then O ----
     if (todo) prefetch();
     if (pending) rows_ready(sm, tb ^ 1);
-    if (two && more) fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, colbase, colbase + ncj, wt, 128);
+    if (split && more) fetch_rows<D>(a, pn.b, pn.h, pn.rb, pn.tot - pn.ctx, Q, colbase, colbase + ncj, wt, 128);
     if (jobs > 0) {
       bar_wait(&sm.pvdone[wg], ppv, sm, a.err);
       ppv ^= 1;
@@ -904,25 +928,35 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       for (int i = 0; i < NC / 8; ++i) up2(l[i], v[2 * i], v[2 * i + 1]);
       join_rows<NC, false>(v, sc.red[warp], lane, ncj);
     }
-    if (two) named_sync(bar, 128);
-    else named_sync(3, 256);
+    if (split) named_sync(bar, 128);
+    else named_sync(kGroups + 1, kSoft);
     const int tiles = end - t0;
-    // alternate tiles: which warpgroups took part
-    const bool used0 = two ? wg == 0 : tiles > 1 || (g0 & 1) == 0;
-    const bool used1 = two ? wg == 1 : tiles > 1 || (g0 & 1) == 1;
     const long long pslot = (2ll * blockIdx.x + (item_no == 0 ? 0 : 1)) * a.cols + colbase;
     const long long orow = static_cast<long long>(b) * a.nodes.N * a.Hq + h * a.G;
-    Scratch& so = two ? sc : sc0;
-    if (wt < ncj && (two || wg == 0)) {
+    // tiles in turn: the warpgroups that took part, of which each writes a
+    // share of the rows
+    const int w0 = split ? wg : 0, w1 = split ? wg + 1 : kGroups;
+    auto used = [&](int w) { return split || (w + kGroups - g0 % kGroups) % kGroups < tiles; };
+    auto scratch = [&](int w) -> Scratch& { return *reinterpret_cast<Scratch*>(P0 + a.poff[w]); };
+    Scratch& so = scratch(w0);
+    if (wt < ncj && wg == w0) {
       // factors of the warpgroups' O, and where the rows go
       const int cc = wt;
-      const float m0 = used0 ? -sm.nm[0][cc] : kNoScore, m1 = used1 ? -sm.nm[1][cc] : kNoScore;
-      const float M = fmaxf(m0, m1);
-      float w0 = used0 ? (m0 == M ? 1.f : exp2f(m0 - M)) : 0.f;
-      float w1 = used1 ? (m1 == M ? 1.f : exp2f(m1 - M)) : 0.f;
-      float L = 0.f;
-      if (used0) L += w0 * ((sc0.red[0][cc] + sc0.red[1][cc]) + (sc0.red[2][cc] + sc0.red[3][cc]));
-      if (used1) L += w1 * ((sc1.red[0][cc] + sc1.red[1][cc]) + (sc1.red[2][cc] + sc1.red[3][cc]));
+      float M = kNoScore, L = 0.f;
+#pragma unroll 1
+      for (int w = w0; w < w1; ++w)
+        if (used(w)) M = fmaxf(M, -sm.nm[(split ? tcol : w * kAlternate) + cc]);
+#pragma unroll 1
+      for (int w = w0; w < w1; ++w) {
+        Scratch& x = scratch(w);
+        float f = 0.f;
+        if (used(w)) {
+          const float m = -sm.nm[(split ? tcol : w * kAlternate) + cc];
+          f = m == M ? 1.f : exp2f(m - M);
+          L += f * ((x.red[0][cc] + x.red[1][cc]) + (x.red[2][cc] + x.red[3][cc]));
+        }
+        x.fac[cc] = f;
+      }
       int row = kNoRow;
       if (cc < rows) {
         const int i = (r0 + cc) / a.G;
@@ -930,8 +964,8 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         const bool absent = anc[node[cc]] == 0, empty = absent || L == 0.f;
         if (direct) {
           const float inv = empty ? 0.f : 1.f / L;
-          w0 *= inv;
-          w1 *= inv;
+#pragma unroll 1
+          for (int w = w0; w < w1; ++w) scratch(w).fac[cc] *= inv;
           if (a.lse) a.lse[orow + row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
           if (empty) row = ~row;
         } else {
@@ -939,52 +973,44 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         }
       }
       so.row[cc] = row;
-      if (two) {
-        so.fac[cc] = w0 + w1;
-      } else {
-        sc0.fac[cc] = w0;
-        sc1.fac[cc] = w1;
-      }
     }
-    if (two) named_sync(bar, 128);
-    else named_sync(3, 256);
+    if (split) named_sync(bar, 128);
+    else named_sync(kGroups + 1, kSoft);
     {
       // 16 rows (columns of O^T) at a time, a warp per 32 output columns;
-      // shared out over the warpgroups (alternate tiles) and, where O^T
-      // repeats itself (D = 64), over the two copies.  Finished rows go
-      // through shared memory, transposed, to 64-byte stores.
+      // shared out over the warpgroups (tiles in turn) and, where O^T repeats
+      // itself (D = 64), over the two copies.  Finished rows go through
+      // shared memory, transposed, to 64-byte stores.
       constexpr int WD = D / 32;
-      const int groups = (two ? 1 : 2) * (4 / WD), me = (two ? 0 : wg) * (4 / WD) + warp / WD;
+      const int groups = (split ? 1 : kGroups) * (4 / WD), me = (split ? 0 : wg) * (4 / WD) + warp / WD;
       const int d0 = (warp % WD) * 32;
       char* obase = a.out + 2 * orow * D + 2 * (d0 + (lane & 3) * 8);
       float* pbase = a.part_o + pslot * D + d0 + (lane >> 2);
-      const uint32_t src0 = two ? tO : tO0, src1 = tO0 + kMaxJob;
-      const bool use_a = two || used0, use_b = !two && used1;
       char* stage = sc.stage[warp];
       const uint32_t st_at = sptr(stage) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);
       const char* ld_at = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
 #pragma unroll 1
       for (int k = me * 16; k < ncj; k += groups * 16) {
-        uint32_t u[16], v[16];
-        if (use_a) tm_ld_frag(src0 + k, u);
-        if (use_b) tm_ld_frag(src1 + k, v);
-        f32x2 f[2], e[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          f[g] = *reinterpret_cast<const f32x2*>(so.fac + k + g * 8 + x2);
-          e[g] = use_b ? *reinterpret_cast<const f32x2*>(sc1.fac + k + g * 8 + x2) : 0ull;
-        }
-        if (use_a) tm_wait_ld(u);
-        if (use_b) tm_wait_ld(v);
         f32x2 o[2][4];
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < 2; ++g)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
-            f32x2 x = use_a ? mul2(pk2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), f[g]) : 0ull;
-            if (use_b) x = fma2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), e[g], x);
-            o[g][q] = x;
+          for (int q = 0; q < 4; ++q) o[g][q] = 0ull;
+#pragma unroll 1
+        for (int w = w0; w < w1; ++w) {
+          if (!used(w)) continue;
+          uint32_t u[16];
+          tm_ld_frag((split ? tO : tO0 + w * kAlternate) + k, u);
+          const float* f = scratch(w).fac + k + x2;
+          const f32x2 f0 = *reinterpret_cast<const f32x2*>(f), f1 = *reinterpret_cast<const f32x2*>(f + 8);
+          tm_wait_ld(u);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int i = (q >> 1) * 8 + g * 4 + (q & 1) * 2;
+              o[g][q] = fma2(pk2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])), g ? f1 : f0, o[g][q]);
+            }
           }
         }
         if (direct) {
@@ -1030,17 +1056,18 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       }
       const unsigned long long nf = sm.nf[tb][0] | (static_cast<unsigned long long>(sm.nf[tb][1]) << 32);
       if (nf) {
-        if (two) named_sync(bar, 128);
-        else named_sync(3, 256);
-        if (wt < D && (two || wg == 0))
+        if (split) named_sync(bar, 128);
+        else named_sync(kGroups + 1, kSoft);
+        if (wt < D && wg == w0)
           add_nonfinite<T, D>(a, b, h, ctx, nf, wt, anc, node, so.row, 0, ncj, a.out + 2 * orow * D,
                               direct ? nullptr : a.part_o + pslot * D);
       }
     }
     tc_before();
-    named_sync(3, 256);  // P and the tables may be written again
-    if (two && more) rows_ready(sm, 0);
+    named_sync(kGroups + 1, kSoft);  // P and the tables may be written again
+    if (split && more) rows_ready(sm, 0);
     g0 += tiles;
+    tails0 += max(end - tail, 0);
     ++item_no;
   }
 }
@@ -1056,9 +1083,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   char* ringv = ring + a.nk * kSlotBytes;
   char* Q = ringv + a.nv * kSlotBytes;
   const int qbytes = a.cols * D * 2;
-  char* P = Q + (a.two ? 1 : 2) * qbytes;
-  const int pbytes = ((a.ncj + 31) / 32) * kPBlock;
-  Misc& sm = *reinterpret_cast<Misc*>(P + 2 * pbytes);
+  char* P = Q + (a.split ? 1 : 2) * qbytes;
+  Misc& sm = *reinterpret_cast<Misc*>(P + a.pbytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = gridDim.x, B = a.nodes.B;
 
@@ -1069,12 +1095,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       bar_init(&sm.vfull[i], 1);
       bar_init(&sm.vempty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      bar_init(&sm.qfull[i], 256);
+    for (int i = 0; i < 2; ++i) bar_init(&sm.qfull[i], kSoft);
+    for (int i = 0; i < kGroups; ++i) {
       bar_init(&sm.sfull[i], 1);
       bar_init(&sm.pfull[i], 128);
       bar_init(&sm.pvdone[i], 1);
     }
+    for (int i = 0; i < kTailBars; ++i) bar_init(&sm.vready[i], 1);
     bar_init(&sm.done, 2);
     sm.abort = 0;
     sm.b0 = sm.h0 = sm.rb0 = sm.t0 = 0;
@@ -1267,46 +1294,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (bad_page) atomicOr(a.err, kErrBadPage);
   } else if (warp == 1) {
     // ---- scores (the warp runs as one; one lane issues) ----
-    const uint32_t iqk = instr<T>(a.ncj, false, false);
     const uint32_t khalf = a.half / 16;
     const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
     const uint32_t qhalf = a.cols * 8;
-    const int halves = a.two ? 2 : 1;
     Pieces pc;
     pc.start(sm);
-    int slot = -1, item = 0, g = 0;
-    uint32_t phase = 0;
+    int slot = -1, item = 0, turn = 0;
+    uint32_t phase = 0, done = 0;  // done: parity of each warpgroup's jobs; bit 8 + w: it has had one
 #pragma unroll 1
     while (pc.next(a)) {
-      const int qb = a.two ? 0 : item & 1;
-      bar_wait(&sm.qfull[qb], (a.two ? item : item >> 1) & 1, sm, a.err);
+      const int qb = a.split ? 0 : item & 1;
+      bar_wait(&sm.qfull[qb], (a.split ? item : item >> 1) & 1, sm, a.err);
       const uint64_t qd = qd0 + __shfl_sync(0xffffffffu, qb, 0) * (qbytes / 16);
       ++item;
 #pragma unroll 1
-      for (int t = pc.t0; t < pc.end; ++t, ++g) {
+      for (int t = pc.t0; t < pc.end; ++t) {
         if (++slot == a.nk) {
           slot = 0;
           phase ^= 1;
         }
         bar_wait(&sm.kfull[slot], phase, sm, a.err);
         const uint64_t kd = kd0 + __shfl_sync(0xffffffffu, slot, 0) * (kSlotBytes / 16);
+        const int w0 = a.split ? 0 : turn, w1 = a.split ? kGroups : turn + 1;
 #pragma unroll 1
-        for (int hf = 0; hf < halves; ++hf) {
+        for (int w = w0; w < w1; ++w) {
           // S of this warpgroup is free once it has made its P of the last one
-          const int w = a.two ? hf : g & 1, n = a.two ? g : g >> 1;
-          if (n > 0) bar_wait(&sm.pfull[w], (n - 1) & 1, sm, a.err);
+          if ((done >> (8 + w)) & 1) bar_wait(&sm.pfull[w], ((done >> w) & 1) ^ 1, sm, a.err);
+          done = (done ^ (1u << w)) | (256u << w);
           tc_after();
-          const uint64_t q = qd + hf * a.ncj * 8;
-          const uint32_t d = __shfl_sync(0xffffffffu, tmem + w * kMaxJob, 0);
+          const uint64_t q = qd + a.off[w] * 8;
+          const uint32_t d = __shfl_sync(0xffffffffu, tmem + (a.split ? a.off[w] : w * kAlternate), 0);
+          const uint32_t id = instr<T>(a.wcols[w], false, false);
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-              tc_mma(d, kd + (k / 4) * khalf + (k & 3) * 2, q + (k / 4) * qhalf + (k & 3) * 2, iqk, k > 0);
+              tc_mma(d, kd + (k / 4) * khalf + (k & 3) * 2, q + (k / 4) * qhalf + (k & 3) * 2, id, k > 0);
             tc_commit(&sm.sfull[w]);
-            if (hf == halves - 1) tc_commit(&sm.kempty[slot]);
+            if (w == w1 - 1) tc_commit(&sm.kempty[slot]);
           }
           __syncwarp();
         }
+        if (++turn == kGroups) turn = 0;
       }
     }
     if (elect_one()) tc_commit(&sm.done);
@@ -1314,41 +1342,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bar_wait(&sm.done, 0, sm, a.err);
   } else if (warp == 3) {
     // ---- values ----
-    const uint32_t ipv = instr<T>(a.ncj, true, true);
     const uint32_t vstep = a.group / 8;  // 16 slots
-    const uint64_t vd0 = operand(sptr(ringv), D == 128 ? a.half : 0, a.group), pd0 = operand(sptr(P), kPBlock, 512, 4);
-    const int halves = a.two ? 2 : 1;
+    const uint64_t vd0 = operand(sptr(ringv), D == 128 ? a.half : 0, a.group), pd0 = operand(sptr(P), kPBlock, 256, 6);
     Pieces pc;
     pc.start(sm);
-    int slot = -1, g = 0;
-    uint32_t phase = 0;
+    int slot = -1, turn = 0, tails = 0;
+    uint32_t phase = 0, ppf = 0;
 #pragma unroll 1
     while (pc.next(a)) {
 #pragma unroll 1
-      for (int t = pc.t0; t < pc.end; ++t, ++g) {
+      for (int t = pc.t0; t < pc.end; ++t) {
         if (++slot == a.nv) {
           slot = 0;
           phase ^= 1;
         }
         bar_wait(&sm.vfull[slot], phase, sm, a.err);
+        if (t >= pc.tail) {  // for the warpgroup that clears what must not be multiplied
+          if (lane == 0) bar_arrive(&sm.vready[tails % kTailBars]);
+          ++tails;
+        }
         const uint64_t vd = vd0 + __shfl_sync(0xffffffffu, slot, 0) * (kSlotBytes / 16);
-        const bool add = t - pc.t0 >= (a.two ? 1 : 2);  // not the warpgroup's first tile of the piece
+        const bool add = t - pc.t0 >= (a.split ? 1 : kGroups);  // not the warpgroup's first tile of the piece
+        const int w0 = a.split ? 0 : turn, w1 = a.split ? kGroups : turn + 1;
 #pragma unroll 1
-        for (int hf = 0; hf < halves; ++hf) {
-          const int w = a.two ? hf : g & 1, n = a.two ? g : g >> 1;
-          bar_wait(&sm.pfull[w], n & 1, sm, a.err);
+        for (int w = w0; w < w1; ++w) {
+          bar_wait(&sm.pfull[w], (ppf >> w) & 1, sm, a.err);
+          ppf ^= 1u << w;
           tc_after();
-          const int wu = __shfl_sync(0xffffffffu, w, 0);
-          const uint64_t pd = pd0 + wu * (pbytes / 16);
-          const uint32_t d = __shfl_sync(0xffffffffu, tmem, 0) + 2 * kMaxJob + wu * kMaxJob;
+          const uint64_t pd = pd0 + a.poff[w] / 16;
+          const uint32_t d =
+              __shfl_sync(0xffffffffu, tmem + kMaxRows + (a.split ? a.off[w] : w * kAlternate), 0);
+          const uint32_t id = instr<T>(a.wcols[w], true, true);
           if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * vstep, pd + k * 64, ipv, add || k > 0);
+            for (int k = 0; k < kTile / 16; ++k) tc_mma(d, vd + k * vstep, pd + k * 32, id, add || k > 0);
             tc_commit(&sm.pvdone[w]);
-            if (hf == halves - 1) tc_commit(&sm.vempty[slot]);
+            if (w == w1 - 1) tc_commit(&sm.vempty[slot]);
           }
           __syncwarp();
         }
+        if (++turn == kGroups) turn = 0;
       }
     }
     if (elect_one()) tc_commit(&sm.done);
@@ -1368,7 +1401,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   } else {
     const int wg = (warp - 4) >> 2;
-    softmax_role<T, D, NC>(a, sm, tmem, Q, qbytes, ringv, P, pbytes, wg);
+    softmax_role<T, D, NC>(a, sm, tmem, Q, qbytes, ringv, P, wg);
   }
   tc_before();
   __syncthreads();
@@ -1539,16 +1572,26 @@ bool encode_groups(CUtensorMap* m, void* base, int dtype, int ps, int H, int pag
 }
 
 struct Shape {
-  int RB, rows, two, ncj, cols;
+  int RB, rows, split, cols, width[kGroups], off[kGroups], poff[kGroups], pbytes;
 };
 Shape shape_of(int R) {
   Shape s;
   s.RB = (R + kMaxRows - 1) / kMaxRows;
   s.rows = (R + s.RB - 1) / s.RB;
-  s.two = s.rows > kAlternate;
-  const int per = s.two ? (s.rows + 1) / 2 : s.rows;
-  s.ncj = (per + 15) / 16 * 16;
-  s.cols = s.two ? 2 * s.ncj : s.ncj;
+  s.split = s.rows > kAlternate;
+  const int units = (s.rows + 15) / 16;
+  s.cols = units * 16;
+  s.pbytes = 0;
+  int off = 0;
+  for (int w = 0; w < kGroups; ++w) {
+    const int mine = s.split ? units / kGroups + (w < units % kGroups) : units;
+    s.width[w] = mine * 16;
+    s.off[w] = off;
+    if (s.split) off += mine * 16;
+    s.poff[w] = s.pbytes;
+    const int p = mine * kPBlock;
+    s.pbytes += p > kPMin ? p : kPMin;
+  }
   return s;
 }
 
@@ -1596,9 +1639,9 @@ cudaError_t launch_t(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a
 template <class T, int D>
 cudaError_t launch_d(const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C, size_t smem,
                      cudaStream_t s) {
-  if (a.ncj <= 32) return launch_t<T, D, 32>(mk, mv, a, C, smem, s);
-  if (a.ncj <= 64) return launch_t<T, D, 64>(mk, mv, a, C, smem, s);
-  return launch_t<T, D, 128>(mk, mv, a, C, smem, s);
+  if (a.wcols[0] <= 32) return launch_t<T, D, 32>(mk, mv, a, C, smem, s);
+  if (a.wcols[0] <= 64) return launch_t<T, D, 64>(mk, mv, a, C, smem, s);
+  return launch_t<T, D, 96>(mk, mv, a, C, smem, s);
 }
 
 }  // namespace
@@ -1613,7 +1656,13 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   a.width = p.kv.width; a.pages = p.kv.pages; a.ps = p.kv.ps;
   a.Hq = p.Hq; a.Hkv = p.kv.Hkv; a.G = p.G; a.R = p.nodes.N * p.G;
   const Shape sh = shape_of(a.R);
-  a.RB = sh.RB; a.rows_per_block = sh.rows; a.two = sh.two; a.ncj = sh.ncj; a.cols = sh.cols;
+  a.RB = sh.RB; a.rows_per_block = sh.rows; a.split = sh.split; a.cols = sh.cols;
+  for (int w = 0; w < kGroups; ++w) {
+    a.wcols[w] = sh.width[w];
+    a.off[w] = sh.off[w];
+    a.poff[w] = sh.poff[w];
+  }
+  a.pbytes = sh.pbytes;
   a.q = p.q; a.q_b = p.q_b; a.q_n = p.q_n; a.q_h = p.q_h;
   a.zero = p.scale == 0.f;
   a.c = a.zero ? 1.f : p.scale * 1.4426950408889634f;
@@ -1644,8 +1693,8 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
     a.ragged = a.ps % kTile != 0;
   }
   const int slot = D * 2 * kTile;
-  const size_t qb = static_cast<size_t>(a.cols) * D * 2, pb = ((a.ncj + 31) / 32) * static_cast<size_t>(kPBlock);
-  const size_t fixed = (a.two ? 1 : 2) * qb + 2 * pb + sizeof(Misc);
+  const size_t qb = static_cast<size_t>(a.cols) * D * 2;
+  const size_t fixed = (a.split ? 1 : 2) * qb + a.pbytes + sizeof(Misc);
   int slots = static_cast<int>((kSmemMax - fixed) / slot);
   if (slots > 2 * kMaxRing) slots = 2 * kMaxRing;
   if (slots < 3) return cudaErrorInvalidConfiguration;
