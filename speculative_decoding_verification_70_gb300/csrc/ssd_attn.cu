@@ -892,7 +892,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 #pragma unroll
         for (int i = 0; i < NC / 8; ++i) old[i] = l[i];
         tile_pass<T, NC>(tS, nch, c2, nm, x2, prow, wt, l, ready);
-        if (!named_or(bar, 128, growth(l, old) > kGrow)) break;
+        if (!named_or(bar, 128, growth(l, old) > kGrow) || raise) break;
         raise = true;
 #pragma unroll
         for (int i = 0; i < NC / 8; ++i) l[i] = old[i];

@@ -175,6 +175,12 @@ struct AttnParams {
   int* err;
 };
 
+// A part of a row, as its CTA leaves it.
+struct LogprobPart {
+  float m, S, U;
+  int count;
+};
+
 struct LogprobParams {
   const void* logits;
   long long row_stride;
@@ -187,6 +193,11 @@ struct LogprobParams {
   int* rank;
   int* top_tok;
   float* top_logprob;
+  bool whole;            // rows are 16-byte aligned
+  int split;             // parts of a row
+  int* counter;          // [R] parts done (0 between calls)
+  LogprobPart* parts;    // [R, split]
+  unsigned long long* part_key;  // [R, split, 32] the parts' best
   int* err;
 };
 
@@ -197,6 +208,7 @@ cudaError_t launch_kv_append(const AppendParams& p, int dtype, int D, bool vec, 
 cudaError_t launch_kv_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStream_t s);
 size_t tree_attention_bytes(int N, int G, int D);
+size_t logprobs_bytes(int R, int V);
 cudaError_t launch_logprobs(const LogprobParams& p, int dtype, bool vec, cudaStream_t s);
 
 }  // namespace ssd

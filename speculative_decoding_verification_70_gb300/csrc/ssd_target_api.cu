@@ -182,7 +182,7 @@ ssd_status ssd_kv_commit(const ssd_paged_kv* kv, int layers, int64_t k_layer, in
 
 size_t ssd_logprobs_workspace_bytes(int R, int V, int K) {
   if (R < 1 || V < 1 || V > (1 << 28) || K < 0 || K > SSD_MAX_TOP) return 0;
-  return SSD_ERRWORD_BYTES;
+  return logprobs_bytes(R, V);
 }
 
 ssd_status ssd_logprobs(const void* logits, ssd_dtype dtype, int64_t row_stride, int n_rows, int V,
@@ -192,6 +192,7 @@ ssd_status ssd_logprobs(const void* logits, ssd_dtype dtype, int64_t row_stride,
   CallRange nvtx_range("ssd_logprobs");
   if (!dtype_ok(dtype)) return SSD_ERR_UNSUPPORTED_DTYPE;
   if (!logits || !tok || !logprob || !ws) return SSD_ERR_INVALID_ARG;
+  if (R > (1 << 26)) return SSD_ERR_INVALID_ARG;
   if (n_rows < 1 || V < 1 || V > (1 << 28) || row_stride < V || R < 1 || (!rows && R > n_rows))
     return SSD_ERR_INVALID_ARG;
   if (K < 0 || K > SSD_MAX_TOP || (K > 0 && (!top_tok || !top_logprob))) return SSD_ERR_INVALID_ARG;
@@ -200,7 +201,7 @@ ssd_status ssd_logprobs(const void* logits, ssd_dtype dtype, int64_t row_stride,
       !aligned(top_logprob, 4) || !aligned(ws, 256))
     return SSD_ERR_INVALID_ARG;
   if (ws_bytes < ssd_logprobs_workspace_bytes(R, V, K)) return SSD_ERR_WORKSPACE;
-  LogprobParams p;
+  LogprobParams p = {};
   p.logits = logits; p.row_stride = row_stride; p.n_rows = n_rows; p.V = V; p.R = R; p.K = K;
   p.rows = rows; p.tok = tok; p.T = T;
   p.logprob = logprob; p.entropy = entropy; p.rank = rank;
