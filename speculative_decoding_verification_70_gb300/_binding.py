@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Dict, Optional
 
 import torch
@@ -108,16 +109,11 @@ class ProfileEntry(ctypes.Structure):
                 ("timed", ctypes.c_int), ("total_ms", ctypes.c_double)]
 
 
-class PagedKV(ctypes.Structure):
-    _fields_ = [("k", _P), ("v", _P),
-                ("k_page", _L), ("k_slot", _L), ("k_head", _L),
-                ("v_page", _L), ("v_slot", _L), ("v_head", _L),
-                ("dtype", _I), ("num_pages", _I), ("page_size", _I), ("Hkv", _I), ("D", _I),
-                ("page_table", _P), ("table_stride", _L), ("max_pages", _I)]
-
-
-class DraftNodes(ctypes.Structure):
-    _fields_ = [("B", _I), ("N", _I), ("ctx_len", _P), ("parent", _P), ("n_nodes", _P)]
+# The host structs of the paged-cache calls (ssd_paged_kv, ssd_draft_nodes), as
+# packed bytes: a ctypes.Structure of so many fields takes three times as long
+# to fill.
+_pack_kv = struct.Struct("@PP6q5iPqi4x").pack
+_pack_nodes = struct.Struct("@iiPPP").pack
 
 
 _lib = None
@@ -545,70 +541,82 @@ def ssd_verify_tree(Z: torch.Tensor, D: torch.Tensor, parent: torch.Tensor,
 
 # ---------------------------------------------------------------------------
 # the target pass around a verification: paged cache, tree attention, answers
+# (one call a layer: the checks below are written to cost a few microseconds)
 # ---------------------------------------------------------------------------
 _KV_DTYPE = {torch.bfloat16: SSD_BF16, torch.float16: SSD_F16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _strides(t: torch.Tensor, one: int):
-    """Element strides, `one` in place of those of dimensions of one entry
-    (which torch leaves arbitrary)."""
-    st = t.stride()
-    return st if 1 not in t.shape else [one if n == 1 else s for n, s in zip(t.shape, st)]
+def _stream_of(stream, t: torch.Tensor) -> int:
+    """The given stream, or the current one of t's device."""
+    if stream is None:
+        return _raw_stream(t.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor) -> PagedKV:
+def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor):
     """k_cache, v_cache: [pages, page_size, Hkv, D] views (any order of the
-    first three dimensions in memory); page_table [B, max_pages] int32."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    first three dimensions in memory; a fourth in front counts layers, of
+    which the struct holds the first); page_table [B, max_pages] int32.
+    Returns the packed struct, Hkv, D and B."""
+    sh = k_cache.shape
+    dt = k_cache.dtype
+    if len(sh) < 4 or v_cache.shape != sh or v_cache.dtype is not dt:
         raise ValueError("k_cache and v_cache must both be [pages, page_size, Hkv, D] of one dtype")
-    code = _KV_DTYPE.get(k_cache.dtype)
+    code = _KV_DTYPE.get(dt)
     if code is None:
-        raise TypeError("the cache must be bfloat16 or float16, got %s" % k_cache.dtype)
+        raise TypeError("the cache must be bfloat16 or float16, got %s" % dt)
     if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
         raise ValueError("the cache and its page table must be CUDA tensors")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.stride(1) != 1:
-        raise ValueError("page_table must be int32 [B, max_pages] with contiguous rows")
-    pages, ps, H, D = k_cache.shape
-    if k_cache.stride(3) != 1 or v_cache.stride(3) != 1:
-        raise ValueError("head entries must be contiguous")
-    ks, vs = _strides(k_cache, D), _strides(v_cache, D)
-    width = page_table.shape[1]
-    return PagedKV(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                   code, pages, ps, H, D, page_table.data_ptr(), max(page_table.stride(0), width),
-                   width)
+    pages, ps, H, D = sh[-4:]
+    kp, ks, kh, kd = k_cache.stride()[-4:]
+    vp, vs, vh, vd = v_cache.stride()[-4:]
+    if pages == 1 or ps == 1 or H == 1:  # torch leaves strides of one entry arbitrary
+        kp, vp = (D, D) if pages == 1 else (kp, vp)
+        ks, vs = (D, D) if ps == 1 else (ks, vs)
+        kh, vh = (D, D) if H == 1 else (kh, vh)
+    ts = page_table.stride()
+    if page_table.dtype is not torch.int32 or len(ts) != 2:
+        raise ValueError("page_table must be int32 [B, max_pages]")
+    B, width = page_table.shape
+    if (ts[1] != 1 and width > 1) or kd != 1 or vd != 1:
+        raise ValueError("head entries and rows of the page table must be contiguous")
+    try:
+        kv = _pack_kv(k_cache.data_ptr(), v_cache.data_ptr(), kp, ks, kh, vp, vs, vh, code, pages,
+                      ps, H, D, page_table.data_ptr(),
+                      ts[0] if ts[0] >= width or B > 1 else width, width)
+    except struct.error:
+        raise ValueError("the cache is too large: %s" % (tuple(sh),)) from None
+    return kv, H, D, B
 
 
 def _i32(t: Optional[torch.Tensor], shape, name: str):
     if t is None:
         return None
-    if t.dtype != torch.int32:
+    if t.dtype is not torch.int32:
         raise TypeError("%s must be int32, got %s" % (name, t.dtype))
     if t.shape != shape or not t.is_contiguous() or not t.is_cuda:
         raise ValueError("%s must be a contiguous CUDA tensor of shape %s" % (name, tuple(shape)))
     return t.data_ptr()
 
 
-def _draft_nodes(B: int, N: int, page_table, ctx_len, parent, n_nodes) -> DraftNodes:
-    if ctx_len is None or page_table.shape[0] != B:
-        raise ValueError("ctx_len and page_table must have one entry (row) per sequence")
-    return DraftNodes(B, N, _i32(ctx_len, (B,), "ctx_len"), _i32(parent, (B, N), "parent"),
-                      _i32(n_nodes, (B,), "n_nodes"))
+def _draft_nodes(B: int, N: int, ctx_len, parent, n_nodes):
+    return _pack_nodes(B, N, _i32(ctx_len, (B,), "ctx_len"),
+                       0 if parent is None else _i32(parent, (B, N), "parent"),
+                       0 if n_nodes is None else _i32(n_nodes, (B,), "n_nodes"))
 
 
-def _heads(t: torch.Tensor, like: torch.Tensor, name: str):
-    """[B, N, heads, D] view with contiguous head entries."""
-    if t.dim() != 4 or not t.is_cuda or t.dtype != like.dtype or t.shape[3] != like.shape[3]:
-        raise ValueError("%s must be a CUDA tensor [B, N, heads, %d] of type %s"
-                         % (name, like.shape[3], like.dtype))
-    if t.stride(3) != 1:
+def _heads(t: torch.Tensor, dt: torch.dtype, B: int, D: int, name: str):
+    """(pointer, shape, three strides) of a [B, N, heads, D] view with contiguous
+    head entries."""
+    sh = t.shape
+    if len(sh) != 4 or sh[0] != B or sh[3] != D or t.dtype is not dt or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor [%d, N, heads, %d] of type %s" % (name, B, D, dt))
+    sb, sn, sh_, sd = t.stride()
+    if sd != 1:
         raise ValueError("%s: head entries must be contiguous" % name)
-    return t.data_ptr()
-
-
-def _error_ws(ws, dev):
-    if ws is None:
-        ws = new_workspace(_ERRWORD_BYTES, dev)
-    return ws
+    # (torch leaves strides of one entry arbitrary)
+    return (t.data_ptr(), sh, 0 if B == 1 else sb, 0 if sh[1] == 1 else sn, 0 if sh[2] == 1 else sh_)
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda",
@@ -639,32 +647,41 @@ def ssd_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: to
     depth(j); parent [B,N] int32 is the tree of ssd_verify_tree, None a chain;
     n_nodes [B] the nodes of each sequence.  cos_sin: rope_table(...) or None;
     q_norm, k_norm: [D] weights or None.  Returns {"q": [B,N,Hq,D], "ws"}."""
-    kv = _paged_kv(k_cache, v_cache, page_table)
-    qp, kp, vp = _heads(q, k_cache, "q"), _heads(k, k_cache, "k"), _heads(v, k_cache, "v")
-    B, N, Hq, D = q.shape
-    if k.shape != (B, N, kv.Hkv, D) or v.shape != k.shape or _strides(v, 0) != _strides(k, 0):
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [pages, page_size, Hkv, D]")
+    kv, H, D, B = _paged_kv(k_cache, v_cache, page_table)
+    dt = k_cache.dtype
+    qp, qsh, qb, qn_, qh = _heads(q, dt, B, D, "q")
+    kp, ksh, kb, kn_, kh = _heads(k, dt, B, D, "k")
+    vp, vsh, vb, vn_, vh = _heads(v, dt, B, D, "v")
+    _, N, Hq, _ = qsh
+    if ksh != vsh or kb != vb or kn_ != vn_ or kh != vh or ksh[1] != N or ksh[2] != H:
         raise ValueError("k and v must be [B, N, Hkv, D] with the same strides")
-    nodes = _draft_nodes(B, N, page_table, ctx_len, parent, n_nodes)
+    nodes = _draft_nodes(B, N, ctx_len, parent, n_nodes)
     max_pos = rot = 0
+    cp = qn = kn = None
     if cos_sin is not None:
         _want(cos_sin, torch.float32, "cos_sin")
         max_pos, rot = cos_sin.shape
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None and (w.dtype != q.dtype or w.numel() != D):
-            raise ValueError("%s must be [D] of q's type" % name)
-    ws = _error_ws(ws, q.device)
+        cp = _dev(cos_sin, "cos_sin")
+    if q_norm is not None or k_norm is not None:
+        for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+            if w is None or w.dtype is not dt or w.numel() != D:
+                raise ValueError("q_norm and k_norm must both be [D] of q's type")
+        qn, kn = _dev(q_norm, "q_norm"), _dev(k_norm, "k_norm")
+    if ws is None:
+        ws = new_workspace(_ERRWORD_BYTES, q.device)
     wp, wn = _ws_ptr(ws)
     out = {} if out is None else out
     qo = out.get("q")
     if qo is None:
-        qo = out["q"] = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
-    elif qo.shape != q.shape or qo.dtype != q.dtype:
+        qo = out["q"] = torch.empty(qsh, dtype=dt, device=q.device)
+    elif qo.shape != qsh or qo.dtype is not dt:
         raise ValueError("out['q'] must be like q")
-    qs, ks = _strides(q, 0), _strides(k, 0)
     _check("ssd_kv_append", load_library().ssd_kv_append(
-        ctypes.byref(kv), ctypes.byref(nodes), Hq, qp, qs[0], qs[1], qs[2], kp, vp, ks[0], ks[1],
-        ks[2], _dev(qo, "out['q']"), _opt(cos_sin, "cos_sin"), max_pos, rot, int(interleaved),
-        _opt(q_norm, "q_norm"), _opt(k_norm, "k_norm"), eps, wp, wn, _stream(stream)))
+        kv, nodes, Hq, qp, qb, qn_, qh, kp, vp, kb, kn_, kh,
+        _dev(qo, "out['q']"), cp, max_pos, rot, interleaved, qn, kn, eps, wp, wn,
+        _stream_of(stream, q)))
     out["ws"] = ws
     return out
 
@@ -684,27 +701,32 @@ def ssd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     and itself.  scale defaults to D ** -0.5.  Returns {"out": [B,N,Hq,D],
     "lse": [B,N,Hq] float32, "ws"}; nodes that are absent get 0 and -inf."""
     lib = load_library()
-    kv = _paged_kv(k_cache, v_cache, page_table)
-    qp = _heads(q, k_cache, "q")
-    B, N, Hq, D = q.shape
-    nodes = _draft_nodes(B, N, page_table, ctx_len, parent, n_nodes)
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [pages, page_size, Hkv, D]")
+    kv, H, D, B = _paged_kv(k_cache, v_cache, page_table)
+    dt = k_cache.dtype
+    qp, qsh, qb, qn, qh = _heads(q, dt, B, D, "q")
+    _, N, Hq, _ = qsh
+    nodes = _draft_nodes(B, N, ctx_len, parent, n_nodes)
     if ws is None:
-        n = lib.ssd_tree_attention_workspace_bytes(B, N, Hq, kv.Hkv, D)
+        n = lib.ssd_tree_attention_workspace_bytes(B, N, Hq, H, D)
         if n == 0:
             raise SSDError("ssd_tree_attention_workspace_bytes", 1)
         ws = new_workspace(n, q.device)
     wp, wn = _ws_ptr(ws)
     o = {} if out is None else out
-    if "out" not in o:
-        o["out"] = torch.empty((B, N, Hq, D), dtype=q.dtype, device=q.device)
-        o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
-    elif o["out"].shape != q.shape or o["out"].dtype != q.dtype or o["lse"].shape != q.shape[:3]:
-        raise ValueError("out must hold out like q and lse [B, N, Hq]")
-    qs = _strides(q, 0)
+    res = o.get("out")
+    if res is None:
+        res = o["out"] = torch.empty(qsh, dtype=dt, device=q.device)
+        lse = o["lse"] = torch.empty(qsh[:3], dtype=torch.float32, device=q.device)
+    else:
+        lse = o["lse"]
+        if res.shape != qsh or res.dtype is not dt or lse.shape != qsh[:3]:
+            raise ValueError("out must hold out like q and lse [B, N, Hq]")
+        _want(lse, torch.float32, "lse")
     _check("ssd_tree_attention", lib.ssd_tree_attention(
-        ctypes.byref(kv), ctypes.byref(nodes), Hq, qp, qs[0], qs[1], qs[2],
-        D ** -0.5 if scale is None else scale, _dev(o["out"], "out"), _dev(o["lse"], "lse"), wp,
-        wn, _stream(stream)))
+        kv, nodes, Hq, qp, qb, qn, qh, D ** -0.5 if scale is None else scale,
+        _dev(res, "out"), _dev(lse, "lse"), wp, wn, _stream_of(stream, q)))
     o["ws"] = ws
     return o
 
@@ -721,26 +743,29 @@ def ssd_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torc
     "ws"}: the lengths after the commit."""
     layers, kl, vl = 1, 0, 0
     if k_cache.dim() == 5:
-        if v_cache.shape != k_cache.shape:
-            raise ValueError("k_cache and v_cache must have one shape")
         layers, kl, vl = k_cache.shape[0], k_cache.stride(0), v_cache.stride(0)
-        k_cache, v_cache = k_cache[0], v_cache[0]
-    kv = _paged_kv(k_cache, v_cache, page_table)
-    B = page_table.shape[0]
+        if layers < 1:
+            raise ValueError("the caches must have a layer")
+    elif k_cache.dim() != 4:
+        raise ValueError("the caches must be [pages, page_size, Hkv, D], layers in front or not")
+    kv, _, _, B = _paged_kv(k_cache, v_cache, page_table)
     N = MAX_TREE_NODES
+    node = None
     if out_node is not None:
-        if out_node.dim() != 2:
-            raise ValueError("out_node must be [B, N]")
-        N = out_node.shape[1]
-    ws = _error_ws(ws, k_cache.device)
+        N = out_node.shape[-1]
+        node = _i32(out_node, (B, N), "out_node")
+    if ws is None:
+        ws = new_workspace(_ERRWORD_BYTES, k_cache.device)
     wp, wn = _ws_ptr(ws)
     o = {} if out is None else out
-    if "ctx_len" not in o:
-        o["ctx_len"] = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+    new = o.get("ctx_len")
+    if new is None:
+        new = o["ctx_len"] = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+    shape = (B,)
     _check("ssd_kv_commit", load_library().ssd_kv_commit(
-        ctypes.byref(kv), layers, kl, vl, B, N, _i32(ctx_len, (B,), "ctx_len"),
-        _i32(accept_len, (B,), "accept_len"), _i32(out_node, (B, N), "out_node"),
-        _i32(o["ctx_len"], (B,), "out['ctx_len']"), wp, wn, _stream(stream)))
+        kv, layers, kl, vl, B, N, _i32(ctx_len, shape, "ctx_len"),
+        _i32(accept_len, shape, "accept_len"), node, _i32(new, shape, "out['ctx_len']"), wp, wn,
+        _stream_of(stream, k_cache)))
     o["ws"] = ws
     return o
 
@@ -756,40 +781,49 @@ def ssd_logprobs(logits: torch.Tensor, tok: torch.Tensor, K: int = 0,
     answer); T [R] float32 or None.  Returns {"logprob", "entropy", "rank",
     "top_tok" [R,K], "top_logprob" [R,K], "ws"} (the last two for K > 0)."""
     lib = load_library()
-    if logits.dim() != 2 or not logits.is_cuda:
+    sh, st = logits.shape, logits.stride()
+    if len(sh) != 2 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [n, V]")
-    n, V = logits.shape
-    if V > 1 and logits.stride(1) != 1:
+    n, V = sh
+    if V > 1 and st[1] != 1:
         raise ValueError("a row of logits must be contiguous")
-    R = tok.numel()
     _want(tok, torch.int32, "tok")
+    R = tok.numel()
+    Tp = rp = tt = tl = None
     if T is not None:
         _want(T, torch.float32, "T")
         if T.numel() != R:
             raise ValueError("T must hold one temperature per token")
-    dev = logits.device
+        Tp = _dev(T, "T")
+    if rows is not None:
+        rp = _i32(rows, (R,), "rows")
     if ws is None:
         nb = lib.ssd_logprobs_workspace_bytes(R, V, K)
         if nb == 0:
             raise SSDError("ssd_logprobs_workspace_bytes", 1)
-        ws = new_workspace(nb, dev)
+        ws = new_workspace(nb, logits.device)
     wp, wn = _ws_ptr(ws)
     o = {} if out is None else out
-    if "logprob" not in o:
-        o["logprob"] = torch.empty(R, dtype=torch.float32, device=dev)
+    lp = o.get("logprob")
+    if lp is None:
+        dev = logits.device
+        lp = o["logprob"] = torch.empty(R, dtype=torch.float32, device=dev)
         o["entropy"] = torch.empty(R, dtype=torch.float32, device=dev)
         o["rank"] = torch.empty(R, dtype=torch.int32, device=dev)
-    if K > 0 and "top_tok" not in o:
-        o["top_tok"] = torch.empty((R, K), dtype=torch.int32, device=dev)
-        o["top_logprob"] = torch.empty((R, K), dtype=torch.float32, device=dev)
-    if o["logprob"].numel() != R or (K > 0 and o["top_tok"].shape != (R, K)):
+    elif lp.numel() != R:
         raise ValueError("out is of another call's sizes")
+    if K > 0:
+        top = o.get("top_tok")
+        if top is None:
+            top = o["top_tok"] = torch.empty((R, K), dtype=torch.int32, device=logits.device)
+            o["top_logprob"] = torch.empty((R, K), dtype=torch.float32, device=logits.device)
+        elif top.shape != (R, K):
+            raise ValueError("out is of another call's sizes")
+        tt, tl = _dev(top, "top_tok"), _dev(o["top_logprob"], "top_logprob")
     _check("ssd_logprobs", lib.ssd_logprobs(
-        logits.data_ptr(), _dtype_code(logits), max(logits.stride(0), V), n, V,
-        _i32(rows, (R,), "rows"), R, _dev(tok, "tok"), _opt(T, "T"), K,
-        _dev(o["logprob"], "logprob"), _dev(o["entropy"], "entropy"), _dev(o["rank"], "rank"),
-        _dev(o["top_tok"], "top_tok") if K > 0 else None,
-        _dev(o["top_logprob"], "top_logprob") if K > 0 else None, wp, wn, _stream(stream)))
+        logits.data_ptr(), _dtype_code(logits), st[0] if st[0] >= V or n > 1 else V, n, V, rp, R,
+        _dev(tok, "tok"), Tp, K, _dev(lp, "logprob"), _dev(o["entropy"], "entropy"),
+        _dev(o["rank"], "rank"), tt, tl, wp, wn, _stream_of(stream, logits)))
     o["ws"] = ws
     return o
 

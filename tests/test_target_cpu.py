@@ -21,13 +21,13 @@ def _kv(**kw):
              v_head=128, dtype=1, num_pages=10, page_size=16, Hkv=8, D=128, page_table=P, table_stride=4,
              max_pages=4)
     f.update(kw)
-    return bd.PagedKV(**f)
+    return bd._pack_kv(*(f[k] or 0 for k in f))
 
 
 def _nodes(**kw):
     f = dict(B=2, N=4, ctx_len=P, parent=None, n_nodes=None)
     f.update(kw)
-    return bd.DraftNodes(**f)
+    return bd._pack_nodes(*(f[k] or 0 for k in f))
 
 
 BAD_KV = [dict(k=None), dict(v=P + 2), dict(page_table=None), dict(page_table=P + 2), dict(num_pages=0),
@@ -40,14 +40,14 @@ BAD_NODES = [dict(B=0), dict(N=0), dict(N=65), dict(ctx_len=None), dict(parent=P
 def _attend(lib, kv=None, nodes=None, Hq=16, q=P, q_b=4 * 16 * 128, q_n=16 * 128, q_h=128, scale=0.1, out=P,
             lse=P, ws=P, n=1 << 40):
     kv, nodes = kv or _kv(), nodes or _nodes()
-    return lib.ssd_tree_attention(ctypes.byref(kv), ctypes.byref(nodes), Hq, q, q_b, q_n, q_h, scale, out, lse,
+    return lib.ssd_tree_attention(kv, nodes, Hq, q, q_b, q_n, q_h, scale, out, lse,
                                   ws, n, None)
 
 
 def _append(lib, kv=None, nodes=None, Hq=16, q=P, k=P, v=P, q_out=P, cos_sin=P, max_pos=99, rot=128, qn=P, kn=P,
             eps=1e-6, ws=P, n=256, q_b=99, kv_h=128):
     kv, nodes = kv or _kv(), nodes or _nodes()
-    return lib.ssd_kv_append(ctypes.byref(kv), ctypes.byref(nodes), Hq, q, q_b, 128, 128, k, v, 512, 128, kv_h,
+    return lib.ssd_kv_append(kv, nodes, Hq, q, q_b, 128, 128, k, v, 512, 128, kv_h,
                              q_out, cos_sin, max_pos, rot, 0, qn, kn, eps, ws, n, None)
 
 
@@ -57,7 +57,7 @@ def test_bad_cache_is_refused(lib, kw):
     assert _attend(lib, kv=_kv(**kw)) == INVALID
     assert _append(lib, kv=_kv(**kw)) == INVALID
     kv = _kv(**kw)
-    assert lib.ssd_kv_commit(ctypes.byref(kv), 1, 0, 0, 2, 4, P, P, P, P + 64, P, 256, None) == INVALID
+    assert lib.ssd_kv_commit(kv, 1, 0, 0, 2, 4, P, P, P, P + 64, P, 256, None) == INVALID
 
 
 @needs_no_gpu
@@ -97,7 +97,7 @@ def test_commit_refusals(lib):
     kv = _kv()
 
     def call(layers=2, kl=1 << 20, vl=1 << 20, B=2, N=4, ctx=P, acc=P, node=P, new=P + 64, ws=P, n=256):
-        return lib.ssd_kv_commit(ctypes.byref(kv), layers, kl, vl, B, N, ctx, acc, node, new, ws, n, None)
+        return lib.ssd_kv_commit(kv, layers, kl, vl, B, N, ctx, acc, node, new, ws, n, None)
     for kw in (dict(layers=0), dict(kl=4), dict(vl=0), dict(B=0), dict(N=65), dict(ctx=None), dict(acc=None),
                dict(new=None), dict(new=P), dict(node=P + 2), dict(ws=None)):
         assert call(**kw) == INVALID, kw
