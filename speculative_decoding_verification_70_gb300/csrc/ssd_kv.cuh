@@ -208,7 +208,7 @@ cudaError_t launch_kv_append(const AppendParams& p, int dtype, int D, bool vec, 
 cudaError_t launch_kv_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStream_t s);
 size_t tree_attention_bytes(int N, int G, int D);
-size_t logprobs_bytes(int R, int V);
+size_t logprobs_bytes(int R, int V, int K);
 cudaError_t launch_logprobs(const LogprobParams& p, int dtype, bool vec, cudaStream_t s);
 
 }  // namespace ssd

@@ -182,7 +182,7 @@ ssd_status ssd_kv_commit(const ssd_paged_kv* kv, int layers, int64_t k_layer, in
 
 size_t ssd_logprobs_workspace_bytes(int R, int V, int K) {
   if (R < 1 || V < 1 || V > (1 << 28) || K < 0 || K > SSD_MAX_TOP) return 0;
-  return logprobs_bytes(R, V);
+  return logprobs_bytes(R, V, K);
 }
 
 ssd_status ssd_logprobs(const void* logits, ssd_dtype dtype, int64_t row_stride, int n_rows, int V,
