@@ -10,21 +10,29 @@
 // rule in a fixed order.  The pass computes z c - round(m c) with one fused
 // multiply-add an element and takes the rounding error of m c out of S and U
 // afterwards (the same rule again); rows whose m c is beyond 2^24 or whose T is
-// below 1e-7 are summed by a plain second loop.  The rank is a count of the
+// below 1e-7 or above 7e22 are summed by a plain second loop.  The rank is a count of the
 // elements that come before the token's logit, known before the pass.
 //
-// Best alternatives: the K-th largest of a few of the first elements bounds the
-// K-th largest of all from below; elements that reach the bound go to a list in
-// shared memory, and the bound rises a few times as the list grows.  The pass
-// compares one maximum per vector with it.  A row with more such elements than
-// the list holds (thousands of equal logits, or of -inf) is searched K times
-// instead.
+// Best alternatives: the K-th largest of the warps' first maxima bounds the K-th
+// largest of all from below; elements that reach the bound go to a list in
+// shared memory, a part of it for each warp, and the bound rises after 4, 16,
+// ... rounds to about the K-th largest of the lists (found by counting at three
+// values at a time), which drops the others.  The pass compares one maximum of
+// a thread and round with it.  A row with more such elements than the lists hold
+// (hundreds of equal logits, or of -inf) is searched K times instead.
 //
-// Bound: HBM for fp32; for bf16 also the instructions (about 8 an element; the
-// largest element, the floor under -inf and the count for the rank are packed
-// 16-bit operations).  One CTA per row, or per part of a row, whose last CTA to
-// finish joins the parts.
+// A warp copies its slices of the row into a ring of its own (bulk copies, two
+// rounds of 2 KB ahead: 96 KB in flight on an SM; with three or four the fp32
+// pass of K = 0 fell from 6.6 to 4 TB/s).  One CTA per row, or per part of a row,
+// whose last CTA to finish joins the parts.
+//
+// Bound: HBM for fp32 (4096 x 151936, K = 5: 389 us, 6.4 TB/s; 2048 rows, K = 0:
+// 187 us, 6.6 TB/s); for bf16 the instructions, 6 an element, and the candidates'
+// steps (384 x 151936: K = 0 25 us, 4.7 TB/s; K = 20 43 us); for a few rows the
+// steps one after another (8 x 128256: K = 0 5.3 us, K = 5 8.4 us).
 #include <math.h>
+
+#include <algorithm>
 
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"
@@ -33,25 +41,32 @@ namespace ssd {
 namespace {
 
 constexpr int kLpThreads = 256;
-constexpr int kLpCtas = 4;        // per SM
+// CTAs of an SM.  Four (64 registers a thread) hide more of the candidates'
+// steps where fp32 rows ask for the best (R = 1000, V = 128256, K = 8: 96 us,
+// three: 103); elsewhere three are as fast or faster (bf16, 384 x 151936, K = 20:
+// 43 us, four: 48; fp32, 2048 x 151936, K = 0: 186, four: 198).
+template <class Tag, bool TOP>
+constexpr int kLpCtas = TOP && Tag::kVec == 4 ? 4 : 3;
 constexpr int kFlight = 4;        // vectors of a thread and round
-constexpr int kStages = 3;        // rounds on their way into shared memory
+constexpr int kStages = 2;        // rounds on their way into shared memory
 constexpr int kSlice = 32 * kFlight;  // a warp's vectors of a round
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kList = 1024;       // elements of the list, a part of it for each warp (one counter
+constexpr int kList = 896;        // elements of the list, a part of it for each warp (one counter
                                   // for all of them, with its atomics, cost more than the pass)
 constexpr int kOwn = kList / kLpWarps;
-constexpr int kMaxSplit = 32;     // parts of a row
+constexpr int kMaxSplit = 31;     // parts of a row (of whose lists each thread takes kHold keys)
+constexpr int kCounters = 1024;   // most rows that are split
+constexpr int kHold = 4;          // most keys of a thread where the best are selected
+constexpr int kFirst = 5;         // most of each warp's maxima of the first round
+constexpr int kRaise = 4;         // rounds before the bound first rises, and the factor to the next time
 constexpr int kLpTop = 32;        // SSD_MAX_TOP
 constexpr float kStep = 16.f;     // excess of an element over m that moves it
 constexpr float kLowest = -3.0e38f;
+constexpr float kLeast = 2e-23f;   // least c of the pass: below it -1e30 c, its floor, is not far below m c
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 using Part = LogprobPart;
-
-constexpr int kRaise = 16;   // candidates of a warp that raise the bound
-constexpr int kFirst = 6;  // most of each warp's maxima of the first round
 
 struct LpSmem {
   uint4 ring[kLpWarps][kStages][kSlice];  // each warp's own
@@ -60,30 +75,32 @@ struct LpSmem {
   unsigned long long best[kLpTop];
   float m[kLpWarps], S[kLpWarps], U[kLpWarps];
   int count[kLpWarps];
-  float top[kLpWarps * kFirst];
+  alignas(16) float top[kLpWarps * kFirst];
+  uint4 range[kLpWarps];
+  alignas(16) uint32_t above[2][kLpWarps];
   unsigned long long wkey[kLpWarps];
   int n[kLpWarps], last;
   float tau;
 };
 
-// A (value, index) pair as one number that orders by value, then by lower
-// index; -0 counts as 0.
-__device__ __forceinline__ unsigned long long key_of(float v, int i) {
+// Values as numbers above 0 of the same order, and back; -0 counts as 0.
+__device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
-  const uint32_t u = b & 0x80000000u ? ~b : b | 0x80000000u;
-  return (static_cast<unsigned long long>(u) << 32) | (0x7fffffffu - static_cast<uint32_t>(i));
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+// A (value, index) pair as one number that orders by value, then by lower
+// index.
+__device__ __forceinline__ unsigned long long key_of(float v, int i) {
+  return (static_cast<unsigned long long>(order_of(v)) << 32) | (0x7fffffffu - static_cast<uint32_t>(i));
 }
 __device__ __forceinline__ float key_value(unsigned long long k) {
-  const uint32_t u = static_cast<uint32_t>(k >> 32);
-  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+  return order_value(static_cast<uint32_t>(k >> 32));
 }
 __device__ __forceinline__ int key_index(unsigned long long k) {
   return static_cast<int>(0x7fffffffu - static_cast<uint32_t>(k));
-}
-__device__ __forceinline__ float redux_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -94,6 +111,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
@@ -148,13 +170,30 @@ struct Raw<F32Tag> {
   }
   __device__ __forceinline__ void none() { r = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
   __device__ __forceinline__ float top() const { return max3(fmaxf(r.x, r.y), r.z, r.w); }
-  // z c - mc, at least about -1000 (2^-1000 (-1000) = 0 where the logit is -inf)
+  // largest of a round's elements
+  __device__ __forceinline__ static float top(const Raw (&w)[kFlight]) {
+    float t = w[0].top();
+#pragma unroll
+    for (int u = 1; u < kFlight; ++u) t = max3(max3(t, w[u].r.x, w[u].r.y), w[u].r.z, w[u].r.w);
+    return t;
+  }
+  // The logits with a floor of -1e30 under them (c is at most 1.5e7, and where
+  // a logit is -inf 2^x x has to be 0), checked a round at a time.
+  __device__ __forceinline__ static void floor(Raw (&w)[kFlight]) {
+    float t = INFINITY;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) t = min3(min3(t, w[u].r.x, w[u].r.y), w[u].r.z, w[u].r.w);
+    if (t < -1e30f) {
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u)
+        w[u].r = make_float4(max_nan(w[u].r.x, -1e30f), max_nan(w[u].r.y, -1e30f), max_nan(w[u].r.z, -1e30f),
+                             max_nan(w[u].r.w, -1e30f));
+    }
+  }
+  // z c - mc
   __device__ __forceinline__ void scaled(f32x2 c, f32x2 m, f32x2 (&x)[4]) const {
-    float a, b;
-    up2(fma2(pk2(r.x, r.y), c, m), a, b);
-    x[0] = pk2(max_nan(a, -1000.f), max_nan(b, -1000.f));
-    up2(fma2(pk2(r.z, r.w), c, m), a, b);
-    x[1] = pk2(max_nan(a, -1000.f), max_nan(b, -1000.f));
+    x[0] = fma2(pk2(r.x, r.y), c, m);
+    x[1] = fma2(pk2(r.z, r.w), c, m);
   }
   __device__ __forceinline__ void count(Bound t, Count& n) const {
     n.n += (r.x > t) + (r.y > t) + (r.z > t) + (r.w > t);
@@ -200,14 +239,24 @@ struct Raw<BF16Tag> {
     const uint32_t w = max_bf16x2(max_bf16x2(r.x, r.y), max_bf16x2(r.z, r.w));
     return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
-  // the floor, -1e30, under the logits themselves: c is at most 1.5e7
+  __device__ __forceinline__ static float top(const Raw (&w)[kFlight]) {
+    uint32_t t = max_bf16x2(max_bf16x2(w[0].r.x, w[0].r.y), max_bf16x2(w[0].r.z, w[0].r.w));
+#pragma unroll
+    for (int u = 1; u < kFlight; ++u)
+      t = max_bf16x2(max_bf16x2(t, max_bf16x2(w[u].r.x, w[u].r.y)), max_bf16x2(w[u].r.z, w[u].r.w));
+    return fmaxf(__uint_as_float(t << 16), __uint_as_float(t & 0xffff0000u));
+  }
+  __device__ __forceinline__ static void floor(Raw (&w)[kFlight]) {
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      w[u].r = make_uint4(max_nan_bf16x2(w[u].r.x, 0xf149f149u), max_nan_bf16x2(w[u].r.y, 0xf149f149u),
+                          max_nan_bf16x2(w[u].r.z, 0xf149f149u), max_nan_bf16x2(w[u].r.w, 0xf149f149u));
+  }
   __device__ __forceinline__ void scaled(f32x2 c, f32x2 m, f32x2 (&x)[4]) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t f = max_nan_bf16x2(w[k], 0xf149f149u);
-      x[k] = fma2(pk2(__uint_as_float(f << 16), __uint_as_float(f & 0xffff0000u)), c, m);
-    }
+    for (int k = 0; k < 4; ++k)
+      x[k] = fma2(pk2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)), c, m);
   }
   __device__ __forceinline__ void count(Bound t, Count& n) const {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -219,14 +268,16 @@ struct Raw<BF16Tag> {
 
 // S and U of a part of a row by a plain second loop around its maximum m:
 // rows whose m c is too large to be rounded once for all elements, and
-// temperatures below 1e-7.
+// temperatures below 1e-7 or above 7e22.
 template <class Tag>
 __device__ __noinline__ void sum_plain(const typename Tag::Elem* z, int i0, int i1, float c, float& m, float& S,
                                        float& E) {
   S = 0.f;
   E = 0.f;
   for (int i = i0 + threadIdx.x; i < i1; i += kLpThreads) {
-    const float x = max_nan((Tag::load1(z + i) - m) * c, -1000.f), e = exp2f(x);
+    const float v = Tag::load1(z + i);
+    if (v == -INFINITY) continue;  // (c = 0 at an infinite T)
+    const float x = max_nan((v - m) * c, -1000.f), e = exp2f(x);
     S += e;
     E = fmaf(e, x, E);
   }
@@ -249,31 +300,117 @@ __device__ __forceinline__ void join_warp(float c, float& m, float& S, float& U)
   }
 }
 
-// Keys that come before one, of the first n (an even number) of `parts` lists
-// kOwn apart.
-__device__ __forceinline__ int rank_of(const unsigned long long* key, int parts, int n, unsigned long long mine) {
-  int rank = 0;
-#pragma unroll 1
-  for (int w = 0; w < parts; ++w) {
-#pragma unroll 4
-    for (int k = 0; k < n; k += 2) {
-      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(key + w * kOwn + k);
-      rank += (two.x > mine) + (two.y > mine);
-    }
+// A bound on the K-th largest of the CTA's orders (a thread's v, 0: none) from
+// below that most of them reach at most, or the K-th largest itself; 1 where
+// there are fewer than K.  Counts at three places of the range that is left, in
+// 10 bits each, until it is found.  Every thread of the CTA calls it.
+__device__ __noinline__ uint32_t bound_of(LpSmem& sm, uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, int K,
+                                          int most) {
+  const uint32_t v[kHold] = {v0, v1, v2, v3};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t hi = 0, lo = ~0u, n = 0;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    hi = max(hi, v[k]);
+    lo = min(lo, v[k] - 1);  // (0 is the largest of these)
+    n += v[k] != 0;
   }
-  return rank;
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) sm.range[warp] = make_uint4(hi, lo, n, 0);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kLpWarps; ++w) {
+    const uint4 q = sm.range[w];
+    hi = max(hi, q.x);
+    lo = min(lo, q.y);
+    n = w == 0 ? q.z : n + q.z;
+  }
+  ++lo;
+  ++hi;
+  if (n <= static_cast<uint32_t>(most)) __syncthreads();  // (before the next call)
+  if (n < static_cast<uint32_t>(K)) return 1;
+  // n >= K reach lo, fewer reach hi
+#pragma unroll 1
+  for (int turn = 0; n > static_cast<uint32_t>(most) && hi - lo > 1; turn ^= 1) {
+    const uint32_t q = max(1u, (hi - lo) >> 2);
+    uint32_t c = 0;
+#pragma unroll
+    for (int k = 0; k < kHold; ++k)
+      c += (v[k] >= lo + q) + (v[k] >= lo + 2 * q) * (1u << 10) + (v[k] >= lo + 3 * q) * (1u << 20);
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (lane == 0) sm.above[turn][warp] = c;
+    __syncthreads();
+    c = 0;
+#pragma unroll
+    for (int w = 0; w < kLpWarps; w += 4) {
+      const uint4 a = *reinterpret_cast<const uint4*>(&sm.above[turn][w]);
+      c += a.x + a.y + a.z + a.w;
+    }
+    uint32_t at = 0;  // the highest place that K reach
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const uint32_t a = (c >> (10 * k)) & 1023u;
+      if (a >= static_cast<uint32_t>(K)) {
+        at = k + 1;
+        n = a;
+      }
+    }
+    if (at < 3) hi = lo + (at + 1) * q;
+    lo += at * q;
+  }
+  if (n > static_cast<uint32_t>(most)) __syncthreads();  // (n is the same for all: every path has one)
+  return lo;
 }
 
-// The K first of different keys (0: none), in order, into best, which holds
-// zeros: every thread counts the keys before its own.
-__device__ __forceinline__ void select_best(const unsigned long long* key, int parts, int n, int K,
-                                            unsigned long long* best) {
+// The K first of the CTA's different keys (a thread's, 0: none), in order, into
+// best, which holds zeros: those that reach a bound, moved to `found`, each
+// ranked by four threads.  `part`: in any order, with others where they fit.
+__device__ __noinline__ void select_best(LpSmem& sm, unsigned long long k0, unsigned long long k1,
+                                         unsigned long long k2, unsigned long long k3, int K,
+                                         unsigned long long* found, bool part) {
+  const unsigned long long key[kHold] = {k0, k1, k2, k3};
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t least =
+      bound_of(sm, static_cast<uint32_t>(k0 >> 32), static_cast<uint32_t>(k1 >> 32), static_cast<uint32_t>(k2 >> 32),
+               static_cast<uint32_t>(k3 >> 32), K, part ? kLpTop : kLpThreads / 4);
+  unsigned in[kHold];
+  int n = 0;
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    in[k] = __ballot_sync(0xffffffffu, static_cast<uint32_t>(key[k] >> 32) >= least);
+    n += __popc(in[k]);
+  }
+  if (lane == 0) sm.n[warp] = n;
+  __syncthreads();
+  int at = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kLpWarps; ++w) {
+    const int m = sm.n[w];
+    at += w < warp ? m : 0;
+    all += m;
+  }
+#pragma unroll
+  for (int k = 0; k < kHold; ++k) {
+    if ((in[k] >> lane) & 1) found[at + __popc(in[k] & ((1u << lane) - 1))] = key[k];
+    at += __popc(in[k]);
+  }
+  __syncthreads();
+  if (part && all <= kLpTop) {
+    if (tid < all) sm.best[tid] = found[tid];
+    return;
+  }
 #pragma unroll 1
-  for (int j = threadIdx.x; j < parts * n; j += kLpThreads) {
-    const unsigned long long mine = key[(j / n) * kOwn + j % n];
-    if (mine == 0) continue;
-    const int rank = rank_of(key, parts, n, mine);
-    if (rank < K) best[rank] = mine;
+  for (int b = 0; b < all; b += kLpThreads / 4) {
+    const int j = b + (tid >> 2);
+    const unsigned long long mine = j < all ? found[j] : 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int k = tid & 3; k < all; k += 4) rank += found[k] > mine;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if ((tid & 3) == 0 && mine && rank < K) sm.best[rank] = mine;
   }
 }
 
@@ -317,6 +454,8 @@ __device__ __forceinline__ bool lp_wait(unsigned long long* bar, uint32_t parity
 template <class Tag>
 __device__ __noinline__ void search_best(LpSmem& sm, const typename Tag::Elem* z, int i0, int i1, int K) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __syncthreads();
+  if (tid < kLpTop) sm.best[tid] = 0;
   unsigned long long last = ~0ull;
 #pragma unroll 1
   for (int k = 0; k < K; ++k) {
@@ -342,7 +481,7 @@ __device__ __noinline__ void search_best(LpSmem& sm, const typename Tag::Elem* z
 }
 
 template <class Tag, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(const __grid_constant__ LogprobParams p) {
   constexpr int N = Tag::kVec;
   constexpr int U = kFlight;
   extern __shared__ __align__(16) char lp_raw[];
@@ -366,6 +505,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
   const int per = (nv + p.split - 1) / p.split;
   const int v0 = min(nv, part * per), v1 = min(nv, v0 + per);
   float m = kLowest, S = 0.f, E = 0.f, zt = INFINITY;
+  f32x2 S2 = pk2(0.f, 0.f), E2 = S2;  // of even and odd elements
   int count = 0;
   if (TOP && tid < kLpTop) sm.best[tid] = 0;
   if (!fail) {
@@ -374,30 +514,31 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
                                    ahead = zt > -INFINITY && zt < INFINITY ? Raw<Tag>::below(zt) : after;
     typename Raw<Tag>::Count cnt;
     float tau = -INFINITY, mc = 0.f;
-    bool plain = c > 1e7f;
-    int own = 0;  // candidates of the warp
-    // the longest of the warps' lists, an even number; the others filled up
-    // with zeros
-    auto longest = [&](int most) {
-      if (lane == 0) sm.n[warp] = own;
-      __syncthreads();
-      int n = 0;
+    bool plain = !(c > kLeast && c < 1e7f);
+    bool over = false;  // more than its list holds
+    // a thread's keys of the list
+    auto keys = [&](unsigned long long (&key)[kHold]) {
+      static_assert(kOwn <= 32 * kHold, "a warp's list");
+      __syncwarp();
+      const int own = sm.n[warp];
+      over |= own > kOwn;
 #pragma unroll
-      for (int w = 0; w < kLpWarps; ++w) n = max(n, sm.n[w]);
-      n = min((n + 1) & ~1, most);
-      for (int k = own + lane; k < n; k += 32) sm.key[warp * kOwn + k] = 0;
-      __syncthreads();
-      return n;
+      for (int k = 0; k < kHold; ++k)
+        key[k] = lane + 32 * k < min(own, kOwn) ? sm.key[warp * kOwn + lane + 32 * k] : 0;
     };
     const f32x2 c2 = pk2(c, c);
+    // S and U for a reference that lies d (in units of x) lower
+    auto shift = [&](float d) {
+      const float f = exp2f(d);
+      const f32x2 f2 = pk2(f, f);
+      E2 = mul2(f2, fma2(S2, pk2(d, d), E2));
+      S2 = mul2(f2, S2);
+    };
     // the rounding error of m c out of the sums
     auto exact = [&]() {
-      if (m == kLowest) return;  // nothing yet
-      const float d = -fmaf(m, c, -mc), f = exp2f(d);
-      E = f * fmaf(S, d, E);
-      S *= f;
+      if (m != kLowest) shift(-fmaf(m, c, -mc));
     };
-    int round = 0, raise_at = 4;
+    int round = 0, raise_at = kRaise;
     Raw<Tag> now[U];
     // aligned rows come by bulk copies, a warp's slices on its own ring
     const int vfull = p.whole ? min(v1, p.V / N) : v0;
@@ -408,6 +549,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
       if (n > 0 && lane == 0) lp_copy(sm.ring[warp][stage], z + static_cast<long long>(v) * N, n * 16, bar + stage);
     };
     if (lane == 0) {
+      sm.n[warp] = 0;
 #pragma unroll
       for (int k = 0; k < kStages; ++k)
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(lp_ptr(bar + k)) : "memory");
@@ -422,12 +564,18 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
     for (int b = v0; b < v1; b += kLpThreads * U, ++round) {
       const int first = slice(round), n = min(kSlice, vfull - first);
       if (n > 0 && !lp_wait(bar + stage, phase)) bits |= kErrTimeout;
+      const uint4* ring = sm.ring[warp][stage] + lane;
+      if (n >= kSlice) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int k = u * 32 + lane;
-        if (k < n) now[u].raw(sm.ring[warp][stage][k]);
-        else if (first + k < v1) now[u].load(z, first + k, p.V, p.whole);
-        else now[u].none();
+        for (int u = 0; u < U; ++u) now[u].raw(ring[u * 32]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int k = u * 32 + lane;
+          if (k < n) now[u].raw(ring[u * 32]);
+          else if (first + k < v1) now[u].load(z, first + k, p.V, p.whole);
+          else now[u].none();
+        }
       }
       __syncwarp();
       fetch(round + kStages, stage);
@@ -435,128 +583,136 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
         stage = 0;
         phase ^= 1;
       }
+      const float top = Raw<Tag>::top(now);
       if (TOP && round == 0) {
         // of every warp the largest of its threads' maxima: the K-th largest
         // of those different elements is the first bound
-        float v = now[0].top();
-#pragma unroll
-        for (int u = 1; u < U; ++u) v = fmaxf(v, now[u].top());
-        const int take = min((K + kLpWarps - 1) / kLpWarps + 1, kFirst);
+        uint32_t v = order_of(top);
+        const int take = (K + kLpWarps - 1) / kLpWarps + 1;
+        static_assert((kLpTop + kLpWarps - 1) / kLpWarps + 1 <= kFirst, "the warps' maxima");
 #pragma unroll 1
         for (int k = 0; k < take; ++k) {
-          const float w = redux_max(v);
-          if (lane == 0) sm.top[warp * take + k] = w;
+          const uint32_t w = __reduce_max_sync(0xffffffffu, v);
+          if (lane == 0) sm.top[warp * take + k] = order_value(w);
           const unsigned who = __ballot_sync(0xffffffffu, v == w);
-          if (lane == __ffs(who) - 1) v = -INFINITY;
+          if (lane == __ffs(who) - 1) v = 0;
         }
         __syncthreads();
         if (tid < kLpWarps * take) {
           const float mine = sm.top[tid];
           int rank = 0;
-#pragma unroll 8
-          for (int k = 0; k < kLpWarps * take; ++k) {
-            const float o = sm.top[k];
-            rank += o > mine || (o == mine && k < tid);
+#pragma unroll 4
+          for (int k = 0; k < kLpWarps * take; k += 4) {
+            const float4 o = *reinterpret_cast<const float4*>(&sm.top[k]);
+            rank += (o.x > mine || (o.x == mine && k < tid)) + (o.y > mine || (o.y == mine && k + 1 < tid)) +
+                    (o.z > mine || (o.z == mine && k + 2 < tid)) + (o.w > mine || (o.w == mine && k + 3 < tid));
           }
           if (rank == K - 1) sm.tau = mine;
         }
         __syncthreads();
         tau = sm.tau;
       }
-      unsigned hit = 0;
+      // the rank: a slice before the token's logit, behind it, its own
+      const int i0 = first * N, i1 = i0 + kSlice * N;
+      if (i1 <= tok || i0 > tok) {
+        const typename Raw<Tag>::Bound t = i0 > tok ? after : ahead;
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u].count(t, cnt);
+      } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float y[8];
+          Tag::unpackraw(now[u].r, y);
+          const int i = (first + u * 32 + lane) * N;
+#pragma unroll
+          for (int k = 0; k < N; ++k) count += y[k] > zt || (y[k] == zt && i + k < tok);
+        }
+      }
+      if (TOP && top >= tau) {
+        // candidates, a vector and an element at a time
+        uint32_t vectors = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) vectors |= now[u].top() >= tau ? 1u << u : 0u;
+#pragma unroll 1
+        for (; vectors; vectors &= vectors - 1) {
+          const int u = __ffs(vectors) - 1;
+          Raw<Tag> w = now[0];
+#pragma unroll
+          for (int k = 1; k < U; ++k)
+            if (u == k) w = now[k];
+          float y[8];
+          Tag::unpackraw(w.r, y);
+          uint32_t hits = 0;
+#pragma unroll
+          for (int k = 0; k < N; ++k) hits |= y[k] >= tau ? 1u << k : 0u;
+#pragma unroll 1
+          for (; hits; hits &= hits - 1) {
+            const int k = __ffs(hits) - 1, i = (first + u * 32 + lane) * N + k;
+            float v = y[0];
+#pragma unroll
+            for (int j = 1; j < N; ++j)
+              if (k == j) v = y[j];
+            if (i >= p.V) break;
+            const int at = atomicAdd(&sm.n[warp], 1);
+            if (at < kOwn) sm.key[warp * kOwn + at] = key_of(v, i);
+          }
+        }
+      }
+      // the reference
+      if ((top - m) * c > kStep) {  // (the first round's from kLowest, S = 0)
+        exact();
+        shift(fmaxf((m - top) * c, -1e4f));
+        m = top;
+        mc = m * c;
+        plain |= !(fabsf(mc) < 16777216.f);
+      }
+      Raw<Tag>::floor(now);
+      const f32x2 m2 = pk2(-mc, -mc);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (first + u * 32 >= v1) break;
-        const Raw<Tag>& w = now[u];
-        const int i = (first + u * 32 + lane) * N;
-        const float top = w.top();
-        // the reference
-        if ((top - m) * c > kStep) {  // (the first vector's from kLowest, S = 0)
-          exact();
-          const float d = fmaxf((m - top) * c, -1e4f), f = exp2f(d);
-          E = f * fmaf(S, d, E);
-          S *= f;
-          m = top;
-          mc = m * c;
-          plain |= !(fabsf(mc) < 16777216.f);
-        }
-        f32x2 x[4], s2 = pk2(0.f, 0.f), e2 = pk2(0.f, 0.f);
-        w.scaled(c2, pk2(-mc, -mc), x);
+        f32x2 x[4];
+        now[u].scaled(c2, m2, x);
 #pragma unroll
         for (int k = 0; k < N / 2; ++k) {
           float a, d;
           up2(x[k], a, d);
           const f32x2 e = pk2(ex2_fast(a), ex2_fast(d));
-          s2 = add2(s2, e);
-          e2 = fma2(e, x[k], e2);
-        }
-        float a, d;
-        up2(s2, a, d);
-        S += a + d;
-        up2(e2, a, d);
-        E += a + d;
-        // the rank: vectors before the token's, behind it, its own
-        if (i > tok || i + N <= tok) {
-          w.count(i > tok ? after : ahead, cnt);
-        } else {
-          float y[8];
-          Tag::unpackraw(w.r, y);
-#pragma unroll
-          for (int k = 0; k < N; ++k) count += y[k] > zt || (y[k] == zt && i + k < tok);
-        }
-        if (TOP) hit |= static_cast<unsigned>(__any_sync(0xffffffffu, top >= tau)) << u;
-      }
-      if (TOP) {
-        // the warp's candidates (one copy of this code for all vectors)
-#pragma unroll 1
-        while (hit) {
-          const int u = __ffs(hit) - 1;
-          hit &= hit - 1;
-          Raw<Tag> w = now[0];
-#pragma unroll
-          for (int k = 1; k < U; ++k)
-            if (u == k) w = now[k];
-          const int i = (first + u * 32 + lane) * N;
-          float y[8];
-          Tag::unpackraw(w.r, y);
-          unsigned hits = 0;
-#pragma unroll
-          for (int k = 0; k < N; ++k) hits |= (y[k] >= tau && i + k < p.V) ? 1u << k : 0u;
-          const int mine = __popc(hits);
-          int at = mine;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, at, d);
-            if (lane >= d) at += o;
-          }
-          const int sum = __shfl_sync(0xffffffffu, at, 31);
-          at += own - mine;
-          own += sum;
-#pragma unroll
-          for (int k = 0; k < N; ++k) {
-            if ((hits >> k) & 1) {
-              if (at < kOwn) sm.key[warp * kOwn + at] = key_of(y[k], i + k);
-              ++at;
-            }
-          }
+          S2 = add2(S2, e);
+          E2 = fma2(e, x[k], E2);
         }
       }
       count += cnt.take();
       if (TOP) {
         if (round + 1 == raise_at && b + kLpThreads * U < v1) {
-          raise_at *= 8;
-          // a bound from the first candidates of every warp
-          const int n = longest(kRaise);
-          if (tid < kLpWarps * kRaise && tid % kRaise < n) {
-            const unsigned long long mine = sm.key[tid / kRaise * kOwn + tid % kRaise];
-            if (mine && rank_of(sm.key, kLpWarps, n, mine) == K - 1) sm.tau = fmaxf(tau, key_value(mine));
+          raise_at *= kRaise;
+          // a bound from the candidates, of which those below it go
+          unsigned long long key[kHold];
+          keys(key);
+          const uint32_t least = bound_of(
+              sm, static_cast<uint32_t>(key[0] >> 32), static_cast<uint32_t>(key[1] >> 32),
+              static_cast<uint32_t>(key[2] >> 32), static_cast<uint32_t>(key[3] >> 32), K, K + K / 4);
+          tau = fmaxf(tau, order_value(least));
+          int own = 0;
+#pragma unroll
+          for (int k = 0; k < kHold; ++k) {
+            const bool in = static_cast<uint32_t>(key[k] >> 32) >= least;
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            if (in) sm.key[warp * kOwn + own + __popc(who & ((1u << lane) - 1))] = key[k];
+            own += __popc(who);
           }
-          __syncthreads();
-          tau = sm.tau;
+          if (lane == 0) sm.n[warp] = own;
+          __syncwarp();
         }
       }
     }
     exact();
+    {
+      float a, d;
+      up2(S2, a, d);
+      S = a + d;
+      up2(E2, a, d);
+      E = a + d;
+    }
     // a masked token: the masked ones before it
     if (tok_ok && zt == -INFINITY)
       for (int i = v0 * N + tid; i < min(tok, v1 * N); i += kLpThreads) count += Tag::load1(z + i) == -INFINITY;
@@ -581,23 +737,24 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
       sm.U[warp] = E;
       sm.count[warp] = count;
     }
-    const int n = TOP ? longest(kOwn) : 0;  // (and the barrier)
-    if (!TOP) __syncthreads();
+    bool full = false;
     if (TOP) {
-      bool full = false;
-#pragma unroll
-      for (int w = 0; w < kLpWarps; ++w) full |= sm.n[w] > kOwn;
+      unsigned long long key[kHold];
+      keys(key);
+      full = __syncthreads_or(over);
+      select_best(sm, key[0], key[1], key[2], key[3], K, reinterpret_cast<unsigned long long*>(sm.ring),
+                  p.split > 1);
       if (full) search_best<Tag>(sm, z, v0 * N, min(p.V, v1 * N), K);
-      else select_best(sm.key, kLpWarps, n, K, sm.best);
+    } else {
+      __syncthreads();
     }
-    if (warp == 0) {
-      const bool in = lane < kLpWarps;
-      m = in ? sm.m[lane] : kLowest;
-      S = in ? sm.S[lane] : 0.f;
-      E = in ? sm.U[lane] : 0.f;
-      join_warp(c, m, S, E);
-      count = __reduce_add_sync(0xffffffffu, in ? sm.count[lane] : 0);
-    }
+    // (by every warp: shuffles where only some warps run cost 250 clocks each)
+    const bool in = lane < kLpWarps;
+    m = in ? sm.m[lane] : kLowest;
+    S = in ? sm.S[lane] : 0.f;
+    E = in ? sm.U[lane] : 0.f;
+    join_warp(c, m, S, E);
+    count = __reduce_add_sync(0xffffffffu, in ? sm.count[lane] : 0);
     __syncthreads();
   }
   bool last = true;
@@ -605,7 +762,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
     Part* parts = p.parts + static_cast<long long>(r) * p.split;
     unsigned long long* tk = p.part_key + static_cast<long long>(r) * p.split * kLpTop;
     if (!fail) {
-      if (TOP && tid < K) {
+      if (TOP && tid < kLpTop) {
         tk[part * kLpTop + tid] = sm.best[tid];
       }
       if (tid == 0) {
@@ -626,21 +783,24 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
     if (!last) return;
     __threadfence();
     if (!fail) {
-      if (warp == 0) {  // lane k holds part k
-        const bool in = lane < p.split;
-        m = in ? __ldcg(&parts[lane].m) : kLowest;
-        S = in ? __ldcg(&parts[lane].S) : 0.f;
-        E = in ? __ldcg(&parts[lane].U) : 0.f;
-        join_warp(c, m, S, E);
-        count = __reduce_add_sync(0xffffffffu, in ? __ldcg(&parts[lane].count) : 0);
-      }
+      const bool in = lane < p.split;  // lane k holds part k
+      m = in ? __ldcg(&parts[lane].m) : kLowest;
+      S = in ? __ldcg(&parts[lane].S) : 0.f;
+      E = in ? __ldcg(&parts[lane].U) : 0.f;
+      join_warp(c, m, S, E);
+      count = __reduce_add_sync(0xffffffffu, in ? __ldcg(&parts[lane].count) : 0);
       if constexpr (TOP) {
-        const int n = p.split * K;
+        const int n = p.split * kLpTop;
         if (tid < kLpTop) sm.best[tid] = 0;
-        for (int j = tid; j < n + (n & 1); j += kLpThreads)
-          sm.key[j] = j < n ? __ldcg(tk + (j / K) * kLpTop + j % K) : 0ull;
-        __syncthreads();
-        select_best(sm.key, 1, n + (n & 1), K, sm.best);
+        unsigned long long key[kHold];
+        static_assert(kMaxSplit * kLpTop <= kHold * kLpThreads && sizeof(sm.ring) >= sizeof(key) * kLpThreads,
+                      "the parts' lists");
+#pragma unroll
+        for (int k = 0; k < kHold; ++k) {
+          const int j = tid + kLpThreads * k;
+          key[k] = j < n ? __ldcg(tk + j) : 0ull;
+        }
+        select_best(sm, key[0], key[1], key[2], key[3], K, reinterpret_cast<unsigned long long*>(sm.ring), false);
         __syncthreads();
       }
     }
@@ -683,17 +843,26 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) logprob_kernel(const __gr
   }
 }
 
-// Parts of a row: as many as make the work of the longest place shortest, in
-// elements: what a CTA reads; its start and end, and its list of K; and the
-// join of the parts' lists (measured at R = 8 .. 4096: 16 K, 1.5 K and 0.2 K
-// elements' time).
-int split_of(int R, int V, int K) {
-  const long long places = 152 * kLpCtas;
+// Parts of a row: as many as make the whole shortest, in elements' time on a
+// full SM (24 K bf16 or 12 K fp32 elements a microsecond).  n CTAs of an SM take
+// turns (one alone reaches 7/8 of the rate) and begin and end in 4 us, or 8 us and
+// 0.1 us K where the best are asked for; the join of the parts costs 1.3 us.
+// (128256 bf16 logits, K = 0: 9.9 us whole, 5.8, 4.9, 5.5 in 4, 8, 31 parts; 384
+// rows of 151936, K = 20: 43 us whole, 54 in two.)
+int split_of(int R, int V, int K, bool half) {
+  const long long us = half ? 24000 : 12000, sms = 152, ctas = K > 0 && !half ? 4 : 3;
+  const long long fixed = K > 0 ? 8 * us + us * K / 10 : 4 * us;
+  const int most = K > 0 && half ? 14 : 10;  // tenths of an element's time
+  const auto wave = [&](long long n, long long v) {
+    return n == 0 ? 0 : fixed + us * (n - 1) / 2 + (n == 1 ? v * 8 / 7 : v * n) * most / 10;
+  };
   long long least = 0;
   int best = 1;
-  for (int s = 1; s <= kMaxSplit && (s == 1 || V / s >= 4096); ++s) {
-    const long long waves = (static_cast<long long>(R) * s + places - 1) / places;
-    const long long cost = waves * (V / s + 16384 + 1536 * K) + (s > 1 ? 16384 + 200ll * s * K : 0);
+  const int parts = R <= kCounters ? kMaxSplit : 1;
+  for (int s = 1; s <= parts && (s == 1 || V / s >= 4096); ++s) {
+    const long long all = static_cast<long long>(R) * s, v = V / s;
+    const long long cost = all / (sms * ctas) * wave(ctas, v) + wave((all % (sms * ctas) + sms - 1) / sms, v) +
+                           (s > 1 ? us * 13 / 10 + us * s / 50 : 0);
     if (s == 1 || cost < least) {
       least = cost;
       best = s;
@@ -713,31 +882,30 @@ cudaError_t launch_t(const LogprobParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-struct LpLayout {
-  size_t counter, parts, key, total;
-};
-LpLayout lp_layout(int R, int V, int K) {
-  const size_t n = static_cast<size_t>(R) * split_of(R, V, K);
-  LpLayout L;
-  L.counter = 256;
-  L.parts = (L.counter + 4ull * R + 255) / 256 * 256;
-  L.key = L.parts + sizeof(Part) * n;
-  L.total = L.key + 8 * kLpTop * n;
-  return L;
-}
+// The counters have a place of their own in front, so that calls of different
+// sizes may take turns with a workspace.
+constexpr size_t kPartsAt = 256 + 4 * kCounters;
+size_t part_keys_at(size_t n) { return kPartsAt + sizeof(Part) * n; }
 
 }  // namespace
 
-size_t logprobs_bytes(int R, int V, int K) { return split_of(R, V, K) > 1 ? lp_layout(R, V, K).total : 256; }
+size_t logprobs_bytes(int R, int V, int K) {
+  size_t most = 256;
+  for (const bool half : {false, true}) {
+    const int split = split_of(R, V, K, half);
+    const size_t n = static_cast<size_t>(R) * split;
+    if (split > 1) most = std::max(most, part_keys_at(n) + 8 * kLpTop * n);
+  }
+  return most;
+}
 
 cudaError_t launch_logprobs(const LogprobParams& p0, int dtype, bool vec, cudaStream_t s) {
   LogprobParams p = p0;
-  p.split = split_of(p.R, p.V, p.K);
-  const LpLayout L = lp_layout(p.R, p.V, p.K);
+  p.split = split_of(p.R, p.V, p.K, dtype == 1);
   char* ws = reinterpret_cast<char*>(p.err);
-  p.counter = reinterpret_cast<int*>(ws + L.counter);
-  p.parts = reinterpret_cast<Part*>(ws + L.parts);
-  p.part_key = reinterpret_cast<unsigned long long*>(ws + L.key);
+  p.counter = reinterpret_cast<int*>(ws + 256);
+  p.parts = reinterpret_cast<Part*>(ws + kPartsAt);
+  p.part_key = reinterpret_cast<unsigned long long*>(ws + part_keys_at(static_cast<size_t>(p.R) * p.split));
   p.whole = vec;
   return dtype == 1 ? launch_t<BF16Tag>(p, s) : launch_t<F32Tag>(p, s);
 }
