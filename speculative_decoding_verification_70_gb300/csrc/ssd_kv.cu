@@ -8,26 +8,31 @@
 // in fp32, rounded once.  It reads q, k, v and one row of the cosine/sine
 // table a token and writes as much: bound by HBM for a batch, by the chain
 // of loads (length -> way to the root -> table row and page id) for a few
-// tokens.
+// tokens.  The grid is one wave, so that the chain is waited for once, and its
+// places are found once a token, by one lane; a lane holds 16 entries of a
+// head, which halves the address arithmetic of eight.  64 trees of 21 tokens,
+// 64 + 16 heads of 128 (55 MB): 14.8 us, 3.8 TB/s (a CTA per token, 8 entries a
+// lane: 24.6 us); 512 chains of 8, 32 + 16 heads of 64: 12.7 us, 4.0 TB/s (26.8);
+// one chain of 8: 3.6 us.
 // kv_commit_kernel: a copy of the accepted rows, bound by HBM (or by its two
 // chained round trips).
+#include <algorithm>
+
+#include "ssd_device.cuh"
 #include "ssd_kv.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kAppThreads = 256;
-constexpr int kAppUnroll = 4;  // head vectors in flight per thread
+constexpr int kAppThreads = 128;
+constexpr int kAppUnroll = 2;   // head vectors in flight per thread
+constexpr int kAppCtas = 7;     // per SM
+constexpr int kAppTokens = 32;  // most tokens of a CTA (a lane finds each one's place)
 
+// Eight entries of a head vector.
 template <bool VEC>
 __device__ __forceinline__ uint4 load8(const char* p) {
-  if (VEC) {
-    uint4 v;
-    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-  }
+  if (VEC) return *reinterpret_cast<const uint4*>(p);
   const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
   uint32_t w[4];
 #pragma unroll
@@ -36,164 +41,227 @@ __device__ __forceinline__ uint4 load8(const char* p) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA per (token, range of heads).  A head vector is spread over D / 8
-// lanes, 16 bytes each; a thread keeps its eight columns for every head it
-// handles, so the cosines, sines and weights are loaded once.  The raw head
-// vectors are loaded before the token's length, tree and page are known:
-// the two latencies overlap.
-template <class T, int D, bool VEC>
-__global__ void __launch_bounds__(kAppThreads) kv_append_kernel(const AppendParams p) {
-  constexpr int LP = D / 8;                    // lanes per head vector
-  constexpr int GROUPS = kAppThreads / LP;     // head vectors side by side
-  const int tid = threadIdx.x;
-  const int g = tid / LP, e = (tid % LP) * 8;  // group; first column
-  const int N = p.nodes.N;
-  const int b = static_cast<int>(blockIdx.x / N), j = static_cast<int>(blockIdx.x % N);
-  const int Hkv = p.kv.Hkv, Hq = p.Hq, Htot = Hq + 2 * Hkv;
-  const int h0 = blockIdx.y * p.heads_per_cta;
-  const int h1 = min(Htot, h0 + p.heads_per_cta);
+struct AppSmem {
+  // of each token: where its heads lie and go to, heads numbered through q, k
+  // and v (0: nowhere); its row of the table, or null
+  uint64_t src[kAppTokens][4], dst[kAppTokens][4];
+  const float* turn[kAppTokens];
+  int there[kAppTokens];
+  alignas(16) float w[2][4][8][4];  // weights of q's and k's norm: a lane's a, b, a, b, four each
+};
 
-  const char* qrow = p.q + 2 * (b * p.q_b + j * p.q_n);
-  const char* krow = p.k + 2 * (b * p.kv_b + j * p.kv_n);
-  const char* vrow = p.v + 2 * (b * p.kv_b + j * p.kv_n);
-  auto src = [&](int h) -> const char* {
-    if (h < Hq) return qrow + 2 * (h * p.q_h + e);
-    if (h < Hq + Hkv) return krow + 2 * ((h - Hq) * p.kv_h + e);
-    return vrow + 2 * ((h - Hq - Hkv) * p.kv_h + e);
-  };
-  uint4 raw[kAppUnroll];
-#pragma unroll
-  for (int u = 0; u < kAppUnroll; ++u) {
-    const int h = h0 + u * GROUPS + g;
-    if (h < h1) raw[u] = load8<VEC>(src(h));
-  }
-
-  // the token's place
-  const int ctx = p.nodes.ctx_len[b];
-  const int nn = p.nodes.n_nodes ? p.nodes.n_nodes[b] : N;
-  bool bad_len, broken;
-  const int n = seq_nodes(ctx, nn, N, p.kv.width, p.kv.ps, bad_len);
-  uint64_t mask;
-  int depth;
-  bool there = node_way(p.nodes.parent ? p.nodes.parent + static_cast<long long>(b) * N : nullptr,
-                        n, j, mask, depth, broken);
-  const long long pos = static_cast<long long>(ctx) + depth;
-  if (there && p.rot > 0 && pos >= p.max_pos) {
-    there = false;
-    bad_len = true;
-  }
-  int page = -1, off = 0;
-  bool store = false;
-  if (there) {
-    store = kv_slot(p.kv.table + b * p.kv.table_stride, p.kv.width, p.kv.pages, p.kv.ps,
-                    static_cast<long long>(ctx) + j, page, off);
-  }
-  if (tid == 0 && blockIdx.y == 0) {
-    const int bits = (bad_len ? kErrBadLength : 0) | (broken ? kErrBadTree : 0) |
-                     (there && !store ? kErrBadPage : 0);
-    if (bits) atomicOr(p.err, bits);
-  }
-
-  // this thread's columns of the rotation and the weights
-  float cs[8], sn[8], wq[8], wk[8];
+// A CTA takes a range of (token, head) pairs; lanes of its first warp find the
+// places of the range's tokens side by side, while the first head vectors are
+// on their way.  A head vector is spread over D / 16 lanes, which hold the pairs
+// of a rotation whole: eight entries (a) and their eight partners (b).
+template <class T, int D, bool VEC, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kAppThreads, kAppCtas) kv_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int LP = D / 16;                // lanes per head vector
+  constexpr int GROUPS = kAppThreads / LP;  // head vectors side by side
+  constexpr int U = kAppUnroll;
+  __shared__ AppSmem sm;
+  const int tid = threadIdx.x, g = tid / LP, l = tid % LP;
+  const int Hq = p.Hq, Hkv = p.kv.Hkv, Htot = Hq + 2 * Hkv, N = p.nodes.N;
+  const long long i0 = static_cast<long long>(blockIdx.x) * p.items;
+  const int items = static_cast<int>(min(static_cast<long long>(p.items), p.all - i0));
+  const bool small = p.all <= INT32_MAX;
+  const int t0 = small ? static_cast<int>(i0) / Htot : static_cast<int>(i0 / Htot);
+  const int h0 = static_cast<int>(i0 - static_cast<long long>(t0) * Htot);
+  // this lane's columns: ea.. and eb.., partners where they turn
   const int half = p.rot / 2;
-  const bool turns = there && e < p.rot;
-  const bool upper = e >= half;
-  if (turns) {
-    const float* row = p.cos_sin + pos * p.rot;
-    if (p.interleaved) {
-      const float4 c = *reinterpret_cast<const float4*>(row + e / 2);
-      const float4 s = *reinterpret_cast<const float4*>(row + half + e / 2);
-      cs[0] = cs[1] = c.x; cs[2] = cs[3] = c.y; cs[4] = cs[5] = c.z; cs[6] = cs[7] = c.w;
-      sn[0] = sn[1] = s.x; sn[2] = sn[3] = s.y; sn[4] = sn[5] = s.z; sn[6] = sn[7] = s.w;
-    } else {
-      const int i = upper ? e - half : e;
+  const bool turns = 16 * l < p.rot;
+  const int ea = NEIGHBOURS || !turns ? 16 * l : 8 * l;
+  const int eb = NEIGHBOURS || !turns ? 16 * l + 8 : half + 8 * l;
+
+  auto kind = [&](int h) { return (h >= Hq) + (h >= Hq + Hkv); };
+  // where head 0 of q, k or v would lie, counted on to k's and v's heads
+  auto source = [&](int t, int kind) {
+    const int b = t / N, j = t % N;
+    return kind == 0   ? reinterpret_cast<uint64_t>(p.q) + 2 * (b * p.q_b + j * p.q_n)
+           : kind == 1 ? reinterpret_cast<uint64_t>(p.k) + 2 * (b * p.kv_b + j * p.kv_n - Hq * p.kv_h)
+                       : reinterpret_cast<uint64_t>(p.v) + 2 * (b * p.kv_b + j * p.kv_n - (Hq + Hkv) * p.kv_h);
+  };
+  const uint64_t q_h = 2 * p.q_h, kv_h = 2 * p.kv_h;
+  struct Vec {
+    uint4 a, b;
+  };
+  auto load = [&](uint64_t base, int h) {
+    const char* r = reinterpret_cast<const char*>(base + (h < Hq ? q_h : kv_h) * static_cast<uint32_t>(h));
+    return Vec{load8<VEC>(r + 2 * ea), load8<VEC>(r + 2 * eb)};
+  };
+  const int tokens = (h0 + items + Htot - 1) / Htot;
+  if (tid < tokens) {
 #pragma unroll
-      for (int t = 0; t < 8; t += 4) {
-        *reinterpret_cast<float4*>(cs + t) = *reinterpret_cast<const float4*>(row + i + t);
-        *reinterpret_cast<float4*>(sn + t) = *reinterpret_cast<const float4*>(row + half + i + t);
-      }
+    for (int k = 0; k < 3; ++k) sm.src[tid][k] = source(t0 + tid, k);
+  }
+  __syncthreads();
+  // the thread's pairs, GROUPS apart: token and head of each in flight, and of
+  // the next to load
+  Vec raw[U];
+  int tag[U];
+  const int dt = GROUPS / Htot, dh = GROUPS % Htot;
+  int lt = (h0 + g) / Htot, lh = (h0 + g) % Htot, li = g;
+  auto next = [&]() {
+    lh += dh;
+    lt += dt;
+    if (lh >= Htot) {
+      lh -= Htot;
+      ++lt;
     }
+    li += GROUPS;
+  };
+  constexpr int kTag = 20;  // bits of a head's number
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (li < items) raw[u] = load(sm.src[lt][kind(lh)], lh);
+    tag[u] = (lt << kTag) | lh;
+    next();
+  }
+
+  // the tokens' places
+  if (tid < tokens) {
+    const int b = (t0 + tid) / N, j = (t0 + tid) % N;
+    const int ctx = p.nodes.ctx_len[b];
+    const int nn = p.nodes.n_nodes ? p.nodes.n_nodes[b] : N;
+    bool bad_len, broken;
+    const int n = seq_nodes(ctx, nn, N, p.kv.width, p.kv.ps, bad_len);
+    uint64_t mask;
+    int depth;
+    bool there = node_way(p.nodes.parent ? p.nodes.parent + static_cast<long long>(b) * N : nullptr, n, j, mask, depth,
+                          broken);
+    const long long pos = static_cast<long long>(ctx) + depth;
+    if (there && p.rot > 0 && pos >= p.max_pos) {
+      there = false;
+      bad_len = true;
+    }
+    int page = -1, off = 0;
+    bool store = false;
+    if (there)
+      store = kv_slot(p.kv.table + b * p.kv.table_stride, p.kv.width, p.kv.pages, p.kv.ps,
+                      static_cast<long long>(ctx) + j, page, off);
+    const int bits = (bad_len ? kErrBadLength : 0) | (broken ? kErrBadTree : 0) | (there && !store ? kErrBadPage : 0);
+    if (bits) atomicOr(p.err, bits);
+    sm.dst[tid][0] = reinterpret_cast<uint64_t>(p.q_out) + 2 * (static_cast<long long>(t0 + tid) * Hq * D);
+    sm.dst[tid][1] = store ? reinterpret_cast<uint64_t>(p.kv.k) +
+                                 2 * (page * p.kv.k_page + off * p.kv.k_slot - Hq * p.kv.k_head)
+                           : 0;
+    sm.dst[tid][2] = store ? reinterpret_cast<uint64_t>(p.kv.v) +
+                                 2 * (page * p.kv.v_page + off * p.kv.v_slot - (Hq + Hkv) * p.kv.v_head)
+                           : 0;
+    sm.turn[tid] = there && p.rot > 0 ? p.cos_sin + pos * p.rot : nullptr;
+    sm.there[tid] = there;
   }
   const bool norm = p.q_norm != nullptr;
-  if (norm) {
-    unpack8<T>(load8<false>(p.q_norm + 2 * e), wq);
-    unpack8<T>(load8<false>(p.k_norm + 2 * e), wk);
-  }
-  const int lane = tid & 31;
-  const int partner = upper ? lane - half / 8 : lane + half / 8;  // neighbour pairs: unused
-
-  for (int base = h0; base < h1; base += kAppUnroll * GROUPS) {
-    if (base != h0) {
+  if (norm && tid < 4 * LP) {  // eight of a lane's weights each
+    const bool second = tid & 1, isk = tid >= 2 * LP;
+    const int lane = tid / 2 % LP;
+    const bool turn = 16 * lane < p.rot;
+    const unsigned short* w = reinterpret_cast<const unsigned short*>(isk ? p.k_norm : p.q_norm);
 #pragma unroll
-      for (int u = 0; u < kAppUnroll; ++u) {
-        const int h = base + u * GROUPS + g;
-        if (h < h1) raw[u] = load8<VEC>(src(h));
-      }
+    for (int k = 0; k < 8; ++k) {
+      const int i = NEIGHBOURS ? 16 * lane + 2 * k + second
+                               : !turn ? 16 * lane + 8 * second + k : half * second + 8 * lane + k;
+      sm.w[isk][2 * (k / 4) + second][lane][k % 4] = T::lo(w[i]);
     }
+  }
+  __syncthreads();
+
+  const uint64_t k_head = 2 * p.kv.k_head, v_head = 2 * p.kv.v_head;
+#pragma unroll 1
+  for (int b = 0; b < items; b += U * GROUPS) {
 #pragma unroll
-    for (int u = 0; u < kAppUnroll; ++u) {
-      const int h = base + u * GROUPS + g;
-      if (base + u * GROUPS >= h1) break;  // uniform over the CTA
-      const bool act = h < h1;
+    for (int u = 0; u < U; ++u) {
+      if (b + u * GROUPS >= items) break;  // uniform over the CTA
+      const bool act = b + u * GROUPS + g < items;
+      const int h = tag[u] & ((1 << kTag) - 1), t = act ? tag[u] >> kTag : 0;
       const bool isq = h < Hq, isv = h >= Hq + Hkv;
-      uint4 o = act ? raw[u] : make_uint4(0, 0, 0, 0);
-      float x[8];
-      unpack8<T>(o, x);
-      if (norm) {
-        float ss = 0.f;
+      Vec o = raw[u];
+      if ((norm || p.rot > 0) && __any_sync(0xffffffffu, act && !isv)) {
+        const uint32_t w[8] = {o.a.x, o.a.y, o.a.z, o.a.w, o.b.x, o.b.y, o.b.z, o.b.w};
+        f32x2 xa[4], xb[4];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) ss = fmaf(x[t], x[t], ss);
-#pragma unroll
-        for (int m = LP / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) x[t] = x[t] * inv * (isq ? wq[t] : wk[t]);
-      }
-      if (p.rot > 0) {
-        float y[8];
-        if (p.interleaved) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) y[t] = x[t ^ 1];
-        } else {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) y[t] = __shfl_sync(0xffffffffu, x[t], partner & 31);
-        }
-        if (turns) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const bool second = p.interleaved ? (t & 1) : upper;
-            const float c = x[t] * cs[t], s = y[t] * sn[t];
-            x[t] = second ? c + s : c - s;
+        for (int k = 0; k < 4; ++k) {
+          if (NEIGHBOURS) {
+            xa[k] = pk2(T::lo(w[2 * k]), T::lo(w[2 * k + 1]));
+            xb[k] = pk2(T::hi(w[2 * k]), T::hi(w[2 * k + 1]));
+          } else {
+            xa[k] = pk2(T::lo(w[k]), T::hi(w[k]));
+            xb[k] = pk2(T::lo(w[k + 4]), T::hi(w[k + 4]));
           }
         }
+        f32x2 inv2 = pk2(1.f, 1.f);
+        if (norm) {
+          f32x2 q = mul2(xa[0], xa[0]);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) q = fma2(xa[k], xa[k], q);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q = fma2(xb[k], xb[k], q);
+          float s0, s1;
+          up2(q, s0, s1);
+          float ss = s0 + s1;
+#pragma unroll
+          for (int m = LP / 2; m > 0; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+          const float inv = rsqrtf(fmaf(ss, 1.0f / D, p.eps));  // (2 units of the last place of fp32)
+          inv2 = pk2(inv, inv);
+        }
+        const float* turn = sm.turn[t];
+        const bool rotate = turn && turns;
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {  // four of a, four of b
+          if (norm) {
+            const float4 wa = *reinterpret_cast<const float4*>(sm.w[!isq][k][l]),
+                         wb = *reinterpret_cast<const float4*>(sm.w[!isq][k + 1][l]);
+            xa[k] = mul2(mul2(xa[k], inv2), pk2(wa.x, wa.y));
+            xa[k + 1] = mul2(mul2(xa[k + 1], inv2), pk2(wa.z, wa.w));
+            xb[k] = mul2(mul2(xb[k], inv2), pk2(wb.x, wb.y));
+            xb[k + 1] = mul2(mul2(xb[k + 1], inv2), pk2(wb.z, wb.w));
+          }
+          if (rotate) {
+            const float4 c = *reinterpret_cast<const float4*>(turn + 8 * l + 2 * k);
+            const float4 s = *reinterpret_cast<const float4*>(turn + half + 8 * l + 2 * k);
+            const f32x2 cc[2] = {pk2(c.x, c.y), pk2(c.z, c.w)}, sn[2] = {pk2(s.x, s.y), pk2(s.z, s.w)};
+            const f32x2 neg[2] = {pk2(-s.x, -s.y), pk2(-s.z, -s.w)};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const f32x2 y = xa[k + i], z = xb[k + i];
+              xa[k + i] = fma2(z, neg[i], mul2(y, cc[i]));
+              xb[k + i] = fma2(y, sn[i], mul2(z, cc[i]));
+            }
+          }
+        }
+        if (!isv) {
+          uint32_t r[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float a0, a1, b0, b1;
+            up2(xa[k], a0, a1);
+            up2(xb[k], b0, b1);
+            r[NEIGHBOURS ? 2 * k : k] = NEIGHBOURS ? T::pack(a0, b0) : T::pack(a0, a1);
+            r[NEIGHBOURS ? 2 * k + 1 : k + 4] = NEIGHBOURS ? T::pack(a1, b1) : T::pack(b0, b1);
+          }
+          o.a = make_uint4(r[0], r[1], r[2], r[3]);
+          o.b = make_uint4(r[4], r[5], r[6], r[7]);
+        }
       }
-      if (!isv && (norm || p.rot > 0)) o = pack8<T>(x);
-      if (!act) continue;
-      if (isq) {
-        if (!there) o = make_uint4(0, 0, 0, 0);
-        char* d = p.q_out + 2 * ((static_cast<long long>(blockIdx.x) * Hq + h) * D + e);
-        *reinterpret_cast<uint4*>(d) = o;
-      } else if (store) {
-        char* d = isv ? p.kv.v + 2 * (page * p.kv.v_page + off * p.kv.v_slot +
-                                      (h - Hq - Hkv) * p.kv.v_head + e)
-                      : p.kv.k + 2 * (page * p.kv.k_page + off * p.kv.k_slot +
-                                      (h - Hq) * p.kv.k_head + e);
-        *reinterpret_cast<uint4*>(d) = o;
+      const uint64_t base = sm.dst[t][kind(h)];
+      if (act && base) {
+        if (isq && !sm.there[t]) o.a = o.b = make_uint4(0, 0, 0, 0);
+        char* d = reinterpret_cast<char*>(base + (isq ? 2 * D : isv ? v_head : k_head) * static_cast<uint32_t>(h));
+        *reinterpret_cast<uint4*>(d + 2 * ea) = o.a;
+        *reinterpret_cast<uint4*>(d + 2 * eb) = o.b;
       }
+      if (li < items) raw[u] = load(sm.src[lt][kind(lh)], lh);
+      tag[u] = (lt << kTag) | lh;
+      next();
     }
   }
 }
 
-template <class T>
-cudaError_t append_t(const AppendParams& p, int D, bool vec, dim3 grid, cudaStream_t s) {
-  if (D == 128) {
-    if (vec) kv_append_kernel<T, 128, true><<<grid, kAppThreads, 0, s>>>(p);
-    else kv_append_kernel<T, 128, false><<<grid, kAppThreads, 0, s>>>(p);
-  } else {
-    if (vec) kv_append_kernel<T, 64, true><<<grid, kAppThreads, 0, s>>>(p);
-    else kv_append_kernel<T, 64, false><<<grid, kAppThreads, 0, s>>>(p);
-  }
+template <class T, int D>
+cudaError_t append_t(const AppendParams& p, bool vec, unsigned grid, cudaStream_t s) {
+  const auto kernel = vec ? (p.interleaved ? kv_append_kernel<T, D, true, true> : kv_append_kernel<T, D, true, false>)
+                          : (p.interleaved ? kv_append_kernel<T, D, false, true> : kv_append_kernel<T, D, false, false>);
+  kernel<<<grid, kAppThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -318,17 +386,16 @@ __global__ void __launch_bounds__(kComThreads) kv_commit_kernel(const CommitPara
 
 cudaError_t launch_kv_append(const AppendParams& p0, int dtype, int D, bool vec, cudaStream_t s) {
   AppendParams p = p0;
-  const long long tokens = static_cast<long long>(p.nodes.B) * p.nodes.N;
-  const int Htot = p.Hq + 2 * p.kv.Hkv;
-  const int groups = kAppThreads / (D / 8);
-  // few tokens: the heads over more CTAs, up to one round of loads each
-  const int most = (Htot + groups - 1) / groups;
-  int split = static_cast<int>(tokens >= 608 ? 1 : (608 + tokens - 1) / tokens);
-  split = split < most ? split : most;
-  const int rounds = (most + split - 1) / split;
-  p.heads_per_cta = rounds * groups;
-  const dim3 grid(static_cast<unsigned>(tokens), (Htot + p.heads_per_cta - 1) / p.heads_per_cta);
-  return dtype == Bf16::kId ? append_t<Bf16>(p, D, vec, grid, s) : append_t<F16>(p, D, vec, grid, s);
+  const int Htot = p.Hq + 2 * p.kv.Hkv, groups = kAppThreads / (D / 16);
+  p.all = static_cast<long long>(p.nodes.B) * p.nodes.N * Htot;
+  // pairs of a CTA: one wave of CTAs, at least a head vector a thread, at most
+  // as many as kAppTokens tokens surely hold
+  const long long places = 152 * kAppCtas;
+  const long long each = (p.all + places - 1) / places, most = static_cast<long long>(kAppTokens - 2) * Htot;
+  p.items = static_cast<int>(std::min((each + groups - 1) / groups * groups, most));
+  const unsigned grid = static_cast<unsigned>((p.all + p.items - 1) / p.items);
+  if (dtype == Bf16::kId) return D == 128 ? append_t<Bf16, 128>(p, vec, grid, s) : append_t<Bf16, 64>(p, vec, grid, s);
+  return D == 128 ? append_t<F16, 128>(p, vec, grid, s) : append_t<F16, 64>(p, vec, grid, s);
 }
 
 cudaError_t launch_kv_commit(const CommitParams& p0, cudaStream_t s) {

@@ -147,7 +147,8 @@ struct AppendParams {
   const char* q_norm;
   const char* k_norm;
   float eps;
-  int heads_per_cta;
+  int items;      // (token, head) pairs of a CTA
+  long long all;  // of the call
   int* err;
 };
 

@@ -112,7 +112,8 @@ ssd_status ssd_kv_append(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, i
   p.q_norm = static_cast<const char*>(q_norm);
   p.k_norm = static_cast<const char*>(k_norm);
   p.eps = eps;
-  p.heads_per_cta = 0;
+  p.items = 0;
+  p.all = 0;
   p.err = static_cast<int*>(ws);
   const bool vec = rows16(q, q_b, q_n, q_h) && rows16(k, kv_b, kv_n, kv_h) && aligned(v, 16);
   ProfScope ps("kv_append", S(stream));
