@@ -66,11 +66,13 @@ constexpr float kNoScore = -1e30f;   // m of a row that has seen nothing
 constexpr int kSmemMax = 227 * 1024;
 
 // A CTA's range of tiles, for the joining kernel.
-struct Range {
+struct alignas(16) Range {
   long long lo;          // first tile (its position in cost)
-  int b, h, rb, t0, T;   // its item, its place there, the item's tiles
+  int t0;                // its place in its item
   int used;              // 0: a range without tiles
+  int b, h, rb, T;       // its item, the item's tiles
 };
+static_assert(sizeof(Range) == 32, "read as two vectors");
 
 struct Args {
   NodesView nodes;
@@ -100,6 +102,7 @@ struct Args {
   float* part_o;            // [2 ctas][cols][D]
   float2* part_ml;          // [2 ctas][cols]
   struct Range* ranges;     // [ctas]
+  unsigned long long per_cta;  // 2^64 / ctas, rounded up
   int* err;
 };
 
@@ -320,8 +323,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // ---------------------------------------------------------------------------
 // the tiles of the batch
 // ---------------------------------------------------------------------------
+// n / tk (most pages fill tiles: a shift instead of a division)
+__device__ __forceinline__ int by_tile(const Args& a, int n) { return a.tk == kTile ? n / kTile : n / a.tk; }
 __device__ __forceinline__ int tiles_of(const Args& a, int tot) {
-  if (a.ps <= kTile) return (tot + a.tk - 1) / a.tk;
+  if (a.ps <= kTile) return by_tile(a, tot + a.tk - 1);
   return (tot / a.ps) * a.tpp + (tot % a.ps + kTile - 1) / kTile;
 }
 // First slot of tile t, and how many it holds.
@@ -357,7 +362,7 @@ __device__ __noinline__ SeqTiles seq_tiles(const Args& a, int b) {
   bool bad;
   q.tot = seq_len(a, b, q.ctx, bad);
   q.T = tiles_of(a, q.tot);
-  q.tail = a.ps <= kTile ? q.ctx / a.tk : (q.ctx / a.ps) * a.tpp + (q.ctx % a.ps) / kTile;
+  q.tail = a.ps <= kTile ? by_tile(a, q.ctx) : (q.ctx / a.ps) * a.tpp + (q.ctx % a.ps) / kTile;
   return q;
 }
 
@@ -969,7 +974,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
           if (a.lse) a.lse[orow + row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
           if (empty) row = ~row;
         } else {
-          a.part_ml[pslot + cc] = make_float2(M, L);
+          a.part_ml[pslot + cc] = make_float2(M, absent ? 0.f : L);  // (0: an empty row)
         }
       }
       so.row[cc] = row;
@@ -1087,6 +1092,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   Misc& sm = *reinterpret_cast<Misc*>(P + a.pbytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = gridDim.x, B = a.nodes.B;
+  const int per = (B + kAttnThreads - 1) / kAttnThreads;
+  if (tid * per < B) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.nodes.ctx_len + tid * per));
 
   if (tid == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
@@ -1127,7 +1134,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // ---- this CTA's range: tiles before each sequence (a block scan over the
   // batch), and where the range starts ----
   {
-    const int per = (B + kAttnThreads - 1) / kAttnThreads;
     const int f = tid * per, e = min(B, f + per);
     const int items = a.Hkv * a.RB;
     long long mine = 0, seqs = 0;  // tiles; sequences with tiles
@@ -1152,7 +1158,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (lane == 31) pre[warp] = inc;
     __syncthreads();
     long long before = inc - mine - (seqs << 40), all = 0;
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < kAttnThreads / 32; ++i) {
       if (i < warp) before += pre[i];
       all += pre[i];
@@ -1160,11 +1166,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const long long tiles = (all & ((1ll << 40) - 1)) * items, n_items = (all >> 40) * items;
     // What an item costs beside its tiles (first and last tile, results), in
     // tiles: kItemCost, less where a range is of a few tiles only.
-    const long long w = min(static_cast<long long>(kItemCost), tiles / (8ll * C));
+    long long w = 0;  // min(kItemCost, tiles / (8 C))
+#pragma unroll
+    for (int k = 1; k <= kItemCost; ++k) w += tiles >= 8ll * k * C;
     const long long W = tiles + w * n_items;
     // The range's ends in cost: [lo, hi); an item's tiles come first in its
     // T + w.  A range may hold no tile.
-    const long long me = blockIdx.x, lo = W * me / C, hi = W * (me + 1) / C;
+    const long long me = blockIdx.x, lo = __umul64hi(W * me, a.per_cta), hi = me + 1 == C ? W : static_cast<long long>(__umul64hi(W * (me + 1), a.per_cta));
     long long p = ((before & ((1ll << 40) - 1)) + w * (before >> 40)) * items;
     const long long mine_cost = (mine + w * seqs) * items;
     if (tid == 0) {
@@ -1181,7 +1189,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (q.T == 0) continue;
       const long long one = q.T + w, end = p + one * items;
       if (lo < end) {
-        int item = lo > p ? static_cast<int>((lo - p) / one) : 0;
+        const unsigned long long d = lo > p ? lo - p : 0;
+        int item = static_cast<int>((d | one) >> 32 ? d / one : static_cast<unsigned>(d) / static_cast<unsigned>(one));
         int t0 = lo > p ? static_cast<int>(lo - p - item * one) : 0;
         if (t0 >= q.T) {  // behind the item's tiles: the next item
           ++item;
@@ -1193,7 +1202,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             Range r;
             r.lo = from;
             r.b = sm.b0 = b;
-            r.h = sm.h0 = item / a.RB;
+            r.h = sm.h0 = a.RB == 1 ? item : item / a.RB;
             r.rb = sm.rb0 = item - r.h * a.RB;
             r.t0 = sm.t0 = t0;
             r.T = sm.T0 = q.T;
@@ -1201,6 +1210,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             sm.tot0 = q.tot;
             sm.tail0 = q.tail;
             r.used = 1;
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(a.table + b * a.table_stride +
+                                                           (a.ps <= kTile ? t0 * a.ppt : t0 / a.tpp)));
             a.ranges[me] = r;
             sm.left = hi - from;
           }
@@ -1421,38 +1432,54 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // Joins the parts of the (sequence, head, row block)s that range borders cut:
 //     M = max m_i,  w_i = 2^(m_i - M),  o = sum w_i O_i / sum w_i l_i
 // in range order.  blockIdx.x: a range that starts inside an item; the first
-// such range of an item does its work, a warp per row.  The loads of all parts
-// are independent: two round trips and the parts' own.
+// such range of an item does its work, a warp per row, four parts' loads on
+// their way at a time.  One round trip finds the ranges around it.  (With a
+// branch per part, which kept the loads apart, 19 parts took 5.4 us, now 2 us;
+// batches of ten took registers from the many short joins of a large batch.)
 // ---------------------------------------------------------------------------
 constexpr int kJoinWarps = 8;
+template <int N>
+struct Size {
+  static constexpr int value = N;
+};
 
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __grid_constant__ Args a, int C) {
+template <class T_, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps, 6) attn_combine_kernel(const __grid_constant__ Args a, int C) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int c = blockIdx.x + 1;
   pdl_wait();
-  const Range me = a.ranges[c];
-  if (!me.used || me.t0 == 0) return;
-  const long long s = me.lo - me.t0, e = s + me.T;
-  int pk = c - 1;  // the range before, which holds the item's tile t0 - 1
-  while (pk > 0 && !a.ranges[pk].used) --pk;
-  const long long before = a.ranges[pk].lo;
+  // ranges c - 1 .. c + 30, a lane each; this one's item
+  union {
+    uint4 v;
+    struct {
+      long long lo;
+      int t0, used;
+    };
+  } head;
+  head.v = make_uint4(0, 0, 0, 0);
+  if (c - 1 + lane < C) head.v = *reinterpret_cast<const uint4*>(a.ranges + c - 1 + lane);
+  const int4 item = *(reinterpret_cast<const int4*>(a.ranges + c) + 1);
+  const int t0 = __shfl_sync(0xffffffffu, head.t0, 1);
+  if (!__shfl_sync(0xffffffffu, head.used, 1) || t0 == 0) return;
+  const int b = item.x, h = item.y, rb = item.z, T = item.w;
+  const long long s = __shfl_sync(0xffffffffu, head.lo, 1) - t0, e = s + T;
+  // the range before, which holds the item's tile t0 - 1
+  int pk = c - 1;
+  long long before = __shfl_sync(0xffffffffu, head.lo, 0);
+  if (!__shfl_sync(0xffffffffu, head.used, 0) && pk > 0) {
+    while (--pk > 0 && !a.ranges[pk].used) {}
+    before = a.ranges[pk].lo;
+  }
   if (before > s) return;  // an earlier range's item
-  const int r0 = me.rb * a.rows_per_block, rows = min(a.rows_per_block, a.R - r0);
+  const int r0 = rb * a.rows_per_block, rows = min(a.rows_per_block, a.R - r0);
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   if (r >= rows) return;
-  const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
-  int ctx;
-  bool bad, broken;
-  const int tot = seq_len(a, me.b, ctx, bad);
-  uint64_t mask;
-  int depth;
-  const bool there =
-      node_way(a.nodes.parent ? a.nodes.parent + static_cast<long long>(me.b) * a.nodes.N : nullptr, tot - ctx, i,
-               mask, depth, broken);
   // the part of range pk + k; only the first can be its CTA's last
   auto part = [&](int k) { return (2ll * (pk + k) + (k == 0 && before < s ? 1 : 0)) * a.cols + r; };
+  const float* const first = a.part_o + part(0) * D + lane * E;
+  const float* const rest = a.part_o + 2ll * pk * a.cols * D + r * D + lane * E;  // of range pk + k: + 2 k cols D
+  const int step = 2 * a.cols * D;
   float M = kNoScore, L = 0.f, o[E];
 #pragma unroll
   for (int q = 0; q < E; ++q) o[q] = 0.f;
@@ -1460,47 +1487,77 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attn_combine_kernel(const __g
   for (int k0 = 0;; k0 += 32) {
     const int k = k0 + lane, at = pk + k;
     bool in = k == 0, past = at >= C;
-    if (!in && !past && a.ranges[at].used) {
-      in = a.ranges[at].lo < e;
+    int used;
+    long long lo;
+    if (k0 > 0 || pk != c - 1) {
+      used = !past && a.ranges[at].used;
+      lo = used ? a.ranges[at].lo : 0;
+    } else {
+      used = head.used;
+      lo = head.lo;
+    }
+    if (!in && !past && used) {
+      in = lo < e;
       past = !in;
     }
     const float2 ml = in ? a.part_ml[part(k)] : make_float2(kNoScore, 0.f);
-    float m = ml.x;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    const float Mn = fmaxf(M, m);
-    const float w = in ? (ml.x == Mn ? 1.f : exp2f(ml.x - Mn)) : 0.f;
-    float l = w * ml.y;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    const float old = M == Mn ? 1.f : exp2f(M - Mn);
-    L = L * old + l;
-    M = Mn;
-#pragma unroll
-    for (int q = 0; q < E; ++q) o[q] *= old;
     const unsigned parts = __ballot_sync(0xffffffffu, in);
     const int n = parts ? 32 - __clz(parts) : 0;
-#pragma unroll 4
-    for (int t = 0; t < n; ++t) {
-      const float wt = __shfl_sync(0xffffffffu, w, t);
-      if (!((parts >> t) & 1)) continue;
-      const float* src = a.part_o + part(k0 + t) * D + lane * E;
+    float w = 0.f;
+    const auto weights = [&]() {
+      float m = ml.x;
 #pragma unroll
-      for (int q = 0; q < E; q += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(src + q);
-        o[q] = fmaf(wt, v.x, o[q]);
-        o[q + 1] = fmaf(wt, v.y, o[q + 1]);
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      const float Mn = fmaxf(M, m);
+      w = in ? (ml.x == Mn ? 1.f : exp2f(ml.x - Mn)) : 0.f;
+      float l = w * ml.y;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+      const float old = M == Mn ? 1.f : exp2f(M - Mn);
+      L = L * old + l;
+      M = Mn;
+#pragma unroll
+      for (int q = 0; q < E; ++q) o[q] *= old;
+    };
+    // kBatch parts' loads on their way at a time
+    const auto batch = [&](int t, auto size) {
+      constexpr int kBatch = decltype(size)::value;
+      float v[kBatch][E];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const bool have = t + i < 32 && (parts >> ((t + i) & 31)) & 1;
+        const float* src = i == 0 && k0 + t == 0 ? first : rest + (k0 + t + i) * step;
+#pragma unroll
+        for (int q = 0; q < E; q += 2) {
+          const float2 x = have ? *reinterpret_cast<const float2*>(src + q) : make_float2(0.f, 0.f);
+          v[i][q] = x.x;
+          v[i][q + 1] = x.y;
+        }
       }
+      if (t == 0) weights();  // (the loads of both are on their way)
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float wt = __shfl_sync(0xffffffffu, w, (t + i) & 31);
+#pragma unroll
+        for (int q = 0; q < E; ++q) o[q] = fmaf(wt, v[i][q], o[q]);
+      }
+    };
+    if (n <= 2) {
+      batch(0, Size<2>{});
+    } else {
+#pragma unroll 1
+      for (int t = 0; t < n; t += 4) batch(t, Size<4>{});
     }
     if (__any_sync(0xffffffffu, past)) break;
   }
-  const bool empty = !there || L == 0.f;
+  const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
+  const bool empty = L == 0.f;
   const float inv = empty ? 0.f : 1.f / L;
-  const long long row = (static_cast<long long>(me.b) * a.nodes.N + i) * a.Hq + me.h * a.G + g;
+  const long long row = (static_cast<long long>(b) * a.nodes.N + i) * a.Hq + h * a.G + g;
   char* out = a.out + 2 * (row * D + lane * E);
 #pragma unroll
   for (int q = 0; q < E; q += 2)
-    *reinterpret_cast<uint32_t*>(out + 2 * q) = empty ? 0u : T::pack(o[q] * inv, o[q + 1] * inv);
+    *reinterpret_cast<uint32_t*>(out + 2 * q) = empty ? 0u : T_::pack(o[q] * inv, o[q + 1] * inv);
   if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
@@ -1720,6 +1777,7 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   int C = sm_count();
   if (C < 1) return cudaErrorInvalidDevice;
   C = C < kMaxCtas ? C : kMaxCtas;
+  a.per_cta = C > 1 ? ~0ull / C + 1 : 0;
   if (dtype == Bf16::kId)
     return D == 128 ? launch_d<Bf16, 128>(mk, mv, a, C, smem, s) : launch_d<Bf16, 64>(mk, mv, a, C, smem, s);
   return D == 128 ? launch_d<F16, 128>(mk, mv, a, C, smem, s) : launch_d<F16, 64>(mk, mv, a, C, smem, s);
