@@ -650,7 +650,8 @@ SSD_API ssd_status ssd_kv_commit(const ssd_paged_kv *kv, int layers, int64_t k_l
  *              logit first, then lower index).  entropy, rank may be NULL.
  *   K, top_tok, top_logprob : 0 <= K <= SSD_MAX_TOP; [R, K], best first.
  *   ws       : ssd_logprobs_workspace_bytes(R, V, K) bytes, for calls of any size
- *              that it is large enough for, but for no other entry point.  R <= 2^26.
+ *              that it is large enough for; entry points that keep more than the
+ *              error word in their workspace need another.  R <= 2^26.
  * A row with a NaN or +inf logit, or only -inf, sets SSD_DEVERR_BAD_LOGITS and
  * gives NaN and -1.  A row id >= n_rows sets SSD_DEVERR_BAD_LENGTH.
  */

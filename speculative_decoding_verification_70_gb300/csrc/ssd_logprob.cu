@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
           Tag::unpackraw(now[u].r, y);
           const int i = (first + u * 32 + lane) * N;
 #pragma unroll
-          for (int k = 0; k < N; ++k) count += y[k] > zt || (y[k] == zt && i + k < tok);
+          for (int k = 0; k < N; ++k) count += y[k] > zt || (y[k] == zt && zt > -INFINITY && i + k < tok);
         }
       }
       if (TOP && top >= tau) {
