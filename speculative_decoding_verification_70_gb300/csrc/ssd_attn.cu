@@ -34,8 +34,9 @@
 //          tile took 1680 cycles, three times 64 take 1200.)
 //
 // m follows the running maximum lazily: P and l come out of one pass over the
-// scores, and only where a row's l grew by more than 2^30 (2^8 for fp16, whose
-// range is short) the warpgroup finds the tile's row maxima, rescales l and O
+// scores, and only where a row's l grew by more than 2^30 (2^15 for fp16, whose
+// range is short: there m is the maximum less 7, so that entries down to 2^-21
+// of the largest keep their precision) the warpgroup finds the tile's row maxima, rescales l and O
 // and repeats the pass.  P keeps its relative precision at
 // any excess, l and O their 32-bit range.
 #include <cuda.h>
@@ -786,7 +787,8 @@ __device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx,
 template <class T, int D, int NC>
 __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* Q, int qbytes, char* V,
                                              char* P0, int wg) {
-  constexpr float kGrow = T::kId == Bf16::kId ? 1073741824.f : 256.f;
+  constexpr float kGrow = T::kId == Bf16::kId ? 1073741824.f : 32768.f;
+  constexpr float kLift = T::kId == Bf16::kId ? 0.f : 7.f;  // log2 of P at a row's maximum
   const bool split = a.split;
   char* P = P0 + a.poff[wg];
   Scratch& sc = *reinterpret_cast<Scratch*>(P);
@@ -880,7 +882,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
           if (wt < ncj) {
             const float mx = fmaxf(fmaxf(sc.red[0][wt], sc.red[1][wt]), fmaxf(sc.red[2][wt], sc.red[3][wt]));
             const float mo = -nm[wt];
-            const float mn = fmaxf(mo, mx);
+            const float mn = fmaxf(mo, mx - kLift);
             sc.fac[wt] = mn == mo ? 1.f : exp2f(mo - mn);
             nm[wt] = -mn;
           }
@@ -979,6 +981,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       }
       so.row[cc] = row;
     }
+    if (split && more) rows_ready(sm, 0);  // (its first scores are made while this piece's results go out)
     if (split) named_sync(bar, 128);
     else named_sync(kGroups + 1, kSoft);
     {
@@ -1070,7 +1073,6 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     }
     tc_before();
     named_sync(kGroups + 1, kSoft);  // P and the tables may be written again
-    if (split && more) rows_ready(sm, 0);
     g0 += tiles;
     tails0 += max(end - tail, 0);
     ++item_no;
