@@ -62,7 +62,6 @@ constexpr int kMaxJob = 96;          // most rows of a warpgroup
 constexpr int kTailBars = 8;
 constexpr int kMaxCtas = 160;
 constexpr int kNoRow = 0x7fffffff;   // a column without a row (rows of zeros: ~row)
-constexpr int kItemCost = 4;         // what an item's start and end cost, in tiles
 constexpr float kNoScore = -1e30f;   // m of a row that has seen nothing
 constexpr int kSmemMax = 227 * 1024;
 
@@ -83,6 +82,7 @@ struct Args {
   int Hq, Hkv, G, R;
   int RB, rows_per_block;   // row blocks of a key/value head
   int split;                // the warpgroups split the rows
+  int item_cost;            // what an item's start and end cost, in tiles
   int cols;                 // columns of S^T: the rows, rounded up to 16
   int wcols[kGroups], off[kGroups];  // a warpgroup's columns
   int poff[kGroups], pbytes;         // its P buffer; all of them
@@ -1167,10 +1167,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     const long long tiles = (all & ((1ll << 40) - 1)) * items, n_items = (all >> 40) * items;
     // What an item costs beside its tiles (first and last tile, results), in
-    // tiles: kItemCost, less where a range is of a few tiles only.
-    long long w = 0;  // min(kItemCost, tiles / (8 C))
-#pragma unroll
-    for (int k = 1; k <= kItemCost; ++k) w += tiles >= 8ll * k * C;
+    // tiles, less where a range is of a few tiles only.
+    long long w = 0;  // min(item_cost, tiles / (4 C))
+#pragma unroll 1
+    for (int k = 1; k <= a.item_cost; ++k) w += tiles >= 4ll * k * C;
     const long long W = tiles + w * n_items;
     // The range's ends in cost: [lo, hi); an item's tiles come first in its
     // T + w.  A range may hold no tile.
@@ -1722,6 +1722,10 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
     a.poff[w] = sh.poff[w];
   }
   a.pbytes = sh.pbytes;
+  // About 5 us of the pass's time.  Measured at 4, 6, 8, 10 tiles: 64 single
+  // tokens, D = 64, 77.6, 71.5, 66.5, 69.3 us; 64 trees of 168 rows, D = 128, 214,
+  // 198, 198, 205; 32 trees of 256 rows 177, 173, 181, 183.
+  a.item_cost = D == 64 && !a.split ? 8 : 6;
   a.q = p.q; a.q_b = p.q_b; a.q_n = p.q_n; a.q_h = p.q_h;
   a.zero = p.scale == 0.f;
   a.c = a.zero ? 1.f : p.scale * 1.4426950408889634f;
