@@ -39,6 +39,16 @@
 // of the largest keep their precision) the warpgroup finds the tile's row maxima, rescales l and O
 // and repeats the pass.  P keeps its relative precision at
 // any excess, l and O their 32-bit range.
+//
+// Bound: HBM for up to 64 rows of a key/value head where the work is long (64
+// contexts of 6800 slots: N = 1, G = 4, D = 128 272 us, 6.6 TB/s; D = 64 154 us,
+// 5.8 TB/s).  With more rows the bytes in flight: Q and P leave four (168 rows)
+// or three (256 rows) slots of 32 KB for the rings, which at a loaded latency of
+// about 4000 cycles is 64 trees of 21 nodes over 500..8000 slots in 198 us, 3.9
+// TB/s, two trees of 64 nodes over 60000 and 130000 slots in 238 us, 3.3 TB/s.
+// Short items: an item's start and end cost 5 us of a CTA (64 single tokens over
+// 200..6000 slots, D = 64: 67 us, 3.4 TB/s).  One short sequence: the chain of
+// set-up, first copies, one tile, results and join (8 nodes over 4096 slots: 20 us).
 #include <cuda.h>
 #include <math.h>
 
@@ -1761,7 +1771,10 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   int slots = static_cast<int>((kSmemMax - fixed) / slot);
   if (slots > 2 * kMaxRing) slots = 2 * kMaxRing;
   if (slots < 3) return cudaErrorInvalidConfiguration;
-  a.nk = slots / 2;
+  // (an odd slot to K: a product of scores frees its K tile at once, but the next
+  // one is wanted a softmax earlier than the next V tile.  Two wide trees, three
+  // slots: 238 us, with two for V 249)
+  a.nk = (slots + 1) / 2;
   a.nv = slots - a.nk;
   const size_t smem = fixed + static_cast<size_t>(slots) * slot;
   CUtensorMap mk, mv;
