@@ -132,7 +132,7 @@ struct alignas(16) Misc {
   unsigned tmem;
   int abort;
 };
-static_assert(sizeof(Misc) <= 3072, "shared memory of 256 rows");
+static_assert(sizeof(Misc) <= 3 * 1024, "shared memory of 256 rows");
 
 // What a warpgroup keeps in its P buffer while that holds no P: between the
 // product of one tile and the P of the next, and at the end of a piece.
