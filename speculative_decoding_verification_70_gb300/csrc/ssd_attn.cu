@@ -1102,7 +1102,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int qbytes = a.cols * D * 2;
   char* P = Q + (a.split ? 1 : 2) * qbytes;
   Misc& sm = *reinterpret_cast<Misc*>(P + a.pbytes);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // (known to be the same for the warp, so that its role runs with uniform registers)
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int C = gridDim.x, B = a.nodes.B;
   const int per = (B + kAttnThreads - 1) / kAttnThreads;
   if (tid * per < B) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.nodes.ctx_len + tid * per));
