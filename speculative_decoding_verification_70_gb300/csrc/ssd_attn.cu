@@ -1240,7 +1240,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   __syncthreads();
   tc_after();
   pdl_trigger();
-  const uint32_t tmem = sm.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);  // (uniform)
 
   if (warp == 0 || warp == 2) {
     // ---- K (warp 0) or V (warp 2) tiles ----
@@ -1330,7 +1330,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     while (pc.next(a)) {
       const int qb = a.split ? 0 : item & 1;
       bar_wait(&sm.qfull[qb], (a.split ? item : item >> 1) & 1, sm, a.err);
-      const uint64_t qd = qd0 + __shfl_sync(0xffffffffu, qb, 0) * (qbytes / 16);
+      const uint64_t qd = qd0 + qb * (qbytes / 16);
       ++item;
 #pragma unroll 1
       for (int t = pc.t0; t < pc.end; ++t) {
@@ -1339,7 +1339,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           phase ^= 1;
         }
         bar_wait(&sm.kfull[slot], phase, sm, a.err);
-        const uint64_t kd = kd0 + __shfl_sync(0xffffffffu, slot, 0) * (kSlotBytes / 16);
+        const uint64_t kd = kd0 + slot * (kSlotBytes / 16);
         const int w0 = a.split ? 0 : turn, w1 = a.split ? kGroups : turn + 1;
 #pragma unroll 1
         for (int w = w0; w < w1; ++w) {
@@ -1348,7 +1348,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           done = (done ^ (1u << w)) | (256u << w);
           tc_after();
           const uint64_t q = qd + a.off[w] * 8;
-          const uint32_t d = __shfl_sync(0xffffffffu, tmem + (a.split ? a.off[w] : w * kAlternate), 0);
+          const uint32_t d = tmem + (a.split ? a.off[w] : w * kAlternate);
           const uint32_t id = instr<T>(a.wcols[w], false, false);
           if (elect_one()) {
 #pragma unroll
@@ -1386,7 +1386,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           if (lane == 0) bar_arrive(&sm.vready[tails % kTailBars]);
           ++tails;
         }
-        const uint64_t vd = vd0 + __shfl_sync(0xffffffffu, slot, 0) * (kSlotBytes / 16);
+        const uint64_t vd = vd0 + slot * (kSlotBytes / 16);
         const bool add = t - pc.t0 >= (a.split ? 1 : kGroups);  // not the warpgroup's first tile of the piece
         const int w0 = a.split ? 0 : turn, w1 = a.split ? kGroups : turn + 1;
 #pragma unroll 1
@@ -1396,7 +1396,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tc_after();
           const uint64_t pd = pd0 + a.poff[w] / 16;
           const uint32_t d =
-              __shfl_sync(0xffffffffu, tmem + kMaxRows + (a.split ? a.off[w] : w * kAlternate), 0);
+              tmem + kMaxRows + (a.split ? a.off[w] : w * kAlternate);
           const uint32_t id = instr<T>(a.wcols[w], true, true);
           if (elect_one()) {
 #pragma unroll
