@@ -26,10 +26,11 @@
 // pass of K = 0 fell from 6.6 to 4 TB/s).  One CTA per row, or per part of a row,
 // whose last CTA to finish joins the parts.
 //
-// Bound: HBM for fp32 (4096 x 151936, K = 5: 389 us, 6.4 TB/s; 2048 rows, K = 0:
-// 187 us, 6.6 TB/s); for bf16 the instructions, 6 an element, and the candidates'
-// steps (384 x 151936: K = 0 25 us, 4.7 TB/s; K = 20 43 us); for a few rows the
-// steps one after another (8 x 128256: K = 0 5.3 us, K = 5 8.4 us).
+// Bound: HBM for fp32 (4096 x 151936, K = 8: 386 us, 6.5 TB/s; 2048 rows, K = 0:
+// 187 us, 6.6 TB/s); 384 rows of bf16 are one wave, which begins and ends together
+// (384 x 151936: K = 0 25 us, 4.7 TB/s) and whose candidates' steps, two raised
+// bounds and the selection leave the memory idle (K = 20 43 us); a few rows are
+// steps one after another (8 x 128256: K = 0 5.3 us, K = 5 8.6 us).
 #include <math.h>
 
 #include <algorithm>
@@ -512,7 +513,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     if (tok_ok) zt = Tag::load1(z + tok);
     const typename Raw<Tag>::Bound after = Raw<Tag>::bound(zt),
                                    ahead = zt > -INFINITY && zt < INFINITY ? Raw<Tag>::below(zt) : after;
-    typename Raw<Tag>::Count cnt;
     float tau = -INFINITY, mc = 0.f;
     bool plain = !(c > kLeast && c < 1e7f);
     bool over = false;  // more than its list holds
@@ -612,20 +612,25 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
         __syncthreads();
         tau = sm.tau;
       }
-      // the rank: a slice before the token's logit, behind it, its own
-      const int i0 = first * N, i1 = i0 + kSlice * N;
-      if (i1 <= tok || i0 > tok) {
-        const typename Raw<Tag>::Bound t = i0 > tok ? after : ahead;
+      // the rank, where an element may come before the token's: a slice before
+      // its logit, behind it, its own
+      if (top >= zt) {
+        const int i0 = first * N, i1 = i0 + kSlice * N;
+        if (i1 <= tok || i0 > tok) {
+          const typename Raw<Tag>::Bound t = i0 > tok ? after : ahead;
+          typename Raw<Tag>::Count cnt;
 #pragma unroll
-        for (int u = 0; u < U; ++u) now[u].count(t, cnt);
-      } else {
+          for (int u = 0; u < U; ++u) now[u].count(t, cnt);
+          count += cnt.take();
+        } else {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float y[8];
-          Tag::unpackraw(now[u].r, y);
-          const int i = (first + u * 32 + lane) * N;
+          for (int u = 0; u < U; ++u) {
+            float y[8];
+            Tag::unpackraw(now[u].r, y);
+            const int i = (first + u * 32 + lane) * N;
 #pragma unroll
-          for (int k = 0; k < N; ++k) count += y[k] > zt || (y[k] == zt && zt > -INFINITY && i + k < tok);
+            for (int k = 0; k < N; ++k) count += y[k] > zt || (y[k] == zt && zt > -INFINITY && i + k < tok);
+          }
         }
       }
       if (TOP && top >= tau) {
@@ -681,7 +686,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
           E2 = fma2(e, x[k], E2);
         }
       }
-      count += cnt.take();
       if (TOP) {
         if (round + 1 == raise_at && b + kLpThreads * U < v1) {
           raise_at *= kRaise;
