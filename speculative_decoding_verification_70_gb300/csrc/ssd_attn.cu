@@ -803,7 +803,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
   char* P = P0 + a.poff[wg];
   Scratch& sc = *reinterpret_cast<Scratch*>(P);
   const int wt = threadIdx.x - 128 - wg * 128;  // thread of the warpgroup = TMEM lane
-  const int warp = wt >> 5, lane = wt & 31;
+  const int warp = __shfl_sync(0xffffffffu, wt >> 5, 0), lane = wt & 31;
   const int x2 = (lane & 3) * 2;  // first of the thread's rows in a group of 8
   const int ncj = a.wcols[wg], nch = ncj / 16, colbase = a.off[wg];
   const int tcol = split ? colbase : wg * kAlternate;  // its columns of TMEM and of nm
