@@ -428,8 +428,9 @@ __device__ __forceinline__ void lp_copy(uint4* dst, const void* src, int bytes, 
                "l"(src), "r"(bytes), "r"(lp_ptr(bar))
                : "memory");
 }
-// Bounded wait: false after a second.
-__device__ __forceinline__ bool lp_wait(unsigned long long* bar, uint32_t parity) {
+// Bounded wait: after a second the error word says so, and 20 ms let the copy
+// land before the shared memory is freed.
+__device__ __forceinline__ void lp_wait(unsigned long long* bar, uint32_t parity, int* err) {
   unsigned long long t0 = 0;
   for (unsigned i = 1;; ++i) {
     uint32_t ok;
@@ -440,12 +441,16 @@ __device__ __forceinline__ bool lp_wait(unsigned long long* bar, uint32_t parity
         : "=r"(ok)
         : "r"(lp_ptr(bar)), "r"(parity), "r"(20000)
         : "memory");
-    if (ok) return true;
+    if (ok) return;
     if ((i & 31) == 0) {
       unsigned long long t;
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
       if (t0 == 0) t0 = t;
-      if (t - t0 > 1000000000ull) return false;
+      if (t - t0 > 1000000000ull) {
+        atomicOr(err, kErrTimeout);
+        for (int k = 0; k < 200; ++k) __nanosleep(100000);
+        return;
+      }
     }
   }
 }
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
 #pragma unroll 1
     for (int b = v0; b < v1; b += kLpThreads * U, ++round) {
       const int first = slice(round), n = min(kSlice, vfull - first);
-      if (n > 0 && !lp_wait(bar + stage, phase)) bits |= kErrTimeout;
+      if (n > 0) lp_wait(bar + stage, phase, p.err);
       const uint4* ring = sm.ring[warp][stage] + lane;
       if (n >= kSlice) {
 #pragma unroll
