@@ -44,10 +44,10 @@
 // contexts of 6800 slots: N = 1, G = 4, D = 128 272 us, 6.6 TB/s; D = 64 154 us,
 // 5.8 TB/s).  With more rows the bytes in flight: Q and P leave four (168 rows)
 // or three (256 rows) slots of 32 KB for the rings, which at a loaded latency of
-// about 4000 cycles is 64 trees of 21 nodes over 500..8000 slots in 198 us, 3.9
-// TB/s, two trees of 64 nodes over 60000 and 130000 slots in 238 us, 3.3 TB/s.
+// about 4000 cycles is 64 trees of 21 nodes over 500..8000 slots in 196 us, 3.9
+// TB/s, two trees of 64 nodes over 60000 and 130000 slots in 235 us, 3.3 TB/s.
 // Short items: an item's start and end cost 5 us of a CTA (64 single tokens over
-// 200..6000 slots, D = 64: 67 us, 3.4 TB/s).  One short sequence: the chain of
+// 200..6000 slots, D = 64: 65 us, 3.5 TB/s).  One short sequence: the chain of
 // set-up, first copies, one tile, results and join (8 nodes over 4096 slots: 20 us).
 #include <cuda.h>
 #include <math.h>
