@@ -15,7 +15,9 @@
 // lane: 24.6 us); 512 chains of 8, 32 + 16 heads of 64: 12.7 us, 4.0 TB/s (26.8);
 // one chain of 8: 3.6 us.
 // kv_commit_kernel: a copy of the accepted rows, bound by HBM (or by its two
-// chained round trips).
+// chained round trips).  64 paths of up to 12 nodes, 32 layers (118 MB): 23.4 us,
+// 5.0 TB/s, of which launch and look-up are 3.6; 64 to 512 threads a CTA, 4 to 12
+// rows in flight and one to four waves of CTAs gave 23.4 to 25.4.
 #include <algorithm>
 
 #include "ssd_device.cuh"
