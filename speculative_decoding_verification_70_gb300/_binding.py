@@ -619,6 +619,19 @@ def _heads(t: torch.Tensor, dt: torch.dtype, B: int, D: int, name: str):
     return (t.data_ptr(), sh, 0 if B == 1 else sb, 0 if sh[1] == 1 else sn, 0 if sh[2] == 1 else sh_)
 
 
+def _result(out: dict, key: str, shape, dtype: torch.dtype, like: torch.Tensor) -> int:
+    """out[key], which is made where it is missing: nothing is written to a
+    tensor of another size or type.  (A vector may come in any shape.)"""
+    t = out.get(key)
+    if t is None:
+        t = out[key] = torch.empty(shape, dtype=dtype, device=like.device)
+    elif t.dtype is not dtype or (t.shape != shape and (len(shape) > 1 or t.numel() != shape[0])):
+        raise ValueError("out[%r] must be a %s tensor of shape %s" % (key, dtype, tuple(shape)))
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("out[%r] must be a contiguous CUDA tensor" % key)
+    return t.data_ptr()
+
+
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda",
                inv_freq: Optional[torch.Tensor] = None) -> torch.Tensor:
     """[max_pos, rot] float32 for ssd_kv_append: rot/2 cosines, then rot/2
@@ -673,14 +686,9 @@ def ssd_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: to
         ws = new_workspace(_ERRWORD_BYTES, q.device)
     wp, wn = _ws_ptr(ws)
     out = {} if out is None else out
-    qo = out.get("q")
-    if qo is None:
-        qo = out["q"] = torch.empty(qsh, dtype=dt, device=q.device)
-    elif qo.shape != qsh or qo.dtype is not dt:
-        raise ValueError("out['q'] must be like q")
+    qo = _result(out, "q", qsh, dt, q)
     _check("ssd_kv_append", load_library().ssd_kv_append(
-        kv, nodes, Hq, qp, qb, qn_, qh, kp, vp, kb, kn_, kh,
-        _dev(qo, "out['q']"), cp, max_pos, rot, interleaved, qn, kn, eps, wp, wn,
+        kv, nodes, Hq, qp, qb, qn_, qh, kp, vp, kb, kn_, kh, qo, cp, max_pos, rot, interleaved, qn, kn, eps, wp, wn,
         _stream_of(stream, q)))
     out["ws"] = ws
     return out
@@ -715,18 +723,11 @@ def ssd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
         ws = new_workspace(n, q.device)
     wp, wn = _ws_ptr(ws)
     o = {} if out is None else out
-    res = o.get("out")
-    if res is None:
-        res = o["out"] = torch.empty(qsh, dtype=dt, device=q.device)
-        lse = o["lse"] = torch.empty(qsh[:3], dtype=torch.float32, device=q.device)
-    else:
-        lse = o["lse"]
-        if res.shape != qsh or res.dtype is not dt or lse.shape != qsh[:3]:
-            raise ValueError("out must hold out like q and lse [B, N, Hq]")
-        _want(lse, torch.float32, "lse")
+    res = _result(o, "out", qsh, dt, q)
+    lse = _result(o, "lse", qsh[:3], torch.float32, q)
     _check("ssd_tree_attention", lib.ssd_tree_attention(
         kv, nodes, Hq, qp, qb, qn, qh, D ** -0.5 if scale is None else scale,
-        _dev(res, "out"), _dev(lse, "lse"), wp, wn, _stream_of(stream, q)))
+        res, lse, wp, wn, _stream_of(stream, q)))
     o["ws"] = ws
     return o
 
@@ -779,7 +780,8 @@ def ssd_logprobs(logits: torch.Tensor, tok: torch.Tensor, K: int = 0,
     [n,V] (rows may be strided), tok [R] int32; rows [R] int32 picks the
     logits row of each answer (e.g. the rows of accepted nodes; < 0: no
     answer); T [R] float32 or None.  Returns {"logprob", "entropy", "rank",
-    "top_tok" [R,K], "top_logprob" [R,K], "ws"} (the last two for K > 0)."""
+    "top_tok" [R,K], "top_logprob" [R,K], "ws"} (top_* for K > 0; taken out of
+    `out` for K = 0)."""
     lib = load_library()
     sh, st = logits.shape, logits.stride()
     if len(sh) != 2 or not logits.is_cuda:
@@ -804,26 +806,18 @@ def ssd_logprobs(logits: torch.Tensor, tok: torch.Tensor, K: int = 0,
         ws = new_workspace(nb, logits.device)
     wp, wn = _ws_ptr(ws)
     o = {} if out is None else out
-    lp = o.get("logprob")
-    if lp is None:
-        dev = logits.device
-        lp = o["logprob"] = torch.empty(R, dtype=torch.float32, device=dev)
-        o["entropy"] = torch.empty(R, dtype=torch.float32, device=dev)
-        o["rank"] = torch.empty(R, dtype=torch.int32, device=dev)
-    elif lp.numel() != R:
-        raise ValueError("out is of another call's sizes")
+    lp = _result(o, "logprob", (R,), torch.float32, logits)
+    en = _result(o, "entropy", (R,), torch.float32, logits)
+    rk = _result(o, "rank", (R,), torch.int32, logits)
     if K > 0:
-        top = o.get("top_tok")
-        if top is None:
-            top = o["top_tok"] = torch.empty((R, K), dtype=torch.int32, device=logits.device)
-            o["top_logprob"] = torch.empty((R, K), dtype=torch.float32, device=logits.device)
-        elif top.shape != (R, K):
-            raise ValueError("out is of another call's sizes")
-        tt, tl = _dev(top, "top_tok"), _dev(o["top_logprob"], "top_logprob")
+        tt = _result(o, "top_tok", (R, K), torch.int32, logits)
+        tl = _result(o, "top_logprob", (R, K), torch.float32, logits)
+    else:  # (not another call's)
+        o.pop("top_tok", None)
+        o.pop("top_logprob", None)
     _check("ssd_logprobs", lib.ssd_logprobs(
         logits.data_ptr(), _dtype_code(logits), st[0] if st[0] >= V or n > 1 else V, n, V, rp, R,
-        _dev(tok, "tok"), Tp, K, _dev(lp, "logprob"), _dev(o["entropy"], "entropy"),
-        _dev(o["rank"], "rank"), tt, tl, wp, wn, _stream_of(stream, logits)))
+        _dev(tok, "tok"), Tp, K, lp, en, rk, tt, tl, wp, wn, _stream_of(stream, logits)))
     o["ws"] = ws
     return o
 
