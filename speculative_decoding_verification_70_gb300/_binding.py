@@ -547,18 +547,49 @@ _KV_DTYPE = {torch.bfloat16: SSD_BF16, torch.float16: SSD_F16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream_of(stream, t: torch.Tensor) -> int:
-    """The given stream, or the current one of t's device."""
+_current_device = torch._C._cuda_getDevice
+
+
+def _stream_of(stream, dev: int) -> int:
+    """The given stream, or the current one.  A kernel starts on the current
+    device, so its tensors and its stream have to lie there."""
+    if _current_device() != dev:
+        raise ValueError("the tensors lie on cuda:%d, but the current device is cuda:%d" % (dev, _current_device()))
     if stream is None:
-        return _raw_stream(t.get_device())
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        return _raw_stream(dev)
+    if not hasattr(stream, "cuda_stream"):
+        return int(stream)
+    if stream.device_index != dev:
+        raise ValueError("the tensors lie on cuda:%d, the stream on cuda:%d" % (dev, stream.device_index))
+    return stream.cuda_stream
+
+
+def _on(t: torch.Tensor, dev: int, name: str) -> int:
+    """The pointer of a contiguous tensor of the call's device."""
+    if t.get_device() != dev:
+        _elsewhere(t, dev, name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _elsewhere(t: torch.Tensor, dev: int, name: str):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (the library has no CPU path)" % name)
+    raise ValueError("%s lies on cuda:%d, other tensors of the call on cuda:%d" % (name, t.get_device(), dev))
+
+
+def _ws_on(ws: torch.Tensor, dev: int):
+    p = _on(ws, dev, "ws")
+    off = (-p) % 256
+    return p + off, ws.numel() - off
 
 
 def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor):
     """k_cache, v_cache: [pages, page_size, Hkv, D] views (any order of the
     first three dimensions in memory; a fourth in front counts layers, of
     which the struct holds the first); page_table [B, max_pages] int32.
-    Returns the packed struct, Hkv, D and B."""
+    Returns the packed struct, Hkv, D, B and the device."""
     sh = k_cache.shape
     dt = k_cache.dtype
     if len(sh) < 4 or v_cache.shape != sh or v_cache.dtype is not dt:
@@ -566,8 +597,9 @@ def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Te
     code = _KV_DTYPE.get(dt)
     if code is None:
         raise TypeError("the cache must be bfloat16 or float16, got %s" % dt)
-    if not (k_cache.is_cuda and v_cache.is_cuda and page_table.is_cuda):
-        raise ValueError("the cache and its page table must be CUDA tensors")
+    dev = k_cache.get_device()
+    if dev < 0 or v_cache.get_device() != dev or page_table.get_device() != dev:
+        raise ValueError("k_cache, v_cache and page_table must lie on one device, as CUDA tensors")
     pages, ps, H, D = sh[-4:]
     kp, ks, kh, kd = k_cache.stride()[-4:]
     vp, vs, vh, vd = v_cache.stride()[-4:]
@@ -587,31 +619,33 @@ def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Te
                       ts[0] if ts[0] >= width or B > 1 else width, width)
     except struct.error:
         raise ValueError("the cache is too large: %s" % (tuple(sh),)) from None
-    return kv, H, D, B
+    return kv, H, D, B, dev
 
 
-def _i32(t: Optional[torch.Tensor], shape, name: str):
-    if t is None:
-        return None
+def _i32(t: torch.Tensor, shape, name: str, dev: int):
     if t.dtype is not torch.int32:
         raise TypeError("%s must be int32, got %s" % (name, t.dtype))
-    if t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor of shape %s" % (name, tuple(shape)))
+    if t.get_device() != dev:
+        _elsewhere(t, dev, name)
     return t.data_ptr()
 
 
-def _draft_nodes(B: int, N: int, ctx_len, parent, n_nodes):
-    return _pack_nodes(B, N, _i32(ctx_len, (B,), "ctx_len"),
-                       0 if parent is None else _i32(parent, (B, N), "parent"),
-                       0 if n_nodes is None else _i32(n_nodes, (B,), "n_nodes"))
+def _draft_nodes(B: int, N: int, ctx_len, parent, n_nodes, dev: int):
+    return _pack_nodes(B, N, _i32(ctx_len, (B,), "ctx_len", dev),
+                       0 if parent is None else _i32(parent, (B, N), "parent", dev),
+                       0 if n_nodes is None else _i32(n_nodes, (B,), "n_nodes", dev))
 
 
-def _heads(t: torch.Tensor, dt: torch.dtype, B: int, D: int, name: str):
+def _heads(t: torch.Tensor, dt: torch.dtype, B: int, D: int, name: str, dev: int):
     """(pointer, shape, three strides) of a [B, N, heads, D] view with contiguous
     head entries."""
     sh = t.shape
-    if len(sh) != 4 or sh[0] != B or sh[3] != D or t.dtype is not dt or not t.is_cuda:
+    if len(sh) != 4 or sh[0] != B or sh[3] != D or t.dtype is not dt:
         raise ValueError("%s must be a CUDA tensor [%d, N, heads, %d] of type %s" % (name, B, D, dt))
+    if t.get_device() != dev:
+        _elsewhere(t, dev, name)
     sb, sn, sh_, sd = t.stride()
     if sd != 1:
         raise ValueError("%s: head entries must be contiguous" % name)
@@ -619,17 +653,15 @@ def _heads(t: torch.Tensor, dt: torch.dtype, B: int, D: int, name: str):
     return (t.data_ptr(), sh, 0 if B == 1 else sb, 0 if sh[1] == 1 else sn, 0 if sh[2] == 1 else sh_)
 
 
-def _result(out: dict, key: str, shape, dtype: torch.dtype, like: torch.Tensor) -> int:
+def _result(out: dict, key: str, shape, dtype: torch.dtype, dev: int) -> int:
     """out[key], which is made where it is missing: nothing is written to a
     tensor of another size or type.  (A vector may come in any shape.)"""
     t = out.get(key)
     if t is None:
-        t = out[key] = torch.empty(shape, dtype=dtype, device=like.device)
+        t = out[key] = torch.empty(shape, dtype=dtype, device=dev)
     elif t.dtype is not dtype or (t.shape != shape and (len(shape) > 1 or t.numel() != shape[0])):
         raise ValueError("out[%r] must be a %s tensor of shape %s" % (key, dtype, tuple(shape)))
-    if not (t.is_cuda and t.is_contiguous()):
-        raise ValueError("out[%r] must be a contiguous CUDA tensor" % key)
-    return t.data_ptr()
+    return _on(t, dev, key)
 
 
 def rope_table(max_pos: int, rot: int, base: float = 10000.0, device="cuda",
@@ -662,34 +694,34 @@ def ssd_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: to
     q_norm, k_norm: [D] weights or None.  Returns {"q": [B,N,Hq,D], "ws"}."""
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [pages, page_size, Hkv, D]")
-    kv, H, D, B = _paged_kv(k_cache, v_cache, page_table)
+    kv, H, D, B, dev = _paged_kv(k_cache, v_cache, page_table)
     dt = k_cache.dtype
-    qp, qsh, qb, qn_, qh = _heads(q, dt, B, D, "q")
-    kp, ksh, kb, kn_, kh = _heads(k, dt, B, D, "k")
-    vp, vsh, vb, vn_, vh = _heads(v, dt, B, D, "v")
+    qp, qsh, qb, qn_, qh = _heads(q, dt, B, D, "q", dev)
+    kp, ksh, kb, kn_, kh = _heads(k, dt, B, D, "k", dev)
+    vp, vsh, vb, vn_, vh = _heads(v, dt, B, D, "v", dev)
     _, N, Hq, _ = qsh
     if ksh != vsh or kb != vb or kn_ != vn_ or kh != vh or ksh[1] != N or ksh[2] != H:
         raise ValueError("k and v must be [B, N, Hkv, D] with the same strides")
-    nodes = _draft_nodes(B, N, ctx_len, parent, n_nodes)
+    nodes = _draft_nodes(B, N, ctx_len, parent, n_nodes, dev)
     max_pos = rot = 0
     cp = qn = kn = None
     if cos_sin is not None:
         _want(cos_sin, torch.float32, "cos_sin")
         max_pos, rot = cos_sin.shape
-        cp = _dev(cos_sin, "cos_sin")
+        cp = _on(cos_sin, dev, "cos_sin")
     if q_norm is not None or k_norm is not None:
         for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
             if w is None or w.dtype is not dt or w.numel() != D:
                 raise ValueError("q_norm and k_norm must both be [D] of q's type")
-        qn, kn = _dev(q_norm, "q_norm"), _dev(k_norm, "k_norm")
+        qn, kn = _on(q_norm, dev, "q_norm"), _on(k_norm, dev, "k_norm")
     if ws is None:
-        ws = new_workspace(_ERRWORD_BYTES, q.device)
-    wp, wn = _ws_ptr(ws)
+        ws = new_workspace(_ERRWORD_BYTES, dev)
+    wp, wn = _ws_on(ws, dev)
     out = {} if out is None else out
-    qo = _result(out, "q", qsh, dt, q)
+    qo = _result(out, "q", qsh, dt, dev)
     _check("ssd_kv_append", load_library().ssd_kv_append(
         kv, nodes, Hq, qp, qb, qn_, qh, kp, vp, kb, kn_, kh, qo, cp, max_pos, rot, interleaved, qn, kn, eps, wp, wn,
-        _stream_of(stream, q)))
+        _stream_of(stream, dev)))
     out["ws"] = ws
     return out
 
@@ -711,23 +743,23 @@ def ssd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     lib = load_library()
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [pages, page_size, Hkv, D]")
-    kv, H, D, B = _paged_kv(k_cache, v_cache, page_table)
+    kv, H, D, B, dev = _paged_kv(k_cache, v_cache, page_table)
     dt = k_cache.dtype
-    qp, qsh, qb, qn, qh = _heads(q, dt, B, D, "q")
+    qp, qsh, qb, qn, qh = _heads(q, dt, B, D, "q", dev)
     _, N, Hq, _ = qsh
-    nodes = _draft_nodes(B, N, ctx_len, parent, n_nodes)
+    nodes = _draft_nodes(B, N, ctx_len, parent, n_nodes, dev)
     if ws is None:
         n = lib.ssd_tree_attention_workspace_bytes(B, N, Hq, H, D)
         if n == 0:
             raise SSDError("ssd_tree_attention_workspace_bytes", 1)
-        ws = new_workspace(n, q.device)
-    wp, wn = _ws_ptr(ws)
+        ws = new_workspace(n, dev)
+    wp, wn = _ws_on(ws, dev)
     o = {} if out is None else out
-    res = _result(o, "out", qsh, dt, q)
-    lse = _result(o, "lse", qsh[:3], torch.float32, q)
+    res = _result(o, "out", qsh, dt, dev)
+    lse = _result(o, "lse", qsh[:3], torch.float32, dev)
     _check("ssd_tree_attention", lib.ssd_tree_attention(
         kv, nodes, Hq, qp, qb, qn, qh, D ** -0.5 if scale is None else scale,
-        res, lse, wp, wn, _stream_of(stream, q)))
+        res, lse, wp, wn, _stream_of(stream, dev)))
     o["ws"] = ws
     return o
 
@@ -749,24 +781,24 @@ def ssd_kv_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torc
             raise ValueError("the caches must have a layer")
     elif k_cache.dim() != 4:
         raise ValueError("the caches must be [pages, page_size, Hkv, D], layers in front or not")
-    kv, _, _, B = _paged_kv(k_cache, v_cache, page_table)
+    kv, _, _, B, dev = _paged_kv(k_cache, v_cache, page_table)
     N = MAX_TREE_NODES
     node = None
     if out_node is not None:
         N = out_node.shape[-1]
-        node = _i32(out_node, (B, N), "out_node")
+        node = _i32(out_node, (B, N), "out_node", dev)
     if ws is None:
-        ws = new_workspace(_ERRWORD_BYTES, k_cache.device)
-    wp, wn = _ws_ptr(ws)
+        ws = new_workspace(_ERRWORD_BYTES, dev)
+    wp, wn = _ws_on(ws, dev)
     o = {} if out is None else out
     new = o.get("ctx_len")
     if new is None:
-        new = o["ctx_len"] = torch.empty(B, dtype=torch.int32, device=k_cache.device)
+        new = o["ctx_len"] = torch.empty(B, dtype=torch.int32, device=dev)
     shape = (B,)
     _check("ssd_kv_commit", load_library().ssd_kv_commit(
-        kv, layers, kl, vl, B, N, _i32(ctx_len, shape, "ctx_len"),
-        _i32(accept_len, shape, "accept_len"), node, _i32(new, shape, "out['ctx_len']"), wp, wn,
-        _stream_of(stream, k_cache)))
+        kv, layers, kl, vl, B, N, _i32(ctx_len, shape, "ctx_len", dev),
+        _i32(accept_len, shape, "accept_len", dev), node, _i32(new, shape, "out['ctx_len']", dev), wp, wn,
+        _stream_of(stream, dev)))
     o["ws"] = ws
     return o
 
@@ -784,7 +816,8 @@ def ssd_logprobs(logits: torch.Tensor, tok: torch.Tensor, K: int = 0,
     `out` for K = 0)."""
     lib = load_library()
     sh, st = logits.shape, logits.stride()
-    if len(sh) != 2 or not logits.is_cuda:
+    dev = logits.get_device()
+    if len(sh) != 2 or dev < 0:
         raise ValueError("logits must be a CUDA tensor [n, V]")
     n, V = sh
     if V > 1 and st[1] != 1:
@@ -796,28 +829,28 @@ def ssd_logprobs(logits: torch.Tensor, tok: torch.Tensor, K: int = 0,
         _want(T, torch.float32, "T")
         if T.numel() != R:
             raise ValueError("T must hold one temperature per token")
-        Tp = _dev(T, "T")
+        Tp = _on(T, dev, "T")
     if rows is not None:
-        rp = _i32(rows, (R,), "rows")
+        rp = _i32(rows, (R,), "rows", dev)
     if ws is None:
         nb = lib.ssd_logprobs_workspace_bytes(R, V, K)
         if nb == 0:
             raise SSDError("ssd_logprobs_workspace_bytes", 1)
-        ws = new_workspace(nb, logits.device)
-    wp, wn = _ws_ptr(ws)
+        ws = new_workspace(nb, dev)
+    wp, wn = _ws_on(ws, dev)
     o = {} if out is None else out
-    lp = _result(o, "logprob", (R,), torch.float32, logits)
-    en = _result(o, "entropy", (R,), torch.float32, logits)
-    rk = _result(o, "rank", (R,), torch.int32, logits)
+    lp = _result(o, "logprob", (R,), torch.float32, dev)
+    en = _result(o, "entropy", (R,), torch.float32, dev)
+    rk = _result(o, "rank", (R,), torch.int32, dev)
     if K > 0:
-        tt = _result(o, "top_tok", (R, K), torch.int32, logits)
-        tl = _result(o, "top_logprob", (R, K), torch.float32, logits)
+        tt = _result(o, "top_tok", (R, K), torch.int32, dev)
+        tl = _result(o, "top_logprob", (R, K), torch.float32, dev)
     else:  # (not another call's)
         o.pop("top_tok", None)
         o.pop("top_logprob", None)
     _check("ssd_logprobs", lib.ssd_logprobs(
         logits.data_ptr(), _dtype_code(logits), st[0] if st[0] >= V or n > 1 else V, n, V, rp, R,
-        _dev(tok, "tok"), Tp, K, lp, en, rk, tt, tl, wp, wn, _stream_of(stream, logits)))
+        _on(tok, dev, "tok"), Tp, K, lp, en, rk, tt, tl, wp, wn, _stream_of(stream, dev)))
     o["ws"] = ws
     return o
 

@@ -57,6 +57,7 @@ def no_launch(lib, monkeypatch):  # noqa: F811
             return call
     monkeypatch.setattr(bd, "load_library", lambda: Fake())
     monkeypatch.setattr(bd, "_raw_stream", lambda d: 0)
+    monkeypatch.setattr(bd, "_current_device", lambda: 0, raising=False)
 
 
 def _logprobs(out, K=2, R=5):
@@ -122,3 +123,80 @@ def test_attention_and_append_outputs(no_launch):
             bd.ssd_kv_append(c["q"], c["k"], c["v"], *at, ws=_ws(), out={"q": gpu(q)})
     with pytest.raises(Launched):
         bd.ssd_kv_append(c["q"], c["k"], c["v"], *at, ws=_ws(), out={"q": gpu(good["out"])})
+
+
+def _append(c, **kw):
+    bd.ssd_kv_append(c["q"], c["k"], c["v"], c["k_cache"], c["v_cache"], c["page_table"], c["ctx_len"],
+                     parent=c["parent"], n_nodes=c["n_nodes"], cos_sin=c["cos_sin"], q_norm=c["q_norm"],
+                     k_norm=c["k_norm"], ws=c["ws"], out={"q": c["out"]}, **kw)
+
+
+def _attend(c, **kw):
+    bd.ssd_tree_attention(c["q"], c["k_cache"], c["v_cache"], c["page_table"], c["ctx_len"], parent=c["parent"],
+                          n_nodes=c["n_nodes"], ws=c["ws"], out={"out": c["out"], "lse": c["lse"]}, **kw)
+
+
+def _commit(c, **kw):
+    bd.ssd_kv_commit(c["k_cache"], c["v_cache"], c["page_table"], c["ctx_len"], c["accept_len"], c["out_node"],
+                     ws=c["ws"], out={"ctx_len": c["new_len"]}, **kw)
+
+
+def _answer(c, **kw):
+    bd.ssd_logprobs(c["logits"], c["tok"], 2, c["T"], rows=c["rows"], ws=c["ws"],
+                    out={k: c[k] for k in ("logprob", "entropy", "rank", "top_tok", "top_logprob")}, **kw)
+
+
+def _all():
+    """Every tensor of the four calls."""
+    c = _case()
+    c.update(n_nodes=torch.tensor([3, 2], dtype=I32), cos_sin=torch.zeros(64, 64), q_norm=torch.ones(64, dtype=BF),
+             k_norm=torch.ones(64, dtype=BF), out=torch.empty((2, 3, 4, 64), dtype=BF), lse=torch.empty((2, 3, 4)),
+             accept_len=torch.tensor([1, 0], dtype=I32), out_node=torch.ones((2, 3), dtype=I32),
+             new_len=torch.empty(2, dtype=I32), logits=torch.zeros(6, 100), tok=torch.zeros(5, dtype=I32),
+             T=torch.ones(5), rows=torch.zeros(5, dtype=I32), ws=_ws(), **_logprob_outputs())
+    return {k: gpu(v) if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+
+
+TENSORS = {
+    _append: "q k v k_cache v_cache page_table ctx_len parent n_nodes cos_sin q_norm k_norm ws out",
+    _attend: "q k_cache v_cache page_table ctx_len parent n_nodes ws out lse",
+    _commit: "k_cache v_cache page_table ctx_len accept_len out_node ws new_len",
+    _answer: "logits tok T rows ws logprob entropy rank top_tok top_logprob"}
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("call", TENSORS, ids=lambda f: f.__name__)
+def test_tensors_of_one_device(no_launch, monkeypatch, call):
+    """A call whose tensors lie on several devices, or on another than the
+    current one, starts no kernel."""
+    c = _all()
+    with pytest.raises(Launched):
+        call(c)
+    for name in TENSORS[call].split():
+        with pytest.raises(ValueError, match="lie"):
+            call({**c, name: gpu(c[name], OnOtherGpu)})
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call({**c, name: torch.Tensor._make_subclass(torch.Tensor, c[name])})
+    other = {k: gpu(v, OnOtherGpu) if isinstance(v, torch.Tensor) else v for k, v in c.items()}
+    with pytest.raises(ValueError, match="current device"):
+        call(other)
+    monkeypatch.setattr(bd, "_current_device", lambda: 1)
+    with pytest.raises(Launched):
+        call(other)
+    with pytest.raises(ValueError, match="current device"):
+        call(c)
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("call", TENSORS, ids=lambda f: f.__name__)
+def test_stream_of_the_tensors_device(no_launch, call):
+    class Stream:
+        cuda_stream, device_index = 5, 0
+
+    class OtherStream(Stream):
+        device_index = 1
+    for stream in (Stream(), 7):
+        with pytest.raises(Launched):
+            call(_all(), stream=stream)
+    with pytest.raises(ValueError, match="stream"):
+        call(_all(), stream=OtherStream())
