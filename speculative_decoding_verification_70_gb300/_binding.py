@@ -623,8 +623,8 @@ def _paged_kv(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Te
 
 
 def _i32(t: torch.Tensor, shape, name: str, dev: int):
-    if t.dtype is not torch.int32:
-        raise TypeError("%s must be int32, got %s" % (name, t.dtype))
+    if t is None or t.dtype is not torch.int32:
+        raise TypeError("%s must be int32, got %s" % (name, t if t is None else t.dtype))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor of shape %s" % (name, tuple(shape)))
     if t.get_device() != dev:

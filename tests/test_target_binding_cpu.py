@@ -200,3 +200,11 @@ def test_stream_of_the_tensors_device(no_launch, call):
             call(_all(), stream=stream)
     with pytest.raises(ValueError, match="stream"):
         call(_all(), stream=OtherStream())
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("call,name", [(_append, "ctx_len"), (_attend, "ctx_len"), (_commit, "ctx_len"),
+                                       (_commit, "accept_len")], ids=lambda x: getattr(x, "__name__", x))
+def test_missing_lengths(no_launch, call, name):
+    with pytest.raises(TypeError, match=name):
+        call({**_all(), name: None})
