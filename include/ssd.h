@@ -542,7 +542,8 @@ typedef struct {
     int Hkv, D;             /* key/value heads; head size 64 or 128 */
     const int32_t *page_table; /* device, [B, max_pages] */
     int64_t table_stride;
-    int max_pages;          /* a sequence holds at most max_pages*page_size slots */
+    int max_pages;          /* a sequence holds at most max_pages*page_size slots;
+                               (max_pages+1)*page_size <= 2^31 - 257 */
 } ssd_paged_kv;
 
 /* The drafted nodes of a batch (HOST struct).  Every node's way to the root

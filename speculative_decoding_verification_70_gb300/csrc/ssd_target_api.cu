@@ -33,7 +33,8 @@ ssd_status check_kv(const ssd_paged_kv* kv) {
   if (kv->page_size > (1 << 20) || kv->Hkv > 1024) return SSD_ERR_INVALID_ARG;
   if (kv->D != 64 && kv->D != 128) return SSD_ERR_INVALID_ARG;
   if (kv->table_stride < kv->max_pages) return SSD_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(kv->max_pages) * kv->page_size > INT32_MAX) return SSD_ERR_INVALID_ARG;
+  // (slots are counted in 32 bits, rounded up to whole pages and tiles)
+  if ((kv->max_pages + 1ll) * kv->page_size > INT32_MAX - 256) return SSD_ERR_INVALID_ARG;
   const int64_t s[6] = {kv->k_page, kv->k_slot, kv->k_head, kv->v_page, kv->v_slot, kv->v_head};
   for (int64_t x : s)
     if (!stride_ok(x) || x < kv->D) return SSD_ERR_INVALID_ARG;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import target_reference as ref
+import test_target_cpu as abi
 from speculative_decoding_verification_70_gb300 import _binding as bd
 from test_abi_cpu import lib, needs_no_gpu  # noqa: F401
 
@@ -208,3 +209,20 @@ def test_stream_of_the_tensors_device(no_launch, call):
 def test_missing_lengths(no_launch, call, name):
     with pytest.raises(TypeError, match=name):
         call({**_all(), name: None})
+
+
+@needs_no_gpu
+@pytest.mark.parametrize("page_size,most", [(1, (1 << 31) - 258), (5, ((1 << 31) - 257) // 5 - 1),
+                                            (16, ((1 << 31) - 257) // 16 - 1), (1 << 20, 2046)])
+def test_tables_at_the_end_of_32_bits(lib, page_size, most):  # noqa: F811
+    """Tables whose last slots, rounded up to a page or a tile of 128, would not
+    be counted in 32 bits are refused; the last that fit reach CUDA (which is not
+    there)."""
+    def kv(width):
+        return abi._kv(page_size=page_size, max_pages=width, table_stride=width)
+
+    def commit(lib, kv):
+        return lib.ssd_kv_commit(kv, 1, 0, 0, 2, 4, abi.P, abi.P, abi.P, abi.P + 64, abi.P, 256, None)
+    for call in (abi._attend, abi._append, commit):
+        assert call(lib, kv=kv(most + 1)) == abi.INVALID
+        assert call(lib, kv=kv(most)) == 3
