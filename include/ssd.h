@@ -553,7 +553,7 @@ typedef struct {
  * ctx_len < 0, n_nodes outside [0, N] or ctx_len + n_nodes beyond its table
  * (SSD_DEVERR_BAD_LENGTH) has no nodes. */
 typedef struct {
-    int B, N;               /* 1 <= N <= SSD_MAX_TREE_NODES */
+    int B, N;               /* 1 <= N <= SSD_MAX_TREE_NODES; B*N < 2^31 - 1024 */
     const int32_t *ctx_len; /* device, [B] */
     const int32_t *parent;  /* device, [B, N]; NULL: a chain */
     const int32_t *n_nodes; /* device, [B]; NULL: N everywhere */

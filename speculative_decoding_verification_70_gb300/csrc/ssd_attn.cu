@@ -1150,7 +1150,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   {
     const int f = tid * per, e = min(B, f + per);
     const int items = a.Hkv * a.RB;
-    long long mine = 0, seqs = 0;  // tiles; sequences with tiles
+    long long mine = 0;  // tiles
+    int seqs = 0;        // sequences with tiles
     bool any_bad = false;
 #pragma unroll 1
     for (int b = f; b < e; ++b) {
@@ -1162,22 +1163,37 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       any_bad |= bad;
     }
     if (any_bad && blockIdx.x == 0) atomicOr(a.err, kErrBadLength);
-    long long inc = mine + (seqs << 40);
+    long long inc = mine;
+    int inc_seqs = seqs;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const long long o = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += o;
+      const int os = __shfl_up_sync(0xffffffffu, inc_seqs, d);
+      if (lane >= d) {
+        inc += o;
+        inc_seqs += os;
+      }
     }
+    constexpr int kWarps = kAttnThreads / 32;
     long long* pre = reinterpret_cast<long long*>(Q);  // not in use yet
-    if (lane == 31) pre[warp] = inc;
-    __syncthreads();
-    long long before = inc - mine - (seqs << 40), all = 0;
-#pragma unroll
-    for (int i = 0; i < kAttnThreads / 32; ++i) {
-      if (i < warp) before += pre[i];
-      all += pre[i];
+    int* pre_seqs = reinterpret_cast<int*>(pre + kWarps);
+    if (lane == 31) {
+      pre[warp] = inc;
+      pre_seqs[warp] = inc_seqs;
     }
-    const long long tiles = (all & ((1ll << 40) - 1)) * items, n_items = (all >> 40) * items;
+    __syncthreads();
+    long long before = inc - mine, all = 0;
+    int before_seqs = inc_seqs - seqs, all_seqs = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) {
+        before += pre[i];
+        before_seqs += pre_seqs[i];
+      }
+      all += pre[i];
+      all_seqs += pre_seqs[i];
+    }
+    const long long tiles = all * items, n_items = static_cast<long long>(all_seqs) * items;
     // What an item costs beside its tiles (first and last tile, results), in
     // tiles, less where a range is of a few tiles only.
     long long w = 0;  // min(item_cost, tiles / (4 C))
@@ -1187,7 +1203,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // The range's ends in cost: [lo, hi); an item's tiles come first in its
     // T + w.  A range may hold no tile.
     const long long me = blockIdx.x, lo = __umul64hi(W * me, a.per_cta), hi = me + 1 == C ? W : static_cast<long long>(__umul64hi(W * (me + 1), a.per_cta));
-    long long p = ((before & ((1ll << 40) - 1)) + w * (before >> 40)) * items;
+    long long p = (before + w * before_seqs) * items;
     const long long mine_cost = (mine + w * seqs) * items;
     if (tid == 0) {
       sm.left = 0;

@@ -46,7 +46,8 @@ ssd_status check_kv(const ssd_paged_kv* kv) {
 ssd_status check_nodes(const ssd_draft_nodes* n) {
   if (!n || !n->ctx_len) return SSD_ERR_INVALID_ARG;
   if (n->B < 1 || n->N < 1 || n->N > SSD_MAX_TREE_NODES) return SSD_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(n->B) * n->N > INT32_MAX) return SSD_ERR_INVALID_ARG;
+  // (sequences and nodes are counted in 32 bits, rounded up to a block's threads)
+  if (static_cast<int64_t>(n->B) * n->N > INT32_MAX - 1024) return SSD_ERR_INVALID_ARG;
   if (!aligned(n->ctx_len, 4) || !aligned(n->parent, 4) || !aligned(n->n_nodes, 4))
     return SSD_ERR_INVALID_ARG;
   return SSD_OK;

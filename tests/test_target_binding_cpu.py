@@ -226,3 +226,11 @@ def test_tables_at_the_end_of_32_bits(lib, page_size, most):  # noqa: F811
     for call in (abi._attend, abi._append, commit):
         assert call(lib, kv=kv(most + 1)) == abi.INVALID
         assert call(lib, kv=kv(most)) == 3
+
+
+@needs_no_gpu
+def test_batches_at_the_end_of_32_bits(lib):  # noqa: F811
+    for N, most in ((1, (1 << 31) - 1025), (64, ((1 << 31) - 1025) // 64)):
+        for call in (abi._attend, abi._append):
+            assert call(lib, nodes=abi._nodes(B=most + 1, N=N)) == abi.INVALID
+            assert call(lib, nodes=abi._nodes(B=most, N=N)) == 3
