@@ -654,7 +654,9 @@ SSD_API ssd_status ssd_kv_commit(const ssd_paged_kv *kv, int layers, int64_t k_l
  *              that it is large enough for; entry points that keep more than the
  *              error word in their workspace need another.  R <= 2^26.
  * A row with a NaN or +inf logit, or only -inf, sets SSD_DEVERR_BAD_LOGITS and
- * gives NaN and -1.  A row id >= n_rows sets SSD_DEVERR_BAD_LENGTH.
+ * gives NaN and -1.  A row id >= n_rows sets SSD_DEVERR_BAD_LENGTH.  A row of
+ * which a part does not arrive within a second sets SSD_DEVERR_TIMEOUT and gives
+ * NaN and -1.
  */
 #define SSD_MAX_TOP 32
 SSD_API size_t ssd_logprobs_workspace_bytes(int R, int V, int K);
@@ -673,6 +675,14 @@ SSD_API ssd_status ssd_logprobs(const void *logits, ssd_dtype dtype, int64_t row
 SSD_API int ssd_selftest_kv_slot(const int32_t *table_row, int max_pages, int num_pages, int page_size,
                          int64_t slot, int32_t *page, int32_t *off);
 SSD_API int ssd_selftest_node(const int32_t *parent, int n, int j, uint64_t *mask, int32_t *depth);
+
+/*
+ * Self-test hook of the bounded waits, process-wide for later calls of
+ * ssd_logprobs: a copy into shared memory that takes longer than limit_us
+ * (1 .. 1000000; 0: the default of a second) has failed; withhold != 0: each
+ * waits for 16 bytes more than its copy brings, so that every wait runs out.
+ */
+SSD_API ssd_status ssd_selftest_copy_wait(int limit_us, int withhold);
 
 /*
  * Launch profiler (observability, not part of the method).  Between

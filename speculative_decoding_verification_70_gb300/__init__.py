@@ -24,6 +24,7 @@ from ._binding import (  # noqa: F401
     profile_begin,
     profile_end,
     rope_table,
+    selftest_copy_wait,
     selftest_exp2,
     set_split,
     set_chain_batch,

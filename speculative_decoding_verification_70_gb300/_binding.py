@@ -99,6 +99,7 @@ SIGNATURES = [
                           _P]),
     ("ssd_selftest_kv_slot", _I, [_P, _I, _I, _I, _L, _P, _P]),
     ("ssd_selftest_node", _I, [_P, _I, _I, _P, _P]),
+    ("ssd_selftest_copy_wait", _I, [_I, _I]),
     ("ssd_profile_begin", _I, [_I]),
     ("ssd_profile_end", _I, [_P, _I, _P]),
 ]
@@ -925,6 +926,13 @@ def selftest_exp2(x_hi: torch.Tensor, x_lo: torch.Tensor, stream=None) -> torch.
     _check("ssd_selftest_exp2", load_library().ssd_selftest_exp2(
         _dev(x_hi, "x_hi"), _dev(x_lo, "x_lo"), _dev(out, "out"), x_hi.numel(), _stream(stream)))
     return out
+
+
+def selftest_copy_wait(limit_us: int = 0, withhold: bool = False):
+    """Let the waits for copies of later ssd_logprobs calls give up after
+    limit_us microseconds (0: a second); withhold: wait for bytes that no copy
+    brings, so that they run out.  Process-wide."""
+    _check("ssd_selftest_copy_wait", load_library().ssd_selftest_copy_wait(int(limit_us), int(withhold)))
 
 
 def set_split(chunk_elems: int = 0, chunks_per_cta: int = 0):

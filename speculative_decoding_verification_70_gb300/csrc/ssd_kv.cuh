@@ -200,6 +200,8 @@ struct LogprobParams {
   LogprobPart* parts;    // [R, split]
   unsigned long long* part_key;  // [R, split, 32] the parts' best
   int* err;
+  unsigned wait_us;      // a copy that takes longer has failed
+  int withheld;          // bytes that are waited for beside the copied ones (self-test)
 };
 
 constexpr int kErrBadTemperature = 0x1, kErrBadLogits = 0x2, kErrBadToken = 0x4, kErrTimeout = 0x10,

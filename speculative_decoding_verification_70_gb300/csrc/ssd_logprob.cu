@@ -82,6 +82,7 @@ struct LpSmem {
   unsigned long long wkey[kLpWarps];
   int n[kLpWarps], last;
   float tau;
+  volatile int lost;  // a copy did not come
 };
 
 // Values as numbers above 0 of the same order, and back; -0 counts as 0.
@@ -421,16 +422,17 @@ __device__ __noinline__ void select_best(LpSmem& sm, unsigned long long k0, unsi
 __device__ __forceinline__ uint32_t lp_ptr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ void lp_copy(uint4* dst, const void* src, int bytes, unsigned long long* bar) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(lp_ptr(bar)), "r"(bytes) : "memory");
+__device__ __forceinline__ void lp_copy(uint4* dst, const void* src, int bytes, unsigned long long* bar, int withheld) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(lp_ptr(bar)), "r"(bytes + withheld)
+               : "memory");
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    lp_ptr(dst)),
                "l"(src), "r"(bytes), "r"(lp_ptr(bar))
                : "memory");
 }
-// Bounded wait: after a second the error word says so, and 20 ms let the copy
-// land before the shared memory is freed.
-__device__ __forceinline__ void lp_wait(unsigned long long* bar, uint32_t parity, int* err) {
+// Bounded wait: after `us` microseconds (or once another wait of the CTA gave
+// up) the row counts as lost; the CTA runs on to its end.
+__device__ __forceinline__ void lp_wait(unsigned long long* bar, uint32_t parity, unsigned us, LpSmem& sm, int* err) {
   unsigned long long t0 = 0;
   for (unsigned i = 1;; ++i) {
     uint32_t ok;
@@ -441,14 +443,14 @@ __device__ __forceinline__ void lp_wait(unsigned long long* bar, uint32_t parity
         : "=r"(ok)
         : "r"(lp_ptr(bar)), "r"(parity), "r"(20000)
         : "memory");
-    if (ok) return;
-    if ((i & 31) == 0) {
+    if (ok || sm.lost) return;
+    if ((i & 31) == 0) {  // the global timer is slow to read
       unsigned long long t;
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
       if (t0 == 0) t0 = t;
-      if (t - t0 > 1000000000ull) {
+      if (t - t0 > us * 1000ull) {
+        sm.lost = 1;
         atomicOr(err, kErrTimeout);
-        for (int k = 0; k < 200; ++k) __nanosleep(100000);
         return;
       }
     }
@@ -513,6 +515,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
   float m = kLowest, S = 0.f, E = 0.f, zt = INFINITY;
   f32x2 S2 = pk2(0.f, 0.f), E2 = S2;  // of even and odd elements
   int count = 0;
+  bool gone = false;  // a copy did not come: no answer
+  if (tid == 0) sm.lost = 0;
+  __syncthreads();
   if (TOP && tid < kLpTop) sm.best[tid] = 0;
   if (!fail) {
     if (tok_ok) zt = Tag::load1(z + tok);
@@ -549,9 +554,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     const int vfull = p.whole ? min(v1, p.V / N) : v0;
     unsigned long long* bar = sm.bar[warp];
     auto slice = [&](int k) { return v0 + k * (kLpThreads * U) + warp * kSlice; };
-    auto fetch = [&](int k, int stage) {
+    int stage = 0;
+    uint32_t phase = 0;
+    auto fetch = [&](int k, int stage, bool lost) {
       const int v = slice(k), n = min(kSlice, vfull - v);
-      if (n > 0 && lane == 0) lp_copy(sm.ring[warp][stage], z + static_cast<long long>(v) * N, n * 16, bar + stage);
+      if (n > 0 && lane == 0 && !lost)  // (a barrier of a copy that did not come is not armed again)
+        lp_copy(sm.ring[warp][stage], z + static_cast<long long>(v) * N, n * 16, bar + stage, p.withheld);
     };
     if (lane == 0) {
       sm.n[warp] = 0;
@@ -562,13 +570,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     }
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) fetch(k, k);
-    int stage = 0;
-    uint32_t phase = 0;
+    for (int k = 0; k < kStages; ++k) fetch(k, k, false);
 #pragma unroll 1
     for (int b = v0; b < v1; b += kLpThreads * U, ++round) {
       const int first = slice(round), n = min(kSlice, vfull - first);
-      if (n > 0) lp_wait(bar + stage, phase, p.err);
+      if (n > 0) lp_wait(bar + stage, phase, p.wait_us, sm, p.err);
+      const bool lost = sm.lost;  // (read beside the elements)
       const uint4* ring = sm.ring[warp][stage] + lane;
       if (n >= kSlice) {
 #pragma unroll
@@ -583,7 +590,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
         }
       }
       __syncwarp();
-      fetch(round + kStages, stage);
+      fetch(round + kStages, stage, lost);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
@@ -725,7 +732,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     // a masked token: the masked ones before it
     if (tok_ok && zt == -INFINITY)
       for (int i = v0 * N + tid; i < min(tok, v1 * N); i += kLpThreads) count += Tag::load1(z + i) == -INFINITY;
-    if (__syncthreads_or(plain)) {
+    const bool again = __syncthreads_or(plain);
+    gone = sm.lost;
+    if (gone)  // copies land before the shared memory is used for something else
+      for (int k = 0; k < 200; ++k) __nanosleep(100000);
+    if (again) {
       float top = -INFINITY;
       for (int i = v0 * N + tid; i < min(p.V, v1 * N); i += kLpThreads) top = fmaxf(top, Tag::load1(z + i));
 #pragma unroll
@@ -776,7 +787,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
       }
       if (tid == 0) {
         Part q;
-        q.m = m; q.S = S; q.U = E; q.count = count;
+        q.m = m; q.S = S; q.U = E; q.count = gone ? -1 : count;
         parts[part] = q;
       }
     }
@@ -797,7 +808,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
       S = in ? __ldcg(&parts[lane].S) : 0.f;
       E = in ? __ldcg(&parts[lane].U) : 0.f;
       join_warp(c, m, S, E);
-      count = __reduce_add_sync(0xffffffffu, in ? __ldcg(&parts[lane].count) : 0);
+      count = in ? __ldcg(&parts[lane].count) : 0;
+      gone = __any_sync(0xffffffffu, count < 0);
+      count = __reduce_add_sync(0xffffffffu, count);
       if constexpr (TOP) {
         const int n = p.split * kLpTop;
         if (tid < kLpTop) sm.best[tid] = 0;
@@ -814,6 +827,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
       }
     }
   }
+  fail |= gone;
   // the answer
   if (tid == 0) {
     if (!fail && !(S > 0.f && S < INFINITY)) {  // NaN, +inf or nothing but -inf

@@ -20,6 +20,10 @@ static_assert(SSD_DEVERR_BAD_TREE == kErrBadTree && SSD_DEVERR_BAD_LENGTH == kEr
 
 namespace {
 
+// How long kernels wait for a copy, and (self-test) bytes that never come.
+unsigned g_wait_us = 1000000;
+int g_withheld = 0;
+
 constexpr int64_t kMaxStride = 1ll << 38;
 
 bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0 && s < kMaxStride; }
@@ -210,9 +214,18 @@ ssd_status ssd_logprobs(const void* logits, ssd_dtype dtype, int64_t row_stride,
   p.logprob = logprob; p.entropy = entropy; p.rank = rank;
   p.top_tok = top_tok; p.top_logprob = top_logprob;
   p.err = static_cast<int*>(ws);
+  p.wait_us = g_wait_us;
+  p.withheld = g_withheld;
   const bool vec = aligned(logits, 16) && (static_cast<size_t>(row_stride) * esize(dtype)) % 16 == 0;
   ProfScope ps("logprobs", S(stream));
   return cuda_status(launch_logprobs(p, dtype == SSD_BF16 ? 1 : 0, vec, S(stream)));
+}
+
+ssd_status ssd_selftest_copy_wait(int limit_us, int withhold) {
+  if (limit_us < 0 || limit_us > 1000000) return SSD_ERR_INVALID_ARG;
+  g_wait_us = limit_us ? limit_us : 1000000;
+  g_withheld = withhold ? 16 : 0;
+  return SSD_OK;
 }
 
 int ssd_selftest_kv_slot(const int32_t* table_row, int max_pages, int num_pages, int page_size,
