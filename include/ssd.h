@@ -608,7 +608,9 @@ SSD_API ssd_status ssd_kv_append(const ssd_paged_kv *kv, const ssd_draft_nodes *
  * An absent node, or one whose seen slots all score -inf, gets out 0 and
  * lse -inf.  Slots that a node does not see never reach its output, whatever
  * they hold (NaN and infinities included).  A page id out of range reads as a
- * page of zeros (SSD_DEVERR_BAD_PAGE).
+ * page of zeros (SSD_DEVERR_BAD_PAGE).  A tile that does not arrive within a
+ * second ends the call (SSD_DEVERR_TIMEOUT); what out and lse hold is undefined
+ * then.
  */
 SSD_API size_t ssd_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
 SSD_API ssd_status ssd_tree_attention(const ssd_paged_kv *kv, const ssd_draft_nodes *nodes, int Hq,
@@ -678,9 +680,10 @@ SSD_API int ssd_selftest_node(const int32_t *parent, int n, int j, uint64_t *mas
 
 /*
  * Self-test hook of the bounded waits, process-wide for later calls of
- * ssd_logprobs: a copy into shared memory that takes longer than limit_us
- * (1 .. 1000000; 0: the default of a second) has failed; withhold != 0: each
- * waits for 16 bytes more than its copy brings, so that every wait runs out.
+ * ssd_tree_attention and ssd_logprobs: a copy into shared memory that takes
+ * longer than limit_us (1 .. 1000000; 0: the default of a second) has failed;
+ * withhold != 0: each waits for 16 bytes more than its copy brings, so that every
+ * wait runs out.
  */
 SSD_API ssd_status ssd_selftest_copy_wait(int limit_us, int withhold);
 

@@ -115,6 +115,8 @@ struct Args {
   struct Range* ranges;     // [ctas]
   unsigned long long per_cta;  // 2^64 / ctas, rounded up
   int* err;
+  unsigned wait_us;         // a wait that takes longer has failed
+  int withheld;             // bytes that are waited for beside the copied ones (self-test)
 };
 
 // Shared memory behind the ring, Q and P (256 rows leave 3 KB for it).
@@ -131,6 +133,7 @@ struct alignas(16) Misc {
   int cost;                         // of an item beside its tiles
   unsigned tmem;
   int abort;
+  unsigned wait_us;
 };
 static_assert(sizeof(Misc) <= 3 * 1024, "shared memory of 256 rows");
 
@@ -182,17 +185,17 @@ __device__ __forceinline__ unsigned long long now_ns() {
   return t;
 }
 
-// Bounded wait: after a second (or once another wait of the CTA gave up) the
-// CTA runs on without waiting, to its end; the error word says so.
+// Bounded wait: after wait_us (or once another wait of the CTA gave up) the CTA
+// runs on without waiting, to its end; the error word says so.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Misc& sm, int* err) {
   unsigned long long t0 = 0;
   for (unsigned i = 1;; ++i) {
     if (bar_try(b, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
     if ((i & 31) == 0) {  // the global timer is slow to read
-      if (*reinterpret_cast<volatile int*>(&sm.abort)) return false;
       const unsigned long long t = now_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > 1000000000ull) {
+      if (t - t0 > sm.wait_us * 1000ull) {
         *reinterpret_cast<volatile int*>(&sm.abort) = 1;
         atomicOr(err, kErrTimeout);
         return false;
@@ -1125,6 +1128,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int i = 0; i < kTailBars; ++i) bar_init(&sm.vready[i], 1);
     bar_init(&sm.done, 2);
     sm.abort = 0;
+    sm.wait_us = a.wait_us;
     sm.b0 = sm.h0 = sm.rb0 = sm.t0 = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1302,7 +1306,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const bool ok = bar_wait(&empty[slot], phase ^ 1, sm, a.err) &&
                         !*reinterpret_cast<volatile int*>(&sm.abort);
         if (__all_sync(0xffffffffu, ok)) {
-          if (lane == 0) bar_expect(&full[slot], boxes * a.box * 128 * HALVES);
+          if (lane == 0) bar_expect(&full[slot], boxes * a.box * 128 * HALVES + a.withheld);
           __syncwarp();
           const uint32_t dst = ring0 + slot * kSlotBytes;
 #pragma unroll 1
@@ -1760,6 +1764,7 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   a.out = p.out; a.lse = p.lse;
   a.vcache = p.kv.v; a.v_page = p.kv.v_page; a.v_slot = p.kv.v_slot; a.v_head = p.kv.v_head;
   a.err = p.err;
+  a.wait_us = p.wait_us; a.withheld = p.withheld;
   const Layout L = layout_of(a.R, D);
   char* ws = reinterpret_cast<char*>(p.err);
   a.ranges = reinterpret_cast<Range*>(ws + L.ranges);

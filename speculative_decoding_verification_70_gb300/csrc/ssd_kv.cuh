@@ -174,6 +174,8 @@ struct AttnParams {
   char* out;
   float* lse;
   int* err;
+  unsigned wait_us;      // a copy that takes longer has failed
+  int withheld;          // bytes that are waited for beside the copied ones (self-test)
 };
 
 // A part of a row, as its CTA leaves it.

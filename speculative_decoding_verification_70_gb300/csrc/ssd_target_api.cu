@@ -157,6 +157,8 @@ ssd_status ssd_tree_attention(const ssd_paged_kv* kv, const ssd_draft_nodes* nod
   p.out = static_cast<char*>(out);
   p.lse = lse;
   p.err = static_cast<int*>(ws);
+  p.wait_us = g_wait_us;
+  p.withheld = g_withheld;
   ProfScope ps("tree_attention", S(stream));
   return cuda_status(launch_tree_attention(p, kv->dtype, kv->D, S(stream)));
 }

@@ -6,7 +6,8 @@ import math
 import pytest
 import torch
 
-from test_gpu_target import BF
+import target_reference as ref
+from test_gpu_target import BF, FP, _check_attention
 
 pytestmark = pytest.mark.gpu
 LIMIT_US = 2000
@@ -62,3 +63,28 @@ def test_logprobs_that_need_no_copies(gpu_lib, withheld):
     assert gpu_lib.get_device_error(r["ws"]) == 0
     want = torch.log_softmax(z[:, 1:].double(), 1)[:, 7]
     assert float((r["logprob"].double() - want).abs().max()) <= 2.0 ** -18 * math.log(999)
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,ctx,dt", [
+    (1, 1, 4, 1, 64, 900, BF),                                   # one sequence in parts
+    (40, 2, 8, 4, 64, tuple(i * 9 for i in range(40)), FP),      # several a block
+    (3, 12, 16, 2, 128, (0, 700, 40), BF),                       # 96 rows: split over the warpgroups
+    (1, 64, 8, 1, 128, 1000, BF)])                               # two row blocks
+def test_attention_over_tiles_that_do_not_arrive(gpu_lib, withheld, B, N, Hq, Hkv, D, ctx, dt):
+    """The call ends with the error bit; then the same call is right."""
+    c = ref.case(B, N, Hq, Hkv, D, 16, ctx, dt, 72)
+    g = ref.to_gpu(c)
+    ws = gpu_lib.new_workspace(gpu_lib.tree_attention_workspace_bytes(B, N, Hq, Hkv, D), "cuda")
+
+    def run():
+        r = gpu_lib.ssd_tree_attention(g["q"], g["k_cache"], g["v_cache"], g["page_table"], g["ctx_len"],
+                                       parent=g["parent"], ws=ws)
+        torch.cuda.synchronize()
+        return r
+    with withheld:
+        run()
+    assert gpu_lib.get_device_error(ws, clear=True) == gpu_lib.DEVERR_TIMEOUT
+    want = _check_attention(gpu_lib, c)
+    again = run()
+    assert gpu_lib.get_device_error(ws) == 0
+    assert torch.equal(again["out"], want["out"]) and torch.equal(again["lse"], want["lse"])
