@@ -268,23 +268,6 @@ struct Raw<BF16Tag> {
   }
 };
 
-// S and U of a part of a row by a plain second loop around its maximum m:
-// rows whose m c is too large to be rounded once for all elements, and
-// temperatures below 1e-7 or above 7e22.
-template <class Tag>
-__device__ __noinline__ void sum_plain(const typename Tag::Elem* z, int i0, int i1, float c, float& m, float& S,
-                                       float& E) {
-  S = 0.f;
-  E = 0.f;
-  for (int i = i0 + threadIdx.x; i < i1; i += kLpThreads) {
-    const float v = Tag::load1(z + i);
-    if (v == -INFINITY) continue;  // (c = 0 at an infinite T)
-    const float x = max_nan((v - m) * c, -1000.f), e = exp2f(x);
-    S += e;
-    E = fmaf(e, x, E);
-  }
-}
-
 // What two lanes or parts hold, joined over the warp in a fixed order: m first,
 // then sums of scaled S and U.
 __device__ __forceinline__ void join_warp(float c, float& m, float& S, float& U) {
@@ -300,6 +283,50 @@ __device__ __forceinline__ void join_warp(float c, float& m, float& S, float& U)
     S += __shfl_xor_sync(0xffffffffu, S, d);
     U += __shfl_xor_sync(0xffffffffu, U, d);
   }
+}
+
+// Maximum m, S and U of a part of a row by two plain loops, for every thread of
+// the CTA: rows whose m c is too large to be rounded once for all elements,
+// temperatures below 1e-7 or above 7e22, and rows that never moved a reference
+// (all logits at or below kLowest; m = -inf and S = 0 where none is finite).
+template <class Tag>
+__device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, int i0, int i1, float c, float& m,
+                                       float& S, float& U) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float top = -INFINITY;
+  for (int i = i0 + tid; i < i1; i += kLpThreads) top = fmaxf(top, Tag::load1(z + i));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  __syncthreads();
+  if (lane == 0) sm.m[warp] = top;
+  __syncthreads();
+  m = -INFINITY;
+  for (int w = 0; w < kLpWarps; ++w) m = fmaxf(m, sm.m[w]);
+  S = 0.f;
+  U = 0.f;
+  for (int i = i0 + tid; i < i1; i += kLpThreads) {
+    const float v = Tag::load1(z + i);
+    if (v == -INFINITY) continue;  // (c = 0 at an infinite T)
+    const float x = max_nan((v - m) * c, -1000.f), e = exp2f(x);
+    S += e;
+    U = fmaf(e, x, U);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    S += __shfl_xor_sync(0xffffffffu, S, d);
+    U += __shfl_xor_sync(0xffffffffu, U, d);
+  }
+  if (lane == 0) {
+    sm.S[warp] = S;
+    sm.U[warp] = U;
+  }
+  __syncthreads();
+  S = U = 0.f;
+  for (int w = 0; w < kLpWarps; ++w) {
+    S += sm.S[w];
+    U += sm.U[w];
+  }
+  __syncthreads();
 }
 
 // A bound on the K-th largest of the CTA's orders (a thread's v, 0: none) from
@@ -737,16 +764,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     if (gone)  // copies land before the shared memory is used for something else
       for (int k = 0; k < 200; ++k) __nanosleep(100000);
     if (again) {
-      float top = -INFINITY;
-      for (int i = v0 * N + tid; i < min(p.V, v1 * N); i += kLpThreads) top = fmaxf(top, Tag::load1(z + i));
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      if (lane == 0) sm.m[warp] = top;
-      __syncthreads();
-      m = kLowest;
-      for (int w = 0; w < kLpWarps; ++w) m = fmaxf(m, sm.m[w]);
-      __syncthreads();
-      sum_plain<Tag>(z, v0 * N, min(p.V, v1 * N), c, m, S, E);
+      sum_plain<Tag>(sm, z, v0 * N, min(p.V, v1 * N), c, m, S, E);
+      if (tid > 0) S = E = 0.f;
     }
     // lanes of a warp, warps of the CTA
     join_warp(c, m, S, E);
@@ -770,7 +789,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     }
     // (by every warp: shuffles where only some warps run cost 250 clocks each)
     const bool in = lane < kLpWarps;
-    m = in ? sm.m[lane] : kLowest;
+    m = in ? sm.m[lane] : -INFINITY;
     S = in ? sm.S[lane] : 0.f;
     E = in ? sm.U[lane] : 0.f;
     join_warp(c, m, S, E);
@@ -804,7 +823,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     __threadfence();
     if (!fail) {
       const bool in = lane < p.split;  // lane k holds part k
-      m = in ? __ldcg(&parts[lane].m) : kLowest;
+      m = in ? __ldcg(&parts[lane].m) : -INFINITY;
       S = in ? __ldcg(&parts[lane].S) : 0.f;
       E = in ? __ldcg(&parts[lane].U) : 0.f;
       join_warp(c, m, S, E);
@@ -828,6 +847,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     }
   }
   fail |= gone;
+  if (!fail && S == 0.f) sum_plain<Tag>(sm, z, 0, p.V, c, m, S, E);  // (no logit above kLowest)
   // the answer
   if (tid == 0) {
     if (!fail && !(S > 0.f && S < INFINITY)) {  // NaN, +inf or nothing but -inf

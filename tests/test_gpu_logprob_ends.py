@@ -1,0 +1,41 @@
+"""Log probabilities at the ends of their range: rows of the type's lowest
+value.
+
+Tolerances as in tests/test_gpu_target.py.
+"""
+import math
+
+import pytest
+import torch
+
+from test_gpu_target import BF, _check_logprobs
+
+pytestmark = pytest.mark.gpu
+F32 = torch.float32
+# (rows, V): whole rows, a row in parts, an odd length
+SIZES = [(5, 3001), (2, 70001), (3, 128256)]
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("K", [0, 4])
+def test_rows_of_the_lowest_values(gpu_lib, dt, K):
+    """Rows whose finite logits all lie at or below -3e38 are rows like others."""
+    low = torch.finfo(dt).min
+    for R, V in SIZES:
+        z = torch.full((R, V), low).to(dt)
+        z[1, ::2] = -math.inf                      # and half of them masked
+        if R > 2:
+            z[2, V // 3] = -3.1e38                 # one token far above the others
+        tok = torch.tensor([7, 1, V // 3, 0, V - 1][:R], dtype=torch.int32)
+        _check_logprobs(gpu_lib, z.cuda(), tok, K)
+        _check_logprobs(gpu_lib, z.cuda(), tok, K, torch.linspace(0.3, 40.0, R))
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_greedy_rows_of_the_lowest_value(gpu_lib, dt):
+    """T = 0: the one-hot at the lowest index."""
+    z = torch.full((2, 9000), torch.finfo(dt).min, dtype=dt)
+    g = gpu_lib.ssd_logprobs(z.cuda(), torch.tensor([0, 5], dtype=torch.int32).cuda(), 2, torch.zeros(2).cuda())
+    assert g["logprob"].tolist() == [0.0, -math.inf] and g["entropy"].tolist() == [0.0, 0.0]
+    assert g["rank"].tolist() == [1, 6] and g["top_tok"].tolist() == [[0, 1]] * 2
+    assert gpu_lib.get_device_error(g["ws"]) == 0
