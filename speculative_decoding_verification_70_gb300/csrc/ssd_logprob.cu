@@ -329,6 +329,16 @@ __device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, 
   __syncthreads();
 }
 
+// Log probability of a logit z under a reference m and ls = log2 S: in units of
+// log 2, or in nats, with the difference halved, where 32 bits do not hold those.
+__device__ __noinline__ float far_log_prob(float z, float m, float T, float ls) {
+  return 2.f * ((0.5f * z - 0.5f * m) / T) - ls * kLn2;
+}
+__device__ __forceinline__ float log_prob(float z, float m, float c, float T, float ls) {
+  const float x = (z - m) * c;
+  return x > -1e30f ? (x - ls) * kLn2 : far_log_prob(z, m, T, ls);
+}
+
 // A bound on the K-th largest of the CTA's orders (a thread's v, 0: none) from
 // below that most of them reach at most, or the K-th largest itself; 1 where
 // there are fewer than K.  Counts at three places of the range that is left, in
@@ -858,7 +868,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     float lp = NAN, H = NAN;
     if (!fail) {
       H = T == 0.f ? 0.f : kLn2 * (ls - E / S);
-      if (tok_ok) lp = T == 0.f ? (count == 0 ? 0.f : -INFINITY) : ((zt - m) * c - ls) * kLn2;
+      if (tok_ok) lp = T == 0.f ? (count == 0 ? 0.f : -INFINITY) : log_prob(zt, m, c, T, ls);
     }
     p.logprob[r] = lp;
     if (p.entropy) p.entropy[r] = H;
@@ -878,7 +888,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
         const unsigned long long k = sm.best[tid];
         const float v = key_value(k);
         i = k ? key_index(k) : -1;
-        lp = i < 0 ? -INFINITY : T == 0.f ? (tid == 0 ? 0.f : -INFINITY) : ((v - sm.m[0]) * c - ls) * kLn2;
+        lp = i < 0 ? -INFINITY : T == 0.f ? (tid == 0 ? 0.f : -INFINITY) : log_prob(v, sm.m[0], c, T, ls);
       }
       p.top_tok[static_cast<long long>(r) * K + tid] = i;
       p.top_logprob[static_cast<long long>(r) * K + tid] = lp;

@@ -1,14 +1,15 @@
 """Log probabilities at the ends of their range: rows of the type's lowest
-value.
+value, tokens there.
 
-Tolerances as in tests/test_gpu_target.py.
+Tolerances as in tests/test_gpu_target.py; what exceeds 32 bits is infinite.
 """
 import math
 
 import pytest
 import torch
 
-from test_gpu_target import BF, _check_logprobs
+import target_reference as ref
+from test_gpu_target import BF, _check_logprobs, _same
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -38,4 +39,28 @@ def test_greedy_rows_of_the_lowest_value(gpu_lib, dt):
     g = gpu_lib.ssd_logprobs(z.cuda(), torch.tensor([0, 5], dtype=torch.int32).cuda(), 2, torch.zeros(2).cuda())
     assert g["logprob"].tolist() == [0.0, -math.inf] and g["entropy"].tolist() == [0.0, 0.0]
     assert g["rank"].tolist() == [1, 6] and g["top_tok"].tolist() == [[0, 1]] * 2
+    assert gpu_lib.get_device_error(g["ws"]) == 0
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("V", [500, 70001])
+def test_tokens_of_the_lowest_value(gpu_lib, dt, V):
+    """A token at the type's lowest value among ordinary ones: about -3.4e38 / T,
+    -inf only where that exceeds 32 bits.  And one that lies further below the
+    best than 32 bits hold, at a T that brings it back."""
+    low = torch.finfo(dt).min
+    z = torch.randn((4, V), generator=torch.Generator().manual_seed(41)).to(dt)
+    z[:, 3] = low
+    z[3, 9] = -low
+    T = torch.tensor([1.0, 2.5, 0.9, 4.0])
+    tok = torch.tensor([3, 3, 3, 3], dtype=torch.int32)
+    lp, H, rank, _, _ = ref.logprobs(z, tok, 1, T)
+    g = gpu_lib.ssd_logprobs(z.cuda(), tok.cuda(), 0, T.cuda())
+    _same(g["logprob"], lp.float().double(), lp.abs().clamp(max=1e300) * 2.0 ** -21, "logprob")
+    assert g["rank"].tolist() == rank.tolist() == [V] * 4
+    few = z[:, :20].contiguous()  # all of them asked for
+    lp, H, rank, top, tlp = ref.logprobs(few, tok, 20, T)
+    g = gpu_lib.ssd_logprobs(few.cuda(), tok.cuda(), 20, T.cuda())
+    assert torch.equal(g["top_tok"].cpu().long(), top)
+    _same(g["top_logprob"], tlp.float().double(), 2.0 ** -19 + tlp.abs() * 2.0 ** -21, "top_logprob")
     assert gpu_lib.get_device_error(g["ws"]) == 0
