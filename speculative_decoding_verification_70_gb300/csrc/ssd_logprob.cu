@@ -268,13 +268,21 @@ struct Raw<BF16Tag> {
   }
 };
 
+// (z - m) c, also where z - m alone exceeds 32 bits.
+__device__ __forceinline__ float scaled(float z, float m, float c) {
+  const float d = z - m;
+  return d > -INFINITY ? d * c : 2.f * ((0.5f * z - 0.5f * m) * c);
+}
+
 // What two lanes or parts hold, joined over the warp in a fixed order: m first,
-// then sums of scaled S and U.
+// then sums of scaled S and U.  FAR: where m may differ by more than 32 bits hold
+// and c be so small that this counts (the lanes of a CTA share m then).
+template <bool FAR = false>
 __device__ __forceinline__ void join_warp(float c, float& m, float& S, float& U) {
   float M = m;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  const float d0 = fmaxf((m - M) * c, -1e4f), f = exp2f(d0);  // 2^-1e4 = 0
+  const float d0 = fmaxf(FAR ? scaled(m, M, c) : (m - M) * c, -1e4f), f = exp2f(d0);  // 2^-1e4 = 0
   U = f * fmaf(S, d0, U);
   S *= f;
   m = M;
@@ -307,7 +315,7 @@ __device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, 
   for (int i = i0 + tid; i < i1; i += kLpThreads) {
     const float v = Tag::load1(z + i);
     if (v == -INFINITY) continue;  // (c = 0 at an infinite T)
-    const float x = max_nan((v - m) * c, -1000.f), e = exp2f(x);
+    const float x = max_nan(scaled(v, m, c), -1000.f), e = exp2f(x);
     S += e;
     U = fmaf(e, x, U);
   }
@@ -332,7 +340,7 @@ __device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, 
 // Log probability of a logit z under a reference m and ls = log2 S: in units of
 // log 2, or in nats, with the difference halved, where 32 bits do not hold those.
 __device__ __noinline__ float far_log_prob(float z, float m, float T, float ls) {
-  return 2.f * ((0.5f * z - 0.5f * m) / T) - ls * kLn2;
+  return z == -INFINITY ? z : 2.f * ((0.5f * z - 0.5f * m) / T) - ls * kLn2;
 }
 __device__ __forceinline__ float log_prob(float z, float m, float c, float T, float ls) {
   const float x = (z - m) * c;
@@ -836,7 +844,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
       m = in ? __ldcg(&parts[lane].m) : -INFINITY;
       S = in ? __ldcg(&parts[lane].S) : 0.f;
       E = in ? __ldcg(&parts[lane].U) : 0.f;
-      join_warp(c, m, S, E);
+      join_warp<true>(c, m, S, E);
       count = in ? __ldcg(&parts[lane].count) : 0;
       gone = __any_sync(0xffffffffu, count < 0);
       count = __reduce_add_sync(0xffffffffu, count);

@@ -1,5 +1,5 @@
 """Log probabilities at the ends of their range: rows of the type's lowest
-value, tokens there.
+value, tokens there, infinite temperatures.
 
 Tolerances as in tests/test_gpu_target.py; what exceeds 32 bits is infinite.
 """
@@ -64,3 +64,34 @@ def test_tokens_of_the_lowest_value(gpu_lib, dt, V):
     assert torch.equal(g["top_tok"].cpu().long(), top)
     _same(g["top_logprob"], tlp.float().double(), 2.0 ** -19 + tlp.abs() * 2.0 ** -21, "top_logprob")
     assert gpu_lib.get_device_error(g["ws"]) == 0
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_masked_tokens_at_infinite_temperature(gpu_lib, dt):
+    """All that are not masked are alike; masked ones have no probability."""
+    z = torch.full((2, 6000), -math.inf, dtype=dt)
+    z[0, 5:8] = torch.tensor([1.0, -2.0, 0.5]).to(dt)
+    z[1, [9, 77]] = torch.tensor([torch.finfo(dt).max, torch.finfo(dt).min], dtype=dt)
+    tok = torch.tensor([4, 77], dtype=torch.int32)
+    g = gpu_lib.ssd_logprobs(z.cuda(), tok.cuda(), 6, torch.full((2,), math.inf).cuda())
+    n = torch.tensor([3.0, 2.0], dtype=torch.float64)
+    want = torch.full((2, 6), -math.inf, dtype=torch.float64)
+    want[0, :3], want[1, :2] = -math.log(3), -math.log(2)
+    _same(g["top_logprob"], want, torch.full_like(want, 2.0 ** -20), "top_logprob")
+    _same(g["logprob"], torch.tensor([-math.inf, -math.log(2)], dtype=torch.float64), torch.full((2,), 2.0 ** -20), "logprob")
+    _same(g["entropy"], n.log(), torch.full((2,), 2.0 ** -20, dtype=torch.float64), "entropy")
+    assert g["top_tok"].tolist() == [[5, 7, 6, 0, 1, 2], [9, 77, 0, 1, 2, 3]]
+    assert g["rank"].tolist() == [8, 2]
+    assert gpu_lib.get_device_error(g["ws"]) == 0
+
+
+def test_differences_beyond_32_bits(gpu_lib):
+    """Logits further apart than 32 bits hold, at temperatures that bring them
+    near again: in one part of a row, and in several."""
+    for V in (2000, 128256):
+        z = torch.zeros((2, V))
+        z[:, 3], z[:, V - 2] = torch.finfo(F32).max, torch.finfo(F32).min
+        z[1, V // 2:] = torch.finfo(F32).min
+        tok = torch.tensor([V - 2, V - 1], dtype=torch.int32)
+        for K in (0, 3):
+            _check_logprobs(gpu_lib, z.cuda(), tok, K, torch.tensor([2e38, 1.5e38]))
