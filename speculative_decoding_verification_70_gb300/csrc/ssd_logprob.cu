@@ -64,6 +64,7 @@ constexpr int kLpTop = 32;        // SSD_MAX_TOP
 constexpr float kStep = 16.f;     // excess of an element over m that moves it
 constexpr float kLowest = -3.0e38f;
 constexpr float kLeast = 2e-23f;   // least c of the pass: below it -1e30 c, its floor, is not far below m c
+constexpr float kMost = 3.402823466e38f;  // c where log2(e) / T is more
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -268,21 +269,21 @@ struct Raw<BF16Tag> {
   }
 };
 
-// (z - m) c, also where z - m alone exceeds 32 bits.
-__device__ __forceinline__ float scaled(float z, float m, float c) {
+// (z - m) c, also where z - m or c exceeds 32 bits.
+__device__ __forceinline__ float scaled(float z, float m, float c, float T) {
   const float d = z - m;
-  return d > -INFINITY ? d * c : 2.f * ((0.5f * z - 0.5f * m) * c);
+  return d > -INFINITY ? (c < kMost ? d * c : d / T * kLog2e) : 2.f * ((0.5f * z - 0.5f * m) * c);
 }
 
 // What two lanes or parts hold, joined over the warp in a fixed order: m first,
 // then sums of scaled S and U.  FAR: where m may differ by more than 32 bits hold
 // and c be so small that this counts (the lanes of a CTA share m then).
 template <bool FAR = false>
-__device__ __forceinline__ void join_warp(float c, float& m, float& S, float& U) {
+__device__ __forceinline__ void join_warp(float c, float T, float& m, float& S, float& U) {
   float M = m;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-  const float d0 = fmaxf(FAR ? scaled(m, M, c) : (m - M) * c, -1e4f), f = exp2f(d0);  // 2^-1e4 = 0
+  const float d0 = fmaxf(FAR ? scaled(m, M, c, T) : (m - M) * c, -1e4f), f = exp2f(d0);  // 2^-1e4 = 0
   U = f * fmaf(S, d0, U);
   S *= f;
   m = M;
@@ -298,8 +299,8 @@ __device__ __forceinline__ void join_warp(float c, float& m, float& S, float& U)
 // temperatures below 1e-7 or above 7e22, and rows that never moved a reference
 // (all logits at or below kLowest; m = -inf and S = 0 where none is finite).
 template <class Tag>
-__device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, int i0, int i1, float c, float& m,
-                                       float& S, float& U) {
+__device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, int i0, int i1, float c, float T,
+                                       float& m, float& S, float& U) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float top = -INFINITY;
   for (int i = i0 + tid; i < i1; i += kLpThreads) top = fmaxf(top, Tag::load1(z + i));
@@ -315,7 +316,7 @@ __device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, 
   for (int i = i0 + tid; i < i1; i += kLpThreads) {
     const float v = Tag::load1(z + i);
     if (v == -INFINITY) continue;  // (c = 0 at an infinite T)
-    const float x = max_nan(scaled(v, m, c), -1000.f), e = exp2f(x);
+    const float x = max_nan(scaled(v, m, c, T), -1000.f), e = exp2f(x);
     S += e;
     U = fmaf(e, x, U);
   }
@@ -338,13 +339,15 @@ __device__ __noinline__ void sum_plain(LpSmem& sm, const typename Tag::Elem* z, 
 }
 
 // Log probability of a logit z under a reference m and ls = log2 S: in units of
-// log 2, or in nats, with the difference halved, where 32 bits do not hold those.
+// log 2, or in nats, with the difference halved, where 32 bits do not hold those
+// or their factor.
 __device__ __noinline__ float far_log_prob(float z, float m, float T, float ls) {
-  return z == -INFINITY ? z : 2.f * ((0.5f * z - 0.5f * m) / T) - ls * kLn2;
+  if (z == -INFINITY) return z;
+  return (z - m > -INFINITY ? (z - m) / T : 2.f * ((0.5f * z - 0.5f * m) / T)) - ls * kLn2;
 }
 __device__ __forceinline__ float log_prob(float z, float m, float c, float T, float ls) {
   const float x = (z - m) * c;
-  return x > -1e30f ? (x - ls) * kLn2 : far_log_prob(z, m, T, ls);
+  return x > -1e30f && c < kMost ? (x - ls) * kLn2 : far_log_prob(z, m, T, ls);
 }
 
 // A bound on the K-th largest of the CTA's orders (a thread's v, 0: none) from
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
   const bool tok_ok = tok >= 0 && tok < p.V;
   if (!tok_ok && tok != -1) bits |= kErrBadToken;
   const int K = TOP ? p.K : 0;
-  const float c = T > 0.f ? kLog2e / T : kLog2e;
+  const float c = T > 0.f ? fminf(kLog2e / T, kMost) : kLog2e;
   const typename Tag::Elem* z =
       static_cast<const typename Tag::Elem*>(p.logits) + static_cast<long long>(fail ? 0 : row) * p.row_stride;
   const int nv = (p.V + N - 1) / N;  // vectors of a row
@@ -782,11 +785,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     if (gone)  // copies land before the shared memory is used for something else
       for (int k = 0; k < 200; ++k) __nanosleep(100000);
     if (again) {
-      sum_plain<Tag>(sm, z, v0 * N, min(p.V, v1 * N), c, m, S, E);
+      sum_plain<Tag>(sm, z, v0 * N, min(p.V, v1 * N), c, T, m, S, E);
       if (tid > 0) S = E = 0.f;
     }
     // lanes of a warp, warps of the CTA
-    join_warp(c, m, S, E);
+    join_warp(c, T, m, S, E);
     count = __reduce_add_sync(0xffffffffu, count);
     if (lane == 0) {
       sm.m[warp] = m;
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     m = in ? sm.m[lane] : -INFINITY;
     S = in ? sm.S[lane] : 0.f;
     E = in ? sm.U[lane] : 0.f;
-    join_warp(c, m, S, E);
+    join_warp(c, T, m, S, E);
     count = __reduce_add_sync(0xffffffffu, in ? sm.count[lane] : 0);
     __syncthreads();
   }
@@ -844,7 +847,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
       m = in ? __ldcg(&parts[lane].m) : -INFINITY;
       S = in ? __ldcg(&parts[lane].S) : 0.f;
       E = in ? __ldcg(&parts[lane].U) : 0.f;
-      join_warp<true>(c, m, S, E);
+      join_warp<true>(c, T, m, S, E);
       count = in ? __ldcg(&parts[lane].count) : 0;
       gone = __any_sync(0xffffffffu, count < 0);
       count = __reduce_add_sync(0xffffffffu, count);
@@ -865,7 +868,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     }
   }
   fail |= gone;
-  if (!fail && S == 0.f) sum_plain<Tag>(sm, z, 0, p.V, c, m, S, E);  // (no logit above kLowest)
+  if (!fail && S == 0.f) sum_plain<Tag>(sm, z, 0, p.V, c, T, m, S, E);  // (no logit above kLowest)
   // the answer
   if (tid == 0) {
     if (!fail && !(S > 0.f && S < INFINITY)) {  // NaN, +inf or nothing but -inf

@@ -1,5 +1,5 @@
 """Log probabilities at the ends of their range: rows of the type's lowest
-value, tokens there, infinite temperatures.
+value, tokens there, infinite temperatures and ones without a reciprocal.
 
 Tolerances as in tests/test_gpu_target.py; what exceeds 32 bits is infinite.
 """
@@ -95,3 +95,28 @@ def test_differences_beyond_32_bits(gpu_lib):
         tok = torch.tensor([V - 2, V - 1], dtype=torch.int32)
         for K in (0, 3):
             _check_logprobs(gpu_lib, z.cuda(), tok, K, torch.tensor([2e38, 1.5e38]))
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("K", [0, 3])
+def test_temperatures_without_reciprocal(gpu_lib, dt, K):
+    """log2(e) / T beyond 32 bits: the best share everything, equally; and
+    logits that are as small as T."""
+    for R, V in ((3, 4001), (3, 70001)):
+        z = torch.randn((R, V), generator=torch.Generator().manual_seed(42)).to(dt)
+        z[0, [40, 1999]] = 9.0
+        z[1, 7] = 9.0
+        T = torch.tensor([1e-40, 3e-39, 2e-45])
+        tok = torch.tensor([1999, 7, 11], dtype=torch.int32)
+        lp, H, rank, top, tlp = ref.logprobs(z, tok, max(K, 1), T)
+        g = gpu_lib.ssd_logprobs(z.cuda(), tok.cuda(), K, T.cuda())
+        _same(g["logprob"], lp.float().double(), torch.full_like(lp, 2.0 ** -20), "logprob")
+        _same(g["entropy"], H, torch.full_like(H, 2.0 ** -20), "entropy")
+        assert torch.equal(g["rank"].cpu().long(), rank.long())
+        if K:
+            assert torch.equal(g["top_tok"].cpu().long(), top)
+            _same(g["top_logprob"], tlp.float().double(), torch.full_like(tlp, 2.0 ** -20), "top_logprob")
+        assert gpu_lib.get_device_error(g["ws"]) == 0
+    z = torch.zeros((1, 64))
+    z[0, 5:9] = torch.tensor([1.0, 2.0, 3.0, 0.5]) * 1e-39
+    _check_logprobs(gpu_lib, z.cuda(), torch.tensor([6], dtype=torch.int32), K, torch.tensor([5e-40]))
