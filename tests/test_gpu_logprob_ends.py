@@ -1,5 +1,6 @@
 """Log probabilities at the ends of their range: rows of the type's lowest
-value, tokens there, infinite temperatures and ones without a reciprocal.
+value, tokens there, infinite temperatures and ones without a reciprocal, and rows of
+which one token takes nearly all.
 
 Tolerances as in tests/test_gpu_target.py; what exceeds 32 bits is infinite.
 """
@@ -120,3 +121,23 @@ def test_temperatures_without_reciprocal(gpu_lib, dt, K):
     z = torch.zeros((1, 64))
     z[0, 5:9] = torch.tensor([1.0, 2.0, 3.0, 0.5]) * 1e-39
     _check_logprobs(gpu_lib, z.cuda(), torch.tensor([6], dtype=torch.int32), K, torch.tensor([5e-40]))
+
+
+@pytest.mark.parametrize("dt", [F32, BF])
+@pytest.mark.parametrize("K", [0, 2])
+@pytest.mark.parametrize("R,V", [(1500, 4097), (40, 70001)])
+def test_no_probability_above_one(gpu_lib, dt, K, R, V):
+    """One token takes all but 1e-9, others share the rest or there is none: a log
+    probability is at most 0 and an entropy at least 0."""
+    gen = torch.Generator().manual_seed(43)
+    z = torch.randn((R, V), generator=gen)
+    best = torch.randint(0, V, (R,), generator=gen)
+    z[torch.arange(R), best] = 30 + 40 * torch.rand(R, generator=gen)
+    z = (z + 60 * torch.rand((R, 1), generator=gen)).to(dt)
+    tok = z.float().argmax(1).to(torch.int32)
+    T = 0.2 + torch.rand(R, generator=gen)
+    for t in (T, torch.ones(R)):
+        g = _check_logprobs(gpu_lib, z.cuda(), tok, K, t)
+        assert float(g["logprob"].max()) <= 0.0 and float(g["entropy"].min()) >= 0.0
+        if K:
+            assert float(g["top_logprob"].max()) <= 0.0
