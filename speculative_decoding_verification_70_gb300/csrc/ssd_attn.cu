@@ -34,11 +34,13 @@
 //          tile took 1680 cycles, three times 64 take 1200.)
 //
 // m follows the running maximum lazily: P and l come out of one pass over the
-// scores, and only where a row's l grew by more than 2^30 (2^15 for fp16, whose
-// range is short: there m is the maximum less 7, so that entries down to 2^-21
-// of the largest keep their precision) the warpgroup finds the tile's row maxima, rescales l and O
-// and repeats the pass.  P keeps its relative precision at
-// any excess, l and O their 32-bit range.
+// scores, and only where a row's l grew by more than 2^12 (fp16: 2^8) of what the
+// maximum adds the warpgroup finds the tile's row maxima, rescales l and O and
+// repeats the pass.  P at a row's maximum is 2^-40 in bf16 (m is the maximum and 40):
+// of 2^28 slots with P up to 2^-28 the sum P V stays within 32 bits whatever V holds, and down to
+// V of 1e-21 their product does not fall below them.  In fp16, whose V ends at 65504
+// and whose range is short, it is 2^7, so that entries down to 2^-21 of the largest
+// keep their precision.
 //
 // Bound: HBM for up to 64 rows of a key/value head where the work is long (64
 // contexts of 6800 slots: N = 1, G = 4, D = 128 272 us, 6.6 TB/s; D = 64 154 us,
@@ -74,6 +76,8 @@ constexpr int kMaxCtas = 160;
 constexpr int kNoRow = 0x7fffffff;   // a column without a row (rows of zeros: ~row)
 constexpr float kNoScore = -1e30f;   // m of a row that has seen nothing
 constexpr int kSmemMax = 227 * 1024;
+template <class T>
+constexpr float kLift = T::kId == Bf16::kId ? -40.f : 7.f;  // log2 of P at a row's maximum
 
 // A CTA's range of tiles, for the joining kernel.
 struct alignas(16) Range {
@@ -576,6 +580,14 @@ __device__ __forceinline__ void tile_pass(uint32_t tS, int nch, f32x2 c2, const 
   st_matrices(a1 + (nch - 1) * kPBlock, w[1]);
 }
 
+// ln(2^m l).  (m goes back to the maximum first, which is exact, so that no digits
+// are lost to the distance.)
+template <class T>
+__device__ __forceinline__ float log_sum(float m, float l) {
+  constexpr float far = kLift<T> < 0.f ? kLift<T> : 0.f, back = kLift<T> < 0.f ? 0x1p40f : 1.f;
+  return (m + far + log2f(l * back)) * 0.6931471805599453f;
+}
+
 // The largest growth of a row sum.
 template <int N>
 __device__ __forceinline__ float growth(const f32x2 (&l)[N], const f32x2 (&old)[N]) {
@@ -800,8 +812,7 @@ __device__ __noinline__ void clean_tile(const Args& a, Misc& sm, int t, int ctx,
 template <class T, int D, int NC>
 __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, char* Q, int qbytes, char* V,
                                              char* P0, int wg) {
-  constexpr float kGrow = T::kId == Bf16::kId ? 1073741824.f : 32768.f;
-  constexpr float kLift = T::kId == Bf16::kId ? 0.f : 7.f;  // log2 of P at a row's maximum
+  constexpr float kGrow = T::kId == Bf16::kId ? 0x1p-28f : 0x1p15f;
   const bool split = a.split;
   char* P = P0 + a.poff[wg];
   Scratch& sc = *reinterpret_cast<Scratch*>(P);
@@ -895,7 +906,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
           if (wt < ncj) {
             const float mx = fmaxf(fmaxf(sc.red[0][wt], sc.red[1][wt]), fmaxf(sc.red[2][wt], sc.red[3][wt]));
             const float mo = -nm[wt];
-            const float mn = fmaxf(mo, mx - kLift);
+            const float mn = fmaxf(mo, mx - kLift<T>);
             sc.fac[wt] = mn == mo ? 1.f : exp2f(mo - mn);
             nm[wt] = -mn;
           }
@@ -986,7 +997,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
           const float inv = empty ? 0.f : 1.f / L;
 #pragma unroll 1
           for (int w = w0; w < w1; ++w) scratch(w).fac[cc] *= inv;
-          if (a.lse) a.lse[orow + row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+          if (a.lse) a.lse[orow + row] = empty ? -INFINITY : log_sum<T>(M, L);
           if (empty) row = ~row;
         } else {
           a.part_ml[pslot + cc] = make_float2(M, absent ? 0.f : L);  // (0: an empty row)
@@ -1592,7 +1603,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 6) attn_combine_kernel(const 
 #pragma unroll
   for (int q = 0; q < E; q += 2)
     *reinterpret_cast<uint32_t*>(out + 2 * q) = empty ? 0u : T_::pack(o[q] * inv, o[q + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : log_sum<T_>(M, L);
 }
 
 // ---------------------------------------------------------------------------
