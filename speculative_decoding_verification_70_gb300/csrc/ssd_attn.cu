@@ -54,6 +54,7 @@
 #include <cuda.h>
 #include <math.h>
 
+#include "ssd_async.cuh"
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"
 
@@ -159,36 +160,9 @@ static_assert(sizeof(Scratch) <= kPMin, "the smallest P buffer");
 // ---------------------------------------------------------------------------
 // mbarriers, TMA, tcgen05
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t sptr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void bar_init(uint64_t* b, int n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(n) : "memory");
-}
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sptr(b)) : "memory");
 }
-__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sptr(b)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.b32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(sptr(b)), "r"(parity), "r"(20000)  // sleeps up to 20 us a try
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ unsigned long long now_ns() {
-  unsigned long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
 // Bounded wait: after wait_us (or once another wait of the CTA gave up) the CTA
 // runs on without waiting, to its end; the error word says so.
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, Misc& sm, int* err) {
@@ -333,11 +307,6 @@ __device__ __forceinline__ void tm_st_frag(uint32_t addr, const uint32_t (&r)[16
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // ---------------------------------------------------------------------------
 // the tiles of the batch
 // ---------------------------------------------------------------------------

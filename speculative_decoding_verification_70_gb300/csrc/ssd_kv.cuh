@@ -117,20 +117,6 @@ struct F16 {
   }
 };
 
-template <class T>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&o)[8]) {
-  o[0] = T::lo(v.x); o[1] = T::hi(v.x);
-  o[2] = T::lo(v.y); o[3] = T::hi(v.y);
-  o[4] = T::lo(v.z); o[5] = T::hi(v.z);
-  o[6] = T::lo(v.w); o[7] = T::hi(v.w);
-}
-
-template <class T>
-__device__ __forceinline__ uint4 pack8(const float (&o)[8]) {
-  return make_uint4(T::pack(o[0], o[1]), T::pack(o[2], o[3]), T::pack(o[4], o[5]),
-                    T::pack(o[6], o[7]));
-}
-
 // ---------------------------------------------------------------------------
 // kernel arguments
 // ---------------------------------------------------------------------------

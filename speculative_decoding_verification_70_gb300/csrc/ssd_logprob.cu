@@ -35,6 +35,7 @@
 
 #include <algorithm>
 
+#include "ssd_async.cuh"
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"
 
@@ -72,7 +73,7 @@ using Part = LogprobPart;
 
 struct LpSmem {
   uint4 ring[kLpWarps][kStages][kSlice];  // each warp's own
-  unsigned long long bar[kLpWarps][kStages];
+  uint64_t bar[kLpWarps][kStages];
   alignas(16) unsigned long long key[kList];  // candidates: order of the value, then of the index
   unsigned long long best[kLpTop];
   float m[kLpWarps], S[kLpWarps], U[kLpWarps];
@@ -111,11 +112,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 __device__ __forceinline__ float min3(float a, float b, float c) {
   float r;
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -471,34 +467,21 @@ __device__ __noinline__ void select_best(LpSmem& sm, unsigned long long k0, unsi
 // ---------------------------------------------------------------------------
 // Bulk copies of a warp's slices into its ring, one mbarrier a stage.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t lp_ptr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void lp_copy(uint4* dst, const void* src, int bytes, unsigned long long* bar, int withheld) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(lp_ptr(bar)), "r"(bytes + withheld)
-               : "memory");
+__device__ __forceinline__ void lp_copy(uint4* dst, const void* src, int bytes, uint64_t* bar, int withheld) {
+  bar_expect(bar, bytes + withheld);
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   lp_ptr(dst)),
-               "l"(src), "r"(bytes), "r"(lp_ptr(bar))
+                   sptr(dst)),
+               "l"(src), "r"(bytes), "r"(sptr(bar))
                : "memory");
 }
 // Bounded wait: after `us` microseconds (or once another wait of the CTA gave
 // up) the row counts as lost; the CTA runs on to its end.
-__device__ __forceinline__ void lp_wait(unsigned long long* bar, uint32_t parity, unsigned us, LpSmem& sm, int* err) {
+__device__ __forceinline__ void lp_wait(uint64_t* bar, uint32_t parity, unsigned us, LpSmem& sm, int* err) {
   unsigned long long t0 = 0;
   for (unsigned i = 1;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.b32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(lp_ptr(bar)), "r"(parity), "r"(20000)
-        : "memory");
-    if (ok || sm.lost) return;
+    if (bar_try(bar, parity) || sm.lost) return;
     if ((i & 31) == 0) {  // the global timer is slow to read
-      unsigned long long t;
-      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      const unsigned long long t = now_ns();
       if (t0 == 0) t0 = t;
       if (t - t0 > us * 1000ull) {
         sm.lost = 1;
@@ -604,7 +587,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     Raw<Tag> now[U];
     // aligned rows come by bulk copies, a warp's slices on its own ring
     const int vfull = p.whole ? min(v1, p.V / N) : v0;
-    unsigned long long* bar = sm.bar[warp];
+    uint64_t* bar = sm.bar[warp];
     auto slice = [&](int k) { return v0 + k * (kLpThreads * U) + warp * kSlice; };
     int stage = 0;
     uint32_t phase = 0;
@@ -616,8 +599,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     if (lane == 0) {
       sm.n[warp] = 0;
 #pragma unroll
-      for (int k = 0; k < kStages; ++k)
-        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(lp_ptr(bar + k)) : "memory");
+      for (int k = 0; k < kStages; ++k) bar_init(bar + k, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
