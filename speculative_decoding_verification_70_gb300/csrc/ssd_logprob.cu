@@ -84,7 +84,8 @@ struct LpSmem {
   unsigned long long wkey[kLpWarps];
   int n[kLpWarps], last;
   float tau;
-  volatile int lost;  // a copy did not come
+  alignas(8) volatile uint8_t lost[kLpWarps];  // a copy of this warp did not come
+  volatile int gone;                           // of some warp: the others need not wait as long
 };
 
 // Values as numbers above 0 of the same order, and back; -0 counts as 0.
@@ -266,9 +267,13 @@ struct Raw<BF16Tag> {
 };
 
 // (z - m) c, also where z - m or c exceeds 32 bits.
+__device__ __noinline__ float far_scaled(float z, float m, float c, float T) {
+  const float d = z - m;
+  return d > -INFINITY ? d / T * kLog2e : 2.f * ((0.5f * z - 0.5f * m) * c);
+}
 __device__ __forceinline__ float scaled(float z, float m, float c, float T) {
   const float d = z - m;
-  return d > -INFINITY ? (c < kMost ? d * c : d / T * kLog2e) : 2.f * ((0.5f * z - 0.5f * m) * c);
+  return d > -INFINITY && c < kMost ? d * c : far_scaled(z, m, c, T);
 }
 
 // What two lanes or parts hold, joined over the warp in a fixed order: m first,
@@ -474,19 +479,21 @@ __device__ __forceinline__ void lp_copy(uint4* dst, const void* src, int bytes, 
                "l"(src), "r"(bytes), "r"(sptr(bar))
                : "memory");
 }
-// Bounded wait: after `us` microseconds (or once another wait of the CTA gave
-// up) the row counts as lost; the CTA runs on to its end.
-__device__ __forceinline__ void lp_wait(uint64_t* bar, uint32_t parity, unsigned us, LpSmem& sm, int* err) {
+// Bounded wait: after `us` microseconds (or once another wait of the CTA gave up)
+// the row counts as lost, and the CTA runs on to its end.
+__device__ __forceinline__ bool lp_wait(uint64_t* bar, uint32_t parity, unsigned us, LpSmem& sm, int* err) {
   unsigned long long t0 = 0;
   for (unsigned i = 1;; ++i) {
-    if (bar_try(bar, parity) || sm.lost) return;
-    if ((i & 31) == 0) {  // the global timer is slow to read
+    if (bar_try(bar, parity)) return true;
+    const bool other = sm.gone;
+    if (other || (i & 31) == 0) {  // the global timer is slow to read
       const unsigned long long t = now_ns();
       if (t0 == 0) t0 = t;
-      if (t - t0 > us * 1000ull) {
-        sm.lost = 1;
+      if (other || t - t0 > us * 1000ull) {
+        sm.lost[threadIdx.x >> 5] = 1;
+        sm.gone = 1;
         atomicOr(err, kErrTimeout);
-        return;
+        return false;
       }
     }
   }
@@ -551,8 +558,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
   f32x2 S2 = pk2(0.f, 0.f), E2 = S2;  // of even and odd elements
   int count = 0;
   bool gone = false;  // a copy did not come: no answer
-  if (tid == 0) sm.lost = 0;
-  __syncthreads();
   if (TOP && tid < kLpTop) sm.best[tid] = 0;
   if (!fail) {
     if (tok_ok) zt = Tag::load1(z + tok);
@@ -586,30 +591,33 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     int round = 0, raise_at = kRaise;
     Raw<Tag> now[U];
     // aligned rows come by bulk copies, a warp's slices on its own ring
-    const int vfull = p.whole ? min(v1, p.V / N) : v0;
+    // (a lane for which a copy did not come waits for none and starts none any more:
+    // its barrier's phase is still open)
+    int vfull = p.whole ? min(v1, p.V / N) : v0;
     uint64_t* bar = sm.bar[warp];
     auto slice = [&](int k) { return v0 + k * (kLpThreads * U) + warp * kSlice; };
     int stage = 0;
     uint32_t phase = 0;
-    auto fetch = [&](int k, int stage, bool lost) {
+    auto fetch = [&](int k, int stage) {
       const int v = slice(k), n = min(kSlice, vfull - v);
-      if (n > 0 && lane == 0 && !lost)  // (a barrier of a copy that did not come is not armed again)
+      if (n > 0 && lane == 0)
         lp_copy(sm.ring[warp][stage], z + static_cast<long long>(v) * N, n * 16, bar + stage, p.withheld);
     };
     if (lane == 0) {
       sm.n[warp] = 0;
+      sm.lost[warp] = 0;
+      sm.gone = 0;  // (by each warp before it looks there)
 #pragma unroll
       for (int k = 0; k < kStages; ++k) bar_init(bar + k, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) fetch(k, k, false);
+    for (int k = 0; k < kStages; ++k) fetch(k, k);
 #pragma unroll 1
     for (int b = v0; b < v1; b += kLpThreads * U, ++round) {
       const int first = slice(round), n = min(kSlice, vfull - first);
-      if (n > 0) lp_wait(bar + stage, phase, p.wait_us, sm, p.err);
-      const bool lost = sm.lost;  // (read beside the elements)
+      if (n > 0 && !lp_wait(bar + stage, phase, p.wait_us, sm, p.err)) vfull = v0;
       const uint4* ring = sm.ring[warp][stage] + lane;
       if (n >= kSlice) {
 #pragma unroll
@@ -624,7 +632,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
         }
       }
       __syncwarp();
-      fetch(round + kStages, stage, lost);
+      fetch(round + kStages, stage);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1;
@@ -767,7 +775,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     if (tok_ok && zt == -INFINITY)
       for (int i = v0 * N + tid; i < min(tok, v1 * N); i += kLpThreads) count += Tag::load1(z + i) == -INFINITY;
     const bool again = __syncthreads_or(plain);
-    gone = sm.lost;
+    gone = *reinterpret_cast<const volatile unsigned long long*>(sm.lost) != 0;
     if (gone)  // copies land before the shared memory is used for something else
       for (int k = 0; k < 200; ++k) __nanosleep(100000);
     if (again) {
@@ -796,7 +804,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     }
     // (by every warp: shuffles where only some warps run cost 250 clocks each)
     const bool in = lane < kLpWarps;
-    m = in ? sm.m[lane] : -INFINITY;
+    m = sm.m[lane % kLpWarps];
     S = in ? sm.S[lane] : 0.f;
     E = in ? sm.U[lane] : 0.f;
     join_warp(c, T, m, S, E);
@@ -830,7 +838,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
     __threadfence();
     if (!fail) {
       const bool in = lane < p.split;  // lane k holds part k
-      m = in ? __ldcg(&parts[lane].m) : -INFINITY;
+      m = __ldcg(&parts[in ? lane : 0].m);
       S = in ? __ldcg(&parts[lane].S) : 0.f;
       E = in ? __ldcg(&parts[lane].U) : 0.f;
       join_warp<true>(c, T, m, S, E);
