@@ -626,7 +626,8 @@ SSD_API ssd_status ssd_tree_attention(const ssd_paged_kv *kv, const ssd_draft_no
  *              stride N): slot ctx + out_node[b, i] moves to slot ctx + 1 + i
  *              for i < accept_len[b].  out_node NULL: a chain, whose nodes
  *              already lie there.
- *   new_len  : [B] int32: ctx_len + 1 + accept_len.  Must not be ctx_len.
+ *   new_len  : [B] int32: ctx_len + 1 + accept_len.  Must not overlap ctx_len or
+ *              accept_len.
  * A negative accept_len commits nothing (new_len = ctx_len), and so does a
  * path that is not increasing within 1 .. N-1 (SSD_DEVERR_BAD_TREE) or a
  * length out of range (SSD_DEVERR_BAD_LENGTH).  A move from or to a page id

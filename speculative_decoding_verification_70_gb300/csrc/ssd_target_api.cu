@@ -75,6 +75,12 @@ NodesView view_of(const ssd_draft_nodes& n) {
   return v;
 }
 
+// n words at a and at b share some.
+bool overlap(const int32_t* a, const int32_t* b, int n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x > y ? x - y : y - x) < 4ull * n;
+}
+
 bool rows16(const void* p, int64_t a, int64_t b, int64_t c) {
   return aligned(p, 16) && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
 }
@@ -173,7 +179,7 @@ ssd_status ssd_kv_commit(const ssd_paged_kv* kv, int layers, int64_t k_layer, in
   if (!ctx_len || !accept_len || !new_len || !ws) return SSD_ERR_INVALID_ARG;
   if (B < 1 || N < 1 || N > SSD_MAX_TREE_NODES || layers < 1) return SSD_ERR_INVALID_ARG;
   if (layers > 1 && (!stride_ok(k_layer) || !stride_ok(v_layer))) return SSD_ERR_INVALID_ARG;
-  if (new_len == ctx_len || new_len == accept_len) return SSD_ERR_INVALID_ARG;
+  if (overlap(new_len, ctx_len, B) || overlap(new_len, accept_len, B)) return SSD_ERR_INVALID_ARG;
   if (!aligned(ctx_len, 4) || !aligned(accept_len, 4) || !aligned(out_node, 4) ||
       !aligned(new_len, 4) || !aligned(ws, 256))
     return SSD_ERR_INVALID_ARG;

@@ -234,3 +234,15 @@ def test_batches_at_the_end_of_32_bits(lib):  # noqa: F811
         for call in (abi._attend, abi._append):
             assert call(lib, nodes=abi._nodes(B=most + 1, N=N)) == abi.INVALID
             assert call(lib, nodes=abi._nodes(B=most, N=N)) == 3
+
+
+@needs_no_gpu
+def test_commit_lengths_that_overlap(lib):  # noqa: F811
+    """New lengths over a part of the old ones: blocks of other layers would read
+    what the first has written."""
+    def commit(new, ctx=abi.P, acc=abi.P + 4096, B=8):
+        return lib.ssd_kv_commit(abi._kv(), 1, 0, 0, B, 4, ctx, acc, abi.P + 8192, new, abi.P, 256, None)
+    for at in (abi.P, abi.P + 4096):
+        for off in (-28, -4, 0, 4, 28):
+            assert commit(at + off) == abi.INVALID
+        assert commit(at - 32) == 3 and commit(at + 32) == 3
