@@ -37,20 +37,24 @@
 // scores, and only where a row's l grew by more than 2^12 (fp16: 2^8) of what the
 // maximum adds the warpgroup finds the tile's row maxima, rescales l and O and
 // repeats the pass.  P at a row's maximum is 2^-40 in bf16 (m is the maximum and 40):
-// of 2^28 slots with P up to 2^-28 the sum P V stays within 32 bits whatever V holds, and down to
-// V of 1e-21 their product does not fall below them.  In fp16, whose V ends at 65504
-// and whose range is short, it is 2^7, so that entries down to 2^-21 of the largest
-// keep their precision.
+// of 2^28 slots with P up to 2^-28 the sum P V stays within 32 bits whatever V holds,
+// and down to V of 1e-21 their product does not fall below them.  In fp16, whose V
+// ends at 65504 and whose range is short, it is 2^7, so that entries down to 2^-21 of
+// the largest keep their precision.  (q k c - m is rounded once, but m itself is a
+// number of 32 bits: scores beyond 2^24 differ by what their own roundings weigh,
+// and beyond 2^30 the rounding of m alone exceeds what an exponential holds.)
 //
 // Bound: HBM for up to 64 rows of a key/value head where the work is long (64
-// contexts of 6800 slots: N = 1, G = 4, D = 128 272 us, 6.6 TB/s; D = 64 154 us,
-// 5.8 TB/s).  With more rows the bytes in flight: Q and P leave four (168 rows)
-// or three (256 rows) slots of 32 KB for the rings, which at a loaded latency of
-// about 4000 cycles is 64 trees of 21 nodes over 500..8000 slots in 196 us, 3.9
-// TB/s, two trees of 64 nodes over 60000 and 130000 slots in 235 us, 3.3 TB/s.
+// contexts of 6800 slots, 32 + 8 heads, N = 1: D = 128 277 us, 6.4 TB/s; D = 64 178
+// us, 5.0 TB/s).  With more rows the bytes in flight: Q and P leave four (168 rows)
+// or three (256 rows) slots of 32 KB for the rings, which come round once in 5 us: 64
+// trees of 21 nodes over 500..8000 slots in 197 us, 3.9 TB/s, two trees of 64 nodes
+// over 60000 and 130000 slots in 235 us, 3.3 TB/s.  Beyond 256 rows every row block
+// reads K and V (8 trees of 64 nodes, 8 heads a group, 500..8000 slots: 97 us).
 // Short items: an item's start and end cost 5 us of a CTA (64 single tokens over
-// 200..6000 slots, D = 64: 65 us, 3.5 TB/s).  One short sequence: the chain of
-// set-up, first copies, one tile, results and join (8 nodes over 4096 slots: 20 us).
+// 200..6000 slots: D = 64 63 us, 3.6 TB/s, D = 128 86 us, 5.3 TB/s).  One short
+// sequence: the chain of set-up, first copies, one tile, results and join (8 nodes
+// over 4096 slots: 20 us).
 #include <cuda.h>
 #include <math.h>
 
@@ -1734,9 +1738,12 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
     a.poff[w] = sh.poff[w];
   }
   a.pbytes = sh.pbytes;
-  // About 5 us of the pass's time.  Measured at 4, 6, 8, 10 tiles: 64 single
-  // tokens, D = 64, 77.6, 71.5, 66.5, 69.3 us; 64 trees of 168 rows, D = 128, 214,
-  // 198, 198, 205; 32 trees of 256 rows 177, 173, 181, 183.
+  // About 5 us of the pass's time.  Measured at 4, 6, 8, 10 tiles: 64 single tokens
+  // over 200..6000 slots, D = 64, 73.0, 66.3, 63.4, 65.5 us, D = 128, 83.6, 85.4,
+  // 86.8, 88.0; 64 chains of 32 rows, D = 128, 89.6, 90.3, 93.1, 95.9; 32 trees of 64
+  // rows, D = 128, 72.2, 63.3, 63.3, 63.4; 64 trees of 168 rows, D = 128, 208.6, 197.0,
+  // 202.1, 209.4, D = 64, 195.5, 189.1, 193.5, 202.1; 32 trees of 128 rows, D = 64, 79.4,
+  // 78.7, 78.7, 78.7; 32 trees of 256 rows, D = 128, 164.5, 162.3, 170.7, 172.8.
   a.item_cost = D == 64 && !a.split ? 8 : 6;
   a.q = p.q; a.q_b = p.q_b; a.q_n = p.q_n; a.q_h = p.q_h;
   a.zero = p.scale == 0.f;
@@ -1776,7 +1783,7 @@ cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStr
   if (slots < 3) return cudaErrorInvalidConfiguration;
   // (an odd slot to K: a product of scores frees its K tile at once, but the next
   // one is wanted a softmax earlier than the next V tile.  Two wide trees, three
-  // slots: 238 us, with two for V 249)
+  // slots: 235 us, with two for V 244)
   a.nk = (slots + 1) / 2;
   a.nv = slots - a.nk;
   const size_t smem = fixed + static_cast<size_t>(slots) * slot;

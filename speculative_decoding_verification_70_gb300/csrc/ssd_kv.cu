@@ -11,9 +11,9 @@
 // tokens.  The grid is one wave, so that the chain is waited for once, and its
 // places are found once a token, by one lane; a lane holds 16 entries of a
 // head, which halves the address arithmetic of eight.  64 trees of 21 tokens,
-// 64 + 16 heads of 128 (55 MB): 14.8 us, 3.8 TB/s (a CTA per token, 8 entries a
-// lane: 24.6 us); 512 chains of 8, 32 + 16 heads of 64: 12.7 us, 4.0 TB/s (26.8);
-// one chain of 8: 3.6 us.
+// 64 + 16 heads of 128 (56 MB): 15.1 us, 3.7 TB/s (a CTA per token, 8 entries a
+// lane: 24.6 us); 512 chains of 8, 32 + 16 heads of 64 (51 MB): 13.1 us, 3.9 TB/s
+// (26.8); one chain of 8: 3.7 us.
 // kv_commit_kernel: a copy of the accepted rows, bound by HBM (or by its two
 // chained round trips).  64 paths of up to 12 nodes, 32 layers (118 MB): 23.4 us,
 // 5.0 TB/s, of which launch and look-up are 3.6; 64 to 512 threads a CTA, 4 to 12

@@ -22,15 +22,16 @@
 // (hundreds of equal logits, or of -inf) is searched K times instead.
 //
 // A warp copies its slices of the row into a ring of its own (bulk copies, two
-// rounds of 2 KB ahead: 96 KB in flight on an SM; with three or four the fp32
-// pass of K = 0 fell from 6.6 to 4 TB/s).  One CTA per row, or per part of a row,
+// rounds of 2 KB ahead: 96 KB in flight on an SM; with three the fp32
+// pass of K = 0 falls from 6.6 to 5.0 TB/s).  One CTA per row, or per part of a row,
 // whose last CTA to finish joins the parts.
 //
 // Bound: HBM for fp32 (4096 x 151936, K = 8: 386 us, 6.5 TB/s; 2048 rows, K = 0:
-// 187 us, 6.6 TB/s); 384 rows of bf16 are one wave, which begins and ends together
-// (384 x 151936: K = 0 25 us, 4.7 TB/s) and whose candidates' steps, two raised
-// bounds and the selection leave the memory idle (K = 20 43 us); a few rows are
-// steps one after another (8 x 128256: K = 0 5.3 us, K = 5 8.6 us).
+// 189 us, 6.6 TB/s); 384 rows of bf16 are one wave, which begins and ends together
+// (384 x 151936: K = 0 26 us, 4.5 TB/s) and whose candidates' steps, two raised
+// bounds and the selection leave the memory idle (K = 20 43 us); a few rows, and
+// short ones, are steps one after another (8 x 128256 bf16: K = 0 6.5 us, K = 5 9.5
+// us; 4096 x 4096 bf16: K = 0 43 us, K = 8 67 us, of 5 us of bytes).
 #include <math.h>
 
 #include <algorithm>
@@ -44,9 +45,10 @@ namespace {
 
 constexpr int kLpThreads = 256;
 // CTAs of an SM.  Four (64 registers a thread) hide more of the candidates'
-// steps where fp32 rows ask for the best (R = 1000, V = 128256, K = 8: 96 us,
-// three: 103); elsewhere three are as fast or faster (bf16, 384 x 151936, K = 20:
-// 43 us, four: 48; fp32, 2048 x 151936, K = 0: 186, four: 198).
+// steps where fp32 rows ask for the best (1000 x 128256, K = 8: 99 us, three: 108;
+// 4096 x 151936: 386, three: 405); elsewhere long rows are faster with three (bf16,
+// 384 x 151936, K = 20: 43 us, four: 46; fp32, 2048 x 151936, K = 0: 189, four: 212),
+// short ones with four (bf16, 4096 x 4096, K = 0: 43, four: 36; K = 8: 67, four: 60).
 template <class Tag, bool TOP>
 constexpr int kLpCtas = TOP && Tag::kVec == 4 ? 4 : 3;
 constexpr int kFlight = 4;        // vectors of a thread and round
@@ -905,8 +907,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas<Tag, TOP>) logprob_kernel(
 // full SM (24 K bf16 or 12 K fp32 elements a microsecond).  n CTAs of an SM take
 // turns (one alone reaches 7/8 of the rate) and begin and end in 4 us, or 8 us and
 // 0.1 us K where the best are asked for; the join of the parts costs 1.3 us.
-// (128256 bf16 logits, K = 0: 9.9 us whole, 5.8, 4.9, 5.5 in 4, 8, 31 parts; 384
-// rows of 151936, K = 20: 43 us whole, 54 in two.)
+// (8 rows of 128256 bf16 logits: K = 0 12.2 us whole, 8.1, 7.0, 6.8 in 4, 8, 31
+// parts, 6.5 as chosen; K = 5 18.5, 11.8, 10.3, 10.1, 9.6; 384 rows of 151936, K = 20:
+// 43 us whole, 54 in two.)
 int split_of(int R, int V, int K, bool half) {
   const long long us = half ? 24000 : 12000, sms = 152, ctas = K > 0 && !half ? 4 : 3;
   const long long fixed = K > 0 ? 8 * us + us * K / 10 : 4 * us;
