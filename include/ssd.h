@@ -603,10 +603,10 @@ SSD_API ssd_status ssd_kv_append(const ssd_paged_kv *kv, const ssd_draft_nodes *
  *   out      : [B, N, Hq, D] contiguous, kv->dtype, 16-byte aligned.
  *   lse      : [B, N, Hq] fp32 or NULL: log sum exp(scale * q.k) of the seen
  *              slots.
- *   scale    : finite.
+ *   scale    : finite, up to 2e38.
  *   ws       : ssd_tree_attention_workspace_bytes(B, N, Hq, Hkv, D) bytes.
  * Scores are held in 32 bits: where scale * q.k exceeds 2^24 their roundings decide
- * between slots, and beyond 2^30 a row may come out empty or NaN.
+ * between slots, and beyond 2^26 a row may come out empty or NaN.
  * An absent node, or one whose seen slots all score -inf, gets out 0 and
  * lse -inf.  Slots that a node does not see never reach its output, whatever
  * they hold (NaN and infinities included).  A page id out of range reads as a

@@ -42,7 +42,7 @@
 // ends at 65504 and whose range is short, it is 2^7, so that entries down to 2^-21 of
 // the largest keep their precision.  (q k c - m is rounded once, but m itself is a
 // number of 32 bits: scores beyond 2^24 differ by what their own roundings weigh,
-// and beyond 2^30 the rounding of m alone exceeds what an exponential holds.)
+// and beyond 2^27 the rounding of m alone exceeds what P holds.)
 //
 // Bound: HBM for up to 64 rows of a key/value head where the work is long (64
 // contexts of 6800 slots, 32 + 8 heads, N = 1: D = 128 277 us, 6.4 TB/s; D = 64 178

@@ -147,7 +147,8 @@ ssd_status ssd_tree_attention(const ssd_paged_kv* kv, const ssd_draft_nodes* nod
   ssd_status st = check_kv(kv);
   if (st == SSD_OK) st = check_nodes(nodes);
   if (st != SSD_OK) return st;
-  if (!q || !out || !ws || !isfinite(scale)) return SSD_ERR_INVALID_ARG;
+  // (scores are counted in units of log 2)
+  if (!q || !out || !ws || !isfinite(scale) || fabsf(scale) > 2e38f) return SSD_ERR_INVALID_ARG;
   if (Hq < kv->Hkv || Hq % kv->Hkv != 0 || Hq / kv->Hkv > 64) return SSD_ERR_INVALID_ARG;
   if (q_b < 0 || q_n < 0 || q_h < 0 || !rows16(q, q_b, q_n, q_h)) return SSD_ERR_INVALID_ARG;
   if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 256)) return SSD_ERR_INVALID_ARG;

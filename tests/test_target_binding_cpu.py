@@ -246,3 +246,12 @@ def test_commit_lengths_that_overlap(lib):  # noqa: F811
         for off in (-28, -4, 0, 4, 28):
             assert commit(at + off) == abi.INVALID
         assert commit(at - 32) == 3 and commit(at + 32) == 3
+
+
+@needs_no_gpu
+def test_scales_beyond_32_bits(lib):  # noqa: F811
+    """A scale that is infinite in units of log 2."""
+    for scale in (2.5e38, 3.4e38, -3.4e38):
+        assert abi._attend(lib, scale=scale) == abi.INVALID
+    for scale in (2e38, -1e38, 1e-40, 0.0):
+        assert abi._attend(lib, scale=scale) == 3
