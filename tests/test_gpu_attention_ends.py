@@ -1,10 +1,8 @@
-"""Tree attention at the ends of its range: values near the type's largest,
-batches of more sequences than a block has threads.
+"""Tree attention at the ends of its range: values near the type's largest, and
+small ones.
 
 Tolerances as in tests/test_gpu_target.py.
 """
-import math
-
 import pytest
 import torch
 
