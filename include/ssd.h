@@ -640,6 +640,100 @@ SSD_API ssd_status ssd_kv_commit(const ssd_paged_kv *kv, int layers, int64_t k_l
                          const int32_t *out_node, int32_t *new_len, void *ws, size_t ws_bytes,
                          ssd_stream_t stream);
 
+/* Most new tokens of a sequence in one call of the operators for chunks. */
+#define SSD_MAX_CHUNK (1 << 20)
+
+/*
+ * ssd_kv_append_at -- ssd_kv_append for chunks and for cut caches: a chain
+ * (parent NULL) may have up to SSD_MAX_CHUNK tokens, and pos0 ([B] int32 or NULL:
+ * ctx_len) gives the position of node 0, which after an eviction is not its slot:
+ * node j has position pos0[b] + depth(j).  (A position < 0 or >= max_pos makes
+ * its node absent where rot > 0.)
+ */
+SSD_API ssd_status ssd_kv_append_at(const ssd_paged_kv *kv, const ssd_draft_nodes *nodes, const int32_t *pos0,
+                         int Hq, const void *q, int64_t q_b, int64_t q_n, int64_t q_h, const void *k,
+                         const void *v, int64_t kv_b, int64_t kv_n, int64_t kv_h, void *q_out,
+                         const float *cos_sin, int max_pos, int rot, int interleaved,
+                         const void *q_norm, const void *k_norm, float eps, void *ws,
+                         size_t ws_bytes, ssd_stream_t stream);
+
+/*
+ * ssd_chunk_attention -- attention of chunks of new tokens over the cache that
+ * already holds them: prompts, parts of prompts, drafted chains, single tokens,
+ * in one ragged batch.  tokens: chains (parent NULL) of up to SSD_MAX_CHUNK
+ * tokens; sequence b has n_nodes[b] (or N) of them, in slots ctx_len[b] ...
+ * The token in slot p sees the slots s <= p with s > p - window (window 0: all
+ * of them) or s < sinks, of key/value head h / (Hq / Hkv);
+ *     out = sum_s p_s v_s,  p = softmax over the seen slots of scale * q.k_s.
+ *   q        : [B, N, Hq, D] with element strides q_b, q_n, q_h, positive
+ *              multiples of 8 (those of a dimension of one entry too), type
+ *              kv->dtype, 16-byte aligned; Hq a multiple of Hkv, at most 64
+ *              heads a group.
+ *   out      : [B, N, Hq, D] contiguous, kv->dtype, 16-byte aligned.
+ *   lse      : [B, N, Hq] fp32 or NULL: log sum exp(scale * q.k) of the seen
+ *              slots.
+ *   ws       : ssd_chunk_attention_workspace_bytes(B, N, Hq, Hkv, D) bytes.
+ * scale, empty rows, tokens that are not there, slots that are not seen, page
+ * ids out of range, scores beyond 2^24 and tiles that do not arrive: as in
+ * ssd_tree_attention.
+ */
+SSD_API size_t ssd_chunk_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
+SSD_API ssd_status ssd_chunk_attention(const ssd_paged_kv *kv, const ssd_draft_nodes *tokens, int Hq,
+                              const void *q, int64_t q_b, int64_t q_n, int64_t q_h, int window,
+                              int sinks, float scale, void *out, float *lse, void *ws, size_t ws_bytes,
+                              ssd_stream_t stream);
+
+/*
+ * ssd_kv_weights -- what attention each slot received: for every slot s below
+ * ctx_len[b] + n_nodes[b] of a sequence with new tokens
+ *     w[b, h, s] = decay * w[b, h, s]
+ *                + sum over the tokens i and query heads g of head h's group that
+ *                  see s of exp(scale * q_ig.k_s - lse_ig),
+ * with the slots that ssd_chunk_attention's token sees and the lse it wrote
+ * (rows of lse -inf add nothing).
+ *   lse      : [B, N, Hq] fp32.
+ *   weights  : fp32, row (b, h) at b*w_b + h*w_h (elements), w_len entries; decay 0
+ *              writes without reading.  Slots behind a sequence's end stay as
+ *              they are.
+ *   kv, tokens, q, window, sinks, scale : as in ssd_chunk_attention; the values
+ *              (v) are not read.
+ *   ws       : SSD_ERRWORD_BYTES.
+ * A sequence with ctx_len + n_nodes > w_len sets SSD_DEVERR_BAD_LENGTH and adds
+ * nothing.  Sums are made in an order that only the sizes decide.
+ */
+SSD_API ssd_status ssd_kv_weights(const ssd_paged_kv *kv, const ssd_draft_nodes *tokens, int Hq, const void *q,
+                         int64_t q_b, int64_t q_n, int64_t q_h, const float *lse, int window, int sinks,
+                         float scale, float decay, float *weights, int64_t w_b, int64_t w_h, int w_len,
+                         void *ws, size_t ws_bytes, ssd_stream_t stream);
+
+/*
+ * ssd_kv_evict -- every sequence longer than `budget` slots cut down to it, in
+ * `layers` caches that share one page table (layer l starts at k + l*k_layer, v +
+ * l*v_layer), every head of every layer by its own weights: the first `sinks`
+ * slots stay, the last `recent`, and of those between the heaviest budget - sinks
+ * - recent (of equal weights the lower slot; -0 equals 0, NaN is below all).
+ * The kept slots' keys and values move to slots 0 .. budget-1 in slot order.
+ *   weights  : fp32, row (l, b, h) at l*w_layer + b*w_b + h*w_h, w_len entries, of
+ *              which the first ctx_len[b] count.
+ *   budget   : >= 1 and >= sinks + recent.
+ *   new_len  : [B] int32: min(ctx_len, budget).  Must not overlap ctx_len.
+ *   kept     : [layers, B, Hkv, budget] int32: the slot that each slot's entry
+ *              came from, -1 behind new_len.
+ *   w_out    : the kept slots' weights, then zeros, w_len entries a row, with its
+ *              own strides; weights itself (with its strides), memory apart from
+ *              it, or NULL.
+ *   ws       : SSD_ERRWORD_BYTES.
+ * A sequence with ctx_len < 0, beyond its table or beyond w_len
+ * (SSD_DEVERR_BAD_LENGTH) stays as it is: new_len = ctx_len, kept = -1, w_out not
+ * written.  A move from or to a page id out of range is left out
+ * (SSD_DEVERR_BAD_PAGE).  Sequences must not share pages.
+ */
+SSD_API ssd_status ssd_kv_evict(const ssd_paged_kv *kv, int layers, int64_t k_layer, int64_t v_layer, int B,
+                         const int32_t *ctx_len, const float *weights, int64_t w_layer, int64_t w_b,
+                         int64_t w_h, int w_len, int budget, int sinks, int recent, int32_t *new_len,
+                         int32_t *kept, float *w_out, int64_t wo_layer, int64_t wo_b, int64_t wo_h,
+                         void *ws, size_t ws_bytes, ssd_stream_t stream);
+
 /*
  * ssd_logprobs -- what a server answers about emitted tokens, in one pass over
  * their rows: log p(tok), the entropy of p in nats, the token's rank and the

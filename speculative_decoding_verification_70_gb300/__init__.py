@@ -18,6 +18,7 @@ from ._binding import (  # noqa: F401
     SIGNATURES,
     SSDError,
     SpecCache,
+    chunk_attention_workspace_bytes,
     get_device_error,
     load_library,
     new_workspace,
@@ -30,10 +31,13 @@ from ._binding import (  # noqa: F401
     set_chain_batch,
     set_step_schedule,
     softmax_workspace_bytes,
+    ssd_chunk_attention,
     ssd_draft_sample,
     ssd_forked_recovery,
     ssd_kv_append,
     ssd_kv_commit,
+    ssd_kv_evict,
+    ssd_kv_weights,
     ssd_logprobs,
     ssd_sample_residual,
     ssd_softmax_temp,
@@ -50,6 +54,7 @@ from ._binding import (  # noqa: F401
 __all__ = [
     "ssd_softmax_temp", "ssd_verify", "ssd_sample_residual", "ssd_forked_recovery",
     "ssd_verify_fork", "ssd_kv_append", "ssd_tree_attention", "ssd_kv_commit", "ssd_logprobs",
+    "ssd_chunk_attention", "ssd_kv_weights", "ssd_kv_evict",
     "rope_table", "SpecCache", "workspace_bytes", "softmax_workspace_bytes",
     "new_workspace", "get_device_error", "load_library", "selftest_exp2", "SSDError",
 ]

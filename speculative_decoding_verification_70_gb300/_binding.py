@@ -34,6 +34,7 @@ DEVERR_BAD_LENGTH = 0x80
 DEVERR_BAD_PAGE = 0x100
 MAX_TREE_NODES = 64
 MAX_TOP = 32
+MAX_CHUNK = 1 << 20
 _ERRWORD_BYTES = 256
 
 # (name, restype, argtypes)
@@ -91,6 +92,14 @@ SIGNATURES = [
     ("ssd_set_step_schedule", _I, [_I, _I]),
     ("ssd_kv_append", _I, [_P, _P, _I, _P, _L, _L, _L, _P, _P, _L, _L, _L, _P, _P, _I, _I, _I,
                            _P, _P, _F, _P, _Z, _P]),
+    ("ssd_kv_append_at", _I, [_P, _P, _P, _I, _P, _L, _L, _L, _P, _P, _L, _L, _L, _P, _P, _I, _I,
+                              _I, _P, _P, _F, _P, _Z, _P]),
+    ("ssd_chunk_attention_workspace_bytes", _Z, [_I, _I, _I, _I, _I]),
+    ("ssd_chunk_attention", _I, [_P, _P, _I, _P, _L, _L, _L, _I, _I, _F, _P, _P, _P, _Z, _P]),
+    ("ssd_kv_weights", _I, [_P, _P, _I, _P, _L, _L, _L, _P, _I, _I, _F, _F, _P, _L, _L, _I, _P, _Z,
+                            _P]),
+    ("ssd_kv_evict", _I, [_P, _I, _L, _L, _I, _P, _P, _L, _L, _L, _I, _I, _I, _I, _P, _P, _P, _L,
+                          _L, _L, _P, _Z, _P]),
     ("ssd_tree_attention_workspace_bytes", _Z, [_I, _I, _I, _I, _I]),
     ("ssd_tree_attention", _I, [_P, _P, _I, _P, _L, _L, _L, _F, _P, _P, _P, _Z, _P]),
     ("ssd_kv_commit", _I, [_P, _I, _L, _L, _I, _I, _P, _P, _P, _P, _P, _Z, _P]),
@@ -684,14 +693,17 @@ def ssd_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: to
                   parent: Optional[torch.Tensor] = None, n_nodes: Optional[torch.Tensor] = None,
                   cos_sin: Optional[torch.Tensor] = None, interleaved: bool = False,
                   q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None,
-                  eps: float = 1e-6, ws: Optional[torch.Tensor] = None,
-                  out: Optional[dict] = None, stream=None) -> Dict[str, torch.Tensor]:
+                  eps: float = 1e-6, pos: Optional[torch.Tensor] = None,
+                  ws: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                  stream=None) -> Dict[str, torch.Tensor]:
     """Norms and position rotation of the drafted nodes' q [B,N,Hq,D] and
     k [B,N,Hkv,D] (views of a packed projection will do), and k, v stored in
     the nodes' slots of the paged cache [pages,page_size,Hkv,D].  Node j of
     sequence b goes to slot ctx_len[b] + j and has position ctx_len[b] +
-    depth(j); parent [B,N] int32 is the tree of ssd_verify_tree, None a chain;
-    n_nodes [B] the nodes of each sequence.  cos_sin: rope_table(...) or None;
+    depth(j); parent [B,N] int32 is the tree of ssd_verify_tree, None a chain
+    (which may have more than 64 tokens: a prompt's chunk); n_nodes [B] the nodes
+    of each sequence.  pos [B] int32: node 0's position where it is not ctx_len
+    (after an eviction).  cos_sin: rope_table(...) or None;
     q_norm, k_norm: [D] weights or None.  Returns {"q": [B,N,Hq,D], "ws"}."""
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [pages, page_size, Hkv, D]")
@@ -720,9 +732,13 @@ def ssd_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, k_cache: to
     wp, wn = _ws_on(ws, dev)
     out = {} if out is None else out
     qo = _result(out, "q", qsh, dt, dev)
-    _check("ssd_kv_append", load_library().ssd_kv_append(
-        kv, nodes, Hq, qp, qb, qn_, qh, kp, vp, kb, kn_, kh, qo, cp, max_pos, rot, interleaved, qn, kn, eps, wp, wn,
-        _stream_of(stream, dev)))
+    rest = (Hq, qp, qb, qn_, qh, kp, vp, kb, kn_, kh, qo, cp, max_pos, rot, interleaved, qn, kn, eps, wp, wn,
+            _stream_of(stream, dev))
+    if pos is None and N <= MAX_TREE_NODES:
+        _check("ssd_kv_append", load_library().ssd_kv_append(kv, nodes, *rest))
+    else:
+        _check("ssd_kv_append_at", load_library().ssd_kv_append_at(
+            kv, nodes, None if pos is None else _i32(pos, (B,), "pos", dev), *rest))
     out["ws"] = ws
     return out
 
@@ -761,6 +777,135 @@ def ssd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     _check("ssd_tree_attention", lib.ssd_tree_attention(
         kv, nodes, Hq, qp, qb, qn, qh, D ** -0.5 if scale is None else scale,
         res, lse, wp, wn, _stream_of(stream, dev)))
+    o["ws"] = ws
+    return o
+
+
+def chunk_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load_library().ssd_chunk_attention_workspace_bytes(B, N, Hq, Hkv, D))
+
+
+def _chunk_q(q: torch.Tensor, dt: torch.dtype, B: int, D: int, dev: int):
+    """(pointer, shape, three strides) of q; a dimension of one entry gets a stride that is
+    allowed."""
+    p, sh, sb, sn, sh_ = _heads(q, dt, B, D, "q", dev)
+    return p, sh, sb if B > 1 else D, sn if sh[1] > 1 else D, sh_ if sh[2] > 1 else D
+
+
+def ssd_chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        page_table: torch.Tensor, ctx_len: torch.Tensor, *,
+                        n_nodes: Optional[torch.Tensor] = None, window: int = 0, sinks: int = 0,
+                        scale: Optional[float] = None, ws: Optional[torch.Tensor] = None,
+                        out: Optional[dict] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Attention of chunks of new tokens q [B,N,Hq,D] (prompts, parts of them, drafted
+    chains, single tokens; n_nodes [B] the tokens of each sequence, None: N) over the paged
+    cache that holds them in slots ctx_len[b] .. (ssd_kv_append).  The token in slot p sees
+    slots s <= p with s > p - window (0: all) or s < sinks.  scale defaults to D ** -0.5.
+    Returns {"out": [B,N,Hq,D], "lse": [B,N,Hq] float32, "ws"}; tokens that are absent get 0
+    and -inf."""
+    lib = load_library()
+    if k_cache.dim() != 4:
+        raise ValueError("the caches must be [pages, page_size, Hkv, D]")
+    kv, H, D, B, dev = _paged_kv(k_cache, v_cache, page_table)
+    dt = k_cache.dtype
+    qp, qsh, qb, qn, qh = _chunk_q(q, dt, B, D, dev)
+    _, N, Hq, _ = qsh
+    nodes = _draft_nodes(B, N, ctx_len, None, n_nodes, dev)
+    if ws is None:
+        n = lib.ssd_chunk_attention_workspace_bytes(B, N, Hq, H, D)
+        if n == 0:
+            raise SSDError("ssd_chunk_attention_workspace_bytes", 1)
+        ws = new_workspace(n, dev)
+    wp, wn = _ws_on(ws, dev)
+    o = {} if out is None else out
+    res = _result(o, "out", qsh, dt, dev)
+    lse = _result(o, "lse", qsh[:3], torch.float32, dev)
+    _check("ssd_chunk_attention", lib.ssd_chunk_attention(
+        kv, nodes, Hq, qp, qb, qn, qh, window, sinks, D ** -0.5 if scale is None else scale,
+        res, lse, wp, wn, _stream_of(stream, dev)))
+    o["ws"] = ws
+    return o
+
+
+def _weights(w: torch.Tensor, lead, name: str, dev: int):
+    """(pointer, strides, entries of a row) of float32 weights [*lead, S]."""
+    if w.dtype is not torch.float32 or w.dim() != len(lead) + 1 or tuple(w.shape[:-1]) != tuple(lead):
+        raise ValueError("%s must be a float32 CUDA tensor [%s, S]" % (name, ", ".join(map(str, lead))))
+    if w.get_device() != dev:
+        _elsewhere(w, dev, name)
+    S, st = w.shape[-1], w.stride()
+    if S > 1 and st[-1] != 1:
+        raise ValueError("rows of %s must be contiguous" % name)
+    # (torch leaves strides of one entry arbitrary)
+    return (w.data_ptr(), *(S if n == 1 else x for n, x in zip(lead, st)), S)
+
+
+def ssd_kv_weights(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Tensor,
+                   ctx_len: torch.Tensor, lse: torch.Tensor, weights: torch.Tensor, *,
+                   n_nodes: Optional[torch.Tensor] = None, window: int = 0, sinks: int = 0,
+                   scale: Optional[float] = None, decay: float = 1.0,
+                   ws: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """What attention each slot received from the tokens of ssd_chunk_attention (same q,
+    cache, lengths, window, sinks and scale; lse [B,N,Hq] its result), summed over the tokens
+    and the heads of a group: weights [B,Hkv,S] float32, in place, weights * decay + sums for
+    the slots of sequences with new tokens (decay 0: the sums alone).  Returns {"weights",
+    "ws"}."""
+    if k_cache.dim() != 4:
+        raise ValueError("the cache must be [pages, page_size, Hkv, D]")
+    kv, H, D, B, dev = _paged_kv(k_cache, k_cache, page_table)
+    qp, qsh, qb, qn, qh = _chunk_q(q, k_cache.dtype, B, D, dev)
+    _, N, Hq, _ = qsh
+    nodes = _draft_nodes(B, N, ctx_len, None, n_nodes, dev)
+    if lse.dtype is not torch.float32 or lse.shape != qsh[:3]:
+        raise ValueError("lse must be a float32 CUDA tensor of shape %s" % (tuple(qsh[:3]),))
+    w, wb, wh, S = _weights(weights, (B, H), "weights", dev)
+    if ws is None:
+        ws = new_workspace(_ERRWORD_BYTES, dev)
+    wp, wn = _ws_on(ws, dev)
+    _check("ssd_kv_weights", load_library().ssd_kv_weights(
+        kv, nodes, Hq, qp, qb, qn, qh, _on(lse, dev, "lse"), window, sinks, D ** -0.5 if scale is None else scale,
+        decay, w, wb, wh, S, wp, wn, _stream_of(stream, dev)))
+    return {"weights": weights, "ws": ws}
+
+
+def ssd_kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch.Tensor,
+                 ctx_len: torch.Tensor, weights: torch.Tensor, budget: int, *, sinks: int = 0,
+                 recent: int = 0, ws: Optional[torch.Tensor] = None, out: Optional[dict] = None,
+                 stream=None) -> Dict[str, torch.Tensor]:
+    """Sequences longer than `budget` slots cut down to it: every head keeps the first
+    `sinks` slots, the last `recent` and of the rest its heaviest, whose keys and values move
+    to the first slots in order.  The caches are [pages,page_size,Hkv,D] with weights
+    [B,Hkv,S], or [layers,pages,page_size,Hkv,D] with weights [layers,B,Hkv,S] for every
+    layer in one call.  Returns {"ctx_len": [B], "kept": [(layers,)B,Hkv,budget] int32 slots
+    the rows came from (-1 behind the length), "weights": those of the kept slots, then zeros
+    (out={"weights": weights} for in place), "ws"}."""
+    layers, kl, vl, lead = 1, 0, 0, ()
+    if k_cache.dim() == 5:
+        layers, kl, vl = k_cache.shape[0], k_cache.stride(0), v_cache.stride(0)
+        lead = (layers,)
+        if layers < 1:
+            raise ValueError("the caches must have a layer")
+    elif k_cache.dim() != 4:
+        raise ValueError("the caches must be [pages, page_size, Hkv, D], layers in front or not")
+    kv, H, _, B, dev = _paged_kv(k_cache, v_cache, page_table)
+    lead += (B, H)
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    w, *wst, S = _weights(weights, lead, "weights", dev)
+    if ws is None:
+        ws = new_workspace(_ERRWORD_BYTES, dev)
+    wp, wn = _ws_on(ws, dev)
+    o = {} if out is None else out
+    new = _result(o, "ctx_len", (B,), torch.int32, dev)
+    kept = _result(o, "kept", lead + (budget,), torch.int32, dev)
+    if o.get("weights") is None:
+        o["weights"] = torch.empty(lead + (S,), dtype=torch.float32, device=dev)
+    wo, *wost, So = _weights(o["weights"], lead, "out['weights']", dev)
+    if So != S:
+        raise ValueError("out['weights'] must have as many entries a row as weights")
+    _check("ssd_kv_evict", load_library().ssd_kv_evict(
+        kv, layers, kl, vl, B, _i32(ctx_len, (B,), "ctx_len", dev), w, *([0] * (3 - len(wst)) + wst), S, budget, sinks,
+        recent, new, kept, wo, *([0] * (3 - len(wost)) + wost), wp, wn, _stream_of(stream, dev)))
     o["ws"] = ws
     return o
 

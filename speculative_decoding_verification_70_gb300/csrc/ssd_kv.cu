@@ -131,8 +131,8 @@ __global__ void __launch_bounds__(kAppThreads, kAppCtas) kv_append_kernel(const 
     int depth;
     bool there = node_way(p.nodes.parent ? p.nodes.parent + static_cast<long long>(b) * N : nullptr, n, j, mask, depth,
                           broken);
-    const long long pos = static_cast<long long>(ctx) + depth;
-    if (there && p.rot > 0 && pos >= p.max_pos) {
+    const long long pos = static_cast<long long>(p.nodes.pos0 ? p.nodes.pos0[b] : ctx) + depth;
+    if (there && p.rot > 0 && (pos < 0 || pos >= p.max_pos)) {
       there = false;
       bad_len = true;
     }

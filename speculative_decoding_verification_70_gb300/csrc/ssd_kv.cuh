@@ -27,6 +27,7 @@ struct NodesView {
   const int* ctx_len;
   const int* parent;   // null: a chain
   const int* n_nodes;  // null: N
+  const int* pos0;     // node 0's position (append only); null: ctx_len
 };
 
 // The number of nodes of a sequence (0 when its lengths are out of range,
@@ -59,7 +60,7 @@ __host__ __device__ inline bool node_way(const int* parent, int n, int j, uint64
   depth = 0;
   if (j < 0 || j >= n) return false;
   if (!parent) {
-    mask = j == 63 ? ~0ull : (2ull << j) - 1;
+    mask = j >= 63 ? ~0ull : (2ull << j) - 1;
     depth = j;
     return true;
   }
@@ -164,6 +165,51 @@ struct AttnParams {
   int withheld;          // bytes that are waited for beside the copied ones (self-test)
 };
 
+struct ChunkParams {
+  KvView kv;
+  NodesView nodes;  // chains of any length
+  int Hq, G, window, sinks;
+  const char* q;
+  long long q_b, q_n, q_h;
+  float scale;
+  char* out;
+  float* lse;
+  int* err;
+  unsigned wait_us;
+  int withheld;
+};
+
+struct WeightsParams {
+  KvView kv;        // (v is not read)
+  NodesView nodes;
+  int Hq, G, window, sinks;
+  const char* q;
+  long long q_b, q_n, q_h;
+  const float* lse;
+  float scale, decay;
+  float* weights;
+  long long w_b, w_h;
+  int w_len;
+  int* err;
+  unsigned wait_us;
+  int withheld;
+};
+
+struct EvictParams {
+  KvView kv;
+  int layers, B, D;
+  long long k_layer, v_layer;
+  const int* ctx_len;
+  const float* weights;
+  long long w_layer, w_b, w_h;
+  int w_len, budget, sinks, recent;
+  int* new_len;
+  int* kept;
+  float* w_out;
+  long long wo_layer, wo_b, wo_h;
+  int* err;
+};
+
 // A part of a row, as its CTA leaves it.
 struct LogprobPart {
   float m, S, U;
@@ -198,6 +244,10 @@ constexpr int kErrBadTemperature = 0x1, kErrBadLogits = 0x2, kErrBadToken = 0x4,
 cudaError_t launch_kv_append(const AppendParams& p, int dtype, int D, bool vec, cudaStream_t s);
 cudaError_t launch_kv_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStream_t s);
+cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaStream_t s);
+size_t chunk_attention_bytes(int N, int G, int D);
+cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, int D, cudaStream_t s);
+cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s);
 size_t tree_attention_bytes(int N, int G, int D);
 size_t logprobs_bytes(int R, int V, int K);
 cudaError_t launch_logprobs(const LogprobParams& p, int dtype, bool vec, cudaStream_t s);

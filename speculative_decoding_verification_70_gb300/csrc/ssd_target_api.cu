@@ -57,6 +57,15 @@ ssd_status check_nodes(const ssd_draft_nodes* n) {
   return SSD_OK;
 }
 
+// Chains of any length.
+ssd_status check_chains(const ssd_draft_nodes* n) {
+  if (!n || n->parent || n->N < 1 || n->N > SSD_MAX_CHUNK) return SSD_ERR_INVALID_ARG;
+  ssd_draft_nodes first = *n;
+  first.N = 1;
+  if (static_cast<int64_t>(n->B) * n->N > INT32_MAX - 1024) return SSD_ERR_INVALID_ARG;
+  return check_nodes(&first);
+}
+
 KvView view_of(const ssd_paged_kv& kv) {
   KvView v;
   v.k = static_cast<char*>(kv.k);
@@ -72,6 +81,7 @@ NodesView view_of(const ssd_draft_nodes& n) {
   NodesView v;
   v.B = n.B; v.N = n.N;
   v.ctx_len = n.ctx_len; v.parent = n.parent; v.n_nodes = n.n_nodes;
+  v.pos0 = nullptr;
   return v;
 }
 
@@ -85,19 +95,15 @@ bool rows16(const void* p, int64_t a, int64_t b, int64_t c) {
   return aligned(p, 16) && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
 }
 
-}  // namespace
-
-extern "C" {
-
-ssd_status ssd_kv_append(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, int Hq, const void* q,
-                         int64_t q_b, int64_t q_n, int64_t q_h, const void* k, const void* v,
-                         int64_t kv_b, int64_t kv_n, int64_t kv_h, void* q_out, const float* cos_sin,
-                         int max_pos, int rot, int interleaved, const void* q_norm,
-                         const void* k_norm, float eps, void* ws, size_t ws_bytes,
-                         ssd_stream_t stream) {
-  CallRange nvtx_range("ssd_kv_append");
+ssd_status append(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, ssd_status nodes_ok, const int32_t* pos0,
+                  int Hq, const void* q,
+                  int64_t q_b, int64_t q_n, int64_t q_h, const void* k, const void* v,
+                  int64_t kv_b, int64_t kv_n, int64_t kv_h, void* q_out, const float* cos_sin,
+                  int max_pos, int rot, int interleaved, const void* q_norm,
+                  const void* k_norm, float eps, void* ws, size_t ws_bytes,
+                  ssd_stream_t stream) {
   ssd_status st = check_kv(kv);
-  if (st == SSD_OK) st = check_nodes(nodes);
+  if (st == SSD_OK) st = nodes_ok;
   if (st != SSD_OK) return st;
   if (!q || !k || !v || !q_out || !ws || Hq < 1 || Hq > 65536) return SSD_ERR_INVALID_ARG;
   if (q_b < 0 || q_n < 0 || q_h < 0 || kv_b < 0 || kv_n < 0 || kv_h < 0) return SSD_ERR_INVALID_ARG;
@@ -113,6 +119,7 @@ ssd_status ssd_kv_append(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, i
   AppendParams p;
   p.kv = view_of(*kv);
   p.nodes = view_of(*nodes);
+  p.nodes.pos0 = pos0;
   p.Hq = Hq; p.rot = rot; p.max_pos = max_pos; p.interleaved = interleaved != 0;
   p.q = static_cast<const char*>(q);
   p.k = static_cast<const char*>(k);
@@ -130,6 +137,39 @@ ssd_status ssd_kv_append(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, i
   const bool vec = rows16(q, q_b, q_n, q_h) && rows16(k, kv_b, kv_n, kv_h) && aligned(v, 16);
   ProfScope ps("kv_append", S(stream));
   return cuda_status(launch_kv_append(p, kv->dtype, kv->D, vec, S(stream)));
+}
+
+// The range of a [layers, B, Hkv, len] view of weights, in bytes from its base.
+int64_t weights_span(int layers, int B, int H, int64_t l, int64_t b, int64_t h, int len) {
+  return 4 * ((layers - 1) * l + (B - 1) * b + (H - 1) * h + len);
+}
+
+}  // namespace
+
+extern "C" {
+
+ssd_status ssd_kv_append(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, int Hq, const void* q,
+                         int64_t q_b, int64_t q_n, int64_t q_h, const void* k, const void* v,
+                         int64_t kv_b, int64_t kv_n, int64_t kv_h, void* q_out, const float* cos_sin,
+                         int max_pos, int rot, int interleaved, const void* q_norm,
+                         const void* k_norm, float eps, void* ws, size_t ws_bytes,
+                         ssd_stream_t stream) {
+  CallRange nvtx_range("ssd_kv_append");
+  return append(kv, nodes, check_nodes(nodes), nullptr, Hq, q, q_b, q_n, q_h, k, v, kv_b, kv_n, kv_h, q_out, cos_sin,
+                max_pos, rot, interleaved, q_norm, k_norm, eps, ws, ws_bytes, stream);
+}
+
+ssd_status ssd_kv_append_at(const ssd_paged_kv* kv, const ssd_draft_nodes* nodes, const int32_t* pos0, int Hq,
+                            const void* q, int64_t q_b, int64_t q_n, int64_t q_h, const void* k, const void* v,
+                            int64_t kv_b, int64_t kv_n, int64_t kv_h, void* q_out, const float* cos_sin,
+                            int max_pos, int rot, int interleaved, const void* q_norm,
+                            const void* k_norm, float eps, void* ws, size_t ws_bytes,
+                            ssd_stream_t stream) {
+  CallRange nvtx_range("ssd_kv_append_at");
+  if (!aligned(pos0, 4)) return SSD_ERR_INVALID_ARG;
+  const ssd_status st = nodes && !nodes->parent ? check_chains(nodes) : check_nodes(nodes);
+  return append(kv, nodes, st, pos0, Hq, q, q_b, q_n, q_h, k, v, kv_b, kv_n, kv_h, q_out, cos_sin, max_pos, rot,
+                interleaved, q_norm, k_norm, eps, ws, ws_bytes, stream);
 }
 
 size_t ssd_tree_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
@@ -194,6 +234,126 @@ ssd_status ssd_kv_commit(const ssd_paged_kv* kv, int layers, int64_t k_layer, in
   p.err = static_cast<int*>(ws);
   ProfScope ps("kv_commit", S(stream));
   return cuda_status(launch_kv_commit(p, S(stream)));
+}
+
+size_t ssd_chunk_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
+  if (B < 1 || N < 1 || N > SSD_MAX_CHUNK || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 64 ||
+      (D != 64 && D != 128))
+    return 0;
+  return chunk_attention_bytes(N, Hq / Hkv, D);
+}
+
+ssd_status ssd_chunk_attention(const ssd_paged_kv* kv, const ssd_draft_nodes* tokens, int Hq, const void* q,
+                               int64_t q_b, int64_t q_n, int64_t q_h, int window, int sinks, float scale,
+                               void* out, float* lse, void* ws, size_t ws_bytes, ssd_stream_t stream) {
+  CallRange nvtx_range("ssd_chunk_attention");
+  ssd_status st = check_kv(kv);
+  if (st == SSD_OK) st = check_chains(tokens);
+  if (st != SSD_OK) return st;
+  if (!q || !out || !ws || !isfinite(scale) || fabsf(scale) > 2e38f) return SSD_ERR_INVALID_ARG;
+  if (Hq < kv->Hkv || Hq % kv->Hkv != 0 || Hq / kv->Hkv > 64) return SSD_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return SSD_ERR_INVALID_ARG;
+  if (!stride_ok(q_b) || !stride_ok(q_n) || !stride_ok(q_h) || !aligned(q, 16)) return SSD_ERR_INVALID_ARG;
+  if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(ws, 256)) return SSD_ERR_INVALID_ARG;
+  if (ws_bytes < ssd_chunk_attention_workspace_bytes(tokens->B, tokens->N, Hq, kv->Hkv, kv->D))
+    return SSD_ERR_WORKSPACE;
+  ChunkParams p;
+  p.kv = view_of(*kv);
+  p.nodes = view_of(*tokens);
+  p.Hq = Hq; p.G = Hq / kv->Hkv;
+  p.window = window; p.sinks = sinks;
+  p.q = static_cast<const char*>(q);
+  p.q_b = q_b; p.q_n = q_n; p.q_h = q_h;
+  p.scale = scale;
+  p.out = static_cast<char*>(out);
+  p.lse = lse;
+  p.err = static_cast<int*>(ws);
+  p.wait_us = g_wait_us;
+  p.withheld = g_withheld;
+  ProfScope ps("chunk_attention", S(stream));
+  return cuda_status(launch_chunk_attention(p, kv->dtype, kv->D, S(stream)));
+}
+
+ssd_status ssd_kv_weights(const ssd_paged_kv* kv, const ssd_draft_nodes* tokens, int Hq, const void* q, int64_t q_b,
+                          int64_t q_n, int64_t q_h, const float* lse, int window, int sinks, float scale, float decay,
+                          float* weights, int64_t w_b, int64_t w_h, int w_len, void* ws, size_t ws_bytes,
+                          ssd_stream_t stream) {
+  CallRange nvtx_range("ssd_kv_weights");
+  ssd_status st = check_kv(kv);
+  if (st == SSD_OK) st = check_chains(tokens);
+  if (st != SSD_OK) return st;
+  if (!q || !lse || !weights || !ws || !isfinite(scale) || fabsf(scale) > 2e38f || !isfinite(decay))
+    return SSD_ERR_INVALID_ARG;
+  if (Hq < kv->Hkv || Hq % kv->Hkv != 0 || Hq / kv->Hkv > 64) return SSD_ERR_INVALID_ARG;
+  if (window < 0 || sinks < 0) return SSD_ERR_INVALID_ARG;
+  if (!stride_ok(q_b) || !stride_ok(q_n) || !stride_ok(q_h) || !aligned(q, 16)) return SSD_ERR_INVALID_ARG;
+  if (w_len < 1 || w_b < w_len || w_h < w_len || w_b >= kMaxStride || w_h >= kMaxStride) return SSD_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(weights, 4) || !aligned(ws, 256)) return SSD_ERR_INVALID_ARG;
+  if (ws_bytes < SSD_ERRWORD_BYTES) return SSD_ERR_WORKSPACE;
+  WeightsParams p;
+  p.kv = view_of(*kv);
+  p.nodes = view_of(*tokens);
+  p.Hq = Hq; p.G = Hq / kv->Hkv;
+  p.window = window; p.sinks = sinks;
+  p.q = static_cast<const char*>(q);
+  p.q_b = q_b; p.q_n = q_n; p.q_h = q_h;
+  p.lse = lse;
+  p.scale = scale; p.decay = decay;
+  p.weights = weights;
+  p.w_b = w_b; p.w_h = w_h; p.w_len = w_len;
+  p.err = static_cast<int*>(ws);
+  p.wait_us = g_wait_us;
+  p.withheld = g_withheld;
+  ProfScope ps("kv_weights", S(stream));
+  return cuda_status(launch_kv_weights(p, kv->dtype, kv->D, S(stream)));
+}
+
+ssd_status ssd_kv_evict(const ssd_paged_kv* kv, int layers, int64_t k_layer, int64_t v_layer, int B,
+                        const int32_t* ctx_len, const float* weights, int64_t w_layer, int64_t w_b, int64_t w_h,
+                        int w_len, int budget, int sinks, int recent, int32_t* new_len, int32_t* kept, float* w_out,
+                        int64_t wo_layer, int64_t wo_b, int64_t wo_h, void* ws, size_t ws_bytes,
+                        ssd_stream_t stream) {
+  CallRange nvtx_range("ssd_kv_evict");
+  const ssd_status st = check_kv(kv);
+  if (st != SSD_OK) return st;
+  if (!ctx_len || !weights || !new_len || !kept || !ws) return SSD_ERR_INVALID_ARG;
+  if (B < 1 || layers < 1 || w_len < 1) return SSD_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(B) * layers > INT32_MAX / kv->Hkv) return SSD_ERR_INVALID_ARG;
+  if (layers > 1 && (!stride_ok(k_layer) || !stride_ok(v_layer))) return SSD_ERR_INVALID_ARG;
+  if (budget < 1 || sinks < 0 || recent < 0 || budget - sinks < recent) return SSD_ERR_INVALID_ARG;
+  if ((layers > 1 && (w_layer < w_len || w_layer >= kMaxStride)) || w_b < w_len || w_h < w_len || w_b >= kMaxStride ||
+      w_h >= kMaxStride)
+    return SSD_ERR_INVALID_ARG;
+  if (w_out && ((layers > 1 && (wo_layer < w_len || wo_layer >= kMaxStride)) || wo_b < w_len || wo_h < w_len ||
+                wo_b >= kMaxStride || wo_h >= kMaxStride))
+    return SSD_ERR_INVALID_ARG;
+  if (w_out) {
+    // the weights themselves, or elsewhere
+    const bool same = w_out == weights && (layers == 1 || wo_layer == w_layer) && (B == 1 || wo_b == w_b) &&
+                      (kv->Hkv == 1 || wo_h == w_h);
+    const uintptr_t x = reinterpret_cast<uintptr_t>(weights), y = reinterpret_cast<uintptr_t>(w_out);
+    const uintptr_t ex = x + weights_span(layers, B, kv->Hkv, w_layer, w_b, w_h, w_len);
+    const uintptr_t ey = y + weights_span(layers, B, kv->Hkv, wo_layer, wo_b, wo_h, w_len);
+    if (!same && x < ey && y < ex) return SSD_ERR_INVALID_ARG;
+  }
+  if (overlap(new_len, ctx_len, B)) return SSD_ERR_INVALID_ARG;
+  if (!aligned(ctx_len, 4) || !aligned(weights, 4) || !aligned(new_len, 4) || !aligned(kept, 4) ||
+      !aligned(w_out, 4) || !aligned(ws, 256))
+    return SSD_ERR_INVALID_ARG;
+  if (ws_bytes < SSD_ERRWORD_BYTES) return SSD_ERR_WORKSPACE;
+  EvictParams p;
+  p.kv = view_of(*kv);
+  p.layers = layers; p.B = B; p.D = kv->D;
+  p.k_layer = k_layer; p.v_layer = v_layer;
+  p.ctx_len = ctx_len;
+  p.weights = weights;
+  p.w_layer = w_layer; p.w_b = w_b; p.w_h = w_h;
+  p.w_len = w_len; p.budget = budget; p.sinks = sinks; p.recent = recent;
+  p.new_len = new_len; p.kept = kept; p.w_out = w_out;
+  p.wo_layer = wo_layer; p.wo_b = wo_b; p.wo_h = wo_h;
+  p.err = static_cast<int*>(ws);
+  ProfScope ps("kv_evict", S(stream));
+  return cuda_status(launch_kv_evict(p, S(stream)));
 }
 
 size_t ssd_logprobs_workspace_bytes(int R, int V, int K) {
