@@ -3,101 +3,1229 @@
 // Token i of a sequence lies in slot p = ctx + i and sees the slots s <= p with
 // s > p - window (window 0: all of them) or s < sinks:
 //     out = sum_s softmax_s(c q k_s) v_s,   lse = log sum_s exp(c q k_s).
-// A warp per (token, query head), a slot at a time, lanes over the head's entries.
+//
+// For one key/value head the rows are the (token, query head of the group) pairs, G
+// heads a token.  A row tile is 128 / G whole tokens, 128 rows at most, on the tensor
+// cores' M axis; over tiles of 128 slots
+//     S = Q K^T  [rows, slots],   P = 2^(c S - m) masked,   O += P V  [rows, D]
+// with Q, K and V in shared memory and S, P and O in tensor memory: a thread of the
+// softmax owns a row, reads its scores, and writes P over them as the next product's
+// operand, so that nothing of S or P passes shared memory and no row needs another
+// thread.
+//
+// An item is a (sequence, block of tokens, key/value head): two row tiles side by side
+// (chunks of more than one row tile), whose softmax and products alternate, or one
+// (short chunks), whose tiles alternate between two score buffers.  Of the slots it
+// takes the tiles that hold first tokens, then those from the window's begin to the
+// block's last token.  One persistent CTA per SM: the batch's tiles are numbered and
+// cut into equal ranges by the lengths on the device, an item's start and end counted
+// as some tiles; an item that is cut leaves its parts (m, l, O in 32 bits) in the
+// workspace, and chunk_join_kernel joins them in range order (the same bits every call).
+//
+// Warps of a CTA:
+//   0, 2   copy K and V tiles, page by page, by TMA into rings of slots
+//   1      issues the products
+//   3      copies Q, and clears what must not be multiplied in V tiles at the edges of
+//          what is seen: rows that no row of the item sees, and NaN or infinite entries
+//          of slots that only some see (added at the end for the rows that see them)
+//   4..11  two warpgroups for the softmax: one for each row tile, or (one row tile) for
+//          every second item, so that an item's end runs beside the next one's begin
+//
+// m follows the running maximum lazily: only where a row's maximum in units of log 2
+// grew by more than 8 are l and O rescaled.  P at m is 2^-40 in bf16, so that sums of
+// finite values stay finite, and 2^7 in fp16, whose V ends at 65504 and whose P at
+// 2^16.
 #include <math.h>
 
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"
+#include "ssd_tc.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 384;
+constexpr int kRegsCopy = 88, kRegsSoft = 208;  // 128 x 88 + 256 x 208 = 384 x 168
+constexpr int kMaxRing = 6;
+constexpr int kMaxCtas = 160;
+constexpr int kEdgeBars = 8;   // edge tiles whose clearing may lie ahead of their products
+constexpr int kFlagSets = 8;   // items whose flags live side by side
+constexpr float kNoScore = -1e30f;  // m of a row that has seen nothing
+constexpr float kGrow = 8.f;
+template <class T>
+constexpr float kLift = T::kId == Bf16::kId ? -40.f : 7.f;  // log2 of P at m
 
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps) chunk_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int E = D / 64;  // pairs of entries a lane
-  const int lane = threadIdx.x & 31;
-  const long long at = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int N = p.nodes.N, Hq = p.Hq;
-  if (at >= static_cast<long long>(p.nodes.B) * N * Hq) return;
-  const int hq = static_cast<int>(at % Hq), i = static_cast<int>(at / Hq % N), b = static_cast<int>(at / Hq / N);
-  const int h = hq / p.G;
-  const int ctx = p.nodes.ctx_len[b], nn = p.nodes.n_nodes ? p.nodes.n_nodes[b] : N;
-  bool bad;
-  const int n = seq_nodes(ctx, nn, N, p.kv.width, p.kv.ps, bad);
-  if (bad && lane == 0) atomicOr(p.err, kErrBadLength);
-  float o[2 * E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < 2 * E; ++e) o[e] = 0.f;
-  if (i < n) {
-    const int pos = ctx + i;
-    const uint32_t* qr =
-        reinterpret_cast<const uint32_t*>(p.q + 2 * (b * p.q_b + i * p.q_n + hq * p.q_h)) + lane * E;
-    float q[2 * E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[2 * e] = T::lo(qr[e]);
-      q[2 * e + 1] = T::hi(qr[e]);
-    }
-    const int* row = p.kv.table + b * p.kv.table_stride;
-    for (int s = 0; s <= pos; ++s) {
-      if (p.window && s >= p.sinks && s <= pos - p.window) {
-        s = pos - p.window;
-        continue;
-      }
-      int page, off;
-      const bool ok = kv_slot(row, p.kv.width, p.kv.pages, p.kv.ps, s, page, off);
-      if (!ok && lane == 0) atomicOr(p.err, kErrBadPage);
-      float x = 0.f, v[2 * E];
-      const uint32_t* kr = reinterpret_cast<const uint32_t*>(
-                               p.kv.k + 2 * (page * p.kv.k_page + off * p.kv.k_slot + h * p.kv.k_head)) + lane * E;
-      const uint32_t* vr = reinterpret_cast<const uint32_t*>(
-                               p.kv.v + 2 * (page * p.kv.v_page + off * p.kv.v_slot + h * p.kv.v_head)) + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const uint32_t k = ok ? kr[e] : 0u, w = ok ? vr[e] : 0u;
-        x = fmaf(q[2 * e], T::lo(k), x);
-        x = fmaf(q[2 * e + 1], T::hi(k), x);
-        v[2 * e] = T::lo(w);
-        v[2 * e + 1] = T::hi(w);
-      }
-#pragma unroll
-      for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      x = p.scale == 0.f ? 0.f : x * p.scale;
-      const float mn = fmaxf(m, x);
-      if (x == -INFINITY) continue;
-      // (2^-40: sums of values near the largest stay finite)
-      const float f = m == mn ? 1.f : expf(m - mn), w = 0x1p-40f * (x == mn ? 1.f : expf(x - mn));
-      l = l * f + w;
-#pragma unroll
-      for (int e = 0; e < 2 * E; ++e) o[e] = fmaf(w, v[e], o[e] * f);
-      m = mn;
+// A CTA's range of tiles, for the joining kernel.
+struct alignas(16) Range {
+  long long lo;       // first tile (its position in cost)
+  int t0, used;       // its place in its item; 0: a range without tiles
+  int b, blk, h, T;   // its item, the item's tiles
+};
+
+struct Args {
+  NodesView nodes;
+  const int* table;
+  long long table_stride;
+  int width, pages, ps;
+  int Hq, Hkv, G;
+  int tq, tpi;             // tokens of a row tile, of an item
+  int NB;                  // blocks of the longest chunk
+  int window, sinks;
+  int item_cost;           // what an item's start and end cost, in tiles
+  int nk, nv;              // slots of the K and V rings
+  int box, ppt, tk, tpp;   // rows of a TMA box, pages a tile, slots a tile, tiles a page
+  int fold;                // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
+  int group, half;         // bytes from 8 slots of a tile to the next, from half to half
+  int cover;               // rows of a tile that TMA writes
+  float c;                 // scale * log2(e)
+  int zero;                // scale 0: scores count as zeros (and c as 1)
+  char* out;
+  float* lse;
+  const char* vcache;      // for the rows that see a slot with NaN or infinities
+  long long v_page, v_slot, v_head;
+  float* part_o;           // [2 ctas][tpi * G][D]
+  float2* part_ml;         // [2 ctas][tpi * G]
+  Range* ranges;           // [ctas]
+  unsigned long long per_cta;  // 2^64 / ctas, rounded up
+  int* err;
+  unsigned wait_us;
+  int withheld;
+};
+
+struct alignas(16) Misc {
+  uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
+  uint64_t qfull[2], qempty[2], sfull[2][2], pfull[2], pvdone[2], ofree[2], vready[kEdgeBars], done;
+  long long left;
+  int b0, blk0, h0, t0;       // first piece
+  int cost;                   // of an item beside its tiles
+  int pad;                    // some sequence has fewer tokens than N
+  unsigned tmem;
+  int abort;
+  unsigned wait_us;
+  unsigned flags[kFlagSets][16];  // slots with NaN or infinite values that some rows see
+  alignas(16) int off[kTile]; // offset of a tile's row from its first slot; far: no slot
+  unsigned plain[4];          // rows of a tile that are slots (pages of up to 128)
+  long long scan[2][kThreads / 32];
+};
+static_assert(sizeof(Misc) <= 3 * 1024, "shared memory beside rings and Q");
+constexpr int kFar = 1 << 30;
+
+// ---------------------------------------------------------------------------
+// tiles, blocks, pieces
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int tile_of(const Args& a, int slot) {
+  if (a.ps > kTile) return (slot / a.ps) * a.tpp + (slot % a.ps) / kTile;
+  return a.tk == kTile ? slot / kTile : slot / a.tk;
+}
+// First slot of tile t, and how many it holds.
+__device__ __forceinline__ void tile_slots(const Args& a, int t, int& first, int& count) {
+  if (a.ps <= kTile) {
+    first = t * a.tk;
+    count = a.tk;
+  } else {
+    const int r = (t % a.tpp) * kTile;
+    first = (t / a.tpp) * a.ps + r;
+    count = min(kTile, a.ps - r);
+  }
+}
+
+__device__ __forceinline__ int seq_tokens(const Args& a, int b, int& ctx, bool& bad) {
+  ctx = __ldg(a.nodes.ctx_len + b);
+  const int nn = a.nodes.n_nodes ? __ldg(a.nodes.n_nodes + b) : a.nodes.N;
+  return seq_nodes(ctx, nn, a.nodes.N, a.width, a.ps, bad);
+}
+
+// What tokens p0 .. p1 (slots) see together: slots < sk and lo .. p1.
+struct Seen {
+  int p0, p1, lo, sk;
+};
+__device__ __forceinline__ Seen seen_by(const Args& a, int p0, int p1) {
+  Seen s;
+  s.p0 = p0;
+  s.p1 = p1;
+  s.lo = a.window ? max(0, p0 - a.window + 1) : 0;
+  s.sk = min(a.sinks, s.lo);
+  return s;
+}
+// Whether they see some of the slots first .. last, and whether each sees all.
+__device__ __forceinline__ bool some(const Seen& s, int first, int last) {
+  return first <= s.p1 && (last >= s.lo || first < s.sk);
+}
+__device__ __forceinline__ bool all(const Args& a, const Seen& s, int first, int last) {
+  return last <= s.p0 && (a.window == 0 || first > s.p1 - a.window || last < a.sinks);
+}
+
+// The tiles of a block: nsk of first tokens, then those from ft on; T in all.
+struct Block {
+  int T, nsk, ft;
+};
+__device__ __forceinline__ Block block_of(const Args& a, const Seen& s) {
+  Block k;
+  k.ft = s.lo > 0 ? tile_of(a, s.lo) : 0;
+  k.nsk = s.sk > 0 ? min(tile_of(a, s.sk - 1) + 1, k.ft) : 0;
+  k.T = k.nsk + tile_of(a, s.p1) - k.ft + 1;
+  return k;
+}
+__device__ __forceinline__ Seen block_seen(const Args& a, int ctx, int n, int blk) {
+  const int i0 = blk * a.tpi;
+  return seen_by(a, ctx + i0, ctx + min(n, i0 + a.tpi) - 1);
+}
+
+// The pieces of a CTA's range, one item after another.  Only the first may start
+// behind its item's tile 0.
+struct Pieces {
+  long long left;  // cost from t0 to the range's end: a tile 1, an item's end w
+  int w, b, blk, h, ctx, n;
+  Seen s;
+  Block k;
+  int t0, end;     // tiles t0 .. end - 1
+  bool fresh;
+  __device__ __forceinline__ void load(const Args& a) {
+    s = block_seen(a, ctx, n, blk);
+    k = block_of(a, s);
+  }
+  __device__ __forceinline__ void start(const Args& a, const Misc& sm) {
+    left = sm.left;
+    w = sm.cost;
+    b = sm.b0;
+    blk = sm.blk0;
+    h = sm.h0;
+    t0 = sm.t0;
+    fresh = true;
+    if (left > 0) {
+      bool bad;
+      n = seq_tokens(a, b, ctx, bad);
+      load(a);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const long long r = (static_cast<long long>(b) * N + i) * Hq + hq;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + 2 * r * D) + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = T::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
-  if (p.lse && lane == 0) p.lse[r] = l == 0.f ? -INFINITY : m + logf(l * 0x1p40f);
+  __device__ __forceinline__ bool direct() const { return t0 == 0 && end == k.T; }
+  __device__ __forceinline__ int tile(int i) const { return i < k.nsk ? i : k.ft + i - k.nsk; }
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (!fresh) {
+      left -= end - t0 + (end == k.T ? w : 0);
+      t0 = 0;
+      if (left > 0 && ++h == a.Hkv) {
+        h = 0;
+        ++blk;
+        if (blk * static_cast<long long>(a.tpi) >= n) {
+          blk = 0;
+          do {
+            if (++b >= a.nodes.B) {
+              left = 0;
+              return false;
+            }
+            bool bad;
+            n = seq_tokens(a, b, ctx, bad);
+          } while (n == 0);
+        }
+        load(a);
+      }
+    }
+    fresh = false;
+    if (left <= 0) return false;
+    end = static_cast<int>(min(static_cast<long long>(k.T), t0 + left));
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// softmax
+// ---------------------------------------------------------------------------
+// Bits 0 .. x - 1 of a word.
+__device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1; }
+
+// The 32 rows from 32 j on of a tile that a token sees: offsets <= hi and (> lo or < sk).
+__device__ __forceinline__ uint32_t seen_word(const Args& a, const Misc& sm, int j, int hi, int lo, int sk) {
+  if (a.cover == kTile && (a.ps > kTile || a.ps == a.box)) {  // row e is offset e
+    const int e = 32 * j;
+    return below(hi + 1 - e) & (~below(lo + 1 - e) | below(sk - e));
+  }
+  uint32_t m = 0;
+#pragma unroll 4
+  for (int e = 0; e < 32; ++e) {
+    const int o = sm.off[32 * j + e];
+    m |= static_cast<uint32_t>(o <= hi && (o > lo || o < sk)) << e;
+  }
+  return m;
+}
+
+// ln(2^m l), m in units of log 2 with P's lift in it.
+template <class T>
+__device__ __forceinline__ float log_sum(float m, float l) {
+  constexpr float far = kLift<T> < 0.f ? kLift<T> : 0.f, back = kLift<T> < 0.f ? 0x1p40f : 1.f;
+  return (m + far + log2f(l * back)) * 0.6931471805599453f;
 }
 
 template <class T>
-cudaError_t launch_t(const ChunkParams& p, int D, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.nodes.B) * p.nodes.N * p.Hq;
-  const unsigned grid = static_cast<unsigned>((rows + kWarps - 1) / kWarps);
-  if (D == 128) chunk_kernel<T, 128><<<grid, 32 * kWarps, 0, s>>>(p);
-  else chunk_kernel<T, 64><<<grid, 32 * kWarps, 0, s>>>(p);
-  return cudaGetLastError();
+__device__ __forceinline__ bool has_nonfinite(const uint4& x) {
+  // an exponent of all ones carries into the sign's place
+  constexpr uint32_t kExp = T::kId == Bf16::kId ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kOne = T::kId == Bf16::kId ? 0x00800080u : 0x04000400u;
+  return (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) & 0x80008000u;
+}
+template <class T>
+__device__ __forceinline__ uint32_t only_finite(uint32_t x) {
+  constexpr uint32_t kExp = T::kId == Bf16::kId ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kOne = T::kId == Bf16::kId ? 0x00800080u : 0x04000400u;
+  const uint32_t c = ((x & kExp) + kOne) & 0x80008000u;
+  return x & (c & 0x8000u ? 0xffff0000u : ~0u) & (c >> 31 ? 0xffffu : ~0u);
+}
+
+// The slot that bit i of an item's flags stands for.
+__device__ __forceinline__ int flag_slot(const Args& a, const Seen& s, int i) {
+  return i < 256 ? s.p0 + i : s.p0 - a.window + 1 + (i - 256);
+}
+
+// Entries k .. k + 31 of the values that are not finite, for a row that sees them.
+template <class T>
+__device__ __forceinline__ void add_nonfinite(const Args& a, int b, int h, const Seen& s, int pos, const unsigned* fl, int k,
+                                              uint32_t (&o)[32]) {
+#pragma unroll 1
+  for (int q = 0; q < 16; ++q) {
+#pragma unroll 1
+    for (unsigned bits = fl[q]; bits; bits &= bits - 1) {
+      const int slot = flag_slot(a, s, 32 * q + __ffs(bits) - 1);
+      int page, off;
+      if (slot > pos || (a.window && slot <= pos - a.window && slot >= a.sinks)) continue;
+      if (!kv_slot(a.table + b * a.table_stride, a.width, a.pages, a.ps, slot, page, off)) continue;
+      const uint32_t* v =
+          reinterpret_cast<const uint32_t*>(a.vcache + 2 * (page * a.v_page + off * a.v_slot + h * a.v_head + k));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t x = v[e];
+        const float lo = T::lo(x), hi = T::hi(x);
+        if (!(fabsf(lo) < INFINITY)) o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + lo);
+        if (!(fabsf(hi) < INFINITY)) o[2 * e + 1] = __float_as_uint(__uint_as_float(o[2 * e + 1]) + hi);
+      }
+    }
+  }
+}
+
+template <class T, int D, bool WIDE>
+__device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, int w) {
+  const int wt = threadIdx.x & 127;  // row of the row tile = lane of tensor memory
+  const uint32_t lanes = static_cast<uint32_t>(wt & 96) << 16;
+  const int tok = wt / a.G, g = wt - tok * a.G;
+  const bool in_tile = tok < a.tq;
+  const f32x2 c2 = pk2(a.c, a.c);
+  const bool down = a.c < 0.f;
+  const float none = down ? INFINITY : -INFINITY;
+  const float size = fabsf(a.c);
+  const uint32_t tO = tmem + lanes + 256 + w * D;
+  uint32_t ppv = 0;    // phase of pvdone[w]
+  uint32_t sph = 0;    // phases of sfull[w][.]
+  int tiles = 0, item = -1;
+  Pieces pc;
+  pc.start(a, sm);
+#pragma unroll 1
+  while (pc.next(a)) {
+    ++item;
+    if (!WIDE && (item & 1) != w) {
+      tiles += pc.end - pc.t0;
+      continue;
+    }
+    // this row tile's tokens
+    const int i0 = pc.blk * a.tpi + (WIDE ? w * a.tq : 0), i1 = min(pc.n, i0 + a.tq) - 1;
+    if (WIDE && i1 < i0) continue;
+    const Seen mine = seen_by(a, pc.ctx + i0, pc.ctx + i1);
+    const int i = i0 + tok, pos = pc.ctx + i;
+    const bool valid = in_tile && i <= i1;
+    const bool busy = __any_sync(0xffffffffu, valid);
+    float m = kNoScore, l = 0.f;
+    int jobs = 0;
+    bool edges = false;  // tiles that the clearing warp has looked at
+#pragma unroll 1
+    for (int at = pc.t0; at < pc.end; ++at, ++tiles) {
+      int first, count;
+      tile_slots(a, pc.tile(at), first, count);
+      if (WIDE && !some(mine, first, first + count - 1)) continue;
+      edges |= !all(a, pc.s, first, first + count - 1);
+      const int buf = WIDE ? w : tiles & 1;
+      bar_wait(&sm.sfull[w][buf], (sph >> buf) & 1, sm, a.err);
+      sph ^= 1u << buf;
+      bool waited = jobs == 0;  // for the last tile's product
+      auto last_done = [&]() {
+        if (!waited) {
+          bar_wait(&sm.pvdone[w], ppv, sm, a.err);
+          ppv ^= 1;
+          tc_after();
+          waited = true;
+        }
+      };
+      tc_after();
+      if (busy) {
+        const uint32_t tS = tmem + lanes + buf * 128;
+        uint32_t s[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tm_ld32(tS + 32 * j, s[j]);
+        tm_wait_loads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tm_tie32(s[j]);
+        if (a.zero) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) s[j][e] = __float_as_uint(__uint_as_float(s[j][e]) * 0.f);
+        }
+        const bool full = all(a, mine, first, first + count - 1);
+        if (!full || count != kTile) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t v;
+            if (full && a.ps <= kTile) {
+              v = sm.plain[j];
+            } else {
+              v = seen_word(a, sm, j, min(pos - first, count - 1), a.window ? pos - a.window - first : -1, a.sinks - first);
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(v & (1u << e))) s[j][e] = __float_as_uint(none);
+          }
+        }
+        float mx[4];
+        if (!down) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mx[j] = __uint_as_float(s[j][0]);
+#pragma unroll
+            for (int e = 1; e < 31; e += 2) mx[j] = max3(mx[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
+            mx[j] = fmaxf(mx[j], __uint_as_float(s[j][31]));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            mx[j] = -__uint_as_float(s[j][0]);
+#pragma unroll
+            for (int e = 1; e < 32; ++e) mx[j] = fmaxf(mx[j], -__uint_as_float(s[j][e]));
+          }
+        }
+        const float top = size * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - kLift<T>;
+        const bool raise = top > (jobs == 0 ? kNoScore : m + kGrow);
+        const float f = raise ? ex2_fast(m - top) : 1.f;
+        if (raise) {
+          m = top;
+          l *= f;
+        }
+        if (jobs > 0 && __any_sync(0xffffffffu, raise)) {
+          last_done();
+#pragma unroll
+          for (int k = 0; k < D; k += 32) {
+            uint32_t o[32];
+            tm_ld32(tO + k, o);
+            tm_wait_loads();
+            tm_tie32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tm_st32(tO + k, o);
+          }
+        }
+        const f32x2 nm = pk2(-m, -m);
+        f32x2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t x0 = s[j + e / 16][(2 * e) & 31], x1 = s[j + e / 16][(2 * e + 1) & 31];
+            float y0, y1;
+            up2(fma2(pk2(__uint_as_float(x0), __uint_as_float(x1)), c2, nm), y0, y1);
+            y0 = ex2_fast(y0);
+            y1 = ex2_fast(y1);
+            sum[e & 3] = add2(sum[e & 3], pk2(y0, y1));
+            p[e] = T::pack(y0, y1);
+          }
+          tm_st32(tS + 16 * j, p);
+        }
+        float a0, a1;
+        up2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+        l += a0 + a1;
+        tm_wait_stores();
+      }
+      last_done();
+      tc_before();
+      bar_arrive(&sm.pfull[buf]);
+      ++jobs;
+    }
+
+    // ---- end of the piece ----
+    if (jobs > 0) {
+      bar_wait(&sm.pvdone[w], ppv, sm, a.err);
+      ppv ^= 1;
+      tc_after();
+    }
+    // (a warp's rows go out 32 columns at a time)
+    const bool direct = pc.direct(), empty = l == 0.f;
+    const float inv = !direct ? 1.f : empty ? 0.f : 1.f / l;
+    const long long row = direct ? (static_cast<long long>(pc.b) * a.nodes.N + i) * a.Hq + pc.h * a.G + g
+                                 : (2ll * blockIdx.x + (item == 0 ? 0 : 1)) * a.tpi * a.G + (WIDE ? w * a.tq * a.G : 0) + wt;
+    const unsigned* fl = sm.flags[item % kFlagSets];
+    unsigned any = 0;
+    if (busy && jobs > 0) {
+      if (edges) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) any |= fl[q];
+      }
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        uint32_t o[32];
+        tm_ld32(tO + k, o);
+        tm_wait_loads();
+        tm_tie32(o);
+        if (any && valid) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pos, fl, k, o);
+        if (valid && direct) {
+          uint4* out = reinterpret_cast<uint4*>(a.out + 2 * (row * D + k));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[e] = empty ? 0u : T::pack(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
+            out[q] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else if (valid) {
+          uint4* out = reinterpret_cast<uint4*>(a.part_o + row * D + k);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) out[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        }
+      }
+    }
+    if (jobs > 0) {
+      tc_before();
+      bar_arrive(&sm.ofree[w]);
+    }
+    if (valid && direct && a.lse) a.lse[row] = empty ? -INFINITY : log_sum<T>(m, l);
+    if (valid && !direct) a.part_ml[row] = make_float2(m, l);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+// A tile on its way through the products.
+struct Step {
+  bool valid, newq, last, edge;
+  uint32_t act, begin;  // row tiles that see some of it; whose first it is
+  int item, no;         // the item; the tile's number in the CTA
+};
+
+template <class T, int D, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
+                 const __grid_constant__ CUtensorMap mapv, const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) char base[];
+  constexpr int HALVES = D / 64;
+  constexpr int kSlotBytes = HALVES * kHalf;
+  char* ring = base;
+  char* ringv = ring + a.nk * kSlotBytes;
+  char* Q = ringv + a.nv * kSlotBytes;
+  Misc& sm = *reinterpret_cast<Misc*>(Q + 2 * kSlotBytes);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int C = gridDim.x, B = a.nodes.B;
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxRing; ++i) {
+      bar_init(&sm.kfull[i], 1);
+      bar_init(&sm.kempty[i], 1);
+      bar_init(&sm.vfull[i], 1);
+      bar_init(&sm.vempty[i], 2);  // the products and the clearing warp
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&sm.qfull[i], 1);
+      bar_init(&sm.qempty[i], 1);
+      bar_init(&sm.sfull[i][0], 1);
+      bar_init(&sm.sfull[i][1], 1);
+      bar_init(&sm.pfull[i], 128);
+      bar_init(&sm.pvdone[i], 1);
+      bar_init(&sm.ofree[i], 128);
+    }
+    for (int i = 0; i < kEdgeBars; ++i) bar_init(&sm.vready[i], 1);
+    bar_init(&sm.done, 1);
+    sm.abort = 0;
+    sm.wait_us = a.wait_us;
+    sm.left = 0;
+    sm.b0 = sm.blk0 = sm.h0 = sm.t0 = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sptr(&sm.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapq));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapk));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapv));
+  }
+  if (tid < kTile) {
+    int o = tid;
+    if (a.ps <= kTile) {
+      const int p = tid / a.box, r = tid - p * a.box;
+      o = p < a.ppt && r < a.ps ? p * a.ps + r : kFar;
+    }
+    sm.off[tid] = o;
+    const unsigned there = __ballot_sync(0xffffffffu, o != kFar);
+    if (lane == 0) sm.plain[tid >> 5] = there;
+  }
+  // rows of the ring that no copy writes are zeros (they meet P = 0, and must not be NaN)
+  if (a.cover < kTile) {
+    for (int i = tid; i < (a.nk + a.nv) * kSlotBytes / 16; i += kThreads)
+      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+    fence_async();
+  }
+
+  // ---- this CTA's range: the cost of the (sequence, block)s before each thread's (a
+  // block scan), and where the range starts ----
+  {
+    const long long pairs = static_cast<long long>(B) * a.NB, per = (pairs + kThreads - 1) / kThreads;
+    const long long f = tid * per, e = min(pairs, f + per);
+    long long mine = 0;  // tiles of a head
+    long long blocks = 0;
+    bool any_bad = false, any_pad = false;
+    int b = -1, ctx = 0, n = 0, blk = 0;
+    auto load = [&](long long at) {
+      if (b < 0) {
+        b = static_cast<int>(at / a.NB);
+        blk = static_cast<int>(at - static_cast<long long>(b) * a.NB);
+      } else if (++blk == a.NB) {
+        blk = 0;
+        ++b;
+      } else {
+        return;
+      }
+      bool bad;
+      n = seq_tokens(a, b, ctx, bad);
+      any_bad |= bad;
+      any_pad |= n < a.nodes.N;
+    };
+#pragma unroll 1
+    for (long long at = f; at < e; ++at) {
+      load(at);
+      if (blk * static_cast<long long>(a.tpi) >= n) continue;
+      mine += block_of(a, block_seen(a, ctx, n, blk)).T;
+      ++blocks;
+    }
+    if (any_bad && blockIdx.x == 0) atomicOr(a.err, kErrBadLength);
+    long long inc = mine, incb = blocks;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, d), ob = __shfl_up_sync(0xffffffffu, incb, d);
+      if (lane >= d) {
+        inc += o;
+        incb += ob;
+      }
+    }
+    if (lane == 31) {
+      sm.scan[0][warp] = inc;
+      sm.scan[1][warp] = incb;
+    }
+    const bool pad = __syncthreads_or(any_pad);
+    long long before = inc - mine, beforeb = incb - blocks, tiles = 0, nblocks = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) {
+        before += sm.scan[0][i];
+        beforeb += sm.scan[1][i];
+      }
+      tiles += sm.scan[0][i];
+      nblocks += sm.scan[1][i];
+    }
+    tiles *= a.Hkv;
+    nblocks *= a.Hkv;
+    // What an item costs beside its tiles, less where a range is of a few tiles only.
+    long long w = 0;  // min(item_cost, tiles / (4 C))
+#pragma unroll 1
+    for (int k = 1; k <= a.item_cost; ++k) w += tiles >= 4ll * k * C;
+    const long long W = tiles + w * nblocks;
+    // The range's ends in cost: [lo, hi); an item's tiles come first in its T + w.  A
+    // range may hold no tile.
+    const long long me = blockIdx.x, lo = __umul64hi(W * me, a.per_cta),
+                    hi = me + 1 == C ? W : static_cast<long long>(__umul64hi(W * (me + 1), a.per_cta));
+    long long p = (before + w * beforeb) * a.Hkv;
+    const long long mine_cost = (mine + w * blocks) * a.Hkv;
+    if (tid == 0) {
+      a.ranges[me].used = 0;
+      sm.cost = static_cast<int>(w);
+      sm.pad = pad;
+    }
+    __syncthreads();
+    // the thread whose blocks hold the range's first tile (lo may lie behind the tiles
+    // of the last item before them)
+    if (lo < p + mine_cost && hi > p && p - lo <= w) {
+      b = -1;
+#pragma unroll 1
+      for (long long at = f; at < e; ++at) {
+        load(at);
+        if (blk * static_cast<long long>(a.tpi) >= n) continue;
+        const int T = block_of(a, block_seen(a, ctx, n, blk)).T;
+        const long long one = T + w, end = p + one * a.Hkv;
+        if (lo < end) {
+          const unsigned long long d = lo > p ? lo - p : 0;
+          int h = static_cast<int>(d / one);
+          int t0 = static_cast<int>(d - h * one);
+          if (t0 >= T) {  // behind the item's tiles: the next item
+            ++h;
+            t0 = 0;
+          }
+          const long long from = p + h * one + t0;  // cost position of the first tile
+          if (h < a.Hkv) {
+            if (from < hi) {
+              Range r;
+              r.lo = from;
+              r.t0 = sm.t0 = t0;
+              r.used = 1;
+              r.b = sm.b0 = b;
+              r.blk = sm.blk0 = blk;
+              r.h = sm.h0 = h;
+              r.T = T;
+              a.ranges[me] = r;
+              sm.left = hi - from;
+            }
+            break;
+          }
+        }
+        p = end;
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  pdl_trigger();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+    softmax_role<T, D, WIDE>(a, sm, tmem, (warp - 4) >> 2);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
+    if (warp == 0 || warp == 2) {
+      // ---- K (warp 0) or V (warp 2) tiles ----
+      const CUtensorMap* map = warp == 0 ? &mapk : &mapv;
+      Pieces pc;
+      pc.start(a, sm);
+      uint64_t* full = warp == 0 ? sm.kfull : sm.vfull;
+      uint64_t* empty = warp == 0 ? sm.kempty : sm.vempty;
+      const uint32_t ring0 = sptr(warp == 0 ? ring : ringv);
+      const int slots = warp == 0 ? a.nk : a.nv;
+      int slot = -1;
+      uint32_t phase = 0;
+      bool bad_page = false;
+#pragma unroll 1
+      while (pc.next(a)) {
+        const int* trow = a.table + pc.b * a.table_stride;
+        // pages of a tile that hold something seen, and this lane's page id
+        auto lookup = [&](int t, int& p0, int& p1) {
+          int first, count, id = 0;
+          tile_slots(a, t, first, count);
+          p0 = p1 = 0;
+          if (a.ps <= kTile) {
+            const int last = min(first + count - 1, first >= pc.s.lo || first + count > pc.s.lo ? pc.s.p1 : pc.s.sk - 1);
+            p0 = first < pc.s.sk ? 0 : max(0, pc.s.lo - first) / a.ps;
+            p1 = (last - first) / a.ps;
+          }
+          const int p = a.ps <= kTile ? t * a.ppt + lane : t / a.tpp;
+          if (a.ps > kTile || (lane >= p0 && lane <= p1)) {
+            id = __ldg(trow + p);
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.pages)) {
+              bad_page = true;
+              id = a.pages;  // out of bounds: zeros
+            }
+          }
+          return id;
+        };
+        int p0n, p1n, id = lookup(pc.tile(pc.t0), p0n, p1n);
+#pragma unroll 1
+        for (int at = pc.t0; at < pc.end; ++at) {
+          const int t = pc.tile(at), cur = id, p0 = p0n, p1 = p1n;
+          if (at + 1 < pc.end) id = lookup(pc.tile(at + 1), p0n, p1n);
+          const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
+          const int unit = a.fold ? cur * a.fold + s0 / 8 : cur;
+          if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+          }
+          const bool ok = bar_wait(&empty[slot], phase ^ 1, sm, a.err) &&
+                          !*reinterpret_cast<volatile int*>(&sm.abort);
+          if (__all_sync(0xffffffffu, ok)) {
+            if (lane == 0) bar_expect(&full[slot], (p1 - p0 + 1) * a.box * 128 * HALVES + a.withheld);
+            __syncwarp();
+            const uint32_t dst = ring0 + slot * kSlotBytes;
+#pragma unroll 1
+            for (int q0 = p0; q0 <= p1; q0 += 8) {
+              int pg[8];
+#pragma unroll
+              for (int p = 0; p < 8; ++p) pg[p] = __shfl_sync(0xffffffffu, unit, (q0 + p) & 31);
+              if (elect_one()) {
+                if (D == 128 && a.fold) {
+#pragma unroll
+                  for (int p = 0; p < 8; ++p)
+                    if (q0 + p <= p1) tma_groups(dst + (q0 + p) * a.box * 256, map, pg[p], pc.h, &full[slot]);
+                } else {
+#pragma unroll
+                  for (int p = 0; p < 8; ++p) {
+                    if (q0 + p <= p1) {
+#pragma unroll
+                      for (int d = 0; d < HALVES; ++d)
+                        tma_rows(dst + (q0 + p) * a.box * 128 + d * kHalf, map, d * 64, s0, pc.h, pg[p], &full[slot]);
+                    }
+                  }
+                }
+              }
+              __syncwarp();
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (bad_page) atomicOr(a.err, kErrBadPage);
+    } else if (warp == 1) {
+      // ---- products (the warp runs as one; one lane issues) ----
+      const uint32_t khalf = a.half / 16, vstep = a.group / 8;
+      const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
+      const uint64_t vd0 = operand(sptr(ringv), D == 128 ? a.half : 0, a.group);
+      const uint32_t ids = instr<T>(kTile, false, false), ido = instr<T>(D, false, true);
+      Pieces pc;
+      pc.start(a, sm);
+      int item = -1, at = 0, no = -1;
+      uint32_t started = 0;
+      bool inside = false;
+      auto gen = [&](Step& st) {
+        st.newq = false;
+        if (!inside || ++at == pc.end) {
+          if (!pc.next(a)) {
+            st.valid = false;
+            return;
+          }
+          inside = true;
+          ++item;
+          at = pc.t0;
+          started = 0;
+          st.newq = true;
+        }
+        st.valid = true;
+        st.last = at + 1 == pc.end;
+        st.item = item;
+        st.no = ++no;
+        int first, count;
+        tile_slots(a, pc.tile(at), first, count);
+        st.edge = !all(a, pc.s, first, first + count - 1);
+        if (WIDE) {
+          const int mid = pc.s.p0 + a.tq;  // the second row tile's first token
+          st.act = some(seen_by(a, pc.s.p0, min(pc.s.p1, mid - 1)), first, first + count - 1) ? 1u : 0u;
+          if (mid <= pc.s.p1 && some(seen_by(a, mid, pc.s.p1), first, first + count - 1)) st.act |= 2u;
+        } else {
+          st.act = 1;
+        }
+        st.begin = st.act & ~started;
+        started |= st.act;
+      };
+      int kslot = -1, vslot = -1, edges = 0;
+      uint32_t kphase = 0, vphase = 0;
+      uint32_t pph = 0, oph = 0;  // phases of pfull (two row tiles) and ofree
+      // scores of one row tile
+      auto scores = [&](const Step& st, int w, bool opens, bool closes) {
+        const int buf = WIDE ? w : st.no & 1, qb = WIDE ? w : st.item & 1;
+        if (opens) {
+          if (st.newq) bar_wait(&sm.qfull[WIDE ? 0 : qb], (WIDE ? st.item : st.item >> 1) & 1, sm, a.err);
+          if (++kslot == a.nk) {
+            kslot = 0;
+            kphase ^= 1;
+          }
+          bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
+        }
+        tc_after();
+        const uint64_t qd = qd0 + qb * (kSlotBytes / 16), kd = kd0 + kslot * (kSlotBytes / 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            tc_mma(tmem + buf * 128, qd + (k / 4) * (kHalf / 16) + (k & 3) * 2, kd + (k / 4) * khalf + (k & 3) * 2, ids,
+                   k > 0);
+          tc_commit(&sm.sfull[WIDE ? w : st.item & 1][buf]);  // (each warpgroup has its own: it skips items)
+          if (closes) {
+            tc_commit(&sm.kempty[kslot]);
+            if (st.last) tc_commit(&sm.qempty[WIDE ? 0 : qb]);
+          }
+        }
+        __syncwarp();
+      };
+      // values of one row tile
+      auto values = [&](const Step& st, int w, bool opens, bool closes) {
+        const int buf = WIDE ? w : st.no & 1, ob = WIDE ? w : st.item & 1;
+        if (opens) {
+          if (++vslot == a.nv) {
+            vslot = 0;
+            vphase ^= 1;
+          }
+          bar_wait(&sm.vfull[vslot], vphase, sm, a.err);
+          if (st.edge) {
+            bar_wait(&sm.vready[edges % kEdgeBars], (edges / kEdgeBars) & 1, sm, a.err);
+            ++edges;
+          }
+        }
+        bar_wait(&sm.pfull[buf], WIDE ? (pph >> w) & 1 : (st.no >> 1) & 1, sm, a.err);
+        pph ^= 1u << w;
+        const bool begin = (st.begin >> w) & 1;
+        if (begin) {  // the results of the last item in these columns have been read
+          bar_wait(&sm.ofree[ob], ((oph >> ob) & 1) ^ 1, sm, a.err);
+          oph ^= 1u << ob;
+        }
+        tc_after();
+        const uint64_t vd = vd0 + vslot * (kSlotBytes / 16);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            tc_mma_ta(tmem + 256 + ob * D, tmem + buf * 128 + k * 8, vd + k * vstep, ido, !begin || k > 0);
+          tc_commit(&sm.pvdone[ob]);
+          if (closes) tc_commit(&sm.vempty[vslot]);
+        }
+        __syncwarp();
+      };
+      Step cur, nxt;
+      gen(nxt);
+      if (WIDE) {
+        if (nxt.valid) {
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w)
+            if ((nxt.act >> w) & 1) scores(nxt, w, w == 0 || nxt.act == 2, w == 1 || nxt.act == 1);
+        }
+#pragma unroll 1
+        while (nxt.valid) {
+          cur = nxt;
+          gen(nxt);
+#pragma unroll 1
+          for (int w = 0; w < 2; ++w) {
+            if ((cur.act >> w) & 1) values(cur, w, w == 0 || cur.act == 2, w == 1 || cur.act == 1);
+            if (nxt.valid && ((nxt.act >> w) & 1)) scores(nxt, w, w == 0 || nxt.act == 2, w == 1 || nxt.act == 1);
+          }
+        }
+      } else {
+        if (nxt.valid) scores(nxt, 0, true, true);
+#pragma unroll 1
+        while (nxt.valid) {
+          cur = nxt;
+          gen(nxt);
+          if (nxt.valid) scores(nxt, 0, true, true);
+          values(cur, 0, true, true);
+        }
+      }
+      if (elect_one()) tc_commit(&sm.done);
+      __syncwarp();
+      bar_wait(&sm.done, 0, sm, a.err);
+    } else {
+      // ---- Q, and what must not be multiplied ----
+      Pieces pq, pc;
+      pq.start(a, sm);
+      pc.start(a, sm);
+      int nq = 0;
+      // the rows of the next item, once the scores of the one before are made
+      auto fetch = [&]() {
+        if (!pq.next(a)) return;
+        const int qb = WIDE ? 0 : nq & 1;
+        const uint32_t ph = (WIDE ? nq : nq >> 1) & 1;
+        ++nq;
+        const bool ok = bar_wait(&sm.qempty[qb], ph ^ 1, sm, a.err) && !*reinterpret_cast<volatile int*>(&sm.abort);
+        if (__all_sync(0xffffffffu, ok)) {
+          const bool two = WIDE && pq.s.p1 - pq.s.p0 >= a.tq;
+          if (lane == 0) bar_expect(&sm.qfull[qb], (two ? 2 : 1) * HALVES * a.tq * a.G * 128 + a.withheld);
+          __syncwarp();
+          if (elect_one()) {
+            for (int w = 0; w < (two ? 2 : 1); ++w)
+              for (int d = 0; d < HALVES; ++d)
+                tma_rows(sptr(Q) + (qb + w) * kSlotBytes + d * kHalf, &mapq, d * 64, pq.h * a.G, pq.blk * a.tpi + w * a.tq,
+                         pq.b, &sm.qfull[qb]);
+          }
+          __syncwarp();
+        }
+      };
+      fetch();
+      int slot = -1, edges = 0, item = -1;
+      uint32_t phase = 0;
+#pragma unroll 1
+      while (pc.next(a)) {
+        ++item;
+        if (!WIDE) fetch();
+        unsigned* fl = sm.flags[item % kFlagSets];
+        if (lane < 16) fl[lane] = 0;
+        __syncwarp();
+#pragma unroll 1
+        for (int at = pc.t0; at < pc.end; ++at) {
+          int first, count;
+          tile_slots(a, pc.tile(at), first, count);
+          if (++slot == a.nv) {
+            slot = 0;
+            phase ^= 1;
+          }
+          bar_wait(&sm.vfull[slot], phase, sm, a.err);
+          if (!all(a, pc.s, first, first + count - 1)) {
+            char* V = ringv + slot * kSlotBytes;
+#pragma unroll 1
+            for (int r = lane; r < kTile; r += 32) {
+              const int o = sm.off[r], s = first + o;
+              if (a.ps <= kTile ? o == kFar : o >= count) continue;  // zeros
+              if (all(a, pc.s, s, s)) continue;
+              uint4* line = reinterpret_cast<uint4*>(V + (r >> 3) * a.group + (r & 7) * 128);
+              const int half = a.half / 16;
+              if (!some(pc.s, s, s)) {
+#pragma unroll
+                for (int v = 0; v < D / 8; ++v) line[(v / 8) * half + ((v ^ r) & 7)] = make_uint4(0, 0, 0, 0);
+                continue;
+              }
+              bool bad = false;
+#pragma unroll
+              for (int v = 0; v < D / 8; ++v) bad |= has_nonfinite<T>(line[(v / 8) * half + ((v ^ r) & 7)]);
+              if (bad) {
+#pragma unroll 1
+                for (int v = 0; v < D / 8; ++v) {
+                  uint4& x = line[(v / 8) * half + (v & 7)];
+                  x = make_uint4(only_finite<T>(x.x), only_finite<T>(x.y), only_finite<T>(x.z), only_finite<T>(x.w));
+                }
+                const int i = s > pc.s.p0 ? s - pc.s.p0 : 256 + s - (pc.s.p0 - a.window + 1);
+                atomicOr(&fl[i >> 5], 1u << (i & 31));
+              }
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.vready[edges % kEdgeBars]);
+            ++edges;
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.vempty[slot]);
+        }
+        if (WIDE) fetch();
+      }
+    }
+  }
+  // ---- tokens that are not there: zeros ----
+  if (sm.pad) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      int n = a.nodes.N, ctx;
+      bool bad;
+      if (b0 + lane < B) n = seq_tokens(a, b0 + lane, ctx, bad);
+      unsigned some = __ballot_sync(0xffffffffu, n < a.nodes.N);
+#pragma unroll 1
+      for (; some; some &= some - 1) {
+        const int j = __ffs(some) - 1, nb = __shfl_sync(0xffffffffu, n, j);
+        const long long rows = static_cast<long long>(a.nodes.N - nb) * a.Hq;
+        const long long r0 = (static_cast<long long>(b0 + j) * a.nodes.N + nb) * a.Hq;
+        const long long from = rows * blockIdx.x / C, to = rows * (blockIdx.x + 1) / C;
+        uint4* o = reinterpret_cast<uint4*>(a.out + 2 * (r0 + from) * D);
+        for (long long i = tid; i < (to - from) * (D / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+          for (long long i = r0 + from + tid; i < r0 + to; i += kThreads) a.lse[i] = -INFINITY;
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 0 && *reinterpret_cast<volatile int*>(&sm.abort)) {
+    // given up: let copies in flight land before the shared memory is freed
+    const unsigned long long t0 = now_ns();
+    while (now_ns() - t0 < 20000000ull) __nanosleep(100000);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the parts of the items that range borders cut:
+//     M = max m_i,  w_i = 2^(m_i - M),  o = sum w_i O_i / sum w_i l_i
+// in range order.  blockIdx.x: a range that starts inside an item; the first such range
+// of an item does its work, a warp per row.
+// ---------------------------------------------------------------------------
+constexpr int kJoinWarps = 8;
+
+template <class T, int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __grid_constant__ Args a, int C) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int c = blockIdx.x + 1;
+  pdl_wait();
+  const Range me = a.ranges[c];
+  if (!me.used || me.t0 == 0) return;
+  const long long s = me.lo - me.t0, e = s + me.T;
+  // the range before, which holds the item's tile t0 - 1
+  int pk = c - 1;
+  while (pk > 0 && !a.ranges[pk].used) --pk;
+  const long long before = a.ranges[pk].lo;
+  if (before > s) return;  // an earlier range's item
+  bool bad;
+  int ctx;
+  const int n = seq_tokens(a, me.b, ctx, bad);
+  const int i0 = me.blk * a.tpi, rows = (min(n, i0 + a.tpi) - i0) * a.G, cap = a.tpi * a.G;
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  float M = kNoScore, L = 0.f, o[E];
+#pragma unroll
+  for (int q = 0; q < E; ++q) o[q] = 0.f;
+#pragma unroll 1
+  for (int k = pk; k < C; ++k) {
+    if (k > pk) {
+      if (!a.ranges[k].used) continue;
+      if (a.ranges[k].lo >= e) break;
+    }
+    // only the first can be its CTA's last piece
+    const long long at = (2ll * k + (k == pk && before < s ? 1 : 0)) * cap + r;
+    const float2 ml = a.part_ml[at];
+    if (ml.y == 0.f) continue;
+    float v[E];
+#pragma unroll
+    for (int q = 0; q < E; ++q) v[q] = a.part_o[at * D + lane * E + q];
+    const float m = fmaxf(M, ml.x);
+    // (at least the smallest number: an infinite value stays infinite)
+    const float x = ml.x == m ? 1.f : fmaxf(exp2f(ml.x - m), 0x1p-126f), y = M == m ? 1.f : fmaxf(exp2f(M - m), 0x1p-126f);
+    const float yo = L == 0.f ? 0.f : y;
+    L = L * yo + ml.y * x;
+#pragma unroll
+    for (int q = 0; q < E; ++q) o[q] = fmaf(v[q], x, o[q] * yo);
+    M = m;
+  }
+  const int tok = r / a.G, g = r - tok * a.G;
+  const bool empty = L == 0.f;
+  const float inv = empty ? 0.f : 1.f / L;
+  const long long row = (static_cast<long long>(me.b) * a.nodes.N + i0 + tok) * a.Hq + me.h * a.G + g;
+  char* out = a.out + 2 * (row * D + lane * E);
+#pragma unroll
+  for (int q = 0; q < E; q += 2)
+    *reinterpret_cast<uint32_t*>(out + 2 * q) = empty ? 0u : T::pack(o[q] * inv, o[q + 1] * inv);
+  if (a.lse && lane == 0) a.lse[row] = empty ? -INFINITY : log_sum<T>(M, L);
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+// Tokens of an item: one row tile where every chunk fits it, else two.
+int item_tokens(int N, int G) {
+  const int tq = kTile / G;
+  return N <= tq ? tq : 2 * tq;
+}
+
+struct Layout {
+  size_t ranges, ml, o, total;
+};
+Layout layout_of(int N, int G, int D) {
+  const size_t rows = static_cast<size_t>(item_tokens(N, G)) * G;
+  Layout L;
+  L.ranges = 256;
+  L.ml = (L.ranges + sizeof(Range) * kMaxCtas + 255) / 256 * 256;
+  L.o = (L.ml + 8ull * 2 * kMaxCtas * rows + 255) / 256 * 256;
+  L.total = L.o + 4ull * 2 * kMaxCtas * rows * D;
+  return L;
+}
+
+// {D, Hq, N, B}; boxes of 64 columns, G heads and tq tokens.
+bool encode_queries(CUtensorMap* m, const ChunkParams& p, int dtype, int D, int tq) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.Hq),
+                              static_cast<cuuint64_t>(p.nodes.N), static_cast<cuuint64_t>(p.nodes.B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.q_h) * 2, static_cast<cuuint64_t>(p.q_n) * 2,
+                                 static_cast<cuuint64_t>(p.q_b) * 2};
+  const cuuint32_t bx[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tq), 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(m, map_type(dtype), 4, const_cast<char*>(p.q), dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T_, int D, bool WIDE>
+cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C,
+                     size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<T_, D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  if (e != cudaSuccess) return e;
+  chunk_kernel<T_, D, WIDE><<<C, kThreads, smem, s>>>(mq, mk, mv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || C < 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C - 1, (a.tpi * a.G + kJoinWarps - 1) / kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T_, D>, a, C);
 }
 
 }  // namespace
 
-size_t chunk_attention_bytes(int, int, int) { return 256; }
+size_t chunk_attention_bytes(int N, int G, int D) { return layout_of(N, G, D).total; }
 
 cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaStream_t s) {
-  return dtype == Bf16::kId ? launch_t<Bf16>(p, D, s) : launch_t<F16>(p, D, s);
+  Args a;
+  const KvView& kv = p.kv;
+  a.nodes = p.nodes;
+  a.table = kv.table;
+  a.table_stride = kv.table_stride;
+  a.width = kv.width; a.pages = kv.pages; a.ps = kv.ps;
+  a.Hq = p.Hq; a.Hkv = kv.Hkv; a.G = p.G;
+  a.tq = kTile / p.G;
+  a.tpi = item_tokens(p.nodes.N, p.G);
+  const bool wide = a.tpi > a.tq;
+  a.NB = (p.nodes.N + a.tpi - 1) / a.tpi;
+  // (a window that no sequence exceeds is none)
+  a.window = p.window < static_cast<long long>(kv.width) * kv.ps ? p.window : 0;
+  a.sinks = a.window ? p.sinks : 0;
+  a.item_cost = 4;
+  a.zero = p.scale == 0.f;
+  a.c = a.zero ? 1.f : p.scale * 1.4426950408889634f;
+  a.out = p.out; a.lse = p.lse;
+  a.vcache = kv.v; a.v_page = kv.v_page; a.v_slot = kv.v_slot; a.v_head = kv.v_head;
+  a.err = p.err;
+  a.wait_us = p.wait_us; a.withheld = p.withheld;
+  const Layout L = layout_of(p.nodes.N, p.G, D);
+  char* ws = reinterpret_cast<char*>(p.err);
+  a.ranges = reinterpret_cast<Range*>(ws + L.ranges);
+  a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
+  a.part_o = reinterpret_cast<float*>(ws + L.o);
+  // tiles: whole pages up to 128 slots; boxes of a multiple of 8 rows (the swizzle's
+  // period), what exceeds the page filled with zeros
+  if (a.ps <= kTile) {
+    a.box = (a.ps + 7) / 8 * 8;
+    a.ppt = kTile / a.box;
+    a.tk = a.ppt * a.ps;
+    a.tpp = 1;
+    a.cover = a.ppt * a.box;
+  } else {
+    a.box = kTile;
+    a.ppt = 1;
+    a.tk = kTile;
+    a.tpp = (a.ps + kTile - 1) / kTile;
+    a.cover = kTile;
+  }
+  const int slot = D * 2 * kTile;
+  const int slots = static_cast<int>((kSmemMax - 2 * slot - sizeof(Misc)) / slot);
+  a.nk = (slots + 1) / 2 < kMaxRing ? (slots + 1) / 2 : kMaxRing;
+  a.nv = slots - a.nk < kMaxRing ? slots - a.nk : kMaxRing;
+  const size_t smem = static_cast<size_t>(a.nk + a.nv + 2) * slot + sizeof(Misc);
+  CUtensorMap mq, mk, mv;
+  const long long gk = page_groups(a.ps, a.pages, kv.k_slot, kv.k_page);
+  const long long gv = page_groups(a.ps, a.pages, kv.v_slot, kv.v_page);
+  a.fold = D == 128 && gk == gv ? static_cast<int>(gk) : 0;
+  a.group = a.fold ? 2048 : 1024;
+  a.half = a.fold ? 1024 : kHalf;
+  const bool ok =
+      a.fold ? encode_groups(&mk, kv.k, dtype, a.ps, a.Hkv, a.pages, kv.k_slot, kv.k_head, gk, a.box) &&
+                   encode_groups(&mv, kv.v, dtype, a.ps, a.Hkv, a.pages, kv.v_slot, kv.v_head, gv, a.box)
+             : encode_rows(&mk, kv.k, dtype, D, a.ps, a.Hkv, a.pages, kv.k_slot, kv.k_head, kv.k_page, a.box) &&
+                   encode_rows(&mv, kv.v, dtype, D, a.ps, a.Hkv, a.pages, kv.v_slot, kv.v_head, kv.v_page, a.box);
+  if (!ok || !encode_queries(&mq, p, dtype, D, a.tq)) return cudaErrorInvalidValue;
+  int C = sm_count();
+  if (C < 1) return cudaErrorInvalidDevice;
+  C = C < kMaxCtas ? C : kMaxCtas;
+  a.per_cta = C > 1 ? ~0ull / C + 1 : 0;
+  const auto launch =
+      dtype == Bf16::kId
+          ? (D == 128 ? (wide ? launch_t<Bf16, 128, true> : launch_t<Bf16, 128, false>)
+                      : (wide ? launch_t<Bf16, 64, true> : launch_t<Bf16, 64, false>))
+          : (D == 128 ? (wide ? launch_t<F16, 128, true> : launch_t<F16, 128, false>)
+                      : (wide ? launch_t<F16, 64, true> : launch_t<F16, 64, false>));
+  return launch(mq, mk, mv, a, C, smem, s);
 }
 
 }  // namespace ssd

@@ -77,6 +77,8 @@ def attention(c, window=0, sinks=0, scale=None):
             # product with v, the result once more
             size = torch.einsum("ngd,sd->ngs", qh.abs(), K[:, h].abs().nan_to_num(0, 0, 0))
             d = (D + 4) * 2.0 ** -24 * torch.where(see[:, None, :], size, 0 * size).amax(2) * abs(scale)
+            # (finite entries of slots that hold others count like all)
+            fine = torch.where(torch.isfinite(V[:, h]), V[:, h], torch.zeros_like(V[:, h]))
             w = torch.einsum("ngs,sd->ngd", p.nan_to_num(0), fine.abs())
             far = torch.where(see[:, None, :], x, 0 * x).abs().nan_to_num(0, 0, 0).amax(2)
             d = d + far * 2.0 ** -23  # the scaled score, and its distance from the reference
