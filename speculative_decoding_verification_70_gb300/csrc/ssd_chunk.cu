@@ -77,8 +77,9 @@ struct Args {
   int fold;                // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
   int group, half;         // bytes from 8 slots of a tile to the next, from half to half
   int cover;               // rows of a tile that TMA writes
-  float c;                 // scale * log2(e)
-  int zero;                // scale 0: scores count as zeros (and c as 1)
+  float c;                 // |scale| * log2(e)
+  int negate;              // scale < 0: the scores' products are negated
+  int zero;                // scale 0: Q counts as zeros (and c as 1)
   char* out;
   float* lse;
   const char* vcache;      // for the rows that see a slot with NaN or infinities
@@ -308,9 +309,6 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
   const int tok = wt / a.G, g = wt - tok * a.G;
   const bool in_tile = tok < a.tq;
   const f32x2 c2 = pk2(a.c, a.c);
-  const bool down = a.c < 0.f;
-  const float none = down ? INFINITY : -INFINITY;
-  const float size = fabsf(a.c);
   const uint32_t tO = tmem + lanes + 256 + w * D;
   uint32_t ppv = 0;    // phase of pvdone[w]
   uint32_t sph = 0;    // phases of sfull[w][.]
@@ -361,12 +359,6 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         tm_wait_loads();
 #pragma unroll
         for (int j = 0; j < 4; ++j) tm_tie32(s[j]);
-        if (a.zero) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[j][e] = __float_as_uint(__uint_as_float(s[j][e]) * 0.f);
-        }
         const bool full = all(a, mine, first, first + count - 1);
         if (!full || count != kTile) {
 #pragma unroll
@@ -379,27 +371,20 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
             }
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(v & (1u << e))) s[j][e] = __float_as_uint(none);
+              if (!(v & (1u << e))) s[j][e] = 0xff800000u;  // -inf
           }
         }
         float mx[4];
-        if (!down) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mx[j] = __uint_as_float(s[j][0]);
+        for (int j = 0; j < 4; ++j) mx[j] = max3(__uint_as_float(s[j][0]), __uint_as_float(s[j][1]), __uint_as_float(s[j][2]));
 #pragma unroll
-            for (int e = 1; e < 31; e += 2) mx[j] = max3(mx[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
-            mx[j] = fmaxf(mx[j], __uint_as_float(s[j][31]));
-          }
-        } else {
+        for (int e = 3; e < 31; e += 2) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            mx[j] = -__uint_as_float(s[j][0]);
-#pragma unroll
-            for (int e = 1; e < 32; ++e) mx[j] = fmaxf(mx[j], -__uint_as_float(s[j][e]));
-          }
+          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
         }
-        const float top = size * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - kLift<T>;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[j][31]));
+        const float top = a.c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - kLift<T>;
         const bool raise = top > (jobs == 0 ? kNoScore : m + kGrow);
         const float f = raise ? ex2_fast(m - top) : 1.f;
         if (raise) {
@@ -408,7 +393,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         }
         if (jobs > 0 && __any_sync(0xffffffffu, raise)) {
           last_done();
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < D; k += 32) {
             uint32_t o[32];
             tm_ld32(tO + k, o);
@@ -422,19 +407,19 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         const f32x2 nm = pk2(-m, -m);
         f32x2 sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          uint32_t p[32];
+        for (int j = 0; j < 4; ++j) {
+          uint32_t p[16];
+          if (j > 0) tm_tie32(s[j]);  // (one quarter at a time: all four want 255 registers)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t x0 = s[j + e / 16][(2 * e) & 31], x1 = s[j + e / 16][(2 * e + 1) & 31];
+          for (int e = 0; e < 16; ++e) {
             float y0, y1;
-            up2(fma2(pk2(__uint_as_float(x0), __uint_as_float(x1)), c2, nm), y0, y1);
+            up2(fma2(pk2(__uint_as_float(s[j][2 * e]), __uint_as_float(s[j][2 * e + 1])), c2, nm), y0, y1);
             y0 = ex2_fast(y0);
             y1 = ex2_fast(y1);
             sum[e & 3] = add2(sum[e & 3], pk2(y0, y1));
             p[e] = T::pack(y0, y1);
           }
-          tm_st32(tS + 16 * j, p);
+          tm_put16(tS + 16 * j, p);
         }
         float a0, a1;
         up2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
@@ -784,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t khalf = a.half / 16, vstep = a.group / 8;
       const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
       const uint64_t vd0 = operand(sptr(ringv), D == 128 ? a.half : 0, a.group);
-      const uint32_t ids = instr<T>(kTile, false, false), ido = instr<T>(D, false, true);
+      const uint32_t ids = instr<T>(kTile, false, false, a.negate), ido = instr<T>(D, false, true);
       Pieces pc;
       pc.start(a, sm);
       int item = -1, at = 0, no = -1;
@@ -932,8 +917,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (elect_one()) {
             for (int w = 0; w < (two ? 2 : 1); ++w)
               for (int d = 0; d < HALVES; ++d)
-                tma_rows(sptr(Q) + (qb + w) * kSlotBytes + d * kHalf, &mapq, d * 64, pq.h * a.G, pq.blk * a.tpi + w * a.tq,
-                         pq.b, &sm.qfull[qb]);
+                tma_rows(sptr(Q) + (qb + w) * kSlotBytes + d * kHalf, &mapq, d * 64, pq.h * a.G,
+                         a.zero ? a.nodes.N : pq.blk * a.tpi + w * a.tq, pq.b, &sm.qfull[qb]);  // (behind the last: zeros)
           }
           __syncwarp();
         }
@@ -1173,7 +1158,8 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
   a.sinks = a.window ? p.sinks : 0;
   a.item_cost = 4;
   a.zero = p.scale == 0.f;
-  a.c = a.zero ? 1.f : p.scale * 1.4426950408889634f;
+  a.c = a.zero ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
+  a.negate = p.scale < 0.f;
   a.out = p.out; a.lse = p.lse;
   a.vcache = kv.v; a.v_page = kv.v_page; a.v_slot = kv.v_slot; a.v_head = kv.v_head;
   a.err = p.err;

@@ -122,9 +122,9 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32
 }
 // Instruction descriptor: 32-bit accumulator, 128 x n, 16-bit operands.
 template <class T>
-__device__ __forceinline__ uint32_t instr(int n, bool a_mn, bool b_mn) {
+__device__ __forceinline__ uint32_t instr(int n, bool a_mn, bool b_mn, bool negate_a = false) {
   const uint32_t f = T::kId == Bf16::kId ? 1u : 0u;
-  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(a_mn) << 15) |
+  return (1u << 4) | (f << 7) | (f << 10) | (static_cast<uint32_t>(negate_a) << 13) | (static_cast<uint32_t>(a_mn) << 15) |
          (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 
@@ -149,6 +149,14 @@ __device__ __forceinline__ void tm_st32(uint32_t addr, const uint32_t (&r)[32]) 
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]));
+}
+// The same with 16 columns (named apart: the tree attention has fragments of its own).
+__device__ __forceinline__ void tm_put16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]));
 }
 __device__ __forceinline__ void tm_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Waits for this thread's tcgen05.ld; tm_tie32 behind it keeps the uses of their
