@@ -77,6 +77,8 @@ struct Args {
   int fold;                // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
   int group, half;         // bytes from 8 slots of a tile to the next, from half to half
   int cover;               // rows of a tile that TMA writes
+  int holes;               // tiles have rows that are no slot, the same in each
+  int uneven;              // tiles that differ: pages above 128 slots whose last tile is not full
   float c;                 // |scale| * log2(e)
   int negate;              // scale < 0: the scores' products are negated
   int zero;                // scale 0: Q counts as zeros (and c as 1)
@@ -156,15 +158,20 @@ __device__ __forceinline__ bool all(const Args& a, const Seen& s, int first, int
   return last <= s.p0 && (a.window == 0 || first > s.p1 - a.window || last < a.sinks);
 }
 
-// The tiles of a block: nsk of first tokens, then those from ft on; T in all.
+// The tiles of a block: nsk of first tokens, then those from ft on; T in all.  Each of
+// its tokens sees every slot of tiles f0 .. f1 - 1; the others are its edges.
 struct Block {
-  int T, nsk, ft;
+  int T, nsk, ft, f0, f1;
+  __device__ __forceinline__ bool edge(int t) const { return t < f0 || t >= f1; }
 };
 __device__ __forceinline__ Block block_of(const Args& a, const Seen& s) {
   Block k;
   k.ft = s.lo > 0 ? tile_of(a, s.lo) : 0;
   k.nsk = s.sk > 0 ? min(tile_of(a, s.sk - 1) + 1, k.ft) : 0;
   k.T = k.nsk + tile_of(a, s.p1) - k.ft + 1;
+  const int low = a.window ? max(0, s.p1 - a.window + 1) : 0;
+  k.f0 = low > 0 ? tile_of(a, low - 1) + 1 : 0;
+  k.f1 = a.uneven ? 0 : tile_of(a, s.p0 + 1);
   return k;
 }
 __device__ __forceinline__ Seen block_seen(const Args& a, int ctx, int n, int blk) {
@@ -302,6 +309,33 @@ __device__ __forceinline__ void add_nonfinite(const Args& a, int b, int h, const
   }
 }
 
+__device__ __forceinline__ float row_max(const uint32_t (&s)[4][32]) {
+  float m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = max3(__uint_as_float(s[j][0]), __uint_as_float(s[j][1]), __uint_as_float(s[j][2]));
+#pragma unroll
+  for (int e = 3; e < 31; e += 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = max3(m[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
+  }
+  return fmaxf(max3(m[0], m[1], m[2]), max3(m[3], __uint_as_float(s[0][31]), max3(__uint_as_float(s[1][31]), __uint_as_float(s[2][31]), __uint_as_float(s[3][31]))));
+}
+
+// A row of D columns of tensor memory times f.
+template <int D>
+__device__ __forceinline__ void scale_columns(uint32_t at, float f) {
+#pragma unroll 1
+  for (int k = 0; k < D; k += 32) {
+    uint32_t o[32];
+    tm_ld32(at + k, o);
+    tm_wait_loads();
+    tm_tie32(o);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+    tm_st32(at + k, o);
+  }
+}
+
 template <class T, int D, bool WIDE>
 __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, int w) {
   const int wt = threadIdx.x & 127;  // row of the row tile = lane of tensor memory
@@ -334,10 +368,14 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
     bool edges = false;  // tiles that the clearing warp has looked at
 #pragma unroll 1
     for (int at = pc.t0; at < pc.end; ++at, ++tiles) {
-      int first, count;
-      tile_slots(a, pc.tile(at), first, count);
-      if (WIDE && !some(mine, first, first + count - 1)) continue;
-      edges |= !all(a, pc.s, first, first + count - 1);
+      const int t = pc.tile(at);
+      const bool edge = pc.k.edge(t);
+      int first = 0, count = kTile;
+      if (edge) {
+        tile_slots(a, t, first, count);
+        if (WIDE && !some(mine, first, first + count - 1)) continue;
+        edges = true;
+      }
       const int buf = WIDE ? w : tiles & 1;
       bar_wait(&sm.sfull[w][buf], (sph >> buf) & 1, sm, a.err);
       sph ^= 1u << buf;
@@ -356,73 +394,60 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         uint32_t s[4][32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) tm_ld32(tS + 32 * j, s[j]);
+        if (WIDE) last_done();  // (made before these scores)
         tm_wait_loads();
 #pragma unroll
         for (int j = 0; j < 4; ++j) tm_tie32(s[j]);
-        const bool full = all(a, mine, first, first + count - 1);
-        if (!full || count != kTile) {
+        if (edge || a.holes) {
+          const int hi = min(pos - first, count - 1), lo = a.window ? pos - a.window - first : -1, sk = a.sinks - first;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            uint32_t v;
-            if (full && a.ps <= kTile) {
-              v = sm.plain[j];
-            } else {
-              v = seen_word(a, sm, j, min(pos - first, count - 1), a.window ? pos - a.window - first : -1, a.sinks - first);
-            }
+            const uint32_t v = edge ? seen_word(a, sm, j, hi, lo, sk) : sm.plain[j];
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (!(v & (1u << e))) s[j][e] = 0xff800000u;  // -inf
           }
         }
-        float mx[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = max3(__uint_as_float(s[j][0]), __uint_as_float(s[j][1]), __uint_as_float(s[j][2]));
-#pragma unroll
-        for (int e = 3; e < 31; e += 2) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j] = fmaxf(mx[j], __uint_as_float(s[j][31]));
-        const float top = a.c * fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) - kLift<T>;
-        const bool raise = top > (jobs == 0 ? kNoScore : m + kGrow);
-        const float f = raise ? ex2_fast(m - top) : 1.f;
-        if (raise) {
-          m = top;
+        const float top = a.c * row_max(s) - kLift<T>;
+        const bool raise = top > (m == kNoScore ? m : m + kGrow);
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? ex2_fast(m - top) : 1.f;
+          if (raise) m = top;
           l *= f;
-        }
-        if (jobs > 0 && __any_sync(0xffffffffu, raise)) {
-          last_done();
-#pragma unroll 1
-          for (int k = 0; k < D; k += 32) {
-            uint32_t o[32];
-            tm_ld32(tO + k, o);
-            tm_wait_loads();
-            tm_tie32(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tm_st32(tO + k, o);
+          if (jobs > 0) {
+            last_done();
+            scale_columns<D>(tO, f);
           }
         }
+        // P a quarter at a time (all four at once want 255 registers), the sums and
+        // stores of one beside the exponentials of the next
         const f32x2 nm = pk2(-m, -m);
-        f32x2 sum[4] = {0ull, 0ull, 0ull, 0ull};
+        f32x2 sum[2] = {0ull, 0ull};
+        auto exps = [&](uint32_t (&x)[32]) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float y0, y1;
+            up2(fma2(pk2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, nm), y0, y1);
+            x[e] = __float_as_uint(ex2_fast(y0));
+            x[e + 1] = __float_as_uint(ex2_fast(y1));
+          }
+        };
+        exps(s[0]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          if (j < 3) exps(s[j < 3 ? j + 1 : 3]);
           uint32_t p[16];
-          if (j > 0) tm_tie32(s[j]);  // (one quarter at a time: all four want 255 registers)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float y0, y1;
-            up2(fma2(pk2(__uint_as_float(s[j][2 * e]), __uint_as_float(s[j][2 * e + 1])), c2, nm), y0, y1);
-            y0 = ex2_fast(y0);
-            y1 = ex2_fast(y1);
-            sum[e & 3] = add2(sum[e & 3], pk2(y0, y1));
+            const float y0 = __uint_as_float(s[j][2 * e]), y1 = __uint_as_float(s[j][2 * e + 1]);
+            sum[e & 1] = add2(sum[e & 1], pk2(y0, y1));
             p[e] = T::pack(y0, y1);
           }
           tm_put16(tS + 16 * j, p);
+          if (j < 2) tm_tie32(s[j < 2 ? j + 2 : 3]);
         }
         float a0, a1;
-        up2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a0, a1);
+        up2(add2(sum[0], sum[1]), a0, a1);
         l += a0 + a1;
         tm_wait_stores();
       }
@@ -642,13 +667,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long at = f; at < e; ++at) {
         load(at);
         if (blk * static_cast<long long>(a.tpi) >= n) continue;
-        const int T = block_of(a, block_seen(a, ctx, n, blk)).T;
-        const long long one = T + w, end = p + one * a.Hkv;
+        const int all_t = block_of(a, block_seen(a, ctx, n, blk)).T;
+        const long long one = all_t + w, end = p + one * a.Hkv;
         if (lo < end) {
           const unsigned long long d = lo > p ? lo - p : 0;
           int h = static_cast<int>(d / one);
           int t0 = static_cast<int>(d - h * one);
-          if (t0 >= T) {  // behind the item's tiles: the next item
+          if (t0 >= all_t) {  // behind the item's tiles: the next item
             ++h;
             t0 = 0;
           }
@@ -662,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               r.b = sm.b0 = b;
               r.blk = sm.blk0 = blk;
               r.h = sm.h0 = h;
-              r.T = T;
+              r.T = all_t;
               a.ranges[me] = r;
               sm.left = hi - from;
             }
@@ -792,15 +817,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         st.last = at + 1 == pc.end;
         st.item = item;
         st.no = ++no;
-        int first, count;
-        tile_slots(a, pc.tile(at), first, count);
-        st.edge = !all(a, pc.s, first, first + count - 1);
-        if (WIDE) {
+        const int t = pc.tile(at);
+        st.edge = pc.k.edge(t);
+        st.act = 1;
+        if (WIDE && !st.edge) {
+          st.act = pc.s.p1 - pc.s.p0 >= a.tq ? 3 : 1;
+        } else if (WIDE) {
+          int first, count;
+          tile_slots(a, t, first, count);
           const int mid = pc.s.p0 + a.tq;  // the second row tile's first token
           st.act = some(seen_by(a, pc.s.p0, min(pc.s.p1, mid - 1)), first, first + count - 1) ? 1u : 0u;
           if (mid <= pc.s.p1 && some(seen_by(a, mid, pc.s.p1), first, first + count - 1)) st.act |= 2u;
-        } else {
-          st.act = 1;
         }
         st.begin = st.act & ~started;
         started |= st.act;
@@ -935,14 +962,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
 #pragma unroll 1
         for (int at = pc.t0; at < pc.end; ++at) {
-          int first, count;
-          tile_slots(a, pc.tile(at), first, count);
+          const int t = pc.tile(at);
           if (++slot == a.nv) {
             slot = 0;
             phase ^= 1;
           }
           bar_wait(&sm.vfull[slot], phase, sm, a.err);
-          if (!all(a, pc.s, first, first + count - 1)) {
+          if (pc.k.edge(t)) {
+            int first, count;
+            tile_slots(a, t, first, count);
             char* V = ringv + slot * kSlotBytes;
 #pragma unroll 1
             for (int r = lane; r < kTile; r += 32) {
@@ -1177,12 +1205,16 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
     a.tk = a.ppt * a.ps;
     a.tpp = 1;
     a.cover = a.ppt * a.box;
+    a.holes = a.tk != kTile;
+    a.uneven = 0;
   } else {
     a.box = kTile;
     a.ppt = 1;
     a.tk = kTile;
     a.tpp = (a.ps + kTile - 1) / kTile;
     a.cover = kTile;
+    a.holes = 0;
+    a.uneven = a.ps % kTile != 0;
   }
   const int slot = D * 2 * kTile;
   const int slots = static_cast<int>((kSmemMax - 2 * slot - sizeof(Misc)) / slot);
