@@ -23,8 +23,9 @@
 // workspace, and chunk_join_kernel joins them in range order (the same bits every call).
 //
 // Warps of a CTA:
-//   0, 2   copy K and V tiles, page by page, by TMA into rings of slots
-//   1      issues the products
+//   0      copies K and V tiles, page by page, by TMA into rings of slots (one row tile: K,
+//          and warp 2 V)
+//   1, 2   issue the products, of a row tile each (one row tile: warp 1)
 //   3      copies Q, and clears what must not be multiplied in V tiles at the edges of
 //          what is seen: rows that no row of the item sees, and NaN or infinite entries
 //          of slots that only some see (added at the end for the rows that see them)
@@ -97,7 +98,7 @@ struct Args {
 
 struct alignas(16) Misc {
   uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
-  uint64_t qfull[2], qempty[2], sfull[2][2], pfull[2], pvdone[2], ofree[2], vready[kEdgeBars], done;
+  uint64_t qfull[2], qempty[2], sfull[2][2], pfull[2][2], pvdone[2], ofree[2], vready[kEdgeBars], done;
   long long left;
   int b0, blk0, h0, t0;       // first piece
   int cost;                   // of an item beside its tiles
@@ -379,7 +380,9 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
       const int buf = WIDE ? w : tiles & 1;
       bar_wait(&sm.sfull[w][buf], (sph >> buf) & 1, sm, a.err);
       sph ^= 1u << buf;
-      bool waited = jobs == 0;  // for the last tile's product
+      // The last tile's product: with two row tiles it was issued before these scores, and
+      // so has been made.
+      bool waited = WIDE || jobs == 0;
       auto last_done = [&]() {
         if (!waited) {
           bar_wait(&sm.pvdone[w], ppv, sm, a.err);
@@ -394,7 +397,6 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         uint32_t s[4][32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) tm_ld32(tS + 32 * j, s[j]);
-        if (WIDE) last_done();  // (made before these scores)
         tm_wait_loads();
 #pragma unroll
         for (int j = 0; j < 4; ++j) tm_tie32(s[j]);
@@ -444,16 +446,24 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
             p[e] = T::pack(y0, y1);
           }
           tm_put16(tS + 16 * j, p);
+          if (j == 1) {
+            tm_wait_stores();
+            tc_before();
+            bar_arrive(&sm.pfull[buf][0]);
+          }
           if (j < 2) tm_tie32(s[j < 2 ? j + 2 : 3]);
         }
         float a0, a1;
         up2(add2(sum[0], sum[1]), a0, a1);
         l += a0 + a1;
         tm_wait_stores();
+      } else {
+        tc_before();
+        bar_arrive(&sm.pfull[buf][0]);
       }
       last_done();
       tc_before();
-      bar_arrive(&sm.pfull[buf]);
+      bar_arrive(&sm.pfull[buf][1]);
       ++jobs;
     }
 
@@ -511,13 +521,257 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-// A tile on its way through the products.
-struct Step {
-  bool valid, newq, last, edge;
-  uint32_t act, begin;  // row tiles that see some of it; whose first it is
-  int item, no;         // the item; the tile's number in the CTA
+// ---------------------------------------------------------------------------
+// copies of K and V
+// ---------------------------------------------------------------------------
+// A ring's next tile: whole pages, of which the seen ones come.
+struct Ring {
+  const CUtensorMap* map;
+  uint64_t *full, *empty;
+  uint32_t base;
+  int slots, slot;
+  uint32_t phase;
 };
+template <int D>
+__device__ __forceinline__ bool load_tile(const Args& a, Misc& sm, Ring& r, int t, int p0, int p1, int id, int h) {
+  constexpr int HALVES = D / 64, kSlotBytes = HALVES * kHalf;
+  const int lane = threadIdx.x & 31;
+  const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
+  const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.pages);
+  if (!good) id = a.pages;  // out of bounds: zeros
+  const int unit = a.fold ? id * a.fold + s0 / 8 : id;
+  if (++r.slot == r.slots) {
+    r.slot = 0;
+    r.phase ^= 1;
+  }
+  uint64_t* full = r.full + r.slot;
+  const bool ok = bar_wait(r.empty + r.slot, r.phase ^ 1, sm, a.err) && !*reinterpret_cast<volatile int*>(&sm.abort);
+  if (!__all_sync(0xffffffffu, ok)) return true;
+  if (lane == 0) bar_expect(full, (p1 - p0 + 1) * a.box * 128 * HALVES + a.withheld);
+  __syncwarp();
+  const uint32_t dst = r.base + r.slot * kSlotBytes;
+  // a lane a page
+  if (lane >= p0 && lane <= p1) {
+    if (D == 128 && a.fold) {
+      tma_groups(dst + lane * a.box * 256, r.map, unit, h, full);
+    } else {
+#pragma unroll
+      for (int d = 0; d < HALVES; ++d)
+        tma_rows(dst + lane * a.box * 128 + d * kHalf, r.map, d * 64, s0, h, unit, full);
+    }
+  }
+  __syncwarp();
+  return good || lane < p0 || lane > p1;
+}
 
+// K, V or both: K a tile ahead, as the products take them.
+template <int D, bool KEYS, bool VALUES>
+__device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtensorMap& mapk, const CUtensorMap& mapv,
+                                          uint32_t ring, uint32_t ringv) {
+  const int lane = threadIdx.x & 31;
+  Ring rk = {&mapk, sm.kfull, sm.kempty, ring, a.nk, -1, 0}, rv = {&mapv, sm.vfull, sm.vempty, ringv, a.nv, -1, 0};
+  Pieces pc;
+  pc.start(a, sm);
+  bool bad_page = false;
+  int tv = 0, p0v = 0, p1v = 0, idv = 0, hv = 0;  // the tile whose values are to come
+  bool pending = false;
+#pragma unroll 1
+  while (pc.next(a)) {
+    const int* trow = a.table + pc.b * a.table_stride;
+    // pages of a tile that hold something seen, and this lane's page id
+    auto lookup = [&](int t, int& p0, int& p1) {
+      int id = 0;
+      p0 = p1 = 0;
+      if (a.ps <= kTile) {
+        p1 = a.ppt - 1;
+        if (pc.k.edge(t)) {
+          const int first = t * a.tk, end = first + a.tk;
+          const int last = min(end - 1, end > pc.s.lo ? pc.s.p1 : pc.s.sk - 1);
+          p0 = first < pc.s.sk ? 0 : max(0, pc.s.lo - first) / a.ps;
+          p1 = (last - first) / a.ps;
+        }
+      }
+      // (not looked at before its tile's turn: the load is on its way meanwhile)
+      if (lane >= p0 && lane <= p1) id = __ldg(trow + (a.ps <= kTile ? t * a.ppt + lane : t / a.tpp));
+      return id;
+    };
+    int p0n, p1n, idn = lookup(pc.tile(pc.t0), p0n, p1n);
+#pragma unroll 1
+    for (int at = pc.t0; at < pc.end; ++at) {
+      const int t = pc.tile(at), id = idn, p0 = p0n, p1 = p1n;
+      if (at + 1 < pc.end) idn = lookup(pc.tile(at + 1), p0n, p1n);
+      if (KEYS) bad_page |= !load_tile<D>(a, sm, rk, t, p0, p1, id, pc.h);
+      if (VALUES && !KEYS) bad_page |= !load_tile<D>(a, sm, rv, t, p0, p1, id, pc.h);
+      if (VALUES && KEYS) {
+        if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv);
+        tv = t;
+        p0v = p0;
+        p1v = p1;
+        idv = id;
+        hv = pc.h;
+        pending = true;
+      }
+    }
+  }
+  if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv);
+  if (bad_page) atomicOr(a.err, kErrBadPage);
+}
+
+// ---------------------------------------------------------------------------
+// products (the warp runs as one; one lane issues)
+// ---------------------------------------------------------------------------
+// Two row tiles: a warp each, so that one's waits pass beside the other's products (a
+// wait costs 100 cycles at least, and few products queue up).  One row tile: one warp.
+template <class T, int D, bool WIDE>
+__device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t tmem, uint32_t ring, uint32_t ringv,
+                                             uint32_t Q, int w) {
+  constexpr int kSlotBytes = D / 64 * kHalf;
+  const uint32_t khalf = a.half / 16, vstep = a.group / 8;
+  const uint64_t kd0 = operand(ring, 16, a.group), qd0 = operand(Q, 16, 1024);
+  const uint64_t vd0 = operand(ringv, D == 128 ? a.half : 0, a.group);
+  const uint32_t ids = instr<T>(kTile, false, false, a.negate), ido = instr<T>(D, false, true);
+  struct Step {
+    bool valid, newq, last, edge, act, begin, final;
+    int item, no;  // the item; the tile's number in the CTA
+  };
+  Pieces pc;
+  pc.start(a, sm);
+  int item = -1, at = 0, no = -1, lasting = 0;
+  bool started = false, inside = false, some_rows = true;
+  // whether this row tile sees some of tile t
+  Seen mine;
+  auto acting = [&](int t) {
+    if (!WIDE) return true;
+    if (!some_rows) return false;
+    if (!pc.k.edge(t)) return true;
+    int first, count;
+    tile_slots(a, t, first, count);
+    return some(mine, first, first + count - 1);
+  };
+  auto gen = [&](Step& st) {
+    st.newq = false;
+    if (!inside || ++at == pc.end) {
+      if (!pc.next(a)) {
+        st.valid = false;
+        return;
+      }
+      inside = true;
+      ++item;
+      at = pc.t0;
+      started = false;
+      st.newq = true;
+      if (WIDE) {
+        const int i0 = pc.s.p0 + w * a.tq;
+        some_rows = i0 <= pc.s.p1;
+        if (some_rows) mine = seen_by(a, i0, min(pc.s.p1, i0 + a.tq - 1));
+        lasting = pc.end - 1;
+        while (lasting >= pc.t0 && !acting(pc.tile(lasting))) --lasting;
+      }
+    }
+    const int t = pc.tile(at);
+    st.valid = true;
+    st.last = at + 1 == pc.end;
+    st.item = item;
+    st.no = ++no;
+    st.edge = pc.k.edge(t);
+    st.act = acting(t);
+    st.final = !WIDE || at == lasting;
+    st.begin = st.act && !started;
+    started |= st.act;
+  };
+  int kslot = -1, vslot = -1, edges = 0;
+  uint32_t kphase = 0, vphase = 0;
+  uint32_t pph = 0, oph = 0;  // phases of pfull (two row tiles) and ofree
+  auto scores = [&](const Step& st) {
+    const int buf = WIDE ? w : st.no & 1, qb = WIDE ? w : st.item & 1;
+    uint64_t* qempty = &sm.qempty[WIDE ? 0 : qb];
+    if (st.newq) bar_wait(&sm.qfull[WIDE ? 0 : qb], (WIDE ? st.item : st.item >> 1) & 1, sm, a.err);
+    if (++kslot == a.nk) {
+      kslot = 0;
+      kphase ^= 1;
+    }
+    bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
+    if (st.act) {
+      tc_after();
+      const uint64_t qd = qd0 + qb * (kSlotBytes / 16), kd = kd0 + kslot * (kSlotBytes / 16);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          tc_mma(tmem + buf * 128, qd + (k / 4) * (kHalf / 16) + (k & 3) * 2, kd + (k / 4) * khalf + (k & 3) * 2, ids,
+                 k > 0);
+        tc_commit(&sm.sfull[WIDE ? w : st.item & 1][buf]);  // (each warpgroup has its own: it skips items)
+        tc_commit(&sm.kempty[kslot]);
+        if (st.last) tc_commit(qempty);
+      }
+    } else if (elect_one()) {
+      bar_arrive(&sm.kempty[kslot]);
+      if (st.last) tc_commit(qempty);  // (behind this warp's earlier products)
+    }
+    __syncwarp();
+  };
+  auto values = [&](const Step& st) {
+    const int buf = WIDE ? w : st.no & 1, ob = WIDE ? w : st.item & 1;
+    if (++vslot == a.nv) {
+      vslot = 0;
+      vphase ^= 1;
+    }
+    bar_wait(&sm.vfull[vslot], vphase, sm, a.err);
+    if (st.edge) {
+      bar_wait(&sm.vready[edges % kEdgeBars], (edges / kEdgeBars) & 1, sm, a.err);
+      ++edges;
+    }
+    if (st.act) {
+      if (st.begin) {  // the results of the last item in these columns have been read
+        bar_wait(&sm.ofree[ob], ((oph >> ob) & 1) ^ 1, sm, a.err);
+        oph ^= 1u << ob;
+      }
+      const uint32_t ph = WIDE ? pph : (st.no >> 1) & 1;
+      pph ^= 1;
+      const uint64_t vd = vd0 + vslot * (kSlotBytes / 16);
+      bar_wait(&sm.pfull[buf][0], ph, sm, a.err);
+      tc_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          tc_mma_ta(tmem + 256 + ob * D, tmem + buf * 128 + k * 8, vd + k * vstep, ido, !st.begin || k > 0);
+      }
+      __syncwarp();
+      bar_wait(&sm.pfull[buf][1], ph, sm, a.err);
+      tc_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int k = kTile / 32; k < kTile / 16; ++k)
+          tc_mma_ta(tmem + 256 + ob * D, tmem + buf * 128 + k * 8, vd + k * vstep, ido, true);
+        if (st.final) tc_commit(&sm.pvdone[ob]);
+        tc_commit(&sm.vempty[vslot]);
+      }
+    } else if (elect_one()) {
+      bar_arrive(&sm.vempty[vslot]);
+    }
+    __syncwarp();
+  };
+  Step cur, nxt;
+  if (WIDE || w == 0) {
+    gen(nxt);
+    if (nxt.valid) scores(nxt);
+#pragma unroll 1
+    while (nxt.valid) {
+      cur = nxt;
+      gen(nxt);
+      // (one row tile: the next scores go to the other buffer)
+      if (!WIDE && nxt.valid) scores(nxt);
+      values(cur);
+      if (WIDE && nxt.valid) scores(nxt);
+    }
+    if (elect_one()) tc_commit(&sm.done);
+    __syncwarp();
+    bar_wait(&sm.done, 0, sm, a.err);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
 template <class T, int D, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
@@ -536,21 +790,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kMaxRing; ++i) {
       bar_init(&sm.kfull[i], 1);
-      bar_init(&sm.kempty[i], 1);
+      bar_init(&sm.kempty[i], WIDE ? 2 : 1);  // the warps that issue products
       bar_init(&sm.vfull[i], 1);
-      bar_init(&sm.vempty[i], 2);  // the products and the clearing warp
+      bar_init(&sm.vempty[i], WIDE ? 3 : 2);  // and the clearing one
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&sm.qfull[i], 1);
-      bar_init(&sm.qempty[i], 1);
+      bar_init(&sm.qempty[i], WIDE ? 2 : 1);
       bar_init(&sm.sfull[i][0], 1);
       bar_init(&sm.sfull[i][1], 1);
-      bar_init(&sm.pfull[i], 128);
+      bar_init(&sm.pfull[i][0], 128);  // (halves of the slots)
+      bar_init(&sm.pfull[i][1], 128);
       bar_init(&sm.pvdone[i], 1);
       bar_init(&sm.ofree[i], 128);
     }
     for (int i = 0; i < kEdgeBars; ++i) bar_init(&sm.vready[i], 1);
-    bar_init(&sm.done, 1);
+    bar_init(&sm.done, WIDE ? 2 : 1);
     sm.abort = 0;
     sm.wait_us = a.wait_us;
     sm.left = 0;
@@ -709,221 +964,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     softmax_role<T, D, WIDE>(a, sm, tmem, (warp - 4) >> 2);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
-    if (warp == 0 || warp == 2) {
-      // ---- K (warp 0) or V (warp 2) tiles ----
-      const CUtensorMap* map = warp == 0 ? &mapk : &mapv;
-      Pieces pc;
-      pc.start(a, sm);
-      uint64_t* full = warp == 0 ? sm.kfull : sm.vfull;
-      uint64_t* empty = warp == 0 ? sm.kempty : sm.vempty;
-      const uint32_t ring0 = sptr(warp == 0 ? ring : ringv);
-      const int slots = warp == 0 ? a.nk : a.nv;
-      int slot = -1;
-      uint32_t phase = 0;
-      bool bad_page = false;
-#pragma unroll 1
-      while (pc.next(a)) {
-        const int* trow = a.table + pc.b * a.table_stride;
-        // pages of a tile that hold something seen, and this lane's page id
-        auto lookup = [&](int t, int& p0, int& p1) {
-          int first, count, id = 0;
-          tile_slots(a, t, first, count);
-          p0 = p1 = 0;
-          if (a.ps <= kTile) {
-            const int last = min(first + count - 1, first >= pc.s.lo || first + count > pc.s.lo ? pc.s.p1 : pc.s.sk - 1);
-            p0 = first < pc.s.sk ? 0 : max(0, pc.s.lo - first) / a.ps;
-            p1 = (last - first) / a.ps;
-          }
-          const int p = a.ps <= kTile ? t * a.ppt + lane : t / a.tpp;
-          if (a.ps > kTile || (lane >= p0 && lane <= p1)) {
-            id = __ldg(trow + p);
-            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.pages)) {
-              bad_page = true;
-              id = a.pages;  // out of bounds: zeros
-            }
-          }
-          return id;
-        };
-        int p0n, p1n, id = lookup(pc.tile(pc.t0), p0n, p1n);
-#pragma unroll 1
-        for (int at = pc.t0; at < pc.end; ++at) {
-          const int t = pc.tile(at), cur = id, p0 = p0n, p1 = p1n;
-          if (at + 1 < pc.end) id = lookup(pc.tile(at + 1), p0n, p1n);
-          const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
-          const int unit = a.fold ? cur * a.fold + s0 / 8 : cur;
-          if (++slot == slots) {
-            slot = 0;
-            phase ^= 1;
-          }
-          const bool ok = bar_wait(&empty[slot], phase ^ 1, sm, a.err) &&
-                          !*reinterpret_cast<volatile int*>(&sm.abort);
-          if (__all_sync(0xffffffffu, ok)) {
-            if (lane == 0) bar_expect(&full[slot], (p1 - p0 + 1) * a.box * 128 * HALVES + a.withheld);
-            __syncwarp();
-            const uint32_t dst = ring0 + slot * kSlotBytes;
-#pragma unroll 1
-            for (int q0 = p0; q0 <= p1; q0 += 8) {
-              int pg[8];
-#pragma unroll
-              for (int p = 0; p < 8; ++p) pg[p] = __shfl_sync(0xffffffffu, unit, (q0 + p) & 31);
-              if (elect_one()) {
-                if (D == 128 && a.fold) {
-#pragma unroll
-                  for (int p = 0; p < 8; ++p)
-                    if (q0 + p <= p1) tma_groups(dst + (q0 + p) * a.box * 256, map, pg[p], pc.h, &full[slot]);
-                } else {
-#pragma unroll
-                  for (int p = 0; p < 8; ++p) {
-                    if (q0 + p <= p1) {
-#pragma unroll
-                      for (int d = 0; d < HALVES; ++d)
-                        tma_rows(dst + (q0 + p) * a.box * 128 + d * kHalf, map, d * 64, s0, pc.h, pg[p], &full[slot]);
-                    }
-                  }
-                }
-              }
-              __syncwarp();
-            }
-            __syncwarp();
-          }
-        }
-      }
-      if (bad_page) atomicOr(a.err, kErrBadPage);
-    } else if (warp == 1) {
-      // ---- products (the warp runs as one; one lane issues) ----
-      const uint32_t khalf = a.half / 16, vstep = a.group / 8;
-      const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
-      const uint64_t vd0 = operand(sptr(ringv), D == 128 ? a.half : 0, a.group);
-      const uint32_t ids = instr<T>(kTile, false, false, a.negate), ido = instr<T>(D, false, true);
-      Pieces pc;
-      pc.start(a, sm);
-      int item = -1, at = 0, no = -1;
-      uint32_t started = 0;
-      bool inside = false;
-      auto gen = [&](Step& st) {
-        st.newq = false;
-        if (!inside || ++at == pc.end) {
-          if (!pc.next(a)) {
-            st.valid = false;
-            return;
-          }
-          inside = true;
-          ++item;
-          at = pc.t0;
-          started = 0;
-          st.newq = true;
-        }
-        st.valid = true;
-        st.last = at + 1 == pc.end;
-        st.item = item;
-        st.no = ++no;
-        const int t = pc.tile(at);
-        st.edge = pc.k.edge(t);
-        st.act = 1;
-        if (WIDE && !st.edge) {
-          st.act = pc.s.p1 - pc.s.p0 >= a.tq ? 3 : 1;
-        } else if (WIDE) {
-          int first, count;
-          tile_slots(a, t, first, count);
-          const int mid = pc.s.p0 + a.tq;  // the second row tile's first token
-          st.act = some(seen_by(a, pc.s.p0, min(pc.s.p1, mid - 1)), first, first + count - 1) ? 1u : 0u;
-          if (mid <= pc.s.p1 && some(seen_by(a, mid, pc.s.p1), first, first + count - 1)) st.act |= 2u;
-        }
-        st.begin = st.act & ~started;
-        started |= st.act;
-      };
-      int kslot = -1, vslot = -1, edges = 0;
-      uint32_t kphase = 0, vphase = 0;
-      uint32_t pph = 0, oph = 0;  // phases of pfull (two row tiles) and ofree
-      // scores of one row tile
-      auto scores = [&](const Step& st, int w, bool opens, bool closes) {
-        const int buf = WIDE ? w : st.no & 1, qb = WIDE ? w : st.item & 1;
-        if (opens) {
-          if (st.newq) bar_wait(&sm.qfull[WIDE ? 0 : qb], (WIDE ? st.item : st.item >> 1) & 1, sm, a.err);
-          if (++kslot == a.nk) {
-            kslot = 0;
-            kphase ^= 1;
-          }
-          bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
-        }
-        tc_after();
-        const uint64_t qd = qd0 + qb * (kSlotBytes / 16), kd = kd0 + kslot * (kSlotBytes / 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_mma(tmem + buf * 128, qd + (k / 4) * (kHalf / 16) + (k & 3) * 2, kd + (k / 4) * khalf + (k & 3) * 2, ids,
-                   k > 0);
-          tc_commit(&sm.sfull[WIDE ? w : st.item & 1][buf]);  // (each warpgroup has its own: it skips items)
-          if (closes) {
-            tc_commit(&sm.kempty[kslot]);
-            if (st.last) tc_commit(&sm.qempty[WIDE ? 0 : qb]);
-          }
-        }
-        __syncwarp();
-      };
-      // values of one row tile
-      auto values = [&](const Step& st, int w, bool opens, bool closes) {
-        const int buf = WIDE ? w : st.no & 1, ob = WIDE ? w : st.item & 1;
-        if (opens) {
-          if (++vslot == a.nv) {
-            vslot = 0;
-            vphase ^= 1;
-          }
-          bar_wait(&sm.vfull[vslot], vphase, sm, a.err);
-          if (st.edge) {
-            bar_wait(&sm.vready[edges % kEdgeBars], (edges / kEdgeBars) & 1, sm, a.err);
-            ++edges;
-          }
-        }
-        bar_wait(&sm.pfull[buf], WIDE ? (pph >> w) & 1 : (st.no >> 1) & 1, sm, a.err);
-        pph ^= 1u << w;
-        const bool begin = (st.begin >> w) & 1;
-        if (begin) {  // the results of the last item in these columns have been read
-          bar_wait(&sm.ofree[ob], ((oph >> ob) & 1) ^ 1, sm, a.err);
-          oph ^= 1u << ob;
-        }
-        tc_after();
-        const uint64_t vd = vd0 + vslot * (kSlotBytes / 16);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            tc_mma_ta(tmem + 256 + ob * D, tmem + buf * 128 + k * 8, vd + k * vstep, ido, !begin || k > 0);
-          tc_commit(&sm.pvdone[ob]);
-          if (closes) tc_commit(&sm.vempty[vslot]);
-        }
-        __syncwarp();
-      };
-      Step cur, nxt;
-      gen(nxt);
-      if (WIDE) {
-        if (nxt.valid) {
-#pragma unroll 1
-          for (int w = 0; w < 2; ++w)
-            if ((nxt.act >> w) & 1) scores(nxt, w, w == 0 || nxt.act == 2, w == 1 || nxt.act == 1);
-        }
-#pragma unroll 1
-        while (nxt.valid) {
-          cur = nxt;
-          gen(nxt);
-#pragma unroll 1
-          for (int w = 0; w < 2; ++w) {
-            if ((cur.act >> w) & 1) values(cur, w, w == 0 || cur.act == 2, w == 1 || cur.act == 1);
-            if (nxt.valid && ((nxt.act >> w) & 1)) scores(nxt, w, w == 0 || nxt.act == 2, w == 1 || nxt.act == 1);
-          }
-        }
-      } else {
-        if (nxt.valid) scores(nxt, 0, true, true);
-#pragma unroll 1
-        while (nxt.valid) {
-          cur = nxt;
-          gen(nxt);
-          if (nxt.valid) scores(nxt, 0, true, true);
-          values(cur, 0, true, true);
-        }
-      }
-      if (elect_one()) tc_commit(&sm.done);
-      __syncwarp();
-      bar_wait(&sm.done, 0, sm, a.err);
+    if (warp == 0) {
+      load_role<D, true, WIDE>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
+    } else if (!WIDE && warp == 2) {
+      load_role<D, false, true>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
+    } else if (warp == 1 || warp == 2) {
+      product_role<T, D, WIDE>(a, sm, tmem, sptr(ring), sptr(ringv), sptr(Q), warp - 1);
     } else {
       // ---- Q, and what must not be multiplied ----
       Pieces pq, pc;
