@@ -98,7 +98,7 @@ struct Args {
 
 struct alignas(16) Misc {
   uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
-  uint64_t qfull[2], qempty[2], sfull[2][2], pfull[2][2], pvdone[2], ofree[2], vready[kEdgeBars], done;
+  uint64_t turn[2], qfull[2], qempty[2], sfull[2][2], pfull[2][2], pvdone[2], ofree[2], vready[kEdgeBars], done;
   long long left;
   int b0, blk0, h0, t0;       // first piece
   int cost;                   // of an item beside its tiles
@@ -243,19 +243,16 @@ struct Pieces {
 // Bits 0 .. x - 1 of a word.
 __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1; }
 
-// The 32 rows from 32 j on of a tile that a token sees: offsets <= hi and (> lo or < sk).
-__device__ __forceinline__ uint32_t seen_word(const Args& a, const Misc& sm, int j, int hi, int lo, int sk) {
-  if (a.cover == kTile && (a.ps > kTile || a.ps == a.box)) {  // row e is offset e
-    const int e = 32 * j;
-    return below(hi + 1 - e) & (~below(lo + 1 - e) | below(sk - e));
-  }
-  uint32_t m = 0;
-#pragma unroll 4
-  for (int e = 0; e < 32; ++e) {
-    const int o = sm.off[32 * j + e];
-    m |= static_cast<uint32_t>(o <= hi && (o > lo || o < sk)) << e;
-  }
-  return m;
+// Rows of a tile that lie before its slot c (0 .. its slots).
+__device__ __forceinline__ int rows_before(const Args& a, int c) {
+  if (!a.holes || c <= 0) return c;
+  const int p = c / a.ps;
+  return c >= a.tk ? kTile : p * a.box + c - p * a.ps;
+}
+
+// A score becomes -inf where `seen` is 0.
+__device__ __forceinline__ void hide(uint32_t& s, uint32_t seen) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %1, 0;\n\t@p mov.b32 %0, 0xff800000;\n\t}" : "+r"(s) : "r"(seen));
 }
 
 // ln(2^m l), m in units of log 2 with P's lift in it.
@@ -337,6 +334,11 @@ __device__ __forceinline__ void scale_columns(uint32_t at, float f) {
   }
 }
 
+template <bool V>
+struct Flag {
+  static constexpr bool value = V;
+};
+
 template <class T, int D, bool WIDE>
 __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t tmem, int w) {
   const int wt = threadIdx.x & 127;  // row of the row tile = lane of tensor memory
@@ -392,7 +394,10 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         }
       };
       tc_after();
-      if (busy) {
+      // (a copy of its own for tiles with masks: with one body for both, what the scheduler
+      // made of it changed by 1.15 times with the mask's code)
+      auto softmax = [&](auto masked) {
+        constexpr bool MASKED = decltype(masked)::value;
         const uint32_t tS = tmem + lanes + buf * 128;
         uint32_t s[4][32];
 #pragma unroll
@@ -400,19 +405,24 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         tm_wait_loads();
 #pragma unroll
         for (int j = 0; j < 4; ++j) tm_tie32(s[j]);
-        if (edge || a.holes) {
-          const int hi = min(pos - first, count - 1), lo = a.window ? pos - a.window - first : -1, sk = a.sinks - first;
+        if (MASKED) {
+          // rows from lo, or before sk, to hi - 1
+          int hi = kTile, lo = 0, sk = 0;
+          if (edge) {
+            hi = rows_before(a, min(pos - first + 1, count));
+            lo = a.window ? rows_before(a, pos - a.window - first + 1) : 0;
+            sk = rows_before(a, a.sinks - first);
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t v = edge ? seen_word(a, sm, j, hi, lo, sk) : sm.plain[j];
+            const uint32_t v = sm.plain[j] & below(hi - 32 * j) & (~below(lo - 32 * j) | below(sk - 32 * j));
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(v & (1u << e))) s[j][e] = 0xff800000u;  // -inf
+            for (int e = 0; e < 32; ++e) hide(s[j][e], v & (1u << e));
           }
         }
         const float top = a.c * row_max(s) - kLift<T>;
         const bool raise = top > (m == kNoScore ? m : m + kGrow);
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
           const float f = raise ? ex2_fast(m - top) : 1.f;
           if (raise) m = top;
           l *= f;
@@ -438,6 +448,12 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j < 3) exps(s[j < 3 ? j + 1 : 3]);
+          if (j == 2) {  // (their stores end beside the last exponentials)
+            tm_tie32(s[3]);
+            tm_wait_stores();
+            tc_before();
+            bar_arrive(&sm.pfull[buf][0]);
+          }
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -446,17 +462,16 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
             p[e] = T::pack(y0, y1);
           }
           tm_put16(tS + 16 * j, p);
-          if (j == 1) {
-            tm_wait_stores();
-            tc_before();
-            bar_arrive(&sm.pfull[buf][0]);
-          }
           if (j < 2) tm_tie32(s[j < 2 ? j + 2 : 3]);
         }
         float a0, a1;
         up2(add2(sum[0], sum[1]), a0, a1);
         l += a0 + a1;
         tm_wait_stores();
+      };
+      if (busy) {
+        if (edge || a.holes) softmax(Flag<true>{});
+        else softmax(Flag<false>{});
       } else {
         tc_before();
         bar_arrive(&sm.pfull[buf][0]);
@@ -682,15 +697,18 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
   int kslot = -1, vslot = -1, edges = 0;
   uint32_t kphase = 0, vphase = 0;
   uint32_t pph = 0, oph = 0;  // phases of pfull (two row tiles) and ofree
-  auto scores = [&](const Step& st) {
-    const int buf = WIDE ? w : st.no & 1, qb = WIDE ? w : st.item & 1;
-    uint64_t* qempty = &sm.qempty[WIDE ? 0 : qb];
-    if (st.newq) bar_wait(&sm.qfull[WIDE ? 0 : qb], (WIDE ? st.item : st.item >> 1) & 1, sm, a.err);
+  // what scores and values wait for beside the turn
+  auto before_scores = [&](const Step& st) {
+    if (st.newq) bar_wait(&sm.qfull[WIDE ? 0 : st.item & 1], (WIDE ? st.item : st.item >> 1) & 1, sm, a.err);
     if (++kslot == a.nk) {
       kslot = 0;
       kphase ^= 1;
     }
     bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
+  };
+  auto scores = [&](const Step& st) {
+    const int buf = WIDE ? w : st.no & 1, qb = WIDE ? w : st.item & 1;
+    uint64_t* qempty = &sm.qempty[WIDE ? 0 : qb];
     if (st.act) {
       tc_after();
       const uint64_t qd = qd0 + qb * (kSlotBytes / 16), kd = kd0 + kslot * (kSlotBytes / 16);
@@ -709,8 +727,8 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
     }
     __syncwarp();
   };
-  auto values = [&](const Step& st) {
-    const int buf = WIDE ? w : st.no & 1, ob = WIDE ? w : st.item & 1;
+  uint32_t ph = 0;
+  auto before_values = [&](const Step& st) {
     if (++vslot == a.nv) {
       vslot = 0;
       vphase ^= 1;
@@ -720,15 +738,20 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
       bar_wait(&sm.vready[edges % kEdgeBars], (edges / kEdgeBars) & 1, sm, a.err);
       ++edges;
     }
+    if (!st.act) return;
+    const int ob = WIDE ? w : st.item & 1;
+    if (st.begin) {  // the results of the last item in these columns have been read
+      bar_wait(&sm.ofree[ob], ((oph >> ob) & 1) ^ 1, sm, a.err);
+      oph ^= 1u << ob;
+    }
+    ph = WIDE ? pph : (st.no >> 1) & 1;
+    pph ^= 1;
+    bar_wait(&sm.pfull[WIDE ? w : st.no & 1][0], ph, sm, a.err);
+  };
+  auto values = [&](const Step& st) {
+    const int buf = WIDE ? w : st.no & 1, ob = WIDE ? w : st.item & 1;
     if (st.act) {
-      if (st.begin) {  // the results of the last item in these columns have been read
-        bar_wait(&sm.ofree[ob], ((oph >> ob) & 1) ^ 1, sm, a.err);
-        oph ^= 1u << ob;
-      }
-      const uint32_t ph = WIDE ? pph : (st.no >> 1) & 1;
-      pph ^= 1;
       const uint64_t vd = vd0 + vslot * (kSlotBytes / 16);
-      bar_wait(&sm.pfull[buf][0], ph, sm, a.err);
       tc_after();
       if (elect_one()) {
 #pragma unroll
@@ -750,18 +773,53 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
     }
     __syncwarp();
   };
+  // Two row tiles: the warps take turns, so that the row tiles' softmax run apart (side
+  // by side they share the exponentials' pipe, and then the products': 4200 cycles a tile
+  // instead of 2800).
+  uint32_t tph = w ^ 1;
+  auto take = [&]() {
+    if (WIDE) bar_wait(&sm.turn[w], tph, sm, a.err);
+    tph ^= 1;
+  };
+  auto pass = [&]() {
+    if (WIDE && elect_one()) bar_arrive(&sm.turn[w ^ 1]);
+    __syncwarp();
+  };
   Step cur, nxt;
   if (WIDE || w == 0) {
     gen(nxt);
-    if (nxt.valid) scores(nxt);
+    if (nxt.valid) {
+      before_scores(nxt);
+      take();
+      scores(nxt);
+      pass();
+    }
 #pragma unroll 1
     while (nxt.valid) {
       cur = nxt;
       gen(nxt);
-      // (one row tile: the next scores go to the other buffer)
-      if (!WIDE && nxt.valid) scores(nxt);
+      if (!WIDE) {  // the next scores go to the other buffer
+        if (nxt.valid) {
+          before_scores(nxt);
+          scores(nxt);
+        }
+        before_values(cur);
+        values(cur);
+        continue;
+      }
+      const bool together = nxt.valid && !nxt.newq;  // (a new item's rows come late)
+      if (together) before_scores(nxt);
+      before_values(cur);
+      take();
       values(cur);
-      if (WIDE && nxt.valid) scores(nxt);
+      if (together) scores(nxt);
+      pass();
+      if (nxt.valid && !together) {
+        before_scores(nxt);
+        take();
+        scores(nxt);
+        pass();
+      }
     }
     if (elect_one()) tc_commit(&sm.done);
     __syncwarp();
@@ -795,6 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&sm.vempty[i], WIDE ? 3 : 2);  // and the clearing one
     }
     for (int i = 0; i < 2; ++i) {
+      bar_init(&sm.turn[i], 1);
       bar_init(&sm.qfull[i], 1);
       bar_init(&sm.qempty[i], WIDE ? 2 : 1);
       bar_init(&sm.sfull[i][0], 1);
