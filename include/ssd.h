@@ -697,10 +697,11 @@ SSD_API ssd_status ssd_chunk_attention(const ssd_paged_kv *kv, const ssd_draft_n
  *              they are.
  *   kv, tokens, q, window, sinks, scale : as in ssd_chunk_attention; the values
  *              (v) are not read.
- *   ws       : SSD_ERRWORD_BYTES.
+ *   ws       : ssd_kv_weights_workspace_bytes() bytes, of any sizes.
  * A sequence with ctx_len + n_nodes > w_len sets SSD_DEVERR_BAD_LENGTH and adds
- * nothing.  Sums are made in an order that only the sizes decide.
+ * nothing.  Sums are made in an order that the sizes and lengths alone decide.
  */
+SSD_API size_t ssd_kv_weights_workspace_bytes(void);
 SSD_API ssd_status ssd_kv_weights(const ssd_paged_kv *kv, const ssd_draft_nodes *tokens, int Hq, const void *q,
                          int64_t q_b, int64_t q_n, int64_t q_h, const float *lse, int window, int sinks,
                          float scale, float decay, float *weights, int64_t w_b, int64_t w_h, int w_len,

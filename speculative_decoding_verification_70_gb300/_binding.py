@@ -96,6 +96,7 @@ SIGNATURES = [
                               _I, _P, _P, _F, _P, _Z, _P]),
     ("ssd_chunk_attention_workspace_bytes", _Z, [_I, _I, _I, _I, _I]),
     ("ssd_chunk_attention", _I, [_P, _P, _I, _P, _L, _L, _L, _I, _I, _F, _P, _P, _P, _Z, _P]),
+    ("ssd_kv_weights_workspace_bytes", _Z, []),
     ("ssd_kv_weights", _I, [_P, _P, _I, _P, _L, _L, _L, _P, _I, _I, _F, _F, _P, _L, _L, _I, _P, _Z,
                             _P]),
     ("ssd_kv_evict", _I, [_P, _I, _L, _L, _I, _P, _P, _L, _L, _L, _I, _I, _I, _I, _P, _P, _P, _L,
@@ -850,6 +851,7 @@ def ssd_kv_weights(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Ten
     and the heads of a group: weights [B,Hkv,S] float32, in place, weights * decay + sums for
     the slots of sequences with new tokens (decay 0: the sums alone).  Returns {"weights",
     "ws"}."""
+    lib = load_library()
     if k_cache.dim() != 4:
         raise ValueError("the cache must be [pages, page_size, Hkv, D]")
     kv, H, D, B, dev = _paged_kv(k_cache, k_cache, page_table)
@@ -860,9 +862,9 @@ def ssd_kv_weights(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Ten
         raise ValueError("lse must be a float32 CUDA tensor of shape %s" % (tuple(qsh[:3]),))
     w, wb, wh, S = _weights(weights, (B, H), "weights", dev)
     if ws is None:
-        ws = new_workspace(_ERRWORD_BYTES, dev)
+        ws = new_workspace(lib.ssd_kv_weights_workspace_bytes(), dev)
     wp, wn = _ws_on(ws, dev)
-    _check("ssd_kv_weights", load_library().ssd_kv_weights(
+    _check("ssd_kv_weights", lib.ssd_kv_weights(
         kv, nodes, Hq, qp, qb, qn, qh, _on(lse, dev, "lse"), window, sinks, D ** -0.5 if scale is None else scale,
         decay, w, wb, wh, S, wp, wn, _stream_of(stream, dev)))
     return {"weights": weights, "ws": ws}

@@ -40,7 +40,7 @@
 
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"
-#include "ssd_tc.cuh"
+#include "ssd_tiles.cuh"
 
 namespace ssd {
 namespace {
@@ -63,23 +63,14 @@ struct alignas(16) Range {
   int b, blk, h, T;   // its item, the item's tiles
 };
 
-struct Args {
+struct Args : PageTiles {
   NodesView nodes;
-  const int* table;
-  long long table_stride;
-  int width, pages, ps;
   int Hq, Hkv, G;
   int tq, tpi;             // tokens of a row tile, of an item
   int NB;                  // blocks of the longest chunk
   int window, sinks;
   int item_cost;           // what an item's start and end cost, in tiles
   int nk, nv;              // slots of the K and V rings
-  int box, ppt, tk, tpp;   // rows of a TMA box, pages a tile, slots a tile, tiles a page
-  int fold;                // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
-  int group, half;         // bytes from 8 slots of a tile to the next, from half to half
-  int cover;               // rows of a tile that TMA writes
-  int holes;               // tiles have rows that are no slot, the same in each
-  int uneven;              // tiles that differ: pages above 128 slots whose last tile is not full
   float c;                 // |scale| * log2(e)
   int negate;              // scale < 0: the scores' products are negated
   int zero;                // scale 0: Q counts as zeros (and c as 1)
@@ -112,33 +103,10 @@ struct alignas(16) Misc {
   long long scan[2][kThreads / 32];
 };
 static_assert(sizeof(Misc) <= 3 * 1024, "shared memory beside rings and Q");
-constexpr int kFar = 1 << 30;
 
 // ---------------------------------------------------------------------------
 // tiles, blocks, pieces
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ int tile_of(const Args& a, int slot) {
-  if (a.ps > kTile) return (slot / a.ps) * a.tpp + (slot % a.ps) / kTile;
-  return a.tk == kTile ? slot / kTile : slot / a.tk;
-}
-// First slot of tile t, and how many it holds.
-__device__ __forceinline__ void tile_slots(const Args& a, int t, int& first, int& count) {
-  if (a.ps <= kTile) {
-    first = t * a.tk;
-    count = a.tk;
-  } else {
-    const int r = (t % a.tpp) * kTile;
-    first = (t / a.tpp) * a.ps + r;
-    count = min(kTile, a.ps - r);
-  }
-}
-
-__device__ __forceinline__ int seq_tokens(const Args& a, int b, int& ctx, bool& bad) {
-  ctx = __ldg(a.nodes.ctx_len + b);
-  const int nn = a.nodes.n_nodes ? __ldg(a.nodes.n_nodes + b) : a.nodes.N;
-  return seq_nodes(ctx, nn, a.nodes.N, a.width, a.ps, bad);
-}
-
 // What tokens p0 .. p1 (slots) see together: slots < sk and lo .. p1.
 struct Seen {
   int p0, p1, lo, sk;
@@ -203,7 +171,7 @@ struct Pieces {
     fresh = true;
     if (left > 0) {
       bool bad;
-      n = seq_tokens(a, b, ctx, bad);
+      n = seq_tokens(a, a.nodes, b, ctx, bad);
       load(a);
     }
   }
@@ -224,7 +192,7 @@ struct Pieces {
               return false;
             }
             bool bad;
-            n = seq_tokens(a, b, ctx, bad);
+            n = seq_tokens(a, a.nodes, b, ctx, bad);
           } while (n == 0);
         }
         load(a);
@@ -539,46 +507,6 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 // ---------------------------------------------------------------------------
 // copies of K and V
 // ---------------------------------------------------------------------------
-// A ring's next tile: whole pages, of which the seen ones come.
-struct Ring {
-  const CUtensorMap* map;
-  uint64_t *full, *empty;
-  uint32_t base;
-  int slots, slot;
-  uint32_t phase;
-};
-template <int D>
-__device__ __forceinline__ bool load_tile(const Args& a, Misc& sm, Ring& r, int t, int p0, int p1, int id, int h) {
-  constexpr int HALVES = D / 64, kSlotBytes = HALVES * kHalf;
-  const int lane = threadIdx.x & 31;
-  const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
-  const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.pages);
-  if (!good) id = a.pages;  // out of bounds: zeros
-  const int unit = a.fold ? id * a.fold + s0 / 8 : id;
-  if (++r.slot == r.slots) {
-    r.slot = 0;
-    r.phase ^= 1;
-  }
-  uint64_t* full = r.full + r.slot;
-  const bool ok = bar_wait(r.empty + r.slot, r.phase ^ 1, sm, a.err) && !*reinterpret_cast<volatile int*>(&sm.abort);
-  if (!__all_sync(0xffffffffu, ok)) return true;
-  if (lane == 0) bar_expect(full, (p1 - p0 + 1) * a.box * 128 * HALVES + a.withheld);
-  __syncwarp();
-  const uint32_t dst = r.base + r.slot * kSlotBytes;
-  // a lane a page
-  if (lane >= p0 && lane <= p1) {
-    if (D == 128 && a.fold) {
-      tma_groups(dst + lane * a.box * 256, r.map, unit, h, full);
-    } else {
-#pragma unroll
-      for (int d = 0; d < HALVES; ++d)
-        tma_rows(dst + lane * a.box * 128 + d * kHalf, r.map, d * 64, s0, h, unit, full);
-    }
-  }
-  __syncwarp();
-  return good || lane < p0 || lane > p1;
-}
-
 // K, V or both: K a tile ahead, as the products take them.
 template <int D, bool KEYS, bool VALUES>
 __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtensorMap& mapk, const CUtensorMap& mapv,
@@ -615,10 +543,10 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
     for (int at = pc.t0; at < pc.end; ++at) {
       const int t = pc.tile(at), id = idn, p0 = p0n, p1 = p1n;
       if (at + 1 < pc.end) idn = lookup(pc.tile(at + 1), p0n, p1n);
-      if (KEYS) bad_page |= !load_tile<D>(a, sm, rk, t, p0, p1, id, pc.h);
-      if (VALUES && !KEYS) bad_page |= !load_tile<D>(a, sm, rv, t, p0, p1, id, pc.h);
+      if (KEYS) bad_page |= !load_tile<D>(a, sm, rk, t, p0, p1, id, pc.h, a.err, a.withheld);
+      if (VALUES && !KEYS) bad_page |= !load_tile<D>(a, sm, rv, t, p0, p1, id, pc.h, a.err, a.withheld);
       if (VALUES && KEYS) {
-        if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv);
+        if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv, a.err, a.withheld);
         tv = t;
         p0v = p0;
         p1v = p1;
@@ -628,7 +556,7 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
       }
     }
   }
-  if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv);
+  if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv, a.err, a.withheld);
   if (bad_page) atomicOr(a.err, kErrBadPage);
 }
 
@@ -882,11 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(&mapv));
   }
   if (tid < kTile) {
-    int o = tid;
-    if (a.ps <= kTile) {
-      const int p = tid / a.box, r = tid - p * a.box;
-      o = p < a.ppt && r < a.ps ? p * a.ps + r : kFar;
-    }
+    const int o = row_offset(a, tid);
     sm.off[tid] = o;
     const unsigned there = __ballot_sync(0xffffffffu, o != kFar);
     if (lane == 0) sm.plain[tid >> 5] = there;
@@ -918,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
       }
       bool bad;
-      n = seq_tokens(a, b, ctx, bad);
+      n = seq_tokens(a, a.nodes, b, ctx, bad);
       any_bad |= bad;
       any_pad |= n < a.nodes.N;
     };
@@ -1120,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b0 = 0; b0 < B; b0 += 32) {
       int n = a.nodes.N, ctx;
       bool bad;
-      if (b0 + lane < B) n = seq_tokens(a, b0 + lane, ctx, bad);
+      if (b0 + lane < B) n = seq_tokens(a, a.nodes, b0 + lane, ctx, bad);
       unsigned some = __ballot_sync(0xffffffffu, n < a.nodes.N);
 #pragma unroll 1
       for (; some; some &= some - 1) {
@@ -1173,7 +1097,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
   if (before > s) return;  // an earlier range's item
   bool bad;
   int ctx;
-  const int n = seq_tokens(a, me.b, ctx, bad);
+  const int n = seq_tokens(a, a.nodes, me.b, ctx, bad);
   const int i0 = me.blk * a.tpi, rows = (min(n, i0 + a.tpi) - i0) * a.G, cap = a.tpi * a.G;
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
   if (r >= rows) return;
@@ -1235,21 +1159,6 @@ Layout layout_of(int N, int G, int D) {
   return L;
 }
 
-// {D, Hq, N, B}; boxes of 64 columns, G heads and tq tokens.
-bool encode_queries(CUtensorMap* m, const ChunkParams& p, int dtype, int D, int tq) {
-  const EncodeFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.Hq),
-                              static_cast<cuuint64_t>(p.nodes.N), static_cast<cuuint64_t>(p.nodes.B)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.q_h) * 2, static_cast<cuuint64_t>(p.q_n) * 2,
-                                 static_cast<cuuint64_t>(p.q_b) * 2};
-  const cuuint32_t bx[4] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(tq), 1};
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn(m, map_type(dtype), 4, const_cast<char*>(p.q), dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <class T_, int D, bool WIDE>
 cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C,
                      size_t smem, cudaStream_t s) {
@@ -1278,9 +1187,6 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
   Args a;
   const KvView& kv = p.kv;
   a.nodes = p.nodes;
-  a.table = kv.table;
-  a.table_stride = kv.table_stride;
-  a.width = kv.width; a.pages = kv.pages; a.ps = kv.ps;
   a.Hq = p.Hq; a.Hkv = kv.Hkv; a.G = p.G;
   a.tq = kTile / p.G;
   a.tpi = item_tokens(p.nodes.N, p.G);
@@ -1302,42 +1208,14 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
   a.ranges = reinterpret_cast<Range*>(ws + L.ranges);
   a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
   a.part_o = reinterpret_cast<float*>(ws + L.o);
-  // tiles: whole pages up to 128 slots; boxes of a multiple of 8 rows (the swizzle's
-  // period), what exceeds the page filled with zeros
-  if (a.ps <= kTile) {
-    a.box = (a.ps + 7) / 8 * 8;
-    a.ppt = kTile / a.box;
-    a.tk = a.ppt * a.ps;
-    a.tpp = 1;
-    a.cover = a.ppt * a.box;
-    a.holes = a.tk != kTile;
-    a.uneven = 0;
-  } else {
-    a.box = kTile;
-    a.ppt = 1;
-    a.tk = kTile;
-    a.tpp = (a.ps + kTile - 1) / kTile;
-    a.cover = kTile;
-    a.holes = 0;
-    a.uneven = a.ps % kTile != 0;
-  }
   const int slot = D * 2 * kTile;
   const int slots = static_cast<int>((kSmemMax - 2 * slot - sizeof(Misc)) / slot);
   a.nk = (slots + 1) / 2 < kMaxRing ? (slots + 1) / 2 : kMaxRing;
   a.nv = slots - a.nk < kMaxRing ? slots - a.nk : kMaxRing;
   const size_t smem = static_cast<size_t>(a.nk + a.nv + 2) * slot + sizeof(Misc);
   CUtensorMap mq, mk, mv;
-  const long long gk = page_groups(a.ps, a.pages, kv.k_slot, kv.k_page);
-  const long long gv = page_groups(a.ps, a.pages, kv.v_slot, kv.v_page);
-  a.fold = D == 128 && gk == gv ? static_cast<int>(gk) : 0;
-  a.group = a.fold ? 2048 : 1024;
-  a.half = a.fold ? 1024 : kHalf;
-  const bool ok =
-      a.fold ? encode_groups(&mk, kv.k, dtype, a.ps, a.Hkv, a.pages, kv.k_slot, kv.k_head, gk, a.box) &&
-                   encode_groups(&mv, kv.v, dtype, a.ps, a.Hkv, a.pages, kv.v_slot, kv.v_head, gv, a.box)
-             : encode_rows(&mk, kv.k, dtype, D, a.ps, a.Hkv, a.pages, kv.k_slot, kv.k_head, kv.k_page, a.box) &&
-                   encode_rows(&mv, kv.v, dtype, D, a.ps, a.Hkv, a.pages, kv.v_slot, kv.v_head, kv.v_page, a.box);
-  if (!ok || !encode_queries(&mq, p, dtype, D, a.tq)) return cudaErrorInvalidValue;
+  if (!page_tiles(a, kv, dtype, D, &mk, &mv) || !encode_queries(&mq, p.q, p.q_b, p.q_n, p.q_h, p.Hq, p.nodes, p.G, dtype, D, a.tq))
+    return cudaErrorInvalidValue;
   int C = sm_count();
   if (C < 1) return cudaErrorInvalidDevice;
   C = C < kMaxCtas ? C : kMaxCtas;

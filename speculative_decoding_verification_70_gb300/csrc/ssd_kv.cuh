@@ -246,6 +246,7 @@ cudaError_t launch_kv_commit(const CommitParams& p, cudaStream_t s);
 cudaError_t launch_tree_attention(const AttnParams& p, int dtype, int D, cudaStream_t s);
 cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaStream_t s);
 size_t chunk_attention_bytes(int N, int G, int D);
+size_t kv_weights_bytes();
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, int D, cudaStream_t s);
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s);
 size_t tree_attention_bytes(int N, int G, int D);

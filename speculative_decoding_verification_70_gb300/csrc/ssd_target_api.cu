@@ -274,6 +274,8 @@ ssd_status ssd_chunk_attention(const ssd_paged_kv* kv, const ssd_draft_nodes* to
   return cuda_status(launch_chunk_attention(p, kv->dtype, kv->D, S(stream)));
 }
 
+size_t ssd_kv_weights_workspace_bytes(void) { return kv_weights_bytes(); }
+
 ssd_status ssd_kv_weights(const ssd_paged_kv* kv, const ssd_draft_nodes* tokens, int Hq, const void* q, int64_t q_b,
                           int64_t q_n, int64_t q_h, const float* lse, int window, int sinks, float scale, float decay,
                           float* weights, int64_t w_b, int64_t w_h, int w_len, void* ws, size_t ws_bytes,
@@ -289,7 +291,7 @@ ssd_status ssd_kv_weights(const ssd_paged_kv* kv, const ssd_draft_nodes* tokens,
   if (!stride_ok(q_b) || !stride_ok(q_n) || !stride_ok(q_h) || !aligned(q, 16)) return SSD_ERR_INVALID_ARG;
   if (w_len < 1 || w_b < w_len || w_h < w_len || w_b >= kMaxStride || w_h >= kMaxStride) return SSD_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(weights, 4) || !aligned(ws, 256)) return SSD_ERR_INVALID_ARG;
-  if (ws_bytes < SSD_ERRWORD_BYTES) return SSD_ERR_WORKSPACE;
+  if (ws_bytes < ssd_kv_weights_workspace_bytes()) return SSD_ERR_WORKSPACE;
   WeightsParams p;
   p.kv = view_of(*kv);
   p.nodes = view_of(*tokens);

@@ -1,0 +1,152 @@
+// ssd_tiles.cuh -- a paged cache as tiles of up to 128 slots for the tensor cores: where a
+// slot lies, copies of a tile, and the queries' copies.
+#pragma once
+
+#include "ssd_tc.cuh"
+
+namespace ssd {
+
+struct PageTiles {
+  const int* table;
+  long long table_stride;
+  int width, pages, ps;
+  int box, ppt, tk, tpp;   // rows of a TMA box, pages a tile, slots a tile, tiles a page
+  int fold;                // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
+  int group, half;         // bytes from 8 slots of a tile to the next, from half to half
+  int cover;               // rows of a tile that TMA writes
+  int holes;               // tiles have rows that are no slot, the same in each
+  int uneven;              // tiles that differ: pages above 128 slots whose last tile is not full
+};
+
+constexpr int kFar = 1 << 30;  // offset of a row that is no slot
+
+__device__ __forceinline__ int tile_of(const PageTiles& a, int slot) {
+  if (a.ps > kTile) return (slot / a.ps) * a.tpp + (slot % a.ps) / kTile;
+  return a.tk == kTile ? slot / kTile : slot / a.tk;
+}
+// First slot of tile t, and how many it holds.
+__device__ __forceinline__ void tile_slots(const PageTiles& a, int t, int& first, int& count) {
+  if (a.ps <= kTile) {
+    first = t * a.tk;
+    count = a.tk;
+  } else {
+    const int r = (t % a.tpp) * kTile;
+    first = (t / a.tpp) * a.ps + r;
+    count = min(kTile, a.ps - r);
+  }
+}
+
+// Offset of a tile's row from its first slot (pages above 128 slots: below the tile's count).
+__device__ __forceinline__ int row_offset(const PageTiles& a, int row) {
+  if (a.ps > kTile) return row;
+  const int p = row / a.box, r = row - p * a.box;
+  return p < a.ppt && r < a.ps ? p * a.ps + r : kFar;
+}
+
+__device__ __forceinline__ int seq_tokens(const PageTiles& a, const NodesView& nodes, int b, int& ctx, bool& bad) {
+  ctx = __ldg(nodes.ctx_len + b);
+  const int nn = nodes.n_nodes ? __ldg(nodes.n_nodes + b) : nodes.N;
+  return seq_nodes(ctx, nn, nodes.N, a.width, a.ps, bad);
+}
+
+// ---------------------------------------------------------------------------
+// copies
+// ---------------------------------------------------------------------------
+// A ring's next tile: whole pages, of which the seen ones come.
+struct Ring {
+  const CUtensorMap* map;
+  uint64_t *full, *empty;
+  uint32_t base;
+  int slots, slot;
+  uint32_t phase;
+};
+template <int D, class Misc>
+__device__ __forceinline__ bool load_tile(const PageTiles& a, Misc& sm, Ring& r, int t, int p0, int p1, int id, int h, int* err,
+                                          int withheld) {
+  constexpr int HALVES = D / 64, kSlotBytes = HALVES * kHalf;
+  const int lane = threadIdx.x & 31;
+  const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
+  const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.pages);
+  if (!good) id = a.pages;  // out of bounds: zeros
+  const int unit = a.fold ? id * a.fold + s0 / 8 : id;
+  if (++r.slot == r.slots) {
+    r.slot = 0;
+    r.phase ^= 1;
+  }
+  uint64_t* full = r.full + r.slot;
+  const bool ok = bar_wait(r.empty + r.slot, r.phase ^ 1, sm, err) && !*reinterpret_cast<volatile int*>(&sm.abort);
+  if (!__all_sync(0xffffffffu, ok)) return true;
+  if (lane == 0) bar_expect(full, (p1 - p0 + 1) * a.box * 128 * HALVES + withheld);
+  __syncwarp();
+  const uint32_t dst = r.base + r.slot * kSlotBytes;
+  // a lane a page
+  if (lane >= p0 && lane <= p1) {
+    if (D == 128 && a.fold) {
+      tma_groups(dst + lane * a.box * 256, r.map, unit, h, full);
+    } else {
+#pragma unroll
+      for (int d = 0; d < HALVES; ++d)
+        tma_rows(dst + lane * a.box * 128 + d * kHalf, r.map, d * 64, s0, h, unit, full);
+    }
+  }
+  __syncwarp();
+  return good || lane < p0 || lane > p1;
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+// The cache's tiles and its maps (mv may be null).
+inline bool page_tiles(PageTiles& a, const KvView& kv, int dtype, int D, CUtensorMap* mk, CUtensorMap* mv) {
+  a.table = kv.table;
+  a.table_stride = kv.table_stride;
+  a.width = kv.width; a.pages = kv.pages; a.ps = kv.ps;
+  // tiles: whole pages up to 128 slots; boxes of a multiple of 8 rows (the swizzle's
+  // period), what exceeds the page filled with zeros
+  if (a.ps <= kTile) {
+    a.box = (a.ps + 7) / 8 * 8;
+    a.ppt = kTile / a.box;
+    a.tk = a.ppt * a.ps;
+    a.tpp = 1;
+    a.cover = a.ppt * a.box;
+    a.holes = a.tk != kTile;
+    a.uneven = 0;
+  } else {
+    a.box = kTile;
+    a.ppt = 1;
+    a.tk = kTile;
+    a.tpp = (a.ps + kTile - 1) / kTile;
+    a.cover = kTile;
+    a.holes = 0;
+    a.uneven = a.ps % kTile != 0;
+  }
+  const long long gk = page_groups(a.ps, a.pages, kv.k_slot, kv.k_page);
+  const long long gv = mv ? page_groups(a.ps, a.pages, kv.v_slot, kv.v_page) : gk;
+  a.fold = D == 128 && gk == gv ? static_cast<int>(gk) : 0;
+  a.group = a.fold ? 2048 : 1024;
+  a.half = a.fold ? 1024 : kHalf;
+  const auto encode = [&](CUtensorMap* m, void* base, long long slot, long long head, long long page, long long groups) {
+    return a.fold ? encode_groups(m, base, dtype, a.ps, kv.Hkv, a.pages, slot, head, groups, a.box)
+                  : encode_rows(m, base, dtype, D, a.ps, kv.Hkv, a.pages, slot, head, page, a.box);
+  };
+  return encode(mk, kv.k, kv.k_slot, kv.k_head, kv.k_page, gk) &&
+         (!mv || encode(mv, kv.v, kv.v_slot, kv.v_head, kv.v_page, gv));
+}
+
+// {D, Hq, N, B}; boxes of 64 columns, G heads and tq tokens.
+inline bool encode_queries(CUtensorMap* m, const char* q, long long q_b, long long q_n, long long q_h, int Hq,
+                           const NodesView& nodes, int G, int dtype, int D, int tq) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(Hq),
+                              static_cast<cuuint64_t>(nodes.N), static_cast<cuuint64_t>(nodes.B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(q_h) * 2, static_cast<cuuint64_t>(q_n) * 2,
+                                 static_cast<cuuint64_t>(q_b) * 2};
+  const cuuint32_t bx[4] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tq), 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(m, map_type(dtype), 4, const_cast<char*>(q), dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace ssd

@@ -1,82 +1,702 @@
 // ssd_weights.cu -- attention weights added up for every slot of the paged cache:
 //     w[h, s] = decay w[h, s] + sum over (token, query head of the group) that see s
 //               of exp(c q k_s - lse).
-// A warp per (sequence, head, slot), a token at a time, lanes over the head's entries.
+//
+// With slots on the tensor cores' M axis and the group's (token, head) rows as columns,
+//     S^T = K Q^T   [128 slots, up to 128 rows]
+// a thread owns a slot: it reads its scores from tensor memory, adds 2^(c' s - lse') over
+// the columns in registers, and no sum crosses threads.  An item is two tiles of slots of
+// a (sequence, key/value head), kept in shared memory while the blocks of rows that see
+// them pass; a warpgroup a tile.  One persistent CTA per SM; the batch's blocks are
+// numbered and cut into equal ranges by the lengths on the device; an item that is cut
+// leaves its sums in the workspace, and weights_join_kernel adds them in range order.
+//
+// Warps of a CTA: 0 copies the blocks of Q, 2 the tiles of K, both by TMA into rings; 1
+// issues the products; 3 brings the columns' -lse; 4..11 two warpgroups for the sums.
 #include <math.h>
 
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"
+#include "ssd_tiles.cuh"
 
 namespace ssd {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kThreads = 384;
+constexpr int kRegsCopy = 88, kRegsSum = 208;  // 128 x 88 + 256 x 208 = 384 x 168
+constexpr int kMaxCtas = 160;
+constexpr int kMaxKeys = 8, kMaxQueries = 4, kBias = 4;  // slots of the rings
+constexpr float kLog2e = 1.4426950408889634f;
 
-template <class T, int D>
-__global__ void __launch_bounds__(32 * kWarps) weights_kernel(const __grid_constant__ WeightsParams p) {
-  constexpr int E = D / 64;
-  const int lane = threadIdx.x & 31;
-  const int s = blockIdx.x * kWarps + (threadIdx.x >> 5), h = blockIdx.y, N = p.nodes.N;
-  for (int b = blockIdx.z; b < p.nodes.B; b += gridDim.z) {
-    const int ctx = p.nodes.ctx_len[b], nn = p.nodes.n_nodes ? p.nodes.n_nodes[b] : N;
-    bool bad;
-    int n = seq_nodes(ctx, nn, N, p.kv.width, p.kv.ps, bad);
-    if (!bad && n > 0 && ctx + n > p.w_len) {
-      bad = true;
-      n = 0;
+// A CTA's range of blocks, for the joining kernel.
+struct alignas(16) Range {
+  long long lo;      // first block (its position in cost)
+  int t0, used;      // its place in its item; 0: a range without blocks
+  int b, p, h, T;    // its item, the item's blocks
+};
+
+struct Args : PageTiles {
+  NodesView nodes;
+  int Hq, Hkv, G;
+  int tq, cols;            // tokens and columns of a block
+  int NP;                  // pairs of tiles of the longest sequence
+  int window, sinks;
+  int item_cost;           // what an item's start and end cost, in blocks
+  int nk, nq;              // slots of the rings
+  float c;                 // |scale| * log2(e)
+  int negate, zero;
+  const float* lse;
+  float decay;
+  float* weights;
+  long long w_b, w_h;
+  int w_len;
+  float* part;             // [2 ctas][256]
+  Range* ranges;
+  unsigned long long per_cta;  // 2^64 / ctas, rounded up
+  int* err;
+  unsigned wait_us;
+  int withheld;
+};
+
+struct alignas(16) Misc {
+  alignas(16) float bias[kBias][kTile];  // -lse of the columns, in units of log 2
+  uint64_t kfull[kMaxKeys], kempty[kMaxKeys], qfull[kMaxQueries], qempty[kMaxQueries], bfull[kBias], bempty[kBias];
+  uint64_t sfull[2][2], sempty[2][2], done;
+  long long left;
+  int b0, p0, h0, t0, cost;
+  unsigned tmem;
+  int abort;
+  unsigned wait_us;
+  long long scan[2][kThreads / 32];
+};
+static_assert(sizeof(Misc) <= 3 * 1024, "shared memory beside the rings");
+
+__device__ __forceinline__ int tokens_of(const Args& a, int b, int& ctx, bool& bad) {
+  const int n = seq_tokens(a, a.nodes, b, ctx, bad);
+  if (n > 0 && ctx > a.w_len - n) bad = true;
+  return bad ? 0 : n;
+}
+
+// A pair of tiles: its slots, and the tokens ia .. ib - 1 that see some of them, in T
+// blocks.
+struct Item {
+  int tiles, first, last, ia, ib, T;
+};
+__device__ __forceinline__ Item item_of(const Args& a, int ctx, int n, int p) {
+  Item x;
+  int count;
+  tile_slots(a, 2 * p, x.first, count);
+  x.last = x.first + count - 1;
+  x.tiles = 1;
+  if (x.last < ctx + n - 1) {
+    int f;
+    tile_slots(a, 2 * p + 1, f, count);
+    x.last = f + count - 1;
+    x.tiles = 2;
+  }
+  x.last = min(x.last, ctx + n - 1);
+  x.ia = max(0, x.first - ctx);
+  x.ib = n;
+  if (a.window && x.first >= a.sinks)
+    x.ib = static_cast<int>(max(0ll, min(static_cast<long long>(n), static_cast<long long>(x.last) + a.window - ctx)));
+  x.T = x.ib > x.ia ? (x.ib - x.ia + a.tq - 1) / a.tq : 0;
+  return x;
+}
+// The pair behind p; behind one that nobody sees, the first that the window reaches.
+__device__ __forceinline__ int pair_after(const Args& a, int ctx, int p, int T) {
+  return T > 0 ? p + 1 : max(p + 1, tile_of(a, max(0, ctx - a.window + 1)) / 2);
+}
+__device__ __forceinline__ int pairs_of(const Args& a, int ctx, int n) {
+  return n > 0 ? tile_of(a, ctx + n - 1) / 2 + 1 : 0;
+}
+
+// The pieces of a CTA's range, one item after another.
+struct Pieces {
+  long long left;
+  int w, b, p, h, ctx, n, pairs;
+  Item k;
+  int t0, end;     // blocks t0 .. end - 1
+  bool fresh;
+  __device__ __forceinline__ void start(const Args& a, const Misc& sm) {
+    left = sm.left;
+    w = sm.cost;
+    b = sm.b0;
+    p = sm.p0;
+    h = sm.h0;
+    t0 = sm.t0;
+    fresh = true;
+    if (left > 0) {
+      bool bad;
+      n = tokens_of(a, b, ctx, bad);
+      pairs = pairs_of(a, ctx, n);
+      k = item_of(a, ctx, n, p);
     }
-    if (bad && s == 0 && h == 0 && lane == 0) atomicOr(p.err, kErrBadLength);
-    if (n == 0 || s >= ctx + n) continue;
-    int page, off;
-    const bool ok = kv_slot(p.kv.table + b * p.kv.table_stride, p.kv.width, p.kv.pages, p.kv.ps, s, page, off);
-    if (!ok && lane == 0) atomicOr(p.err, kErrBadPage);
-    const uint32_t* kr = reinterpret_cast<const uint32_t*>(
-                             p.kv.k + 2 * (page * p.kv.k_page + off * p.kv.k_slot + h * p.kv.k_head)) + lane * E;
-    float k[2 * E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const uint32_t w = ok ? kr[e] : 0u;
-      k[2 * e] = T::lo(w);
-      k[2 * e + 1] = T::hi(w);
-    }
-    float sum = 0.f;
-    for (int i = max(0, s - ctx); i < n; ++i) {
-      if (p.window && s >= p.sinks && s <= ctx + i - p.window) break;
-      for (int g = 0; g < p.G; ++g) {
-        const int hq = h * p.G + g;
-        const uint32_t* qr =
-            reinterpret_cast<const uint32_t*>(p.q + 2 * (b * p.q_b + i * p.q_n + hq * p.q_h)) + lane * E;
-        float x = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          x = fmaf(T::lo(qr[e]), k[2 * e], x);
-          x = fmaf(T::hi(qr[e]), k[2 * e + 1], x);
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        const float lse = p.lse[(static_cast<long long>(b) * N + i) * p.Hq + hq];
-        if (lse != -INFINITY) sum += expf((p.scale == 0.f ? 0.f : x * p.scale) - lse);
+  }
+  __device__ __forceinline__ bool direct() const { return t0 == 0 && end == k.T; }
+  __device__ __forceinline__ bool next(const Args& a) {
+    if (!fresh) {
+      left -= end - t0 + (end == k.T ? w : 0);
+      t0 = 0;
+      if (left > 0 && ++h == a.Hkv) {
+        h = 0;
+        do {
+          p = pair_after(a, ctx, p, k.T);
+          while (p >= pairs) {
+            if (++b >= a.nodes.B) {
+              left = 0;
+              return false;
+            }
+            bool bad;
+            n = tokens_of(a, b, ctx, bad);
+            pairs = pairs_of(a, ctx, n);
+            p = 0;
+          }
+          k = item_of(a, ctx, n, p);
+        } while (k.T == 0);
       }
     }
-    if (lane == 0) {
-      float* w = p.weights + b * p.w_b + h * p.w_h + s;
-      *w = p.decay == 0.f ? sum : fmaf(p.decay, *w, sum);
+    fresh = false;
+    if (left <= 0) return false;
+    end = static_cast<int>(min(static_cast<long long>(k.T), t0 + left));
+    return true;
+  }
+};
+
+// The (sequence, pair)s from number `at` on, up to number e; f(pair's item).
+template <class F>
+__device__ __forceinline__ void each_pair(const Args& a, long long at, long long e, F&& f) {
+  int ctx = 0, n = 0, pairs = 0, had = -1;
+#pragma unroll 1
+  while (at < e) {
+    const int b = static_cast<int>(at / a.NP), p = static_cast<int>(at - static_cast<long long>(b) * a.NP);
+    if (b != had) {
+      bool bad;
+      n = tokens_of(a, b, ctx, bad);
+      if (bad && p == 0 && blockIdx.x == 0) atomicOr(a.err, kErrBadLength);
+      pairs = pairs_of(a, ctx, n);
+      had = b;
     }
+    if (p >= pairs) {  // the next sequence
+      at += a.NP - p;
+      continue;
+    }
+    const Item k = item_of(a, ctx, n, p);
+    if (k.T > 0 && !f(b, p, k)) return;
+    at += min(pair_after(a, ctx, p, k.T), a.NP) - p;
   }
 }
 
-template <class T>
-cudaError_t launch_t(const WeightsParams& p, int D, cudaStream_t s) {
-  const dim3 grid((p.w_len + kWarps - 1) / kWarps, p.kv.Hkv, p.nodes.B < 65535 ? p.nodes.B : 65535);
-  if (D == 128) weights_kernel<T, 128><<<grid, 32 * kWarps, 0, s>>>(p);
-  else weights_kernel<T, 64><<<grid, 32 * kWarps, 0, s>>>(p);
-  return cudaGetLastError();
+__device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? ~0u : (1u << x) - 1; }
+
+// ---------------------------------------------------------------------------
+// sums: a warpgroup a tile, a thread a slot
+// ---------------------------------------------------------------------------
+template <bool MASKED>
+__device__ __forceinline__ float block_sum(const Args& a, uint32_t (&s)[4][32], const float* bias, int chunks, int lo,
+                                           int hi) {
+  const f32x2 c2 = pk2(a.c, a.c);
+  f32x2 sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j >= chunks) break;
+    if (MASKED) {
+      const uint32_t v = below(hi - 32 * j) & ~below(lo - 32 * j);
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (!(v & (1u << e))) s[j][e] = 0xff800000u;  // -inf
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const float4 m = *reinterpret_cast<const float4*>(bias + 32 * j + e);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float y0, y1;
+        up2(fma2(pk2(__uint_as_float(s[j][e + 2 * q]), __uint_as_float(s[j][e + 2 * q + 1])), c2,
+                 q ? pk2(m.z, m.w) : pk2(m.x, m.y)),
+            y0, y1);
+        sum[q] = add2(sum[q], pk2(ex2_fast(y0), ex2_fast(y1)));
+      }
+    }
+  }
+  float x, y;
+  up2(add2(sum[0], sum[1]), x, y);
+  return x + y;
+}
+
+__device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem, int w) {
+  const int wt = threadIdx.x & 127;
+  const uint32_t lanes = static_cast<uint32_t>(wt & 96) << 16;
+  const int off = row_offset(a, wt), chunks = a.cols / 32;
+  int jobs = 0, block = 0, item = -1;
+  Pieces pc;
+  pc.start(a, sm);
+#pragma unroll 1
+  while (pc.next(a)) {
+    ++item;
+    const bool mine = w < pc.k.tiles;
+    int first = 0, count = 0;
+    if (mine) tile_slots(a, 2 * pc.p + w, first, count);
+    const int slot = first + off;
+    const bool there = mine && off < count && slot < pc.ctx + pc.n;
+    float* at = a.weights + pc.b * a.w_b + pc.h * a.w_h + slot;
+    float old = 0.f;
+    if (there && pc.direct() && a.decay != 0.f) old = *at;  // (on its way during the sums)
+    // tokens that see the slot: from ts to te - 1
+    const int ts = slot - pc.ctx;
+    const int te = a.window && slot >= a.sinks
+                       ? static_cast<int>(min(static_cast<long long>(pc.k.ib), static_cast<long long>(ts) + a.window))
+                       : pc.k.ib;
+    float acc = 0.f;
+#pragma unroll 1
+    for (int t = pc.t0; t < pc.end; ++t, ++block) {
+      const int bs = block % kBias;
+      uint64_t* bempty = &sm.bempty[bs];
+      if (mine) {
+        const int buf = jobs & 1;
+        bar_wait(&sm.sfull[w][buf], (jobs >> 1) & 1, sm, a.err);
+        ++jobs;
+        tc_after();
+        const uint32_t tS = tmem + lanes + (2 * buf + w) * 128;
+        uint32_t s[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < chunks) tm_ld32(tS + 32 * j, s[j]);
+        tm_wait_loads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j < chunks) tm_tie32(s[j]);
+        tc_before();
+        bar_arrive(&sm.sempty[w][buf]);
+        const int i0 = pc.k.ia + t * a.tq, used = min(a.tq, pc.k.ib - i0);
+        int lo = min(max(ts - i0, 0), a.tq), hi = min(max(te - i0, 0), used);
+        if (!there) hi = 0;
+        bar_wait(&sm.bfull[bs], (block / kBias) & 1, sm, a.err);
+        // (columns that are no row, behind the block's, are masked like those that do not see it)
+        if (__all_sync(0xffffffffu, lo == 0 && hi * a.G == a.cols)) acc += block_sum<false>(a, s, sm.bias[bs], chunks, 0, 0);
+        else acc += block_sum<true>(a, s, sm.bias[bs], chunks, lo * a.G, hi * a.G);
+      } else {
+        bar_wait(&sm.bfull[bs], (block / kBias) & 1, sm, a.err);
+      }
+      bar_arrive(bempty);
+    }
+    if (!there) continue;
+    if (pc.direct()) *at = a.decay == 0.f ? acc : fmaf(a.decay, old, acc);
+    else a.part[(2 * blockIdx.x + (item == 0 ? 0 : 1)) * 256 + w * 128 + wt] = acc;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
+                   const __grid_constant__ Args a) {
+  extern __shared__ __align__(1024) char base[];
+  constexpr int HALVES = D / 64;
+  constexpr int kSlotBytes = HALVES * kHalf;
+  char* ring = base;
+  char* Q = ring + a.nk * kSlotBytes;
+  const int qhalf = a.cols * 128, qbytes = qhalf * HALVES;
+  Misc& sm = *reinterpret_cast<Misc*>(Q + a.nq * qbytes);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int C = gridDim.x, B = a.nodes.B;
+
+  if (tid == 0) {
+    for (int i = 0; i < kMaxKeys; ++i) {
+      bar_init(&sm.kfull[i], 1);
+      bar_init(&sm.kempty[i], 1);
+    }
+    for (int i = 0; i < kMaxQueries; ++i) {
+      bar_init(&sm.qfull[i], 1);
+      bar_init(&sm.qempty[i], 1);
+    }
+    for (int i = 0; i < kBias; ++i) {
+      bar_init(&sm.bfull[i], 1);
+      bar_init(&sm.bempty[i], 256);
+    }
+    for (int i = 0; i < 4; ++i) {
+      bar_init(&sm.sfull[i >> 1][i & 1], 1);
+      bar_init(&sm.sempty[i >> 1][i & 1], 128);
+    }
+    bar_init(&sm.done, 1);
+    sm.abort = 0;
+    sm.wait_us = a.wait_us;
+    sm.left = 0;
+    sm.b0 = sm.p0 = sm.h0 = sm.t0 = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sptr(&sm.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 0 && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapq));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&mapk));
+  }
+  // ---- this CTA's range ----
+  {
+    const long long all = static_cast<long long>(B) * a.NP, per = (all + kThreads - 1) / kThreads;
+    const long long f = tid * per, e = min(all, f + per);
+    long long mine = 0, pairs = 0;  // blocks of a head, and pairs that have some
+    each_pair(a, f, e, [&](int, int, const Item& k) {
+      mine += k.T;
+      ++pairs;
+      return true;
+    });
+    long long inc = mine, incp = pairs;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, inc, d), op = __shfl_up_sync(0xffffffffu, incp, d);
+      if (lane >= d) {
+        inc += o;
+        incp += op;
+      }
+    }
+    if (lane == 31) {
+      sm.scan[0][warp] = inc;
+      sm.scan[1][warp] = incp;
+    }
+    __syncthreads();
+    long long before = inc - mine, beforep = incp - pairs, blocks = 0, items = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) {
+      if (i < warp) {
+        before += sm.scan[0][i];
+        beforep += sm.scan[1][i];
+      }
+      blocks += sm.scan[0][i];
+      items += sm.scan[1][i];
+    }
+    const long long w = a.item_cost, W = (blocks + w * items) * a.Hkv;
+    const long long me = blockIdx.x, lo = __umul64hi(W * me, a.per_cta),
+                    hi = me + 1 == C ? W : static_cast<long long>(__umul64hi(W * (me + 1), a.per_cta));
+    long long p = (before + w * beforep) * a.Hkv;
+    const long long mine_cost = (mine + w * pairs) * a.Hkv;
+    if (tid == 0) {
+      a.ranges[me].used = 0;
+      sm.cost = static_cast<int>(w);
+    }
+    __syncthreads();
+    // the thread whose pairs hold the range's first block (lo may lie behind the blocks of
+    // the last item before them)
+    if (lo < p + mine_cost && hi > p && p - lo <= w) {
+      each_pair(a, f, e, [&](int b, int pair, const Item& k) {
+        const long long one = k.T + w, end = p + one * a.Hkv;
+        if (lo < end) {
+          const unsigned long long d = lo > p ? lo - p : 0;
+          int h = static_cast<int>(d / one);
+          int t0 = static_cast<int>(d - h * one);
+          if (t0 >= k.T) {  // behind the item's blocks: the next item
+            ++h;
+            t0 = 0;
+          }
+          const long long from = p + h * one + t0;  // cost position of the first block
+          if (h < a.Hkv) {
+            if (from < hi) {
+              Range r;
+              r.lo = from;
+              r.t0 = sm.t0 = t0;
+              r.used = 1;
+              r.b = sm.b0 = b;
+              r.p = sm.p0 = pair;
+              r.h = sm.h0 = h;
+              r.T = k.T;
+              a.ranges[me] = r;
+              sm.left = hi - from;
+            }
+            return false;
+          }
+        }
+        p = end;
+        return true;
+      });
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  pdl_trigger();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
+
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
+    sum_role(a, sm, tmem, (warp - 4) >> 2);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
+    Pieces pc;
+    pc.start(a, sm);
+    if (warp == 0) {
+      // ---- blocks of Q ----
+      int slot = -1;
+      uint32_t phase = 0;
+#pragma unroll 1
+      while (pc.next(a)) {
+#pragma unroll 1
+        for (int t = pc.t0; t < pc.end; ++t) {
+          if (++slot == a.nq) {
+            slot = 0;
+            phase ^= 1;
+          }
+          const bool ok = bar_wait(&sm.qempty[slot], phase ^ 1, sm, a.err) &&
+                          !*reinterpret_cast<volatile int*>(&sm.abort);
+          if (__all_sync(0xffffffffu, ok) && elect_one()) {
+            bar_expect(&sm.qfull[slot], HALVES * a.tq * a.G * 128 + a.withheld);
+            // (scale 0: behind the last token, zeros)
+            const int i0 = a.zero ? a.nodes.N : pc.k.ia + t * a.tq;
+            for (int d = 0; d < HALVES; ++d)
+              tma_rows(sptr(Q) + slot * qbytes + d * qhalf, &mapq, d * 64, pc.h * a.G, i0, pc.b, &sm.qfull[slot]);
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == 2) {
+      // ---- tiles of K ----
+      Ring rk = {&mapk, sm.kfull, sm.kempty, sptr(ring), a.nk, -1, 0};
+      bool bad_page = false;
+      // the pages of a tile that hold slots, and this lane's page id
+      auto lookup = [&](int t, int& p1) {
+        int first, count;
+        tile_slots(a, t, first, count);
+        p1 = a.ps <= kTile ? min(a.ppt - 1, (pc.ctx + pc.n - 1 - first) / a.ps) : 0;
+        if (lane > p1) return 0;
+        return __ldg(a.table + pc.b * a.table_stride + (a.ps <= kTile ? t * a.ppt + lane : t / a.tpp));
+      };
+#pragma unroll 1
+      while (pc.next(a)) {
+        int pl[2], id[2] = {0, 0};
+        id[0] = lookup(2 * pc.p, pl[0]);
+        if (pc.k.tiles == 2) id[1] = lookup(2 * pc.p + 1, pl[1]);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (w < pc.k.tiles) bad_page |= !load_tile<D>(a, sm, rk, 2 * pc.p + w, 0, pl[w], id[w], pc.h, a.err, a.withheld);
+      }
+      if (bad_page) atomicOr(a.err, kErrBadPage);
+    } else if (warp == 3) {
+      // ---- the columns' -lse ----
+      int block = 0;
+#pragma unroll 1
+      while (pc.next(a)) {
+#pragma unroll 1
+        for (int t = pc.t0; t < pc.end; ++t, ++block) {
+          const int bs = block % kBias, i0 = pc.k.ia + t * a.tq, rows = min(a.tq, pc.k.ib - i0) * a.G;
+          const float* lse = a.lse + (static_cast<long long>(pc.b) * a.nodes.N + i0) * a.Hq + pc.h * a.G;
+          float x[kTile / 32];
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k) {
+            const int r = lane + 32 * k, i = r / a.G;
+            x[k] = r < rows ? __ldg(lse + static_cast<long long>(i) * a.Hq + r - i * a.G) : -INFINITY;
+          }
+          bar_wait(&sm.bempty[bs], ((block / kBias) & 1) ^ 1, sm, a.err);
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k) sm.bias[bs][lane + 32 * k] = x[k] == -INFINITY ? -INFINITY : -x[k] * kLog2e;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm.bfull[bs]);
+        }
+      }
+    } else {
+      // ---- products ----
+      const uint32_t khalf = a.half / 16, id = instr<T>(a.cols, false, false, a.negate);
+      const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
+      int qslot = -1, kslot = -1, jobs[2] = {0, 0};
+      uint32_t qphase = 0, kphase = 0;
+#pragma unroll 1
+      while (pc.next(a)) {
+        int ks[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (w >= pc.k.tiles) continue;
+          if (++kslot == a.nk) {
+            kslot = 0;
+            kphase ^= 1;
+          }
+          ks[w] = kslot;
+          bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
+        }
+#pragma unroll 1
+        for (int t = pc.t0; t < pc.end; ++t) {
+          if (++qslot == a.nq) {
+            qslot = 0;
+            qphase ^= 1;
+          }
+          bar_wait(&sm.qfull[qslot], qphase, sm, a.err);
+          const uint64_t qd = qd0 + qslot * (qbytes / 16);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (w >= pc.k.tiles) continue;
+            const int buf = jobs[w] & 1;
+            bar_wait(&sm.sempty[w][buf], ((jobs[w] >> 1) & 1) ^ 1, sm, a.err);
+            ++jobs[w];
+            tc_after();
+            const uint64_t kd = kd0 + ks[w] * (kSlotBytes / 16);
+            if (elect_one()) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                tc_mma(tmem + (2 * buf + w) * 128, kd + (k / 4) * khalf + (k & 3) * 2,
+                       qd + (k / 4) * (qhalf / 16) + (k & 3) * 2, id, k > 0);
+              tc_commit(&sm.sfull[w][buf]);
+              if (w == pc.k.tiles - 1) tc_commit(&sm.qempty[qslot]);
+              if (t + 1 == pc.end) tc_commit(&sm.kempty[ks[w]]);
+            }
+            __syncwarp();
+          }
+        }
+      }
+      if (elect_one()) tc_commit(&sm.done);
+      __syncwarp();
+      bar_wait(&sm.done, 0, sm, a.err);
+    }
+  }
+  // ---- pairs of tiles that no token sees: their weights fade ----
+  if (a.decay != 1.f && a.window) {
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      int n = 0, ctx = 0;
+      bool bad;
+      if (b0 + lane < B) n = tokens_of(a, b0 + lane, ctx, bad);
+      unsigned some = __ballot_sync(0xffffffffu, n > 0 && ctx >= a.window);
+#pragma unroll 1
+      for (; some; some &= some - 1) {
+        const int j = __ffs(some) - 1, c = __shfl_sync(0xffffffffu, ctx, j);
+        // (a pair of which the window or the first tokens reach a part is an item)
+        const int p0 = a.sinks > 0 ? tile_of(a, min(a.sinks - 1, c)) / 2 + 1 : 0, p1 = tile_of(a, c - a.window + 1) / 2;
+        if (p0 >= p1) continue;
+        int from, to, count;
+        tile_slots(a, 2 * p0, from, count);
+        tile_slots(a, 2 * p1, to, count);
+        const long long m = static_cast<long long>(to - from) * a.Hkv;
+        for (long long i = blockIdx.x * static_cast<long long>(kThreads) + tid; i < m;
+             i += static_cast<long long>(C) * kThreads) {
+          const int h = static_cast<int>(i / (to - from));
+          float* at = a.weights + (b0 + j) * a.w_b + h * a.w_h + from + (i - static_cast<long long>(h) * (to - from));
+          *at = a.decay == 0.f ? 0.f : a.decay * *at;
+        }
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 0 && *reinterpret_cast<volatile int*>(&sm.abort)) {
+    // given up: let copies in flight land before the shared memory is freed
+    const unsigned long long t0 = now_ns();
+    while (now_ns() - t0 < 20000000ull) __nanosleep(100000);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// Adds the parts of the items that range borders cut, in range order.  blockIdx.x: a range
+// that starts inside an item; the first such range of an item does its work, a thread a slot.
+__global__ void __launch_bounds__(256) weights_join_kernel(const __grid_constant__ Args a, int C) {
+  const int c = blockIdx.x + 1, w = threadIdx.x >> 7, wt = threadIdx.x & 127;
+  pdl_wait();
+  const Range me = a.ranges[c];
+  if (!me.used || me.t0 == 0) return;
+  const long long s = me.lo - me.t0, e = s + me.T;
+  int pk = c - 1;
+  while (pk > 0 && !a.ranges[pk].used) --pk;
+  const long long before = a.ranges[pk].lo;
+  if (before > s) return;  // an earlier range's item
+  int ctx, first, count;
+  bool bad;
+  const int n = tokens_of(a, me.b, ctx, bad);
+  if (w >= item_of(a, ctx, n, me.p).tiles) return;
+  tile_slots(a, 2 * me.p + w, first, count);
+  const int off = row_offset(a, wt), slot = first + off;
+  if (off >= count || slot >= ctx + n) return;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int k = pk; k < C; ++k) {
+    if (k > pk) {
+      if (!a.ranges[k].used) continue;
+      if (a.ranges[k].lo >= e) break;
+    }
+    sum += a.part[(2 * k + (k == pk && before < s ? 1 : 0)) * 256 + threadIdx.x];
+  }
+  float* at = a.weights + me.b * a.w_b + me.h * a.w_h + slot;
+  *at = a.decay == 0.f ? sum : fmaf(a.decay, *at, sum);
+}
+
+struct Layout {
+  size_t ranges, part, total;
+};
+Layout layout() {
+  Layout L;
+  L.ranges = 256;
+  L.part = (L.ranges + sizeof(Range) * kMaxCtas + 255) / 256 * 256;
+  L.total = L.part + 4ull * 2 * kMaxCtas * 256;
+  return L;
+}
+
+template <class T, int D>
+cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const Args& a, int C, size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(weights_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  if (e != cudaSuccess) return e;
+  weights_kernel<T, D><<<C, kThreads, smem, s>>>(mq, mk, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || C < 2) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C - 1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, weights_join_kernel, a, C);
 }
 
 }  // namespace
 
+size_t kv_weights_bytes() { return layout().total; }
+
 cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, int D, cudaStream_t s) {
-  return dtype == Bf16::kId ? launch_t<Bf16>(p, D, s) : launch_t<F16>(p, D, s);
+  Args a;
+  a.nodes = p.nodes;
+  a.Hq = p.Hq; a.Hkv = p.kv.Hkv; a.G = p.G;
+  a.tq = kTile / p.G < p.nodes.N ? kTile / p.G : p.nodes.N;
+  a.cols = (a.tq * p.G + 31) / 32 * 32;
+  const long long most = static_cast<long long>(p.kv.width) * p.kv.ps;
+  a.window = p.window < most ? p.window : 0;  // (a window that no sequence exceeds is none)
+  a.sinks = a.window ? p.sinks : 0;
+  a.item_cost = 1;
+  a.zero = p.scale == 0.f;
+  a.c = a.zero ? 1.f : fabsf(p.scale) * kLog2e;
+  a.negate = p.scale < 0.f;
+  a.lse = p.lse; a.decay = p.decay;
+  a.weights = p.weights; a.w_b = p.w_b; a.w_h = p.w_h; a.w_len = p.w_len;
+  a.err = p.err;
+  a.wait_us = p.wait_us; a.withheld = p.withheld;
+  const Layout L = layout();
+  char* ws = reinterpret_cast<char*>(p.err);
+  a.ranges = reinterpret_cast<Range*>(ws + L.ranges);
+  a.part = reinterpret_cast<float*>(ws + L.part);
+  CUtensorMap mq, mk;
+  if (!page_tiles(a, p.kv, dtype, D, &mk, nullptr) ||
+      !encode_queries(&mq, p.q, p.q_b, p.q_n, p.q_h, p.Hq, p.nodes, p.G, dtype, D, a.tq))
+    return cudaErrorInvalidValue;
+  const long long slots = most < p.w_len ? most : p.w_len;
+  const long long tiles = a.ps <= kTile ? (slots + a.tk - 1) / a.tk : (slots / a.ps + 1) * a.tpp;
+  a.NP = static_cast<int>((tiles + 1) / 2);
+  // as many tiles of K as fit beside three or four blocks of Q
+  const size_t slot = static_cast<size_t>(D) * 2 * kTile, qslot = static_cast<size_t>(D) * 2 * a.cols;
+  a.nq = a.cols > 64 ? 3 : kMaxQueries;
+  const size_t left = kSmemMax - sizeof(Misc) - a.nq * qslot;
+  a.nk = static_cast<int>(left / slot < kMaxKeys ? left / slot : kMaxKeys);
+  const size_t smem = a.nk * slot + a.nq * qslot + sizeof(Misc);
+  int C = sm_count();
+  if (C < 1) return cudaErrorInvalidDevice;
+  C = C < kMaxCtas ? C : kMaxCtas;
+  a.per_cta = C > 1 ? ~0ull / C + 1 : 0;
+  const auto launch = dtype == Bf16::kId ? (D == 128 ? launch_t<Bf16, 128> : launch_t<Bf16, 64>)
+                                         : (D == 128 ? launch_t<F16, 128> : launch_t<F16, 64>);
+  return launch(mq, mk, a, C, smem, s);
 }
 
 }  // namespace ssd

@@ -24,7 +24,7 @@ def _attend(lib, kv=None, tokens=None, Hq=16, q=P, q_b=4 * 16 * 128, q_n=16 * 12
 
 
 def _sum(lib, kv=None, tokens=None, Hq=16, q=P, q_b=4 * 16 * 128, q_n=16 * 128, q_h=128, lse=P, window=5, sinks=1,
-         scale=0.1, decay=1.0, w=P, w_b=8 * 64, w_h=64, w_len=64, ws=P, n=256):
+         scale=0.1, decay=1.0, w=P, w_b=8 * 64, w_h=64, w_len=64, ws=P, n=1 << 40):
     return lib.ssd_kv_weights(kv or _kv(), tokens or _nodes(), Hq, q, q_b, q_n, q_h, lse, window, sinks, scale, decay, w,
                               w_b, w_h, w_len, ws, n, None)
 
@@ -71,7 +71,8 @@ def test_weights_refusals(lib):
                dict(w=P + 2), dict(w_len=0), dict(w_b=63), dict(w_h=63), dict(w_b=1 << 38), dict(ws=None),
                dict(ws=P + 64)):
         assert _sum(lib, **kw) == INVALID, kw
-    assert _sum(lib, n=255) == WORKSPACE
+    need = lib.ssd_kv_weights_workspace_bytes()
+    assert need >= 256 and _sum(lib, n=need - 1) == WORKSPACE
 
 
 @needs_no_gpu
