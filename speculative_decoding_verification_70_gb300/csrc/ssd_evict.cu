@@ -17,10 +17,9 @@ namespace {
 
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kPerLane = 16;                              // slots of a lane
-constexpr int kChunk = kPickThreads * kPerLane;           // slots of a CTA at a time
+constexpr int kPerLane = 16;                              // most slots of a lane
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 
 // Ordered as the weights are; NaN below all of them.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -58,24 +57,27 @@ __device__ __forceinline__ int far_int(uint32_t at) {
 
 // Exclusive sums of a and b over the CTA's warps (each given by its warp), and the totals.
 __device__ __forceinline__ void warps_before(PickSmem& sm, int& a, int& b, int& all_a, int& all_b) {
-  const int warp = threadIdx.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
+  if (lane == 0) {
     sm.warp[0][warp] = a;
     sm.warp[1][warp] = b;
   }
   __syncthreads();
-  a = b = all_a = all_b = 0;
+  int x = lane < kPickWarps ? sm.warp[0][lane] : 0, y = lane < kPickWarps ? sm.warp[1][lane] : 0;
 #pragma unroll
-  for (int i = 0; i < kPickWarps; ++i) {
-    const int x = sm.warp[0][i], y = sm.warp[1][i];
-    if (i < warp) {
-      a += x;
-      b += y;
+  for (int d = 1; d < kPickWarps; d <<= 1) {
+    const int ox = __shfl_up_sync(0xffffffffu, x, d), oy = __shfl_up_sync(0xffffffffu, y, d);
+    if (lane >= d) {
+      x += ox;
+      y += oy;
     }
-    all_a += x;
-    all_b += y;
   }
+  all_a = __shfl_sync(0xffffffffu, x, kPickWarps - 1);
+  all_b = __shfl_sync(0xffffffffu, y, kPickWarps - 1);
+  a = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
+  b = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
+  if (warp == 0) a = b = 0;
 }
 
 __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ EvictParams p, int cluster) {
@@ -99,20 +101,23 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
   // the slots that compete, how many of them stay, and this CTA's segment
   const int lo = p.sinks, hi = ctx - p.recent;
   int need = C - p.sinks - p.recent;
-  const int seg = ((ctx + cluster - 1) / cluster + 511) / 512 * 512;
+  const int seg = ((ctx + cluster - 1) / cluster + 31) / 32 * 32;
   const int s0 = min(ctx, rank * seg), s1 = min(ctx, s0 + seg);
-  const int chunks = max(1, (s1 - s0 + kChunk - 1) / kChunk);
-  // a warp's 512 slots of a chunk, 32 side by side
-  uint32_t key[kPerLane];
-  auto slot_of = [&](int chunk, int k) { return s0 + chunk * kChunk + warp * (32 * kPerLane) + k * 32 + lane; };
-  auto load = [&](int chunk) {
+  // slots of a lane at a time: all, or 16.  A warp's lie 32 side by side.
+  const int pl = min(kPerLane, max(1, (s1 - s0 + kPickThreads - 1) / kPickThreads));
+  const int chunk = pl * kPickThreads, chunks = max(1, (s1 - s0 + chunk - 1) / chunk);
+  uint32_t key[kPerLane], comp = 0;  // keys, and which of them compete
+  auto slot_of = [&](int c, int k) { return s0 + c * chunk + (warp * pl + k) * 32 + lane; };
+  auto load = [&](int c) {
+    comp = 0;
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
-      const int s = slot_of(chunk, k);
+      if (k >= pl) break;
+      const int s = slot_of(c, k);
       key[k] = s < s1 ? key_of(w[s]) : 0u;
+      comp |= static_cast<uint32_t>(s >= lo && s < hi && s < s1) << k;
     }
   };
-  auto competes = [&](int s) { return s >= lo && s < hi && s < s1; };
   load(0);
   uint32_t want = 0, known = 0;  // the last one's key as far as it is known
   if (need > 0) {  // (fewer than compete)
@@ -125,9 +130,11 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
       for (int c = 0; c < chunks; ++c) {
         if (chunks > 1) load(c);
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k)
-          if (competes(slot_of(c, k)) && (key[k] & known) == want)
+        for (int k = 0; k < kPerLane; ++k) {
+          if (k >= pl) break;
+          if (((comp >> k) & 1) && (key[k] & known) == want)
             atomicAdd(&sm.hist[(key[k] >> shift) & ((1 << bits) - 1)], 1);
+        }
       }
       if (cluster > 1) cluster_sync();
       else __syncthreads();
@@ -135,12 +142,19 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
       const int at = kBins - 4 - 4 * tid;
       int4 v = make_int4(0, 0, 0, 0);
       if (cluster > 1) {
-        for (int r = 0; r < cluster; ++r) {
-          const int4 x = far_int4(of_rank(&sm.hist[at], r));
-          v.x += x.x;
-          v.y += x.y;
-          v.z += x.z;
-          v.w += x.w;
+        // (eight loads on their way at a time)
+        for (int r0 = 0; r0 < cluster; r0 += 8) {
+          int4 x[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            x[r] = r0 + r < cluster ? far_int4(of_rank(&sm.hist[at], r0 + r)) : make_int4(0, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) {
+            v.x += x[r].x;
+            v.y += x[r].y;
+            v.z += x[r].z;
+            v.w += x[r].w;
+          }
         }
       } else {
         v = *reinterpret_cast<const int4*>(&sm.hist[at]);
@@ -178,25 +192,31 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
     }
   }
   const bool none = need == 0;
-  // what stays: outside the middle, above the last one's key, or equal and early enough
-  auto classes = [&](int c, int k, bool& stay, bool& equal) {
-    const int s = slot_of(c, k);
-    const bool middle = s >= lo && s < hi;
-    const uint32_t x = key[k] & known;
-    stay = s < s1 && (!middle || (!none && x > want));
-    equal = s < s1 && middle && !none && x == want;
+  // what stays of a lane's slots: outside the middle, or above the last one's key; and
+  // what is equal to it
+  uint32_t stays = 0, equals = 0;
+  auto classes = [&](int c) {
+    stays = equals = 0;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+      if (k >= pl) break;
+      const uint32_t x = key[k] & known;
+      stays |= static_cast<uint32_t>(x > want) << k;
+      equals |= static_cast<uint32_t>(x == want) << k;
+    }
+    if (none) stays = equals = 0;
+    // slots of the segment that do not compete
+    const int there = min(pl, max(0, (s1 - slot_of(c, 0) + 31) / 32));
+    stays = (stays & comp) | (((1u << there) - 1) & ~comp);
+    equals &= comp;
   };
   int gt = 0, eq = 0;  // of the segment, by warp
 #pragma unroll 1
   for (int c = 0; c < chunks; ++c) {
     if (chunks > 1) load(c);
-#pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      bool stay, equal;
-      classes(c, k, stay, equal);
-      gt += __popc(__ballot_sync(0xffffffffu, stay));
-      eq += __popc(__ballot_sync(0xffffffffu, equal));
-    }
+    classes(c);
+    gt += __reduce_add_sync(0xffffffffu, __popc(stays));
+    eq += __reduce_add_sync(0xffffffffu, __popc(equals));
   }
   int all_gt, all_eq, a = gt, e = eq;
   warps_before(sm, a, e, all_gt, all_eq);
@@ -218,16 +238,9 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
   for (int c = 0; c < chunks; ++c) {
     if (chunks > 1) {  // this chunk's counts of the warps before
       load(c);
-      gt = eq = 0;
-#pragma unroll
-      for (int k = 0; k < kPerLane; ++k) {
-        bool stay, equal;
-        classes(c, k, stay, equal);
-        gt += __popc(__ballot_sync(0xffffffffu, stay));
-        eq += __popc(__ballot_sync(0xffffffffu, equal));
-      }
-      a = gt;
-      e = eq;
+      classes(c);
+      a = __reduce_add_sync(0xffffffffu, __popc(stays));
+      e = __reduce_add_sync(0xffffffffu, __popc(equals));
       warps_before(sm, a, e, all_gt, all_eq);
     }
     // equal ones before this warp, and where it writes
@@ -236,8 +249,9 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
     const unsigned under = (1u << lane) - 1;
 #pragma unroll
     for (int k = 0; k < kPerLane; ++k) {
-      bool stay, equal;
-      classes(c, k, stay, equal);
+      if (k >= pl) break;
+      const bool equal = (equals >> k) & 1;
+      bool stay = (stays >> k) & 1;
       const unsigned em = __ballot_sync(0xffffffffu, equal);
       if (equal && eb + __popc(em & under) < need) stay = true;
       eb += __popc(em);
@@ -254,112 +268,110 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
 // moves
 // ---------------------------------------------------------------------------
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 512;  // most rows of a block
+constexpr int kMoveBytes = 32768;                // of a CTA's rows at a time
+constexpr int kMoveRows = kMoveBytes / 128;      // at most
 
 struct MoveSmem {
+  uint4 rows[2][kMoveBytes / 16];
   long long src[2][kMoveRows], dst[2][kMoveRows];  // bytes from the head's first entry; -1: nothing to move
 };
 
-// blockIdx.y: a group of K's columns, of V's, or the weights.  L lanes a row of 16 bytes
-// each, U rows in flight a thread.
-template <int U>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p, int groups,
-                                                                  int L) {
-  __shared__ MoveSmem sm;
-  const int tid = threadIdx.x, unit = blockIdx.x;
+// A cluster per (unit, K or V; or the weights), which takes its rows in rounds, a CTA
+// kMoveBytes of them: on their way into shared memory while the places of the next round
+// are found, and out again once every CTA of the cluster has its own, beside the next
+// round's loads (whose sources lie behind this round's targets).
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p, int cluster) {
+  extern __shared__ __align__(16) char dyn[];
+  MoveSmem& sm = *reinterpret_cast<MoveSmem*>(dyn);
+  const int tid = threadIdx.x, rank = blockIdx.x % cluster, unit = blockIdx.x / cluster;
   const int H = p.kv.Hkv, h = unit % H, b = unit / H % p.B, layer = unit / H / p.B;
   const int C = p.budget;
   pdl_wait();
   const int ctx = p.ctx_len[b];
+  // (all CTAs of a cluster take the same way)
   if (ctx < 0 || ctx > p.w_len || ctx > static_cast<long long>(p.kv.width) * p.kv.ps) return;
   const int* kept = p.kept + static_cast<long long>(unit) * C;
-  if (static_cast<int>(blockIdx.y) == 2 * groups) {
+  auto round_sync = [&]() {
+    if (cluster > 1) cluster_sync();
+    else __syncthreads();
+  };
+  if (blockIdx.y == 2) {
     // ---- weights ----
     const float* w = p.weights + layer * p.w_layer + b * p.w_b + h * p.w_h;
     float* wo = p.w_out + layer * p.wo_layer + b * p.wo_b + h * p.wo_h;
     const int n = min(ctx, C);
-    constexpr int V = 8;
-    for (int at = 0; at < n; at += V * kMoveThreads) {
+    constexpr int V = 4;
+#pragma unroll 1
+    for (int at = rank * V * kMoveThreads; at - rank * V * kMoveThreads < n; at += cluster * V * kMoveThreads) {
       float x[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int r = at + k * kMoveThreads + tid;
         x[k] = r < n ? w[kept[r]] : 0.f;
       }
-      __syncthreads();
+      round_sync();
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int r = at + k * kMoveThreads + tid;
         if (r < n) wo[r] = x[k];
       }
     }
-    for (int r = n + tid; r < p.w_len; r += kMoveThreads) wo[r] = 0.f;
+    for (int r = n + rank * kMoveThreads + tid; r < p.w_len; r += cluster * kMoveThreads) wo[r] = 0.f;
     return;
   }
   if (ctx <= C) return;
-  const bool isv = static_cast<int>(blockIdx.y) >= groups;
-  const int group = isv ? blockIdx.y - groups : blockIdx.y;
-  const int side = kMoveThreads / L, R = side * U;  // rows side by side, of a block
+  const bool isv = blockIdx.y == 1;
+  const int per = p.D / 8, rows = kMoveThreads * 8 / per;  // 16-byte pieces of a row; rows of a CTA and round
   const int* table = p.kv.table + b * p.kv.table_stride;
-  char* base = (isv ? p.kv.v + 2 * (layer * p.v_layer + h * p.kv.v_head)
-                    : p.kv.k + 2 * (layer * p.k_layer + h * p.kv.k_head)) + (group * L + tid % L) * 16;
+  char* base = isv ? p.kv.v + 2 * (layer * p.v_layer + h * p.kv.v_head) : p.kv.k + 2 * (layer * p.k_layer + h * p.kv.k_head);
   const long long pg = 2 * (isv ? p.kv.v_page : p.kv.k_page), sl = 2 * (isv ? p.kv.v_slot : p.kv.k_slot);
-  auto places = [&](int at, int buf) {
-    for (int i = tid; i < R; i += kMoveThreads) {
-      const int r = at + i;
-      long long from = -1, to = -1;
-      if (r < C) {
-        const int s = kept[r];
-        if (s != r) {
-          int sp, so, dp, d_o;
-          const bool x = kv_slot(table, p.kv.width, p.kv.pages, p.kv.ps, s, sp, so);
-          const bool y = kv_slot(table, p.kv.width, p.kv.pages, p.kv.ps, r, dp, d_o);
-          if (x && y) {
-            from = sp * pg + so * sl;
-            to = dp * pg + d_o * sl;
-          } else {
-            atomicOr(p.err, kErrBadPage);
-          }
-        }
+  auto places = [&](int round, int buf) {
+    if (tid >= rows) return;
+    const int r = (round * cluster + rank) * rows + tid;
+    long long from = -1, to = -1;
+    const int s = r < C ? kept[r] : r;
+    if (s != r) {
+      const int fp = table[s / p.kv.ps], tp = table[r / p.kv.ps];
+      if (static_cast<unsigned>(fp) < static_cast<unsigned>(p.kv.pages) &&
+          static_cast<unsigned>(tp) < static_cast<unsigned>(p.kv.pages)) {
+        from = fp * pg + s % p.kv.ps * sl;
+        to = tp * pg + r % p.kv.ps * sl;
+      } else {
+        atomicOr(p.err, kErrBadPage);
       }
-      sm.src[buf][i] = from;
-      sm.dst[buf][i] = to;
     }
+    sm.src[buf][tid] = from;
+    sm.dst[buf][tid] = to;
   };
-  const int row = tid / L;
-  uint4 x[2][U];
+  const int col = tid % per, row = tid / per, side = kMoveThreads / per;
   auto load = [&](int buf) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < 8; ++u) {
       const long long from = sm.src[buf][u * side + row];
-      if (from >= 0) x[buf][u] = *reinterpret_cast<const uint4*>(base + from);
+      if (from >= 0)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(
+                         __cvta_generic_to_shared(&sm.rows[buf][u * kMoveThreads + tid]))),
+                     "l"(base + from + col * 16)
+                     : "memory");
     }
   };
-  auto store = [&](int buf) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long to = sm.dst[buf][u * side + row];
-      if (to >= 0) *reinterpret_cast<uint4*>(base + to) = x[buf][u];
-    }
-  };
-  // (a block's sources lie behind the targets of the one before, so its loads may pass
-  // that one's stores)
+  const int rounds = (C + cluster * rows - 1) / (cluster * rows);
   places(0, 0);
   __syncthreads();
   load(0);
 #pragma unroll 1
-  for (int at = 0; at < C; at += 2 * R) {
-    places(at + R, 1);
-    __syncthreads();
-    load(1);
-    store(0);
-    if (at + R >= C) break;
+  for (int i = 0; i < rounds; ++i) {
+    const int buf = i & 1;
+    if (i + 1 < rounds) places(i + 1, buf ^ 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    round_sync();
+    if (i + 1 < rounds) load(buf ^ 1);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {  // (what this thread has brought)
+      const long long to = sm.dst[buf][u * side + row];
+      if (to >= 0) *reinterpret_cast<uint4*>(base + to + col * 16) = sm.rows[buf][u * kMoveThreads + tid];
+    }
     __syncthreads();  // (the places have been read)
-    places(at + 2 * R, 0);
-    __syncthreads();
-    load(0);
-    store(1);
-    __syncthreads();
   }
 }
 
@@ -370,6 +382,11 @@ cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s) {
   // a cluster as large as gives each SM two CTAs, with at least 2048 slots each
   int cluster = 1;
   while (cluster < kMaxCluster && units * cluster * 2 <= 2 * 152 && p.w_len / (2 * cluster) >= 2048) cluster *= 2;
+  if (cluster > 8) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(evict_pick_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * cluster);
   cfg.blockDim = dim3(kPickThreads);
@@ -382,17 +399,22 @@ cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_pick_kernel, p, cluster);
   if (e != cudaSuccess) return e;
-  // groups of columns (64 bytes at least) as give each SM two CTAs
-  int groups = 1;
-  while (units * 2 * groups < 2 * 152 && p.D * 2 / (2 * groups) >= 64) groups *= 2;
-  const int L = p.D / 8 / groups;
-  cfg.gridDim = dim3(units, 2 * groups + (p.w_out ? 1 : 0));
+  // clusters as large as give each SM three CTAs
+  int wide = 1;
+  while (wide < 8 && units * 2 * wide * 2 <= 3 * 152) wide *= 2;
+  const cudaError_t f = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(MoveSmem));
+  if (f != cudaSuccess) return f;
+  cfg.gridDim = dim3(units * wide, p.w_out ? 3 : 2);
   cfg.blockDim = dim3(kMoveThreads);
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  // (256 / L * U rows a block: 512 at most)
-  return L >= 4 ? cudaLaunchKernelEx(&cfg, evict_move_kernel<8>, p, groups, L)
-                : cudaLaunchKernelEx(&cfg, evict_move_kernel<4>, p, groups, L);
+  cfg.dynamicSmemBytes = sizeof(MoveSmem);
+  cudaLaunchAttribute both[2];
+  both[0] = at;
+  both[0].val.clusterDim.x = wide;
+  both[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  both[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = both;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, p, wide);
 }
 
 }  // namespace ssd
