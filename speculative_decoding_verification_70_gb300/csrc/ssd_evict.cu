@@ -15,11 +15,11 @@
 namespace ssd {
 namespace {
 
-constexpr int kPickThreads = 512;
-constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kEvictThreads = 512;
+constexpr int kWarps = kEvictThreads / 32;
 constexpr int kPerLane = 16;                              // most slots of a lane
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 8;
 
 // Ordered as the weights are; NaN below all of them.
 __device__ __forceinline__ uint32_t key_of(float w) {
@@ -29,8 +29,8 @@ __device__ __forceinline__ uint32_t key_of(float w) {
 }
 
 struct PickSmem {
-  alignas(16) int hist[kBins];
-  int warp[2][kPickWarps];
+  alignas(16) int hist[kBins], tot[kBins];  // of the CTA; of the cluster (a share of the bins a CTA)
+  int warp[2][kWarps];
   int count[2];       // of the segment: those that stay whatever equal ones do, and equal ones
   int bin, above, in_bin;
 };
@@ -64,26 +64,25 @@ __device__ __forceinline__ void warps_before(PickSmem& sm, int& a, int& b, int& 
     sm.warp[1][warp] = b;
   }
   __syncthreads();
-  int x = lane < kPickWarps ? sm.warp[0][lane] : 0, y = lane < kPickWarps ? sm.warp[1][lane] : 0;
+  int x = lane < kWarps ? sm.warp[0][lane] : 0, y = lane < kWarps ? sm.warp[1][lane] : 0;
 #pragma unroll
-  for (int d = 1; d < kPickWarps; d <<= 1) {
+  for (int d = 1; d < kWarps; d <<= 1) {
     const int ox = __shfl_up_sync(0xffffffffu, x, d), oy = __shfl_up_sync(0xffffffffu, y, d);
     if (lane >= d) {
       x += ox;
       y += oy;
     }
   }
-  all_a = __shfl_sync(0xffffffffu, x, kPickWarps - 1);
-  all_b = __shfl_sync(0xffffffffu, y, kPickWarps - 1);
+  all_a = __shfl_sync(0xffffffffu, x, kWarps - 1);
+  all_b = __shfl_sync(0xffffffffu, y, kWarps - 1);
   a = __shfl_sync(0xffffffffu, x, (warp + 31) & 31);
   b = __shfl_sync(0xffffffffu, y, (warp + 31) & 31);
   if (warp == 0) a = b = 0;
 }
 
-__global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ EvictParams p, int cluster) {
-  __shared__ PickSmem sm;
+// By all threads of a cluster; the CTA is number `rank` of it.
+__device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int unit, int rank, int cluster) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = blockIdx.x % cluster, unit = blockIdx.x / cluster;
   const int H = p.kv.Hkv, h = unit % H, b = unit / H % p.B, layer = unit / H / p.B;
   const int ctx = p.ctx_len[b], C = p.budget;
   const bool bad = ctx < 0 || ctx > p.w_len || ctx > static_cast<long long>(p.kv.width) * p.kv.ps;
@@ -94,7 +93,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
   }
   // (all CTAs of a cluster take the same way)
   if (bad || ctx <= C) {
-    for (int r = rank * kPickThreads + tid; r < C; r += cluster * kPickThreads) kept[r] = !bad && r < ctx ? r : -1;
+    for (int r = rank * kEvictThreads + tid; r < C; r += cluster * kEvictThreads) kept[r] = !bad && r < ctx ? r : -1;
     return;
   }
   const float* w = p.weights + layer * p.w_layer + b * p.w_b + h * p.w_h;
@@ -104,19 +103,21 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
   const int seg = ((ctx + cluster - 1) / cluster + 31) / 32 * 32;
   const int s0 = min(ctx, rank * seg), s1 = min(ctx, s0 + seg);
   // slots of a lane at a time: all, or 16.  A warp's lie 32 side by side.
-  const int pl = min(kPerLane, max(1, (s1 - s0 + kPickThreads - 1) / kPickThreads));
-  const int chunk = pl * kPickThreads, chunks = max(1, (s1 - s0 + chunk - 1) / chunk);
+  const int pl = min(kPerLane, max(1, (s1 - s0 + kEvictThreads - 1) / kEvictThreads));
+  const int chunk = pl * kEvictThreads, chunks = max(1, (s1 - s0 + chunk - 1) / chunk);
   uint32_t key[kPerLane], comp = 0;  // keys, and which of them compete
   auto slot_of = [&](int c, int k) { return s0 + c * chunk + (warp * pl + k) * 32 + lane; };
   auto load = [&](int c) {
-    comp = 0;
+    // (without a branch, so that all loads are on their way at once)
+    const int first = slot_of(c, 0), count = min(pl, (s1 - first + 31) / 32);
+    float x[kPerLane];
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
-      if (k >= pl) break;
-      const int s = slot_of(c, k);
-      key[k] = s < s1 ? key_of(w[s]) : 0u;
-      comp |= static_cast<uint32_t>(s >= lo && s < hi && s < s1) << k;
-    }
+    for (int k = 0; k < kPerLane; ++k) x[k] = k < count ? w[first + 32 * k] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) key[k] = key_of(x[k]);
+    // those from lo to hi - 1
+    const int from = min(max((lo - first + 31) >> 5, 0), 31), to = min(max((min(hi, s1) - first + 31) >> 5, 0), pl);
+    comp = ((1u << to) - 1) & ~((1u << from) - 1);
   };
   load(0);
   uint32_t want = 0, known = 0;  // the last one's key as far as it is known
@@ -138,24 +139,21 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
       }
       if (cluster > 1) cluster_sync();
       else __syncthreads();
-      // bins from the heaviest on, four a thread
+      // bins from the heaviest on, four a thread.  (A cluster's CTAs add up a share of the
+      // bins each: with every CTA reading all histograms, 16 of 8 KB took 13 us.)
       const int at = kBins - 4 - 4 * tid;
-      int4 v = make_int4(0, 0, 0, 0);
+      int4 v;
       if (cluster > 1) {
-        // (eight loads on their way at a time)
-        for (int r0 = 0; r0 < cluster; r0 += 8) {
-          int4 x[8];
+        const int share = kBins / cluster;
+        if (tid < share) {
+          int x = 0;
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            x[r] = r0 + r < cluster ? far_int4(of_rank(&sm.hist[at], r0 + r)) : make_int4(0, 0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            v.x += x[r].x;
-            v.y += x[r].y;
-            v.z += x[r].z;
-            v.w += x[r].w;
-          }
+          for (int r = 0; r < kMaxCluster; ++r)
+            if (r < cluster) x += far_int(of_rank(&sm.hist[rank * share + tid], r));
+          sm.tot[rank * share + tid] = x;
         }
+        cluster_sync();
+        v = far_int4(of_rank(&sm.tot[at], at / share));
       } else {
         v = *reinterpret_cast<const int4*>(&sm.hist[at]);
       }
@@ -186,8 +184,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
       known |= ((1u << bits) - 1) << shift;
       need -= sm.above;  // those of the bin that stay
       const bool done = need == sm.in_bin;
-      if (cluster > 1) cluster_sync();  // (the histograms have been read)
-      else __syncthreads();
+      __syncthreads();
       if (done) break;
     }
   }
@@ -226,7 +223,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
       sm.count[0] = all_gt;
       sm.count[1] = all_eq;
     }
-    cluster_sync();
+    cluster_sync();  // (and the histograms' sums have been read)
     for (int r = 0; r < rank; ++r) {
       const int g = far_int(of_rank(&sm.count[0], r)), q = far_int(of_rank(&sm.count[1], r));
       out += g + min(max(need - equal_before, 0), q);
@@ -267,8 +264,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 // moves
 // ---------------------------------------------------------------------------
-constexpr int kMoveThreads = 256;
-constexpr int kMoveBytes = 32768;                // of a CTA's rows at a time
+constexpr int kMoveBytes = 49152;                // of a CTA's rows at a time
 constexpr int kMoveRows = kMoveBytes / 128;      // at most
 
 struct MoveSmem {
@@ -280,48 +276,51 @@ struct MoveSmem {
 // kMoveBytes of them: on their way into shared memory while the places of the next round
 // are found, and out again once every CTA of the cluster has its own, beside the next
 // round's loads (whose sources lie behind this round's targets).
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p, int cluster) {
-  extern __shared__ __align__(16) char dyn[];
-  MoveSmem& sm = *reinterpret_cast<MoveSmem*>(dyn);
-  const int tid = threadIdx.x, rank = blockIdx.x % cluster, unit = blockIdx.x / cluster;
-  const int H = p.kv.Hkv, h = unit % H, b = unit / H % p.B, layer = unit / H / p.B;
-  const int C = p.budget;
-  pdl_wait();
+__device__ __forceinline__ void round_sync(int cluster) {
+  if (cluster > 1) cluster_sync();
+  else __syncthreads();
+}
+
+__device__ __forceinline__ bool in_range(const EvictParams& p, int ctx) {
+  return ctx >= 0 && ctx <= p.w_len && ctx <= static_cast<long long>(p.kv.width) * p.kv.ps;
+}
+
+__device__ __forceinline__ void move_weights(const EvictParams& p, int unit, int rank, int cluster) {
+  const int tid = threadIdx.x, H = p.kv.Hkv, h = unit % H, b = unit / H % p.B, layer = unit / H / p.B, C = p.budget;
   const int ctx = p.ctx_len[b];
-  // (all CTAs of a cluster take the same way)
-  if (ctx < 0 || ctx > p.w_len || ctx > static_cast<long long>(p.kv.width) * p.kv.ps) return;
+  if (!in_range(p, ctx)) return;
   const int* kept = p.kept + static_cast<long long>(unit) * C;
-  auto round_sync = [&]() {
-    if (cluster > 1) cluster_sync();
-    else __syncthreads();
-  };
-  if (blockIdx.y == 2) {
-    // ---- weights ----
+  {
     const float* w = p.weights + layer * p.w_layer + b * p.w_b + h * p.w_h;
     float* wo = p.w_out + layer * p.wo_layer + b * p.wo_b + h * p.wo_h;
     const int n = min(ctx, C);
     constexpr int V = 4;
 #pragma unroll 1
-    for (int at = rank * V * kMoveThreads; at - rank * V * kMoveThreads < n; at += cluster * V * kMoveThreads) {
+    for (int at = rank * V * kEvictThreads; at - rank * V * kEvictThreads < n; at += cluster * V * kEvictThreads) {
       float x[V];
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const int r = at + k * kMoveThreads + tid;
+        const int r = at + k * kEvictThreads + tid;
         x[k] = r < n ? w[kept[r]] : 0.f;
       }
-      round_sync();
+      round_sync(cluster);
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const int r = at + k * kMoveThreads + tid;
+        const int r = at + k * kEvictThreads + tid;
         if (r < n) wo[r] = x[k];
       }
     }
-    for (int r = n + rank * kMoveThreads + tid; r < p.w_len; r += cluster * kMoveThreads) wo[r] = 0.f;
-    return;
+    for (int r = n + rank * kEvictThreads + tid; r < p.w_len; r += cluster * kEvictThreads) wo[r] = 0.f;
   }
-  if (ctx <= C) return;
-  const bool isv = blockIdx.y == 1;
-  const int per = p.D / 8, rows = kMoveThreads * 8 / per;  // 16-byte pieces of a row; rows of a CTA and round
+}
+
+__device__ __forceinline__ void move_rows(const EvictParams& p, MoveSmem& sm, int unit, int rank, int cluster, bool isv) {
+  constexpr int U = kMoveBytes / 16 / kEvictThreads;
+  const int tid = threadIdx.x, H = p.kv.Hkv, h = unit % H, b = unit / H % p.B, layer = unit / H / p.B, C = p.budget;
+  const int ctx = p.ctx_len[b];
+  if (!in_range(p, ctx) || ctx <= C) return;
+  const int* kept = p.kept + static_cast<long long>(unit) * C;
+  const int per = p.D / 8, rows = kEvictThreads * U / per;  // 16-byte pieces of a row; rows of a CTA and round
   const int* table = p.kv.table + b * p.kv.table_stride;
   char* base = isv ? p.kv.v + 2 * (layer * p.v_layer + h * p.kv.v_head) : p.kv.k + 2 * (layer * p.k_layer + h * p.kv.k_head);
   const long long pg = 2 * (isv ? p.kv.v_page : p.kv.k_page), sl = 2 * (isv ? p.kv.v_slot : p.kv.k_slot);
@@ -343,19 +342,20 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     sm.src[buf][tid] = from;
     sm.dst[buf][tid] = to;
   };
-  const int col = tid % per, row = tid / per, side = kMoveThreads / per;
+  const int col = tid % per, row = tid / per, side = kEvictThreads / per;
   auto load = [&](int buf) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < U; ++u) {
       const long long from = sm.src[buf][u * side + row];
       if (from >= 0)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(
-                         __cvta_generic_to_shared(&sm.rows[buf][u * kMoveThreads + tid]))),
+                         __cvta_generic_to_shared(&sm.rows[buf][u * kEvictThreads + tid]))),
                      "l"(base + from + col * 16)
                      : "memory");
     }
   };
   const int rounds = (C + cluster * rows - 1) / (cluster * rows);
+  __syncthreads();
   places(0, 0);
   __syncthreads();
   load(0);
@@ -364,55 +364,76 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int buf = i & 1;
     if (i + 1 < rounds) places(i + 1, buf ^ 1);
     asm volatile("cp.async.wait_all;" ::: "memory");
-    round_sync();
+    round_sync(cluster);
     if (i + 1 < rounds) load(buf ^ 1);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {  // (what this thread has brought)
+    for (int u = 0; u < U; ++u) {  // (what this thread has brought)
       const long long to = sm.dst[buf][u * side + row];
-      if (to >= 0) *reinterpret_cast<uint4*>(base + to + col * 16) = sm.rows[buf][u * kMoveThreads + tid];
+      if (to >= 0) *reinterpret_cast<uint4*>(base + to + col * 16) = sm.rows[buf][u * kEvictThreads + tid];
     }
     __syncthreads();  // (the places have been read)
   }
+}
+
+// Few units: clusters that pick, then clusters that move (blockIdx.y: K, V, the weights).
+__global__ void __launch_bounds__(kEvictThreads) evict_pick_kernel(const __grid_constant__ EvictParams p, int cluster) {
+  __shared__ PickSmem sm;
+  pick(p, sm, blockIdx.x / cluster, blockIdx.x % cluster, cluster);
+}
+__global__ void __launch_bounds__(kEvictThreads) evict_move_kernel(const __grid_constant__ EvictParams p, int cluster) {
+  extern __shared__ __align__(16) char dyn[];
+  const int unit = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+  pdl_wait();
+  if (blockIdx.y == 2) move_weights(p, unit, rank, cluster);
+  else move_rows(p, *reinterpret_cast<MoveSmem*>(dyn), unit, rank, cluster, blockIdx.y == 1);
+}
+// Many units: a CTA each, so that one's choice runs beside others' moves.
+__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ __align__(16) char dyn[];
+  MoveSmem& sm = *reinterpret_cast<MoveSmem*>(dyn);
+  pick(p, *reinterpret_cast<PickSmem*>(dyn), blockIdx.x, 0, 1);
+  __syncthreads();
+  move_rows(p, sm, blockIdx.x, 0, 1, false);
+  move_rows(p, sm, blockIdx.x, 0, 1, true);
+  if (p.w_out) move_weights(p, blockIdx.x, 0, 1);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s) {
   const unsigned units = static_cast<unsigned>(p.layers) * p.B * p.kv.Hkv;
-  // a cluster as large as gives each SM two CTAs, with at least 2048 slots each
+  // (both ways at 304 units of 4096 slots, measured below)
+  const bool many = units > 152;
+  const void* big = many ? reinterpret_cast<const void*>(evict_kernel) : reinterpret_cast<const void*>(evict_move_kernel);
+  cudaError_t e = cudaFuncSetAttribute(big, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(MoveSmem));
+  if (e != cudaSuccess) return e;
+  if (many) {
+    evict_kernel<<<units, kEvictThreads, sizeof(MoveSmem), s>>>(p);
+    return cudaGetLastError();
+  }
+  // clusters as large as give each SM a CTA, with at least 2048 slots each
   int cluster = 1;
   while (cluster < kMaxCluster && units * cluster * 2 <= 2 * 152 && p.w_len / (2 * cluster) >= 2048) cluster *= 2;
-  if (cluster > 8) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(evict_pick_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(units * cluster);
-  cfg.blockDim = dim3(kPickThreads);
+  cfg.blockDim = dim3(kEvictThreads);
   cfg.stream = s;
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = cluster;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_pick_kernel, p, cluster);
+  e = cudaLaunchKernelEx(&cfg, evict_pick_kernel, p, cluster);
   if (e != cudaSuccess) return e;
-  // clusters as large as give each SM three CTAs
+  // and as give each SM two of those that move
   int wide = 1;
-  while (wide < 8 && units * 2 * wide * 2 <= 3 * 152) wide *= 2;
-  const cudaError_t f = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(MoveSmem));
-  if (f != cudaSuccess) return f;
+  while (wide < kMaxCluster && units * 2 * wide * 2 <= 2 * 152) wide *= 2;
   cfg.gridDim = dim3(units * wide, p.w_out ? 3 : 2);
-  cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = sizeof(MoveSmem);
-  cudaLaunchAttribute both[2];
-  both[0] = at;
-  both[0].val.clusterDim.x = wide;
-  both[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  both[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = both;
+  at[0].val.clusterDim.x = wide;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, evict_move_kernel, p, wide);
 }
