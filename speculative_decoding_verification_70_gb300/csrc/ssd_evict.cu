@@ -264,7 +264,7 @@ __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int uni
 // ---------------------------------------------------------------------------
 // moves
 // ---------------------------------------------------------------------------
-constexpr int kMoveBytes = 49152;                // of a CTA's rows at a time
+constexpr int kMoveBytes = 32768;                // of a CTA's rows at a time
 constexpr int kMoveRows = kMoveBytes / 128;      // at most
 
 struct MoveSmem {
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_move_kernel(const __grid_
   else move_rows(p, *reinterpret_cast<MoveSmem*>(dyn), unit, rank, cluster, blockIdx.y == 1);
 }
 // Many units: a CTA each, so that one's choice runs beside others' moves.
-__global__ void __launch_bounds__(kEvictThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) char dyn[];
   MoveSmem& sm = *reinterpret_cast<MoveSmem*>(dyn);
   pick(p, *reinterpret_cast<PickSmem*>(dyn), blockIdx.x, 0, 1);
