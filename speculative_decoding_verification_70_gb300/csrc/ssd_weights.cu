@@ -7,12 +7,13 @@
 // a thread owns a slot: it reads its scores from tensor memory, adds 2^(c' s - lse') over
 // the columns in registers, and no sum crosses threads.  An item is two tiles of slots of
 // a (sequence, key/value head), kept in shared memory while the blocks of rows that see
-// them pass; a warpgroup a tile.  One persistent CTA per SM; the batch's blocks are
+// them pass.  One persistent CTA per SM; the batch's blocks are
 // numbered and cut into equal ranges by the lengths on the device; an item that is cut
 // leaves its sums in the workspace, and weights_join_kernel adds them in range order.
 //
 // Warps of a CTA: 0 copies the blocks of Q, 2 the tiles of K, both by TMA into rings; 1
-// issues the products; 3 brings the columns' -lse; 4..11 two warpgroups for the sums.
+// issues the products; 3 brings the columns' -lse; 4..19 four warpgroups for the sums, two
+// a tile, which take its blocks in turn.
 #include <math.h>
 
 #include "ssd_device.cuh"
@@ -22,8 +23,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsCopy = 88, kRegsSum = 208;  // 128 x 88 + 256 x 208 = 384 x 168
+constexpr int kSumThreads = 640;
 constexpr int kMaxCtas = 160;
 constexpr int kMaxKeys = 8, kMaxQueries = 4, kBias = 4;  // slots of the rings
 constexpr float kLog2e = 1.4426950408889634f;
@@ -67,9 +67,10 @@ struct alignas(16) Misc {
   unsigned tmem;
   int abort;
   unsigned wait_us;
-  long long scan[2][kThreads / 32];
+  long long scan[2][kSumThreads / 32];
+  float other[2][kTile];      // sums of the warpgroups that do not lead
 };
-static_assert(sizeof(Misc) <= 3 * 1024, "shared memory beside the rings");
+static_assert(sizeof(Misc) <= 4 * 1024, "shared memory beside the rings");
 
 __device__ __forceinline__ int tokens_of(const Args& a, int b, int& ctx, bool& bad) {
   const int n = seq_tokens(a, a.nodes, b, ctx, bad);
@@ -191,43 +192,58 @@ __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 
 // ---------------------------------------------------------------------------
 // sums: a warpgroup a tile, a thread a slot
 // ---------------------------------------------------------------------------
+// 16 columns' sum.
 template <bool MASKED>
-__device__ __forceinline__ float block_sum(const Args& a, uint32_t (&s)[4][32], const float* bias, int chunks, int lo,
-                                           int hi) {
+__device__ __forceinline__ void add_columns(f32x2 c2, uint32_t (&s)[16], const float* bias, uint32_t seen, f32x2 (&sum)[2]) {
+  if (MASKED) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (!(seen & (1u << e))) s[e] = 0xff800000u;  // -inf
+  }
+#pragma unroll
+  for (int e = 0; e < 16; e += 4) {
+    const float4 m = *reinterpret_cast<const float4*>(bias + e);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float y0, y1;
+      up2(fma2(pk2(__uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1])), c2, q ? pk2(m.z, m.w) : pk2(m.x, m.y)),
+          y0, y1);
+      sum[q] = add2(sum[q], pk2(ex2_fast(y0), ex2_fast(y1)));
+    }
+  }
+}
+
+// A block's columns, 16 at a time, the next ones on their way meanwhile.
+template <bool MASKED, class Read>
+__device__ __forceinline__ float block_sum(const Args& a, uint32_t tS, const float* bias, int lo, int hi, Read&& read) {
   const f32x2 c2 = pk2(a.c, a.c);
   f32x2 sum[2] = {0ull, 0ull};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j >= chunks) break;
-    if (MASKED) {
-      const uint32_t v = below(hi - 32 * j) & ~below(lo - 32 * j);
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (!(v & (1u << e))) s[j][e] = 0xff800000u;  // -inf
-    }
-#pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-      const float4 m = *reinterpret_cast<const float4*>(bias + 32 * j + e);
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        float y0, y1;
-        up2(fma2(pk2(__uint_as_float(s[j][e + 2 * q]), __uint_as_float(s[j][e + 2 * q + 1])), c2,
-                 q ? pk2(m.z, m.w) : pk2(m.x, m.y)),
-            y0, y1);
-        sum[q] = add2(sum[q], pk2(ex2_fast(y0), ex2_fast(y1)));
-      }
-    }
+  uint32_t s0[16], s1[16];
+  tm_get16(tS, s0);
+#pragma unroll 1
+  for (int j = 0; j < a.cols; j += 32) {
+    tm_wait_loads();
+    tm_tie16(s0);
+    tm_get16(tS + j + 16, s1);
+    add_columns<MASKED>(c2, s0, bias + j, below(hi - j) & ~below(lo - j), sum);
+    tm_wait_loads();
+    tm_tie16(s1);
+    if (j + 32 < a.cols) tm_get16(tS + j + 32, s0);
+    else read();
+    add_columns<MASKED>(c2, s1, bias + j + 16, below(hi - j - 16) & ~below(lo - j - 16), sum);
   }
   float x, y;
   up2(add2(sum[0], sum[1]), x, y);
   return x + y;
 }
 
-__device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem, int w) {
+// Warpgroup `half` of the two of tile w of each item takes every second block.
+__device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem, int w, int half) {
   const int wt = threadIdx.x & 127;
-  const uint32_t lanes = static_cast<uint32_t>(wt & 96) << 16;
-  const int off = row_offset(a, wt), chunks = a.cols / 32;
-  int jobs = 0, block = 0, item = -1;
+  const uint32_t tS = tmem + (static_cast<uint32_t>(wt & 96) << 16) + (2 * half + w) * 128;
+  const int off = row_offset(a, wt);
+  int block = 0, item = -1;
+  uint32_t ph = 0;  // phase of sfull
   Pieces pc;
   pc.start(a, sm);
 #pragma unroll 1
@@ -238,9 +254,11 @@ __device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem,
     if (mine) tile_slots(a, 2 * pc.p + w, first, count);
     const int slot = first + off;
     const bool there = mine && off < count && slot < pc.ctx + pc.n;
+    // the sums of two warpgroups are joined by the one with the item's first block
+    const bool two = pc.end - pc.t0 > 1, leads = (block & 1) == half;
     float* at = a.weights + pc.b * a.w_b + pc.h * a.w_h + slot;
     float old = 0.f;
-    if (there && pc.direct() && a.decay != 0.f) old = *at;  // (on its way during the sums)
+    if (leads && there && pc.direct() && a.decay != 0.f) old = *at;  // (on its way during the sums)
     // tokens that see the slot: from ts to te - 1
     const int ts = slot - pc.ctx;
     const int te = a.window && slot >= a.sinks
@@ -249,37 +267,33 @@ __device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem,
     float acc = 0.f;
 #pragma unroll 1
     for (int t = pc.t0; t < pc.end; ++t, ++block) {
+      if ((block & 1) != half) continue;
       const int bs = block % kBias;
-      uint64_t* bempty = &sm.bempty[bs];
+      if (mine) bar_wait(&sm.sfull[w][half], ph, sm, a.err);
+      bar_wait(&sm.bfull[bs], (block / kBias) & 1, sm, a.err);
       if (mine) {
-        const int buf = jobs & 1;
-        bar_wait(&sm.sfull[w][buf], (jobs >> 1) & 1, sm, a.err);
-        ++jobs;
+        ph ^= 1;
         tc_after();
-        const uint32_t tS = tmem + lanes + (2 * buf + w) * 128;
-        uint32_t s[4][32];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < chunks) tm_ld32(tS + 32 * j, s[j]);
-        tm_wait_loads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j < chunks) tm_tie32(s[j]);
-        tc_before();
-        bar_arrive(&sm.sempty[w][buf]);
         const int i0 = pc.k.ia + t * a.tq, used = min(a.tq, pc.k.ib - i0);
         int lo = min(max(ts - i0, 0), a.tq), hi = min(max(te - i0, 0), used);
         if (!there) hi = 0;
-        bar_wait(&sm.bfull[bs], (block / kBias) & 1, sm, a.err);
+        auto read = [&]() {
+          tc_before();
+          bar_arrive(&sm.sempty[w][half]);
+        };
         // (columns that are no row, behind the block's, are masked like those that do not see it)
-        if (__all_sync(0xffffffffu, lo == 0 && hi * a.G == a.cols)) acc += block_sum<false>(a, s, sm.bias[bs], chunks, 0, 0);
-        else acc += block_sum<true>(a, s, sm.bias[bs], chunks, lo * a.G, hi * a.G);
-      } else {
-        bar_wait(&sm.bfull[bs], (block / kBias) & 1, sm, a.err);
+        if (__all_sync(0xffffffffu, lo == 0 && hi * a.G == a.cols)) acc += block_sum<false>(a, tS, sm.bias[bs], 0, 0, read);
+        else acc += block_sum<true>(a, tS, sm.bias[bs], lo * a.G, hi * a.G, read);
       }
-      bar_arrive(bempty);
+      bar_arrive(&sm.bempty[bs]);
     }
-    if (!there) continue;
+    if (mine && two) {
+      if (!leads) sm.other[w][wt] = acc;
+      named_sync(1 + w, 256);
+      if (leads) acc += sm.other[w][wt];
+      named_sync(1 + w, 256);
+    }
+    if (!there || !leads) continue;
     if (pc.direct()) *at = a.decay == 0.f ? acc : fmaf(a.decay, old, acc);
     else a.part[(2 * blockIdx.x + (item == 0 ? 0 : 1)) * 256 + w * 128 + wt] = acc;
   }
@@ -289,7 +303,7 @@ __device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem,
 // the kernel
 // ---------------------------------------------------------------------------
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kSumThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
                    const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) char base[];
@@ -338,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // ---- this CTA's range ----
   {
-    const long long all = static_cast<long long>(B) * a.NP, per = (all + kThreads - 1) / kThreads;
+    const long long all = static_cast<long long>(B) * a.NP, per = (all + kSumThreads - 1) / kSumThreads;
     const long long f = tid * per, e = min(all, f + per);
     long long mine = 0, pairs = 0;  // blocks of a head, and pairs that have some
     each_pair(a, f, e, [&](int, int, const Item& k) {
@@ -362,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     long long before = inc - mine, beforep = incp - pairs, blocks = 0, items = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < kSumThreads / 32; ++i) {
       if (i < warp) {
         before += sm.scan[0][i];
         beforep += sm.scan[1][i];
@@ -422,10 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
 
   if (warp >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
-    sum_role(a, sm, tmem, (warp - 4) >> 2);
+    sum_role(a, sm, tmem, ((warp - 4) >> 2) & 1, (warp - 4) >> 3);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
     Pieces pc;
     pc.start(a, sm);
     if (warp == 0) {
@@ -456,52 +468,93 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- tiles of K ----
       Ring rk = {&mapk, sm.kfull, sm.kempty, sptr(ring), a.nk, -1, 0};
       bool bad_page = false;
-      // the pages of a tile that hold slots, and this lane's page id
-      auto lookup = [&](int t, int& p1) {
-        int first, count;
-        tile_slots(a, t, first, count);
-        p1 = a.ps <= kTile ? min(a.ppt - 1, (pc.ctx + pc.n - 1 - first) / a.ps) : 0;
-        if (lane > p1) return 0;
-        return __ldg(a.table + pc.b * a.table_stride + (a.ps <= kTile ? t * a.ppt + lane : t / a.tpp));
+      // an item's tiles: the pages that hold slots, and this lane's page id, on its way
+      // while the tiles of the item before are copied
+      struct Tiles {
+        int tiles, t, h, pl[2], id[2];
       };
+      auto lookup = [&](Tiles& x) {
+        x.tiles = 0;
+        if (!pc.next(a)) return;
+        x.tiles = pc.k.tiles;
+        x.t = 2 * pc.p;
+        x.h = pc.h;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          x.id[w] = 0;
+          if (w >= x.tiles) continue;
+          int first, count;
+          tile_slots(a, x.t + w, first, count);
+          x.pl[w] = a.ps <= kTile ? min(a.ppt - 1, (pc.ctx + pc.n - 1 - first) / a.ps) : 0;
+          if (lane <= x.pl[w])
+            x.id[w] = __ldg(a.table + pc.b * a.table_stride + (a.ps <= kTile ? (x.t + w) * a.ppt + lane : (x.t + w) / a.tpp));
+        }
+      };
+      Tiles cur, nxt;
+      lookup(nxt);
 #pragma unroll 1
-      while (pc.next(a)) {
-        int pl[2], id[2] = {0, 0};
-        id[0] = lookup(2 * pc.p, pl[0]);
-        if (pc.k.tiles == 2) id[1] = lookup(2 * pc.p + 1, pl[1]);
+      while (nxt.tiles) {
+        cur = nxt;
+        lookup(nxt);
 #pragma unroll
         for (int w = 0; w < 2; ++w)
-          if (w < pc.k.tiles) bad_page |= !load_tile<D>(a, sm, rk, 2 * pc.p + w, 0, pl[w], id[w], pc.h, a.err, a.withheld);
+          if (w < cur.tiles) bad_page |= !load_tile<D>(a, sm, rk, cur.t + w, 0, cur.pl[w], cur.id[w], cur.h, a.err, a.withheld);
       }
       if (bad_page) atomicOr(a.err, kErrBadPage);
     } else if (warp == 3) {
-      // ---- the columns' -lse ----
-      int block = 0;
-#pragma unroll 1
-      while (pc.next(a)) {
-#pragma unroll 1
-        for (int t = pc.t0; t < pc.end; ++t, ++block) {
-          const int bs = block % kBias, i0 = pc.k.ia + t * a.tq, rows = min(a.tq, pc.k.ib - i0) * a.G;
-          const float* lse = a.lse + (static_cast<long long>(pc.b) * a.nodes.N + i0) * a.Hq + pc.h * a.G;
-          float x[kTile / 32];
+      int place[kTile / 32];  // of a column's lse behind the block's first
 #pragma unroll
-          for (int k = 0; k < kTile / 32; ++k) {
-            const int r = lane + 32 * k, i = r / a.G;
-            x[k] = r < rows ? __ldg(lse + static_cast<long long>(i) * a.Hq + r - i * a.G) : -INFINITY;
+      for (int k = 0; k < kTile / 32; ++k) {
+        const int r = lane + 32 * k;
+        place[k] = r / a.G * a.Hq + r % a.G;
+      }
+      // ---- the columns' -lse, loaded two blocks ahead ----
+      int t = 0, end = 0, block = 0;
+      struct Lse {
+        int there;
+        float x[kTile / 32];
+      };
+      auto load = [&](Lse& l) {
+        l.there = 0;
+        if (++t >= end) {
+          if (end < 0 || !pc.next(a)) {
+            end = -1;
+            t = 0;
+            return;
           }
-          bar_wait(&sm.bempty[bs], ((block / kBias) & 1) ^ 1, sm, a.err);
-#pragma unroll
-          for (int k = 0; k < kTile / 32; ++k) sm.bias[bs][lane + 32 * k] = x[k] == -INFINITY ? -INFINITY : -x[k] * kLog2e;
-          __syncwarp();
-          if (lane == 0) bar_arrive(&sm.bfull[bs]);
+          t = pc.t0;
+          end = pc.end;
         }
+        l.there = 1;
+        const int i0 = pc.k.ia + t * a.tq, rows = min(a.tq, pc.k.ib - i0) * a.G;
+        const float* lse = a.lse + (static_cast<long long>(pc.b) * a.nodes.N + i0) * a.Hq + pc.h * a.G;
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          l.x[k] = lane + 32 * k < rows ? __ldg(lse + place[k]) : -INFINITY;
+      };
+      Lse l0, l1, l2;
+      load(l0);
+      load(l1);
+#pragma unroll 1
+      while (l0.there) {
+        load(l2);
+        const int bs = block % kBias;
+        bar_wait(&sm.bempty[bs], ((block / kBias) & 1) ^ 1, sm, a.err);
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          sm.bias[bs][lane + 32 * k] = l0.x[k] == -INFINITY ? -INFINITY : -l0.x[k] * kLog2e;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm.bfull[bs]);
+        ++block;
+        l0 = l1;
+        l1 = l2;
       }
     } else {
       // ---- products ----
       const uint32_t khalf = a.half / 16, id = instr<T>(a.cols, false, false, a.negate);
       const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
-      int qslot = -1, kslot = -1, jobs[2] = {0, 0};
-      uint32_t qphase = 0, kphase = 0;
+      int qslot = -1, kslot = -1, block = 0;
+      uint32_t qphase = 0, kphase = 0, sph = 0;  // (sph: of sempty)
 #pragma unroll 1
       while (pc.next(a)) {
         int ks[2];
@@ -516,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
         }
 #pragma unroll 1
-        for (int t = pc.t0; t < pc.end; ++t) {
+        for (int t = pc.t0; t < pc.end; ++t, ++block) {
           if (++qslot == a.nq) {
             qslot = 0;
             qphase ^= 1;
@@ -526,9 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (w >= pc.k.tiles) continue;
-            const int buf = jobs[w] & 1;
-            bar_wait(&sm.sempty[w][buf], ((jobs[w] >> 1) & 1) ^ 1, sm, a.err);
-            ++jobs[w];
+            const int buf = block & 1, bit = 2 * w + buf;
+            bar_wait(&sm.sempty[w][buf], ((sph >> bit) & 1) ^ 1, sm, a.err);
+            sph ^= 1u << bit;
             tc_after();
             const uint64_t kd = kd0 + ks[w] * (kSlotBytes / 16);
             if (elect_one()) {
@@ -567,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tile_slots(a, 2 * p0, from, count);
         tile_slots(a, 2 * p1, to, count);
         const long long m = static_cast<long long>(to - from) * a.Hkv;
-        for (long long i = blockIdx.x * static_cast<long long>(kThreads) + tid; i < m;
-             i += static_cast<long long>(C) * kThreads) {
+        for (long long i = blockIdx.x * static_cast<long long>(kSumThreads) + tid; i < m;
+             i += static_cast<long long>(C) * kSumThreads) {
           const int h = static_cast<int>(i / (to - from));
           float* at = a.weights + (b0 + j) * a.w_b + h * a.w_h + from + (i - static_cast<long long>(h) * (to - from));
           *at = a.decay == 0.f ? 0.f : a.decay * *at;
@@ -637,7 +690,7 @@ template <class T, int D>
 cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const Args& a, int C, size_t smem, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(weights_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
-  weights_kernel<T, D><<<C, kThreads, smem, s>>>(mq, mk, a);
+  weights_kernel<T, D><<<C, kSumThreads, smem, s>>>(mq, mk, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || C < 2) return e;
   cudaLaunchConfig_t cfg = {};
