@@ -11,7 +11,7 @@
 // numbered and cut into equal ranges by the lengths on the device; an item that is cut
 // leaves its sums in the workspace, and weights_join_kernel adds them in range order.
 //
-// Warps of a CTA: 0 copies the blocks of Q, 2 the tiles of K, both by TMA into rings; 1
+// Warps of a CTA: 0 copies the blocks of Q, 2 and 20 the tiles of K, by TMA into rings; 1
 // issues the products; 3 brings the columns' -lse; 4..19 four warpgroups for the sums, two
 // a tile, which take its blocks in turn.
 #include <math.h>
@@ -23,9 +23,9 @@
 namespace ssd {
 namespace {
 
-constexpr int kSumThreads = 640;
+constexpr int kSumThreads = 672;
 constexpr int kMaxCtas = 160;
-constexpr int kMaxKeys = 8, kMaxQueries = 4, kBias = 4;  // slots of the rings
+constexpr int kMaxKeys = 4, kMaxQueries = 4, kBias = 4;  // slots of the rings (of K two, for the tiles of an item)
 constexpr float kLog2e = 1.4426950408889634f;
 
 // A CTA's range of blocks, for the joining kernel.
@@ -60,7 +60,7 @@ struct Args : PageTiles {
 
 struct alignas(16) Misc {
   alignas(16) float bias[kBias][kTile];  // -lse of the columns, in units of log 2
-  uint64_t kfull[kMaxKeys], kempty[kMaxKeys], qfull[kMaxQueries], qempty[kMaxQueries], bfull[kBias], bempty[kBias];
+  uint64_t kfull[2][kMaxKeys], kempty[2][kMaxKeys], qfull[kMaxQueries], qempty[kMaxQueries], bfull[kBias], bempty[kBias];
   uint64_t sfull[2][2], sempty[2][2], done;
   long long left;
   int b0, p0, h0, t0, cost;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   constexpr int HALVES = D / 64;
   constexpr int kSlotBytes = HALVES * kHalf;
   char* ring = base;
-  char* Q = ring + a.nk * kSlotBytes;
+  char* Q = ring + 2 * a.nk * kSlotBytes;
   const int qhalf = a.cols * 128, qbytes = qhalf * HALVES;
   Misc& sm = *reinterpret_cast<Misc*>(Q + a.nq * qbytes);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   const int C = gridDim.x, B = a.nodes.B;
 
   if (tid == 0) {
-    for (int i = 0; i < kMaxKeys; ++i) {
-      bar_init(&sm.kfull[i], 1);
-      bar_init(&sm.kempty[i], 1);
+    for (int i = 0; i < 2 * kMaxKeys; ++i) {
+      bar_init(&sm.kfull[i / kMaxKeys][i % kMaxKeys], 1);
+      bar_init(&sm.kempty[i / kMaxKeys][i % kMaxKeys], 1);
     }
     for (int i = 0; i < kMaxQueries; ++i) {
       bar_init(&sm.qfull[i], 1);
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   pdl_trigger();
   const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem, 0);
 
-  if (warp >= 4) {
+  if (warp >= 4 && warp < 20) {
     sum_role(a, sm, tmem, ((warp - 4) >> 2) & 1, (warp - 4) >> 3);
   } else {
     Pieces pc;
@@ -464,41 +464,36 @@ __global__ void __launch_bounds__(kSumThreads, 1)
           __syncwarp();
         }
       }
-    } else if (warp == 2) {
-      // ---- tiles of K ----
-      Ring rk = {&mapk, sm.kfull, sm.kempty, sptr(ring), a.nk, -1, 0};
+    } else if (warp == 2 || warp == 20) {
+      // ---- first (2) or second (20) tiles of K ----
+      const int w = warp == 20;
+      Ring rk = {&mapk, sm.kfull[w], sm.kempty[w], sptr(ring) + w * a.nk * kSlotBytes, a.nk, -1, 0};
       bool bad_page = false;
-      // an item's tiles: the pages that hold slots, and this lane's page id, on its way
-      // while the tiles of the item before are copied
-      struct Tiles {
-        int tiles, t, h, pl[2], id[2];
+      // an item's tile: the pages that hold slots, and this lane's page id, on its way
+      // while the tile of the item before is copied
+      struct Tile {
+        int t, h, pl, id;
       };
-      auto lookup = [&](Tiles& x) {
-        x.tiles = 0;
-        if (!pc.next(a)) return;
-        x.tiles = pc.k.tiles;
-        x.t = 2 * pc.p;
+      auto lookup = [&](Tile& x) {
+        x.t = -1;
+        do {
+          if (!pc.next(a)) return;
+        } while (w >= pc.k.tiles);
+        x.t = 2 * pc.p + w;
         x.h = pc.h;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          x.id[w] = 0;
-          if (w >= x.tiles) continue;
-          int first, count;
-          tile_slots(a, x.t + w, first, count);
-          x.pl[w] = a.ps <= kTile ? min(a.ppt - 1, (pc.ctx + pc.n - 1 - first) / a.ps) : 0;
-          if (lane <= x.pl[w])
-            x.id[w] = __ldg(a.table + pc.b * a.table_stride + (a.ps <= kTile ? (x.t + w) * a.ppt + lane : (x.t + w) / a.tpp));
-        }
+        x.id = 0;
+        int first, count;
+        tile_slots(a, x.t, first, count);
+        x.pl = a.ps <= kTile ? min(a.ppt - 1, (pc.ctx + pc.n - 1 - first) / a.ps) : 0;
+        if (lane <= x.pl) x.id = __ldg(a.table + pc.b * a.table_stride + (a.ps <= kTile ? x.t * a.ppt + lane : x.t / a.tpp));
       };
-      Tiles cur, nxt;
+      Tile cur, nxt;
       lookup(nxt);
 #pragma unroll 1
-      while (nxt.tiles) {
+      while (nxt.t >= 0) {
         cur = nxt;
         lookup(nxt);
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (w < cur.tiles) bad_page |= !load_tile<D>(a, sm, rk, cur.t + w, 0, cur.pl[w], cur.id[w], cur.h, a.err, a.withheld);
+        bad_page |= !load_tile<D>(a, sm, rk, cur.t, 0, cur.pl, cur.id, cur.h, a.err, a.withheld);
       }
       if (bad_page) atomicOr(a.err, kErrBadPage);
     } else if (warp == 3) {
@@ -549,24 +544,22 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         l0 = l1;
         l1 = l2;
       }
-    } else {
+    } else if (warp == 1) {
       // ---- products ----
       const uint32_t khalf = a.half / 16, id = instr<T>(a.cols, false, false, a.negate);
       const uint64_t kd0 = operand(sptr(ring), 16, a.group), qd0 = operand(sptr(Q), 16, 1024);
-      int qslot = -1, kslot = -1, block = 0;
-      uint32_t qphase = 0, kphase = 0, sph = 0;  // (sph: of sempty)
+      int qslot = -1, kslot[2] = {-1, -1}, block = 0;
+      uint32_t qphase = 0, kphase[2] = {0, 0}, sph = 0;  // (sph: of sempty)
 #pragma unroll 1
       while (pc.next(a)) {
-        int ks[2];
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (w >= pc.k.tiles) continue;
-          if (++kslot == a.nk) {
-            kslot = 0;
-            kphase ^= 1;
+          if (++kslot[w] == a.nk) {
+            kslot[w] = 0;
+            kphase[w] ^= 1;
           }
-          ks[w] = kslot;
-          bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
+          bar_wait(&sm.kfull[w][kslot[w]], kphase[w], sm, a.err);
         }
 #pragma unroll 1
         for (int t = pc.t0; t < pc.end; ++t, ++block) {
@@ -583,7 +576,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             bar_wait(&sm.sempty[w][buf], ((sph >> bit) & 1) ^ 1, sm, a.err);
             sph ^= 1u << bit;
             tc_after();
-            const uint64_t kd = kd0 + ks[w] * (kSlotBytes / 16);
+            const uint64_t kd = kd0 + (w * a.nk + kslot[w]) * (kSlotBytes / 16);
             if (elect_one()) {
 #pragma unroll
               for (int k = 0; k < D / 16; ++k)
@@ -591,7 +584,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
                        qd + (k / 4) * (qhalf / 16) + (k & 3) * 2, id, k > 0);
               tc_commit(&sm.sfull[w][buf]);
               if (w == pc.k.tiles - 1) tc_commit(&sm.qempty[qslot]);
-              if (t + 1 == pc.end) tc_commit(&sm.kempty[ks[w]]);
+              if (t + 1 == pc.end) tc_commit(&sm.kempty[w][kslot[w]]);
             }
             __syncwarp();
           }
@@ -737,12 +730,13 @@ cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, int D, cudaStre
   const long long slots = most < p.w_len ? most : p.w_len;
   const long long tiles = a.ps <= kTile ? (slots + a.tk - 1) / a.tk : (slots / a.ps + 1) * a.tpp;
   a.NP = static_cast<int>((tiles + 1) / 2);
-  // as many tiles of K as fit beside three or four blocks of Q
+  // as many tiles of K as fit beside the blocks of Q (two of 32 KB: a third would leave one
+  // slot a ring of K)
   const size_t slot = static_cast<size_t>(D) * 2 * kTile, qslot = static_cast<size_t>(D) * 2 * a.cols;
-  a.nq = a.cols > 64 ? 3 : kMaxQueries;
+  a.nq = qslot > 16384 ? 2 : kMaxQueries;
   const size_t left = kSmemMax - sizeof(Misc) - a.nq * qslot;
-  a.nk = static_cast<int>(left / slot < kMaxKeys ? left / slot : kMaxKeys);
-  const size_t smem = a.nk * slot + a.nq * qslot + sizeof(Misc);
+  a.nk = static_cast<int>(left / (2 * slot) < kMaxKeys ? left / (2 * slot) : kMaxKeys);
+  const size_t smem = 2 * a.nk * slot + a.nq * qslot + sizeof(Misc);
   int C = sm_count();
   if (C < 1) return cudaErrorInvalidDevice;
   C = C < kMaxCtas ? C : kMaxCtas;
