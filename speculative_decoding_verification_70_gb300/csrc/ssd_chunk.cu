@@ -51,6 +51,7 @@ constexpr int kMaxRing = 6;
 constexpr int kMaxCtas = 160;
 constexpr int kEdgeBars = 8;   // edge tiles whose clearing may lie ahead of their products
 constexpr int kFlagSets = 8;   // items whose flags live side by side
+constexpr int kStage = 2 * kTile * 128;  // 32 columns of O of the copies, by warpgroup
 constexpr float kNoScore = -1e30f;  // m of a row that has seen nothing
 constexpr float kGrow = 8.f;
 template <class T>
@@ -67,6 +68,7 @@ struct Args : PageTiles {
   NodesView nodes;
   int Hq, Hkv, G;
   int tq, tpi;             // tokens of a row tile, of an item
+  int copies;              // of the rows in a row tile (1, 2, 4)
   int NB;                  // blocks of the longest chunk
   int window, sinks;
   int item_cost;           // what an item's start and end cost, in tiles
@@ -302,6 +304,27 @@ __device__ __forceinline__ void scale_columns(uint32_t at, float f) {
   }
 }
 
+// Columns k .. k + 31 of a row: results, or a part.
+template <class T, int D>
+__device__ __forceinline__ void write_columns(const Args& a, const uint32_t (&o)[32], long long row, int k, bool direct,
+                                              bool empty, float inv) {
+  if (direct) {
+    uint4* out = reinterpret_cast<uint4*>(a.out + 2 * (row * D + k));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        y[e] = empty ? 0u : T::pack(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
+      out[q] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+  } else {
+    uint4* out = reinterpret_cast<uint4*>(a.part_o + row * D + k);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) out[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+  }
+}
+
 template <bool V>
 struct Flag {
   static constexpr bool value = V;
@@ -475,21 +498,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
         tm_wait_loads();
         tm_tie32(o);
         if (any && valid) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pos, fl, k, o);
-        if (valid && direct) {
-          uint4* out = reinterpret_cast<uint4*>(a.out + 2 * (row * D + k));
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              y[e] = empty ? 0u : T::pack(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
-            out[q] = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        } else if (valid) {
-          uint4* out = reinterpret_cast<uint4*>(a.part_o + row * D + k);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) out[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-        }
+        if (valid) write_columns<T, D>(a, o, row, k, direct, empty, inv);
       }
     }
     if (jobs > 0) {
@@ -504,6 +513,227 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
+// Entries k .. k + 31 of a row that came out NaN or infinite because a slot that every row
+// sees holds such a value, which met other copies' weights of 0 as well: what the values
+// alone make of them.
+template <class T>
+__device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, int k, uint32_t (&o)[32]) {
+  float x[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) x[e] = 0.f;
+#pragma unroll 1
+  for (int at = pc.t0; at < pc.end; ++at) {
+    int first, count;
+    tile_slots(a, pc.tile(at), first, count);
+#pragma unroll 1
+    for (int s = first; s < first + count; ++s) {
+      int page, off;
+      if (!all(a, pc.s, s, s)) continue;  // (cleared)
+      if (!kv_slot(a.table + pc.b * a.table_stride, a.width, a.pages, a.ps, s, page, off)) continue;
+      const uint32_t* v =
+          reinterpret_cast<const uint32_t*>(a.vcache + 2 * (page * a.v_page + off * a.v_slot + pc.h * a.v_head + k));
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint32_t y = v[e];
+        if (!(fabsf(T::lo(y)) < INFINITY)) x[2 * e] += T::lo(y);
+        if (!(fabsf(T::hi(y)) < INFINITY)) x[2 * e + 1] += T::hi(y);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(fabsf(__uint_as_float(o[e])) < INFINITY) && !(fabsf(x[e]) < INFINITY)) o[e] = __float_as_uint(x[e]);
+}
+
+// Few rows (64 at most): they lie in the row tile two or four times, and a copy takes its
+// part of a tile's slots alone, so that a thread has 64 or 32 scores instead of 128.  The
+// copies have their own m, l and O, which are joined at the item's end.
+template <class T, int D>
+__device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tmem, char* stage, int w) {
+  const int wt = threadIdx.x & 127, span = kTile / a.copies;
+  const uint32_t lanes = static_cast<uint32_t>(wt & 96) << 16;
+  const int copy = wt / span, r = wt - copy * span, nq = span / 32, q0 = copy * nq;  // its quarters of the slots
+  const int tok = r / a.G, g = r - tok * a.G;
+  const f32x2 c2 = pk2(a.c, a.c);
+  const uint32_t tO = tmem + lanes + 256 + w * D;
+  uint32_t ppv = 0;    // phase of pvdone[w]
+  uint32_t sph = 0;    // phases of sfull[w][.]
+  int tiles = 0, item = -1;
+  Pieces pc;
+  pc.start(a, sm);
+#pragma unroll 1
+  while (pc.next(a)) {
+    ++item;
+    if ((item & 1) != w) {
+      tiles += pc.end - pc.t0;
+      continue;
+    }
+    const int i = pc.blk * a.tpi + tok, pos = pc.ctx + i;
+    const bool valid = tok < a.tq && i < pc.n;
+    float m = kNoScore, l = 0.f;
+    int jobs = 0;
+    bool edges = false;
+#pragma unroll 1
+    for (int at = pc.t0; at < pc.end; ++at, ++tiles) {
+      const int t = pc.tile(at);
+      const bool edge = pc.k.edge(t);
+      edges |= edge;
+      const int buf = tiles & 1;
+      bar_wait(&sm.sfull[w][buf], (sph >> buf) & 1, sm, a.err);
+      sph ^= 1u << buf;
+      bool waited = jobs == 0;  // for the last tile's product
+      auto last_done = [&]() {
+        if (!waited) {
+          bar_wait(&sm.pvdone[w], ppv, sm, a.err);
+          ppv ^= 1;
+          tc_after();
+          waited = true;
+        }
+      };
+      tc_after();
+      const uint32_t tS = tmem + lanes + buf * 128;
+      uint32_t s[2][32];
+      tm_ld32(tS + 32 * q0, s[0]);
+      if (nq == 2) tm_ld32(tS + 32 * q0 + 32, s[1]);
+      tm_wait_loads();
+      tm_tie32(s[0]);
+      tm_tie32(s[1]);
+      if (edge || a.holes) {
+        int hi = kTile, lo = 0, sk = 0;
+        if (edge) {
+          int first, count;
+          tile_slots(a, t, first, count);
+          hi = rows_before(a, min(pos - first + 1, count));
+          lo = a.window ? rows_before(a, pos - a.window - first + 1) : 0;
+          sk = rows_before(a, a.sinks - first);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e0 = 32 * (q0 + j);
+          const uint32_t v = j < nq ? sm.plain[q0 + j] & below(hi - e0) & (~below(lo - e0) | below(sk - e0)) : 0u;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) hide(s[j][e], v & (1u << e));
+        }
+      }
+      float mx[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mx[j] = max3(__uint_as_float(s[j][0]), __uint_as_float(s[j][1]), __uint_as_float(s[j][2]));
+#pragma unroll
+        for (int e = 3; e < 31; e += 2) mx[j] = max3(mx[j], __uint_as_float(s[j][e]), __uint_as_float(s[j][e + 1]));
+        mx[j] = fmaxf(mx[j], __uint_as_float(s[j][31]));
+      }
+      const float top = a.c * (nq == 2 ? fmaxf(mx[0], mx[1]) : mx[0]) - kLift<T>;
+      const bool raise = top > (m == kNoScore ? m : m + kGrow);
+      if (__any_sync(0xffffffffu, raise)) {
+        const float f = raise ? ex2_fast(m - top) : 1.f;
+        if (raise) m = top;
+        l *= f;
+        if (jobs > 0) {
+          last_done();
+          scale_columns<D>(tO, f);
+        }
+      }
+      const f32x2 nm = pk2(-m, -m);
+      f32x2 sum[2] = {0ull, 0ull};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (j >= nq) break;
+        uint32_t p[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float y0, y1;
+          up2(fma2(pk2(__uint_as_float(s[j][2 * e]), __uint_as_float(s[j][2 * e + 1])), c2, nm), y0, y1);
+          y0 = ex2_fast(y0);
+          y1 = ex2_fast(y1);
+          sum[e & 1] = add2(sum[e & 1], pk2(y0, y1));
+          p[e] = T::pack(y0, y1);
+        }
+        tm_put16(tS + 16 * (q0 + j), p);
+      }
+      // no weight for the other copies' slots
+      uint32_t zero[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) zero[e] = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < q0 || q >= q0 + nq) tm_put16(tS + 16 * q, zero);
+      float a0, a1;
+      up2(add2(sum[0], sum[1]), a0, a1);
+      l += a0 + a1;
+      tm_wait_stores();
+      last_done();
+      tc_before();
+      bar_arrive(&sm.pfull[buf][0]);
+      bar_arrive(&sm.pfull[buf][1]);
+      ++jobs;
+    }
+
+    // ---- end of the piece: the copies joined ----
+    bar_wait(&sm.pvdone[w], ppv, sm, a.err);
+    ppv ^= 1;
+    tc_after();
+    float2* ml = reinterpret_cast<float2*>(stage);
+    ml[wt] = make_float2(m, l);
+    named_sync(1 + w, 128);
+    float M = kNoScore, L = 0.f;
+    for (int k = 0; k < a.copies; ++k) M = fmaxf(M, ml[k * span + r].x);
+    for (int k = 0; k < a.copies; ++k) {
+      const float2 x = ml[k * span + r];
+      L += x.x == M ? x.y : x.y * ex2_fast(x.x - M);
+    }
+    named_sync(1 + w, 128);
+    const float f = m == M ? 1.f : ex2_fast(m - M);
+    const bool direct = pc.direct(), empty = L == 0.f, out_row = valid && copy == 0;
+    const float inv = !direct ? 1.f : empty ? 0.f : 1.f / L;
+    const long long row = direct ? (static_cast<long long>(pc.b) * a.nodes.N + i) * a.Hq + pc.h * a.G + g
+                                 : (2ll * blockIdx.x + (item == 0 ? 0 : 1)) * a.tpi * a.G + r;
+    const unsigned* fl = sm.flags[item % kFlagSets];
+    unsigned any = 0;
+    if (edges) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) any |= fl[q];
+    }
+    uint4* line = reinterpret_cast<uint4*>(stage + wt * 128);
+#pragma unroll 1
+    for (int k = 0; k < D; k += 32) {
+      uint32_t o[32];
+      tm_ld32(tO + k, o);
+      tm_wait_loads();
+      tm_tie32(o);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) line[q ^ (wt & 7)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      named_sync(1 + w, 128);
+      if (out_row) {
+        for (int c = 1; c < a.copies; ++c) {
+          const uint4* other = reinterpret_cast<const uint4*>(stage + (c * span + r) * 128);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint4 x = other[q ^ (wt & 7)];  // (copies lie multiples of 8 rows apart)
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[4 * q + e] = __float_as_uint(__uint_as_float(o[4 * q + e]) + __uint_as_float(y[e]));
+          }
+        }
+        bool finite = true;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) finite = finite && fabsf(__uint_as_float(o[e])) < INFINITY;
+        if (!finite) seen_nonfinite<T>(a, pc, k, o);
+        if (any) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pos, fl, k, o);
+        write_columns<T, D>(a, o, row, k, direct, empty, inv);
+      }
+      named_sync(1 + w, 128);
+    }
+    tc_before();
+    bar_arrive(&sm.ofree[w]);
+    if (out_row && direct && a.lse) a.lse[row] = empty ? -INFINITY : log_sum<T>(M, L);
+    if (out_row && !direct) a.part_ml[row] = make_float2(M, L);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // copies of K and V
 // ---------------------------------------------------------------------------
@@ -758,17 +988,21 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <class T, int D, bool WIDE>
+// MODE: one row tile, two, or one with copies of its rows.
+enum { kOne, kTwo, kCopies };
+template <class T, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
                  const __grid_constant__ CUtensorMap mapv, const __grid_constant__ Args a) {
   extern __shared__ __align__(1024) char base[];
+  constexpr bool WIDE = MODE == kTwo;
   constexpr int HALVES = D / 64;
   constexpr int kSlotBytes = HALVES * kHalf;
   char* ring = base;
   char* ringv = ring + a.nk * kSlotBytes;
   char* Q = ringv + a.nv * kSlotBytes;
-  Misc& sm = *reinterpret_cast<Misc*>(Q + 2 * kSlotBytes);
+  char* stage = Q + 2 * kSlotBytes;  // (copies) 16 KB a warpgroup
+  Misc& sm = *reinterpret_cast<Misc*>(stage + (MODE == kCopies ? kStage : 0));
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int C = gridDim.x, B = a.nodes.B;
@@ -944,7 +1178,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
-    softmax_role<T, D, WIDE>(a, sm, tmem, (warp - 4) >> 2);
+    const int w = (warp - 4) >> 2;
+    if constexpr (MODE == kCopies) share_role<T, D>(a, sm, tmem, stage + w * (kStage / 2), w);
+    else softmax_role<T, D, WIDE>(a, sm, tmem, w);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
     if (warp == 0) {
@@ -967,14 +1203,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq;
         const bool ok = bar_wait(&sm.qempty[qb], ph ^ 1, sm, a.err) && !*reinterpret_cast<volatile int*>(&sm.abort);
         if (__all_sync(0xffffffffu, ok)) {
-          const bool two = WIDE && pq.s.p1 - pq.s.p0 >= a.tq;
-          if (lane == 0) bar_expect(&sm.qfull[qb], (two ? 2 : 1) * HALVES * a.tq * a.G * 128 + a.withheld);
+          // boxes of rows: of one row tile, of two, or the same for every copy
+          const int boxes = MODE == kCopies ? a.copies : WIDE && pq.s.p1 - pq.s.p0 >= a.tq ? 2 : 1;
+          if (lane == 0) bar_expect(&sm.qfull[qb], boxes * HALVES * a.tq * a.G * 128 + a.withheld);
           __syncwarp();
           if (elect_one()) {
-            for (int w = 0; w < (two ? 2 : 1); ++w)
+            for (int w = 0; w < boxes; ++w)
               for (int d = 0; d < HALVES; ++d)
-                tma_rows(sptr(Q) + (qb + w) * kSlotBytes + d * kHalf, &mapq, d * 64, pq.h * a.G,
-                         a.zero ? a.nodes.N : pq.blk * a.tpi + w * a.tq, pq.b, &sm.qfull[qb]);  // (behind the last: zeros)
+                tma_rows(sptr(Q) + (MODE == kCopies ? qb * kSlotBytes + w * (kTile / a.copies) * 128 : (qb + w) * kSlotBytes) +
+                             d * kHalf,
+                         &mapq, d * 64, pq.h * a.G,
+                         a.zero ? a.nodes.N : pq.blk * a.tpi + (WIDE ? w * a.tq : 0),  // (behind the last: zeros)
+                         pq.b, &sm.qfull[qb]);
           }
           __syncwarp();
         }
@@ -1140,10 +1380,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
-// Tokens of an item: one row tile where every chunk fits it, else two.
+// Tokens of an item: all where copies of them fit a row tile, one row tile of them where
+// every chunk fits it, else two.
 int item_tokens(int N, int G) {
   const int tq = kTile / G;
-  return N <= tq ? tq : 2 * tq;
+  return N * static_cast<long long>(G) <= kTile / 2 ? N : N <= tq ? tq : 2 * tq;
 }
 
 struct Layout {
@@ -1159,12 +1400,12 @@ Layout layout_of(int N, int G, int D) {
   return L;
 }
 
-template <class T_, int D, bool WIDE>
+template <class T_, int D, int MODE>
 cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C,
                      size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<T_, D, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<T_, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
-  chunk_kernel<T_, D, WIDE><<<C, kThreads, smem, s>>>(mq, mk, mv, a);
+  chunk_kernel<T_, D, MODE><<<C, kThreads, smem, s>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || C < 2) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1179,6 +1420,13 @@ cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T_, D>, a, C);
 }
 
+template <class T_, int D>
+cudaError_t launch_m(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C, int mode,
+                     size_t smem, cudaStream_t s) {
+  const auto launch = mode == kTwo ? launch_t<T_, D, kTwo> : mode == kOne ? launch_t<T_, D, kOne> : launch_t<T_, D, kCopies>;
+  return launch(mq, mk, mv, a, C, smem, s);
+}
+
 }  // namespace
 
 size_t chunk_attention_bytes(int N, int G, int D) { return layout_of(N, G, D).total; }
@@ -1188,9 +1436,11 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
   const KvView& kv = p.kv;
   a.nodes = p.nodes;
   a.Hq = p.Hq; a.Hkv = kv.Hkv; a.G = p.G;
-  a.tq = kTile / p.G;
   a.tpi = item_tokens(p.nodes.N, p.G);
-  const bool wide = a.tpi > a.tq;
+  const int rows = a.tpi * p.G;
+  a.copies = rows <= kTile / 4 ? 4 : rows <= kTile / 2 ? 2 : 1;
+  a.tq = a.copies > 1 ? a.tpi : kTile / p.G;
+  const int mode = a.copies > 1 ? kCopies : a.tpi > a.tq ? kTwo : kOne;
   a.NB = (p.nodes.N + a.tpi - 1) / a.tpi;
   // (a window that no sequence exceeds is none)
   a.window = p.window < static_cast<long long>(kv.width) * kv.ps ? p.window : 0;
@@ -1209,10 +1459,11 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
   a.part_ml = reinterpret_cast<float2*>(ws + L.ml);
   a.part_o = reinterpret_cast<float*>(ws + L.o);
   const int slot = D * 2 * kTile;
-  const int slots = static_cast<int>((kSmemMax - 2 * slot - sizeof(Misc)) / slot);
+  const size_t beside = 2 * slot + (mode == kCopies ? kStage : 0) + sizeof(Misc);
+  const int slots = static_cast<int>((kSmemMax - beside) / slot);
   a.nk = (slots + 1) / 2 < kMaxRing ? (slots + 1) / 2 : kMaxRing;
   a.nv = slots - a.nk < kMaxRing ? slots - a.nk : kMaxRing;
-  const size_t smem = static_cast<size_t>(a.nk + a.nv + 2) * slot + sizeof(Misc);
+  const size_t smem = static_cast<size_t>(a.nk + a.nv) * slot + beside;
   CUtensorMap mq, mk, mv;
   if (!page_tiles(a, kv, dtype, D, &mk, &mv) || !encode_queries(&mq, p.q, p.q_b, p.q_n, p.q_h, p.Hq, p.nodes, p.G, dtype, D, a.tq))
     return cudaErrorInvalidValue;
@@ -1220,13 +1471,9 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
   if (C < 1) return cudaErrorInvalidDevice;
   C = C < kMaxCtas ? C : kMaxCtas;
   a.per_cta = C > 1 ? ~0ull / C + 1 : 0;
-  const auto launch =
-      dtype == Bf16::kId
-          ? (D == 128 ? (wide ? launch_t<Bf16, 128, true> : launch_t<Bf16, 128, false>)
-                      : (wide ? launch_t<Bf16, 64, true> : launch_t<Bf16, 64, false>))
-          : (D == 128 ? (wide ? launch_t<F16, 128, true> : launch_t<F16, 128, false>)
-                      : (wide ? launch_t<F16, 64, true> : launch_t<F16, 64, false>));
-  return launch(mq, mk, mv, a, C, smem, s);
+  const auto launch = dtype == Bf16::kId ? (D == 128 ? launch_m<Bf16, 128> : launch_m<Bf16, 64>)
+                                         : (D == 128 ? launch_m<F16, 128> : launch_m<F16, 64>);
+  return launch(mq, mk, mv, a, C, mode, smem, s);
 }
 
 }  // namespace ssd
