@@ -857,12 +857,12 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
   uint32_t pph = 0, oph = 0;  // phases of pfull (two row tiles) and ofree
   // what scores and values wait for beside the turn
   auto before_scores = [&](const Step& st) {
-    if (st.newq) bar_wait(&sm.qfull[WIDE ? 0 : st.item & 1], (WIDE ? st.item : st.item >> 1) & 1, sm, a.err);
+    if (st.newq) bar_await(&sm.qfull[WIDE ? 0 : st.item & 1], (WIDE ? st.item : st.item >> 1) & 1, sm, a.err);
     if (++kslot == a.nk) {
       kslot = 0;
       kphase ^= 1;
     }
-    bar_wait(&sm.kfull[kslot], kphase, sm, a.err);
+    bar_await(&sm.kfull[kslot], kphase, sm, a.err);
   };
   auto scores = [&](const Step& st) {
     const int buf = WIDE ? w : st.no & 1, qb = WIDE ? w : st.item & 1;
@@ -891,20 +891,20 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
       vslot = 0;
       vphase ^= 1;
     }
-    bar_wait(&sm.vfull[vslot], vphase, sm, a.err);
+    bar_await(&sm.vfull[vslot], vphase, sm, a.err);
     if (st.edge) {
-      bar_wait(&sm.vready[edges % kEdgeBars], (edges / kEdgeBars) & 1, sm, a.err);
+      bar_await(&sm.vready[edges % kEdgeBars], (edges / kEdgeBars) & 1, sm, a.err);
       ++edges;
     }
     if (!st.act) return;
     const int ob = WIDE ? w : st.item & 1;
     if (st.begin) {  // the results of the last item in these columns have been read
-      bar_wait(&sm.ofree[ob], ((oph >> ob) & 1) ^ 1, sm, a.err);
+      bar_await(&sm.ofree[ob], ((oph >> ob) & 1) ^ 1, sm, a.err);
       oph ^= 1u << ob;
     }
     ph = WIDE ? pph : (st.no >> 1) & 1;
     pph ^= 1;
-    bar_wait(&sm.pfull[WIDE ? w : st.no & 1][0], ph, sm, a.err);
+    bar_await(&sm.pfull[WIDE ? w : st.no & 1][0], ph, sm, a.err);
   };
   auto values = [&](const Step& st) {
     const int buf = WIDE ? w : st.no & 1, ob = WIDE ? w : st.item & 1;
@@ -917,7 +917,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
           tc_mma_ta(tmem + 256 + ob * D, tmem + buf * 128 + k * 8, vd + k * vstep, ido, !st.begin || k > 0);
       }
       __syncwarp();
-      bar_wait(&sm.pfull[buf][1], ph, sm, a.err);
+      bar_await(&sm.pfull[buf][1], ph, sm, a.err);
       tc_after();
       if (elect_one()) {
 #pragma unroll
@@ -936,7 +936,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
   // instead of 2800).
   uint32_t tph = w ^ 1;
   auto take = [&]() {
-    if (WIDE) bar_wait(&sm.turn[w], tph, sm, a.err);
+    if (WIDE) bar_await(&sm.turn[w], tph, sm, a.err);
     tph ^= 1;
   };
   auto pass = [&]() {
@@ -981,7 +981,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
     }
     if (elect_one()) tc_commit(&sm.done);
     __syncwarp();
-    bar_wait(&sm.done, 0, sm, a.err);
+    bar_await(&sm.done, 0, sm, a.err);
   }
 }
 
@@ -1201,7 +1201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qb = WIDE ? 0 : nq & 1;
         const uint32_t ph = (WIDE ? nq : nq >> 1) & 1;
         ++nq;
-        const bool ok = bar_wait(&sm.qempty[qb], ph ^ 1, sm, a.err) && !*reinterpret_cast<volatile int*>(&sm.abort);
+        const bool ok = bar_await(&sm.qempty[qb], ph ^ 1, sm, a.err) && !*reinterpret_cast<volatile int*>(&sm.abort);
         if (__all_sync(0xffffffffu, ok)) {
           // boxes of rows: of one row tile, of two, or the same for every copy
           const int boxes = MODE == kCopies ? a.copies : WIDE && pq.s.p1 - pq.s.p0 >= a.tq ? 2 : 1;
@@ -1236,7 +1236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             slot = 0;
             phase ^= 1;
           }
-          bar_wait(&sm.vfull[slot], phase, sm, a.err);
+          bar_await(&sm.vfull[slot], phase, sm, a.err);
           if (pc.k.edge(t)) {
             int first, count;
             tile_slots(a, t, first, count);

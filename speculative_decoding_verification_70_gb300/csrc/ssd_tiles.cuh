@@ -74,7 +74,7 @@ __device__ __forceinline__ bool load_tile(const PageTiles& a, Misc& sm, Ring& r,
     r.phase ^= 1;
   }
   uint64_t* full = r.full + r.slot;
-  const bool ok = bar_wait(r.empty + r.slot, r.phase ^ 1, sm, err) && !*reinterpret_cast<volatile int*>(&sm.abort);
+  const bool ok = bar_await(r.empty + r.slot, r.phase ^ 1, sm, err) && !*reinterpret_cast<volatile int*>(&sm.abort);
   if (!__all_sync(0xffffffffu, ok)) return true;
   if (lane == 0) bar_expect(full, (p1 - p0 + 1) * a.box * 128 * HALVES + withheld);
   __syncwarp();

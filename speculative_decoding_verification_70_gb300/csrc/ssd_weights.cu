@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             slot = 0;
             phase ^= 1;
           }
-          const bool ok = bar_wait(&sm.qempty[slot], phase ^ 1, sm, a.err) &&
+          const bool ok = bar_await(&sm.qempty[slot], phase ^ 1, sm, a.err) &&
                           !*reinterpret_cast<volatile int*>(&sm.abort);
           if (__all_sync(0xffffffffu, ok) && elect_one()) {
             bar_expect(&sm.qfull[slot], HALVES * a.tq * a.G * 128 + a.withheld);
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       while (l0.there) {
         load(l2);
         const int bs = block % kBias;
-        bar_wait(&sm.bempty[bs], ((block / kBias) & 1) ^ 1, sm, a.err);
+        bar_await(&sm.bempty[bs], ((block / kBias) & 1) ^ 1, sm, a.err);
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
           sm.bias[bs][lane + 32 * k] = l0.x[k] == -INFINITY ? -INFINITY : -l0.x[k] * kLog2e;
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             kslot[w] = 0;
             kphase[w] ^= 1;
           }
-          bar_wait(&sm.kfull[w][kslot[w]], kphase[w], sm, a.err);
+          bar_await(&sm.kfull[w][kslot[w]], kphase[w], sm, a.err);
         }
 #pragma unroll 1
         for (int t = pc.t0; t < pc.end; ++t, ++block) {
@@ -567,13 +567,13 @@ __global__ void __launch_bounds__(kSumThreads, 1)
             qslot = 0;
             qphase ^= 1;
           }
-          bar_wait(&sm.qfull[qslot], qphase, sm, a.err);
+          bar_await(&sm.qfull[qslot], qphase, sm, a.err);
           const uint64_t qd = qd0 + qslot * (qbytes / 16);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (w >= pc.k.tiles) continue;
             const int buf = block & 1, bit = 2 * w + buf;
-            bar_wait(&sm.sempty[w][buf], ((sph >> bit) & 1) ^ 1, sm, a.err);
+            bar_await(&sm.sempty[w][buf], ((sph >> bit) & 1) ^ 1, sm, a.err);
             sph ^= 1u << bit;
             tc_after();
             const uint64_t kd = kd0 + (w * a.nk + kslot[w]) * (kSlotBytes / 16);
@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       }
       if (elect_one()) tc_commit(&sm.done);
       __syncwarp();
-      bar_wait(&sm.done, 0, sm, a.err);
+      bar_await(&sm.done, 0, sm, a.err);
     }
   }
   // ---- pairs of tiles that no token sees: their weights fade ----
