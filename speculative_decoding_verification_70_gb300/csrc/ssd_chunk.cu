@@ -1049,8 +1049,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned there = __ballot_sync(0xffffffffu, o != kFar);
     if (lane == 0) sm.plain[tid >> 5] = there;
   }
-  // rows of the ring that no copy writes are zeros (they meet P = 0, and must not be NaN)
-  if (a.cover < kTile) {
+  // Rows between pages are zeros (they meet P = 0, and must not be NaN): in an edge tile the
+  // pages that nobody sees are not copied, and nothing clears their rows that are no slot.
+  if (a.holes) {
     for (int i = tid; i < (a.nk + a.nv) * kSlotBytes / 16; i += kThreads)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
     fence_async();

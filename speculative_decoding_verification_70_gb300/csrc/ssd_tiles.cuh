@@ -13,7 +13,6 @@ struct PageTiles {
   int box, ppt, tk, tpp;   // rows of a TMA box, pages a tile, slots a tile, tiles a page
   int fold;                // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
   int group, half;         // bytes from 8 slots of a tile to the next, from half to half
-  int cover;               // rows of a tile that TMA writes
   int holes;               // tiles have rows that are no slot, the same in each
   int uneven;              // tiles that differ: pages above 128 slots whose last tile is not full
 };
@@ -108,7 +107,6 @@ inline bool page_tiles(PageTiles& a, const KvView& kv, int dtype, int D, CUtenso
     a.ppt = kTile / a.box;
     a.tk = a.ppt * a.ps;
     a.tpp = 1;
-    a.cover = a.ppt * a.box;
     a.holes = a.tk != kTile;
     a.uneven = 0;
   } else {
@@ -116,7 +114,6 @@ inline bool page_tiles(PageTiles& a, const KvView& kv, int dtype, int D, CUtenso
     a.ppt = 1;
     a.tk = kTile;
     a.tpp = (a.ps + kTile - 1) / kTile;
-    a.cover = kTile;
     a.holes = 0;
     a.uneven = a.ps % kTile != 0;
   }

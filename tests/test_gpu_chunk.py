@@ -210,3 +210,14 @@ def test_same_bits_every_call_and_in_a_graph(gpu_lib):
             r = lib.ssd_chunk_attention(*args, **kw)
             assert torch.equal(r["out"], first[0]) and torch.equal(r["lse"], first[1])
             assert lib.get_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("N", [1, 24, 200])
+def test_nothing_of_an_earlier_kernel_stays_in_shared_memory(gpu_lib, N):
+    """Pages of 5: the rows between them, in tiles of which the window leaves few pages, after a
+    call that filled every CTA's shared memory with NaN."""
+    c = case(8, N, 20, 4, 128, 16, 3000, FP, 16, fill="random")
+    c["v_cache"][:] = math.nan
+    c["k_cache"][:] = math.nan
+    attend(gpu_lib, c)
+    check(gpu_lib, case(22, N, 20, 4, 128, 5, tuple(i * 61 for i in range(22)), FP, 17, order="head"), 128, 1)
