@@ -746,38 +746,39 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
   Pieces pc;
   pc.start(a, sm);
   bool bad_page = false;
-  int tv = 0, p0v = 0, p1v = 0, idv = 0, hv = 0;  // the tile whose values are to come
+  int s0v = 0, p0v = 0, p1v = 0, idv = 0, hv = 0;  // the tile whose values are to come
   bool pending = false;
 #pragma unroll 1
   while (pc.next(a)) {
     const int* trow = a.table + pc.b * a.table_stride;
-    // pages of a tile that hold something seen, and this lane's page id
-    auto lookup = [&](int t, int& p0, int& p1) {
+    // boxes of a tile that hold something seen, and this lane's page id
+    auto lookup = [&](int t, int& p0, int& p1, int& s0) {
       int id = 0;
       p0 = p1 = 0;
-      if (a.ps <= kTile) {
-        p1 = a.ppt - 1;
+      if (!a.uneven) {
+        p1 = a.boxes - 1;
         if (pc.k.edge(t)) {
           const int first = t * a.tk, end = first + a.tk;
           const int last = min(end - 1, end > pc.s.lo ? pc.s.p1 : pc.s.sk - 1);
-          p0 = first < pc.s.sk ? 0 : max(0, pc.s.lo - first) / a.ps;
-          p1 = (last - first) / a.ps;
+          p0 = first < pc.s.sk ? 0 : max(0, pc.s.lo - first) / a.step;
+          p1 = (last - first) / a.step;
         }
       }
       // (not looked at before its tile's turn: the load is on its way meanwhile)
-      if (lane >= p0 && lane <= p1) id = __ldg(trow + (a.ps <= kTile ? t * a.ppt + lane : t / a.tpp));
+      const int place = box_page(a, t, s0);
+      if (lane >= p0 && lane <= p1) id = __ldg(trow + place);
       return id;
     };
-    int p0n, p1n, idn = lookup(pc.tile(pc.t0), p0n, p1n);
+    int p0n, p1n, s0n, idn = lookup(pc.tile(pc.t0), p0n, p1n, s0n);
 #pragma unroll 1
     for (int at = pc.t0; at < pc.end; ++at) {
-      const int t = pc.tile(at), id = idn, p0 = p0n, p1 = p1n;
-      if (at + 1 < pc.end) idn = lookup(pc.tile(at + 1), p0n, p1n);
-      if (KEYS) bad_page |= !load_tile<D>(a, sm, rk, t, p0, p1, id, pc.h, a.err, a.withheld);
-      if (VALUES && !KEYS) bad_page |= !load_tile<D>(a, sm, rv, t, p0, p1, id, pc.h, a.err, a.withheld);
+      const int id = idn, p0 = p0n, p1 = p1n, s0 = s0n;
+      if (at + 1 < pc.end) idn = lookup(pc.tile(at + 1), p0n, p1n, s0n);
+      if (KEYS) bad_page |= !load_tile<D>(a, sm, rk, p0, p1, id, s0, pc.h, a.err, a.withheld);
+      if (VALUES && !KEYS) bad_page |= !load_tile<D>(a, sm, rv, p0, p1, id, s0, pc.h, a.err, a.withheld);
       if (VALUES && KEYS) {
-        if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv, a.err, a.withheld);
-        tv = t;
+        if (pending) load_tile<D>(a, sm, rv, p0v, p1v, idv, s0v, hv, a.err, a.withheld);
+        s0v = s0;
         p0v = p0;
         p1v = p1;
         idv = id;
@@ -786,7 +787,7 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
       }
     }
   }
-  if (pending) load_tile<D>(a, sm, rv, tv, p0v, p1v, idv, hv, a.err, a.withheld);
+  if (pending) load_tile<D>(a, sm, rv, p0v, p1v, idv, s0v, hv, a.err, a.withheld);
   if (bad_page) atomicOr(a.err, kErrBadPage);
 }
 
@@ -1245,7 +1246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int r = lane; r < kTile; r += 32) {
               const int o = sm.off[r], s = first + o;
-              if (a.ps <= kTile ? o == kFar : o >= count) continue;  // zeros
+              if (o >= count) continue;  // zeros
               if (all(a, pc.s, s, s)) continue;
               uint4* line = reinterpret_cast<uint4*>(V + (r >> 3) * a.group + (r & 7) * 128);
               const int half = a.half / 16;

@@ -244,10 +244,10 @@ inline bool encode_rows(CUtensorMap* m, void* base, int dtype, int D, int ps, in
 }
 
 // Groups of 8 slots a page apart, where the cache's strides make the slots of
-// all pages one sequence of such groups; 0 where they don't, or where a tile
-// could run over a page's end.
-inline long long page_groups(int ps, int pages, long long slot, long long page) {
-  if (ps % 8 != 0 || (ps > kTile && ps % kTile != 0) || (ps < kTile && kTile % ps != 0)) return 0;
+// all pages one sequence of such groups; 0 where they don't, or where a box (0: a
+// page's part of a tile) could run over a page's end.
+inline long long page_groups(int ps, int pages, long long slot, long long page, int box = 0) {
+  if (box ? ps % box != 0 : ps % 8 != 0 || (ps > kTile && ps % kTile != 0) || (ps < kTile && kTile % ps != 0)) return 0;
   if (page % (8 * slot) != 0) return 0;
   const long long g = page / (8 * slot);
   return g >= ps / 8 && g * (pages + 1ll) < (1ll << 31) ? g : 0;

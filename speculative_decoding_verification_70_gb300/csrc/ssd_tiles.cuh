@@ -10,22 +10,24 @@ struct PageTiles {
   const int* table;
   long long table_stride;
   int width, pages, ps;
-  int box, ppt, tk, tpp;   // rows of a TMA box, pages a tile, slots a tile, tiles a page
+  int box, boxes;          // rows of a TMA box, boxes of a tile
+  int step, tk;            // slots of a box, of a tile
+  int tpp;                 // (uneven) tiles a page
   int fold;                // copies of whole groups of 8 slots: groups a page (0: rows of 64-column halves)
   int group, half;         // bytes from 8 slots of a tile to the next, from half to half
   int holes;               // tiles have rows that are no slot, the same in each
-  int uneven;              // tiles that differ: pages above 128 slots whose last tile is not full
+  int uneven;              // tiles that differ: a page's tiles of 128 slots and a rest
 };
 
 constexpr int kFar = 1 << 30;  // offset of a row that is no slot
 
 __device__ __forceinline__ int tile_of(const PageTiles& a, int slot) {
-  if (a.ps > kTile) return (slot / a.ps) * a.tpp + (slot % a.ps) / kTile;
+  if (a.uneven) return (slot / a.ps) * a.tpp + (slot % a.ps) / kTile;
   return a.tk == kTile ? slot / kTile : slot / a.tk;
 }
 // First slot of tile t, and how many it holds.
 __device__ __forceinline__ void tile_slots(const PageTiles& a, int t, int& first, int& count) {
-  if (a.ps <= kTile) {
+  if (!a.uneven) {
     first = t * a.tk;
     count = a.tk;
   } else {
@@ -35,11 +37,22 @@ __device__ __forceinline__ void tile_slots(const PageTiles& a, int t, int& first
   }
 }
 
-// Offset of a tile's row from its first slot (pages above 128 slots: below the tile's count).
+// Offset of a tile's row from its first slot (uneven: a slot's below the tile's count).
 __device__ __forceinline__ int row_offset(const PageTiles& a, int row) {
-  if (a.ps > kTile) return row;
+  if (!a.holes) return row;
   const int p = row / a.box, r = row - p * a.box;
-  return p < a.ppt && r < a.ps ? p * a.ps + r : kFar;
+  return p < a.boxes && r < a.ps ? p * a.ps + r : kFar;
+}
+
+// This lane's box of tile t: its page's place in the table, and its first slot there.
+__device__ __forceinline__ int box_page(const PageTiles& a, int t, int& s0) {
+  if (a.uneven) {
+    s0 = (t % a.tpp) * kTile;
+    return t / a.tpp;
+  }
+  const unsigned slot = static_cast<unsigned>(t) * a.tk + (threadIdx.x & 31) * a.step, p = slot / a.ps;
+  s0 = slot - p * a.ps;
+  return p;
 }
 
 __device__ __forceinline__ int seq_tokens(const PageTiles& a, const NodesView& nodes, int b, int& ctx, bool& bad) {
@@ -51,7 +64,7 @@ __device__ __forceinline__ int seq_tokens(const PageTiles& a, const NodesView& n
 // ---------------------------------------------------------------------------
 // copies
 // ---------------------------------------------------------------------------
-// A ring's next tile: whole pages, of which the seen ones come.
+// A ring's next tile: boxes p0 .. p1, this lane's from slot s0 of page id.
 struct Ring {
   const CUtensorMap* map;
   uint64_t *full, *empty;
@@ -60,11 +73,10 @@ struct Ring {
   uint32_t phase;
 };
 template <int D, class Misc>
-__device__ __forceinline__ bool load_tile(const PageTiles& a, Misc& sm, Ring& r, int t, int p0, int p1, int id, int h, int* err,
-                                          int withheld) {
+__device__ __forceinline__ bool load_tile(const PageTiles& a, Misc& sm, Ring& r, int p0, int p1, int id, int s0, int h,
+                                          int* err, int withheld) {
   constexpr int HALVES = D / 64, kSlotBytes = HALVES * kHalf;
   const int lane = threadIdx.x & 31;
-  const int s0 = a.ps <= kTile ? 0 : (t % a.tpp) * kTile;
   const bool good = static_cast<unsigned>(id) < static_cast<unsigned>(a.pages);
   if (!good) id = a.pages;  // out of bounds: zeros
   const int unit = a.fold ? id * a.fold + s0 / 8 : id;
@@ -78,7 +90,7 @@ __device__ __forceinline__ bool load_tile(const PageTiles& a, Misc& sm, Ring& r,
   if (lane == 0) bar_expect(full, (p1 - p0 + 1) * a.box * 128 * HALVES + withheld);
   __syncwarp();
   const uint32_t dst = r.base + r.slot * kSlotBytes;
-  // a lane a page
+  // a lane a box
   if (lane >= p0 && lane <= p1) {
     if (D == 128 && a.fold) {
       tma_groups(dst + lane * a.box * 256, r.map, unit, h, full);
@@ -100,25 +112,32 @@ inline bool page_tiles(PageTiles& a, const KvView& kv, int dtype, int D, CUtenso
   a.table = kv.table;
   a.table_stride = kv.table_stride;
   a.width = kv.width; a.pages = kv.pages; a.ps = kv.ps;
-  // tiles: whole pages up to 128 slots; boxes of a multiple of 8 rows (the swizzle's
-  // period), what exceeds the page filled with zeros
-  if (a.ps <= kTile) {
-    a.box = (a.ps + 7) / 8 * 8;
-    a.ppt = kTile / a.box;
-    a.tk = a.ppt * a.ps;
-    a.tpp = 1;
-    a.holes = a.tk != kTile;
-    a.uneven = 0;
-  } else {
-    a.box = kTile;
-    a.ppt = 1;
-    a.tk = kTile;
+  // Tiles of 128 slots from boxes that lie in one page: of the largest power of two that
+  // divides the page, at least 8 (the swizzle's period).  Other pages (1, 5, 200 + 1): up to
+  // 128 slots whole pages, what a box of a multiple of 8 rows exceeds them by filled with
+  // zeros; above that a page's tiles of 128 and a rest.  (Boxes of parts of pages against
+  // whole pages, 4096 tokens at 4000, 32 / 8 heads of 64: pages of 24 336 us against 342,
+  // of 48 260 against 409, of 200 336 against 434; 64 single tokens at 4000: 178 us against
+  // 186, 198, 234.)
+  a.box = kTile;
+  while (a.ps % a.box != 0) a.box /= 2;
+  a.holes = a.uneven = 0;
+  a.step = a.box;
+  a.boxes = kTile / a.box;
+  a.tk = kTile;
+  a.tpp = 1;
+  if (a.box < 8) {
+    a.uneven = a.ps > kTile;
+    a.holes = !a.uneven;
+    a.box = a.uneven ? kTile : (a.ps + 7) / 8 * 8;
+    a.boxes = kTile / a.box;
+    a.step = a.uneven ? kTile : a.ps;
+    a.tk = a.boxes * a.step;
     a.tpp = (a.ps + kTile - 1) / kTile;
-    a.holes = 0;
-    a.uneven = a.ps % kTile != 0;
   }
-  const long long gk = page_groups(a.ps, a.pages, kv.k_slot, kv.k_page);
-  const long long gv = mv ? page_groups(a.ps, a.pages, kv.v_slot, kv.v_page) : gk;
+  const int whole = a.holes || a.uneven ? 0 : a.box;
+  const long long gk = page_groups(a.ps, a.pages, kv.k_slot, kv.k_page, whole);
+  const long long gv = mv ? page_groups(a.ps, a.pages, kv.v_slot, kv.v_page, whole) : gk;
   a.fold = D == 128 && gk == gv ? static_cast<int>(gk) : 0;
   a.group = a.fold ? 2048 : 1024;
   a.half = a.fold ? 1024 : kHalf;

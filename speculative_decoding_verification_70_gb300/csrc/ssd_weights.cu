@@ -469,10 +469,10 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       const int w = warp == 20;
       Ring rk = {&mapk, sm.kfull[w], sm.kempty[w], sptr(ring) + w * a.nk * kSlotBytes, a.nk, -1, 0};
       bool bad_page = false;
-      // an item's tile: the pages that hold slots, and this lane's page id, on its way
+      // an item's tile: the boxes that hold slots, and this lane's page id, on its way
       // while the tile of the item before is copied
       struct Tile {
-        int t, h, pl, id;
+        int t, h, pl, id, s0;
       };
       auto lookup = [&](Tile& x) {
         x.t = -1;
@@ -484,8 +484,9 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         x.id = 0;
         int first, count;
         tile_slots(a, x.t, first, count);
-        x.pl = a.ps <= kTile ? min(a.ppt - 1, (pc.ctx + pc.n - 1 - first) / a.ps) : 0;
-        if (lane <= x.pl) x.id = __ldg(a.table + pc.b * a.table_stride + (a.ps <= kTile ? x.t * a.ppt + lane : x.t / a.tpp));
+        x.pl = a.uneven ? 0 : min(a.boxes - 1, (pc.ctx + pc.n - 1 - first) / a.step);
+        const int place = box_page(a, x.t, x.s0);
+        if (lane <= x.pl) x.id = __ldg(a.table + pc.b * a.table_stride + place);
       };
       Tile cur, nxt;
       lookup(nxt);
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
       while (nxt.t >= 0) {
         cur = nxt;
         lookup(nxt);
-        bad_page |= !load_tile<D>(a, sm, rk, cur.t, 0, cur.pl, cur.id, cur.h, a.err, a.withheld);
+        bad_page |= !load_tile<D>(a, sm, rk, 0, cur.pl, cur.id, cur.s0, cur.h, a.err, a.withheld);
       }
       if (bad_page) atomicOr(a.err, kErrBadPage);
     } else if (warp == 3) {
@@ -728,7 +729,7 @@ cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, int D, cudaStre
       !encode_queries(&mq, p.q, p.q_b, p.q_n, p.q_h, p.Hq, p.nodes, p.G, dtype, D, a.tq))
     return cudaErrorInvalidValue;
   const long long slots = most < p.w_len ? most : p.w_len;
-  const long long tiles = a.ps <= kTile ? (slots + a.tk - 1) / a.tk : (slots / a.ps + 1) * a.tpp;
+  const long long tiles = !a.uneven ? (slots + a.tk - 1) / a.tk : (slots / a.ps + 1) * a.tpp;
   a.NP = static_cast<int>((tiles + 1) / 2);
   // as many tiles of K as fit beside the blocks of Q (two of 32 KB: a third would leave one
   // slot a ring of K)

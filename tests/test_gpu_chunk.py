@@ -221,3 +221,12 @@ def test_nothing_of_an_earlier_kernel_stays_in_shared_memory(gpu_lib, N):
     c["k_cache"][:] = math.nan
     attend(gpu_lib, c)
     check(gpu_lib, case(22, N, 20, 4, 128, 5, tuple(i * 61 for i in range(22)), FP, 17, order="head"), 128, 1)
+
+
+@pytest.mark.parametrize("page", [2, 12, 40, 72, 130, 136, 201])
+def test_page_sizes(gpu_lib, page):
+    """Pages whose parts make a tile, ones that need whole pages, and both kinds above 128."""
+    for N, D, order in ((1, 64, "slot"), (60, 128, "slot"), (60, 128, "head"), (210, 64, "slot")):
+        c = case(3, N, 8, 2, D, page, (0, 131, 620), BF, page, order=order)
+        check(gpu_lib, c)
+        check(gpu_lib, c, 150, 9)
