@@ -547,7 +547,10 @@ __device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, 
 
 // Few rows (64 at most): they lie in the row tile two or four times, and a copy takes its
 // part of a tile's slots alone, so that a thread has 64 or 32 scores instead of 128.  The
-// copies have their own m, l and O, which are joined at the item's end.
+// copies have their own m, l and O, which are joined at the item's end.  With heads of 64
+// (whose tiles come in half the time) the warpgroups take turns within an item, as copies
+// of each other, and the O's of two items lie side by side in tensor memory; with heads of
+// 128 each has its own items.
 template <class T, int D>
 __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tmem, char* stage, int w) {
   const int wt = threadIdx.x & 127, span = kTile / a.copies;
@@ -555,7 +558,11 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
   const int copy = wt / span, r = wt - copy * span, nq = span / 32, q0 = copy * nq;  // its quarters of the slots
   const int tok = r / a.G, g = r - tok * a.G;
   const f32x2 c2 = pk2(a.c, a.c);
-  const uint32_t tO = tmem + lanes + 256 + w * D;
+  constexpr bool ALT = D == 64;
+  auto sync = [&]() {
+    if (ALT) named_sync(1, 256);
+    else named_sync(1 + w, 128);
+  };
   uint32_t ppv = 0;    // phase of pvdone[w]
   uint32_t sph = 0;    // phases of sfull[w][.]
   int tiles = 0, item = -1;
@@ -564,10 +571,11 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
 #pragma unroll 1
   while (pc.next(a)) {
     ++item;
-    if ((item & 1) != w) {
+    if (!ALT && (item & 1) != w) {
       tiles += pc.end - pc.t0;
       continue;
     }
+    const uint32_t tO = tmem + lanes + 256 + (ALT ? (item & 1) * 2 + w : w) * D;
     const int i = pc.blk * a.tpi + tok, pos = pc.ctx + i;
     const bool valid = tok < a.tq && i < pc.n;
     float m = kNoScore, l = 0.f;
@@ -578,6 +586,7 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       const int t = pc.tile(at);
       const bool edge = pc.k.edge(t);
       edges |= edge;
+      if (ALT && (tiles & 1) != w) continue;
       const int buf = tiles & 1;
       bar_wait(&sm.sfull[w][buf], (sph >> buf) & 1, sm, a.err);
       sph ^= 1u << buf;
@@ -670,19 +679,22 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
     }
 
     // ---- end of the piece: the copies joined ----
-    bar_wait(&sm.pvdone[w], ppv, sm, a.err);
-    ppv ^= 1;
-    tc_after();
+    if (jobs > 0) {
+      bar_wait(&sm.pvdone[w], ppv, sm, a.err);
+      ppv ^= 1;
+      tc_after();
+    }
+    const int line0 = ALT ? w * 128 + wt : wt, lines = ALT ? 256 : 128;  // this thread's; of all copies
     float2* ml = reinterpret_cast<float2*>(stage);
-    ml[wt] = make_float2(m, l);
-    named_sync(1 + w, 128);
+    ml[line0] = make_float2(m, l);
+    sync();
     float M = kNoScore, L = 0.f;
-    for (int k = 0; k < a.copies; ++k) M = fmaxf(M, ml[k * span + r].x);
-    for (int k = 0; k < a.copies; ++k) {
-      const float2 x = ml[k * span + r];
+    for (int k = r; k < lines; k += span) M = fmaxf(M, ml[k].x);
+    for (int k = r; k < lines; k += span) {
+      const float2 x = ml[k];
       L += x.x == M ? x.y : x.y * ex2_fast(x.x - M);
     }
-    named_sync(1 + w, 128);
+    sync();
     const float f = m == M ? 1.f : ex2_fast(m - M);
     const bool direct = pc.direct(), empty = L == 0.f, out_row = valid && copy == 0;
     const float inv = !direct ? 1.f : empty ? 0.f : 1.f / L;
@@ -694,7 +706,7 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
 #pragma unroll
       for (int q = 0; q < 16; ++q) any |= fl[q];
     }
-    uint4* line = reinterpret_cast<uint4*>(stage + wt * 128);
+    uint4* line = reinterpret_cast<uint4*>(stage + line0 * 128);
 #pragma unroll 1
     for (int k = 0; k < D; k += 32) {
       uint32_t o[32];
@@ -702,16 +714,19 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       tm_wait_loads();
       tm_tie32(o);
 #pragma unroll
-      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+      for (int e = 0; e < 32; ++e) o[e] = jobs > 0 ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
 #pragma unroll
       for (int q = 0; q < 8; ++q) line[q ^ (wt & 7)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-      named_sync(1 + w, 128);
-      if (out_row) {
-        for (int c = 1; c < a.copies; ++c) {
-          const uint4* other = reinterpret_cast<const uint4*>(stage + (c * span + r) * 128);
+      sync();
+      if (out_row && (!ALT || k == 32 * w)) {  // (a warpgroup's half of the columns)
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
+#pragma unroll 1
+        for (int c = r; c < lines; c += span) {
+          const uint4* part = reinterpret_cast<const uint4*>(stage + c * 128);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const uint4 x = other[q ^ (wt & 7)];  // (copies lie multiples of 8 rows apart)
+            const uint4 x = part[q ^ (wt & 7)];  // (copies lie multiples of 8 rows apart)
             const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -725,10 +740,11 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
         if (any) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pos, fl, k, o);
         write_columns<T, D>(a, o, row, k, direct, empty, inv);
       }
-      named_sync(1 + w, 128);
+      sync();
     }
     tc_before();
-    bar_arrive(&sm.ofree[w]);
+    bar_arrive(&sm.ofree[item & 1]);
+    if (ALT && w == 1) continue;
     if (out_row && direct && a.lse) a.lse[row] = empty ? -INFINITY : log_sum<T>(M, L);
     if (out_row && !direct) a.part_ml[row] = make_float2(M, L);
   }
@@ -796,7 +812,7 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
 // ---------------------------------------------------------------------------
 // Two row tiles: a warp each, so that one's waits pass beside the other's products (a
 // wait costs 100 cycles at least, and few products queue up).  One row tile: one warp.
-template <class T, int D, bool WIDE>
+template <class T, int D, bool WIDE, bool ALT>
 __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t tmem, uint32_t ring, uint32_t ringv,
                                              uint32_t Q, int w) {
   constexpr int kSlotBytes = D / 64 * kHalf;
@@ -805,7 +821,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
   const uint64_t vd0 = operand(ringv, D == 128 ? a.half : 0, a.group);
   const uint32_t ids = instr<T>(kTile, false, false, a.negate), ido = instr<T>(D, false, true);
   struct Step {
-    bool valid, newq, last, edge, act, begin, final;
+    bool valid, newq, last, edge, act, begin, fresh, final;  // (fresh: O's first product)
     int item, no;  // the item; the tile's number in the CTA
   };
   Pieces pc;
@@ -851,6 +867,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
     st.act = acting(t);
     st.final = !WIDE || at == lasting;
     st.begin = st.act && !started;
+    st.fresh = ALT ? at < pc.t0 + 2 : st.begin;
     started |= st.act;
   };
   int kslot = -1, vslot = -1, edges = 0;
@@ -876,7 +893,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
         for (int k = 0; k < D / 16; ++k)
           tc_mma(tmem + buf * 128, qd + (k / 4) * (kHalf / 16) + (k & 3) * 2, kd + (k / 4) * khalf + (k & 3) * 2, ids,
                  k > 0);
-        tc_commit(&sm.sfull[WIDE ? w : st.item & 1][buf]);  // (each warpgroup has its own: it skips items)
+        tc_commit(&sm.sfull[WIDE ? w : ALT ? buf : st.item & 1][buf]);  // (each warpgroup has its own: it skips items)
         tc_commit(&sm.kempty[kslot]);
         if (st.last) tc_commit(qempty);
       }
@@ -909,13 +926,14 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
   };
   auto values = [&](const Step& st) {
     const int buf = WIDE ? w : st.no & 1, ob = WIDE ? w : st.item & 1;
+    const uint32_t tO = tmem + 256 + (ALT ? ob * 2 + buf : ob) * D;
     if (st.act) {
       const uint64_t vd = vd0 + vslot * (kSlotBytes / 16);
       tc_after();
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
-          tc_mma_ta(tmem + 256 + ob * D, tmem + buf * 128 + k * 8, vd + k * vstep, ido, !st.begin || k > 0);
+          tc_mma_ta(tO, tmem + buf * 128 + k * 8, vd + k * vstep, ido, !st.fresh || k > 0);
       }
       __syncwarp();
       bar_await(&sm.pfull[buf][1], ph, sm, a.err);
@@ -923,8 +941,8 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
       if (elect_one()) {
 #pragma unroll
         for (int k = kTile / 32; k < kTile / 16; ++k)
-          tc_mma_ta(tmem + 256 + ob * D, tmem + buf * 128 + k * 8, vd + k * vstep, ido, true);
-        if (st.final) tc_commit(&sm.pvdone[ob]);
+          tc_mma_ta(tO, tmem + buf * 128 + k * 8, vd + k * vstep, ido, true);
+        if (st.final) tc_commit(&sm.pvdone[ALT ? buf : ob]);
         tc_commit(&sm.vempty[vslot]);
       }
     } else if (elect_one()) {
@@ -1024,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&sm.pfull[i][0], 128);  // (halves of the slots)
       bar_init(&sm.pfull[i][1], 128);
       bar_init(&sm.pvdone[i], 1);
-      bar_init(&sm.ofree[i], 128);
+      bar_init(&sm.ofree[i], MODE == kCopies && D == 64 ? 256 : 128);
     }
     for (int i = 0; i < kEdgeBars; ++i) bar_init(&sm.vready[i], 1);
     bar_init(&sm.done, WIDE ? 2 : 1);
@@ -1181,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = (warp - 4) >> 2;
-    if constexpr (MODE == kCopies) share_role<T, D>(a, sm, tmem, stage + w * (kStage / 2), w);
+    if constexpr (MODE == kCopies) share_role<T, D>(a, sm, tmem, D == 64 ? stage : stage + w * (kStage / 2), w);
     else softmax_role<T, D, WIDE>(a, sm, tmem, w);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
@@ -1190,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (!WIDE && warp == 2) {
       load_role<D, false, true>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
     } else if (warp == 1 || warp == 2) {
-      product_role<T, D, WIDE>(a, sm, tmem, sptr(ring), sptr(ringv), sptr(Q), warp - 1);
+      product_role<T, D, WIDE, MODE == kCopies && D == 64>(a, sm, tmem, sptr(ring), sptr(ringv), sptr(Q), warp - 1);
     } else {
       // ---- Q, and what must not be multiplied ----
       Pieces pq, pc;
@@ -1346,27 +1364,58 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
   float M = kNoScore, L = 0.f, o[E];
 #pragma unroll
   for (int q = 0; q < E; ++q) o[q] = 0.f;
+  // a lane a range, so that few loads wait for one another (8 items in 19 parts each)
 #pragma unroll 1
-  for (int k = pk; k < C; ++k) {
-    if (k > pk) {
-      if (!a.ranges[k].used) continue;
-      if (a.ranges[k].lo >= e) break;
-    }
+  for (int k0 = pk; k0 < C; k0 += 32) {
+    const int k = k0 + lane;
+    const int used = k < C ? a.ranges[k].used : 0;
+    const long long lo = k < C ? a.ranges[k].lo : 0;
+    const bool in = used && (k == pk || lo < e);
     // only the first can be its CTA's last piece
     const long long at = (2ll * k + (k == pk && before < s ? 1 : 0)) * cap + r;
-    const float2 ml = a.part_ml[at];
-    if (ml.y == 0.f) continue;
-    float v[E];
+    const float2 ml = in ? a.part_ml[at] : make_float2(kNoScore, 0.f);
+    unsigned parts = __ballot_sync(0xffffffffu, ml.y != 0.f);
+    const bool last = __any_sync(0xffffffffu, used && !in);
+    if (parts) {
+      float m = ml.y != 0.f ? fmaxf(M, ml.x) : M;
 #pragma unroll
-    for (int q = 0; q < E; ++q) v[q] = a.part_o[at * D + lane * E + q];
-    const float m = fmaxf(M, ml.x);
-    // (at least the smallest number: an infinite value stays infinite)
-    const float x = ml.x == m ? 1.f : fmaxf(exp2f(ml.x - m), 0x1p-126f), y = M == m ? 1.f : fmaxf(exp2f(M - m), 0x1p-126f);
-    const float yo = L == 0.f ? 0.f : y;
-    L = L * yo + ml.y * x;
+      for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      // (at least the smallest number: an infinite value stays infinite)
+      const float x = ml.x == m ? 1.f : fmaxf(exp2f(ml.x - m), 0x1p-126f);
+      const float y = L == 0.f ? 0.f : M == m ? 1.f : fmaxf(exp2f(M - m), 0x1p-126f);
+      L *= y;
 #pragma unroll
-    for (int q = 0; q < E; ++q) o[q] = fmaf(v[q], x, o[q] * yo);
-    M = m;
+      for (int q = 0; q < E; ++q) o[q] *= y;
+      M = m;
+      while (parts) {
+        float w[4], v[4][E];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int from = __ffs(parts) - 1;
+          const float wu = __shfl_sync(0xffffffffu, x, from & 31), lu = __shfl_sync(0xffffffffu, ml.y, from & 31);
+          const long long place = __shfl_sync(0xffffffffu, at, from & 31);
+          w[u] = 0.f;
+#pragma unroll
+          for (int q = 0; q < E; ++q) v[u][q] = 0.f;
+          if (from >= 0) {
+            w[u] = wu;
+            L = fmaf(lu, wu, L);
+#pragma unroll
+            for (int q = 0; q < E; q += 2) {
+              const float2 z = *reinterpret_cast<const float2*>(a.part_o + place * D + lane * E + q);
+              v[u][q] = z.x;
+              v[u][q + 1] = z.y;
+            }
+          }
+          parts &= parts - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int q = 0; q < E; ++q) o[q] = fmaf(v[u][q], w[u], o[q]);
+      }
+    }
+    if (last) break;
   }
   const int tok = r / a.G, g = r - tok * a.G;
   const bool empty = L == 0.f;
