@@ -89,16 +89,30 @@ struct Args : PageTiles {
   int withheld;
 };
 
+// What tokens p0 .. p1 (slots) see together: slots < sk and lo .. p1.
+struct Seen {
+  int p0, p1, lo, sk;
+};
+// The tiles of a block: nsk of first tokens, then those from ft on; T in all.  Each of
+// its tokens sees every slot of tiles f0 .. f1 - 1; the others are its edges.
+struct Block {
+  int T, nsk, ft, f0, f1;
+  __device__ __forceinline__ bool edge(int t) const { return t < f0 || t >= f1; }
+};
 struct alignas(16) Misc {
   uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
   uint64_t turn[2], qfull[2], qempty[2], sfull[2][2], pfull[2][2], pvdone[2], ofree[2], vready[kEdgeBars], done;
   long long left;
   int b0, blk0, h0, t0;       // first piece
+  int ctx0, n0;
+  Seen s0;
+  Block k0;
   int cost;                   // of an item beside its tiles
   int pad;                    // some sequence has fewer tokens than N
   unsigned tmem;
   int abort;
   unsigned wait_us;
+  float sums[2][kTile / 2];   // l of an item's rows (copies)
   unsigned flags[kFlagSets][16];  // slots with NaN or infinite values that some rows see
   alignas(16) int off[kTile]; // offset of a tile's row from its first slot; far: no slot
   unsigned plain[4];          // rows of a tile that are slots (pages of up to 128)
@@ -109,10 +123,6 @@ static_assert(sizeof(Misc) <= 3 * 1024, "shared memory beside rings and Q");
 // ---------------------------------------------------------------------------
 // tiles, blocks, pieces
 // ---------------------------------------------------------------------------
-// What tokens p0 .. p1 (slots) see together: slots < sk and lo .. p1.
-struct Seen {
-  int p0, p1, lo, sk;
-};
 __device__ __forceinline__ Seen seen_by(const Args& a, int p0, int p1) {
   Seen s;
   s.p0 = p0;
@@ -129,12 +139,6 @@ __device__ __forceinline__ bool all(const Args& a, const Seen& s, int first, int
   return last <= s.p0 && (a.window == 0 || first > s.p1 - a.window || last < a.sinks);
 }
 
-// The tiles of a block: nsk of first tokens, then those from ft on; T in all.  Each of
-// its tokens sees every slot of tiles f0 .. f1 - 1; the others are its edges.
-struct Block {
-  int T, nsk, ft, f0, f1;
-  __device__ __forceinline__ bool edge(int t) const { return t < f0 || t >= f1; }
-};
 __device__ __forceinline__ Block block_of(const Args& a, const Seen& s) {
   Block k;
   k.ft = s.lo > 0 ? tile_of(a, s.lo) : 0;
@@ -163,7 +167,7 @@ struct Pieces {
     s = block_seen(a, ctx, n, blk);
     k = block_of(a, s);
   }
-  __device__ __forceinline__ void start(const Args& a, const Misc& sm) {
+  __device__ __forceinline__ void start(const Misc& sm) {
     left = sm.left;
     w = sm.cost;
     b = sm.b0;
@@ -171,11 +175,10 @@ struct Pieces {
     h = sm.h0;
     t0 = sm.t0;
     fresh = true;
-    if (left > 0) {
-      bool bad;
-      n = seq_tokens(a, a.nodes, b, ctx, bad);
-      load(a);
-    }
+    ctx = sm.ctx0;
+    n = sm.n0;
+    s = sm.s0;
+    k = sm.k0;
   }
   __device__ __forceinline__ bool direct() const { return t0 == 0 && end == k.T; }
   __device__ __forceinline__ int tile(int i) const { return i < k.nsk ? i : k.ft + i - k.nsk; }
@@ -252,10 +255,10 @@ __device__ __forceinline__ int flag_slot(const Args& a, const Seen& s, int i) {
   return i < 256 ? s.p0 + i : s.p0 - a.window + 1 + (i - 256);
 }
 
-// Entries k .. k + 31 of the values that are not finite, for a row that sees them.
-template <class T>
+// N entries from k on of the values that are not finite, for a row that sees them.
+template <class T, int N>
 __device__ __forceinline__ void add_nonfinite(const Args& a, int b, int h, const Seen& s, int pos, const unsigned* fl, int k,
-                                              uint32_t (&o)[32]) {
+                                              uint32_t (&o)[N]) {
 #pragma unroll 1
   for (int q = 0; q < 16; ++q) {
 #pragma unroll 1
@@ -267,7 +270,7 @@ __device__ __forceinline__ void add_nonfinite(const Args& a, int b, int h, const
       const uint32_t* v =
           reinterpret_cast<const uint32_t*>(a.vcache + 2 * (page * a.v_page + off * a.v_slot + h * a.v_head + k));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < N / 2; ++e) {
         const uint32_t x = v[e];
         const float lo = T::lo(x), hi = T::hi(x);
         if (!(fabsf(lo) < INFINITY)) o[2 * e] = __float_as_uint(__uint_as_float(o[2 * e]) + lo);
@@ -304,24 +307,28 @@ __device__ __forceinline__ void scale_columns(uint32_t at, float f) {
   }
 }
 
-// Columns k .. k + 31 of a row: results, or a part.
-template <class T, int D>
-__device__ __forceinline__ void write_columns(const Args& a, const uint32_t (&o)[32], long long row, int k, bool direct,
+// N columns of a row from k on: results, or a part.
+template <class T, int D, int N>
+__device__ __forceinline__ void write_columns(const Args& a, const uint32_t (&o)[N], long long row, int k, bool direct,
                                               bool empty, float inv) {
   if (direct) {
-    uint4* out = reinterpret_cast<uint4*>(a.out + 2 * (row * D + k));
+    uint2* out = reinterpret_cast<uint2*>(a.out + 2 * (row * D + k));
+    uint32_t y[N / 2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t y[4];
+    for (int e = 0; e < N / 2; ++e)
+      y[e] = empty ? 0u : T::pack(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+    if (N % 8 == 0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        y[e] = empty ? 0u : T::pack(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv);
-      out[q] = make_uint4(y[0], y[1], y[2], y[3]);
+      for (int q = 0; q < N / 8; ++q)
+        reinterpret_cast<uint4*>(out)[q] = make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) out[q] = make_uint2(y[2 * q], y[2 * q + 1]);
     }
   } else {
     uint4* out = reinterpret_cast<uint4*>(a.part_o + row * D + k);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) out[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    for (int q = 0; q < N / 4; ++q) out[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
   }
 }
 
@@ -342,7 +349,7 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
   uint32_t sph = 0;    // phases of sfull[w][.]
   int tiles = 0, item = -1;
   Pieces pc;
-  pc.start(a, sm);
+  pc.start(sm);
 #pragma unroll 1
   while (pc.next(a)) {
     ++item;
@@ -513,14 +520,14 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-// Entries k .. k + 31 of a row that came out NaN or infinite because a slot that every row
+// N entries from k on of a row that came out NaN or infinite because a slot that every row
 // sees holds such a value, which met other copies' weights of 0 as well: what the values
 // alone make of them.
-template <class T>
-__device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, int k, uint32_t (&o)[32]) {
-  float x[32];
+template <class T, int N>
+__device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, int k, uint32_t (&o)[N]) {
+  float x[N];
 #pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] = 0.f;
+  for (int e = 0; e < N; ++e) x[e] = 0.f;
 #pragma unroll 1
   for (int at = pc.t0; at < pc.end; ++at) {
     int first, count;
@@ -533,7 +540,7 @@ __device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, 
       const uint32_t* v =
           reinterpret_cast<const uint32_t*>(a.vcache + 2 * (page * a.v_page + off * a.v_slot + pc.h * a.v_head + k));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
+      for (int e = 0; e < N / 2; ++e) {
         const uint32_t y = v[e];
         if (!(fabsf(T::lo(y)) < INFINITY)) x[2 * e] += T::lo(y);
         if (!(fabsf(T::hi(y)) < INFINITY)) x[2 * e + 1] += T::hi(y);
@@ -541,7 +548,7 @@ __device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, 
     }
   }
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
+  for (int e = 0; e < N; ++e)
     if (!(fabsf(__uint_as_float(o[e])) < INFINITY) && !(fabsf(x[e]) < INFINITY)) o[e] = __float_as_uint(x[e]);
 }
 
@@ -567,7 +574,7 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
   uint32_t sph = 0;    // phases of sfull[w][.]
   int tiles = 0, item = -1;
   Pieces pc;
-  pc.start(a, sm);
+  pc.start(sm);
 #pragma unroll 1
   while (pc.next(a)) {
     ++item;
@@ -684,9 +691,9 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       ppv ^= 1;
       tc_after();
     }
-    const int line0 = ALT ? w * 128 + wt : wt, lines = ALT ? 256 : 128;  // this thread's; of all copies
+    const int id = ALT ? w * 128 + wt : wt, lines = ALT ? 256 : 128;  // this thread; all that work on the item
     float2* ml = reinterpret_cast<float2*>(stage);
-    ml[line0] = make_float2(m, l);
+    ml[id] = make_float2(m, l);
     sync();
     float M = kNoScore, L = 0.f;
     for (int k = r; k < lines; k += span) M = fmaxf(M, ml[k].x);
@@ -694,19 +701,28 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       const float2 x = ml[k];
       L += x.x == M ? x.y : x.y * ex2_fast(x.x - M);
     }
+    const bool direct = pc.direct();
+    auto place = [&](int token, int head) {
+      return direct ? (static_cast<long long>(pc.b) * a.nodes.N + pc.blk * a.tpi + token) * a.Hq + pc.h * a.G + head
+                    : (2ll * blockIdx.x + (item == 0 ? 0 : 1)) * a.tpi * a.G + token * a.G + head;
+    };
+    float* sums = sm.sums[ALT ? 0 : w];
+    if (valid && id < span) {
+      sums[r] = L;
+      const long long row = place(tok, g);
+      if (!direct) a.part_ml[row] = make_float2(M, L);
+      else if (a.lse) a.lse[row] = L == 0.f ? -INFINITY : log_sum<T>(M, L);
+    }
     sync();
     const float f = m == M ? 1.f : ex2_fast(m - M);
-    const bool direct = pc.direct(), empty = L == 0.f, out_row = valid && copy == 0;
-    const float inv = !direct ? 1.f : empty ? 0.f : 1.f / L;
-    const long long row = direct ? (static_cast<long long>(pc.b) * a.nodes.N + i) * a.Hq + pc.h * a.G + g
-                                 : (2ll * blockIdx.x + (item == 0 ? 0 : 1)) * a.tpi * a.G + r;
     const unsigned* fl = sm.flags[item % kFlagSets];
     unsigned any = 0;
     if (edges) {
 #pragma unroll
       for (int q = 0; q < 16; ++q) any |= fl[q];
     }
-    uint4* line = reinterpret_cast<uint4*>(stage + line0 * 128);
+    uint4* line = reinterpret_cast<uint4*>(stage + id * 128);
+    const int quads = min(a.tq, pc.n - pc.blk * a.tpi) * a.G * 8;
 #pragma unroll 1
     for (int k = 0; k < D; k += 32) {
       uint32_t o[32];
@@ -718,35 +734,28 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
 #pragma unroll
       for (int q = 0; q < 8; ++q) line[q ^ (wt & 7)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
       sync();
-      if (out_row && (!ALT || k == 32 * w)) {  // (a warpgroup's half of the columns)
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0;
+      // four columns of a row a thread
 #pragma unroll 1
-        for (int c = r; c < lines; c += span) {
-          const uint4* part = reinterpret_cast<const uint4*>(stage + c * 128);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint4 x = part[q ^ (wt & 7)];  // (copies lie multiples of 8 rows apart)
-            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[4 * q + e] = __float_as_uint(__uint_as_float(o[4 * q + e]) + __uint_as_float(y[e]));
-          }
+      for (int i = id; i < quads; i += lines) {
+        const int rr = i >> 3, q = i & 7, token = rr / a.G;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = rr; c < lines; c += span) {
+          // (copies lie multiples of 8 rows apart)
+          const float4 y = *reinterpret_cast<const float4*>(stage + c * 128 + (q ^ (rr & 7)) * 16);
+          x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
-        bool finite = true;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) finite = finite && fabsf(__uint_as_float(o[e])) < INFINITY;
-        if (!finite) seen_nonfinite<T>(a, pc, k, o);
-        if (any) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pos, fl, k, o);
-        write_columns<T, D>(a, o, row, k, direct, empty, inv);
+        uint32_t z[4] = {__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)};
+        const bool finite = fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY;
+        if (!finite) seen_nonfinite<T>(a, pc, k + 4 * q, z);
+        if (any) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pc.ctx + pc.blk * a.tpi + token, fl, k + 4 * q, z);
+        const float sum = sums[rr];
+        write_columns<T, D>(a, z, place(token, rr - token * a.G), k + 4 * q, direct, sum == 0.f,
+                            !direct ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
       }
       sync();
     }
     tc_before();
     bar_arrive(&sm.ofree[item & 1]);
-    if (ALT && w == 1) continue;
-    if (out_row && direct && a.lse) a.lse[row] = empty ? -INFINITY : log_sum<T>(M, L);
-    if (out_row && !direct) a.part_ml[row] = make_float2(M, L);
   }
 }
 
@@ -760,7 +769,7 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
   const int lane = threadIdx.x & 31;
   Ring rk = {&mapk, sm.kfull, sm.kempty, ring, a.nk, -1, 0}, rv = {&mapv, sm.vfull, sm.vempty, ringv, a.nv, -1, 0};
   Pieces pc;
-  pc.start(a, sm);
+  pc.start(sm);
   bool bad_page = false;
   int s0v = 0, p0v = 0, p1v = 0, idv = 0, hv = 0;  // the tile whose values are to come
   bool pending = false;
@@ -825,7 +834,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
     int item, no;  // the item; the tile's number in the CTA
   };
   Pieces pc;
-  pc.start(a, sm);
+  pc.start(sm);
   int item = -1, at = 0, no = -1, lasting = 0;
   bool started = false, inside = false, some_rows = true;
   // whether this row tile sees some of tile t
@@ -1159,7 +1168,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (long long at = f; at < e; ++at) {
         load(at);
         if (blk * static_cast<long long>(a.tpi) >= n) continue;
-        const int all_t = block_of(a, block_seen(a, ctx, n, blk)).T;
+        const Seen seen = block_seen(a, ctx, n, blk);
+        const Block k = block_of(a, seen);
+        const int all_t = k.T;
         const long long one = all_t + w, end = p + one * a.Hkv;
         if (lo < end) {
           const unsigned long long d = lo > p ? lo - p : 0;
@@ -1182,6 +1193,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               r.T = all_t;
               a.ranges[me] = r;
               sm.left = hi - from;
+              sm.ctx0 = ctx;
+              sm.n0 = n;
+              sm.s0 = seen;
+              sm.k0 = k;
             }
             break;
           }
@@ -1212,8 +1227,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ---- Q, and what must not be multiplied ----
       Pieces pq, pc;
-      pq.start(a, sm);
-      pc.start(a, sm);
+      pq.start(sm);
+      pc.start(sm);
       int nq = 0;
       // the rows of the next item, once the scores of the one before are made
       auto fetch = [&]() {
