@@ -778,8 +778,9 @@ SSD_API int ssd_selftest_node(const int32_t *parent, int n, int j, uint64_t *mas
 
 /*
  * Self-test hook of the bounded waits, process-wide for later calls of
- * ssd_tree_attention and ssd_logprobs: a copy into shared memory that takes
- * longer than limit_us (1 .. 1000000; 0: the default of a second) has failed;
+ * ssd_tree_attention, ssd_chunk_attention, ssd_kv_weights and ssd_logprobs: a copy
+ * into shared memory that takes longer than limit_us (1 .. 1000000; 0: the default
+ * of a second) has failed;
  * withhold != 0: each waits for 16 bytes more than its copy brings, so that every
  * wait runs out.
  */

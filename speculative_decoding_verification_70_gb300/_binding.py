@@ -1076,8 +1076,8 @@ def selftest_exp2(x_hi: torch.Tensor, x_lo: torch.Tensor, stream=None) -> torch.
 
 
 def selftest_copy_wait(limit_us: int = 0, withhold: bool = False):
-    """Let the waits for copies of later ssd_tree_attention and ssd_logprobs calls
-    give up after limit_us microseconds (0: a second); withhold: wait for bytes
+    """Let the waits for copies of later ssd_tree_attention, ssd_chunk_attention,
+    ssd_kv_weights and ssd_logprobs calls give up after limit_us microseconds (0: a second); withhold: wait for bytes
     that no copy brings, so that they run out.  Process-wide."""
     _check("ssd_selftest_copy_wait", load_library().ssd_selftest_copy_wait(int(limit_us), int(withhold)))
 
