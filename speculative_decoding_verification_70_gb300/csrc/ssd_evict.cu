@@ -145,12 +145,12 @@ __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int uni
       int4 v;
       if (cluster > 1) {
         const int share = kBins / cluster;
-        if (tid < share) {
+        for (int i = rank * share + tid; i < (rank + 1) * share; i += kEvictThreads) {
           int x = 0;
 #pragma unroll
           for (int r = 0; r < kMaxCluster; ++r)
-            if (r < cluster) x += far_int(of_rank(&sm.hist[rank * share + tid], r));
-          sm.tot[rank * share + tid] = x;
+            if (r < cluster) x += far_int(of_rank(&sm.hist[i], r));
+          sm.tot[i] = x;
         }
         cluster_sync();
         v = far_int4(of_rank(&sm.tot[at], at / share));

@@ -7,7 +7,7 @@ import torch
 
 import chunk_reference as cref
 import target_reference as ref
-from test_gpu_budget import add_weights, check_weights
+from test_gpu_budget import add_weights, check_evict, check_weights, evict_case
 from test_gpu_chunk import attend, case, check
 from test_gpu_target import _same
 from test_gpu_waits import withheld  # noqa: F401  (a fixture)
@@ -197,3 +197,13 @@ def test_a_budgeted_cache_from_prompt_to_decoding(gpu_lib, D, order):
     cut()
     tokens(1, 1)
     assert all(lib.get_device_error(w) == 0 for w in tables)
+
+
+@pytest.mark.parametrize("ctx", [4094, 4500, 8190, 9000, 16500])
+@pytest.mark.parametrize("layers,Hkv", [(1, 1), (5, 8), (19, 4), (19, 8), (20, 8)])
+def test_cuts_of_all_numbers_of_heads(gpu_lib, layers, Hkv, ctx):
+    """From one head to more than there are SMs, at lengths where the CTAs that choose a head's
+    slots are one, two, four and eight."""
+    if layers * Hkv > 100 and ctx > 5000:
+        ctx = ctx // 4
+    check_evict(gpu_lib, *evict_case(layers, 1, Hkv, 64, 16, ctx, BF, ctx), 700, 4, 100, in_place=Hkv == 4)
