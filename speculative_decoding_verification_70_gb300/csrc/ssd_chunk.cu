@@ -45,13 +45,15 @@
 namespace ssd {
 namespace {
 
+// One row tile, two, or one with copies of its rows.
+enum { kOne, kTwo, kCopies };
 constexpr int kThreads = 384;
 constexpr int kRegsCopy = 88, kRegsSoft = 208;  // 128 x 88 + 256 x 208 = 384 x 168
 constexpr int kMaxRing = 6;
 constexpr int kMaxCtas = 160;
 constexpr int kEdgeBars = 8;   // edge tiles whose clearing may lie ahead of their products
 constexpr int kFlagSets = 8;   // items whose flags live side by side
-constexpr int kStage = 2 * kTile * 128;  // 32 columns of O of the copies, by warpgroup
+constexpr int kStage = 2 * kTile * 128;  // 32 columns of O of the copies
 constexpr float kNoScore = -1e30f;  // m of a row that has seen nothing
 constexpr float kGrow = 8.f;
 template <class T>
@@ -112,7 +114,7 @@ struct alignas(16) Misc {
   unsigned tmem;
   int abort;
   unsigned wait_us;
-  float sums[2][kTile / 2];   // l of an item's rows (copies)
+  float sums[kTile / 2];   // l of an item's rows (copies)
   unsigned flags[kFlagSets][16];  // slots with NaN or infinite values that some rows see
   alignas(16) int off[kTile]; // offset of a tile's row from its first slot; far: no slot
   unsigned plain[4];          // rows of a tile that are slots (pages of up to 128)
@@ -552,24 +554,22 @@ __device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, 
     if (!(fabsf(__uint_as_float(o[e])) < INFINITY) && !(fabsf(x[e]) < INFINITY)) o[e] = __float_as_uint(x[e]);
 }
 
-// Few rows (64 at most): they lie in the row tile two or four times, and a copy takes its
-// part of a tile's slots alone, so that a thread has 64 or 32 scores instead of 128.  The
-// copies have their own m, l and O, which are joined at the item's end.  With heads of 64
-// (whose tiles come in half the time) the warpgroups take turns within an item, as copies
-// of each other, and the O's of two items lie side by side in tensor memory; with heads of
-// 128 each has its own items.
-template <class T, int D>
+// Few rows (64 at most) of heads of 64, whose tiles come in half the time of heads of 128:
+// they lie in the row tile two or four times, and a copy takes its part of a tile's slots
+// alone, so that a thread has 64 or 32 scores instead of 128; and the warpgroups take turns
+// within an item, as copies of each other.  The copies have their own m, l and O, which
+// are joined at the item's end; the O's of two items lie side by side in tensor memory.
+// (64 single tokens under a window of 2048, 32 / 8 heads: 68 us, with rows once and a
+// warpgroup an item 95.  Heads of 128 are as fast without: 64 / 8 heads, 64 single tokens
+// at 6800 279 us both ways, a chain of 8 under a window 27 us with copies and 24 without.)
+template <class T>
 __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tmem, char* stage, int w) {
   const int wt = threadIdx.x & 127, span = kTile / a.copies;
   const uint32_t lanes = static_cast<uint32_t>(wt & 96) << 16;
   const int copy = wt / span, r = wt - copy * span, nq = span / 32, q0 = copy * nq;  // its quarters of the slots
   const int tok = r / a.G, g = r - tok * a.G;
   const f32x2 c2 = pk2(a.c, a.c);
-  constexpr bool ALT = D == 64;
-  auto sync = [&]() {
-    if (ALT) named_sync(1, 256);
-    else named_sync(1 + w, 128);
-  };
+  constexpr int D = 64, kLines = 256;  // (threads that work on an item)
   uint32_t ppv = 0;    // phase of pvdone[w]
   uint32_t sph = 0;    // phases of sfull[w][.]
   int tiles = 0, item = -1;
@@ -578,11 +578,7 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
 #pragma unroll 1
   while (pc.next(a)) {
     ++item;
-    if (!ALT && (item & 1) != w) {
-      tiles += pc.end - pc.t0;
-      continue;
-    }
-    const uint32_t tO = tmem + lanes + 256 + (ALT ? (item & 1) * 2 + w : w) * D;
+    const uint32_t tO = tmem + lanes + 256 + ((item & 1) * 2 + w) * D;
     const int i = pc.blk * a.tpi + tok, pos = pc.ctx + i;
     const bool valid = tok < a.tq && i < pc.n;
     float m = kNoScore, l = 0.f;
@@ -593,8 +589,8 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       const int t = pc.tile(at);
       const bool edge = pc.k.edge(t);
       edges |= edge;
-      if (ALT && (tiles & 1) != w) continue;
-      const int buf = tiles & 1;
+      if ((tiles & 1) != w) continue;
+      const int buf = w;
       bar_wait(&sm.sfull[w][buf], (sph >> buf) & 1, sm, a.err);
       sph ^= 1u << buf;
       bool waited = jobs == 0;  // for the last tile's product
@@ -691,13 +687,13 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       ppv ^= 1;
       tc_after();
     }
-    const int id = ALT ? w * 128 + wt : wt, lines = ALT ? 256 : 128;  // this thread; all that work on the item
+    const int id = w * 128 + wt;
     float2* ml = reinterpret_cast<float2*>(stage);
     ml[id] = make_float2(m, l);
-    sync();
+    named_sync(1, kLines);
     float M = kNoScore, L = 0.f;
-    for (int k = r; k < lines; k += span) M = fmaxf(M, ml[k].x);
-    for (int k = r; k < lines; k += span) {
+    for (int k = r; k < kLines; k += span) M = fmaxf(M, ml[k].x);
+    for (int k = r; k < kLines; k += span) {
       const float2 x = ml[k];
       L += x.x == M ? x.y : x.y * ex2_fast(x.x - M);
     }
@@ -706,14 +702,13 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       return direct ? (static_cast<long long>(pc.b) * a.nodes.N + pc.blk * a.tpi + token) * a.Hq + pc.h * a.G + head
                     : (2ll * blockIdx.x + (item == 0 ? 0 : 1)) * a.tpi * a.G + token * a.G + head;
     };
-    float* sums = sm.sums[ALT ? 0 : w];
     if (valid && id < span) {
-      sums[r] = L;
+      sm.sums[r] = L;
       const long long row = place(tok, g);
       if (!direct) a.part_ml[row] = make_float2(M, L);
       else if (a.lse) a.lse[row] = L == 0.f ? -INFINITY : log_sum<T>(M, L);
     }
-    sync();
+    named_sync(1, kLines);
     const float f = m == M ? 1.f : ex2_fast(m - M);
     const unsigned* fl = sm.flags[item % kFlagSets];
     unsigned any = 0;
@@ -733,13 +728,13 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
       for (int e = 0; e < 32; ++e) o[e] = jobs > 0 ? __float_as_uint(__uint_as_float(o[e]) * f) : 0u;
 #pragma unroll
       for (int q = 0; q < 8; ++q) line[q ^ (wt & 7)] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-      sync();
+      named_sync(1, kLines);
       // four columns of a row a thread
 #pragma unroll 1
-      for (int i = id; i < quads; i += lines) {
+      for (int i = id; i < quads; i += kLines) {
         const int rr = i >> 3, q = i & 7, token = rr / a.G;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = rr; c < lines; c += span) {
+        for (int c = rr; c < kLines; c += span) {
           // (copies lie multiples of 8 rows apart)
           const float4 y = *reinterpret_cast<const float4*>(stage + c * 128 + (q ^ (rr & 7)) * 16);
           x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
@@ -748,11 +743,11 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
         const bool finite = fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY;
         if (!finite) seen_nonfinite<T>(a, pc, k + 4 * q, z);
         if (any) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pc.ctx + pc.blk * a.tpi + token, fl, k + 4 * q, z);
-        const float sum = sums[rr];
+        const float sum = sm.sums[rr];
         write_columns<T, D>(a, z, place(token, rr - token * a.G), k + 4 * q, direct, sum == 0.f,
                             !direct ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
       }
-      sync();
+      named_sync(1, kLines);
     }
     tc_before();
     bar_arrive(&sm.ofree[item & 1]);
@@ -821,9 +816,10 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
 // ---------------------------------------------------------------------------
 // Two row tiles: a warp each, so that one's waits pass beside the other's products (a
 // wait costs 100 cycles at least, and few products queue up).  One row tile: one warp.
-template <class T, int D, bool WIDE, bool ALT>
+template <class T, int D, int MODE>
 __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t tmem, uint32_t ring, uint32_t ringv,
                                              uint32_t Q, int w) {
+  constexpr bool WIDE = MODE == kTwo, ALT = MODE == kCopies;
   constexpr int kSlotBytes = D / 64 * kHalf;
   const uint32_t khalf = a.half / 16, vstep = a.group / 8;
   const uint64_t kd0 = operand(ring, 16, a.group), qd0 = operand(Q, 16, 1024);
@@ -1016,8 +1012,6 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-// MODE: one row tile, two, or one with copies of its rows.
-enum { kOne, kTwo, kCopies };
 template <class T, int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
@@ -1029,7 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   char* ring = base;
   char* ringv = ring + a.nk * kSlotBytes;
   char* Q = ringv + a.nv * kSlotBytes;
-  char* stage = Q + 2 * kSlotBytes;  // (copies) 16 KB a warpgroup
+  char* stage = Q + 2 * kSlotBytes;  // (copies)
   Misc& sm = *reinterpret_cast<Misc*>(stage + (MODE == kCopies ? kStage : 0));
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -1051,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&sm.pfull[i][0], 128);  // (halves of the slots)
       bar_init(&sm.pfull[i][1], 128);
       bar_init(&sm.pvdone[i], 1);
-      bar_init(&sm.ofree[i], MODE == kCopies && D == 64 ? 256 : 128);
+      bar_init(&sm.ofree[i], MODE == kCopies ? 256 : 128);
     }
     for (int i = 0; i < kEdgeBars; ++i) bar_init(&sm.vready[i], 1);
     bar_init(&sm.done, WIDE ? 2 : 1);
@@ -1214,7 +1208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 4) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
     const int w = (warp - 4) >> 2;
-    if constexpr (MODE == kCopies) share_role<T, D>(a, sm, tmem, D == 64 ? stage : stage + w * (kStage / 2), w);
+    if constexpr (MODE == kCopies) share_role<T>(a, sm, tmem, stage, w);
     else softmax_role<T, D, WIDE>(a, sm, tmem, w);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
@@ -1223,7 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (!WIDE && warp == 2) {
       load_role<D, false, true>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
     } else if (warp == 1 || warp == 2) {
-      product_role<T, D, WIDE, MODE == kCopies && D == 64>(a, sm, tmem, sptr(ring), sptr(ringv), sptr(Q), warp - 1);
+      product_role<T, D, MODE>(a, sm, tmem, sptr(ring), sptr(ringv), sptr(Q), warp - 1);
     } else {
       // ---- Q, and what must not be multiplied ----
       Pieces pq, pc;
@@ -1447,17 +1441,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) chunk_join_kernel(const __gri
 // host
 // ---------------------------------------------------------------------------
 // Tokens of an item: all where copies of them fit a row tile, one row tile of them where
-// every chunk fits it, else two.
-int item_tokens(int N, int G) {
+// every chunk fits it, else two (with one: 8192 tokens, 64 / 8 heads 1343 us against 831;
+// 16 chunks of 40 at 4000, 32 / 8 heads of 128 108 us against 83).
+int item_tokens(int N, int G, int D) {
   const int tq = kTile / G;
-  return N * static_cast<long long>(G) <= kTile / 2 ? N : N <= tq ? tq : 2 * tq;
+  return D == 64 && N * static_cast<long long>(G) <= kTile / 2 ? N : N <= tq ? tq : 2 * tq;
 }
 
 struct Layout {
   size_t ranges, ml, o, total;
 };
 Layout layout_of(int N, int G, int D) {
-  const size_t rows = static_cast<size_t>(item_tokens(N, G)) * G;
+  const size_t rows = static_cast<size_t>(item_tokens(N, G, D)) * G;
   Layout L;
   L.ranges = 256;
   L.ml = (L.ranges + sizeof(Range) * kMaxCtas + 255) / 256 * 256;
@@ -1489,8 +1484,10 @@ cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
 template <class T_, int D>
 cudaError_t launch_m(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C, int mode,
                      size_t smem, cudaStream_t s) {
-  const auto launch = mode == kTwo ? launch_t<T_, D, kTwo> : mode == kOne ? launch_t<T_, D, kOne> : launch_t<T_, D, kCopies>;
-  return launch(mq, mk, mv, a, C, smem, s);
+  if constexpr (D == 64) {
+    if (mode == kCopies) return launch_t<T_, D, kCopies>(mq, mk, mv, a, C, smem, s);
+  }
+  return mode == kTwo ? launch_t<T_, D, kTwo>(mq, mk, mv, a, C, smem, s) : launch_t<T_, D, kOne>(mq, mk, mv, a, C, smem, s);
 }
 
 }  // namespace
@@ -1502,15 +1499,16 @@ cudaError_t launch_chunk_attention(const ChunkParams& p, int dtype, int D, cudaS
   const KvView& kv = p.kv;
   a.nodes = p.nodes;
   a.Hq = p.Hq; a.Hkv = kv.Hkv; a.G = p.G;
-  a.tpi = item_tokens(p.nodes.N, p.G);
+  a.tpi = item_tokens(p.nodes.N, p.G, D);
   const int rows = a.tpi * p.G;
-  a.copies = rows <= kTile / 4 ? 4 : rows <= kTile / 2 ? 2 : 1;
+  a.copies = D == 128 ? 1 : rows <= kTile / 4 ? 4 : rows <= kTile / 2 ? 2 : 1;
   a.tq = a.copies > 1 ? a.tpi : kTile / p.G;
   const int mode = a.copies > 1 ? kCopies : a.tpi > a.tq ? kTwo : kOne;
   a.NB = (p.nodes.N + a.tpi - 1) / a.tpi;
   // (a window that no sequence exceeds is none)
   a.window = p.window < static_cast<long long>(kv.width) * kv.ps ? p.window : 0;
   a.sinks = a.window ? p.sinks : 0;
+  // (2, 4, 7: a prompt of 8192 964, 826, 847 us; a ragged batch under a window 280, 264, 294)
   a.item_cost = 4;
   a.zero = p.scale == 0.f;
   a.c = a.zero ? 1.f : fabsf(p.scale) * 1.4426950408889634f;
