@@ -716,7 +716,7 @@ SSD_API ssd_status ssd_kv_weights(const ssd_paged_kv *kv, const ssd_draft_nodes 
  * The kept slots' keys and values move to slots 0 .. budget-1 in slot order.
  *   weights  : fp32, row (l, b, h) at l*w_layer + b*w_b + h*w_h, w_len entries, of
  *              which the first ctx_len[b] count.
- *   budget   : >= 1 and >= sinks + recent.
+ *   budget   : >= 1 and >= sinks + recent; like w_len below 2^31 - 2^16.
  *   new_len  : [B] int32: min(ctx_len, budget).  Must not overlap ctx_len.
  *   kept     : [layers, B, Hkv, budget] int32: the slot that each slot's entry
  *              came from, -1 behind new_len.

@@ -15,27 +15,37 @@
 //
 // An item is a (sequence, block of tokens, key/value head): two row tiles side by side
 // (chunks of more than one row tile), whose softmax and products alternate, or one
-// (short chunks), whose tiles alternate between two score buffers.  Of the slots it
-// takes the tiles that hold first tokens, then those from the window's begin to the
-// block's last token.  One persistent CTA per SM: the batch's tiles are numbered and
-// cut into equal ranges by the lengths on the device, an item's start and end counted
-// as some tiles; an item that is cut leaves its parts (m, l, O in 32 bits) in the
-// workspace, and chunk_join_kernel joins them in range order (the same bits every call).
+// (short chunks), whose tiles alternate between two score buffers, or the few rows of
+// short chunks of heads of 64 as copies.  Of the slots it takes the tiles that hold first
+// tokens, then those from the window's begin to the block's last token.  One persistent
+// CTA per SM: the batch's tiles are numbered and cut into equal ranges by the lengths on
+// the device, an item's start and end counted as some tiles; an item that is cut leaves
+// its parts (m, l, O in 32 bits) in the workspace, and chunk_join_kernel joins them in
+// range order (the same bits every call).
 //
 // Warps of a CTA:
-//   0      copies K and V tiles, page by page, by TMA into rings of slots (one row tile: K,
+//   0      copies K and V tiles, a lane a box, by TMA into rings of slots (one row tile: K,
 //          and warp 2 V)
 //   1, 2   issue the products, of a row tile each (one row tile: warp 1)
 //   3      copies Q, and clears what must not be multiplied in V tiles at the edges of
 //          what is seen: rows that no row of the item sees, and NaN or infinite entries
 //          of slots that only some see (added at the end for the rows that see them)
-//   4..11  two warpgroups for the softmax: one for each row tile, or (one row tile) for
-//          every second item, so that an item's end runs beside the next one's begin
+//   4..11  two warpgroups for the softmax: one for each row tile; or (one row tile) one for
+//          every second item, so that an item's end runs beside the next one's begin; or
+//          (copies) one for every second tile
 //
 // m follows the running maximum lazily: only where a row's maximum in units of log 2
 // grew by more than 8 are l and O rescaled.  P at m is 2^-40 in bf16, so that sums of
 // finite values stay finite, and 2^7 in fp16, whose V ends at 65504 and whose P at
-// 2^16.
+// 2^16.  P is rounded to the cache's type, which the product's operands share; scores, m,
+// l and O are held in 32 bits, and l adds the weights before they are rounded.
+//
+// What bounds it: long chunks, the chain of a row tile's scores, softmax (1400 cycles),
+// weights and products, of which the two row tiles overlap 2800 cycles a pair of tiles
+// (products of heads of 128: 2048): a prompt of 8192 tokens, 64 / 8 heads of 128, 830 us
+// (1320 TFLOP/s, at the GPU's power limit).  Single tokens, the copies: 64 at 6800 slots,
+// 64 / 8 heads of 128, 279 us (6.4 TB/s).  Few slots, latency: a chain of 8 under a window
+// of 4096 24 us, of which 7 until the first scores, 3 to end an item and 6 to join parts.
 #include <math.h>
 
 #include "ssd_device.cuh"

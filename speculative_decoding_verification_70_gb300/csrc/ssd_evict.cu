@@ -1,14 +1,19 @@
 // ssd_evict.cu -- a paged cache cut down to a budget of slots a sequence, each
 // key/value head keeping its heaviest ones.
 //
-// evict_pick_kernel, a cluster of CTAs per (layer, sequence, head), a segment of the slots
+// pick(), a CTA or a cluster of them per (layer, sequence, head), a segment of the slots
 // each: the first `sinks` slots and the last `recent` stay; of those between, the weight
 // of the last one that stays is found by its bits (11 a pass, a histogram of them summed
 // over the cluster; done as soon as all of a bin stay), then the stays of the segments
 // before are added up and the list of the kept slots is written in slot order.
-// evict_move_kernel moves rows and weights: entry r of the list goes to slot r.  A source
-// lies at or behind its target, so that blocks of rows taken in order, all of a block's
-// loads before its stores, read every row before it is overwritten.
+// move_rows() and move_weights(): entry r of the list goes to slot r.  A source lies at or
+// behind its target, so that blocks of rows taken in order, all of a block's loads before
+// its stores, read every row before it is overwritten.
+// Nothing is computed in floating point: weights are compared by their bits.
+//
+// What bounds it: many heads, the bytes moved, read and written (80 layers, 1024 of 4096
+// slots kept, 131 us, 5.3 TB/s); few, the passes over the weights, which wait for one
+// another (2 layers, 8192 of 100003 slots: 69 us, 38 of them the choice).
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"
 

@@ -323,6 +323,8 @@ ssd_status ssd_kv_evict(const ssd_paged_kv* kv, int layers, int64_t k_layer, int
   if (static_cast<int64_t>(B) * layers > INT32_MAX / kv->Hkv) return SSD_ERR_INVALID_ARG;
   if (layers > 1 && (!stride_ok(k_layer) || !stride_ok(v_layer))) return SSD_ERR_INVALID_ARG;
   if (budget < 1 || sinks < 0 || recent < 0 || budget - sinks < recent) return SSD_ERR_INVALID_ARG;
+  // (slots are counted up to 2^16 beyond either)
+  if (w_len > INT32_MAX - 65536 || budget > INT32_MAX - 65536) return SSD_ERR_INVALID_ARG;
   if ((layers > 1 && (w_layer < w_len || w_layer >= kMaxStride)) || w_b < w_len || w_h < w_len || w_b >= kMaxStride ||
       w_h >= kMaxStride)
     return SSD_ERR_INVALID_ARG;

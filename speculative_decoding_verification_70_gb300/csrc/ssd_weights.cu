@@ -14,6 +14,12 @@
 // Warps of a CTA: 0 copies the blocks of Q, 2 and 20 the tiles of K, by TMA into rings; 1
 // issues the products; 3 brings the columns' -lse; 4..19 four warpgroups for the sums, two
 // a tile, which take its blocks in turn.
+//
+// Scores, exponentials and sums are held in 32 bits; nothing is rounded to fewer.  What
+// bounds it: few rows, the bytes of K and of the weights (64 single tokens at 200..8000,
+// 64 / 8 heads of 128: 64 us, 4.5 TB/s); many, the exponentials and what stands before and
+// behind them in a warp (4 prompts of up to 5500 slots, 32 / 8 heads of 64: 110 us, of which
+// the exponentials' pipe alone would want 50).
 #include <math.h>
 
 #include "ssd_device.cuh"
@@ -712,7 +718,7 @@ cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, int D, cudaStre
   const long long most = static_cast<long long>(p.kv.width) * p.kv.ps;
   a.window = p.window < most ? p.window : 0;  // (a window that no sequence exceeds is none)
   a.sinks = a.window ? p.sinks : 0;
-  a.item_cost = 1;
+  a.item_cost = 1;  // (an item's tiles of K, its first block and its sums)
   a.zero = p.scale == 0.f;
   a.c = a.zero ? 1.f : fabsf(p.scale) * kLog2e;
   a.negate = p.scale < 0.f;
@@ -732,7 +738,7 @@ cudaError_t launch_kv_weights(const WeightsParams& p, int dtype, int D, cudaStre
   const long long tiles = !a.uneven ? (slots + a.tk - 1) / a.tk : (slots / a.ps + 1) * a.tpp;
   a.NP = static_cast<int>((tiles + 1) / 2);
   // as many tiles of K as fit beside the blocks of Q (two of 32 KB: a third would leave one
-  // slot a ring of K)
+  // slot a ring of K, and an item's tiles would wait for the last item's sums)
   const size_t slot = static_cast<size_t>(D) * 2 * kTile, qslot = static_cast<size_t>(D) * 2 * a.cols;
   a.nq = qslot > 16384 ? 2 : kMaxQueries;
   const size_t left = kSmemMax - sizeof(Misc) - a.nq * qslot;

@@ -212,3 +212,10 @@ def test_plain_eviction_by_hand():
     for r, s in enumerate([0, 2, 4, 7, 8]):
         assert torch.equal(at(k, r), at(c["k_cache"], s)) and torch.equal(at(v, r), at(c["v_cache"], s))
     assert torch.equal(at(k, 6), at(c["k_cache"], 6))
+
+
+@needs_no_gpu
+def test_cuts_that_count_beyond_32_bits_are_refused(lib):
+    big = 2 ** 31 - 65536
+    assert _evict(lib, budget=big) == INVALID
+    assert _evict(lib, layers=1, w_l=big, w_b=big, w_h=big, w_len=big, wo=None) == INVALID
