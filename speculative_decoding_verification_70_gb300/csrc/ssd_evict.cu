@@ -22,7 +22,6 @@ namespace {
 
 constexpr int kEvictThreads = 512;
 constexpr int kWarps = kEvictThreads / 32;
-constexpr int kPerLane = 16;                              // most slots of a lane
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 
@@ -32,6 +31,9 @@ __device__ __forceinline__ uint32_t key_of(float w) {
   const int b = __float_as_int(w + 0.f);  // (-0 counts as 0)
   return static_cast<uint32_t>(b) ^ (b < 0 ? 0xffffffffu : 0x80000000u);
 }
+
+// Bits 0 .. n - 1, n up to 32.
+__device__ __forceinline__ uint32_t first_bits(int n) { return n < 32 ? (1u << n) - 1 : ~0u; }
 
 struct PickSmem {
   alignas(16) int hist[kBins], tot[kBins];  // of the CTA; of the cluster (a share of the bins a CTA)
@@ -85,7 +87,9 @@ __device__ __forceinline__ void warps_before(PickSmem& sm, int& a, int& b, int& 
   if (warp == 0) a = b = 0;
 }
 
-// By all threads of a cluster; the CTA is number `rank` of it.
+// By all threads of a cluster; the CTA is number `rank` of it.  PER: most slots of a lane at
+// a time (a segment above 512 of them is read again for every pass).
+template <int PER>
 __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int unit, int rank, int cluster) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int H = p.kv.Hkv, h = unit % H, b = unit / H % p.B, layer = unit / H / p.B;
@@ -107,22 +111,22 @@ __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int uni
   int need = C - p.sinks - p.recent;
   const int seg = ((ctx + cluster - 1) / cluster + 31) / 32 * 32;
   const int s0 = min(ctx, rank * seg), s1 = min(ctx, s0 + seg);
-  // slots of a lane at a time: all, or 16.  A warp's lie 32 side by side.
-  const int pl = min(kPerLane, max(1, (s1 - s0 + kEvictThreads - 1) / kEvictThreads));
+  // slots of a lane at a time: all, or PER.  A warp's lie 32 side by side.
+  const int pl = min(PER, max(1, (s1 - s0 + kEvictThreads - 1) / kEvictThreads));
   const int chunk = pl * kEvictThreads, chunks = max(1, (s1 - s0 + chunk - 1) / chunk);
-  uint32_t key[kPerLane], comp = 0;  // keys, and which of them compete
+  uint32_t key[PER], comp = 0;  // keys, and which of them compete
   auto slot_of = [&](int c, int k) { return s0 + c * chunk + (warp * pl + k) * 32 + lane; };
   auto load = [&](int c) {
     // (without a branch, so that all loads are on their way at once)
     const int first = slot_of(c, 0), count = min(pl, (s1 - first + 31) / 32);
-    float x[kPerLane];
+    float x[PER];
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) x[k] = k < count ? w[first + 32 * k] : 0.f;
+    for (int k = 0; k < PER; ++k) x[k] = k < count ? w[first + 32 * k] : 0.f;
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) key[k] = key_of(x[k]);
+    for (int k = 0; k < PER; ++k) key[k] = key_of(x[k]);
     // those from lo to hi - 1
-    const int from = min(max((lo - first + 31) >> 5, 0), 31), to = min(max((min(hi, s1) - first + 31) >> 5, 0), pl);
-    comp = ((1u << to) - 1) & ~((1u << from) - 1);
+    const int from = min(max((lo - first + 31) >> 5, 0), 32), to = min(max((min(hi, s1) - first + 31) >> 5, 0), pl);
+    comp = first_bits(to) & ~first_bits(from);
   };
   load(0);
   uint32_t want = 0, known = 0;  // the last one's key as far as it is known
@@ -136,7 +140,7 @@ __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int uni
       for (int c = 0; c < chunks; ++c) {
         if (chunks > 1) load(c);
 #pragma unroll
-        for (int k = 0; k < kPerLane; ++k) {
+        for (int k = 0; k < PER; ++k) {
           if (k >= pl) break;
           if (((comp >> k) & 1) && (key[k] & known) == want)
             atomicAdd(&sm.hist[(key[k] >> shift) & ((1 << bits) - 1)], 1);
@@ -200,7 +204,7 @@ __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int uni
   auto classes = [&](int c) {
     stays = equals = 0;
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
+    for (int k = 0; k < PER; ++k) {
       if (k >= pl) break;
       const uint32_t x = key[k] & known;
       stays |= static_cast<uint32_t>(x > want) << k;
@@ -209,7 +213,7 @@ __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int uni
     if (none) stays = equals = 0;
     // slots of the segment that do not compete
     const int there = min(pl, max(0, (s1 - slot_of(c, 0) + 31) / 32));
-    stays = (stays & comp) | (((1u << there) - 1) & ~comp);
+    stays = (stays & comp) | (first_bits(there) & ~comp);
     equals &= comp;
   };
   int gt = 0, eq = 0;  // of the segment, by warp
@@ -250,7 +254,7 @@ __device__ __forceinline__ void pick(const EvictParams& p, PickSmem& sm, int uni
     int at = out + a + min(max(need - equal_before, 0), e);
     const unsigned under = (1u << lane) - 1;
 #pragma unroll
-    for (int k = 0; k < kPerLane; ++k) {
+    for (int k = 0; k < PER; ++k) {
       if (k >= pl) break;
       const bool equal = (equals >> k) & 1;
       bool stay = (stays >> k) & 1;
@@ -281,9 +285,12 @@ struct MoveSmem {
 // kMoveBytes of them: on their way into shared memory while the places of the next round
 // are found, and out again once every CTA of the cluster has its own, beside the next
 // round's loads (whose sources lie behind this round's targets).
+// (Relaxed: it orders copies that have ended before other CTAs' writes, and no values pass.)
 __device__ __forceinline__ void round_sync(int cluster) {
-  if (cluster > 1) cluster_sync();
-  else __syncthreads();
+  if (cluster > 1)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+  else
+    __syncthreads();
 }
 
 __device__ __forceinline__ bool in_range(const EvictParams& p, int ctx) {
@@ -308,7 +315,8 @@ __device__ __forceinline__ void move_weights(const EvictParams& p, int unit, int
         const int r = at + k * kEvictThreads + tid;
         x[k] = r < n ? w[kept[r]] : 0.f;
       }
-      round_sync(cluster);
+      if (cluster > 1) cluster_sync();  // (released: loads to registers may still be on their way)
+      else __syncthreads();
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int r = at + k * kEvictThreads + tid;
@@ -383,7 +391,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, MoveSmem& sm, in
 // Few units: clusters that pick, then clusters that move (blockIdx.y: K, V, the weights).
 __global__ void __launch_bounds__(kEvictThreads) evict_pick_kernel(const __grid_constant__ EvictParams p, int cluster) {
   __shared__ PickSmem sm;
-  pick(p, sm, blockIdx.x / cluster, blockIdx.x % cluster, cluster);
+  pick<32>(p, sm, blockIdx.x / cluster, blockIdx.x % cluster, cluster);
 }
 __global__ void __launch_bounds__(kEvictThreads) evict_move_kernel(const __grid_constant__ EvictParams p, int cluster) {
   extern __shared__ __align__(16) char dyn[];
@@ -396,7 +404,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_move_kernel(const __grid_
 __global__ void __launch_bounds__(kEvictThreads, 3) evict_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) char dyn[];
   MoveSmem& sm = *reinterpret_cast<MoveSmem*>(dyn);
-  pick(p, *reinterpret_cast<PickSmem*>(dyn), blockIdx.x, 0, 1);
+  pick<16>(p, *reinterpret_cast<PickSmem*>(dyn), blockIdx.x, 0, 1);
   __syncthreads();
   move_rows(p, sm, blockIdx.x, 0, 1, false);
   move_rows(p, sm, blockIdx.x, 0, 1, true);
