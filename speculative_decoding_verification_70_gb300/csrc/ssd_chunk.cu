@@ -768,7 +768,7 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
 // copies of K and V
 // ---------------------------------------------------------------------------
 // K, V or both: K a tile ahead, as the products take them.
-template <int D, bool KEYS, bool VALUES>
+template <int D, bool KEYS, bool VALUES, bool GATHER>
 __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtensorMap& mapk, const CUtensorMap& mapv,
                                           uint32_t ring, uint32_t ringv) {
   const int lane = threadIdx.x & 31;
@@ -776,14 +776,14 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
   Pieces pc;
   pc.start(sm);
   bool bad_page = false;
-  int s0v = 0, p0v = 0, p1v = 0, idv = 0, hv = 0;  // the tile whose values are to come
+  Place idv = {};
+  int p0v = 0, p1v = 0, hv = 0;  // the tile whose values are to come
   bool pending = false;
 #pragma unroll 1
   while (pc.next(a)) {
     const int* trow = a.table + pc.b * a.table_stride;
-    // boxes of a tile that hold something seen, and this lane's page id
-    auto lookup = [&](int t, int& p0, int& p1, int& s0) {
-      int id = 0;
+    // boxes of a tile that hold something seen, and this lane's page ids
+    auto lookup = [&](int t, int& p0, int& p1) {
       p0 = p1 = 0;
       if (!a.uneven) {
         p1 = a.boxes - 1;
@@ -795,20 +795,19 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
         }
       }
       // (not looked at before its tile's turn: the load is on its way meanwhile)
-      const int place = box_page(a, t, s0);
-      if (lane >= p0 && lane <= p1) id = __ldg(trow + place);
-      return id;
+      return box_place<GATHER>(a, trow, t, pc.s.p1, lane >= p0 && lane <= p1);
     };
-    int p0n, p1n, s0n, idn = lookup(pc.tile(pc.t0), p0n, p1n, s0n);
+    int p0n, p1n;
+    Place idn = lookup(pc.tile(pc.t0), p0n, p1n);
 #pragma unroll 1
     for (int at = pc.t0; at < pc.end; ++at) {
-      const int id = idn, p0 = p0n, p1 = p1n, s0 = s0n;
-      if (at + 1 < pc.end) idn = lookup(pc.tile(at + 1), p0n, p1n, s0n);
-      if (KEYS) bad_page |= !load_tile<D>(a, sm, rk, p0, p1, id, s0, pc.h, a.err, a.withheld);
-      if (VALUES && !KEYS) bad_page |= !load_tile<D>(a, sm, rv, p0, p1, id, s0, pc.h, a.err, a.withheld);
+      const Place id = idn;
+      const int p0 = p0n, p1 = p1n;
+      if (at + 1 < pc.end) idn = lookup(pc.tile(at + 1), p0n, p1n);
+      if (KEYS) bad_page |= !load_tile<D, GATHER>(a, sm, rk, p0, p1, id, pc.h, a.err, a.withheld);
+      if (VALUES && !KEYS) bad_page |= !load_tile<D, GATHER>(a, sm, rv, p0, p1, id, pc.h, a.err, a.withheld);
       if (VALUES && KEYS) {
-        if (pending) load_tile<D>(a, sm, rv, p0v, p1v, idv, s0v, hv, a.err, a.withheld);
-        s0v = s0;
+        if (pending) load_tile<D, GATHER>(a, sm, rv, p0v, p1v, idv, hv, a.err, a.withheld);
         p0v = p0;
         p1v = p1;
         idv = id;
@@ -817,7 +816,7 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
       }
     }
   }
-  if (pending) load_tile<D>(a, sm, rv, p0v, p1v, idv, s0v, hv, a.err, a.withheld);
+  if (pending) load_tile<D, GATHER>(a, sm, rv, p0v, p1v, idv, hv, a.err, a.withheld);
   if (bad_page) atomicOr(a.err, kErrBadPage);
 }
 
@@ -1022,7 +1021,7 @@ __device__ __forceinline__ void product_role(const Args& a, Misc& sm, uint32_t t
 // ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <class T, int D, int MODE>
+template <class T, int D, int MODE, bool GATHER>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
                  const __grid_constant__ CUtensorMap mapv, const __grid_constant__ Args a) {
@@ -1223,9 +1222,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCopy));
     if (warp == 0) {
-      load_role<D, true, WIDE>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
+      load_role<D, true, WIDE, GATHER>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
     } else if (!WIDE && warp == 2) {
-      load_role<D, false, true>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
+      load_role<D, false, true, GATHER>(a, sm, mapk, mapv, sptr(ring), sptr(ringv));
     } else if (warp == 1 || warp == 2) {
       product_role<T, D, MODE>(a, sm, tmem, sptr(ring), sptr(ringv), sptr(Q), warp - 1);
     } else {
@@ -1471,12 +1470,12 @@ Layout layout_of(int N, int G, int D) {
   return L;
 }
 
-template <class T_, int D, int MODE>
-cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C,
+template <class T_, int D, int MODE, bool GATHER>
+cudaError_t launch_g(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C,
                      size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<T_, D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  cudaError_t e = cudaFuncSetAttribute(chunk_kernel<T_, D, MODE, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
-  chunk_kernel<T_, D, MODE><<<C, kThreads, smem, s>>>(mq, mk, mv, a);
+  chunk_kernel<T_, D, MODE, GATHER><<<C, kThreads, smem, s>>>(mq, mk, mv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || C < 2) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1489,6 +1488,13 @@ cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T_, D>, a, C);
+}
+
+template <class T_, int D, int MODE>
+cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const Args& a, int C,
+                     size_t smem, cudaStream_t s) {
+  return a.gather ? launch_g<T_, D, MODE, true>(mq, mk, mv, a, C, smem, s)
+                  : launch_g<T_, D, MODE, false>(mq, mk, mv, a, C, smem, s);
 }
 
 template <class T_, int D>

@@ -97,6 +97,16 @@ __device__ __forceinline__ void tma_groups(uint32_t dst, const CUtensorMap* map,
       : "memory");
 }
 
+// Four rows of 64 columns from column x on.
+__device__ __forceinline__ void tma_gather(uint32_t dst, const CUtensorMap* map, int x, const int (&row)[4],
+                                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(map), "r"(sptr(bar)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3])
+      : "memory");
+}
+
 __device__ __forceinline__ void fence_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -265,6 +275,18 @@ inline bool encode_groups(CUtensorMap* m, void* base, int dtype, int ps, int H, 
   const cuuint32_t bx[5] = {64, 8, 2, static_cast<cuuint32_t>(box / 8), 1};
   const cuuint32_t one[5] = {1, 1, 1, 1, 1};
   return fn(m, map_type(dtype), 5, base, dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// {columns, rows}; four rows of 64 columns at a time, each by its number.
+inline bool encode_gather(CUtensorMap* m, void* base, int dtype, long long columns, long long rows, long long slot) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(slot) * 2};
+  const cuuint32_t bx[2] = {64, 1}, one[2] = {1, 1};
+  return fn(m, map_type(dtype), 2, base, dims, strides, bx, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

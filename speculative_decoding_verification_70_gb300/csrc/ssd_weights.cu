@@ -306,9 +306,49 @@ __device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem,
 }
 
 // ---------------------------------------------------------------------------
+// copies of K: first (w = 0) or second tiles of items
+// ---------------------------------------------------------------------------
+template <int D, bool GATHER>
+__device__ __forceinline__ void keys_role(const Args& a, Misc& sm, const CUtensorMap& map, uint32_t ring, int w) {
+  constexpr int kSlotBytes = D / 64 * kHalf;
+  const int lane = threadIdx.x & 31;
+  Pieces pc;
+  pc.start(a, sm);
+  Ring rk = {&map, sm.kfull[w], sm.kempty[w], ring + w * a.nk * kSlotBytes, a.nk, -1, 0};
+  bool bad_page = false;
+  // an item's tile: the boxes that hold slots, and this lane's page id, on its way
+  // while the tile of the item before is copied
+  struct Tile {
+    int t, h, pl;
+    Place id;
+  };
+  auto lookup = [&](Tile& x) {
+    x.t = -1;
+    do {
+      if (!pc.next(a)) return;
+    } while (w >= pc.k.tiles);
+    x.t = 2 * pc.p + w;
+    x.h = pc.h;
+    int first, count;
+    tile_slots(a, x.t, first, count);
+    x.pl = a.uneven ? 0 : min(a.boxes - 1, (pc.ctx + pc.n - 1 - first) / a.step);
+    x.id = box_place<GATHER>(a, a.table + pc.b * a.table_stride, x.t, pc.ctx + pc.n - 1, lane <= x.pl);
+  };
+  Tile cur, nxt;
+  lookup(nxt);
+#pragma unroll 1
+  while (nxt.t >= 0) {
+    cur = nxt;
+    lookup(nxt);
+    bad_page |= !load_tile<D, GATHER>(a, sm, rk, 0, cur.pl, cur.id, cur.h, a.err, a.withheld);
+  }
+  if (bad_page) atomicOr(a.err, kErrBadPage);
+}
+
+// ---------------------------------------------------------------------------
 // the kernel
 // ---------------------------------------------------------------------------
-template <class T, int D>
+template <class T, int D, bool GATHER>
 __global__ void __launch_bounds__(kSumThreads, 1)
     weights_kernel(const __grid_constant__ CUtensorMap mapq, const __grid_constant__ CUtensorMap mapk,
                    const __grid_constant__ Args a) {
@@ -473,36 +513,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
     } else if (warp == 2 || warp == 20) {
       // ---- first (2) or second (20) tiles of K ----
       const int w = warp == 20;
-      Ring rk = {&mapk, sm.kfull[w], sm.kempty[w], sptr(ring) + w * a.nk * kSlotBytes, a.nk, -1, 0};
-      bool bad_page = false;
-      // an item's tile: the boxes that hold slots, and this lane's page id, on its way
-      // while the tile of the item before is copied
-      struct Tile {
-        int t, h, pl, id, s0;
-      };
-      auto lookup = [&](Tile& x) {
-        x.t = -1;
-        do {
-          if (!pc.next(a)) return;
-        } while (w >= pc.k.tiles);
-        x.t = 2 * pc.p + w;
-        x.h = pc.h;
-        x.id = 0;
-        int first, count;
-        tile_slots(a, x.t, first, count);
-        x.pl = a.uneven ? 0 : min(a.boxes - 1, (pc.ctx + pc.n - 1 - first) / a.step);
-        const int place = box_page(a, x.t, x.s0);
-        if (lane <= x.pl) x.id = __ldg(a.table + pc.b * a.table_stride + place);
-      };
-      Tile cur, nxt;
-      lookup(nxt);
-#pragma unroll 1
-      while (nxt.t >= 0) {
-        cur = nxt;
-        lookup(nxt);
-        bad_page |= !load_tile<D>(a, sm, rk, 0, cur.pl, cur.id, cur.s0, cur.h, a.err, a.withheld);
-      }
-      if (bad_page) atomicOr(a.err, kErrBadPage);
+      keys_role<D, GATHER>(a, sm, mapk, sptr(ring), w);
     } else if (warp == 3) {
       int place[kTile / 32];  // of a column's lse behind the block's first
 #pragma unroll
@@ -686,11 +697,11 @@ Layout layout() {
   return L;
 }
 
-template <class T, int D>
-cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const Args& a, int C, size_t smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(weights_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+template <class T, int D, bool GATHER>
+cudaError_t launch_g(const CUtensorMap& mq, const CUtensorMap& mk, const Args& a, int C, size_t smem, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(weights_kernel<T, D, GATHER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
   if (e != cudaSuccess) return e;
-  weights_kernel<T, D><<<C, kSumThreads, smem, s>>>(mq, mk, a);
+  weights_kernel<T, D, GATHER><<<C, kSumThreads, smem, s>>>(mq, mk, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || C < 2) return e;
   cudaLaunchConfig_t cfg = {};
@@ -703,6 +714,11 @@ cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const Args& a
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, weights_join_kernel, a, C);
+}
+
+template <class T, int D>
+cudaError_t launch_t(const CUtensorMap& mq, const CUtensorMap& mk, const Args& a, int C, size_t smem, cudaStream_t s) {
+  return a.gather ? launch_g<T, D, true>(mq, mk, a, C, smem, s) : launch_g<T, D, false>(mq, mk, a, C, smem, s);
 }
 
 }  // namespace

@@ -230,3 +230,40 @@ def test_page_sizes(gpu_lib, page):
         c = case(3, N, 8, 2, D, page, (0, 131, 620), BF, page, order=order)
         check(gpu_lib, c)
         check(gpu_lib, c, 150, 9)
+
+
+@pytest.mark.parametrize("page", [1, 3, 5, 12, 130, 201])
+@pytest.mark.parametrize("gap", [False, True])
+def test_odd_pages_out_of_range_and_apart(gpu_lib, page, gap):
+    """Page ids out of range give zeros; the same with pages that lie no whole number of slots
+    apart (and after a call that left NaN in shared memory)."""
+    lib = gpu_lib
+    for N, D in ((1, 64), (50, 128), (200, 64)):
+        if gap:
+            nans = case(8, N, 8, 2, D, 16, 3000, BF, 16, fill="random")
+            nans["v_cache"][:] = math.nan
+            nans["k_cache"][:] = math.nan
+            attend(lib, nans)
+        c = case(2, N, 8, 2, D, page, (150, 420), BF, 60 + page, fill="random")
+        if gap:
+            for n in ("k_cache", "v_cache"):
+                t = c[n]
+                flat = torch.zeros((t.shape[0], page * 2 * D + 8), dtype=BF, device="cuda")
+                c[n] = flat[:, :page * 2 * D].view(t.shape)
+                c[n].copy_(t)
+        g = ref.to_gpu({**c, "k_cache": None, "v_cache": None})
+        for bad in (False, True):
+            if bad:
+                c["page_table"][0, 100 // page] = c["k_cache"].shape[0]
+                c["page_table"][1, 300 // page] = -2
+                g["page_table"] = c["page_table"].cuda()
+            plain = {**c, "k_cache": c["k_cache"].cpu(), "v_cache": c["v_cache"].cpu()}
+            for window, sinks in ((0, 0), (330, 2)):
+                out, lse, tol, ltol = cref.attention(plain, window, sinks)
+                r = lib.ssd_chunk_attention(g["q"], c["k_cache"].cuda() if not gap else c["k_cache"],
+                                            c["v_cache"].cuda() if not gap else c["v_cache"], g["page_table"],
+                                            g["ctx_len"], window=window, sinks=sinks)
+                torch.cuda.synchronize()
+                assert lib.get_device_error(r["ws"]) == (lib.DEVERR_BAD_PAGE if bad else 0)
+                _same(r["out"], out, tol, "out")
+                _same(r["lse"], lse, ltol, "lse")
