@@ -42,8 +42,8 @@
 //
 // What bounds it: long chunks, the chain of a row tile's scores, softmax (1400 cycles),
 // weights and products, of which the two row tiles overlap 2800 cycles a pair of tiles
-// (products of heads of 128: 2048): a prompt of 8192 tokens, 64 / 8 heads of 128, 830 us
-// (1320 TFLOP/s, at the GPU's power limit).  Single tokens, the copies: 64 at 6800 slots,
+// (products of heads of 128: 2048): a prompt of 8192 tokens, 64 / 8 heads of 128, 840 us
+// (1310 TFLOP/s, at the GPU's power limit).  Single tokens, the copies: 64 at 6800 slots,
 // 64 / 8 heads of 128, 279 us (6.4 TB/s).  Few slots, latency: a chain of 8 under a window
 // of 4096 24 us, of which 7 until the first scores, 3 to end an item and 6 to join parts.
 #include <math.h>
@@ -569,7 +569,7 @@ __device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, 
 // alone, so that a thread has 64 or 32 scores instead of 128; and the warpgroups take turns
 // within an item, as copies of each other.  The copies have their own m, l and O, which
 // are joined at the item's end; the O's of two items lie side by side in tensor memory.
-// (64 single tokens under a window of 2048, 32 / 8 heads: 68 us, with rows once and a
+// (64 single tokens under a window of 2048, 32 / 8 heads: 70 us, with rows once and a
 // warpgroup an item 95.  Heads of 128 are as fast without: 64 / 8 heads, 64 single tokens
 // at 6800 279 us both ways, a chain of 8 under a window 27 us with copies and 24 without.)
 template <class T>

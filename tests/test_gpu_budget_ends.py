@@ -207,3 +207,59 @@ def test_cuts_of_all_numbers_of_heads(gpu_lib, layers, Hkv, ctx):
     if layers * Hkv > 100 and ctx > 5000:
         ctx = ctx // 4
     check_evict(gpu_lib, *evict_case(layers, 1, Hkv, 64, 16, ctx, BF, ctx), 700, 4, 100, in_place=Hkv == 4)
+
+
+def test_batches_of_empty_sequences(gpu_lib):
+    """No new tokens at all: zeros and -inf, the weights as they were; nothing to cut."""
+    lib = gpu_lib
+    for N, D in ((1, 64), (6, 128), (200, 64)):
+        c = case(5, N, 8, 2, D, 16, (0, 40, 3, 0, 99), BF, 60, fill="random")
+        c["n_nodes"] = torch.zeros(5, dtype=torch.int32)
+        out = {"out": torch.full((5, N, 8, D), math.nan, dtype=BF, device="cuda"),
+               "lse": torch.full((5, N, 8), math.nan, device="cuda")}
+        r = attend(lib, c, out=out)
+        assert bool((r["out"] == 0).all()) and bool((r["lse"] == -math.inf).all())
+        w = torch.rand((5, 2, 300))
+        u = add_weights(lib, c, torch.full((5, N, 8), -math.inf), w, decay=0.5)
+        assert torch.equal(u["weights"].cpu(), w)
+        assert lib.get_device_error(r["ws"]) == 0 and lib.get_device_error(u["ws"]) == 0
+    check_evict(lib, *evict_case(2, 3, 2, 64, 16, (0, 0, 0), BF, 61), 7, 1, 2)
+
+
+@pytest.mark.parametrize("N,D", [(1, 64), (2, 128)])
+def test_many_sequences(gpu_lib, N, D):
+    """More sequences than CTAs and than threads of one."""
+    c = case(900, N, 4, 2, D, 16, tuple((i * 7) % 90 for i in range(900)), FP, 62, fill="random")
+    check(gpu_lib, c, 50, 2)
+    check_weights(gpu_lib, c, 50, 2)
+
+
+@pytest.mark.parametrize("page", [16, 1])
+def test_caches_beyond_32_bits(gpu_lib, page):
+    """Pages behind the first 2^32 bytes and 2^31 entries of a cache."""
+    lib = gpu_lib
+    H, D = 8, 128
+    small = case(2, 40, 16, H, D, page, (100, 333), BF, 70, fill="random")
+    used = small["k_cache"].shape[0]
+    first = (2 ** 31 + 2 ** 20) // (page * H * D)
+    g = ref.to_gpu(small)
+    for n in ("k_cache", "v_cache"):
+        big = torch.empty((first + used, page, H, D), dtype=BF, device="cuda")
+        big[first:] = g[n]
+        g[n] = big
+    g["page_table"] = torch.where(g["page_table"] >= 0, g["page_table"] + first, -1).to(torch.int32)
+    out, lse, tol, ltol = cref.attention(small, 90, 3)
+    r = lib.ssd_chunk_attention(g["q"], g["k_cache"], g["v_cache"], g["page_table"], g["ctx_len"], window=90, sinks=3)
+    _same(r["out"], out, tol, "out")
+    _same(r["lse"], lse, ltol, "lse")
+    w = torch.rand((2, H, 400), generator=torch.Generator().manual_seed(2))
+    want, wtol = cref.weights(small, r["lse"].cpu(), w, 90, 3)
+    u = lib.ssd_kv_weights(g["q"], g["k_cache"], g["page_table"], g["ctx_len"], r["lse"], w.cuda(), window=90, sinks=3)
+    _same(u["weights"], want, wtol, "weights")
+    c = {**small, "k_cache": small["k_cache"][None], "v_cache": small["v_cache"][None]}
+    k, v, new, kept, wout = cref.evict(c, w[None], 64, 4, 9)
+    e = lib.ssd_kv_evict(g["k_cache"], g["v_cache"], g["page_table"], g["ctx_len"], w.cuda(), 64, sinks=4, recent=9)
+    torch.cuda.synchronize()
+    assert torch.equal(e["kept"].cpu(), kept[0]) and torch.equal(e["ctx_len"].cpu(), new)
+    assert torch.equal(g["k_cache"][first:].cpu(), k[0]) and torch.equal(g["v_cache"][first:].cpu(), v[0])
+    assert all(lib.get_device_error(x["ws"]) == 0 for x in (r, u, e))
