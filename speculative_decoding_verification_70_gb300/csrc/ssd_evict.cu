@@ -286,12 +286,13 @@ struct MoveSmem {
 // kMoveBytes of them: on their way into shared memory while the places of the next round
 // are found, and out again once every CTA of the cluster has its own, beside the next
 // round's loads (whose sources lie behind this round's targets).
-// (Relaxed: it orders copies that have ended before other CTAs' writes, and no values pass.)
+// (The cluster's barrier is relaxed: it orders copies that have ended before other CTAs'
+// writes, and no values pass between CTAs.  The places of the next round pass between a
+// CTA's threads, by its own barrier.)
 __device__ __forceinline__ void round_sync(int cluster) {
+  __syncthreads();
   if (cluster > 1)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-  else
-    __syncthreads();
 }
 
 __device__ __forceinline__ bool in_range(const EvictParams& p, int ctx) {
