@@ -198,14 +198,10 @@ __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 
 // ---------------------------------------------------------------------------
 // sums: a warpgroup a tile, a thread a slot
 // ---------------------------------------------------------------------------
-// 16 columns' sum.
+// 16 columns' sum.  (A column that the slot does not see is left out behind its bias, which
+// may be NaN.)
 template <bool MASKED>
 __device__ __forceinline__ void add_columns(f32x2 c2, uint32_t (&s)[16], const float* bias, uint32_t seen, f32x2 (&sum)[2]) {
-  if (MASKED) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (!(seen & (1u << e))) s[e] = 0xff800000u;  // -inf
-  }
 #pragma unroll
   for (int e = 0; e < 16; e += 4) {
     const float4 m = *reinterpret_cast<const float4*>(bias + e);
@@ -214,6 +210,10 @@ __device__ __forceinline__ void add_columns(f32x2 c2, uint32_t (&s)[16], const f
       float y0, y1;
       up2(fma2(pk2(__uint_as_float(s[e + 2 * q]), __uint_as_float(s[e + 2 * q + 1])), c2, q ? pk2(m.z, m.w) : pk2(m.x, m.y)),
           y0, y1);
+      if (MASKED) {
+        if (!(seen & (1u << (e + 2 * q)))) y0 = -INFINITY;
+        if (!(seen & (2u << (e + 2 * q)))) y1 = -INFINITY;
+      }
       sum[q] = add2(sum[q], pk2(ex2_fast(y0), ex2_fast(y1)));
     }
   }
