@@ -690,8 +690,8 @@ SSD_API ssd_status ssd_chunk_attention(const ssd_paged_kv *kv, const ssd_draft_n
  *                + sum over the tokens i and query heads g of head h's group that
  *                  see s of exp(scale * q_ig.k_s - lse_ig),
  * with the slots that ssd_chunk_attention's token sees and the lse it wrote
- * (rows of lse -inf add nothing; those of lse NaN make the slots that they see
- * NaN, and no others).
+ * (rows of lse -inf add nothing, whatever they score; those of lse NaN make the
+ * slots that they see NaN, and no others).
  *   lse      : [B, N, Hq] fp32.
  *   weights  : fp32, row (b, h) at b*w_b + h*w_h (elements), w_len entries; decay 0
  *              writes without reading.  Slots behind a sequence's end stay as

@@ -66,6 +66,7 @@ struct Args : PageTiles {
 
 struct alignas(16) Misc {
   alignas(16) float bias[kBias][kTile];  // -lse of the columns, in units of log 2
+  uint4 none[kBias];                     // columns whose lse is -inf: they add nothing, whatever they score
   uint64_t kfull[2][kMaxKeys], kempty[2][kMaxKeys], qfull[kMaxQueries], qempty[kMaxQueries], bfull[kBias], bempty[kBias];
   uint64_t sfull[2][2], sempty[2][2], done;
   long long left;
@@ -221,7 +222,8 @@ __device__ __forceinline__ void add_columns(f32x2 c2, uint32_t (&s)[16], const f
 
 // A block's columns, 16 at a time, the next ones on their way meanwhile.
 template <bool MASKED, class Read>
-__device__ __forceinline__ float block_sum(const Args& a, uint32_t tS, const float* bias, int lo, int hi, Read&& read) {
+__device__ __forceinline__ float block_sum(const Args& a, uint32_t tS, const float* bias, const uint32_t* none, int lo,
+                                           int hi, Read&& read) {
   const f32x2 c2 = pk2(a.c, a.c);
   f32x2 sum[2] = {0ull, 0ull};
   uint32_t s0[16], s1[16];
@@ -231,12 +233,13 @@ __device__ __forceinline__ float block_sum(const Args& a, uint32_t tS, const flo
     tm_wait_loads();
     tm_tie16(s0);
     tm_get16(tS + j + 16, s1);
-    add_columns<MASKED>(c2, s0, bias + j, below(hi - j) & ~below(lo - j), sum);
+    const uint32_t seen = MASKED ? below(hi - j) & ~below(lo - j) & ~none[j / 32] : 0u;
+    add_columns<MASKED>(c2, s0, bias + j, seen, sum);
     tm_wait_loads();
     tm_tie16(s1);
     if (j + 32 < a.cols) tm_get16(tS + j + 32, s0);
     else read();
-    add_columns<MASKED>(c2, s1, bias + j + 16, below(hi - j - 16) & ~below(lo - j - 16), sum);
+    add_columns<MASKED>(c2, s1, bias + j + 16, seen >> 16, sum);
   }
   float x, y;
   up2(add2(sum[0], sum[1]), x, y);
@@ -288,8 +291,11 @@ __device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem,
           bar_arrive(&sm.sempty[w][half]);
         };
         // (columns that are no row, behind the block's, are masked like those that do not see it)
-        if (__all_sync(0xffffffffu, lo == 0 && hi * a.G == a.cols)) acc += block_sum<false>(a, tS, sm.bias[bs], 0, 0, read);
-        else acc += block_sum<true>(a, tS, sm.bias[bs], lo * a.G, hi * a.G, read);
+        const uint4 none = sm.none[bs];
+        const bool whole = lo == 0 && hi * a.G == a.cols && (none.x | none.y | none.z | none.w) == 0;
+        const uint32_t* out = reinterpret_cast<const uint32_t*>(&sm.none[bs]);
+        if (__all_sync(0xffffffffu, whole)) acc += block_sum<false>(a, tS, sm.bias[bs], out, 0, 0, read);
+        else acc += block_sum<true>(a, tS, sm.bias[bs], out, lo * a.G, hi * a.G, read);
       }
       bar_arrive(&sm.bempty[bs]);
     }
@@ -543,7 +549,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         const float* lse = a.lse + (static_cast<long long>(pc.b) * a.nodes.N + i0) * a.Hq + pc.h * a.G;
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k)
-          l.x[k] = lane + 32 * k < rows ? __ldg(lse + place[k]) : -INFINITY;
+          l.x[k] = lane + 32 * k < rows ? __ldg(lse + place[k]) : 0.f;
       };
       Lse l0, l1, l2;
       load(l0);
@@ -553,9 +559,13 @@ __global__ void __launch_bounds__(kSumThreads, 1)
         load(l2);
         const int bs = block % kBias;
         bar_await(&sm.bempty[bs], ((block / kBias) & 1) ^ 1, sm, a.err);
+        uint32_t none[kTile / 32];
 #pragma unroll
-        for (int k = 0; k < kTile / 32; ++k)
-          sm.bias[bs][lane + 32 * k] = l0.x[k] == -INFINITY ? -INFINITY : -l0.x[k] * kLog2e;
+        for (int k = 0; k < kTile / 32; ++k) {
+          none[k] = __ballot_sync(0xffffffffu, l0.x[k] == -INFINITY);
+          sm.bias[bs][lane + 32 * k] = -l0.x[k] * kLog2e;
+        }
+        if (lane == 0) sm.none[bs] = make_uint4(none[0], none[1], none[2], none[3]);
         __syncwarp();
         if (lane == 0) bar_arrive(&sm.bfull[bs]);
         ++block;

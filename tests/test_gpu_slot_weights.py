@@ -39,3 +39,42 @@ def test_nan_lse_reaches_the_slots_that_its_row_sees(gpu_lib, N, D, window, sink
     r = add_weights(gpu_lib, c, lse, w, window=window, sinks=sinks, decay=0.5)
     _same(r["weights"], want, tol, "weights")
     assert gpu_lib.get_device_error(r["ws"]) == 0
+
+
+@pytest.mark.parametrize("spoil", ["nan", "inf", "key"])
+@pytest.mark.parametrize("N,D,ctx", [(1, 64, (300, 20)), (6, 128, (90, 700)), (32, 64, (300, 5)), (150, 128, (300, 0)),
+                                     (150, 64, (0, 900))])
+def test_rows_of_lse_minus_infinity_add_nothing_whatever_they_score(gpu_lib, N, D, ctx, spoil):
+    """Rows that a caller takes out so: their queries are NaN, or infinite (scores of all
+    signs), or every row's key is NaN somewhere."""
+    c = case(2, N, 8, 2, D, 16, ctx, FP if D == 64 else BF, 9)
+    out = torch.zeros((2, N, 8), dtype=torch.bool)
+    out[0, N // 2] = True
+    out[1, :, 5] = True
+    out[1, N - 1, 1:3] = True
+    q = c["q"].clone()
+    if spoil == "nan":
+        q[out] = math.nan
+    elif spoil == "inf":
+        q[out] = 0.0
+        q[..., 7][out] = math.inf
+    c["q"] = q
+    _, lse, _, _ = cref.attention(c)
+    lse = lse.float()
+    lse[out] = -math.inf
+    if spoil == "key":  # (other rows that see the slot spoil it, in its own place alone)
+        for b in range(2):
+            s = int(c["ctx_len"][b]) // 2
+            c["k_cache"][c["page_table"][b, s // 16].long(), s % 16, 1, 3] = math.nan
+            s = int(c["ctx_len"][b]) + N - 1
+            c["k_cache"][c["page_table"][b, s // 16].long(), s % 16] = math.inf
+    assert bool(torch.isfinite(lse[~out]).all())
+    w = start(c)
+    # (of these rows the plain form takes nothing, so any queries will do; its tolerance of
+    # finite ones is theirs, 0, while one of NaN would be 0 times NaN)
+    want, tol = cref.weights({**c, "q": torch.where(out[..., None], torch.zeros_like(q), q)}, lse, w, decay=0.5)
+    r = add_weights(gpu_lib, c, lse, w, decay=0.5)
+    _same(r["weights"], want, tol, "weights")
+    lse[:] = -math.inf
+    r = add_weights(gpu_lib, c, lse, w, decay=1.0)
+    assert torch.equal(r["weights"].cpu(), w)
