@@ -530,38 +530,74 @@ __device__ __forceinline__ void softmax_role(const Args& a, Misc& sm, uint32_t t
 }
 
 // ---------------------------------------------------------------------------
-// the kernel
+// softmax of copies
 // ---------------------------------------------------------------------------
-// N entries from k on of a row that came out NaN or infinite because a slot that every row
+// Four entries from k on of a row that came out NaN or infinite because a slot that every row
 // sees holds such a value, which met other copies' weights of 0 as well: what the values
-// alone make of them.
-template <class T, int N>
-__device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, int k, uint32_t (&o)[N]) {
-  float x[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) x[e] = 0.f;
+// alone make of them.  By the lanes of a warp that write results, which share the piece's
+// slots (alone, each took 29 ms for 20000; the CTA's other warps give up waiting after a
+// second).
+template <class T>
+__device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, int k, uint32_t (&o)[4]) {
+  const unsigned here = __activemask();
+  const int n = __popc(here), me = __popc(here & ((1u << (threadIdx.x & 31)) - 1));
+  unsigned odd[3][2] = {};  // columns with NaN, inf, -inf
 #pragma unroll 1
   for (int at = pc.t0; at < pc.end; ++at) {
     int first, count;
     tile_slots(a, pc.tile(at), first, count);
 #pragma unroll 1
-    for (int s = first; s < first + count; ++s) {
+    for (int s = first + me; s < first + count; s += n) {
       int page, off;
       if (!all(a, pc.s, s, s)) continue;  // (cleared)
       if (!kv_slot(a.table + pc.b * a.table_stride, a.width, a.pages, a.ps, s, page, off)) continue;
-      const uint32_t* v =
-          reinterpret_cast<const uint32_t*>(a.vcache + 2 * (page * a.v_page + off * a.v_slot + pc.h * a.v_head + k));
+      const uint4* v = reinterpret_cast<const uint4*>(a.vcache + 2 * (page * a.v_page + off * a.v_slot + pc.h * a.v_head));
+      uint4 x[8];
 #pragma unroll
-      for (int e = 0; e < N / 2; ++e) {
-        const uint32_t y = v[e];
-        if (!(fabsf(T::lo(y)) < INFINITY)) x[2 * e] += T::lo(y);
-        if (!(fabsf(T::hi(y)) < INFINITY)) x[2 * e + 1] += T::hi(y);
+      for (int i = 0; i < 8; ++i) x[i] = v[i];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!has_nonfinite<T>(x[i])) continue;
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t y = e < 2 ? w[0] : e < 4 ? w[1] : e < 6 ? w[2] : w[3];
+          const float f = e & 1 ? T::hi(y) : T::lo(y);
+          const unsigned bit = 1u << (8 * (i & 3) + e);
+          if (f != f) odd[0][i >> 2] |= bit;
+          else if (f == INFINITY) odd[1][i >> 2] |= bit;
+          else if (f == -INFINITY) odd[2][i >> 2] |= bit;
+        }
       }
     }
   }
+  __syncwarp(here);
 #pragma unroll
-  for (int e = 0; e < N; ++e)
-    if (!(fabsf(__uint_as_float(o[e])) < INFINITY) && !(fabsf(x[e]) < INFINITY)) o[e] = __float_as_uint(x[e]);
+  for (int q = 0; q < 6; ++q) odd[q >> 1][q & 1] = __reduce_or_sync(here, odd[q >> 1][q & 1]);
+  const bool second = k >= 32;
+  const unsigned nan = (second ? odd[0][1] : odd[0][0]) >> (k & 31), up = (second ? odd[1][1] : odd[1][0]) >> (k & 31),
+                 down = (second ? odd[2][1] : odd[2][0]) >> (k & 31);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const unsigned bit = 1u << e;
+    if (!(fabsf(__uint_as_float(o[e])) < INFINITY) && ((nan | up | down) & bit))
+      o[e] = (nan | (up & down)) & bit ? 0x7fc00000u : up & bit ? 0x7f800000u : 0xff800000u;
+  }
+}
+
+// The same (not if it is only rows whose l, the row's `sum`, is NaN as well: scores that are
+// not finite need no more), and the values that only some rows see, for a token in slot `pos`.
+// Out of line: few calls come here, and its instructions would stand between those of every
+// item (64 single tokens under a window 72 us, in line 73 to 77).
+template <class T>
+__device__ __noinline__ uint4 mend_copies(const Args& a, const Pieces pc, const unsigned* fl, int pos, float sum, int k, uint4 x) {
+  uint32_t z[4] = {x.x, x.y, x.z, x.w};
+  bool finite = true;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) finite = finite && fabsf(__uint_as_float(z[e])) < INFINITY;
+  if (__any_sync(__activemask(), !finite && sum > 0.f)) seen_nonfinite<T>(a, pc, k, z);
+  add_nonfinite<T>(a, pc.b, pc.h, pc.s, pos, fl, k, z);
+  return make_uint4(z[0], z[1], z[2], z[3]);
 }
 
 // Few rows (64 at most) of heads of 64, whose tiles come in half the time of heads of 128:
@@ -569,7 +605,7 @@ __device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, 
 // alone, so that a thread has 64 or 32 scores instead of 128; and the warpgroups take turns
 // within an item, as copies of each other.  The copies have their own m, l and O, which
 // are joined at the item's end; the O's of two items lie side by side in tensor memory.
-// (64 single tokens under a window of 2048, 32 / 8 heads: 70 us, with rows once and a
+// (64 single tokens under a window of 2048, 32 / 8 heads: 72 us, with rows once and a
 // warpgroup an item 95.  Heads of 128 are as fast without: 64 / 8 heads, 64 single tokens
 // at 6800 279 us both ways, a chain of 8 under a window 27 us with copies and 24 without.)
 template <class T>
@@ -749,11 +785,12 @@ __device__ __forceinline__ void share_role(const Args& a, Misc& sm, uint32_t tme
           const float4 y = *reinterpret_cast<const float4*>(stage + c * 128 + (q ^ (rr & 7)) * 16);
           x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
         }
-        uint32_t z[4] = {__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)};
-        const bool finite = fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY;
-        if (!finite) seen_nonfinite<T>(a, pc, k + 4 * q, z);
-        if (any) add_nonfinite<T>(a, pc.b, pc.h, pc.s, pc.ctx + pc.blk * a.tpi + token, fl, k + 4 * q, z);
         const float sum = sm.sums[rr];
+        uint4 y = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w));
+        const bool finite = fabsf(x.x) < INFINITY && fabsf(x.y) < INFINITY && fabsf(x.z) < INFINITY && fabsf(x.w) < INFINITY;
+        if (__builtin_expect(__any_sync(__activemask(), !finite || any), 0))
+          y = mend_copies<T>(a, pc, fl, pc.ctx + pc.blk * a.tpi + token, sum, k + 4 * q, y);
+        const uint32_t z[4] = {y.x, y.y, y.z, y.w};
         write_columns<T, D>(a, z, place(token, rr - token * a.G), k + 4 * q, direct, sum == 0.f,
                             !direct ? 1.f : sum == 0.f ? 0.f : 1.f / sum);
       }
