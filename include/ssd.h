@@ -675,7 +675,8 @@ SSD_API ssd_status ssd_kv_append_at(const ssd_paged_kv *kv, const ssd_draft_node
  *   ws       : ssd_chunk_attention_workspace_bytes(B, N, Hq, Hkv, D) bytes.
  * scale, empty rows, tokens that are not there, slots that are not seen, page
  * ids out of range, scores beyond 2^24 and tiles that do not arrive: as in
- * ssd_tree_attention.
+ * ssd_tree_attention.  Table entries of pages of which no token sees a slot
+ * (between the first tokens and the window) may hold anything.
  */
 SSD_API size_t ssd_chunk_attention_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
 SSD_API ssd_status ssd_chunk_attention(const ssd_paged_kv *kv, const ssd_draft_nodes *tokens, int Hq,
@@ -696,8 +697,8 @@ SSD_API ssd_status ssd_chunk_attention(const ssd_paged_kv *kv, const ssd_draft_n
  *   weights  : fp32, row (b, h) at b*w_b + h*w_h (elements), w_len entries; decay 0
  *              writes without reading.  Slots behind a sequence's end stay as
  *              they are.
- *   kv, tokens, q, window, sinks, scale : as in ssd_chunk_attention; the values
- *              (v) are not read.
+ *   kv, tokens, q, window, sinks, scale, page ids : as in ssd_chunk_attention;
+ *              the values (v) are not read.
  *   ws       : ssd_kv_weights_workspace_bytes() bytes, of any sizes.
  * A sequence with ctx_len + n_nodes > w_len sets SSD_DEVERR_BAD_LENGTH and adds
  * nothing.  Sums are made in an order that the sizes and lengths alone decide.

@@ -854,7 +854,18 @@ __device__ __forceinline__ void load_role(const Args& a, Misc& sm, const CUtenso
     }
   }
   if (pending) load_tile<D, GATHER>(a, sm, rv, p0v, p1v, idv, hv, a.err, a.withheld);
-  if (bad_page) atomicOr(a.err, kErrBadPage);
+  // whether somebody sees them (looked up once more: the copies' loop has no time for it)
+  if (__any_sync(0xffffffffu, bad_page)) {
+    bad_page = false;
+    pc.start(sm);
+#pragma unroll 1
+    while (pc.next(a)) {
+#pragma unroll 4
+      for (int at = pc.t0; at < pc.end; ++at)
+        bad_page |= bad_box<GATHER>(a, a.table + pc.b * a.table_stride, pc.tile(at), pc.s.p1, pc.s.lo, pc.s.sk);
+    }
+    if (bad_page) atomicOr(a.err, kErrBadPage);
+  }
 }
 
 // ---------------------------------------------------------------------------

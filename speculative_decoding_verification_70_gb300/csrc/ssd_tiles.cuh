@@ -72,6 +72,28 @@ __device__ __forceinline__ Place box_place(const PageTiles& a, const int* trow, 
   return x;
 }
 
+// Whether this lane's box of tile t has a page id out of range at a slot that somebody sees: of
+// those up to `last` the ones before sk and from lo on (other entries of a table may be
+// anything).
+template <bool GATHER>
+__device__ __forceinline__ bool bad_box(const PageTiles& a, const int* trow, int t, int last, int lo, int sk) {
+  const int lane = threadIdx.x & 31;
+  int first, count;
+  tile_slots(a, t, first, count);
+  if (!a.uneven) {
+    first += lane * a.step;
+    count = a.step;
+  }
+  if (lane >= a.boxes || first > last) return false;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < (GATHER ? 4 : 1); ++i) {
+    const int s = min(first + i, last), end = GATHER ? s + 1 : first + count;  // (in one page)
+    bad |= (s < sk || end > lo) && static_cast<unsigned>(__ldg(trow + s / a.ps)) >= static_cast<unsigned>(a.pages);
+  }
+  return bad;
+}
+
 __device__ __forceinline__ int seq_tokens(const PageTiles& a, const NodesView& nodes, int b, int& ctx, bool& bad) {
   ctx = __ldg(nodes.ctx_len + b);
   const int nn = nodes.n_nodes ? __ldg(nodes.n_nodes + b) : nodes.N;
@@ -81,7 +103,7 @@ __device__ __forceinline__ int seq_tokens(const PageTiles& a, const NodesView& n
 // ---------------------------------------------------------------------------
 // copies
 // ---------------------------------------------------------------------------
-// A ring's next tile: boxes p0 .. p1.
+// A ring's next tile: boxes p0 .. p1.  False where this lane's has a page id out of range.
 struct Ring {
   const CUtensorMap* map;
   uint64_t *full, *empty;

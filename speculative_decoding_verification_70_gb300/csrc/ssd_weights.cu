@@ -348,7 +348,18 @@ __device__ __forceinline__ void keys_role(const Args& a, Misc& sm, const CUtenso
     lookup(nxt);
     bad_page |= !load_tile<D, GATHER>(a, sm, rk, 0, cur.pl, cur.id, cur.h, a.err, a.withheld);
   }
-  if (bad_page) atomicOr(a.err, kErrBadPage);
+  // whether somebody sees them
+  if (__any_sync(0xffffffffu, bad_page)) {
+    bad_page = false;
+    pc.start(a, sm);
+#pragma unroll 1
+    while (pc.next(a)) {
+      const int lo = a.window ? max(0, pc.ctx - a.window + 1) : 0;
+      if (w < pc.k.tiles)
+        bad_page |= bad_box<GATHER>(a, a.table + pc.b * a.table_stride, 2 * pc.p + w, pc.ctx + pc.n - 1, lo, min(a.sinks, lo));
+    }
+    if (bad_page) atomicOr(a.err, kErrBadPage);
+  }
 }
 
 // ---------------------------------------------------------------------------
