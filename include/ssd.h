@@ -702,6 +702,8 @@ SSD_API ssd_status ssd_chunk_attention(const ssd_paged_kv *kv, const ssd_draft_n
  *   ws       : ssd_kv_weights_workspace_bytes() bytes, of any sizes.
  * A sequence with ctx_len + n_nodes > w_len sets SSD_DEVERR_BAD_LENGTH and adds
  * nothing.  Sums are made in an order that the sizes and lengths alone decide.
+ * After a call that was given up (SSD_DEVERR_TIMEOUT) each weight is as it was or
+ * as the call was to make it.
  */
 SSD_API size_t ssd_kv_weights_workspace_bytes(void);
 SSD_API ssd_status ssd_kv_weights(const ssd_paged_kv *kv, const ssd_draft_nodes *tokens, int Hq, const void *q,

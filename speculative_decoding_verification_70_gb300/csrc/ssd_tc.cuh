@@ -51,6 +51,7 @@ inline __device__ __noinline__ bool bar_await_more(uint64_t* b, uint32_t parity,
     if (*abort) return false;
     if (now_ns() - t0 > wait_us * 1000ull) {
       *abort = 1;
+      __threadfence_block();  // (before what runs on without its data)
       atomicOr(err, kErrTimeout);
       return false;
     }

@@ -37,7 +37,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // A CTA's range of blocks, for the joining kernel.
 struct alignas(16) Range {
   long long lo;      // first block (its position in cost)
-  int t0, used;      // its place in its item; 0: a range without blocks
+  int t0, used;      // its place in its item; 0: a range without blocks, 2: one that was given up
   int b, p, h, T;    // its item, the item's blocks
 };
 
@@ -305,7 +305,8 @@ __device__ __forceinline__ void sum_role(const Args& a, Misc& sm, uint32_t tmem,
       if (leads) acc += sm.other[w][wt];
       named_sync(1 + w, 256);
     }
-    if (!there || !leads) continue;
+    // (a wait that gave up: what is there stays)
+    if (!there || !leads || *reinterpret_cast<volatile int*>(&sm.abort)) continue;
     if (pc.direct()) *at = a.decay == 0.f ? acc : fmaf(a.decay, old, acc);
     else a.part[(2 * blockIdx.x + (item == 0 ? 0 : 1)) * 256 + w * 128 + wt] = acc;
   }
@@ -664,6 +665,7 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   tc_before();
   __syncthreads();
   if (warp == 0 && *reinterpret_cast<volatile int*>(&sm.abort)) {
+    if (lane == 0 && a.ranges[blockIdx.x].used) a.ranges[blockIdx.x].used = 2;
     // given up: let copies in flight land before the shared memory is freed
     const unsigned long long t0 = now_ns();
     while (now_ns() - t0 < 20000000ull) __nanosleep(100000);
@@ -675,7 +677,8 @@ __global__ void __launch_bounds__(kSumThreads, 1)
   }
 }
 
-// Adds the parts of the items that range borders cut, in range order.  blockIdx.x: a range
+// Adds the parts of the items that range borders cut, in range order (not where a part's CTA
+// gave up).  blockIdx.x: a range
 // that starts inside an item; the first such range of an item does its work, a thread a slot.
 __global__ void __launch_bounds__(256) weights_join_kernel(const __grid_constant__ Args a, int C) {
   const int c = blockIdx.x + 1, w = threadIdx.x >> 7, wt = threadIdx.x & 127;
@@ -701,6 +704,7 @@ __global__ void __launch_bounds__(256) weights_join_kernel(const __grid_constant
       if (!a.ranges[k].used) continue;
       if (a.ranges[k].lo >= e) break;
     }
+    if (a.ranges[k].used == 2) return;
     sum += a.part[(2 * k + (k == pk && before < s ? 1 : 0)) * 256 + threadIdx.x];
   }
   float* at = a.weights + me.b * a.w_b + me.h * a.w_h + slot;

@@ -9,6 +9,7 @@ import chunk_reference as cref
 from test_gpu_budget import add_weights, check_weights
 from test_gpu_chunk import case
 from test_gpu_target import _same
+from test_gpu_waits import withheld  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -78,3 +79,23 @@ def test_rows_of_lse_minus_infinity_add_nothing_whatever_they_score(gpu_lib, N, 
     lse[:] = -math.inf
     r = add_weights(gpu_lib, c, lse, w, decay=1.0)
     assert torch.equal(r["weights"].cpu(), w)
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D,ctx,window", [
+    (1, 1, 8, 2, 64, 5000, 0),      # an item in parts
+    (40, 3, 8, 2, 128, 300, 0),     # items that are whole
+    (2, 200, 8, 2, 64, 700, 150)])  # blocks of rows, and slots that nobody sees
+def test_weights_outlive_tiles_that_do_not_arrive(gpu_lib, withheld, B, N, Hq, Hkv, D, ctx, window):  # noqa: F811
+    """A call that gives up leaves every entry as it was or as it should become."""
+    lib = gpu_lib
+    c = case(B, N, Hq, Hkv, D, 16, ctx, BF, 73)
+    _, lse, _, _ = cref.attention(c, window, 4)
+    lse, w = lse.float(), start(c)
+    good = add_weights(lib, c, lse, w, window=window, sinks=4, decay=0.5)
+    with withheld:
+        lost = add_weights(lib, c, lse, w, window=window, sinks=4, decay=0.5, ws=good["ws"])
+    assert lib.get_device_error(good["ws"], clear=True) == lib.DEVERR_TIMEOUT
+    got = lost["weights"].cpu()
+    assert bool(((got == w) | (got == good["weights"].cpu())).all())
+    again = add_weights(lib, c, lse, w, window=window, sinks=4, decay=0.5, ws=good["ws"])
+    assert lib.get_device_error(good["ws"]) == 0 and torch.equal(again["weights"], good["weights"])
