@@ -8,6 +8,7 @@ import torch
 import chunk_reference as cref
 import target_reference as ref
 from test_gpu_chunk import attend, case, check
+from test_gpu_waits import withheld  # noqa: F401  (a fixture)
 
 pytestmark = pytest.mark.gpu
 BF, FP = torch.bfloat16, torch.float16
@@ -95,3 +96,20 @@ def test_what_is_not_finite_does_not_hold_up_a_batch(gpu_lib):
     v = g["v_cache"].clone()
     v[p, o] = math.inf
     assert _us(gpu_lib, {**g, "v_cache": v}) < 10 * plain + 20
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,ctx", [
+    (2, 8, 16, 2, 5000),    # 64 rows, two copies, items in parts
+    (3, 5, 18, 2, 40),      # 45 rows, whole items
+    (1, 4, 16, 2, 3000)])   # 32 rows, four copies
+def test_copies_of_tiles_that_do_not_arrive(gpu_lib, withheld, B, N, Hq, Hkv, ctx):  # noqa: F811
+    """The call ends with the error bit; then the same call is right, with its workspace."""
+    lib = gpu_lib
+    c = case(B, N, Hq, Hkv, 64, 16, ctx, BF, 75)
+    good = check(lib, c)
+    with withheld:
+        attend(lib, c, ws=good["ws"])
+    assert lib.get_device_error(good["ws"], clear=True) == lib.DEVERR_TIMEOUT
+    again = attend(lib, c, ws=good["ws"])
+    assert lib.get_device_error(good["ws"]) == 0
+    assert torch.equal(again["out"], good["out"]) and torch.equal(again["lse"], good["lse"])

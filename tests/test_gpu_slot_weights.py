@@ -99,3 +99,35 @@ def test_weights_outlive_tiles_that_do_not_arrive(gpu_lib, withheld, B, N, Hq, H
     assert bool(((got == w) | (got == good["weights"].cpu())).all())
     again = add_weights(lib, c, lse, w, window=window, sinks=4, decay=0.5, ws=good["ws"])
     assert lib.get_device_error(good["ws"]) == 0 and torch.equal(again["weights"], good["weights"])
+
+
+@pytest.mark.parametrize("page", [2, 12, 40, 72, 130, 136, 201])
+def test_page_sizes(gpu_lib, page):
+    """Pages whose parts make a tile, ones that need whole pages, and both kinds above 128."""
+    for N, D, order in ((1, 64, "slot"), (60, 128, "slot"), (60, 128, "head"), (210, 64, "slot")):
+        c = case(3, N, 8, 2, D, page, (0, 131, 620), BF, page, order=order)
+        check_weights(gpu_lib, c, decay=0.5)
+        check_weights(gpu_lib, c, 150, 9, decay=0.5)
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.5, -1.0])
+@pytest.mark.parametrize("sinks", [0, 4, 300])
+@pytest.mark.parametrize("page", [1, 5, 16, 201])
+def test_what_no_token_sees_fades(gpu_lib, page, sinks, decay):
+    """Slots between the first tokens and the window, of tiles that nobody looks at and of ones
+    that somebody does."""
+    for N, D in ((1, 64), (70, 128)):
+        c = case(4, N, 8, 2, D, page, (99, 1500, 3001, 700), BF, 74, fill="random")
+        check_weights(gpu_lib, c, 100, sinks, decay=decay)
+
+
+@pytest.mark.parametrize("order", ["slot", "head"])
+@pytest.mark.parametrize("page", [1, 3, 5, 12, 130, 201])
+def test_odd_pages_out_of_range(gpu_lib, page, order):
+    lib = gpu_lib
+    for N, D in ((1, 64), (50, 128), (200, 64)):
+        c = case(2, N, 8, 2, D, page, (150, 420), BF, 60 + page, fill="random", order=order)
+        c["page_table"][0, 100 // page] = c["k_cache"].shape[0]
+        c["page_table"][1, 300 // page] = -2
+        check_weights(lib, c, decay=0.9, error=lib.DEVERR_BAD_PAGE)
+        check_weights(lib, c, 330, 2, decay=0.9, error=lib.DEVERR_BAD_PAGE)
