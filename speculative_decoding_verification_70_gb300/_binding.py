@@ -782,6 +782,13 @@ def ssd_tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     return o
 
 
+def _slots(**counts):
+    """Numbers of slots as the library takes them, in 32 bits (which would be cut to them)."""
+    for name, x in counts.items():
+        if not -(1 << 31) <= x < 1 << 31:
+            raise ValueError("%s must be below 2^31, got %d" % (name, x))
+
+
 def chunk_attention_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
     return int(load_library().ssd_chunk_attention_workspace_bytes(B, N, Hq, Hkv, D))
 
@@ -807,6 +814,7 @@ def ssd_chunk_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.T
     lib = load_library()
     if k_cache.dim() != 4:
         raise ValueError("the caches must be [pages, page_size, Hkv, D]")
+    _slots(window=window, sinks=sinks)
     kv, H, D, B, dev = _paged_kv(k_cache, v_cache, page_table)
     dt = k_cache.dtype
     qp, qsh, qb, qn, qh = _chunk_q(q, dt, B, D, dev)
@@ -854,6 +862,7 @@ def ssd_kv_weights(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Ten
     lib = load_library()
     if k_cache.dim() != 4:
         raise ValueError("the cache must be [pages, page_size, Hkv, D]")
+    _slots(window=window, sinks=sinks)
     kv, H, D, B, dev = _paged_kv(k_cache, k_cache, page_table)
     qp, qsh, qb, qn, qh = _chunk_q(q, k_cache.dtype, B, D, dev)
     _, N, Hq, _ = qsh
@@ -893,6 +902,7 @@ def ssd_kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, page_table: torch
     lead += (B, H)
     if budget < 1:
         raise ValueError("budget must be at least 1")
+    _slots(budget=budget, sinks=sinks, recent=recent)
     w, *wst, S = _weights(weights, lead, "weights", dev)
     if ws is None:
         ws = new_workspace(_ERRWORD_BYTES, dev)
