@@ -665,6 +665,7 @@ SSD_API ssd_status ssd_kv_append_at(const ssd_paged_kv *kv, const ssd_draft_node
  * The token in slot p sees the slots s <= p with s > p - window (window 0: all
  * of them) or s < sinks, of key/value head h / (Hq / Hkv);
  *     out = sum_s p_s v_s,  p = softmax over the seen slots of scale * q.k_s.
+ * (window and sinks count slots, which after ssd_kv_evict are no positions.)
  *   q        : [B, N, Hq, D] with element strides q_b, q_n, q_h, positive
  *              multiples of 8 (those of a dimension of one entry too), type
  *              kv->dtype, 16-byte aligned; Hq a multiple of Hkv, at most 64

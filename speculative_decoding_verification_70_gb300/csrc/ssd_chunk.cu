@@ -588,7 +588,7 @@ __device__ __forceinline__ void seen_nonfinite(const Args& a, const Pieces& pc, 
 // The same (not if it is only rows whose l, the row's `sum`, is NaN as well: scores that are
 // not finite need no more), and the values that only some rows see, for a token in slot `pos`.
 // Out of line: few calls come here, and its instructions would stand between those of every
-// item (64 single tokens under a window 72 us, in line 73 to 77).
+// item (64 single tokens under a window took 1 to 5 of 72 us more with it in line).
 template <class T>
 __device__ __noinline__ uint4 mend_copies(const Args& a, const Pieces pc, const unsigned* fl, int pos, float sum, int k, uint4 x) {
   uint32_t z[4] = {x.x, x.y, x.z, x.w};
@@ -605,7 +605,7 @@ __device__ __noinline__ uint4 mend_copies(const Args& a, const Pieces pc, const 
 // alone, so that a thread has 64 or 32 scores instead of 128; and the warpgroups take turns
 // within an item, as copies of each other.  The copies have their own m, l and O, which
 // are joined at the item's end; the O's of two items lie side by side in tensor memory.
-// (64 single tokens under a window of 2048, 32 / 8 heads: 72 us, with rows once and a
+// (64 single tokens under a window of 2048, 32 / 8 heads: 71 us, with rows once and a
 // warpgroup an item 95.  Heads of 128 are as fast without: 64 / 8 heads, 64 single tokens
 // at 6800 279 us both ways, a chain of 8 under a window 27 us with copies and 24 without.)
 template <class T>

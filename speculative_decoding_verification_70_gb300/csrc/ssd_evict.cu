@@ -12,8 +12,8 @@
 // Nothing is computed in floating point: weights are compared by their bits.
 //
 // What bounds it: many heads, the bytes moved, read and written (80 layers, 1024 of 4096
-// slots kept, 131 us, 5.3 TB/s); few, the passes over the weights, which wait for one
-// another (2 layers, 8192 of 100003 slots: 55 us, half of them the choice; 69 with 16 slots
+// slots kept, 133 us, 5.2 TB/s); few, the passes over the weights, which wait for one
+// another (2 layers, 8192 of 100003 slots: 56 us, half of them the choice; 69 with 16 slots
 // a lane, read again in every pass, and releasing barriers between the rounds of rows).
 #include "ssd_device.cuh"
 #include "ssd_kv.cuh"

@@ -17,8 +17,8 @@
 //
 // Scores, exponentials and sums are held in 32 bits; nothing is rounded to fewer.  What
 // bounds it: few rows, the bytes of K and of the weights (64 single tokens at 200..8000,
-// 64 / 8 heads of 128: 64 us, 4.5 TB/s); many, the exponentials and what stands before and
-// behind them in a warp (4 prompts of up to 5500 slots, 32 / 8 heads of 64: 110 us, of which
+// 64 / 8 heads of 128: 64 us, 4.6 TB/s); many, the exponentials and what stands before and
+// behind them in a warp (4 prompts of up to 5500 slots, 32 / 8 heads of 64: 108 us, of which
 // the exponentials' pipe alone would want 50).
 #include <math.h>
 
